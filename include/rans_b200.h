@@ -453,6 +453,209 @@ int rans_decode_to_values(const uint8_t *in, uint64_t in_bytes, const uint64_t *
                           float *values, void *workspace, uint64_t workspace_bytes,
                           void *stream);
 
+/* ------------------------------------------- tokens under a model's logits ---- */
+
+/*
+ * Coding a text under a language model: one distribution per position, given
+ * as a row of logits over a vocabulary of up to RANS_MAX_VOCAB tokens, where
+ * the indexed coder above takes one of K prepared rows per symbol.  (The pages
+ * code text under a model too -- "compress-zip" README: a model's integer
+ * probabilities feed an arithmetic coder, and both sides have to compute the
+ * same ones -- without spelling the steps out; this is the library's own
+ * reading, on its own rANS.)
+ *
+ * A row's adjusted logits z and the interval of token v, all float32
+ * operations rounded to nearest one by one (no fused multiply-add):
+ *   count = occurrences of v in the row's history; if count > 0:
+ *     z = z > 0 ? z / repetition : z * repetition
+ *     z = z - (presence + frequency * count)
+ *   z = z + bias of v (the row's last entry for v, if any)
+ *   v is alive unless its mask bit is 0 or z = -inf
+ *   y = z * (log2(e) * inv_temperature), log2(e) = 0x1.715476p+0f
+ *   d = max(y - max over alive of y, -64), k = rint(d), f = d - k
+ *   p = ((f * 0x1.c2a218p-5f + 0x1.f00c4ep-3f) * f + 0x1.62f5fap-1f) * f + 1
+ *       (2^f to a relative 1.02e-4: under 1e-8 bits of code length)
+ *   w = rint(p * 2^(21 + k)), an integer; 0 for tokens not alive
+ *   start of v = floor((2^24 - N) * (sum of w below v) / (sum of all w))
+ *                + alive tokens below v,        N = alive tokens of the row
+ *   freq of v  = start of the next token - start of v (>= 1 when alive)
+ * Sums are of integers, so the intervals of a row depend on that row alone:
+ * not on the batch it came in, the launch or the order of additions, and the
+ * decoder, which sees one row per step, reproduces what the encoder saw in a
+ * whole text.  If every alive y is -inf (finite logits that overflow), all
+ * alive tokens weigh the same.  A NaN or +inf logit of an alive token (or one
+ * whose y overflows) is RANS_ERR_RANGE; one under a 0 mask bit is not read.
+ *
+ * Streams: RANS64 states and words (lower bound 2^31, 32-bit words, one state
+ * per stream) at RANS_TOKEN_PRECISION bits: a token renormalises when
+ * x >= 2^39 * freq, then x -> (x / freq) 2^24 + x mod freq + start.
+ */
+#define RANS_MAX_VOCAB (1 << 19)
+#define RANS_TOKEN_PRECISION 24
+
+/* Logits element types. */
+enum { RANS_LOGITS_F32 = 0, RANS_LOGITS_F16 = 1, RANS_LOGITS_BF16 = 2 };
+
+/* Rows of logits: row r starts at data + r * row_stride (in elements); a row's
+ * `vocab` elements are contiguous.  row_stride >= vocab when rows > 1; data is
+ * aligned to its element type. */
+typedef struct rans_logits {
+    const void *data;
+    int32_t dtype;          /* RANS_LOGITS_* */
+    int32_t vocab;          /* 1 .. RANS_MAX_VOCAB */
+    int64_t rows;
+    int64_t row_stride;
+} rans_logits;
+
+/*
+ * What is done to logits before they are used: penalties for tokens of a
+ * row's history, biases, temperature, and a mask of allowed tokens.  NULL
+ * parts are left out.  A window [begin, end) is clipped to the array's length;
+ * windows may overlap (the rows of one text share it, each up to its own
+ * position).  Ids outside the vocabulary are skipped.
+ */
+typedef struct rans_adjust {
+    /* for all rows, when `params` is NULL: repetition and inv_temperature
+     * positive and finite, frequency and presence finite */
+    float repetition, frequency, presence, inv_temperature;
+    const float *params;           /* device: the same four per row, or NULL */
+    const int32_t *history;        /* device int32[history_len], or NULL */
+    const int64_t *history_begin;  /* device int64[rows] */
+    const int64_t *history_end;    /* device int64[rows] */
+    int64_t history_len;
+    const int32_t *bias_ids;       /* device int32[bias_len], or NULL */
+    const float *bias_values;      /* device float[bias_len] */
+    const int64_t *bias_begin;     /* device int64[rows] */
+    const int64_t *bias_end;       /* device int64[rows] */
+    int64_t bias_len;
+    const uint32_t *mask;          /* device: bit v & 31 of word v >> 5 is 1 where
+                                      token v is allowed; NULL allows all */
+    int64_t mask_stride;           /* words between rows' masks, >= ceil(vocab / 32);
+                                      0: one mask for all rows */
+} rans_adjust;
+
+/*
+ * The adjusted logits themselves, for a sampler: out = z * inv_temperature,
+ * -inf where the mask is 0, rounded once to out_dtype.  (The coder multiplies z
+ * by log2(e) * inv_temperature instead; hand it the logits and the adjustment,
+ * not this result, to code under the distribution defined above.)  NaN and
+ * infinities that the mask leaves in place go through as they are.
+ *   out: device, row r at out + r * out_stride elements (out_stride >= vocab
+ *        when rows > 1); may be logits->data itself when dtype and stride
+ *        agree, and overlaps it in no other way.
+ * Asynchronous; records no device errors.
+ */
+int rans_adjust_logits(const rans_logits *logits, const rans_adjust *adjust, void *out,
+                       int32_t out_dtype, int64_t out_stride, void *stream);
+
+/*
+ * The interval of one token per row: starts[r], freqs[r] of tokens[r] under
+ * row r.  A row whose token is -1 is skipped (its starts and freqs stay as
+ * they were).  adjust may be NULL.
+ *   status: device, 256 bytes, 256-byte aligned, zeroed once by the caller;
+ *           the first error stays in it until rans_get_status(status) reads
+ *           it.  A token outside the vocabulary is RANS_ERR_INDEX, one that is
+ *           not alive RANS_ERR_ZERO_FREQ, a row with a bad logit
+ *           RANS_ERR_RANGE; such a row's start and freq are 0.
+ *   tokens: device int32[rows]; starts, freqs: device uint32[rows] out.
+ * Asynchronous.
+ */
+int rans_token_intervals(const rans_logits *logits, const rans_adjust *adjust,
+                         const int32_t *tokens, uint32_t *starts, uint32_t *freqs, void *status,
+                         void *stream);
+
+/*
+ * Streams of n intervals: element i codes on [starts[i], starts[i] + freqs[i])
+ * of 2^RANS_TOKEN_PRECISION.  chunking: RANS_CHUNK_CONTIG or
+ * RANS_CHUNK_EXPLICIT, interleave 1, index_block 1, format RANS_FMT_RANS64;
+ * anything else is RANS_ERR_ARG.  Container, workspace and errors as for
+ * rans_encode_with_indexes (sizes from the same queries); an interval with
+ * freq 0 is RANS_ERR_ZERO_FREQ, one past 2^24 RANS_ERR_RANGE.  Asynchronous.
+ */
+int rans_encode_intervals(const uint32_t *starts, const uint32_t *freqs, int64_t n,
+                          const rans_chunking *chunking, uint8_t *out, uint64_t out_capacity,
+                          uint64_t *stream_offsets, void *workspace, uint64_t workspace_bytes,
+                          void *stream);
+
+/*
+ * Decoder states of S streams: states[2 k] = the 64-bit state, states[2 k + 1]
+ * = words of stream k taken so far.  Reads each stream's first two words; a
+ * stream without a valid state is RANS_ERR_CORRUPT (and its state 0).
+ *   in: 4-byte aligned; status: as for rans_token_intervals.  Asynchronous.
+ */
+int rans_token_states(const uint8_t *in, uint64_t in_bytes, const uint64_t *stream_offsets,
+                      int64_t S, uint64_t *states, void *status, void *stream);
+
+/*
+ * One decoding step: row r of the logits gives the next token of stream
+ * stream_ids[r] (NULL: stream r, rows <= S).  tokens[r] receives it and
+ * states_out the stream's new state; states_out may be states_in.  A row with
+ * stream id -1 is skipped (tokens[r] stays as it was), and states_out of
+ * streams that no row names is not written.  On an error (id outside [0, S) or
+ * named by two rows: RANS_ERR_INDEX; a bad state or a stream at its end:
+ * RANS_ERR_CORRUPT; no token alive: RANS_ERR_ZERO_FREQ; a bad logit:
+ * RANS_ERR_RANGE) the row's token is -1 and its stream's state goes out as it
+ * came in (for an id that is out of range or named twice, it is not written).
+ *   Other arguments as above.  Asynchronous.
+ */
+int rans_decode_tokens(const rans_logits *logits, const rans_adjust *adjust, const uint8_t *in,
+                       uint64_t in_bytes, const uint64_t *stream_offsets, int64_t S,
+                       const int32_t *stream_ids, const uint64_t *states_in,
+                       uint64_t *states_out, int32_t *tokens, void *status, void *stream);
+
+/*
+ * Checks that S decoded streams ended as they should: every word taken and the
+ * state back at 2^31; else RANS_ERR_CORRUPT in `status`.  Asynchronous.
+ */
+int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S, const uint64_t *states,
+                             void *status, void *stream);
+
+/*
+ * The coder's rate as a loss: the code length (in nats) of a teacher's tokens
+ * under a student's logits, less the teacher's own entropy, with its gradient.
+ * The teacher is given as the table builders take a row: listed
+ * probabilities and the mass of the tail.  With p_i = exp(logprobs[i]) over
+ * the row's K entries, q = softmax(inv_temperature * logits) and q_t the
+ * student's mass outside the list:
+ *   tail != 0: p_t = max(0, 1 - sum p);
+ *     loss = sum p_i (log p_i - log q_i) + p_t (log p_t - log q_t)
+ *   tail == 0: p_i /= sum p, p_t = 0.
+ * With K = 1 and log probability 0 the loss is the token's own code length.
+ *   d loss / d logit v = inv_temperature * (P q_v - p_v) for listed v,
+ *                        inv_temperature * (P - p_t / q_t) q_v for others,
+ * P = sum p + p_t.  The gradient is weighted by grad_losses[r] per row.
+ * Entries with id -1 or log probability -inf are absent; a row with none left
+ * gives loss 0 and gradient 0.  If the entries list the whole vocabulary there
+ * is no tail and p_t = 0.  A student with no mass where the teacher has some
+ * has loss +inf.  Rows with a NaN or +inf logit give NaN.  An id outside the
+ * vocabulary, or listed twice in a row, is RANS_ERR_INDEX in `status` (as for
+ * rans_token_intervals); the row's results are then undefined.
+ *   ids: device int32[rows][K]; logprobs: device float[rows][K];
+ *   1 <= K <= RANS_MAX_TOP; losses: device float[rows] out;
+ *   stats: device float[rows][8] out, 16-byte aligned, for the backward pass;
+ *   grad: device, the logits' dtype, row r at grad + r * grad_stride elements
+ *         (>= vocab when rows > 1); may be logits->data itself when the
+ *         strides agree, and overlaps it in no other way.
+ * rans_distill_backward takes the same logits, ids, logprobs and
+ * inv_temperature as the forward call that wrote `stats`.  rans_distill is both in one call,
+ * for loops that know the rows' weights beforehand.  All are asynchronous, and
+ * the results of a row depend on that row alone.
+ */
+#define RANS_MAX_TOP 4096
+
+int rans_distill_forward(const rans_logits *logits, const int32_t *ids, const float *logprobs,
+                         int32_t K, float inv_temperature, int32_t tail, float *losses,
+                         float *stats, void *status, void *stream);
+
+int rans_distill_backward(const rans_logits *logits, const int32_t *ids, const float *logprobs,
+                          int32_t K, float inv_temperature, const float *stats,
+                          const float *grad_losses, void *grad, int64_t grad_stride,
+                          void *stream);
+
+int rans_distill(const rans_logits *logits, const int32_t *ids, const float *logprobs,
+                 int32_t K, float inv_temperature, int32_t tail, const float *grad_losses,
+                 float *losses, void *grad, int64_t grad_stride, void *status, void *stream);
+
 /* Synchronises `stream` and returns the first error recorded in `workspace`
  * (RANS_OK if none), then clears it. */
 int rans_get_status(void *workspace, void *stream);

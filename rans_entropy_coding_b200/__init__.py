@@ -18,4 +18,12 @@ from ._lib import (  # noqa: F401
     rans_gaussian_lengths, rans_get_status, rans_max_compressed_bytes, rans_num_streams,
     rans_tables, rans_tables_bytes, rans_tables_prepare, rans_tables_refresh,
     rans_tables_refresh_from_scales)
-from .interface import RansCoder, from_byte_strings, to_byte_strings  # noqa: F401,E402
+from ._lib import rans_adjust, rans_logits  # noqa: F401,E402
+from .tokens import (  # noqa: F401,E402
+    MAX_TOP, MAX_VOCAB, TOKEN_PRECISION, LogitAdjust, adjust_logits, decode_tokens,
+    distill_loss, distill_loss_and_grad, encode_intervals, new_status, pack_mask,
+    rans_adjust_logits, rans_decode_tokens, rans_distill, rans_distill_backward,
+    rans_distill_forward, rans_encode_intervals, rans_token_intervals, rans_token_states,
+    rans_token_states_finish, token_intervals, token_states)
+from .interface import (  # noqa: F401,E402
+    RansCoder, TokenCoder, from_byte_strings, to_byte_strings)

@@ -62,11 +62,29 @@ class rans_tables(ctypes.Structure):
                 ("alias_remap_offset", ctypes.c_uint64)]
 
 
+class rans_logits(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("dtype", ctypes.c_int32), ("vocab", ctypes.c_int32),
+                ("rows", ctypes.c_int64), ("row_stride", ctypes.c_int64)]
+
+
+class rans_adjust(ctypes.Structure):
+    _fields_ = [("repetition", ctypes.c_float), ("frequency", ctypes.c_float),
+                ("presence", ctypes.c_float), ("inv_temperature", ctypes.c_float),
+                ("params", ctypes.c_void_p), ("history", ctypes.c_void_p),
+                ("history_begin", ctypes.c_void_p), ("history_end", ctypes.c_void_p),
+                ("history_len", ctypes.c_int64), ("bias_ids", ctypes.c_void_p),
+                ("bias_values", ctypes.c_void_p), ("bias_begin", ctypes.c_void_p),
+                ("bias_end", ctypes.c_void_p), ("bias_len", ctypes.c_int64),
+                ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64)]
+
+
 # (name, restype, argtypes) for every exported symbol of include/rans_b200.h
 _P, _I32, _I64, _U64, _F64, _F32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint64, ctypes.c_double, ctypes.c_float)
 _CHP = ctypes.POINTER(rans_chunking)
 _TBP = ctypes.POINTER(rans_tables)
+_LGP = ctypes.POINTER(rans_logits)
+_ADP = ctypes.POINTER(rans_adjust)
 SIGNATURES = [
     ("rans_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("rans_version", ctypes.c_int, []),
@@ -96,6 +114,16 @@ SIGNATURES = [
      [_P, _P, _P, _I64, _P, _I32, _F32, _TBP, _CHP, _P, _U64, _P, _P, _U64, _P]),
     ("rans_decode_to_values", ctypes.c_int,
      [_P, _U64, _P, _P, _P, _I64, _P, _I32, _F32, _TBP, _CHP, _P, _P, _U64, _P]),
+    ("rans_adjust_logits", ctypes.c_int, [_LGP, _ADP, _P, _I32, _I64, _P]),
+    ("rans_token_intervals", ctypes.c_int, [_LGP, _ADP, _P, _P, _P, _P, _P]),
+    ("rans_encode_intervals", ctypes.c_int, [_P, _P, _I64, _CHP, _P, _U64, _P, _P, _U64, _P]),
+    ("rans_token_states", ctypes.c_int, [_P, _U64, _P, _I64, _P, _P, _P]),
+    ("rans_decode_tokens", ctypes.c_int,
+     [_LGP, _ADP, _P, _U64, _P, _I64, _P, _P, _P, _P, _P, _P]),
+    ("rans_token_states_finish", ctypes.c_int, [_P, _I64, _P, _P, _P]),
+    ("rans_distill_forward", ctypes.c_int, [_LGP, _P, _P, _I32, _F32, _I32, _P, _P, _P, _P]),
+    ("rans_distill_backward", ctypes.c_int, [_LGP, _P, _P, _I32, _F32, _P, _P, _P, _I64, _P]),
+    ("rans_distill", ctypes.c_int, [_LGP, _P, _P, _I32, _F32, _I32, _P, _P, _P, _I64, _P, _P]),
     ("rans_get_status", ctypes.c_int, [_P, _P]),
     ("rans_debug_divide", ctypes.c_int, [_P, _P, _I64, _P, _P, _P]),
     ("rans_debug_wait_timeout", ctypes.c_int, [_P, ctypes.c_uint32, _P]),

@@ -1,6 +1,7 @@
 // api.cu -- the extern "C" entry points of librans_b200: argument checks,
 // chunking geometry, workspace layout and launch order.  Every coding step
-// runs in the kernels of tables.cu, encode.cu and decode.cu.
+// runs in the kernels of tables.cu, encode.cu and decode.cu; logits.cu,
+// tokens.cu and distill.cu hold those of tokens under a model's logits.
 #include <cstring>
 #include <mutex>
 #include <vector>
@@ -500,6 +501,236 @@ RANS_API int rans_decode_to_values(const uint8_t *in, uint64_t in_bytes,
   if (g.S == 0) return RANS_OK;
   return rb::launch_decode_float(in, in_bytes, stream_offsets, scales, means, scale_table,
                                  scale_bound, *tables, g, values, status, s);
+}
+
+// ---- tokens under a model's logits --------------------------------------
+
+namespace {
+
+// Bytes per element of a logits type, 0 for none.
+int logits_bytes(int32_t dtype) {
+  return dtype == RANS_LOGITS_F32 ? 4 : dtype == RANS_LOGITS_F16 || dtype == RANS_LOGITS_BF16 ? 2
+                                                                                             : 0;
+}
+
+bool aligned_to(const void *p, uint64_t bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
+}
+
+int check_logits(const rans_logits *in) {
+  if (!in || in->rows < 0 || in->vocab < 1 || in->vocab > RANS_MAX_VOCAB) return RANS_ERR_ARG;
+  const int e = logits_bytes(in->dtype);
+  if (e == 0) return RANS_ERR_ARG;
+  if (in->rows > 1 && in->row_stride < in->vocab) return RANS_ERR_ARG;
+  if (in->rows > 0 && (!in->data || !aligned_to(in->data, (uint64_t)e))) return RANS_ERR_ARG;
+  return RANS_OK;
+}
+
+bool finite(float x) { return x - x == 0.0f; }
+
+// The adjustment of a call in `out`: the caller's, checked, or a neutral one.
+int check_adjust(const rans_adjust *a, int32_t vocab, rans_adjust &out) {
+  if (!a) {
+    std::memset(&out, 0, sizeof(out));
+    out.repetition = 1.0f;
+    out.inv_temperature = 1.0f;
+    return RANS_OK;
+  }
+  out = *a;
+  if (!a->params &&
+      (!(a->repetition > 0.0f) || !finite(a->repetition) || !(a->inv_temperature > 0.0f) ||
+       !finite(a->inv_temperature) || !finite(a->frequency) || !finite(a->presence)))
+    return RANS_ERR_ARG;
+  if (a->history && (!a->history_begin || !a->history_end || a->history_len < 0))
+    return RANS_ERR_ARG;
+  if (a->bias_ids && (!a->bias_values || !a->bias_begin || !a->bias_end || a->bias_len < 0))
+    return RANS_ERR_ARG;
+  if (a->mask && a->mask_stride != 0 && a->mask_stride < (vocab + 31) / 32) return RANS_ERR_ARG;
+  return RANS_OK;
+}
+
+int check_status_word(const void *status) {
+  return status && aligned_to(status, 256) ? RANS_OK : RANS_ERR_ARG;
+}
+
+int check_streams(const uint8_t *in, uint64_t in_bytes, const uint64_t *offsets, int64_t S) {
+  if (S < 0 || (S > 0 && !offsets)) return RANS_ERR_ARG;
+  if ((in_bytes > 0 && !in) || !aligned_to(in, 4)) return RANS_ERR_ARG;
+  return RANS_OK;
+}
+
+int check_distill(const rans_logits *in, const int32_t *ids, const float *lp, int32_t K,
+                  float inv_temperature) {
+  const int st = check_logits(in);
+  if (st) return st;
+  if (K < 1 || K > RANS_MAX_TOP) return RANS_ERR_ARG;
+  if (!(inv_temperature > 0.0f) || !finite(inv_temperature)) return RANS_ERR_ARG;
+  if (in->rows > 0 && (!ids || !lp)) return RANS_ERR_ARG;
+  return RANS_OK;
+}
+
+// A result of the logits' shape: its rows, and what it may share with them.
+int check_result(const rans_logits *in, const void *out, int32_t dtype, int64_t stride) {
+  const int e = logits_bytes(dtype);
+  if (e == 0) return RANS_ERR_ARG;
+  if (in->rows == 0) return RANS_OK;
+  if (!out || !aligned_to(out, (uint64_t)e)) return RANS_ERR_ARG;
+  if (in->rows > 1 && stride < in->vocab) return RANS_ERR_ARG;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(in->data), b = reinterpret_cast<uintptr_t>(out);
+  const uint64_t ein = (uint64_t)logits_bytes(in->dtype);
+  const uint64_t la = ((uint64_t)(in->rows - 1) * (uint64_t)in->row_stride + in->vocab) * ein;
+  const uint64_t lb = ((uint64_t)(in->rows - 1) * (uint64_t)stride + in->vocab) * (uint64_t)e;
+  if (a < b + lb && b < a + la) {
+    // the same rows, or interleaved ones of one buffer
+    if (dtype != in->dtype || (in->rows > 1 && stride != in->row_stride)) return RANS_ERR_ARG;
+    if (a == b) return RANS_OK;
+    if (in->rows == 1) return RANS_ERR_ARG;
+    const uint64_t d = a < b ? b - a : a - b, row = (uint64_t)stride * ein;
+    const uint64_t off = d % row, len = (uint64_t)in->vocab * ein;
+    if (off < len || row - off < len) return RANS_ERR_ARG;
+  }
+  return RANS_OK;
+}
+
+}  // namespace
+
+RANS_API int rans_adjust_logits(const rans_logits *logits, const rans_adjust *adjust, void *out,
+                                int32_t out_dtype, int64_t out_stride, void *stream) {
+  NvtxRange nvtx_("rans_adjust_logits");
+  rans_adjust a;
+  int st = check_logits(logits);
+  if (!st) st = check_adjust(adjust, logits->vocab, a);
+  if (!st) st = check_result(logits, out, out_dtype, out_stride);
+  if (st || logits->rows == 0) return st;
+  return rb::launch_adjust(*logits, a, out, out_dtype, out_stride, as_stream(stream));
+}
+
+RANS_API int rans_token_intervals(const rans_logits *logits, const rans_adjust *adjust,
+                                  const int32_t *tokens, uint32_t *starts, uint32_t *freqs,
+                                  void *status, void *stream) {
+  NvtxRange nvtx_("rans_token_intervals");
+  rans_adjust a;
+  int st = check_logits(logits);
+  if (!st) st = check_adjust(adjust, logits->vocab, a);
+  if (!st) st = check_status_word(status);
+  if (st) return st;
+  if (logits->rows == 0) return RANS_OK;
+  if (!tokens || !starts || !freqs) return RANS_ERR_ARG;
+  return rb::launch_token_intervals(*logits, a, tokens, starts, freqs,
+                                    static_cast<int32_t *>(status), as_stream(stream));
+}
+
+RANS_API int rans_encode_intervals(const uint32_t *starts, const uint32_t *freqs, int64_t n,
+                                   const rans_chunking *chunking, uint8_t *out,
+                                   uint64_t out_capacity, uint64_t *stream_offsets,
+                                   void *workspace, uint64_t workspace_bytes, void *stream) {
+  NvtxRange nvtx_("rans_encode_intervals");
+  if (n > 0 && (!starts || !freqs)) return RANS_ERR_ARG;
+  if (!stream_offsets || !workspace || (out_capacity > 0 && !out)) return RANS_ERR_ARG;
+  if (!aligned_to(workspace, 256) || !aligned_to(out, 4)) return RANS_ERR_ARG;
+  Geom g;
+  int st = make_geom(chunking, n, g);
+  if (st) return st;
+  if (g.kind != RANS_CHUNK_CONTIG && g.kind != RANS_CHUNK_EXPLICIT) return RANS_ERR_ARG;
+  if (g.W != 1 || g.ib_shift != 0 || g.fmt != RANS_FMT_RANS64 || g.alias) return RANS_ERR_ARG;
+  if (workspace_bytes < enc_ws_bytes(g)) return RANS_ERR_CAPACITY;
+  cudaStream_t s = as_stream(stream);
+  char *ws = reinterpret_cast<char *>(workspace);
+  int32_t *status = reinterpret_cast<int32_t *>(ws);
+  uint64_t *lens = reinterpret_cast<uint64_t *>(ws + kWsHeader);
+  char *scratch = ws + kWsHeader + lens_bytes(g);
+  if (cudaMemsetAsync(ws, 0, kWsHeader + 8ull * (uint64_t)g.S, s) != cudaSuccess)
+    return RANS_ERR_CUDA;
+  if (g.S > 0) {
+    st = rb::launch_encode_intervals(starts, freqs, g, scratch, lens, status, s);
+    if (st) return st;
+  }
+  return rb::launch_compact(g, scratch, lens, out, out_capacity, stream_offsets, status, s);
+}
+
+RANS_API int rans_token_states(const uint8_t *in, uint64_t in_bytes,
+                               const uint64_t *stream_offsets, int64_t S, uint64_t *states,
+                               void *status, void *stream) {
+  NvtxRange nvtx_("rans_token_states");
+  int st = check_streams(in, in_bytes, stream_offsets, S);
+  if (!st) st = check_status_word(status);
+  if (st) return st;
+  if (S == 0) return RANS_OK;
+  if (!states) return RANS_ERR_ARG;
+  return rb::launch_token_states(in, in_bytes, stream_offsets, S, states,
+                                 static_cast<int32_t *>(status), as_stream(stream));
+}
+
+RANS_API int rans_decode_tokens(const rans_logits *logits, const rans_adjust *adjust,
+                                const uint8_t *in, uint64_t in_bytes,
+                                const uint64_t *stream_offsets, int64_t S,
+                                const int32_t *stream_ids, const uint64_t *states_in,
+                                uint64_t *states_out, int32_t *tokens, void *status,
+                                void *stream) {
+  NvtxRange nvtx_("rans_decode_tokens");
+  rans_adjust a;
+  int st = check_logits(logits);
+  if (!st) st = check_adjust(adjust, logits->vocab, a);
+  if (!st) st = check_streams(in, in_bytes, stream_offsets, S);
+  if (!st) st = check_status_word(status);
+  if (st) return st;
+  if (!stream_ids && logits->rows > S) return RANS_ERR_ARG;
+  if (logits->rows == 0) return RANS_OK;
+  if (!states_in || !states_out || !tokens || !stream_offsets) return RANS_ERR_ARG;
+  return rb::launch_decode_tokens(*logits, a, in, in_bytes, stream_offsets, S, stream_ids,
+                                  states_in, states_out, tokens, static_cast<int32_t *>(status),
+                                  as_stream(stream));
+}
+
+RANS_API int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S,
+                                      const uint64_t *states, void *status, void *stream) {
+  NvtxRange nvtx_("rans_token_states_finish");
+  if (S < 0 || (S > 0 && (!stream_offsets || !states))) return RANS_ERR_ARG;
+  const int st = check_status_word(status);
+  if (st || S == 0) return st;
+  return rb::launch_token_finish(stream_offsets, S, states, static_cast<int32_t *>(status),
+                                 as_stream(stream));
+}
+
+RANS_API int rans_distill_forward(const rans_logits *logits, const int32_t *ids,
+                                  const float *logprobs, int32_t K, float inv_temperature,
+                                  int32_t tail, float *losses, float *stats, void *status,
+                                  void *stream) {
+  NvtxRange nvtx_("rans_distill_forward");
+  int st = check_distill(logits, ids, logprobs, K, inv_temperature);
+  if (!st) st = check_status_word(status);
+  if (st || logits->rows == 0) return st;
+  if (!losses || !stats || !aligned_to(stats, 16)) return RANS_ERR_ARG;
+  return rb::launch_distill_forward(*logits, ids, logprobs, K, inv_temperature, tail, losses,
+                                    stats, static_cast<int32_t *>(status), as_stream(stream));
+}
+
+RANS_API int rans_distill_backward(const rans_logits *logits, const int32_t *ids,
+                                   const float *logprobs, int32_t K, float inv_temperature,
+                                   const float *stats, const float *grad_losses, void *grad,
+                                   int64_t grad_stride, void *stream) {
+  NvtxRange nvtx_("rans_distill_backward");
+  int st = check_distill(logits, ids, logprobs, K, inv_temperature);
+  if (!st) st = check_result(logits, grad, logits->dtype, grad_stride);
+  if (st || logits->rows == 0) return st;
+  if (!stats || !aligned_to(stats, 16) || !grad_losses) return RANS_ERR_ARG;
+  return rb::launch_distill_backward(*logits, ids, logprobs, K, inv_temperature, stats,
+                                     grad_losses, grad, grad_stride, as_stream(stream));
+}
+
+RANS_API int rans_distill(const rans_logits *logits, const int32_t *ids, const float *logprobs,
+                          int32_t K, float inv_temperature, int32_t tail,
+                          const float *grad_losses, float *losses, void *grad,
+                          int64_t grad_stride, void *status, void *stream) {
+  NvtxRange nvtx_("rans_distill");
+  int st = check_distill(logits, ids, logprobs, K, inv_temperature);
+  if (!st) st = check_result(logits, grad, logits->dtype, grad_stride);
+  if (!st) st = check_status_word(status);
+  if (st || logits->rows == 0) return st;
+  if (!losses || !grad_losses) return RANS_ERR_ARG;
+  return rb::launch_distill(*logits, ids, logprobs, K, inv_temperature, tail, grad_losses, losses,
+                            grad, grad_stride, static_cast<int32_t *>(status),
+                            as_stream(stream));
 }
 
 RANS_API int rans_get_status(void *workspace, void *stream) {

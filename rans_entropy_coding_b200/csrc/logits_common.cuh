@@ -1,0 +1,268 @@
+// logits_common.cuh -- reading rows of logits with their adjustments
+// (penalties, biases, masks), shared by the kernels of logits.cu, tokens.cu
+// and distill.cu.
+//
+// Rows may start anywhere an element may (odd vocabularies, strided views).
+// A kernel walks a row in vectors of 16 bytes at 16-byte aligned addresses:
+// element v sits at u = v + shift, where shift is the row's distance in
+// elements from the aligned address below it; only the first and the last
+// vector of a row are partial, and those are read element by element.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "rans_b200.h"
+
+namespace rb {
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+template <typename T>
+struct VecOf {
+  static constexpr int N = 16 / (int)sizeof(T);
+};
+
+__device__ __forceinline__ float logit_float(float x) { return x; }
+__device__ __forceinline__ float logit_float(__half x) { return __half2float(x); }
+__device__ __forceinline__ float logit_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+template <typename T>
+__device__ __forceinline__ T float_logit(float x);
+template <>
+__device__ __forceinline__ float float_logit<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half float_logit<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 float_logit<__nv_bfloat16>(float x) {
+  return __float2bfloat16_rn(x);
+}
+
+__device__ __forceinline__ void unpack16(const uint4 &q, float (&z)[4], float) {
+  z[0] = __uint_as_float(q.x);
+  z[1] = __uint_as_float(q.y);
+  z[2] = __uint_as_float(q.z);
+  z[3] = __uint_as_float(q.w);
+}
+__device__ __forceinline__ void unpack16(const uint4 &q, float (&z)[8], __half) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
+    z[2 * i] = f.x;
+    z[2 * i + 1] = f.y;
+  }
+}
+__device__ __forceinline__ void unpack16(const uint4 &q, float (&z)[8], __nv_bfloat16) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    z[2 * i] = __uint_as_float(w[i] << 16);
+    z[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack16(const float (&z)[4], float) {
+  return make_uint4(__float_as_uint(z[0]), __float_as_uint(z[1]), __float_as_uint(z[2]),
+                    __float_as_uint(z[3]));
+}
+__device__ __forceinline__ uint4 pack16(const float (&z)[8], __half) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2 h = __floats2half2_rn(z[2 * i], z[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 pack16(const float (&z)[8], __nv_bfloat16) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t *>(&h);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// One row as the kernels walk it.
+template <typename T>
+struct Row {
+  const T *at0;  // 16-byte aligned: element u sits at at0 + u
+  int shift;     // u of element 0
+  int vocab;
+
+  __device__ __forceinline__ Row(const void *data, int64_t r, int64_t stride, int v) {
+    const T *p = static_cast<const T *>(data) + r * stride;
+    shift = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
+    at0 = p - shift;
+    vocab = v;
+  }
+  __device__ __forceinline__ int end() const { return shift + vocab; }
+  __device__ __forceinline__ bool whole(int u0) const {
+    return u0 >= shift && u0 + VecOf<T>::N <= end();
+  }
+  // The vector at u0 (a multiple of its size); elements off the row's ends
+  // read `fill`.
+  __device__ __forceinline__ void load(int u0, float (&z)[VecOf<T>::N], float fill) const {
+    if (whole(u0)) {
+      unpack16(*reinterpret_cast<const uint4 *>(at0 + u0), z, T());
+    } else {
+#pragma unroll
+      for (int i = 0; i < VecOf<T>::N; ++i)
+        z[i] = u0 + i >= shift && u0 + i < end() ? logit_float(at0[u0 + i]) : fill;
+    }
+  }
+};
+
+// ---------------------------------------------------------- adjustments --
+// One row's adjustments, resolved from rans_adjust.
+struct RowAdjust {
+  float repetition, frequency, presence, inv_temperature;
+  const int32_t *history;  // the row's window
+  int64_t history_n;
+  const int32_t *bias_ids;
+  const float *bias_values;
+  int64_t bias_n;
+  const uint32_t *mask;  // the row's words, or NULL
+  int mask_words;
+
+  __device__ __forceinline__ bool touches() const { return history_n > 0 || bias_n > 0; }
+};
+
+__device__ __forceinline__ int64_t clip_window(const int64_t *begin, const int64_t *end,
+                                               int64_t r, int64_t len, int64_t &b) {
+  b = begin[r];
+  int64_t e = end[r];
+  b = b < 0 ? 0 : (b > len ? len : b);
+  e = e > len ? len : e;
+  return e > b ? e - b : 0;
+}
+
+__device__ __forceinline__ RowAdjust row_adjust(const rans_adjust &a, int64_t r, int vocab) {
+  RowAdjust x;
+  x.repetition = a.repetition;
+  x.frequency = a.frequency;
+  x.presence = a.presence;
+  x.inv_temperature = a.inv_temperature;
+  if (a.params) {
+    const float *p = a.params + 4 * r;
+    x.repetition = p[0];
+    x.frequency = p[1];
+    x.presence = p[2];
+    x.inv_temperature = p[3];
+  }
+  int64_t b = 0;
+  x.history = nullptr;
+  x.history_n = 0;
+  if (a.history) {
+    x.history_n = clip_window(a.history_begin, a.history_end, r, a.history_len, b);
+    x.history = a.history + b;
+  }
+  x.bias_ids = nullptr;
+  x.bias_values = nullptr;
+  x.bias_n = 0;
+  if (a.bias_ids) {
+    x.bias_n = clip_window(a.bias_begin, a.bias_end, r, a.bias_len, b);
+    x.bias_ids = a.bias_ids + b;
+    x.bias_values = a.bias_values + b;
+  }
+  x.mask = a.mask ? a.mask + r * a.mask_stride : nullptr;
+  x.mask_words = (vocab + 31) >> 5;
+  return x;
+}
+
+// Mask bits of tokens v0 .. v0 + 31 in bits 0 .. 31 (0 off the row's ends; v0
+// may be a few tokens below 0 where a row's first vector is partial).
+__device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int words, int v0) {
+  const int w = v0 >> 5;
+  const uint32_t lo = w >= 0 && w < words ? mask[w] : 0u;
+  const int s = v0 & 31;
+  if (s <= 24) return lo >> s;  // the callers use 8 bits at most
+  const uint32_t hi = w + 1 < words ? mask[w + 1] : 0u;
+  return __funnelshift_r(lo, hi, s);
+}
+
+// Which of kTouchSpan consecutive tokens a row's history and biases touch.
+// Counts and bias entries sit in shared memory, one cell per token (a hash
+// would need a bound on the distinct tokens of a window); a bitmap beside them
+// lets the untouched majority pass with one test per vector.
+constexpr int kTouchSpan = 8192;
+
+struct TouchTable {
+  uint32_t bits[kTouchSpan / 32];
+  uint32_t count[kTouchSpan];
+  uint32_t bias[kTouchSpan];  // 1 + the last entry's position in the row's list
+};
+
+// Fills the table for u in [u_lo, u_lo + kTouchSpan); every thread of the
+// block calls it.  Integer adds, maxima and ors: the result does not depend on
+// the threads' order.
+__device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, int shift,
+                                           int vocab, int u_lo, int tid, int threads) {
+  __syncthreads();
+  for (int i = tid; i < kTouchSpan / 32; i += threads) t.bits[i] = 0;
+  uint4 *c = reinterpret_cast<uint4 *>(t.count);
+  for (int i = tid; i < kTouchSpan / 4; i += threads) c[i] = make_uint4(0, 0, 0, 0);
+  if (a.bias_n > 0) {
+    uint4 *b = reinterpret_cast<uint4 *>(t.bias);
+    for (int i = tid; i < kTouchSpan / 4; i += threads) b[i] = make_uint4(0, 0, 0, 0);
+  }
+  __syncthreads();
+  for (int64_t i = tid; i < a.history_n; i += threads) {
+    const int v = a.history[i];
+    if (v < 0 || v >= vocab) continue;
+    const int k = v + shift - u_lo;
+    if (k < 0 || k >= kTouchSpan) continue;
+    atomicAdd(&t.count[k], 1u);
+    atomicOr(&t.bits[k >> 5], 1u << (k & 31));
+  }
+  for (int64_t i = tid; i < a.bias_n; i += threads) {
+    const int v = a.bias_ids[i];
+    if (v < 0 || v >= vocab) continue;
+    const int k = v + shift - u_lo;
+    if (k < 0 || k >= kTouchSpan) continue;
+    atomicMax(&t.bias[k], (uint32_t)i + 1u);
+    atomicOr(&t.bits[k >> 5], 1u << (k & 31));
+  }
+  __syncthreads();
+}
+
+// The penalties and bias of one touched token (cell k of the table).
+__device__ __forceinline__ float touched_logit(float z, const TouchTable &t, const RowAdjust &a,
+                                               int k) {
+  const uint32_t n = t.count[k];
+  if (n > 0) {
+    z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
+    z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(n), a.frequency), a.presence));
+  }
+  if (a.bias_n > 0) {
+    const uint32_t e = t.bias[k];
+    if (e > 0) z = __fadd_rn(z, a.bias_values[e - 1]);
+  }
+  return z;
+}
+
+// Penalties and biases of a vector at u0 (u0 - u_lo inside the table).
+template <int N>
+__device__ __forceinline__ void touch_vector(float (&z)[N], const TouchTable &t,
+                                             const RowAdjust &a, int k0) {
+  const uint32_t hit = (t.bits[k0 >> 5] >> (k0 & 31)) & ((1u << N) - 1u);
+  if (hit == 0) return;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (hit >> i & 1) z[i] = touched_logit(z[i], t, a, k0 + i);
+}
+
+// -inf where the row's mask is 0.
+template <int N>
+__device__ __forceinline__ void mask_vector(float (&z)[N], const RowAdjust &a, int v0) {
+  const uint32_t ok = mask_bits(a.mask, a.mask_words, v0);
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (!(ok >> i & 1)) z[i] = kNegInf;
+}
+
+}  // namespace rb

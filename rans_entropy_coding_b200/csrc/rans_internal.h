@@ -64,6 +64,36 @@ int launch_decode(const uint8_t *in, uint64_t in_bytes, const uint64_t *offsets,
 int launch_debug_divide(const uint64_t *x, const uint32_t *f, int64_t n, uint64_t *q,
                         uint32_t *r, cudaStream_t st);
 
+// Adjusted logits into out (dtype RANS_LOGITS_*).
+int launch_adjust(const rans_logits &in, const rans_adjust &adj, void *out, int out_dtype,
+                  int64_t out_stride, cudaStream_t st);
+// One token's interval per row; rows of one decoding step; streams of
+// intervals into scratch slots (lengths in lens, as launch_encode); decoder
+// states of S streams and their check at the end.
+int launch_token_intervals(const rans_logits &in, const rans_adjust &adj, const int32_t *tokens,
+                           uint32_t *starts, uint32_t *freqs, int32_t *status, cudaStream_t st);
+int launch_decode_tokens(const rans_logits &in, const rans_adjust &adj, const uint8_t *data,
+                         uint64_t data_bytes, const uint64_t *offsets, int64_t S,
+                         const int32_t *stream_ids, const uint64_t *states_in,
+                         uint64_t *states_out, int32_t *tokens, int32_t *status,
+                         cudaStream_t st);
+int launch_encode_intervals(const uint32_t *starts, const uint32_t *freqs, const Geom &g,
+                            char *scratch, uint64_t *lens, int32_t *status, cudaStream_t st);
+int launch_token_states(const uint8_t *in, uint64_t in_bytes, const uint64_t *offsets, int64_t S,
+                        uint64_t *states, int32_t *status, cudaStream_t st);
+int launch_token_finish(const uint64_t *offsets, int64_t S, const uint64_t *states,
+                        int32_t *status, cudaStream_t st);
+// The distillation loss per row with its figures, and the gradient from them.
+int launch_distill_forward(const rans_logits &in, const int32_t *ids, const float *lp, int K,
+                           float inv_t, int tail, float *losses, float *stats, int32_t *status,
+                           cudaStream_t st);
+int launch_distill_backward(const rans_logits &in, const int32_t *ids, const float *lp, int K,
+                            float inv_t, const float *stats, const float *grads, void *grad,
+                            int64_t stride, cudaStream_t st);
+int launch_distill(const rans_logits &in, const int32_t *ids, const float *lp, int K,
+                   float inv_t, int tail, const float *grads, float *losses, void *grad,
+                   int64_t stride, int32_t *status, cudaStream_t st);
+
 // A tensor map (CUtensorMap, 128 bytes, 64-byte aligned) for a 3-D int32
 // tensor of width x height x depth elements (row-major, width fastest) and a
 // box of box_w x box_h x 1; base 16-byte aligned, width * 4 a multiple of 16.

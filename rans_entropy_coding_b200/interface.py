@@ -10,6 +10,7 @@ Argument marshalling only: every coding step runs in librans_b200's kernels.
 import torch
 
 from . import _lib as L
+from . import tokens as T
 
 _SYM = {torch.int32, torch.int16, torch.uint8}
 
@@ -106,6 +107,70 @@ class RansCoder:
     def _need_tables(self):
         if self.tables is None:
             raise RuntimeError("set the rows first (set_scale_table, set_pmfs or set_cdfs)")
+
+
+class TokenCoder:
+    """Texts coded under a language model's logits, one stream per text.
+
+    Encoding: ``add`` rows of logits with their tokens as the model yields
+    them, the texts one after another, then ``streams`` once.  Decoding:
+    ``begin`` with the streams, then one ``step`` per position with the logits
+    that follow from the tokens so far, then ``finish``.  Both sides must see
+    the same logits, bit for bit, and the same adjustments; a row's interval
+    does not depend on the batch it comes in.
+    """
+
+    def __init__(self, device="cuda"):
+        self.device = torch.device(device)
+        self.status = T.new_status(self.device)
+        self._parts = []
+        self._in = None
+
+    def add(self, logits, tokens, adjust=None):
+        """Intervals of the next tokens.len() positions."""
+        tokens = torch.as_tensor(tokens, dtype=torch.int32, device=self.device).reshape(-1)
+        self._parts.append(T.token_intervals(logits, tokens, adjust, status=self.status))
+        return self
+
+    def streams(self, lengths):
+        """(data, stream_offsets) of the texts added so far, of these lengths
+        (summing to the positions added); device errors raise."""
+        starts = torch.cat([p[0] for p in self._parts]) if self._parts else \
+            torch.empty(0, dtype=torch.int32, device=self.device)
+        freqs = torch.cat([p[1] for p in self._parts]) if self._parts else starts.clone()
+        cuts = [0]
+        for n in lengths:
+            cuts.append(cuts[-1] + int(n))
+        if cuts[-1] != starts.numel() or min(lengths, default=0) < 0:
+            raise ValueError("lengths sum to %d, %d positions added" % (cuts[-1], starts.numel()))
+        L.check(L.rans_get_status(self.status), "token_intervals")
+        cuts = torch.tensor(cuts, dtype=torch.int64, device=self.device)
+        out, offs, ws = T.encode_intervals(starts, freqs, L.Chunking.explicit(cuts))
+        L.check(L.rans_get_status(ws), "encode_intervals")
+        self._parts = []
+        return out[:int(offs[-1].item())].clone(), offs
+
+    def begin(self, data, stream_offsets):
+        data = torch.as_tensor(data, dtype=torch.uint8).to(self.device).contiguous()
+        offs = torch.as_tensor(stream_offsets, dtype=torch.int64).to(self.device).contiguous()
+        self._in = (data, offs)
+        self.states = T.token_states(data, offs, self.status)
+        return self
+
+    def step(self, logits, adjust=None, stream_ids=None):
+        """Next tokens (int32 [rows]); row r belongs to stream stream_ids[r]
+        (default r; -1 skips the row)."""
+        if self._in is None:
+            raise RuntimeError("begin with the streams first")
+        tokens, _ = T.decode_tokens(logits, *self._in, self.states, adjust, stream_ids,
+                                    out_states=self.states, status=self.status)
+        return tokens
+
+    def finish(self):
+        """Raises unless every stream was decoded without an error and to its
+        end."""
+        L.check(T.rans_token_states_finish(self._in[1], self.states, self.status), "finish")
+        L.check(L.rans_get_status(self.status), "decode_tokens")
 
 
 def to_byte_strings(data, stream_offsets):

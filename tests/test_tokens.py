@@ -1,0 +1,204 @@
+"""Tokens under a model's logits, without a GPU: refusals at the C entry
+points and in the Python layer, the mask packing, and the oracle's own coder."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+import rans_entropy_coding_b200 as rb
+import token_oracle as TO
+from rans_entropy_coding_b200 import build as rbuild
+
+P = 1 << 20  # an address that nothing reads: every call here is refused on the host
+
+
+@pytest.fixture(scope="module")
+def lib():
+    rbuild.build()
+    return rb.lib()
+
+
+def logits(data=P, dtype=0, vocab=100, rows=4, stride=100):
+    c = rb.rans_logits()
+    c.data, c.dtype, c.vocab, c.rows, c.row_stride = data, dtype, vocab, rows, stride
+    return c
+
+
+def adjust(**kw):
+    c = rb.rans_adjust()
+    c.repetition = c.inv_temperature = 1.0
+    for k, v in kw.items():
+        setattr(c, k, v)
+    return c
+
+
+BAD_LOGITS = [dict(data=None), dict(dtype=3), dict(dtype=-1), dict(vocab=0),
+              dict(vocab=rb.MAX_VOCAB + 1, stride=rb.MAX_VOCAB + 1), dict(rows=-1),
+              dict(stride=99), dict(data=P + 2)]
+BAD_ADJUST = [dict(repetition=0.0), dict(repetition=float("inf")), dict(repetition=float("nan")),
+              dict(inv_temperature=0.0), dict(inv_temperature=-1.0),
+              dict(inv_temperature=float("inf")), dict(frequency=float("nan")),
+              dict(presence=float("inf")), dict(history=P), dict(history=P, history_begin=P),
+              dict(history=P, history_begin=P, history_end=P, history_len=-1), dict(bias_ids=P),
+              dict(bias_ids=P, bias_values=P, bias_begin=P),
+              dict(bias_ids=P, bias_values=P, bias_begin=P, bias_end=P, bias_len=-1),
+              dict(mask=P, mask_stride=3), dict(mask=P, mask_stride=-4)]
+
+
+def calls(lib, lg, ad=None):
+    """Every entry point that takes logits, with good other arguments."""
+    a = None if ad is None else ctypes.byref(ad)
+    x = ctypes.byref(lg)
+    yield lib.rans_adjust_logits(x, a, P + (8 << 20), 0, 100, None)
+    yield lib.rans_token_intervals(x, a, P, P, P, P, None)
+    yield lib.rans_decode_tokens(x, a, P, 64, P, 8, None, P, P, P, P, None)
+    if ad is None:
+        yield lib.rans_distill_forward(x, P, P, 5, 1.0, 1, P, P, P, None)
+        yield lib.rans_distill_backward(x, P, P, 5, 1.0, P, P, P + (8 << 20), 100, None)
+        yield lib.rans_distill(x, P, P, 5, 1.0, 1, P, P, P + (8 << 20), 100, P, None)
+
+
+@pytest.mark.parametrize("bad", BAD_LOGITS, ids=str)
+def test_bad_logits_are_refused(lib, bad):
+    assert list(calls(lib, logits(**bad))) == [rb.ERR_ARG] * 6
+
+
+@pytest.mark.parametrize("bad", BAD_ADJUST, ids=str)
+def test_bad_adjustments_are_refused(lib, bad):
+    assert list(calls(lib, logits(), adjust(**bad))) == [rb.ERR_ARG] * 3
+
+
+def test_no_rows_do_nothing(lib):
+    assert list(calls(lib, logits(rows=0, data=None))) == [rb.OK] * 6
+    x = ctypes.byref(logits(rows=0, data=None))
+    assert lib.rans_adjust_logits(x, None, None, 0, 0, None) == rb.OK
+    assert lib.rans_token_states(None, 0, P, 0, None, P, None) == rb.OK
+    assert lib.rans_token_states_finish(None, 0, None, P, None) == rb.OK
+
+
+def test_results_that_overlap_are_refused(lib):
+    x = logits(rows=3, vocab=100, stride=256)
+
+    def result(out, dtype=0, stride=256, lg=x):
+        return lib.rans_adjust_logits(ctypes.byref(lg), None, out, dtype, stride, None)
+
+    assert result(P, dtype=1) == rb.ERR_ARG              # in place with another type
+    assert result(P, stride=300) == rb.ERR_ARG           # or another stride
+    assert result(P + 4) == rb.ERR_ARG                   # shifted by one element
+    assert result(P + 4 * 99) == rb.ERR_ARG
+    assert result(P - 4 * 99) == rb.ERR_ARG
+    assert result(P + 4 * 157) == rb.ERR_ARG             # its row 0 reaches row 1
+    assert result(P + 4 * 355) == rb.ERR_ARG             # the last element of row 1
+    assert result(P + 4, lg=logits(rows=1)) == rb.ERR_ARG
+    assert result(0) == rb.ERR_ARG
+    assert result(P + (1 << 20), dtype=7) == rb.ERR_ARG
+    assert result(P + (1 << 20), stride=99) == rb.ERR_ARG
+    assert result(P + (1 << 20) + 2) == rb.ERR_ARG       # not aligned to the type
+    assert lib.rans_distill(ctypes.byref(x), P, P, 5, 1.0, 1, P, P, P + 4, 256, P,
+                            None) == rb.ERR_ARG
+    assert lib.rans_distill_backward(ctypes.byref(x), P, P, 5, 1.0, P, P, P + 4, 256,
+                                     None) == rb.ERR_ARG
+
+
+def test_bad_pointers_and_counts_are_refused(lib):
+    x = ctypes.byref(logits())
+    S = rb.ERR_ARG
+    for k in (3, 4, 5):  # tokens, starts, freqs
+        args = [x, None, P, P, P, P, None]
+        args[k - 1] = None
+        assert lib.rans_token_intervals(*args) == S
+    assert lib.rans_token_intervals(x, None, P, P, P, P + 8, None) == S   # status alignment
+    assert lib.rans_token_intervals(x, None, P, P, P, None, None) == S
+    good = [x, None, P, 64, P, 8, None, P, P, P, P, None]
+    for k, v in ((2, None), (2, P + 2), (4, None), (5, -1), (5, 3), (7, None), (8, None),
+                 (9, None), (10, None), (10, P + 4)):
+        args = list(good)
+        args[k] = v
+        assert lib.rans_decode_tokens(*args) == S, (k, v)
+    assert lib.rans_token_states(P, 64, None, 2, P, P, None) == S
+    assert lib.rans_token_states(P, 64, P, 2, None, P, None) == S
+    assert lib.rans_token_states(P + 1, 64, P, 2, P, P, None) == S
+    assert lib.rans_token_states_finish(P, 2, None, P, None) == S
+    assert lib.rans_token_states_finish(P, -1, P, P, None) == S
+    for K in (0, -1, rb.MAX_TOP + 1):
+        assert lib.rans_distill_forward(x, P, P, K, 1.0, 1, P, P, P, None) == S
+    for t in (0.0, -1.0, float("inf"), float("nan")):
+        assert lib.rans_distill_forward(x, P, P, 4, t, 1, P, P, P, None) == S
+    assert lib.rans_distill_forward(x, P, P, 4, 1.0, 1, P, P + 8, P, None) == S  # stats alignment
+    assert lib.rans_distill_forward(x, None, P, 4, 1.0, 1, P, P, P, None) == S
+    assert lib.rans_distill(x, P, P, 4, 1.0, 1, None, P, P + (1 << 20), 100, P, None) == S
+
+
+def test_encode_intervals_refusals(lib):
+    def call(ch, starts=P, freqs=P, n=10, out=P, cap=4096, offs=P, ws=P, ws_bytes=1 << 20):
+        return lib.rans_encode_intervals(starts, freqs, n, ctypes.byref(ch.c), out, cap, offs, ws,
+                                         ws_bytes, None)
+
+    one = rb.Chunking.contig(2)
+    assert call(rb.Chunking.contig(2, interleave=32)) == rb.ERR_ARG
+    assert call(rb.Chunking.contig(2, index_block=2)) == rb.ERR_ARG
+    assert call(rb.Chunking.contig(2, fmt="rans32_16")) == rb.ERR_ARG
+    assert call(rb.Chunking.contig(2, alias=True)) == rb.ERR_ARG
+    assert call(rb.Chunking.tiled((1, 1, 2, 5), 1, 2, 5, interleave=1)) == rb.ERR_ARG
+    assert call(one, starts=None) == rb.ERR_ARG
+    assert call(one, out=P + 2) == rb.ERR_ARG
+    assert call(one, ws=P + 16) == rb.ERR_ARG
+    assert call(one, offs=None) == rb.ERR_ARG
+    assert call(one, n=-1) == rb.ERR_ARG
+    assert call(one, ws_bytes=256) == rb.ERR_CAPACITY
+
+
+def test_python_layer_refuses_host_tensors_and_bad_shapes():
+    x = torch.zeros(2, 8)
+    with pytest.raises(ValueError):
+        rb.adjust_logits(x, rb.LogitAdjust())
+    with pytest.raises(ValueError):
+        rb.distill_loss(x, torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1))
+    for kw in (dict(temperature=0.0), dict(temperature=float("nan")), dict(repetition=-1.0),
+               dict(frequency=float("inf")), dict(temperature=float("inf"))):
+        with pytest.raises(ValueError):
+            rb.LogitAdjust(**kw)
+    with pytest.raises(ValueError):   # host tensors
+        rb.LogitAdjust(mask=torch.zeros(4, dtype=torch.int32))
+    with pytest.raises(ValueError):   # wrong type
+        rb.LogitAdjust(mask=torch.zeros(4, dtype=torch.int64))
+
+
+@pytest.mark.parametrize("vocab", [1, 31, 32, 33, 100])
+def test_pack_mask(vocab):
+    g = torch.Generator().manual_seed(vocab)
+    ok = torch.rand(3, vocab, generator=g) < 0.5
+    words = rb.pack_mask(ok)
+    assert words.dtype == torch.int32 and words.shape == (3, (vocab + 31) // 32)
+    for r in range(3):
+        assert np.array_equal(TO.allowed(dict(mask=words.numpy()), r, vocab), ok[r].numpy())
+    assert torch.equal(rb.pack_mask(ok[1]), words[1])
+
+
+def test_oracle_intervals_tile_the_range_and_follow_the_softmax():
+    rng = np.random.default_rng(3)
+    row = rng.normal(0, 3, 500).astype(np.float32)
+    row[7] = -np.inf
+    adj = dict(temperature=0.7)
+    b = TO.bounds(row, adj, 0)
+    f = np.diff(np.array(b))
+    assert b[0] == 0 and b[-1] == 1 << 24 and f[7] == 0 and (np.delete(f, 7) >= 1).all()
+    z = row.astype(np.float64) / 0.7
+    p = np.exp(z - z.max())
+    p /= p.sum()
+    # 2^f to 1.02e-4 (also in the sum), a weight's rounding half a unit of 2^21
+    # times the largest weight's share, the room given up for N ones, flooring
+    bound = 2.1e-4 * p + 0.5 * 2.0 ** -21 * (1 + 500 * p) + 500 * 2.0 ** -24 * p + 2.0 ** -24 * 2
+    assert (np.abs(f * 2.0 ** -24 - p) <= bound).all()
+
+
+def test_oracle_coder_round_trip():
+    rng = np.random.default_rng(4)
+    row = rng.normal(0, 4, 300).astype(np.float32)
+    b = TO.bounds(row, {}, 0)
+    tokens = rng.integers(0, 300, 200)
+    data = TO.encode([b[t] for t in tokens], [b[t + 1] - b[t] for t in tokens])
+    d = TO.Decoder(data)
+    assert [d.step(b) for _ in tokens] == list(tokens)
+    assert d.x == TO.LOW and d.at == len(d.words)
