@@ -490,7 +490,7 @@ int rans_decode_to_values(const uint8_t *in, uint64_t in_bytes, const uint64_t *
  * per stream) at RANS_TOKEN_PRECISION bits: a token renormalises when
  * x >= 2^39 * freq, then x -> (x / freq) 2^24 + x mod freq + start.
  */
-#define RANS_MAX_VOCAB (1 << 19)
+#define RANS_MAX_VOCAB ((1 << 19) - 8)
 #define RANS_TOKEN_PRECISION 24
 
 /* Logits element types. */

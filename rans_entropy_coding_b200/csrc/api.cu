@@ -4,6 +4,7 @@
 // tokens.cu and distill.cu hold those of tokens under a model's logits.
 #include <cstring>
 #include <mutex>
+#include <utility>
 #include <vector>
 
 #include <nvtx3/nvToolsExt.h>
@@ -55,6 +56,7 @@ struct OccEntry {
 std::mutex g_launch_mutex;
 std::vector<SmemEntry> g_smem_set;
 std::vector<OccEntry> g_occ;
+std::vector<std::pair<const void *, int>> g_cluster_set;
 }  // namespace
 
 cudaError_t ensure_dyn_smem(const void *fn, uint32_t bytes) {
@@ -71,6 +73,18 @@ cudaError_t ensure_dyn_smem(const void *fn, uint32_t bytes) {
     }
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess) g_smem_set.push_back({fn, dev, bytes});
+  return e;
+}
+
+cudaError_t ensure_cluster(const void *fn) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  std::lock_guard<std::mutex> lock(g_launch_mutex);
+  for (const auto &x : g_cluster_set)
+    if (x.first == fn && x.second == dev) return cudaSuccess;
+  e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+  if (e == cudaSuccess) g_cluster_set.push_back({fn, dev});
   return e;
 }
 

@@ -198,34 +198,33 @@ struct TouchTable {
 };
 
 // Fills the table for u in [u_lo, u_lo + kTouchSpan); every thread of the
-// block calls it.  Integer adds, maxima and ors: the result does not depend on
+// block calls it.  Only cells that are touched are ever read, so only those
+// are cleared.  Integer adds, maxima and ors: the result does not depend on
 // the threads' order.
 __device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, int shift,
                                            int vocab, int u_lo, int tid, int threads) {
+  auto cell = [&](int v) {
+    const int k = v + shift - u_lo;
+    return v >= 0 && v < vocab && k >= 0 && k < kTouchSpan ? k : -1;
+  };
   __syncthreads();
   for (int i = tid; i < kTouchSpan / 32; i += threads) t.bits[i] = 0;
-  uint4 *c = reinterpret_cast<uint4 *>(t.count);
-  for (int i = tid; i < kTouchSpan / 4; i += threads) c[i] = make_uint4(0, 0, 0, 0);
-  if (a.bias_n > 0) {
-    uint4 *b = reinterpret_cast<uint4 *>(t.bias);
-    for (int i = tid; i < kTouchSpan / 4; i += threads) b[i] = make_uint4(0, 0, 0, 0);
+  __syncthreads();
+  for (int64_t i = tid; i < a.history_n + a.bias_n; i += threads) {
+    const int k = cell(i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n]);
+    if (k < 0) continue;
+    t.count[k] = 0;
+    t.bias[k] = 0;
+    atomicOr(&t.bits[k >> 5], 1u << (k & 31));
   }
   __syncthreads();
   for (int64_t i = tid; i < a.history_n; i += threads) {
-    const int v = a.history[i];
-    if (v < 0 || v >= vocab) continue;
-    const int k = v + shift - u_lo;
-    if (k < 0 || k >= kTouchSpan) continue;
-    atomicAdd(&t.count[k], 1u);
-    atomicOr(&t.bits[k >> 5], 1u << (k & 31));
+    const int k = cell(a.history[i]);
+    if (k >= 0) atomicAdd(&t.count[k], 1u);
   }
   for (int64_t i = tid; i < a.bias_n; i += threads) {
-    const int v = a.bias_ids[i];
-    if (v < 0 || v >= vocab) continue;
-    const int k = v + shift - u_lo;
-    if (k < 0 || k >= kTouchSpan) continue;
-    atomicMax(&t.bias[k], (uint32_t)i + 1u);
-    atomicOr(&t.bits[k >> 5], 1u << (k & 31));
+    const int k = cell(a.bias_ids[i]);
+    if (k >= 0) atomicMax(&t.bias[k], (uint32_t)i + 1u);
   }
   __syncthreads();
 }
@@ -238,10 +237,8 @@ __device__ __forceinline__ float touched_logit(float z, const TouchTable &t, con
     z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
     z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(n), a.frequency), a.presence));
   }
-  if (a.bias_n > 0) {
-    const uint32_t e = t.bias[k];
-    if (e > 0) z = __fadd_rn(z, a.bias_values[e - 1]);
-  }
+  const uint32_t e = t.bias[k];
+  if (e > 0) z = __fadd_rn(z, a.bias_values[e - 1]);
   return z;
 }
 

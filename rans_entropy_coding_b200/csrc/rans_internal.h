@@ -110,6 +110,8 @@ int smem_optin(int device);
 // dynamic shared memory limit to at least `bytes`, and its resident blocks
 // per SM at `threads` threads and `smem` bytes of dynamic shared memory.
 cudaError_t ensure_dyn_smem(const void *fn, uint32_t bytes);
+// Allow the kernel clusters of up to 16 blocks (8 is the portable limit).
+cudaError_t ensure_cluster(const void *fn);
 cudaError_t blocks_per_sm(int *out, const void *fn, int threads, uint32_t smem);
 
 }  // namespace rb

@@ -7,6 +7,8 @@
 // kernel (and any other IEEE machine) gets the same one; all sums are of
 // integers, so neither the split of a row over threads nor the order of
 // additions can change an interval.
+#include <type_traits>
+
 #include "logits_common.cuh"
 #include "rans_common.cuh"
 #include "rans_internal.h"
@@ -91,22 +93,148 @@ __device__ __forceinline__ bool starts_by(uint64_t c, uint32_t r, uint64_t total
 }
 
 // ------------------------------------------------------------------ rows --
-constexpr int kTokThreads = 512;
-constexpr int kTokWarps = kTokThreads / 32;
-constexpr int kTokMaxSpans = RANS_MAX_VOCAB / kTouchSpan + 1;
+// A row is shared by a cluster of 1 to kMaxCluster blocks, which exchange its
+// maximum and then its sums through each other's shared memory.  Weights are
+// relative to the maximum, so the row is walked twice; the second walk finds
+// it in L2 (or L1).  What bounds the kernel with many rows is not the memory
+// but the format's own roundings, about ten instructions per logit.
+// A warp takes "tiles" of 32 lanes x kTileVecs vectors of 16 bytes, lane after
+// lane and vector row after vector row, so that a tile is a run of consecutive
+// tokens whose sums a decoding row keeps.
+constexpr int kTileVecs = 4;
+constexpr int kRowThreads = 512;  // most threads of a block
+constexpr int kRowWarps = kRowThreads / 32;
+constexpr int kMaxCluster = 16;
 
 struct Sums {
   uint64_t w;
   uint32_t n;
 };
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) { return {a.w + b.w, a.n + b.n}; }
 
-__device__ __forceinline__ Sums warp_sum(Sums s) {
+__device__ __forceinline__ Sums warp_total(Sums v) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    s.w += __shfl_xor_sync(kFull, s.w, o);
-    s.n += __shfl_xor_sync(kFull, s.n, o);
+  for (int o = 16; o > 0; o >>= 1) v.w += __shfl_xor_sync(kFull, v.w, o);
+  v.n = __reduce_add_sync(kFull, v.n);
+  return v;
+}
+// Sums of this lane and the ones below it.
+__device__ __forceinline__ Sums warp_scan(Sums v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint64_t w = __shfl_up_sync(kFull, v.w, o);
+    const uint32_t n = __shfl_up_sync(kFull, v.n, o);
+    if (lane >= o) v = v + Sums{w, n};
   }
-  return s;
+  return v;
+}
+
+// A warp's sums on their way to another block.
+struct WarpSums {
+  uint64_t w, below_w;  // weights of all its tokens; of those below the coded one
+  uint32_t n, below_n;  // alive tokens
+};
+
+__device__ __forceinline__ float warp_max_nan(float x) {
+  float y;
+  asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The larger (NaN if either is) and the smaller of packed pairs.
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __half) {
+  uint32_t c;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __half) {
+  uint32_t c;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t c;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t c;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
+// Running extremes of raw vectors, in the type they come in.
+template <typename T>
+struct Extremes {
+  uint32_t top = sizeof(T) == 2 ? (std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u)
+                                : 0xff800000u;
+  uint32_t low = top & 0x7fff7fffu;
+  __device__ __forceinline__ void take(const uint4 &q) {
+    if constexpr (sizeof(T) == 2) {
+      top = pair_max(top, pair_max(pair_max(q.x, q.y, T()), pair_max(q.z, q.w, T()), T()), T());
+      low = pair_min(low, pair_min(pair_min(q.x, q.y, T()), pair_min(q.z, q.w, T()), T()), T());
+    } else {
+      float z[4];
+      unpack16(q, z, T());
+      float a = __uint_as_float(top), b = __uint_as_float(low);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        a = max_nan(a, z[i]);
+        b = fminf(b, z[i]);
+      }
+      top = __float_as_uint(a);
+      low = __float_as_uint(b);
+    }
+  }
+  __device__ __forceinline__ static float2 both(uint32_t x) {
+    if constexpr (sizeof(T) == 2) {
+      float z[8];
+      unpack16(make_uint4(x, 0, 0, 0), z, T());
+      return make_float2(z[0], z[1]);
+    } else {
+      return make_float2(__uint_as_float(x), __uint_as_float(x));
+    }
+  }
+  __device__ __forceinline__ float largest() const {
+    const float2 f = both(top);
+    return max_nan(f.x, f.y);
+  }
+  __device__ __forceinline__ float smallest() const {
+    const float2 f = both(low);
+    return fminf(f.x, f.y);
+  }
+};
+
+// Two weights without the clamp (d >= -64 is the caller's to know), each with
+// the bits of 2^23 still on top.  A product is written as a * b + zero2, where
+// zero2 holds two -0 that the compiler does not know: it makes a packed product
+// and the packed sum behind it (an explicit .rn on both, a literal -0, or
+// -fmad=false notwithstanding) into one multiply-add, and half of all results
+// then differ from the two roundings of the format.
+__device__ __forceinline__ uint2 raw_weights(float a, float b, uint64_t scale2, uint64_t ymax2,
+                                             uint64_t zero2) {
+  uint64_t z, d, t, k, f, p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(a), "f"(b));
+  auto both = [](float c) {
+    return (uint64_t)__float_as_uint(c) << 32 | __float_as_uint(c);
+  };
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(z), "l"(scale2), "l"(zero2));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(d), "l"(ymax2));  // ymax2 holds -ymax
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(t) : "l"(d), "l"(both(kRound)));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(k) : "l"(t), "l"(both(-kRound)));
+  // f = d - k is exact, so this product and sum round as the difference does
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(f) : "l"(k), "l"(both(-1.0f)), "l"(d));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(f), "l"(both(kC3)), "l"(zero2));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(p), "l"(both(kC2)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(f), "l"(zero2));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(p), "l"(both(kC1)));
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(p), "l"(f), "l"(zero2));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(p), "l"(both(kScaleW)));
+  const uint32_t lo = (uint32_t)p + ((uint32_t)t << 23);
+  const uint32_t hi = (uint32_t)(p >> 32) + ((uint32_t)(t >> 32) << 23);
+  p = (uint64_t)hi << 32 | lo;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(p), "l"(both(kUnit)));
+  return make_uint2((uint32_t)p, (uint32_t)(p >> 32));
 }
 
 // Where a decoding row's symbol comes from.
@@ -121,267 +249,421 @@ struct Coded {
   int32_t *tokens;
 };
 
-// One block per row.  Pass 1 finds the row's maximum, pass 2 its sums; an
-// encoding row also sums what lies below its token, a decoding row keeps the
-// sums of every span and looks for its slot in the span that holds it.
-template <typename T, bool DECODE>
-__global__ void __launch_bounds__(kTokThreads)
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// The address of a block's shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t peer_address(const void *p, uint32_t rank) {
+  uint32_t a;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;"
+      : "=r"(a)
+      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void peer_store(uint32_t a, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+
+__device__ __forceinline__ void peer_store(uint32_t a, uint64_t x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
+}
+
+// The streams' side of a decoding row: a token whose interval is [s, s + f).
+__device__ __forceinline__ void take_token(const Coded &cd, int64_t r, int64_t stream, uint64_t x,
+                                           uint64_t taken, int token, uint32_t s, uint32_t f,
+                                           int32_t *status) {
+  uint64_t y = (uint64_t)f * (x >> kTokPrec) + (x & (kTokTotal - 1)) - s;
+  uint64_t used = taken;
+  if (y < kL) {
+    const uint64_t off = cd.offsets[stream], lim = cd.offsets[stream + 1];
+    const bool ok = !(off & 3) && off <= lim && lim <= cd.in_bytes && taken < (lim - off) / 4;
+    if (ok) {
+      y = y << 32 | reinterpret_cast<const uint32_t *>(cd.in)[off / 4 + taken];
+      used = taken + 1;
+    } else {
+      report(status, RANS_ERR_CORRUPT, stream);
+      token = -1;
+      y = x;
+    }
+  }
+  cd.tokens[r] = token;
+  cd.states_out[2 * stream] = y;
+  cd.states_out[2 * stream + 1] = used;
+}
+
+// One cluster per row.  ADJ: with penalties, biases or a mask.
+template <typename T, bool DECODE, bool ADJ>
+__global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     token_rows_kernel(rans_logits in, rans_adjust adj, const int32_t *tokens, uint32_t *starts,
-                      uint32_t *freqs, Coded cd, int32_t *status) {
+                      uint32_t *freqs, Coded cd, int32_t *status, int slice, uint64_t zero2) {
   extern __shared__ __align__(16) unsigned char smem[];
-  TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
-  __shared__ float red_max[kTokWarps];
-  __shared__ Sums red[kTokWarps], red2[kTokWarps];
-  __shared__ Sums span_sum[kTokMaxSpans];
-  __shared__ uint32_t own_weight;
   constexpr int N = VecOf<T>::N;
+  constexpr int kVecRow = 32 * N;                // tokens of a warp's vectors
+  constexpr int kTile = kVecRow * kTileVecs;
+  TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
+  uint2 *tile_sums = reinterpret_cast<uint2 *>(smem + (ADJ ? sizeof(TouchTable) : 0));
+  __shared__ float peer_max[kMaxCluster * kRowWarps];
+  __shared__ WarpSums peer_sums[kMaxCluster * kRowWarps];
+  __shared__ uint32_t own_weight;
+  __shared__ int found_tile;
+  __shared__ Sums found_base, found_all;
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
-  const int64_t r = blockIdx.x;
+  const int threads = blockDim.x, warps = threads >> 5;
+  const uint32_t rank = cluster_rank(), peers = cluster_size();
+  const int64_t r = blockIdx.x / peers;
   const Row<T> row(in.data, r, in.row_stride, in.vocab);
-  const RowAdjust a = row_adjust(adj, r, in.vocab);
-  const bool touch = a.touches();
 
   int target = -1;
   int64_t stream = r;
   uint64_t x = 0, taken = 0;
+  // every block of a row finds the same, and all leave before their first
+  // barrier or none
+  auto refuse = [&](int code, int64_t detail, bool state) {
+    if (rank != 0 || tid != 0) return;
+    report(status, code, detail);
+    if constexpr (DECODE) {
+      cd.tokens[r] = -1;
+      if (state) {
+        cd.states_out[2 * stream] = x;
+        cd.states_out[2 * stream + 1] = taken;
+      }
+    } else {
+      starts[r] = 0;
+      freqs[r] = 0;
+    }
+  };
   if constexpr (DECODE) {
     if (cd.stream_ids) stream = cd.stream_ids[r];
     if (stream == -1) return;
     int bad = stream < 0 || stream >= cd.S;
-    if (!bad && cd.stream_ids)
-      for (int64_t i = tid; i < in.rows; i += kTokThreads)
+    if (!bad && cd.stream_ids) {
+      for (int64_t i = tid; i < in.rows; i += threads)
         bad |= i != r && cd.stream_ids[i] == (int32_t)stream;
-    bad = __syncthreads_or(bad);
-    if (bad) {
-      if (tid == 0) {
-        report(status, RANS_ERR_INDEX, r);
-        cd.tokens[r] = -1;
-      }
-      return;
+      bad = __syncthreads_or(bad);
     }
+    if (bad) return refuse(RANS_ERR_INDEX, r, false);
     x = cd.states_in[2 * stream];
     taken = cd.states_in[2 * stream + 1];
-    __syncthreads();
-    if (x < kL || x >> 63) {
-      if (tid == 0) {
-        report(status, RANS_ERR_CORRUPT, stream);
-        cd.tokens[r] = -1;
-        cd.states_out[2 * stream] = x;
-        cd.states_out[2 * stream + 1] = taken;
-      }
-      return;
-    }
+    if (x < kL || x >> 63) return refuse(RANS_ERR_CORRUPT, stream, true);
   } else {
     target = tokens[r];
     if (target == -1) return;
-    if (target < 0 || target >= in.vocab) {
-      if (tid == 0) {
-        report(status, RANS_ERR_INDEX, r);
-        starts[r] = 0;
-        freqs[r] = 0;
-      }
-      return;
-    }
+    if (target < 0 || target >= in.vocab) return refuse(RANS_ERR_INDEX, r, false);
+  }
+  // a block's shared memory may be written by others once it runs: waited for
+  // below, after the first walk
+  if (peers > 1) {
+    __syncwarp();
+    cluster_arrive();
   }
 
-  // the adjusted logits of the vector at u0
-  auto fetch = [&](int u0, int u_lo, float (&z)[N]) {
-    row.load(u0, z, kNegInf);
-    if (touch) touch_vector<N>(z, table, a, u0 - u_lo);
-    if (a.mask) mask_vector<N>(z, a, u0 - row.shift);
-    if (!row.whole(u0)) {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (u0 + i < row.shift || u0 + i >= row.end()) z[i] = kNegInf;
+  RowAdjust a;
+  bool touch = false;
+  if constexpr (ADJ) {
+    a = row_adjust(adj, r, in.vocab);
+    touch = a.touches();
+  }
+  const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
+  // Walks this block's tiles span by span (one span without a table):
+  // body(tile's first u, its number).
+  constexpr int kSpan = ADJ ? kTouchSpan / kTile * kTile : 1 << 30;
+  int table_at = -1;
+  auto spans = [&](auto body) {
+    for (int u_lo = lo; u_lo < hi; u_lo = kSpan < hi - u_lo ? u_lo + kSpan : hi) {
+      if (ADJ && touch && table_at != u_lo) {
+        fill_touch(table, a, row.shift, in.vocab, u_lo, tid, threads);
+        table_at = u_lo;
+      }
+      const int u_hi = kSpan < hi - u_lo ? u_lo + kSpan : hi;
+      for (int u = u_lo + wid * kTile; u < u_hi; u += warps * kTile) body(u, (u - lo) / kTile);
     }
   };
-
-  float m = kNegInf;
-  for (int u_lo = 0; u_lo < row.end(); u_lo += kTouchSpan) {
-    if (touch) fill_touch(table, a, row.shift, in.vocab, u_lo, tid, kTokThreads);
-    for (int u0 = u_lo + tid * N; u0 < min(u_lo + kTouchSpan, row.end()); u0 += kTokThreads * N) {
-      float z[N];
-      fetch(u0, u_lo, z);
-#pragma unroll
-      for (int i = 0; i < N; ++i) m = max_nan(m, z[i]);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
-  if (lane == 0) red_max[wid] = m;
-  __syncthreads();
-  m = red_max[0];
-  for (int w = 1; w < kTokWarps; ++w) m = max_nan(m, red_max[w]);
-  const RowScale rs = row_scale(m, a.inv_temperature);
-  if (rs.error != RANS_OK) {
-    if (tid == 0) {
-      report(status, rs.error, r);
-      if constexpr (DECODE) {
-        cd.tokens[r] = -1;
-        cd.states_out[2 * stream] = x;
-        cd.states_out[2 * stream + 1] = taken;
-      } else {
-        starts[r] = 0;
-        freqs[r] = 0;
-      }
-    }
-    return;
-  }
-
-  const int u_target = row.shift + target;
-  Sums all = {0, 0}, below = {0, 0};
-  if (tid == 0) own_weight = 0xffffffffu;
-  for (int u_lo = 0, span = 0; u_lo < row.end(); u_lo += kTouchSpan, ++span) {
-    if (touch) fill_touch(table, a, row.shift, in.vocab, u_lo, tid, kTokThreads);
-    else __syncthreads();
-    Sums s = {0, 0};
-    for (int u0 = u_lo + tid * N; u0 < min(u_lo + kTouchSpan, row.end()); u0 += kTokThreads * N) {
-      float z[N];
-      fetch(u0, u_lo, z);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const uint32_t w = token_weight(z[i], rs.scale, rs.ymax);
-        const uint32_t n = z[i] > kNegInf ? 1u : 0u;
-        s.w += w;
-        s.n += n;
-        if constexpr (!DECODE) {
-          if (u0 + i < u_target) {
-            below.w += w;
-            below.n += n;
-          }
-          if (u0 + i == u_target && n) own_weight = w;
-        }
-      }
-    }
-    all.w += s.w;
-    all.n += s.n;
-    if constexpr (DECODE) {
-      s = warp_sum(s);
-      if (lane == 0) red[wid] = s;
-      __syncthreads();
-      if (tid == 0) {
-        Sums t = {0, 0};
-        for (int w = 0; w < kTokWarps; ++w) {
-          t.w += red[w].w;
-          t.n += red[w].n;
-        }
-        span_sum[span] = t;
-      }
-    }
-  }
-  all = warp_sum(all);
-  below = warp_sum(below);
-  __syncthreads();
-  if (lane == 0) {
-    red[wid] = all;
-    red2[wid] = below;
-  }
-  __syncthreads();
-  all = red[0];
-  below = red2[0];
-  for (int w = 1; w < kTokWarps; ++w) {
-    all.w += red[w].w;
-    all.n += red[w].n;
-    below.w += red2[w].w;
-    below.n += red2[w].n;
-  }
-
-  if constexpr (!DECODE) {
-    if (tid == 0) {
-      if (own_weight == 0xffffffffu) {
-        report(status, RANS_ERR_ZERO_FREQ, r);
-        starts[r] = 0;
-        freqs[r] = 0;
-      } else {
-        const uint32_t s = interval_start(below.w, below.n, all.w, all.n);
-        starts[r] = s;
-        freqs[r] = interval_start(below.w + own_weight, below.n + 1, all.w, all.n) - s;
-      }
-    }
-  } else {
-    const uint32_t slot = (uint32_t)x & (kTokTotal - 1);
-    // the last span that starts at or before the slot
-    Sums base = {0, 0};
-    int span = 0;
-    for (;; ++span) {
-      if ((span + 1) * kTouchSpan >= row.end()) break;
-      const Sums next = {base.w + span_sum[span].w, base.n + span_sum[span].n};
-      if (!starts_by(next.w, next.n, all.w, all.n, slot)) break;
-      base = next;
-    }
-    // warp 0 walks it, a warp's worth of vectors at a time.  The decoded token
-    // is the last alive one that starts at or before the slot.
-    const int u_lo = span * kTouchSpan;
-    if (touch) fill_touch(table, a, row.shift, in.vocab, u_lo, tid, kTokThreads);
-    if (wid != 0) return;
-    bool done = false;
-    for (int ub = u_lo; !done && ub < min(u_lo + kTouchSpan, row.end()); ub += 32 * N) {
-      const int u0 = ub + lane * N;
-      float z[N];
+  // adjusted logits of this lane's vector at u0
+  auto fetch = [&](int u0, float (&z)[N]) {
+    row.load(u0, z, kNegInf);
+    if constexpr (ADJ) {
       if (u0 < row.end()) {
-        fetch(u0, u_lo, z);
+        if (touch) touch_vector<N>(z, table, a, u0 - table_at);
+        if (a.mask) mask_vector<N>(z, a, u0 - row.shift);
+      }
+      if (!row.whole(u0)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (u0 + i < row.shift || u0 + i >= row.end()) z[i] = kNegInf;
+      }
+    }
+  };
+  auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
+
+  // first walk: the maximum; and the least logit of the tiles inside the row
+  float m = kNegInf, least;
+  {
+    Extremes<T> ends;
+    float least_adj = __builtin_huge_valf();
+    spans([&](int u, int) {
+      if (!ADJ && inside(u)) {
+        uint4 q[kTileVecs];
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k)
+          q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k) ends.take(q[k]);
       } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) z[i] = kNegInf;
-      }
-      Sums mine = {0, 0};
+        for (int k = 0; k < kTileVecs; ++k) {
+          float z[N];
+          fetch(u + k * kVecRow + lane * N, z);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        mine.w += token_weight(z[i], rs.scale, rs.ymax);
-        mine.n += z[i] > kNegInf;
-      }
-      Sums incl = mine;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const uint64_t pw = __shfl_up_sync(kFull, incl.w, o);
-        const uint32_t pn = __shfl_up_sync(kFull, incl.n, o);
-        if (lane >= o) {
-          incl.w += pw;
-          incl.n += pn;
-        }
-      }
-      Sums at = {base.w + incl.w - mine.w, base.n + incl.n - mine.n};
-      const uint64_t end_w = __shfl_sync(kFull, base.w + incl.w, 31);
-      const uint32_t end_n = __shfl_sync(kFull, base.n + incl.n, 31);
-      // the token sits in this lane if an alive token of it contains the slot
-      uint32_t s0 = 0, f0 = 0;
-      int found = -1;
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        if (!(z[i] > kNegInf)) continue;
-        const Sums next = {at.w + token_weight(z[i], rs.scale, rs.ymax), at.n + 1};
-        if (starts_by(at.w, at.n, all.w, all.n, slot) &&
-            !starts_by(next.w, next.n, all.w, all.n, slot)) {
-          found = u0 + i - row.shift;
-          s0 = interval_start(at.w, at.n, all.w, all.n);
-          f0 = interval_start(next.w, next.n, all.w, all.n) - s0;
-        }
-        at = next;
-      }
-      if (found >= 0) {
-        uint64_t y = (uint64_t)f0 * (x >> kTokPrec) + slot - s0;
-        uint64_t used = taken;
-        int token = found;
-        if (y < kL) {
-          const uint64_t off = cd.offsets[stream], lim = cd.offsets[stream + 1];
-          const bool ok = !(off & 3) && off <= lim && lim <= cd.in_bytes &&
-                          taken < (lim - off) / 4;
-          if (ok) {
-            y = y << 32 | reinterpret_cast<const uint32_t *>(cd.in)[off / 4 + taken];
-            used = taken + 1;
-          } else {
-            report(status, RANS_ERR_CORRUPT, stream);
-            token = -1;
-            y = x;
+          for (int i = 0; i < N; ++i) {
+            m = max_nan(m, z[i]);
+            if (ADJ) least_adj = fminf(least_adj, z[i]);
           }
         }
-        cd.tokens[r] = token;
-        cd.states_out[2 * stream] = y;
-        cd.states_out[2 * stream + 1] = used;
       }
-      done = __any_sync(kFull, found >= 0);
-      base.w = end_w;
-      base.n = end_n;
+    });
+    m = max_nan(m, ends.largest());
+    least = ADJ ? least_adj : ends.smallest();
+  }
+  m = warp_max_nan(m);
+  if (tid == 0) own_weight = 0xffffffffu;
+  if (peers > 1) {
+    cluster_wait();
+    if (lane < (int)peers)
+      peer_store(peer_address(&peer_max[rank * warps + wid], lane), __float_as_uint(m));
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    if (lane == 0) peer_max[wid] = m;
+    __syncthreads();
+  }
+  m = kNegInf;
+  for (int i = lane; i < (int)peers * warps; i += 32) m = max_nan(m, peer_max[i]);
+  m = warp_max_nan(m);
+  const RowScale rs =
+      row_scale(m, adj.params ? adj.params[4 * r + 3] : adj.inv_temperature);
+  if (rs.error != RANS_OK) return refuse(rs.error, r, true);
+
+  // Second walk: the weights.  Where a warp's smallest logit needs no clamp
+  // there is no dead token either, and the weights go two at a time.
+  const int u_target = row.shift + target;
+  const bool plain = __all_sync(
+      kFull, __fsub_rn(__fmul_rn(least, rs.scale), rs.ymax) >= kLowest && least > kNegInf);
+  const uint64_t scale2 = (uint64_t)__float_as_uint(rs.scale) << 32 | __float_as_uint(rs.scale);
+  const uint64_t ymax2 =
+      (uint64_t)__float_as_uint(-rs.ymax) << 32 | __float_as_uint(-rs.ymax);
+  WarpSums s = {0, 0, 0, 0};
+  spans([&](int u, int tile) {
+    // a lane's weights of a tile stay below 2^26, a tile's below 2^31
+    uint32_t w = 0, n = 0;
+    if (plain && (ADJ || inside(u))) {
+      if constexpr (!ADJ) {
+        uint4 q[kTileVecs];
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k)
+          q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k) {
+          float z[N];
+          unpack16(q[k], z, T());
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const uint2 b = raw_weights(z[i], z[i + 1], scale2, ymax2, zero2);
+            w += b.x + b.y;
+          }
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k) {
+          float z[N];
+          fetch(u + k * kVecRow + lane * N, z);
+#pragma unroll
+          for (int i = 0; i < N; i += 2) {
+            const uint2 b = raw_weights(z[i], z[i + 1], scale2, ymax2, zero2);
+            w += b.x + b.y;
+          }
+        }
+      }
+      w -= (uint32_t)(N * kTileVecs) * __float_as_uint(kUnit);
+      n = N * kTileVecs;
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTileVecs; ++k) {
+        float z[N];
+        fetch(u + k * kVecRow + lane * N, z);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          w += token_weight(z[i], rs.scale, rs.ymax);
+          n += z[i] > kNegInf ? 1u : 0u;
+        }
+      }
+    }
+    s.w += w;
+    s.n += n;
+    if constexpr (DECODE) {
+      w = __reduce_add_sync(kFull, w);
+      n = __reduce_add_sync(kFull, n);
+      if (lane == 0) tile_sums[tile] = make_uint2(w, n);
+    } else if (u + kTile <= u_target) {
+      s.below_w += w;
+      s.below_n += n;
+    } else if (u <= u_target) {
+      // the token's own tile: once per row
+      for (int k = 0; k < kTileVecs; ++k) {
+        const int u0 = u + k * kVecRow + lane * N;
+        float z[N];
+        fetch(u0, z);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const uint32_t wi = token_weight(z[i], rs.scale, rs.ymax);
+          const uint32_t ni = z[i] > kNegInf ? 1u : 0u;
+          if (u0 + i < u_target) {
+            s.below_w += wi;
+            s.below_n += ni;
+          }
+          if (u0 + i == u_target && ni) peer_store(peer_address(&own_weight, 0), wi);
+        }
+      }
+    }
+  });
+  const Sums sum = warp_total({s.w, s.n});
+  Sums below = {0, 0};
+  if constexpr (!DECODE) below = warp_total({s.below_w, s.below_n});
+  if (lane < (DECODE ? (int)peers : 1)) {
+    const uint32_t at = peer_address(&peer_sums[rank * warps + wid], lane);
+    peer_store(at, sum.w);
+    peer_store(at + 16, sum.n);
+    if constexpr (!DECODE) {
+      peer_store(at + 8, below.w);
+      peer_store(at + 20, below.n);
+    }
+  }
+  if (peers > 1) {
+    __syncwarp();
+    cluster_arrive();
+    cluster_wait();
+  } else {
+    __syncthreads();
+  }
+  if (!DECODE && (rank != 0 || wid != 0)) return;
+
+  if (wid == 0) {
+    // the row's sums; of the blocks before this one (below the token), and of
+    // this one
+    Sums all = {0, 0}, before = {0, 0}, mine = {0, 0};
+    for (int i = lane; i < (int)peers * warps; i += 32) {
+      const WarpSums p = peer_sums[i];
+      all = all + Sums{p.w, p.n};
+      if constexpr (DECODE) {
+        if (i < (int)rank * warps) before = before + Sums{p.w, p.n};
+        else if (i < (int)(rank + 1) * warps) mine = mine + Sums{p.w, p.n};
+      } else {
+        before = before + Sums{p.below_w, p.below_n};
+      }
+    }
+    all = warp_total(all);
+    before = warp_total(before);
+    if constexpr (!DECODE) {
+      if (lane != 0) return;
+      if (own_weight == 0xffffffffu) return refuse(RANS_ERR_ZERO_FREQ, r, false);
+      const uint32_t b = interval_start(before.w, before.n, all.w, all.n);
+      starts[r] = b;
+      freqs[r] = interval_start(before.w + own_weight, before.n + 1, all.w, all.n) - b;
+      return;
+    } else {
+      // the block whose tokens hold the slot finds the tile that does, 32
+      // tiles at a time
+      const uint32_t slot = (uint32_t)x & (kTokTotal - 1);
+      auto holds = [&](Sums at, Sums next) {
+        return starts_by(at.w, at.n, all.w, all.n, slot) &&
+               !starts_by(next.w, next.n, all.w, all.n, slot);
+      };
+      mine = warp_total(mine);
+      int tile = -1;
+      if (holds(before, before + mine)) {
+        Sums base = before;
+        const int tiles = (hi - lo + kTile - 1) / kTile;
+        for (int t0 = 0; t0 < tiles && tile < 0; t0 += 32) {
+          const uint2 own = t0 + lane < tiles ? tile_sums[t0 + lane] : make_uint2(0, 0);
+          const Sums next = base + warp_scan({own.x, own.y}, lane);
+          const Sums at = {next.w - own.x, next.n - own.y};
+          const uint32_t hit = __ballot_sync(kFull, holds(at, next));
+          if (hit) {
+            const int l = __ffs(hit) - 1;
+            tile = t0 + l;
+            base.w = __shfl_sync(kFull, at.w, l);
+            base.n = __shfl_sync(kFull, at.n, l);
+          } else {
+            base.w = __shfl_sync(kFull, next.w, 31);
+            base.n = __shfl_sync(kFull, next.n, 31);
+          }
+        }
+        if (lane == 0) {
+          found_base = base;
+          found_all = all;
+        }
+      }
+      if (lane == 0) found_tile = tile;
+    }
+  }
+  if constexpr (DECODE) {
+    __syncthreads();
+    const int tile = found_tile;
+    if (tile < 0) return;
+    const int u = lo + tile * kTile;
+    if (ADJ && touch) {
+      const int u_lo = lo + (u - lo) / kSpan * kSpan;
+      if (table_at != u_lo) {
+        fill_touch(table, a, row.shift, in.vocab, u_lo, tid, threads);
+        table_at = u_lo;
+      }
+    }
+    if (wid != 0) return;
+    const uint32_t slot = (uint32_t)x & (kTokTotal - 1);
+    const Sums all = found_all;
+    auto holds = [&](Sums at, Sums next) {
+      return starts_by(at.w, at.n, all.w, all.n, slot) &&
+             !starts_by(next.w, next.n, all.w, all.n, slot);
+    };
+    Sums base = found_base;
+    for (int k = 0; k < kTileVecs; ++k) {
+      const int u0 = u + k * kVecRow + lane * N;
+      float z[N];
+      fetch(u0, z);
+      Sums own = {0, 0};
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        own = own + Sums{token_weight(z[i], rs.scale, rs.ymax), z[i] > kNegInf ? 1u : 0u};
+      const Sums next = base + warp_scan(own, lane);
+      Sums at = {next.w - own.w, next.n - own.n};
+      if (holds(at, next)) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          if (!(z[i] > kNegInf)) continue;
+          const Sums after = {at.w + token_weight(z[i], rs.scale, rs.ymax), at.n + 1};
+          if (holds(at, after)) {
+            const uint32_t b = interval_start(at.w, at.n, all.w, all.n);
+            take_token(cd, r, stream, x, taken, u0 + i - row.shift, b,
+                       interval_start(after.w, after.n, all.w, all.n) - b, status);
+          }
+          at = after;
+        }
+      }
+      base.w = __shfl_sync(kFull, next.w, 31);
+      base.n = __shfl_sync(kFull, next.n, 31);
     }
   }
 }
@@ -485,30 +767,76 @@ __global__ void token_finish_kernel(const uint64_t *offsets, int64_t S, const ui
     report(status, RANS_ERR_CORRUPT, k);
 }
 
-template <typename T>
-int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *tokens,
-                  uint32_t *starts, uint32_t *freqs, const Coded *cd, int32_t *status,
-                  cudaStream_t st) {
-  auto kern = cd ? token_rows_kernel<T, true> : token_rows_kernel<T, false>;
-  const bool touch = adj.history != nullptr || adj.bias_ids != nullptr;
-  const uint32_t smem = touch ? (uint32_t)sizeof(TouchTable) : 0u;
-  if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
-  if (in.rows > 0x7fffffff) return RANS_ERR_ARG;
-  kern<<<(unsigned)in.rows, kTokThreads, smem, st>>>(in, adj, tokens, starts, freqs,
-                                                     cd ? *cd : Coded(), status);
-  return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
+// Blocks per row: one, while the rows alone fill the SMs; twice as many as
+// long as all blocks would still run at once and each keeps a tile for eight
+// warps.  With penalties or biases, enough that a block's tokens fit one table.
+struct RowShape {
+  int peers, threads, slice;
+};
+constexpr int kFewWarps = 8;
+
+RowShape row_shape(int64_t rows, int tokens, int tile, bool touch, int sms) {
+  const int tiles = (tokens + tile - 1) / tile;
+  auto per = [&](int peers) { return (tiles + peers - 1) / peers; };
+  int peers = 1;
+  if (touch)
+    while (peers < kMaxCluster && per(peers) * tile > kTouchSpan) peers *= 2;
+  while (peers < kMaxCluster && rows * peers * 2 <= 2 * sms && per(peers * 2) >= kFewWarps)
+    peers *= 2;
+  const int warps = per(peers) < kRowWarps ? per(peers) : kRowWarps;
+  return {peers, warps * 32, per(peers) * tile};
 }
 
+template <typename T, bool DECODE>
+int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *tokens,
+                  uint32_t *starts, uint32_t *freqs, const Coded &cd, int32_t *status,
+                  cudaStream_t st) {
+  const bool touch = adj.history != nullptr || adj.bias_ids != nullptr;
+  auto kern = touch || adj.mask ? token_rows_kernel<T, DECODE, true>
+                                : token_rows_kernel<T, DECODE, false>;
+  const bool adjusted = touch || adj.mask;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
+  constexpr int kTile = 32 * VecOf<T>::N * kTileVecs;
+  // rows that all start on 16 bytes have no empty places before them
+  const bool aligned = reinterpret_cast<uintptr_t>(in.data) % 16 == 0 &&
+                       (in.rows == 1 || in.row_stride % VecOf<T>::N == 0);
+  const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), kTile,
+                                   touch, num_sms(dev));
+  const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) : 0u) +
+                        (DECODE ? (uint32_t)(shape.slice / kTile * sizeof(uint2)) : 0u);
+  if (ensure_cluster((const void *)kern) != cudaSuccess) return RANS_ERR_CUDA;
+  if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
+  if (in.rows > 0x7fffffff / shape.peers) return RANS_ERR_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(in.rows * shape.peers));
+  cfg.blockDim = dim3((unsigned)shape.threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)shape.peers;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, in, adj, tokens, starts, freqs, cd, status,
+                            shape.slice, (uint64_t)0x8000000080000000ull) == cudaSuccess
+             ? RANS_OK
+             : RANS_ERR_CUDA;
+}
+
+template <bool DECODE>
 int launch_rows(const rans_logits &in, const rans_adjust &adj, const int32_t *tokens,
-                uint32_t *starts, uint32_t *freqs, const Coded *cd, int32_t *status,
+                uint32_t *starts, uint32_t *freqs, const Coded &cd, int32_t *status,
                 cudaStream_t st) {
   switch (in.dtype) {
     case RANS_LOGITS_F32:
-      return launch_rows_t<float>(in, adj, tokens, starts, freqs, cd, status, st);
+      return launch_rows_t<float, DECODE>(in, adj, tokens, starts, freqs, cd, status, st);
     case RANS_LOGITS_F16:
-      return launch_rows_t<__half>(in, adj, tokens, starts, freqs, cd, status, st);
+      return launch_rows_t<__half, DECODE>(in, adj, tokens, starts, freqs, cd, status, st);
     default:
-      return launch_rows_t<__nv_bfloat16>(in, adj, tokens, starts, freqs, cd, status, st);
+      return launch_rows_t<__nv_bfloat16, DECODE>(in, adj, tokens, starts, freqs, cd, status, st);
   }
 }
 
@@ -516,7 +844,7 @@ int launch_rows(const rans_logits &in, const rans_adjust &adj, const int32_t *to
 
 int launch_token_intervals(const rans_logits &in, const rans_adjust &adj, const int32_t *tokens,
                            uint32_t *starts, uint32_t *freqs, int32_t *status, cudaStream_t st) {
-  return launch_rows(in, adj, tokens, starts, freqs, nullptr, status, st);
+  return launch_rows<false>(in, adj, tokens, starts, freqs, Coded(), status, st);
 }
 
 int launch_decode_tokens(const rans_logits &in, const rans_adjust &adj, const uint8_t *data,
@@ -525,7 +853,7 @@ int launch_decode_tokens(const rans_logits &in, const rans_adjust &adj, const ui
                          uint64_t *states_out, int32_t *tokens, int32_t *status,
                          cudaStream_t st) {
   const Coded cd = {data, data_bytes, offsets, S, stream_ids, states_in, states_out, tokens};
-  return launch_rows(in, adj, nullptr, nullptr, nullptr, &cd, status, st);
+  return launch_rows<true>(in, adj, nullptr, nullptr, nullptr, cd, status, st);
 }
 
 int launch_encode_intervals(const uint32_t *starts, const uint32_t *freqs, const Geom &g,

@@ -17,7 +17,7 @@ import torch
 from . import _lib as L
 
 _LOGITS_CODE = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-MAX_VOCAB = 1 << 19
+MAX_VOCAB = (1 << 19) - 8
 MAX_TOP = 4096
 TOKEN_PRECISION = 24
 
