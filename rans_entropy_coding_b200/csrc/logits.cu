@@ -18,12 +18,14 @@ __global__ void __launch_bounds__(kAdjThreads)
   const int64_t r = blockIdx.x / spans;
   const int u_lo = (int)(blockIdx.x % spans) * kTouchSpan;
   const Row<T> row(in.data, r, in.row_stride, in.vocab);
-  const RowAdjust a = row_adjust(adj, r, in.vocab);
+  __shared__ RowAdjust a;
+  if (threadIdx.x == 0) a = row_adjust(adj, r, in.vocab);
+  __syncthreads();
   const int u_hi = min(u_lo + kTouchSpan, row.end());
   bool touch = false;
   if constexpr (TOUCH) {
     touch = a.touches();
-    if (touch) fill_touch(table, a, row.shift, in.vocab, u_lo, threadIdx.x, kAdjThreads);
+    if (touch) fill_touch(table, a, row.shift, in.vocab, u_lo, u_hi, threadIdx.x, kAdjThreads);
   }
   O *o = out + r * out_stride - row.shift;
   for (int u0 = u_lo + (int)threadIdx.x * N; u0 < u_hi; u0 += kAdjThreads * N) {

@@ -118,7 +118,9 @@ struct Row {
 };
 
 // ---------------------------------------------------------- adjustments --
-// One row's adjustments, resolved from rans_adjust.
+// One row's adjustments, resolved from rans_adjust.  Kernels keep it in shared
+// memory: it is the same for all threads, and most of it is read for touched
+// tokens alone.
 struct RowAdjust {
   float repetition, frequency, presence, inv_temperature;
   const int32_t *history;  // the row's window
@@ -185,68 +187,127 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int words, i
   return __funnelshift_r(lo, hi, s);
 }
 
-// Which of kTouchSpan consecutive tokens a row's history and biases touch.
-// Counts and bias entries sit in shared memory, one cell per token (a hash
-// would need a bound on the distinct tokens of a window); a bitmap beside them
-// lets the untouched majority pass with one test per vector.
+// Which tokens a row's history and biases touch, with their counts and bias
+// entries, in shared memory.  A bitmap lets the untouched majority pass with
+// one test per vector.  A window of up to kHashWindow entries (history and
+// biases together) goes into a hash table, which covers up to kHashSpan tokens
+// at once; a longer one has a cell per token, kTouchSpan tokens at a time.
+constexpr int kHashSlots = 4096;
+constexpr int kHashWindow = kHashSlots / 2;
+constexpr int kHashSpan = 1 << 17;
 constexpr int kTouchSpan = 8192;
 
 struct TouchTable {
-  uint32_t bits[kTouchSpan / 32];
-  uint32_t count[kTouchSpan];
-  uint32_t bias[kTouchSpan];  // 1 + the last entry's position in the row's list
+  union {
+    struct {
+      uint32_t bits[kHashSpan / 32];
+      int32_t key[kHashSlots];    // place in the span, or -1
+      uint32_t count[kHashSlots];
+      uint32_t bias[kHashSlots];  // 1 + the last entry's position in the row's list
+    } hash;
+    struct {
+      uint32_t bits[kTouchSpan / 32];
+      uint32_t count[kTouchSpan];
+      uint32_t bias[kTouchSpan];
+    } cells;
+  };
 };
 
-// Fills the table for u in [u_lo, u_lo + kTouchSpan); every thread of the
-// block calls it.  Only cells that are touched are ever read, so only those
-// are cleared.  Integer adds, maxima and ors: the result does not depend on
-// the threads' order.
+__device__ __forceinline__ bool small_window(const RowAdjust &a) {
+  return a.history_n + a.bias_n <= kHashWindow;
+}
+// Tokens that a table of the row's covers.
+__device__ __forceinline__ int touch_span(const RowAdjust &a) {
+  return small_window(a) ? kHashSpan : kTouchSpan;
+}
+
+__device__ __forceinline__ uint32_t hash_slot(int k) {
+  return (uint32_t)k * 2654435761u >> 20;  // Fibonacci hashing to 12 bits
+}
+static_assert(kHashSlots == 1 << 12, "hash_slot gives 12 bits");
+
+// Fills the table for u in [u_lo, u_lo + touch_span); every thread of the
+// block calls it.  Integer adds, maxima and ors: what a token finds in it does
+// not depend on the threads' order.
 __device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, int shift,
-                                           int vocab, int u_lo, int tid, int threads) {
-  auto cell = [&](int v) {
+                                           int vocab, int u_lo, int u_hi, int tid, int threads) {
+  const bool hashed = small_window(a);
+  const int span = min(touch_span(a), u_hi - u_lo);
+  auto place = [&](int64_t i) {
+    const int v = i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n];
     const int k = v + shift - u_lo;
-    return v >= 0 && v < vocab && k >= 0 && k < kTouchSpan ? k : -1;
+    return v >= 0 && v < vocab && k >= 0 && k < span ? k : -1;
   };
+  const int64_t n = a.history_n + a.bias_n;
   __syncthreads();
-  for (int i = tid; i < kTouchSpan / 32; i += threads) t.bits[i] = 0;
-  __syncthreads();
-  for (int64_t i = tid; i < a.history_n + a.bias_n; i += threads) {
-    const int k = cell(i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n]);
-    if (k < 0) continue;
-    t.count[k] = 0;
-    t.bias[k] = 0;
-    atomicOr(&t.bits[k >> 5], 1u << (k & 31));
-  }
-  __syncthreads();
-  for (int64_t i = tid; i < a.history_n; i += threads) {
-    const int k = cell(a.history[i]);
-    if (k >= 0) atomicAdd(&t.count[k], 1u);
-  }
-  for (int64_t i = tid; i < a.bias_n; i += threads) {
-    const int k = cell(a.bias_ids[i]);
-    if (k >= 0) atomicMax(&t.bias[k], (uint32_t)i + 1u);
+  uint32_t *bits = hashed ? t.hash.bits : t.cells.bits;
+  for (int i = tid; i < (span + 31) / 32; i += threads) bits[i] = 0;
+  if (hashed) {
+    uint4 *key = reinterpret_cast<uint4 *>(t.hash.key);  // keys, then counts and biases
+    for (int i = tid; i < kHashSlots / 4; i += threads)
+      key[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
+    for (int i = tid; i < kHashSlots / 2; i += threads)
+      key[kHashSlots / 4 + i] = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    for (int i = tid; i < (int)n; i += threads) {
+      const int k = place(i);
+      if (k < 0) continue;
+      atomicOr(&bits[k >> 5], 1u << (k & 31));
+      uint32_t s = hash_slot(k);
+      // at most kHashWindow keys: a free slot is always found
+      for (int old; (old = atomicCAS(&t.hash.key[s], -1, k)) != -1 && old != k;)
+        s = (s + 1) & (kHashSlots - 1);
+      if (i < a.history_n) atomicAdd(&t.hash.count[s], 1u);
+      else atomicMax(&t.hash.bias[s], (uint32_t)(i - a.history_n) + 1u);
+    }
+  } else {
+    // only cells that are touched are ever read, so only those are cleared
+    __syncthreads();
+    for (int64_t i = tid; i < n; i += threads) {
+      const int k = place(i);
+      if (k < 0) continue;
+      t.cells.count[k] = 0;
+      t.cells.bias[k] = 0;
+      atomicOr(&bits[k >> 5], 1u << (k & 31));
+    }
+    __syncthreads();
+    for (int64_t i = tid; i < n; i += threads) {
+      const int k = place(i);
+      if (k < 0) continue;
+      if (i < a.history_n) atomicAdd(&t.cells.count[k], 1u);
+      else atomicMax(&t.cells.bias[k], (uint32_t)(i - a.history_n) + 1u);
+    }
   }
   __syncthreads();
 }
 
-// The penalties and bias of one touched token (cell k of the table).
-__device__ __forceinline__ float touched_logit(float z, const TouchTable &t, const RowAdjust &a,
-                                               int k) {
-  const uint32_t n = t.count[k];
+// The penalties and bias of one touched token (place k of the table's span).
+static __device__ __noinline__ float touched_logit(float z, const TouchTable &t, const RowAdjust &a,
+                                            int k) {  // both in shared memory
+  uint32_t n, e;
+  if (small_window(a)) {
+    uint32_t s = hash_slot(k);
+    while (t.hash.key[s] != k) s = (s + 1) & (kHashSlots - 1);  // its bit is set: it is there
+    n = t.hash.count[s];
+    e = t.hash.bias[s];
+  } else {
+    n = t.cells.count[k];
+    e = t.cells.bias[k];
+  }
   if (n > 0) {
     z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
     z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(n), a.frequency), a.presence));
   }
-  const uint32_t e = t.bias[k];
   if (e > 0) z = __fadd_rn(z, a.bias_values[e - 1]);
   return z;
 }
 
-// Penalties and biases of a vector at u0 (u0 - u_lo inside the table).
+// Penalties and biases of a vector at place k0 of the table's span.
 template <int N>
 __device__ __forceinline__ void touch_vector(float (&z)[N], const TouchTable &t,
                                              const RowAdjust &a, int k0) {
-  const uint32_t hit = (t.bits[k0 >> 5] >> (k0 & 31)) & ((1u << N) - 1u);
+  const uint32_t *bits = small_window(a) ? t.hash.bits : t.cells.bits;
+  const uint32_t hit = (bits[k0 >> 5] >> (k0 & 31)) & ((1u << N) - 1u);
   if (hit == 0) return;
 #pragma unroll
   for (int i = 0; i < N; ++i)

@@ -370,34 +370,38 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     cluster_arrive();
   }
 
-  RowAdjust a;
-  bool touch = false;
+  __shared__ RowAdjust a;
+  bool touch = false, masked = false;
+  int span = 1 << 30;  // tokens per table
   if constexpr (ADJ) {
-    a = row_adjust(adj, r, in.vocab);
+    if (tid == 0) a = row_adjust(adj, r, in.vocab);
+    __syncthreads();
     touch = a.touches();
+    masked = a.mask != nullptr;
+    if (touch) span = touch_span(a);
   }
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
-  // Walks this block's tiles span by span (one span without a table):
-  // body(tile's first u, its number).
-  constexpr int kSpan = ADJ ? kTouchSpan / kTile * kTile : 1 << 30;
   int table_at = -1;
-  auto spans = [&](auto body) {
-    for (int u_lo = lo; u_lo < hi; u_lo = kSpan < hi - u_lo ? u_lo + kSpan : hi) {
-      if (ADJ && touch && table_at != u_lo) {
-        fill_touch(table, a, row.shift, in.vocab, u_lo, tid, threads);
-        table_at = u_lo;
-      }
-      const int u_hi = kSpan < hi - u_lo ? u_lo + kSpan : hi;
+  auto need_table = [&](int u_lo) {
+    if (!ADJ || !touch || table_at == u_lo) return;
+    fill_touch(table, a, row.shift, in.vocab, u_lo, hi, tid, threads);
+    table_at = u_lo;
+  };
+  // walks this block's tiles: body(tile's first u, its number)
+  auto walk = [&](auto body) {
+    for (int u_lo = lo; u_lo < hi; u_lo = span < hi - u_lo ? u_lo + span : hi) {
+      need_table(u_lo);
+      const int u_hi = span < hi - u_lo ? u_lo + span : hi;
       for (int u = u_lo + wid * kTile; u < u_hi; u += warps * kTile) body(u, (u - lo) / kTile);
     }
   };
-  // adjusted logits of this lane's vector at u0
+  // adjusted logits of this lane's vector at u0, wherever that is
   auto fetch = [&](int u0, float (&z)[N]) {
     row.load(u0, z, kNegInf);
     if constexpr (ADJ) {
       if (u0 < row.end()) {
         if (touch) touch_vector<N>(z, table, a, u0 - table_at);
-        if (a.mask) mask_vector<N>(z, a, u0 - row.shift);
+        if (masked) mask_vector<N>(z, a, u0 - row.shift);
       }
       if (!row.whole(u0)) {
 #pragma unroll
@@ -406,36 +410,60 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
       }
     }
   };
+  // A tile inside the row is loaded at once, with its mask bits.
   auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
-
-  // first walk: the maximum; and the least logit of the tiles inside the row
-  float m = kNegInf, least;
-  {
-    Extremes<T> ends;
-    float least_adj = __builtin_huge_valf();
-    spans([&](int u, int) {
-      if (!ADJ && inside(u)) {
-        uint4 q[kTileVecs];
+  auto load_tile = [&](int u, uint4 (&q)[kTileVecs], uint32_t (&ok)[kTileVecs]) {
 #pragma unroll
-        for (int k = 0; k < kTileVecs; ++k)
-          q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+    for (int k = 0; k < kTileVecs; ++k)
+      q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+    if (ADJ && masked) {
+#pragma unroll
+      for (int k = 0; k < kTileVecs; ++k) {
+        const int v0 = u + k * kVecRow + lane * N - row.shift, w = v0 >> 5;
+        ok[k] = __funnelshift_r(a.mask[w], a.mask[min(w + 1, a.mask_words - 1)], v0 & 31);
+      }
+    }
+  };
+
+  // First walk: the maximum, and the least logit that the mask leaves in the
+  // tiles inside the row.
+  float m = kNegInf, least = __builtin_huge_valf();
+  Extremes<T> ends;
+  walk([&](int u, int) {
+    if (inside(u)) {
+      uint4 q[kTileVecs];
+      uint32_t ok[kTileVecs];
+      load_tile(u, q, ok);
+      if constexpr (!ADJ) {
 #pragma unroll
         for (int k = 0; k < kTileVecs; ++k) ends.take(q[k]);
       } else {
 #pragma unroll
         for (int k = 0; k < kTileVecs; ++k) {
           float z[N];
-          fetch(u + k * kVecRow + lane * N, z);
+          unpack16(q[k], z, T());
+          if (touch) touch_vector<N>(z, table, a, u + k * kVecRow + lane * N - table_at);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            m = max_nan(m, z[i]);
-            if (ADJ) least_adj = fminf(least_adj, z[i]);
+            const bool alive = !masked || (ok[k] >> i & 1);
+            m = max_nan(m, alive ? z[i] : kNegInf);
+            least = fminf(least, alive ? z[i] : __builtin_huge_valf());
           }
         }
       }
-    });
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTileVecs; ++k) {
+        float z[N];
+        fetch(u + k * kVecRow + lane * N, z);
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = max_nan(m, z[i]);
+      }
+    }
+  });
+  if constexpr (!ADJ) {
     m = max_nan(m, ends.largest());
-    least = ADJ ? least_adj : ends.smallest();
+    least = ends.smallest();
   }
   m = warp_max_nan(m);
   if (tid == 0) own_weight = 0xffffffffu;
@@ -457,48 +485,48 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
       row_scale(m, adj.params ? adj.params[4 * r + 3] : adj.inv_temperature);
   if (rs.error != RANS_OK) return refuse(rs.error, r, true);
 
-  // Second walk: the weights.  Where a warp's smallest logit needs no clamp
-  // there is no dead token either, and the weights go two at a time.
+  // Second walk: the weights.  Where a warp's smallest logit needs no clamp,
+  // only the mask makes dead tokens, and the weights go two at a time; a
+  // masked token then takes a logit whose d is -40, hence weight 0 (which
+  // wants a maximum that 40 can be told from, and a factor).
   const int u_target = row.shift + target;
   const bool plain = __all_sync(
-      kFull, __fsub_rn(__fmul_rn(least, rs.scale), rs.ymax) >= kLowest && least > kNegInf);
+      kFull, __fsub_rn(__fmul_rn(least, rs.scale), rs.ymax) >= kLowest && least > kNegInf &&
+                 (!ADJ || (fabsf(rs.ymax) < 65536.0f && rs.scale > 0.0f)));
+  const float dead = ADJ ? (rs.ymax - 40.0f) / rs.scale : 0.0f;
   const uint64_t scale2 = (uint64_t)__float_as_uint(rs.scale) << 32 | __float_as_uint(rs.scale);
   const uint64_t ymax2 =
       (uint64_t)__float_as_uint(-rs.ymax) << 32 | __float_as_uint(-rs.ymax);
   WarpSums s = {0, 0, 0, 0};
-  spans([&](int u, int tile) {
+  walk([&](int u, int tile) {
     // a lane's weights of a tile stay below 2^26, a tile's below 2^31
     uint32_t w = 0, n = 0;
-    if (plain && (ADJ || inside(u))) {
-      if constexpr (!ADJ) {
-        uint4 q[kTileVecs];
+    if (plain && inside(u)) {
+      uint4 q[kTileVecs];
+      uint32_t ok[kTileVecs];
+      load_tile(u, q, ok);
 #pragma unroll
-        for (int k = 0; k < kTileVecs; ++k)
-          q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+      for (int k = 0; k < kTileVecs; ++k) {
+        float z[N];
+        unpack16(q[k], z, T());
+        if constexpr (ADJ) {
+          if (touch) touch_vector<N>(z, table, a, u + k * kVecRow + lane * N - table_at);
+          if (masked) {
 #pragma unroll
-        for (int k = 0; k < kTileVecs; ++k) {
-          float z[N];
-          unpack16(q[k], z, T());
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const uint2 b = raw_weights(z[i], z[i + 1], scale2, ymax2, zero2);
-            w += b.x + b.y;
+            for (int i = 0; i < N; ++i) z[i] = ok[k] >> i & 1 ? z[i] : dead;
+            n += __popc(ok[k] & ((1u << N) - 1u));
+          } else {
+            n += N;
           }
         }
-      } else {
 #pragma unroll
-        for (int k = 0; k < kTileVecs; ++k) {
-          float z[N];
-          fetch(u + k * kVecRow + lane * N, z);
-#pragma unroll
-          for (int i = 0; i < N; i += 2) {
-            const uint2 b = raw_weights(z[i], z[i + 1], scale2, ymax2, zero2);
-            w += b.x + b.y;
-          }
+        for (int i = 0; i < N; i += 2) {
+          const uint2 b = raw_weights(z[i], z[i + 1], scale2, ymax2, zero2);
+          w += b.x + b.y;
         }
       }
       w -= (uint32_t)(N * kTileVecs) * __float_as_uint(kUnit);
-      n = N * kTileVecs;
+      if constexpr (!ADJ) n = N * kTileVecs;
     } else {
 #pragma unroll
       for (int k = 0; k < kTileVecs; ++k) {
@@ -624,13 +652,7 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     const int tile = found_tile;
     if (tile < 0) return;
     const int u = lo + tile * kTile;
-    if (ADJ && touch) {
-      const int u_lo = lo + (u - lo) / kSpan * kSpan;
-      if (table_at != u_lo) {
-        fill_touch(table, a, row.shift, in.vocab, u_lo, tid, threads);
-        table_at = u_lo;
-      }
-    }
+    need_table(lo + (u - lo) / span * span);
     if (wid != 0) return;
     const uint32_t slot = (uint32_t)x & (kTokTotal - 1);
     const Sums all = found_all;
@@ -769,18 +791,16 @@ __global__ void token_finish_kernel(const uint64_t *offsets, int64_t S, const ui
 
 // Blocks per row: one, while the rows alone fill the SMs; twice as many as
 // long as all blocks would still run at once and each keeps a tile for eight
-// warps.  With penalties or biases, enough that a block's tokens fit one table.
+// warps.
 struct RowShape {
   int peers, threads, slice;
 };
 constexpr int kFewWarps = 8;
 
-RowShape row_shape(int64_t rows, int tokens, int tile, bool touch, int sms) {
+RowShape row_shape(int64_t rows, int tokens, int tile, int sms) {
   const int tiles = (tokens + tile - 1) / tile;
   auto per = [&](int peers) { return (tiles + peers - 1) / peers; };
   int peers = 1;
-  if (touch)
-    while (peers < kMaxCluster && per(peers) * tile > kTouchSpan) peers *= 2;
   while (peers < kMaxCluster && rows * peers * 2 <= 2 * sms && per(peers * 2) >= kFewWarps)
     peers *= 2;
   const int warps = per(peers) < kRowWarps ? per(peers) : kRowWarps;
@@ -802,7 +822,7 @@ int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *
   const bool aligned = reinterpret_cast<uintptr_t>(in.data) % 16 == 0 &&
                        (in.rows == 1 || in.row_stride % VecOf<T>::N == 0);
   const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), kTile,
-                                   touch, num_sms(dev));
+                                   num_sms(dev));
   const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) : 0u) +
                         (DECODE ? (uint32_t)(shape.slice / kTile * sizeof(uint2)) : 0u);
   if (ensure_cluster((const void *)kern) != cudaSuccess) return RANS_ERR_CUDA;

@@ -37,9 +37,10 @@ def make_logits(n, v, dtype, pad=0, seed=0, offset=0):
     return x
 
 
-def make_adjust(n, v, seed, history=True, bias=True, mask=True, per_row=False):
+def make_adjust(n, v, seed, history=True, bias=True, mask=True, per_row=False, long=700):
     """(LogitAdjust, the oracle's dict): windows that overlap, repeat ids, are
-    empty, run past the arrays' ends or hold ids outside the vocabulary."""
+    empty, run past the arrays' ends or hold ids outside the vocabulary.
+    `long`: the history array's length (row 1's window is all of it)."""
     rng = np.random.default_rng(seed)
     o = dict(temperature=0.8, repetition=1.25, frequency=0.1, presence=0.35)
     if per_row:
@@ -59,8 +60,8 @@ def make_adjust(n, v, seed, history=True, bias=True, mask=True, per_row=False):
         return b.astype(np.int64), e.astype(np.int64)
 
     if history:
-        toks = np.minimum(rng.integers(-2, v + 2, 700), rng.integers(0, v + 2, 700))
-        o["history"] = (toks.astype(np.int32), *spans(700))
+        toks = np.minimum(rng.integers(-2, v + 2, long), rng.integers(0, v + 2, long))
+        o["history"] = (toks.astype(np.int32), *spans(long))
     if bias:
         ids = rng.integers(-1, v + 1, 60).astype(np.int32)
         o["bias"] = (ids, rng.normal(0, 3, 60).astype(np.float32), *spans(60))
@@ -246,6 +247,69 @@ def test_intervals_errors_and_skipped_rows():
     low[0] = -math.inf
     b = TO.bounds(low.numpy(), {}, 0)
     assert one(low, 5) == (b[5], b[6] - b[5], rb.OK)
+
+
+@pytest.mark.parametrize("long", [1988, 1989, 6000])
+@pytest.mark.parametrize("v", [40, 1000, 20011])
+def test_long_histories(v, long):
+    """Windows on both sides of what a hash table takes (2048 entries with the
+    biases), full of repeats in a small vocabulary and spread over spans in a
+    large one."""
+    n = 4
+    x = make_logits(n, v, BF16, 1, seed=14)
+    a, o = make_adjust(n, v, seed=long + v, long=long)
+    check_adjusted(rb.adjust_logits(x, a, dtype=F32), x, o, n)
+    rng, st = np.random.default_rng(v), rb.new_status()
+    b = [TO.bounds(row, o, r) for r, row in enumerate(numpy_rows(x))]
+    tok = np.array([rng.choice(np.flatnonzero(np.diff(q))) for q in b], np.int32)
+    s, f = rb.token_intervals(x, torch.from_numpy(tok).cuda(), a, status=st)
+    assert s.tolist() == [q[t] for q, t in zip(b, tok)]
+    assert f.tolist() == [q[t + 1] - q[t] for q, t in zip(b, tok)]
+    slots = rng.integers(0, 1 << 24, n)
+    states = torch.tensor([[(1 << 62) + int(k), 2] for k in slots], device="cuda")
+    tok, _ = rb.decode_tokens(x, torch.zeros(8 * n, dtype=torch.uint8, device="cuda"),
+                              torch.arange(n + 1, device="cuda") * 8, states, a, status=st)
+    assert tok.tolist() == [int(np.searchsorted(q, k, side="right")) - 1
+                            for q, k in zip(b, slots)]
+    status_ok(st)
+
+
+@pytest.mark.parametrize("dtype,v,n", [(F16, 150001, 160), (BF16, 131072, 150), (F32, 70003, 75),
+                                       (BF16, rb.MAX_VOCAB, 3)])
+def test_many_rows_and_large_vocabularies(dtype, v, n):
+    """The split of a row over blocks follows the number of rows: the same rows
+    in another batch give the same intervals, tokens and states."""
+    x = make_logits(n, v, dtype, 3 if v % 2 else 0, seed=15)
+    a, o = make_adjust(n, v, seed=15, mask=False)
+    st = rb.new_status()
+    g = torch.Generator("cuda").manual_seed(1)
+    tok = torch.randint(0, v, (n,), device="cuda", generator=g).to(torch.int32)
+    words = torch.randint(-2**31, 2**31, (4 * n,), device="cuda", generator=g).to(torch.int32)
+    data, offs = words.view(torch.uint8), torch.arange(n + 1, device="cuda") * 16
+    states = torch.stack([torch.randint(1 << 31, 1 << 55, (n,), device="cuda", generator=g),
+                          torch.full((n,), 2, device="cuda")], 1)
+
+    def one(r, adj):
+        p = {k: (tuple(torch.from_numpy(q).cuda() for q in (*w[:-2], w[-2][r:r + 1],
+                                                             w[-1][r:r + 1]))
+                 if isinstance(w, tuple) else w) for k, w in o.items()}
+        return rb.LogitAdjust(**p) if adj else None
+
+    for adj in (None, a):
+        s, f = rb.token_intervals(x, tok, adj, status=st)
+        t, new = rb.decode_tokens(x, data, offs, states, adj, status=st)
+        for r in sorted({0, 1, n // 2, n - 1}):
+            s1, f1 = rb.token_intervals(x[r:r + 1], tok[r:r + 1], one(r, adj), status=st)
+            assert (int(s1), int(f1)) == (int(s[r]), int(f[r]))
+            t1, n1 = rb.decode_tokens(x[r:r + 1], data, offs[r:r + 2], states[r:r + 1],
+                                      one(r, adj), status=st)
+            assert int(t1) == int(t[r]) and torch.equal(n1[0], new[r])
+        r = n // 2
+        b = TO.bounds(numpy_rows(x[r:r + 1])[0], {} if adj is None else o, r)
+        assert int(s[r]) == b[int(tok[r])]
+        slot = int(states[r, 0]) & ((1 << 24) - 1)
+        assert int(t[r]) == int(np.searchsorted(b, slot, side="right")) - 1
+    status_ok(st)
 
 
 # ---------------------------------------------------------------- streams --
