@@ -83,8 +83,8 @@ _P, _I32, _I64, _U64, _F64, _F32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_in
                                    ctypes.c_uint64, ctypes.c_double, ctypes.c_float)
 _CHP = ctypes.POINTER(rans_chunking)
 _TBP = ctypes.POINTER(rans_tables)
-_LGP = ctypes.POINTER(rans_logits)
-_ADP = ctypes.POINTER(rans_adjust)
+# rans_logits and rans_adjust pointers: a byref() or a struct's packed bytes
+_LGP = _ADP = ctypes.c_void_p
 SIGNATURES = [
     ("rans_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("rans_version", ctypes.c_int, []),

@@ -187,22 +187,27 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int words, i
   return __funnelshift_r(lo, hi, s);
 }
 
-// Which tokens a row's history and biases touch, with their counts and bias
-// entries, in shared memory.  A bitmap lets the untouched majority pass with
-// one test per vector.  A window of up to kHashWindow entries (history and
-// biases together) goes into a hash table, which covers up to kHashSpan tokens
-// at once; a longer one has a cell per token, kTouchSpan tokens at a time.
+// Which tokens a row's history and biases touch, and their adjusted logits, in
+// shared memory.  They are few, but spread out: handled where they are met,
+// nearly every warp would stop for one in every vector (49 instructions per
+// logit, measured on rows of 50,000 tokens with 300 touched).  So they are
+// gathered and adjusted first, the kernels' main walks leave them out by a
+// bitmap, and what they add comes from the table, a token per thread.
+// Up to kTouchSpan tokens have a cell each.  A block with more of a row's
+// tokens covers up to kHashSpan at once with a hash table, if the row's window
+// (history and biases together) has at most kHashWindow entries; else it goes
+// kTouchSpan tokens at a time.
 constexpr int kHashSlots = 4096;
 constexpr int kHashWindow = kHashSlots / 2;
 constexpr int kHashSpan = 1 << 17;
 constexpr int kTouchSpan = 8192;
 
-struct TouchTable {
+struct __align__(16) TouchTable {
   union {
     struct {
       uint32_t bits[kHashSpan / 32];
       int32_t key[kHashSlots];    // place in the span, or -1
-      uint32_t count[kHashSlots];
+      uint32_t count[kHashSlots]; // occurrences; then the adjusted logit
       uint32_t bias[kHashSlots];  // 1 + the last entry's position in the row's list
     } hash;
     struct {
@@ -211,6 +216,16 @@ struct TouchTable {
       uint32_t bias[kTouchSpan];
     } cells;
   };
+  bool hashed;
+  int u_lo, span;  // covers u in [u_lo, u_lo + span)
+
+  __device__ __forceinline__ uint32_t *bitmap() { return hashed ? hash.bits : cells.bits; }
+  // Bits of the touched ones of N tokens from u0 on (a multiple of N).
+  template <int N>
+  __device__ __forceinline__ uint32_t hits(int u0) {
+    const int k = u0 - u_lo;
+    return (bitmap()[k >> 5] >> (k & 31)) & ((1u << N) - 1u);
+  }
 };
 
 __device__ __forceinline__ bool small_window(const RowAdjust &a) {
@@ -226,20 +241,67 @@ __device__ __forceinline__ uint32_t hash_slot(int k) {
 }
 static_assert(kHashSlots == 1 << 12, "hash_slot gives 12 bits");
 
-// Fills the table for u in [u_lo, u_lo + touch_span); every thread of the
-// block calls it.  Integer adds, maxima and ors: what a token finds in it does
-// not depend on the threads' order.
-__device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, int shift,
-                                           int vocab, int u_lo, int u_hi, int tid, int threads) {
-  const bool hashed = small_window(a);
+// body(u, its adjusted logit) for every touched token of the table, spread over
+// the block's threads.
+template <class Body>
+__device__ __forceinline__ void each_touched(TouchTable &t, int tid, int threads, Body body) {
+  if (t.hashed) {
+    for (int s = tid; s < kHashSlots; s += threads)
+      if (t.hash.key[s] >= 0)
+        body(t.u_lo + t.hash.key[s], __uint_as_float(t.hash.count[s]));
+  } else {
+    for (int w = tid; w < kTouchSpan / 32; w += threads)
+      for (uint32_t b = w * 32 < t.span ? t.cells.bits[w] : 0u; b != 0; b &= b - 1) {
+        const int k = w * 32 + __ffs(b) - 1;
+        body(t.u_lo + k, __uint_as_float(t.cells.count[k]));
+      }
+  }
+}
+
+// The adjusted logit of a touched token.
+__device__ __forceinline__ float touched_logit(TouchTable &t, int u) {
+  const int k = u - t.u_lo;
+  if (!t.hashed) return __uint_as_float(t.cells.count[k]);
+  uint32_t s = hash_slot(k);
+  while (t.hash.key[s] != k) s = (s + 1) & (kHashSlots - 1);  // its bit is set: it is there
+  return __uint_as_float(t.hash.count[s]);
+}
+
+// Fills the table for u in [u_lo, min(u_lo + touch_span, u_hi)); every thread
+// of the block calls it, and a barrier ends it.  Counts come from integer
+// adds, maxima and ors: what a token finds does not depend on the threads'
+// order.
+template <typename T>
+__device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, const Row<T> &row,
+                                           int u_lo, int u_hi, int tid, int threads) {
   const int span = min(touch_span(a), u_hi - u_lo);
+  const bool hashed = span > kTouchSpan;
+  const int64_t n = a.history_n + a.bias_n;
   auto place = [&](int64_t i) {
     const int v = i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n];
-    const int k = v + shift - u_lo;
-    return v >= 0 && v < vocab && k >= 0 && k < span ? k : -1;
+    const int k = v + row.shift - u_lo;
+    return v >= 0 && v < row.vocab && k >= 0 && k < span ? k : -1;
   };
-  const int64_t n = a.history_n + a.bias_n;
+  // the adjusted logit of the token at place k
+  auto adjusted = [&](int k, uint32_t count, uint32_t entry) {
+    const int u = u_lo + k, v = u - row.shift;
+    float z = logit_float(row.at0[u]);
+    if (count > 0) {
+      z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
+      z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(count), a.frequency), a.presence));
+    }
+    if (entry > 0) z = __fadd_rn(z, a.bias_values[entry - 1]);
+    if (a.mask && !(a.mask[v >> 5] >> (v & 31) & 1)) z = kNegInf;
+    return __float_as_uint(z);
+  };
+  // the first entry is on its way while the table is cleared
+  const int first = tid < n ? place(tid) : -1;
   __syncthreads();
+  if (tid == 0) {
+    t.hashed = hashed;
+    t.u_lo = u_lo;
+    t.span = span;
+  }
   uint32_t *bits = hashed ? t.hash.bits : t.cells.bits;
   for (int i = tid; i < (span + 31) / 32; i += threads) bits[i] = 0;
   if (hashed) {
@@ -250,7 +312,7 @@ __device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, in
       key[kHashSlots / 4 + i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     for (int i = tid; i < (int)n; i += threads) {
-      const int k = place(i);
+      const int k = i == tid ? first : place(i);
       if (k < 0) continue;
       atomicOr(&bits[k >> 5], 1u << (k & 31));
       uint32_t s = hash_slot(k);
@@ -260,11 +322,15 @@ __device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, in
       if (i < a.history_n) atomicAdd(&t.hash.count[s], 1u);
       else atomicMax(&t.hash.bias[s], (uint32_t)(i - a.history_n) + 1u);
     }
+    __syncthreads();
+    for (int s = tid; s < kHashSlots; s += threads)
+      if (t.hash.key[s] >= 0)
+        t.hash.count[s] = adjusted(t.hash.key[s], t.hash.count[s], t.hash.bias[s]);
   } else {
     // only cells that are touched are ever read, so only those are cleared
     __syncthreads();
     for (int64_t i = tid; i < n; i += threads) {
-      const int k = place(i);
+      const int k = i == tid ? first : place(i);
       if (k < 0) continue;
       t.cells.count[k] = 0;
       t.cells.bias[k] = 0;
@@ -272,46 +338,19 @@ __device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, in
     }
     __syncthreads();
     for (int64_t i = tid; i < n; i += threads) {
-      const int k = place(i);
+      const int k = i == tid ? first : place(i);
       if (k < 0) continue;
       if (i < a.history_n) atomicAdd(&t.cells.count[k], 1u);
       else atomicMax(&t.cells.bias[k], (uint32_t)(i - a.history_n) + 1u);
     }
+    __syncthreads();
+    for (int w = tid; w < (span + 31) / 32; w += threads)
+      for (uint32_t b = bits[w]; b != 0; b &= b - 1) {
+        const int k = w * 32 + __ffs(b) - 1;
+        t.cells.count[k] = adjusted(k, t.cells.count[k], t.cells.bias[k]);
+      }
   }
   __syncthreads();
-}
-
-// The penalties and bias of one touched token (place k of the table's span).
-static __device__ __noinline__ float touched_logit(float z, const TouchTable &t, const RowAdjust &a,
-                                            int k) {  // both in shared memory
-  uint32_t n, e;
-  if (small_window(a)) {
-    uint32_t s = hash_slot(k);
-    while (t.hash.key[s] != k) s = (s + 1) & (kHashSlots - 1);  // its bit is set: it is there
-    n = t.hash.count[s];
-    e = t.hash.bias[s];
-  } else {
-    n = t.cells.count[k];
-    e = t.cells.bias[k];
-  }
-  if (n > 0) {
-    z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
-    z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(n), a.frequency), a.presence));
-  }
-  if (e > 0) z = __fadd_rn(z, a.bias_values[e - 1]);
-  return z;
-}
-
-// Penalties and biases of a vector at place k0 of the table's span.
-template <int N>
-__device__ __forceinline__ void touch_vector(float (&z)[N], const TouchTable &t,
-                                             const RowAdjust &a, int k0) {
-  const uint32_t *bits = small_window(a) ? t.hash.bits : t.cells.bits;
-  const uint32_t hit = (bits[k0 >> 5] >> (k0 & 31)) & ((1u << N) - 1u);
-  if (hit == 0) return;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (hit >> i & 1) z[i] = touched_logit(z[i], t, a, k0 + i);
 }
 
 // -inf where the row's mask is 0.

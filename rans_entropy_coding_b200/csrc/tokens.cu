@@ -381,27 +381,39 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     if (touch) span = touch_span(a);
   }
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
+  if (DECODE && ADJ && touch)  // added to after the first walk's barrier
+    for (int i = tid; i < slice / kTile; i += threads) tile_sums[i] = make_uint2(0, 0);
   int table_at = -1;
   auto need_table = [&](int u_lo) {
     if (!ADJ || !touch || table_at == u_lo) return;
-    fill_touch(table, a, row.shift, in.vocab, u_lo, hi, tid, threads);
+    fill_touch(table, a, row, u_lo, hi, tid, threads);
     table_at = u_lo;
   };
-  // walks this block's tiles: body(tile's first u, its number)
-  auto walk = [&](auto body) {
+  // walks this block's tiles, body(tile's first u, its number), and the touched
+  // tokens of its tables, which the tiles leave out: touched_body(u, logit)
+  auto walk = [&](auto body, auto touched_body) {
     for (int u_lo = lo; u_lo < hi; u_lo = span < hi - u_lo ? u_lo + span : hi) {
       need_table(u_lo);
       const int u_hi = span < hi - u_lo ? u_lo + span : hi;
       for (int u = u_lo + wid * kTile; u < u_hi; u += warps * kTile) body(u, (u - lo) / kTile);
+      if (ADJ && touch) each_touched(table, tid, threads, touched_body);
     }
   };
-  // adjusted logits of this lane's vector at u0, wherever that is
-  auto fetch = [&](int u0, float (&z)[N]) {
+  // adjusted logits of this lane's vector at u0, wherever that is; touched ones
+  // read -inf unless asked for
+  auto fetch = [&](int u0, float (&z)[N], bool all) {
     row.load(u0, z, kNegInf);
     if constexpr (ADJ) {
       if (u0 < row.end()) {
-        if (touch) touch_vector<N>(z, table, a, u0 - table_at);
         if (masked) mask_vector<N>(z, a, u0 - row.shift);
+        if (touch) {
+          const uint32_t hit = table.hits<N>(u0);
+          if (hit) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+              if (hit >> i & 1) z[i] = all ? touched_logit(table, u0 + i) : kNegInf;
+          }
+        }
       }
       if (!row.whole(u0)) {
 #pragma unroll
@@ -416,11 +428,19 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
 #pragma unroll
     for (int k = 0; k < kTileVecs; ++k)
       q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
-    if (ADJ && masked) {
+    if constexpr (ADJ) {
+      // the tokens that the mask leaves and nothing touches
 #pragma unroll
       for (int k = 0; k < kTileVecs; ++k) {
         const int v0 = u + k * kVecRow + lane * N - row.shift, w = v0 >> 5;
-        ok[k] = __funnelshift_r(a.mask[w], a.mask[min(w + 1, a.mask_words - 1)], v0 & 31);
+        ok[k] = ~0u;
+        if (masked)
+          ok[k] = __funnelshift_r(a.mask[w], a.mask[min(w + 1, a.mask_words - 1)], v0 & 31);
+      }
+      if (touch) {
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k)
+          ok[k] &= ~table.hits<N>(u + k * kVecRow + lane * N);
       }
     }
   };
@@ -442,10 +462,9 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
         for (int k = 0; k < kTileVecs; ++k) {
           float z[N];
           unpack16(q[k], z, T());
-          if (touch) touch_vector<N>(z, table, a, u + k * kVecRow + lane * N - table_at);
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            const bool alive = !masked || (ok[k] >> i & 1);
+            const bool alive = ok[k] >> i & 1;
             m = max_nan(m, alive ? z[i] : kNegInf);
             least = fminf(least, alive ? z[i] : __builtin_huge_valf());
           }
@@ -455,12 +474,12 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
 #pragma unroll
       for (int k = 0; k < kTileVecs; ++k) {
         float z[N];
-        fetch(u + k * kVecRow + lane * N, z);
+        fetch(u + k * kVecRow + lane * N, z, false);
 #pragma unroll
         for (int i = 0; i < N; ++i) m = max_nan(m, z[i]);
       }
     }
-  });
+  }, [&](int, float z) { m = max_nan(m, z); });
   if constexpr (!ADJ) {
     m = max_nan(m, ends.largest());
     least = ends.smallest();
@@ -510,14 +529,9 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
         float z[N];
         unpack16(q[k], z, T());
         if constexpr (ADJ) {
-          if (touch) touch_vector<N>(z, table, a, u + k * kVecRow + lane * N - table_at);
-          if (masked) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) z[i] = ok[k] >> i & 1 ? z[i] : dead;
-            n += __popc(ok[k] & ((1u << N) - 1u));
-          } else {
-            n += N;
-          }
+          for (int i = 0; i < N; ++i) z[i] = ok[k] >> i & 1 ? z[i] : dead;
+          n += __popc(ok[k] & ((1u << N) - 1u));
         }
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
@@ -531,7 +545,7 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
 #pragma unroll
       for (int k = 0; k < kTileVecs; ++k) {
         float z[N];
-        fetch(u + k * kVecRow + lane * N, z);
+        fetch(u + k * kVecRow + lane * N, z, false);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           w += token_weight(z[i], rs.scale, rs.ymax);
@@ -544,7 +558,14 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     if constexpr (DECODE) {
       w = __reduce_add_sync(kFull, w);
       n = __reduce_add_sync(kFull, n);
-      if (lane == 0) tile_sums[tile] = make_uint2(w, n);
+      if (lane == 0) {
+        if (ADJ && touch) {  // touched tokens are added by others
+          atomicAdd(&tile_sums[tile].x, w);
+          atomicAdd(&tile_sums[tile].y, n);
+        } else {
+          tile_sums[tile] = make_uint2(w, n);
+        }
+      }
     } else if (u + kTile <= u_target) {
       s.below_w += w;
       s.below_n += n;
@@ -553,7 +574,7 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
       for (int k = 0; k < kTileVecs; ++k) {
         const int u0 = u + k * kVecRow + lane * N;
         float z[N];
-        fetch(u0, z);
+        fetch(u0, z, false);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const uint32_t wi = token_weight(z[i], rs.scale, rs.ymax);
@@ -565,6 +586,21 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
           if (u0 + i == u_target && ni) peer_store(peer_address(&own_weight, 0), wi);
         }
       }
+    }
+  }, [&](int u, float z) {
+    const uint32_t w = token_weight(z, rs.scale, rs.ymax);
+    const uint32_t n = z > kNegInf ? 1u : 0u;
+    s.w += w;
+    s.n += n;
+    if constexpr (DECODE) {
+      atomicAdd(&tile_sums[(u - lo) / kTile].x, w);
+      atomicAdd(&tile_sums[(u - lo) / kTile].y, n);
+    } else {
+      if (u < u_target) {
+        s.below_w += w;
+        s.below_n += n;
+      }
+      if (u == u_target && n) peer_store(peer_address(&own_weight, 0), w);
     }
   });
   const Sums sum = warp_total({s.w, s.n});
@@ -664,7 +700,7 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     for (int k = 0; k < kTileVecs; ++k) {
       const int u0 = u + k * kVecRow + lane * N;
       float z[N];
-      fetch(u0, z);
+      fetch(u0, z, true);
       Sums own = {0, 0};
 #pragma unroll
       for (int i = 0; i < N; ++i)

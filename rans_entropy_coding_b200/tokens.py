@@ -11,6 +11,7 @@ learn of device errors (``check(rans_get_status(status))``).
 """
 import contextlib
 import ctypes
+import struct
 
 import torch
 
@@ -21,49 +22,59 @@ MAX_VOCAB = (1 << 19) - 8
 MAX_TOP = 4096
 TOKEN_PRECISION = 24
 
+# These calls are made once per decoded token, where the host's time counts: a
+# tensor's facts are asked once each, devices are compared by index, and
+# rans_logits is packed rather than built field by field.
+_pack_logits = struct.Struct("@Piiqq").pack
+assert struct.calcsize("@Piiqq") == ctypes.sizeof(L.rans_logits)
 _no_context = contextlib.nullcontext()
 
 
-def _place(device, stream):
+def _place(dev, stream):
     """Context in which to allocate and launch: the tensors' device and the
     caller's stream, where either is not the current one."""
     if stream is not None:
+        if stream.device.index != dev:
+            raise ValueError("stream on %s, tensors on cuda:%d" % (stream.device, dev))
         return torch.cuda.stream(stream)
-    if device.index != torch.cuda.current_device():
-        return torch.cuda.device(device)
+    if dev != torch.cuda.current_device():
+        return torch.cuda.device(dev)
     return _no_context
 
 
-def _launch_stream(device, stream):
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    if s.device != device:
-        raise ValueError("stream on %s, tensors on %s" % (s.device, device))
-    return ctypes.c_void_p(s.cuda_stream)
+def _raw_stream(dev):
+    """The device's current stream, as an address."""
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _logits(x, what="logits"):
+def _rows(x, what="logits"):
+    """(device index, rows, vocab, dtype code, row stride) of rows of logits."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
         raise ValueError("%s: a CUDA tensor [rows, vocab]" % what)
-    if x.dtype not in _LOGITS_CODE:
+    code = _LOGITS_CODE.get(x.dtype)
+    if code is None:
         raise ValueError("%s: float32, float16 or bfloat16, not %s" % (what, x.dtype))
     n, v = x.shape
     if not 1 <= v <= MAX_VOCAB:
         raise ValueError("%s: a vocabulary of 1 to %d tokens" % (what, MAX_VOCAB))
-    if (v > 1 and x.stride(1) != 1) or (n > 1 and x.stride(0) < v):
+    step, one = x.stride()
+    if (v > 1 and one != 1) or (n > 1 and step < v):
         raise ValueError("%s: rows must be contiguous and must not overlap" % what)
-    c = L.rans_logits()
-    c.data, c.dtype, c.vocab = x.data_ptr(), _LOGITS_CODE[x.dtype], v
-    c.rows, c.row_stride = n, max(x.stride(0), v)
-    return c
+    return x.get_device(), n, v, code, max(step, v)
 
 
-def _tensor(x, dtype, shape, device, what):
-    """A contiguous CUDA tensor of this type and shape on this device."""
-    if not isinstance(x, torch.Tensor) or x.dtype != dtype or x.device != device or \
-            not x.is_contiguous() or (shape is not None and tuple(x.shape) != tuple(shape)):
-        raise ValueError("%s: a contiguous %s tensor%s on %s" % (
-            what, dtype, "" if shape is None else " of shape %s" % (tuple(shape),), device))
-    return x
+def _packed(x, rows):
+    return _pack_logits(x.data_ptr(), rows[3], rows[2], rows[1], rows[4])
+
+
+def _tensor(x, dtype, shape, dev, what):
+    """The address of a contiguous CUDA tensor of this type and shape on device
+    `dev` (an index)."""
+    if not isinstance(x, torch.Tensor) or x.dtype is not dtype or x.get_device() != dev or \
+            not x.is_contiguous() or (shape is not None and x.shape != shape):
+        raise ValueError("%s: a contiguous %s tensor%s on cuda:%d" % (
+            what, dtype, "" if shape is None else " of shape %s" % (tuple(shape),), dev))
+    return x.data_ptr()
 
 
 def new_status(device="cuda"):
@@ -72,154 +83,155 @@ def new_status(device="cuda"):
     return torch.zeros(32, dtype=torch.int64, device=device)
 
 
-def _status(status, device):
+def _status(status, dev):
     if status is None:
-        return new_status(device)
-    if not isinstance(status, torch.Tensor) or status.device != device or \
+        return new_status(dev)
+    if not isinstance(status, torch.Tensor) or status.get_device() != dev or \
             not status.is_contiguous() or status.numel() * status.element_size() < 256:
-        raise ValueError("status: from new_status() on %s" % device)
+        raise ValueError("status: from new_status() on cuda:%d" % dev)
     return status
 
 
 # ---------------------------------------------------------- C entry points --
-def _ref(adjust, logits):
-    return None if adjust is None else ctypes.byref(adjust.bind(logits))
+def _ref(adjust, rows):
+    return None if adjust is None else adjust.bind(rows)
 
 
 def rans_adjust_logits(logits, adjust, out, stream=None):
-    c, o = _logits(logits), _logits(out, "out")
-    if out.shape != logits.shape or out.device != logits.device:
+    rows, o = _rows(logits), _rows(out, "out")
+    if o[:3] != rows[:3]:
         raise ValueError("out: a tensor of the logits' shape on their device")
-    with _place(logits.device, stream):
-        return L.lib().rans_adjust_logits(
-            ctypes.byref(c), _ref(adjust, logits), L._ptr(out), o.dtype, o.row_stride,
-            _launch_stream(logits.device, stream))
+    with _place(rows[0], stream):
+        return L.lib().rans_adjust_logits(_packed(logits, rows), _ref(adjust, rows),
+                                          out.data_ptr(), o[3], o[4], _raw_stream(rows[0]))
 
 
 def rans_token_intervals(logits, adjust, tokens, starts, freqs, status, stream=None):
-    c, n, dev = _logits(logits), logits.shape[0], logits.device
-    for x, what in ((tokens, "tokens"), (starts, "starts"), (freqs, "freqs")):
-        _tensor(x, torch.int32, (n,), dev, what)
+    rows = _rows(logits)
+    dev, n = rows[:2]
+    t = _tensor(tokens, torch.int32, (n,), dev, "tokens")
+    s = _tensor(starts, torch.int32, (n,), dev, "starts")
+    f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
     with _place(dev, stream):
-        return L.lib().rans_token_intervals(
-            ctypes.byref(c), _ref(adjust, logits), L._ptr(tokens), L._ptr(starts),
-            L._ptr(freqs), L._ptr(_status(status, dev)), _launch_stream(dev, stream))
+        return L.lib().rans_token_intervals(_packed(logits, rows), _ref(adjust, rows), t, s, f,
+                                            _status(status, dev).data_ptr(), _raw_stream(dev))
 
 
 def rans_encode_intervals(starts, freqs, n, chunking, out, stream_offsets, workspace,
                           stream=None):
-    dev = starts.device
-    _tensor(starts, torch.int32, (n,), dev, "starts")
-    _tensor(freqs, torch.int32, (n,), dev, "freqs")
-    _tensor(out, torch.uint8, None, dev, "out")
-    _tensor(workspace, torch.uint8, None, dev, "workspace")
+    dev = starts.get_device()
+    s = _tensor(starts, torch.int32, (n,), dev, "starts")
+    f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
+    o = _tensor(out, torch.uint8, None, dev, "out")
+    w = _tensor(workspace, torch.uint8, None, dev, "workspace")
     S = L.rans_num_streams(chunking, n)
-    if S >= 0:
-        _tensor(stream_offsets, torch.int64, (S + 1,), dev, "stream_offsets")
+    offs = _tensor(stream_offsets, torch.int64, (S + 1,) if S >= 0 else None, dev,
+                   "stream_offsets")
     with _place(dev, stream):
-        return L.lib().rans_encode_intervals(
-            L._ptr(starts), L._ptr(freqs), n, ctypes.byref(chunking.c), L._ptr(out), out.numel(),
-            L._ptr(stream_offsets), L._ptr(workspace), workspace.numel(),
-            _launch_stream(dev, stream))
+        return L.lib().rans_encode_intervals(s, f, n, ctypes.byref(chunking.c), o, out.numel(),
+                                             offs, w, workspace.numel(), _raw_stream(dev))
 
 
 def _streams(data, stream_offsets):
-    dev = data.device
-    _tensor(data, torch.uint8, None, dev, "data")
-    _tensor(stream_offsets, torch.int64, None, dev, "stream_offsets")
-    if stream_offsets.numel() < 1:
+    """(device index, S, the two addresses)."""
+    dev = data.get_device()
+    d = _tensor(data, torch.uint8, None, dev, "data")
+    o = _tensor(stream_offsets, torch.int64, None, dev, "stream_offsets")
+    S = stream_offsets.numel() - 1
+    if S < 0:
         raise ValueError("stream_offsets: S + 1 offsets")
-    return dev, stream_offsets.numel() - 1
+    return dev, S, d, o
 
 
 def rans_token_states(data, stream_offsets, states, status, stream=None):
-    dev, S = _streams(data, stream_offsets)
-    _tensor(states, torch.int64, (S, 2), dev, "states")
+    dev, S, d, o = _streams(data, stream_offsets)
+    s = _tensor(states, torch.int64, (S, 2), dev, "states")
     with _place(dev, stream):
-        return L.lib().rans_token_states(
-            L._ptr(data), data.numel(), L._ptr(stream_offsets), S, L._ptr(states),
-            L._ptr(_status(status, dev)), _launch_stream(dev, stream))
+        return L.lib().rans_token_states(d, data.numel(), o, S, s,
+                                         _status(status, dev).data_ptr(), _raw_stream(dev))
 
 
 def rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states_in, states_out,
                        tokens, status, stream=None):
-    c, n = _logits(logits), logits.shape[0]
-    dev, S = _streams(data, stream_offsets)
-    if dev != logits.device:
-        raise ValueError("data on %s, logits on %s" % (dev, logits.device))
-    if stream_ids is not None:
-        _tensor(stream_ids, torch.int32, (n,), dev, "stream_ids")
-    _tensor(states_in, torch.int64, (S, 2), dev, "states")
-    _tensor(states_out, torch.int64, (S, 2), dev, "states_out")
-    _tensor(tokens, torch.int32, (n,), dev, "tokens")
+    rows = _rows(logits)
+    dev, S, d, o = _streams(data, stream_offsets)
+    if dev != rows[0]:
+        raise ValueError("data on cuda:%d, logits on cuda:%d" % (dev, rows[0]))
+    n = rows[1]
+    ids = None if stream_ids is None else _tensor(stream_ids, torch.int32, (n,), dev,
+                                                  "stream_ids")
+    a = _tensor(states_in, torch.int64, (S, 2), dev, "states")
+    b = _tensor(states_out, torch.int64, (S, 2), dev, "states_out")
+    t = _tensor(tokens, torch.int32, (n,), dev, "tokens")
     with _place(dev, stream):
         return L.lib().rans_decode_tokens(
-            ctypes.byref(c), _ref(adjust, logits), L._ptr(data), data.numel(),
-            L._ptr(stream_offsets), S, L._ptr(stream_ids), L._ptr(states_in),
-            L._ptr(states_out), L._ptr(tokens), L._ptr(_status(status, dev)),
-            _launch_stream(dev, stream))
+            _packed(logits, rows), _ref(adjust, rows), d, data.numel(), o, S, ids, a, b, t,
+            _status(status, dev).data_ptr(), _raw_stream(dev))
 
 
 def rans_token_states_finish(stream_offsets, states, status, stream=None):
-    dev, S = _streams(torch.empty(0, dtype=torch.uint8, device=states.device), stream_offsets)
-    _tensor(states, torch.int64, (S, 2), dev, "states")
+    dev = states.get_device()
+    o = _tensor(stream_offsets, torch.int64, None, dev, "stream_offsets")
+    S = stream_offsets.numel() - 1
+    s = _tensor(states, torch.int64, (S, 2), dev, "states")
     with _place(dev, stream):
-        return L.lib().rans_token_states_finish(
-            L._ptr(stream_offsets), S, L._ptr(states), L._ptr(_status(status, dev)),
-            _launch_stream(dev, stream))
+        return L.lib().rans_token_states_finish(o, S, s, _status(status, dev).data_ptr(),
+                                                _raw_stream(dev))
 
 
 def _teacher(logits, ids, logprobs):
-    c, n, dev = _logits(logits), logits.shape[0], logits.device
+    """(rows of the logits, K, the teacher's two addresses)."""
+    rows = _rows(logits)
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or not 1 <= ids.shape[1] <= MAX_TOP:
         raise ValueError("ids: a tensor [rows, K], K from 1 to %d" % MAX_TOP)
-    _tensor(ids, torch.int32, (n, ids.shape[1]), dev, "ids")
-    _tensor(logprobs, torch.float32, (n, ids.shape[1]), dev, "logprobs")
-    return c, n, ids.shape[1], dev
+    K = ids.shape[1]
+    i = _tensor(ids, torch.int32, (rows[1], K), rows[0], "ids")
+    return rows, K, i, _tensor(logprobs, torch.float32, (rows[1], K), rows[0], "logprobs")
 
 
 def rans_distill_forward(logits, ids, logprobs, inv_temperature, tail, losses, stats, status,
                          stream=None):
-    c, n, K, dev = _teacher(logits, ids, logprobs)
-    _tensor(losses, torch.float32, (n,), dev, "losses")
-    _tensor(stats, torch.float32, (n, 8), dev, "stats")
+    rows, K, i, lp = _teacher(logits, ids, logprobs)
+    dev, n = rows[:2]
+    o = _tensor(losses, torch.float32, (n,), dev, "losses")
+    s = _tensor(stats, torch.float32, (n, 8), dev, "stats")
     with _place(dev, stream):
         return L.lib().rans_distill_forward(
-            ctypes.byref(c), L._ptr(ids), L._ptr(logprobs), K, inv_temperature, int(tail),
-            L._ptr(losses), L._ptr(stats), L._ptr(_status(status, dev)),
-            _launch_stream(dev, stream))
+            _packed(logits, rows), i, lp, K, inv_temperature, int(tail), o, s,
+            _status(status, dev).data_ptr(), _raw_stream(dev))
 
 
-def _grad_of(logits, grad):
-    o = _logits(grad, "grad")
-    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device:
+def _grad_of(rows, grad):
+    """(address, row stride) of a gradient of these rows."""
+    o = _rows(grad, "grad")
+    if o[:4] != rows[:4]:
         raise ValueError("grad: a tensor of the logits' shape and type on their device")
-    return o.row_stride
+    return grad.data_ptr(), o[4]
 
 
 def rans_distill_backward(logits, ids, logprobs, inv_temperature, stats, grad_losses, grad,
                           stream=None):
-    c, n, K, dev = _teacher(logits, ids, logprobs)
-    _tensor(stats, torch.float32, (n, 8), dev, "stats")
-    _tensor(grad_losses, torch.float32, (n,), dev, "grad_losses")
-    stride = _grad_of(logits, grad)
+    rows, K, i, lp = _teacher(logits, ids, logprobs)
+    dev, n = rows[:2]
+    s = _tensor(stats, torch.float32, (n, 8), dev, "stats")
+    w = _tensor(grad_losses, torch.float32, (n,), dev, "grad_losses")
+    g, step = _grad_of(rows, grad)
     with _place(dev, stream):
-        return L.lib().rans_distill_backward(
-            ctypes.byref(c), L._ptr(ids), L._ptr(logprobs), K, inv_temperature, L._ptr(stats),
-            L._ptr(grad_losses), L._ptr(grad), stride, _launch_stream(dev, stream))
+        return L.lib().rans_distill_backward(_packed(logits, rows), i, lp, K, inv_temperature, s,
+                                             w, g, step, _raw_stream(dev))
 
 
 def rans_distill(logits, ids, logprobs, inv_temperature, tail, grad_losses, losses, grad, status,
                  stream=None):
-    c, n, K, dev = _teacher(logits, ids, logprobs)
-    _tensor(grad_losses, torch.float32, (n,), dev, "weights")
-    _tensor(losses, torch.float32, (n,), dev, "losses")
-    stride = _grad_of(logits, grad)
+    rows, K, i, lp = _teacher(logits, ids, logprobs)
+    dev, n = rows[:2]
+    w = _tensor(grad_losses, torch.float32, (n,), dev, "weights")
+    o = _tensor(losses, torch.float32, (n,), dev, "losses")
+    g, step = _grad_of(rows, grad)
     with _place(dev, stream):
-        return L.lib().rans_distill(
-            ctypes.byref(c), L._ptr(ids), L._ptr(logprobs), K, inv_temperature, int(tail),
-            L._ptr(grad_losses), L._ptr(losses), L._ptr(grad), stride,
-            L._ptr(_status(status, dev)), _launch_stream(dev, stream))
+        return L.lib().rans_distill(_packed(logits, rows), i, lp, K, inv_temperature, int(tail),
+                                    w, o, g, step, _status(status, dev).data_ptr(),
+                                    _raw_stream(dev))
 
 
 # ----------------------------------------------------------------- helpers --
@@ -267,20 +279,19 @@ class LogitAdjust:
     def __init__(self, temperature=1.0, repetition=1.0, frequency=0.0, presence=0.0,
                  history=None, bias=None, mask=None):
         c = L.rans_adjust()
-        self.c, self._rows, self._words, self._keep, self._device = c, None, 0, [], None
+        self.c, self._n, self._words, self._dev = c, None, 0, None
+        self._keep = keep = [history, bias, mask]
         parts = (repetition, frequency, presence, temperature)
         if any(isinstance(x, torch.Tensor) for x in parts):
-            rows = {x.numel() for x in parts if isinstance(x, torch.Tensor)}
-            dev = [x.device for x in parts if isinstance(x, torch.Tensor)][0]
-            if len(rows) != 1:
-                raise ValueError("per-row parameters of different lengths")
-            n = rows.pop()
+            one = [x for x in parts if isinstance(x, torch.Tensor)][0]
+            dev, n = self._on(one, one.numel()), one.numel()
             cols = [x if isinstance(x, torch.Tensor) else
-                    torch.full((n,), float(x), device=dev) for x in parts]
+                    torch.full((n,), float(x), device=one.device) for x in parts]
             for x in cols:
                 _tensor(x, torch.float32, (n,), dev, "per-row parameters")
             cols[3] = 1.0 / cols[3]
-            c.params = self._hold(torch.stack(cols, 1), n)
+            keep.append(torch.stack(cols, 1))
+            c.params = keep[-1].data_ptr()
         else:
             c.repetition = _positive(repetition, "repetition")
             c.frequency = _finite(frequency, "frequency")
@@ -289,68 +300,70 @@ class LogitAdjust:
                                           "1 / temperature")
         if history is not None:
             tokens, begin, end = history
-            dev, n = tokens.device, begin.numel()
-            _tensor(tokens, torch.int32, (tokens.numel(),), dev, "history tokens")
-            _tensor(begin, torch.int64, (n,), dev, "history begin")
-            _tensor(end, torch.int64, (n,), dev, "history end")
-            if tokens.numel() > 0:
-                c.history, c.history_len = self._hold(tokens), tokens.numel()
-                c.history_begin, c.history_end = self._hold(begin, n), self._hold(end, n)
+            k, n = tokens.numel(), begin.numel()
+            dev = self._on(begin, n)
+            t = _tensor(tokens, torch.int32, (k,), dev, "history tokens")
+            b = _tensor(begin, torch.int64, (n,), dev, "history begin")
+            e = _tensor(end, torch.int64, (n,), dev, "history end")
+            if k > 0:
+                c.history, c.history_begin, c.history_end, c.history_len = t, b, e, k
         if bias is not None:
             ids, values, begin, end = bias
-            dev, n = ids.device, begin.numel()
-            _tensor(ids, torch.int32, (ids.numel(),), dev, "bias ids")
-            _tensor(values, torch.float32, (ids.numel(),), dev, "bias values")
-            _tensor(begin, torch.int64, (n,), dev, "bias begin")
-            _tensor(end, torch.int64, (n,), dev, "bias end")
-            if ids.numel() > 0:
-                c.bias_ids, c.bias_values = self._hold(ids), self._hold(values)
-                c.bias_len = ids.numel()
-                c.bias_begin, c.bias_end = self._hold(begin, n), self._hold(end, n)
+            k, n = ids.numel(), begin.numel()
+            dev = self._on(begin, n)
+            i = _tensor(ids, torch.int32, (k,), dev, "bias ids")
+            w = _tensor(values, torch.float32, (k,), dev, "bias values")
+            b = _tensor(begin, torch.int64, (n,), dev, "bias begin")
+            e = _tensor(end, torch.int64, (n,), dev, "bias end")
+            if k > 0:
+                c.bias_ids, c.bias_values, c.bias_len = i, w, k
+                c.bias_begin, c.bias_end = b, e
         if mask is not None:
-            if mask.dtype != torch.int32 or mask.dim() not in (1, 2) or \
+            if mask.dtype is not torch.int32 or mask.dim() not in (1, 2) or \
                     (mask.shape[-1] > 1 and mask.stride(-1) != 1):
                 raise ValueError("mask: int32 words [rows, words] or [words], from pack_mask")
             self._words = mask.shape[-1]
             if mask.dim() == 2:
-                if mask.shape[0] > 1 and mask.stride(0) < mask.shape[1]:
+                n, step = mask.shape[0], mask.stride(0)
+                if n > 1 and step < self._words:
                     raise ValueError("mask: rows must not overlap")
-                c.mask = self._hold(mask, mask.shape[0])
-                c.mask_stride = max(mask.stride(0), mask.shape[1])
+                self._on(mask, n)
+                c.mask_stride = max(step, self._words)
             else:
-                c.mask = self._hold(mask)
+                self._on(mask, self._n)
+            c.mask = mask.data_ptr()
 
-    def _hold(self, x, rows=None):
-        if not x.is_cuda or (self._device is not None and x.device != self._device):
+    def _on(self, x, n):
+        """The device of a part for n rows, which all parts share."""
+        dev = x.get_device()
+        if dev < 0 or self._dev not in (None, dev):
             raise ValueError("LogitAdjust takes CUDA tensors on one device")
-        if rows is not None:
-            if self._rows is not None and rows != self._rows:
-                raise ValueError("parts for %d and for %d rows" % (self._rows, rows))
-            self._rows = rows
-        self._device = x.device
-        self._keep.append(x)
-        return x.data_ptr()
+        if n is not None and self._n not in (None, n):
+            raise ValueError("parts for %d and for %d rows" % (self._n, n))
+        self._dev, self._n = dev, n
+        return dev
 
-    def bind(self, logits):
-        """The C struct, checked against the rows it is to be used on."""
-        n, v = logits.shape
-        if self._device is not None and self._device != logits.device:
-            raise ValueError("LogitAdjust on %s, logits on %s" % (self._device, logits.device))
-        if self._rows is not None and self._rows != n:
-            raise ValueError("LogitAdjust for %d rows, logits of %d" % (self._rows, n))
+    def bind(self, rows):
+        """The C struct, checked against the rows it is to be used on (as
+        _rows has them)."""
+        dev, n, v = rows[:3]
+        if self._dev not in (None, dev):
+            raise ValueError("LogitAdjust on cuda:%d, logits on cuda:%d" % (self._dev, dev))
+        if self._n not in (None, n):
+            raise ValueError("LogitAdjust for %d rows, logits of %d" % (self._n, n))
         if self.c.mask and self._words < (v + 31) // 32:
             raise ValueError("mask: %d words for %d tokens" % (self._words, v))
-        return self.c
+        return ctypes.byref(self.c)
 
 
 def adjust_logits(logits, adjust, out=None, dtype=None, stream=None):
     """Adjusted logits (penalties, biases, temperature, mask) for a sampler, in
     the logits' type or `dtype`; out may be the logits themselves."""
-    _logits(logits)
-    with _place(logits.device, stream):
-        if out is None:
+    if out is None:
+        dev = _rows(logits)[0]
+        with _place(dev, stream):
             out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=logits.device)
-        L.check(rans_adjust_logits(logits, adjust, out, stream), "adjust_logits")
+    L.check(rans_adjust_logits(logits, adjust, out, stream), "adjust_logits")
     return out
 
 
@@ -358,15 +371,15 @@ def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status
                     stream=None):
     """(starts, freqs), int32 [rows]: each row's interval of its token at
     TOKEN_PRECISION bits.  Rows with token -1 are skipped."""
-    _logits(logits)
-    with _place(logits.device, stream):
-        n, dev = logits.shape[0], logits.device
+    dev, n = _rows(logits)[:2]
+    with _place(dev, stream):
         if starts is None:
-            starts = torch.empty(n, dtype=torch.int32, device=dev)
+            starts = torch.empty(n, dtype=torch.int32, device=logits.device)
         if freqs is None:
-            freqs = torch.empty(n, dtype=torch.int32, device=dev)
-        L.check(rans_token_intervals(logits, adjust, tokens, starts, freqs,
-                                     _status(status, dev), stream), "token_intervals")
+            freqs = torch.empty(n, dtype=torch.int32, device=logits.device)
+        status = _status(status, dev)
+    L.check(rans_token_intervals(logits, adjust, tokens, starts, freqs, status, stream),
+            "token_intervals")
     return starts, freqs
 
 
@@ -378,24 +391,27 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
     S = L.rans_num_streams(chunking, n)
     if S < 0:
         L.check(int(S), "num_streams")
-    with _place(dev, stream):
+    with _place(starts.get_device(), stream):
         if ws is None:
-            ws = L.aligned_empty(L.rans_encode_workspace_bytes(chunking, n), dev)
+            # torch's blocks are aligned to 512 bytes, as the workspace has to be to 256
+            ws = torch.empty(L.rans_encode_workspace_bytes(chunking, n), dtype=torch.uint8,
+                             device=dev)
         if out is None:
             out = torch.empty(L.rans_max_compressed_bytes(chunking, n), dtype=torch.uint8,
                               device=dev)
         offsets = torch.empty(S + 1, dtype=torch.int64, device=dev)
-        L.check(rans_encode_intervals(starts, freqs, n, chunking, out, offsets, ws, stream),
-                "encode_intervals")
+    L.check(rans_encode_intervals(starts, freqs, n, chunking, out, offsets, ws, stream),
+            "encode_intervals")
     return out, offsets, ws
 
 
 def token_states(data, stream_offsets, status=None, stream=None):
     """Decoder states of the streams, int64 [S, 2]: state and words taken."""
-    with _place(data.device, stream):
-        states = torch.empty(stream_offsets.numel() - 1, 2, dtype=torch.int64,
-                             device=data.device)
-        L.check(rans_token_states(data, stream_offsets, states, status, stream), "token_states")
+    dev, S = _streams(data, stream_offsets)[:2]
+    with _place(dev, stream):
+        states = torch.empty(S, 2, dtype=torch.int64, device=data.device)
+        status = _status(status, dev)
+    L.check(rans_token_states(data, stream_offsets, states, status, stream), "token_states")
     return states
 
 
@@ -404,18 +420,18 @@ def decode_tokens(logits, data, stream_offsets, states, adjust=None, stream_ids=
     """One decoding step: (tokens int32 [rows], new states).  Row r is the next
     position of stream stream_ids[r] (default r); out_states may be `states`.
     Rows with stream id -1 are skipped; without `tokens` they read -1."""
-    _logits(logits)
-    n, dev = logits.shape[0], logits.device
+    dev, n = _rows(logits)[:2]
     with _place(dev, stream):
         if out_states is None:
             every = stream_ids is None and n == stream_offsets.numel() - 1
             out_states = torch.empty_like(states) if every else states.clone()
         if tokens is None:
-            tokens = torch.empty(n, dtype=torch.int32, device=dev) if stream_ids is None else \
-                torch.full((n,), -1, dtype=torch.int32, device=dev)
-        L.check(rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states,
-                                   out_states, tokens, _status(status, dev), stream),
-                "decode_tokens")
+            tokens = torch.empty(n, dtype=torch.int32, device=logits.device) \
+                if stream_ids is None else \
+                torch.full((n,), -1, dtype=torch.int32, device=logits.device)
+        status = _status(status, dev)
+    L.check(rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states,
+                               out_states, tokens, status, stream), "decode_tokens")
     return tokens, out_states
 
 
@@ -447,11 +463,11 @@ def distill_loss(logits, ids, logprobs, temperature=1.0, tail=True, status=None)
     [rows], in nats, differentiable in the logits.  tail: the teacher's
     remaining mass is one more bucket; else its list is renormalised.  The
     teacher's probabilities take no gradient."""
-    _teacher(logits, ids, logprobs)
     inv = _positive(1.0 / _positive(temperature, "temperature"), "1 / temperature")
-    with _place(logits.device, None):
+    dev = _rows(logits)[0]
+    with _place(dev, None):
         return _Distill.apply(logits, ids, logprobs.detach(), inv, bool(tail),
-                              _status(status, logits.device))
+                              _status(status, dev))
 
 
 def distill_loss_and_grad(logits, ids, logprobs, weights, temperature=1.0, tail=True, grad=None,
@@ -459,12 +475,13 @@ def distill_loss_and_grad(logits, ids, logprobs, weights, temperature=1.0, tail=
     """(losses, gradient of sum(weights * losses) in the logits) in one call, for
     training loops that know the rows' weights; no autograd graph is built.
     grad may be the logits themselves."""
-    _teacher(logits, ids, logprobs)
     inv = _positive(1.0 / _positive(temperature, "temperature"), "1 / temperature")
-    with _place(logits.device, stream):
-        losses = torch.empty(logits.shape[0], dtype=torch.float32, device=logits.device)
+    dev, n = _rows(logits)[:2]
+    with _place(dev, stream):
+        losses = torch.empty(n, dtype=torch.float32, device=logits.device)
         if grad is None:
             grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        L.check(rans_distill(logits, ids, logprobs, inv, tail, weights, losses, grad,
-                             _status(status, logits.device), stream), "distill")
+        status = _status(status, dev)
+    L.check(rans_distill(logits, ids, logprobs, inv, tail, weights, losses, grad, status, stream),
+            "distill")
     return losses, grad
