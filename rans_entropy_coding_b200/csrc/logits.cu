@@ -6,76 +6,124 @@
 namespace rb {
 namespace {
 
-// A block takes kAdjTile elements of a row, all loaded before anything else.
-constexpr int kAdjThreads = 256;
+// A block takes a run of a row's tiles.  kAdjThreads threads stream them, four
+// vectors of 16 bytes each; where a history or biases are given, kTableThreads
+// more gather and adjust the touched logits meanwhile, whose values then go
+// over what the stream left in their places.  (That wait for window, table and
+// logits is a chain of memory latencies; before the stream, it cost as much as
+// the stream itself.)  In place, the touched logits have to be read first, and
+// all threads wait for that.
+constexpr int kAdjThreads = 512;
 constexpr int kAdjVecs = 4;
+constexpr int kTableThreads = 128;
 
 template <typename T, typename O, bool TOUCH, bool MASK>
-__global__ void __launch_bounds__(kAdjThreads)
-    adjust_kernel(rans_logits in, rans_adjust adj, O *out, int64_t out_stride, int blocks) {
+__global__ void __launch_bounds__(TOUCH ? kAdjThreads + kTableThreads : kAdjThreads, TOUCH ? 2 : 3)
+    adjust_kernel(rans_logits in, rans_adjust adj, O *out, int64_t out_stride, int blocks,
+                  int per_block) {
   extern __shared__ __align__(16) unsigned char smem[];
   TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
   constexpr int N = VecOf<T>::N;
   constexpr int kTile = kAdjThreads * kAdjVecs * N;
-  static_assert(kTile <= kTouchSpan, "one table per block");
-  const int tid = threadIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31;
   const int64_t r = blockIdx.x / blocks;
-  const int u_lo = (int)(blockIdx.x % blocks) * kTile;
   const Row<T> row(in.data, r, in.row_stride, in.vocab);
-  const int u_hi = min(u_lo + kTile, row.end());
-  uint4 q[kAdjVecs];
-#pragma unroll
-  for (int k = 0; k < kAdjVecs; ++k) {
-    const int u0 = u_lo + (k * kAdjThreads + tid) * N;
-    if (row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
-  }
+  const int lo = (int)(blockIdx.x % blocks) * per_block, hi = min(lo + per_block, row.end());
+  if (lo >= hi) return;
   const uint32_t *mask = MASK ? adj.mask + r * adj.mask_stride : nullptr;
   const int words = (in.vocab + 31) >> 5;
-  uint32_t ok[kAdjVecs];
-  if constexpr (MASK) {
-#pragma unroll
-    for (int k = 0; k < kAdjVecs; ++k)
-      ok[k] = mask_bits(mask, words, u_lo + (k * kAdjThreads + tid) * N - row.shift);
-  }
   const float inv_temperature = adj.params ? adj.params[4 * r + 3] : adj.inv_temperature;
-  bool touch = false;
-  if constexpr (TOUCH) {
-    __shared__ RowAdjust a;
-    if (tid == 0) a = row_adjust(adj, r, in.vocab);
-    __syncthreads();
-    touch = a.touches();
-    if (touch) fill_touch(table, a, row, u_lo, u_hi, tid, kAdjThreads);
-  }
   O *o = out + r * out_stride - row.shift;  // element u goes to o[u]
-  const bool aligned = (reinterpret_cast<uintptr_t>(o + u_lo) & 15) == 0 && sizeof(O) == sizeof(T);
+
+  auto stream = [&](int from, int to) {
+    for (int u = from; u < to; u += kTile) {
+      uint4 q[kAdjVecs];
+      uint32_t ok[kAdjVecs];
 #pragma unroll
-  for (int k = 0; k < kAdjVecs; ++k) {
-    const int u0 = u_lo + (k * kAdjThreads + tid) * N;
-    if (u0 >= u_hi) break;
-    float z[N];
-    const bool whole = row.whole(u0);
-    if (whole) unpack16(q[k], z, T());
-    else row.load(u0, z, 0.0f);
+      for (int k = 0; k < kAdjVecs; ++k) {
+        const int u0 = u + (k * kAdjThreads + tid) * N;
+        if (row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+      }
+      if constexpr (MASK) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      z[i] = __fmul_rn(z[i], inv_temperature);
-      if (MASK && !(ok[k] >> i & 1)) z[i] = kNegInf;
+        for (int k = 0; k < kAdjVecs; ++k)
+          ok[k] = load_mask<N>(mask, words, u + (k * kAdjThreads + tid - lane) * N - row.shift,
+                               lane);
+      }
+#pragma unroll
+      for (int k = 0; k < kAdjVecs; ++k) {
+        const int u0 = u + (k * kAdjThreads + tid) * N;
+        if (u0 - lane * N >= to) break;  // (a whole warp's)
+        const bool whole = row.whole(u0);
+        float z[N];
+        if (whole) unpack16(q[k], z, T());
+        else row.load(u0, z, 0.0f);
+#pragma unroll
+        for (int i = 0; i < N; ++i) z[i] = __fmul_rn(z[i], inv_temperature);
+        if constexpr (MASK) {
+          const uint32_t bits = lane_mask<N>(ok[k], u0 - lane * N - row.shift, lane);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (!(bits >> i & 1)) z[i] = kNegInf;
+        }
+        if constexpr (sizeof(O) == sizeof(T)) {
+          store_vectors(o, u0, pack16(z, O()), whole, row.shift, row.end());
+        } else {
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (u0 + i >= row.shift && u0 + i < row.end()) o[u0 + i] = float_logit<O>(z[i]);
+        }
+      }
     }
-    if (whole && aligned) {
-      if constexpr (sizeof(O) == sizeof(T))
-        *reinterpret_cast<uint4 *>(o + u0) = pack16(z, O());
+  };
+  if constexpr (!TOUCH) {
+    stream(lo, hi);
+  } else {
+    __shared__ RowAdjust a;
+    __shared__ bool table_dense;
+    constexpr int kAll = kAdjThreads + kTableThreads;
+    auto all = [] { __syncthreads(); };
+    auto write_touched = [&] {
+      each_touched(table, tid, kAll, [&](int u, float z) {
+        o[u] = float_logit<O>(__fmul_rn(z, inv_temperature));
+      });
+    };
+    bool dense = false;
+    int u_lo = lo;
+    if (static_cast<const void *>(out) != in.data) {
+      if (tid < kAdjThreads) {
+        stream(lo, hi);
+      } else {
+        auto among = [] { asm volatile("bar.sync 1, %0;" ::"n"(kTableThreads) : "memory"); };
+        if (tid == kAdjThreads) a = row_adjust(adj, r, in.vocab);
+        among();
+        if (a.touches())
+          u_lo += fill_touch(table, a, row, lo, hi, dense, tid - kAdjThreads, kTableThreads,
+                             among);
+        if (tid == kAdjThreads) table_dense = dense;
+      }
+      __syncthreads();
+      if (!a.touches()) return;
+      write_touched();
+      dense = table_dense;
+      // what the first table does not cover
+      u_lo = lo + table.span;
+      while (u_lo < hi) {
+        u_lo += fill_touch(table, a, row, u_lo, hi, dense, tid, kAll, all);
+        write_touched();
+      }
     } else {
-#pragma unroll
-      for (int i = 0; i < N; ++i)
-        if (u0 + i >= row.shift && u0 + i < row.end()) o[u0 + i] = float_logit<O>(z[i]);
+      if (tid == 0) a = row_adjust(adj, r, in.vocab);
+      __syncthreads();
+      while (u_lo < hi) {
+        const int from = u_lo;
+        if (a.touches()) u_lo += fill_touch(table, a, row, from, hi, dense, tid, kAll, all);
+        else u_lo = hi;
+        if (tid < kAdjThreads) stream(from, u_lo);
+        __syncthreads();
+        if (a.touches()) write_touched();
+      }
     }
-  }
-  if constexpr (TOUCH) {
-    if (!touch) return;
-    __syncthreads();  // the touched tokens' final values go over what stands there
-    each_touched(table, tid, kAdjThreads, [&](int u, float z) {
-      o[u] = float_logit<O>(__fmul_rn(z, inv_temperature));
-    });
   }
 }
 
@@ -88,11 +136,18 @@ int launch_adjust_t(const rans_logits &in, const rans_adjust &adj, void *out, in
                                 : adjust_kernel<T, O, false, false>);
   const uint32_t smem = touch ? (uint32_t)sizeof(TouchTable) : 0u;
   if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
   constexpr int kTile = kAdjThreads * kAdjVecs * VecOf<T>::N;
-  const int blocks = (in.vocab + VecOf<T>::N - 1 + kTile - 1) / kTile;
+  const int tiles = (in.vocab + VecOf<T>::N - 1 + kTile - 1) / kTile;
+  // tiles per block: one, until there are kAdjBlocks blocks for every SM
+  constexpr int kAdjBlocks = 6;
+  int64_t per = in.rows * tiles / ((int64_t)kAdjBlocks * num_sms(dev));
+  per = per < 1 ? 1 : per > tiles ? tiles : per;
+  const int blocks = (int)((tiles + per - 1) / per);
   if (in.rows > 0x7fffffff / blocks) return RANS_ERR_ARG;
-  kern<<<(unsigned)(in.rows * blocks), kAdjThreads, smem, st>>>(
-      in, adj, static_cast<O *>(out), out_stride, blocks);
+  kern<<<(unsigned)(in.rows * blocks), touch ? kAdjThreads + kTableThreads : kAdjThreads, smem,
+         st>>>(in, adj, static_cast<O *>(out), out_stride, blocks, (int)per * kTile);
   return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
 }
 

@@ -117,6 +117,67 @@ struct Row {
   }
 };
 
+// Stores a warp's 32 vectors of packed elements (lane l's at u0 = the warp's
+// first + l * N) to o[u0 ...], any alignment.  Where o's 16-byte boundaries fall
+// inside the vectors (odd vocabularies: the rows of a contiguous result start
+// anywhere), a lane joins its vector's tail to the next lane's head and stores
+// that; what is left at the two ends goes out as N single elements, a lane
+// each.  `whole`: every element of the lane's vector is to be stored; else
+// those with from <= u < to are, one by one.
+template <typename T>
+__device__ __forceinline__ void store_vectors(T *o, int u0, uint4 p, bool whole, int from, int to) {
+  constexpr int N = VecOf<T>::N;
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  const int past = (int)((reinterpret_cast<uintptr_t>(o + u0) & 15) / sizeof(T));
+  if (past == 0 && whole) {
+    *reinterpret_cast<uint4 *>(o + u0) = p;
+    return;
+  }
+  if (past == 0 || !__all_sync(kAll, whole)) {
+    const T *e = reinterpret_cast<const T *>(&p);
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (u0 + i >= from && u0 + i < to) o[u0 + i] = e[i];
+    return;
+  }
+  const int skip = N - past;  // elements up to the boundary; the same for the row
+  uint32_t w[8] = {p.x, p.y, p.z, p.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(kAll, w[i], 1);
+  // lane 0's first `skip` elements and lane 31's others, one per lane
+  uint32_t ends[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t a = __shfl_sync(kAll, w[i], 0), b = __shfl_sync(kAll, w[i], 31);
+    // an element of lane 0 sits below `skip`, one of lane 31 from it on
+    const int first = i * (int)(4 / sizeof(T));
+    if constexpr (sizeof(T) == 4) ends[i] = first < skip ? a : b;
+    else ends[i] = ((first < skip ? a : b) & 0xffffu) | ((first + 1 < skip ? a : b) & 0xffff0000u);
+  }
+  if (lane < N) {
+    const int i = lane * (int)sizeof(T) / 4;
+    const uint32_t x = i == 0 ? ends[0] : i == 1 ? ends[1] : i == 2 ? ends[2] : ends[3];
+    T *at = o + u0 - lane * N + (lane < skip ? lane : 31 * N + lane);
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t *>(at) = x;
+    else *reinterpret_cast<uint16_t *>(at) = (uint16_t)(lane & 1 ? x >> 16 : x);
+  }
+  const int words = skip * (int)sizeof(T) / 4;
+  if (words & 1) {
+#pragma unroll
+    for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+  }
+  if (words & 2) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+  }
+  if (sizeof(T) == 2 && (skip & 1)) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  if (lane < 31) *reinterpret_cast<uint4 *>(o + u0 + skip) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // ---------------------------------------------------------- adjustments --
 // One row's adjustments, resolved from rans_adjust.  Kernels keep it in shared
 // memory: it is the same for all threads, and most of it is read for touched
@@ -193,12 +254,11 @@ __device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int words, i
 // logit, measured on rows of 50,000 tokens with 300 touched).  So they are
 // gathered and adjusted first, the kernels' main walks leave them out by a
 // bitmap, and what they add comes from the table, a token per thread.
-// Up to kTouchSpan tokens have a cell each.  A block with more of a row's
-// tokens covers up to kHashSpan at once with a hash table, if the row's window
-// (history and biases together) has at most kHashWindow entries; else it goes
-// kTouchSpan tokens at a time.
+// The table is a hash that covers up to kHashSpan tokens at once.  If they
+// have more than kHashTokens touched ones among them, there is a cell per token
+// instead, for kTouchSpan tokens at a time.
 constexpr int kHashSlots = 4096;
-constexpr int kHashWindow = kHashSlots / 2;
+constexpr int kHashTokens = kHashSlots * 7 / 8;
 constexpr int kHashSpan = 1 << 17;
 constexpr int kTouchSpan = 8192;
 
@@ -209,6 +269,7 @@ struct __align__(16) TouchTable {
       int32_t key[kHashSlots];    // place in the span, or -1
       uint32_t count[kHashSlots]; // occurrences; then the adjusted logit
       uint32_t bias[kHashSlots];  // 1 + the last entry's position in the row's list
+      uint16_t used[kHashTokens]; // the slots in use, in any order
     } hash;
     struct {
       uint32_t bits[kTouchSpan / 32];
@@ -216,39 +277,35 @@ struct __align__(16) TouchTable {
       uint32_t bias[kTouchSpan];
     } cells;
   };
-  bool hashed;
   int u_lo, span;  // covers u in [u_lo, u_lo + span)
+  int n_used;      // touched tokens in the hash; more than kHashTokens: too many
+  int shift;       // 32 - log2(slots)
+  bool dense;      // a cell per token
 
-  __device__ __forceinline__ uint32_t *bitmap() { return hashed ? hash.bits : cells.bits; }
+  __device__ __forceinline__ uint32_t *bitmap() { return dense ? cells.bits : hash.bits; }
   // Bits of the touched ones of N tokens from u0 on (a multiple of N).
   template <int N>
   __device__ __forceinline__ uint32_t hits(int u0) {
     const int k = u0 - u_lo;
     return (bitmap()[k >> 5] >> (k & 31)) & ((1u << N) - 1u);
   }
+  __device__ __forceinline__ uint32_t slot(int k) const {
+    return (uint32_t)k * 2654435761u >> shift;  // Fibonacci hashing
+  }
+  __device__ __forceinline__ uint32_t next(uint32_t s) const {
+    return (s + 1) & ((1u << (32 - shift)) - 1u);
+  }
 };
-
-__device__ __forceinline__ bool small_window(const RowAdjust &a) {
-  return a.history_n + a.bias_n <= kHashWindow;
-}
-// Tokens that a table of the row's covers.
-__device__ __forceinline__ int touch_span(const RowAdjust &a) {
-  return small_window(a) ? kHashSpan : kTouchSpan;
-}
-
-__device__ __forceinline__ uint32_t hash_slot(int k) {
-  return (uint32_t)k * 2654435761u >> 20;  // Fibonacci hashing to 12 bits
-}
-static_assert(kHashSlots == 1 << 12, "hash_slot gives 12 bits");
 
 // body(u, its adjusted logit) for every touched token of the table, spread over
 // the block's threads.
 template <class Body>
 __device__ __forceinline__ void each_touched(TouchTable &t, int tid, int threads, Body body) {
-  if (t.hashed) {
-    for (int s = tid; s < kHashSlots; s += threads)
-      if (t.hash.key[s] >= 0)
-        body(t.u_lo + t.hash.key[s], __uint_as_float(t.hash.count[s]));
+  if (!t.dense) {
+    for (int i = tid; i < t.n_used; i += threads) {
+      const int s = t.hash.used[i];
+      body(t.u_lo + t.hash.key[s], __uint_as_float(t.hash.count[s]));
+    }
   } else {
     for (int w = tid; w < kTouchSpan / 32; w += threads)
       for (uint32_t b = w * 32 < t.span ? t.cells.bits[w] : 0u; b != 0; b &= b - 1) {
@@ -261,96 +318,145 @@ __device__ __forceinline__ void each_touched(TouchTable &t, int tid, int threads
 // The adjusted logit of a touched token.
 __device__ __forceinline__ float touched_logit(TouchTable &t, int u) {
   const int k = u - t.u_lo;
-  if (!t.hashed) return __uint_as_float(t.cells.count[k]);
-  uint32_t s = hash_slot(k);
-  while (t.hash.key[s] != k) s = (s + 1) & (kHashSlots - 1);  // its bit is set: it is there
+  if (t.dense) return __uint_as_float(t.cells.count[k]);
+  uint32_t s = t.slot(k);
+  while (t.hash.key[s] != k) s = t.next(s);  // its bit is set: it is there
   return __uint_as_float(t.hash.count[s]);
 }
 
-// Fills the table for u in [u_lo, min(u_lo + touch_span, u_hi)); every thread
-// of the block calls it, and a barrier ends it.  Counts come from integer
-// adds, maxima and ors: what a token finds does not depend on the threads'
-// order.
-template <typename T>
-__device__ __forceinline__ void fill_touch(TouchTable &t, const RowAdjust &a, const Row<T> &row,
-                                           int u_lo, int u_hi, int tid, int threads) {
-  const int span = min(touch_span(a), u_hi - u_lo);
-  const bool hashed = span > kTouchSpan;
+// Fills the table from u_lo on, up to u_hi, and returns the tokens it covers.
+// `dense` is a block's memory of having met too many touched tokens (false at
+// first).  Called by `threads` threads of the block that meet at `barrier`,
+// which also begins and ends it.  Counts
+// come from integer adds, maxima and ors: what a token finds does not depend on
+// the threads' order.
+template <typename T, class Barrier>
+__device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, const Row<T> &row,
+                                          int u_lo, int u_hi, bool &dense, int tid, int threads,
+                                          Barrier barrier) {
   const int64_t n = a.history_n + a.bias_n;
-  auto place = [&](int64_t i) {
-    const int v = i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n];
-    const int k = v + row.shift - u_lo;
-    return v >= 0 && v < row.vocab && k >= 0 && k < span ? k : -1;
+  int span = min(kHashSpan, u_hi - u_lo);
+  // body(place in the span or -1, entry) for the window's entries, four loads
+  // in flight per thread
+  auto window = [&](auto body) {
+    for (int64_t i0 = tid; i0 < n; i0 += 4 * threads) {
+      int v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int64_t i = i0 + j * threads;
+        v[j] = i >= n ? -1 : i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n];
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int k = v[j] + row.shift - u_lo;
+        if (v[j] >= 0 && v[j] < row.vocab && k >= 0 && k < span) body(k, i0 + j * threads);
+      }
+    }
   };
   // the adjusted logit of the token at place k
   auto adjusted = [&](int k, uint32_t count, uint32_t entry) {
     const int u = u_lo + k, v = u - row.shift;
     float z = logit_float(row.at0[u]);
+    const uint32_t ok = a.mask ? a.mask[v >> 5] >> (v & 31) & 1u : 1u;
+    const float bias = entry > 0 ? a.bias_values[entry - 1] : 0.0f;
     if (count > 0) {
       z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
       z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(count), a.frequency), a.presence));
     }
-    if (entry > 0) z = __fadd_rn(z, a.bias_values[entry - 1]);
-    if (a.mask && !(a.mask[v >> 5] >> (v & 31) & 1)) z = kNegInf;
-    return __float_as_uint(z);
+    if (entry > 0) z = __fadd_rn(z, bias);
+    return __float_as_uint(ok ? z : kNegInf);
   };
-  // the first entry is on its way while the table is cleared
-  const int first = tid < n ? place(tid) : -1;
-  __syncthreads();
-  if (tid == 0) {
-    t.hashed = hashed;
-    t.u_lo = u_lo;
-    t.span = span;
-  }
-  uint32_t *bits = hashed ? t.hash.bits : t.cells.bits;
-  for (int i = tid; i < (span + 31) / 32; i += threads) bits[i] = 0;
-  if (hashed) {
-    uint4 *key = reinterpret_cast<uint4 *>(t.hash.key);  // keys, then counts and biases
-    for (int i = tid; i < kHashSlots / 4; i += threads)
-      key[i] = make_uint4(~0u, ~0u, ~0u, ~0u);
-    for (int i = tid; i < kHashSlots / 2; i += threads)
-      key[kHashSlots / 4 + i] = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    for (int i = tid; i < (int)n; i += threads) {
-      const int k = i == tid ? first : place(i);
-      if (k < 0) continue;
-      atomicOr(&bits[k >> 5], 1u << (k & 31));
-      uint32_t s = hash_slot(k);
-      // at most kHashWindow keys: a free slot is always found
-      for (int old; (old = atomicCAS(&t.hash.key[s], -1, k)) != -1 && old != k;)
-        s = (s + 1) & (kHashSlots - 1);
+
+  if (!dense) {
+    // twice the window's entries, up to kHashSlots
+    int log2 = 6;
+    while (log2 < 12 && (1 << log2) < 2 * n) ++log2;
+    const int slots = 1 << log2;
+    barrier();
+    if (tid == 0) {
+      t.u_lo = u_lo;
+      t.span = span;
+      t.n_used = 0;
+      t.shift = 32 - log2;
+      t.dense = false;
+    }
+    uint32_t *bits = t.hash.bits;
+    for (int i = tid; i < (span + 31) / 32; i += threads) bits[i] = 0;
+    for (int i = tid; i < slots; i += threads) {
+      t.hash.key[i] = -1;
+      t.hash.count[i] = 0;
+      t.hash.bias[i] = 0;
+    }
+    barrier();
+    window([&](int k, int64_t i) {
+      uint32_t s = t.slot(k);
+      int old = 0, tries = 0;
+      // (a full table ends the search)
+      while (tries++ < slots && (old = atomicCAS(&t.hash.key[s], -1, k)) != -1 && old != k)
+        s = t.next(s);
+      if (old == -1) {
+        const int at = atomicAdd(&t.n_used, 1);
+        if (at < kHashTokens) t.hash.used[at] = (uint16_t)s;
+        atomicOr(&bits[k >> 5], 1u << (k & 31));
+      }
+      if (old != -1 && old != k) return;
       if (i < a.history_n) atomicAdd(&t.hash.count[s], 1u);
       else atomicMax(&t.hash.bias[s], (uint32_t)(i - a.history_n) + 1u);
-    }
-    __syncthreads();
-    for (int s = tid; s < kHashSlots; s += threads)
-      if (t.hash.key[s] >= 0)
+    });
+    barrier();
+    dense = t.n_used > kHashTokens;
+    if (!dense) {
+      for (int i = tid; i < t.n_used; i += threads) {
+        const int s = t.hash.used[i];
         t.hash.count[s] = adjusted(t.hash.key[s], t.hash.count[s], t.hash.bias[s]);
-  } else {
-    // only cells that are touched are ever read, so only those are cleared
-    __syncthreads();
-    for (int64_t i = tid; i < n; i += threads) {
-      const int k = i == tid ? first : place(i);
-      if (k < 0) continue;
-      t.cells.count[k] = 0;
-      t.cells.bias[k] = 0;
-      atomicOr(&bits[k >> 5], 1u << (k & 31));
-    }
-    __syncthreads();
-    for (int64_t i = tid; i < n; i += threads) {
-      const int k = i == tid ? first : place(i);
-      if (k < 0) continue;
-      if (i < a.history_n) atomicAdd(&t.cells.count[k], 1u);
-      else atomicMax(&t.cells.bias[k], (uint32_t)(i - a.history_n) + 1u);
-    }
-    __syncthreads();
-    for (int w = tid; w < (span + 31) / 32; w += threads)
-      for (uint32_t b = bits[w]; b != 0; b &= b - 1) {
-        const int k = w * 32 + __ffs(b) - 1;
-        t.cells.count[k] = adjusted(k, t.cells.count[k], t.cells.bias[k]);
       }
+      barrier();
+      return span;
+    }
   }
-  __syncthreads();
+  span = min(kTouchSpan, u_hi - u_lo);
+  uint32_t *bits = t.cells.bits;
+  barrier();
+  if (tid == 0) {
+    t.u_lo = u_lo;
+    t.span = span;
+    t.dense = true;
+  }
+  for (int i = tid; i < (span + 31) / 32; i += threads) bits[i] = 0;
+  for (int i = tid; i < span; i += threads) {
+    t.cells.count[i] = 0;
+    t.cells.bias[i] = 0;
+  }
+  barrier();
+  window([&](int k, int64_t i) {
+    if (i < a.history_n) atomicAdd(&t.cells.count[k], 1u);
+    else atomicMax(&t.cells.bias[k], (uint32_t)(i - a.history_n) + 1u);
+    atomicOr(&bits[k >> 5], 1u << (k & 31));
+  });
+  barrier();
+  for (int w = tid; w < (span + 31) / 32; w += threads)
+    for (uint32_t b = bits[w]; b != 0; b &= b - 1) {
+      const int k = w * 32 + __ffs(b) - 1;
+      t.cells.count[k] = adjusted(k, t.cells.count[k], t.cells.bias[k]);
+    }
+  barrier();
+  return span;
+}
+
+// Mask bits of a warp's vectors, lane l's N tokens from v0 + l * N on: a few
+// lanes load the words, each word once, and the others get theirs by shuffles.
+// (v0 may be below 0 by part of a vector, whose bits mean nothing there.)
+template <int N>
+__device__ __forceinline__ uint32_t load_mask(const uint32_t *mask, int words, int v0, int lane) {
+  const int w = (v0 >> 5) + lane;
+  return lane <= N ? mask[min(max(w, 0), words - 1)] : 0u;
+}
+template <int N>
+__device__ __forceinline__ uint32_t lane_mask(uint32_t loaded, int v0, int lane) {
+  const int v = v0 + lane * N, from = (v >> 5) - (v0 >> 5);
+  const uint32_t a = __shfl_sync(0xffffffffu, loaded, from);
+  const uint32_t b = __shfl_sync(0xffffffffu, loaded, from + 1);
+  return __funnelshift_r(a, b, v & 31);
 }
 
 // -inf where the row's mask is 0.

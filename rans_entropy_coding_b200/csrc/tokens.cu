@@ -372,29 +372,28 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
 
   __shared__ RowAdjust a;
   bool touch = false, masked = false;
-  int span = 1 << 30;  // tokens per table
   if constexpr (ADJ) {
     if (tid == 0) a = row_adjust(adj, r, in.vocab);
     __syncthreads();
     touch = a.touches();
     masked = a.mask != nullptr;
-    if (touch) span = touch_span(a);
   }
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
   if (DECODE && ADJ && touch)  // added to after the first walk's barrier
     for (int i = tid; i < slice / kTile; i += threads) tile_sums[i] = make_uint2(0, 0);
-  int table_at = -1;
+  int table_at = -1, span = 1 << 30;  // where the table starts, its tokens
+  bool dense = false;
   auto need_table = [&](int u_lo) {
     if (!ADJ || !touch || table_at == u_lo) return;
-    fill_touch(table, a, row, u_lo, hi, tid, threads);
+    span = fill_touch(table, a, row, u_lo, hi, dense, tid, threads, [] { __syncthreads(); });
     table_at = u_lo;
   };
   // walks this block's tiles, body(tile's first u, its number), and the touched
   // tokens of its tables, which the tiles leave out: touched_body(u, logit)
   auto walk = [&](auto body, auto touched_body) {
-    for (int u_lo = lo; u_lo < hi; u_lo = span < hi - u_lo ? u_lo + span : hi) {
+    for (int u_lo = lo, u_hi; u_lo < hi; u_lo = u_hi) {
       need_table(u_lo);
-      const int u_hi = span < hi - u_lo ? u_lo + span : hi;
+      u_hi = span < hi - u_lo ? u_lo + span : hi;
       for (int u = u_lo + wid * kTile; u < u_hi; u += warps * kTile) body(u, (u - lo) / kTile);
       if (ADJ && touch) each_touched(table, tid, threads, touched_body);
     }
@@ -430,12 +429,16 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
       q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
     if constexpr (ADJ) {
       // the tokens that the mask leaves and nothing touches
+      if (masked) {
 #pragma unroll
-      for (int k = 0; k < kTileVecs; ++k) {
-        const int v0 = u + k * kVecRow + lane * N - row.shift, w = v0 >> 5;
-        ok[k] = ~0u;
-        if (masked)
-          ok[k] = __funnelshift_r(a.mask[w], a.mask[min(w + 1, a.mask_words - 1)], v0 & 31);
+        for (int k = 0; k < kTileVecs; ++k)
+          ok[k] = load_mask<N>(a.mask, a.mask_words, u + k * kVecRow - row.shift, lane);
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k)
+          ok[k] = lane_mask<N>(ok[k], u + k * kVecRow - row.shift, lane);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k) ok[k] = ~0u;
       }
       if (touch) {
 #pragma unroll
@@ -688,7 +691,8 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     const int tile = found_tile;
     if (tile < 0) return;
     const int u = lo + tile * kTile;
-    need_table(lo + (u - lo) / span * span);
+    // (tables start a whole number of spans after the block's first token)
+    need_table(lo + (u - lo) / (dense ? kTouchSpan : kHashSpan) * (dense ? kTouchSpan : kHashSpan));
     if (wid != 0) return;
     const uint32_t slot = (uint32_t)x & (kTokTotal - 1);
     const Sums all = found_all;
