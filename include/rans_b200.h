@@ -638,8 +638,10 @@ int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S, const ui
  *         strides agree, and overlaps it in no other way.
  * rans_distill_backward takes the same logits, ids, logprobs and
  * inv_temperature as the forward call that wrote `stats`.  rans_distill is both in one call,
- * for loops that know the rows' weights beforehand.  All are asynchronous, and
- * the results of a row depend on that row alone.
+ * for loops that know the rows' weights beforehand.  All are asynchronous.  A
+ * row may be shared by several blocks when there are few, so the same row in
+ * another batch gives the same results to rounding, not to the bit; the same
+ * call twice gives the same bits.
  */
 #define RANS_MAX_TOP 4096
 

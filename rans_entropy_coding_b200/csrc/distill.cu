@@ -1,18 +1,21 @@
 // distill.cu -- the coder's rate as a loss: distillation from a teacher's
 // listed probabilities and tail, forward and backward.
 //
-// Write m for a maximum in logits, c = inv_temperature * log2(e).  The listed
-// tokens are few: their terms are summed in double.  All others only enter
-// through their own sum, kept against their own maximum, so that a student's
-// small tail mass keeps its precision (1 - sum q would lose it):
-//   R = sum over others of 2^(c (z - m_rest)),
-//   Z = R 2^(c (m_rest - m)) + sum over listed of e^(inv_t (z_i - m)),
-//   q_t = R 2^(c (m_rest - m)) / Z.
-// The gradient of an unlisted token is then 2^(c (z - m_rest)) times one factor
-// per row, inv_t (P q_t - p_t) / R, with no difference of close numbers per
-// element.
+// Write c = inv_temperature * log2(e).  The listed tokens are few: their terms
+// are summed in double.  All others only enter through their own sum
+//   R = sum over others of 2^(c z - s),   s = c * (their largest logit), rounded,
+// so that a student's small tail mass keeps its precision (1 - sum q would lose
+// it).  With m the row's largest logit and Z = sum of e^(inv_t (z - m)) over all,
+// the gradient of an unlisted token is 2^(c z - s) times one factor per row,
+// inv_t (P q_t - p_t) / R: one multiply-add, one exponential and one product,
+// with no difference of close numbers per element.
+//
+// A row is walked twice, once for R and once for the gradient; the second walk
+// finds it in L2.  With many rows a block takes a row; with few, a cluster of
+// blocks shares it and exchanges its maxima and sums.
 #include <cmath>
 
+#include "cluster.cuh"
 #include "logits_common.cuh"
 #include "rans_common.cuh"
 #include "rans_internal.h"
@@ -20,9 +23,15 @@
 namespace rb {
 namespace {
 
-constexpr int kDisThreads = 512;
-constexpr int kDisWarps = kDisThreads / 32;
+constexpr int kStreamThreads = 512;  // walk the row
+constexpr int kStreamWarps = kStreamThreads / 32;
+constexpr int kListThreads = 128;    // take care of the listed tokens meanwhile
+constexpr int kListWarps = kListThreads / 32;
+constexpr int kDisThreads = kStreamThreads + kListThreads;
+constexpr int kDisVecs = 4;
+constexpr int kDisCluster = 8;
 constexpr double kLog2eD = 1.4426950408889634;
+constexpr double kLn2D = 0.6931471805599453;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -32,36 +41,15 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // Per-row figures from the forward pass to the backward one (8 floats).
 struct RowStats {
-  float m_rest;    // largest logit of an unlisted token (0 if there is none)
-  float rest;      // inv_t (P q_t - p_t) / R, the unlisted tokens' factor
-  float m_all;     // largest logit of the row
-  float inv_z;     // 1 / Z
-  float mass;      // P
-  float inv_p;     // 1 / sum p without a tail (0: no entry left), else 1
+  float offset;  // s
+  float rest;    // inv_t (P q_t - p_t) / R, the unlisted tokens' factor
+  float m_all;   // m
+  float inv_z;   // 1 / Z
+  float mass;    // P
+  float inv_p;   // 1 / sum p without a tail (0: no entry left), else 1
   float pad[2];
 };
 static_assert(sizeof(RowStats) == 32, "8 floats");
-
-// Bits of the listed tokens by u; shared memory.  Reports an id outside the
-// vocabulary or listed twice.  Every thread of the block calls it.
-__device__ __forceinline__ void list_bits(uint32_t *bits, int words, const int32_t *ids,
-                                          const float *lp, int K, int shift, int vocab,
-                                          int64_t r, int32_t *status) {
-  for (int i = threadIdx.x; i < words; i += kDisThreads) bits[i] = 0;
-  __syncthreads();
-  for (int i = threadIdx.x; i < K; i += kDisThreads) {
-    const int v = ids[i];
-    if (v == -1 || lp[i] == kNegInf) continue;
-    if (v < 0 || v >= vocab) {
-      if (status) report(status, RANS_ERR_INDEX, r);
-      continue;
-    }
-    const int u = v + shift;
-    const uint32_t old = atomicOr(&bits[u >> 5], 1u << (u & 31));
-    if (status && (old >> (u & 31) & 1)) report(status, RANS_ERR_INDEX, r);
-  }
-  __syncthreads();
-}
 
 __device__ __forceinline__ bool entry(const int32_t *ids, const float *lp, int i, int vocab,
                                       int &v, float &l) {
@@ -70,266 +58,406 @@ __device__ __forceinline__ bool entry(const int32_t *ids, const float *lp, int i
   return v >= 0 && v < vocab && l != kNegInf;
 }
 
-// Sum over the block in a fixed order; every thread gets it.
-template <typename X>
-__device__ __forceinline__ X block_sum(X x, X *red) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  X t = red[0];
-  for (int w = 1; w < kDisWarps; ++w) t += red[w];
-  return t;
-}
+// The threads that see to the listed tokens.
+struct Listed {
+  int tid;  // 0 .. kListThreads - 1
+  double *red;
 
-__device__ __forceinline__ float block_max(float x, float *red) {
+  __device__ __forceinline__ void barrier() const {
+    asm volatile("bar.sync 1, %0;" ::"n"(kListThreads) : "memory");
+  }
+  // Sum over them, in a fixed order; every one gets it.
+  __device__ __forceinline__ double sum(double x) const {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
-  __syncthreads();
-  float t = red[0];
-  for (int w = 1; w < kDisWarps; ++w) t = fmaxf(t, red[w]);
-  return t;
-}
+    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+    barrier();
+    if ((tid & 31) == 0) red[tid >> 5] = x;
+    barrier();
+    double t = red[0];
+#pragma unroll
+    for (int w = 1; w < kListWarps; ++w) t += red[w];
+    return t;
+  }
+  __device__ __forceinline__ double max(double x) const {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = fmax(x, __shfl_xor_sync(kFull, x, o));
+    barrier();
+    if ((tid & 31) == 0) red[tid >> 5] = x;
+    barrier();
+    double t = red[0];
+#pragma unroll
+    for (int w = 1; w < kListWarps; ++w) t = fmax(t, red[w]);
+    return t;
+  }
+};
 
-// The row's loss and figures from the unlisted tokens' maximum and sum.
-// Every thread calls it with the same m_rest and R.
+// What the listed tokens give: sums over the entries present.
+struct ListSums {
+  double m;      // largest of their logits (0 if none is finite)
+  bool some;     // one is
+  double z;      // e^(inv_t (z - m))
+  double p;      // p
+  double plp;    // p log p
+  double pz;     // p inv_t (z - m), where p > 0
+  double count;
+};
+
 template <typename T>
-__device__ __forceinline__ void row_figures(const Row<T> &row, const int32_t *ids,
-                                            const float *lp, int K, float inv_t, bool tail,
-                                            float m_rest, double R, double *red, float *redf,
-                                            float &loss, RowStats &st) {
+__device__ __forceinline__ ListSums list_sums(const Listed &g, const Row<T> &row,
+                                              const int32_t *ids, const float *lp, int K,
+                                              double it) {
   const T *z = row.at0 + row.shift;
-  float m = m_rest;
-  double sp = 0.0, count = 0.0;
-  for (int i = threadIdx.x; i < K; i += kDisThreads) {
+  ListSums s = {-HUGE_VAL, false, 0, 0, 0, 0, 0};
+  bool nan = false;
+  for (int i = g.tid; i < K; i += kListThreads) {
     int v;
     float l;
     if (!entry(ids, lp, i, row.vocab, v, l)) continue;
-    m = fmaxf(m, logit_float(z[v]));
-    sp += exp((double)l);
-    count += 1.0;
+    const float zi = logit_float(z[v]);
+    nan |= zi != zi;
+    s.m = fmax(s.m, (double)zi);
+    const double p = exp((double)l);
+    s.p += p;
+    s.plp += p > 0.0 || p != p ? p * (double)l : 0.0;
+    s.count += 1.0;
   }
-  m = block_max(m, redf);
-  sp = block_sum(sp, red);
-  count = block_sum(count, red);
-  if (m == kNegInf) m = 0.0f;
+  s.m = g.max(s.m);
+  s.some = s.m > -HUGE_VAL;
+  if (!s.some) s.m = 0.0;
+  for (int i = g.tid; i < K; i += kListThreads) {
+    int v;
+    float l;
+    if (!entry(ids, lp, i, row.vocab, v, l)) continue;
+    const double d = ((double)logit_float(z[v]) - s.m) * it, p = exp((double)l);
+    s.z += exp(d);
+    s.pz += p > 0.0 ? p * d : 0.0;
+  }
+  if (nan) s.z = NAN;
+  s.z = g.sum(s.z);
+  s.p = g.sum(s.p);
+  s.plp = g.sum(s.plp);
+  s.pz = g.sum(s.pz);
+  s.count = g.sum(s.count);
+  return s;
+}
+
+// The row's loss and figures.  R sums 2^(c z - offset) over the unlisted
+// tokens, whose largest logit is m_rest (-inf: none has a finite one).
+__device__ __forceinline__ void row_figures(const ListSums &s, double R, float m_rest,
+                                            float offset, float c, float inv_t, bool tail,
+                                            int vocab, float &loss, RowStats &st) {
   const double it = (double)inv_t;
-  double top = 0.0;
-  for (int i = threadIdx.x; i < K; i += kDisThreads) {
-    int v;
-    float l;
-    if (entry(ids, lp, i, row.vocab, v, l))
-      top += exp(((double)logit_float(z[v]) - (double)m) * it);
-  }
-  top = block_sum(top, red);
-  const bool some = R > 0.0 || R != R;  // an unlisted token with a finite logit
-  const double rest = some ? R * exp(((double)m_rest - (double)m) * it) : 0.0;
+  const bool some = R > 0.0 || R != R;
+  double m = fmax(s.some ? s.m : -HUGE_VAL, some ? (double)m_rest : -HUGE_VAL);
+  if (m == -HUGE_VAL) m = 0.0;
+  // R with its offset's rounding taken back, by the elements' own factor c
+  const double log_r =
+      some ? (log2(R) + ((double)offset - (double)c * (double)m_rest)) * kLn2D : -HUGE_VAL;
+  const double log_rest = log_r + ((double)(some ? m_rest : 0.0f) - m) * it;  // against m
+  const double rest = some ? exp(log_rest) : 0.0;
+  const double top = s.some || s.z != s.z ? s.z * exp((s.m - m) * it) : 0.0;
   const double Z = rest + top, lz = log(Z);
-  const bool no_tail = !tail || count >= (double)row.vocab;
-  const double norm = tail ? 1.0 : (sp > 0.0 ? 1.0 / sp : 0.0);
-  const double pt = no_tail ? 0.0 : fmax(0.0, 1.0 - sp);
-  const double mass = sp * norm + pt;
+  const double norm = tail ? 1.0 : (s.p > 0.0 ? 1.0 / s.p : 0.0);
+  const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
+  const double mass = s.p * norm + pt;
+  const bool ignored = !tail && !(s.p > 0.0) && s.p == s.p;
+  // sum p (log p - log q), p = norm * listed p
   double part = 0.0;
-  const double lognorm = tail || !(sp > 0.0) ? 0.0 : -log(sp);
-  for (int i = threadIdx.x; i < K; i += kDisThreads) {
-    int v;
-    float l;
-    if (!entry(ids, lp, i, row.vocab, v, l)) continue;
-    const double lpi = (double)l + lognorm;
-    const double lq = ((double)logit_float(z[v]) - (double)m) * it - lz;
-    const double p = exp(lpi);
-    if (p > 0.0 || p != p) part += p * (lpi - lq);
-  }
-  part = block_sum(part, red);
-  if (pt > 0.0) {
-    const double lqt = some ? ((double)m_rest - (double)m) * it + log(R) - lz : -HUGE_VAL;
-    part += pt * (log(pt) - lqt);
-  }
-  const bool ignored = !tail && !(sp > 0.0) && sp == sp;
+  if (s.p > 0.0 || s.p != s.p)
+    part = norm * (s.plp + s.p * (tail ? 0.0 : -log(s.p)) - s.pz - s.p * ((s.m - m) * it - lz));
+  if (pt > 0.0) part += pt * (log(pt) - (some ? log_rest - lz : -HUGE_VAL));
   loss = ignored ? (Z == Z ? 0.0f : (float)Z) : (float)part;
-  st.m_rest = some && m_rest > kNegInf ? m_rest : 0.0f;
+  st.offset = some ? offset : 0.0f;
   st.rest = some && !ignored ? (float)(it * (mass * (rest / Z) - pt) / R) : 0.0f;
   if (Z != Z) st.rest = (float)Z;
-  st.m_all = m;
+  st.m_all = (float)m;
   st.inv_z = (float)(1.0 / Z);
   st.mass = (float)mass;
   st.inv_p = (float)norm;
   st.pad[0] = st.pad[1] = 0.0f;
 }
 
-template <typename T>
-__device__ __forceinline__ void forward_row(const Row<T> &row, const uint32_t *bits,
-                                            const int32_t *ids, const float *lp, int K,
-                                            float inv_t, bool tail, double *red, float *redf,
-                                            float &loss, RowStats &st) {
+// A warp's part of R.
+struct Part {
+  float m, r;  // largest unlisted logit; sum of 2^(c z - c m)
+};
+
+// -inf in the places of a packed vector that `hit` names.
+__device__ __forceinline__ uint4 strike(uint4 q, uint32_t hit, float) {
+  uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (hit >> i & 1) w[i] = 0xff800000u;
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 strike16(uint4 q, uint32_t hit, uint32_t dead) {
+  uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t at = (hit >> (2 * i) & 1 ? 0xffffu : 0u) | (hit >> (2 * i + 1) & 1 ? 0xffff0000u : 0u);
+    w[i] = (w[i] & ~at) | (dead & at);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+__device__ __forceinline__ uint4 strike(uint4 q, uint32_t hit, __half) {
+  return strike16(q, hit, 0xfc00fc00u);
+}
+__device__ __forceinline__ uint4 strike(uint4 q, uint32_t hit, __nv_bfloat16) {
+  return strike16(q, hit, 0xff80ff80u);
+}
+
+enum { kForward = 1, kBackward = 2 };
+
+// One cluster per row.  WHAT: kForward writes losses and (without kBackward)
+// stats; kBackward the gradient, from stats where there is no forward pass.
+template <typename T, int WHAT>
+__global__ void __launch_bounds__(kDisThreads, 2)
+    distill_kernel(rans_logits in, const int32_t *ids, const float *lp, int K, float inv_t,
+                   int tail, float *losses, RowStats *stats, const float *grads, T *grad,
+                   int64_t grad_stride, int32_t *status, int slice) {
+  extern __shared__ uint32_t bits[];  // listed tokens of this block's slice
   constexpr int N = VecOf<T>::N;
+  constexpr int kVecRow = 32 * N, kTile = kVecRow * kDisVecs;
+  __shared__ double red[kListWarps];
+  __shared__ Part parts[kDisCluster * kStreamWarps];
+  __shared__ RowStats figures;
+  __shared__ float top_z[(WHAT & kBackward) ? RANS_MAX_TOP : 1];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const uint32_t rank = cluster_rank(), peers = cluster_size();
+  const int64_t r = blockIdx.x / peers;
+  const Row<T> row(in.data, r, in.row_stride, in.vocab);
+  const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
+  const bool lists = tid >= kStreamThreads;
+  const Listed group = {tid - kStreamThreads, red};
   const float c = (float)((double)inv_t * kLog2eD);
-  float m = kNegInf, s = 0.0f;
-  for (int u0 = threadIdx.x * N; u0 < row.end(); u0 += kDisThreads * N) {
-    float z[N];
-    row.load(u0, z, kNegInf);
-    const uint32_t hit = bits[u0 >> 5] >> (u0 & 31) & ((1u << N) - 1u);
-    float vm = kNegInf;
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (hit >> i & 1) z[i] = kNegInf;
-      vm = fmaxf(vm, z[i]);
-    }
-    if (vm > m) {
-      s *= exp2_fast((m - vm) * c);
-      m = vm;
-    }
-    const float mz = m == kNegInf ? 0.0f : m;
-#pragma unroll
-    for (int i = 0; i < N; ++i) s += exp2_fast((z[i] - mz) * c);
-  }
-  const float m_rest = block_max(m, redf);
-  const double R =
-      block_sum(m == kNegInf ? (double)s : (double)s * (double)exp2_fast((m - m_rest) * c), red);
-  row_figures(row, ids, lp, K, inv_t, tail, m_rest, R, red, redf, loss, st);
-}
-
-// The gradient of a row, given its figures.
-template <typename T>
-__device__ __forceinline__ void backward_row(const Row<T> &row, const uint32_t *bits,
-                                             const int32_t *ids, const float *lp, int K,
-                                             float inv_t, const RowStats &st, float g, T *o,
-                                             float *top_z) {
-  constexpr int N = VecOf<T>::N;
-  const float c = (float)((double)inv_t * kLog2eD);
-  // grad may be the logits' own memory: the listed ones are read first
-  for (int i = threadIdx.x; i < K; i += kDisThreads) {
-    int v;
-    float l;
-    if (entry(ids, lp, i, row.vocab, v, l)) top_z[i] = logit_float(row.at0[row.shift + v]);
-  }
-  __syncthreads();
-  const float factor = st.rest * g;
-  for (int u0 = threadIdx.x * N; u0 < row.end(); u0 += kDisThreads * N) {
-    float z[N];
-    row.load(u0, z, kNegInf);
-    const uint32_t hit = bits[u0 >> 5] >> (u0 & 31) & ((1u << N) - 1u);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const int u = u0 + i;
-      if (u >= row.shift && u < row.end() && !(hit >> i & 1))
-        o[u - row.shift] = float_logit<T>(exp2_fast((z[i] - st.m_rest) * c) * factor);
-    }
-  }
-  for (int i = threadIdx.x; i < K; i += kDisThreads) {
-    int v;
-    float l;
-    if (!entry(ids, lp, i, row.vocab, v, l)) continue;
-    const float q = expf((top_z[i] - st.m_all) * inv_t) * st.inv_z;
-    const float p = expf(l) * st.inv_p;
-    o[v] = float_logit<T>((st.mass * q - p) * inv_t * g);
-  }
-}
-
-template <typename T>
-__global__ void __launch_bounds__(kDisThreads)
-    distill_forward_kernel(rans_logits in, const int32_t *ids, const float *lp, int K,
-                           float inv_t, int tail, float *losses, RowStats *stats,
-                           int32_t *status) {
-  extern __shared__ uint32_t bits[];
-  __shared__ double red[kDisWarps];
-  __shared__ float redf[kDisWarps];
-  const int64_t r = blockIdx.x;
-  const Row<T> row(in.data, r, in.row_stride, in.vocab);
   ids += r * K;
   lp += r * K;
-  const int words = (in.vocab + VecOf<T>::N + 31) / 32;
-  list_bits(bits, words, ids, lp, K, row.shift, in.vocab, r, status);
-  float loss;
-  RowStats st;
-  forward_row(row, bits, ids, lp, K, inv_t, tail != 0, red, redf, loss, st);
-  if (threadIdx.x == 0) {
-    losses[r] = loss;
-    stats[r] = st;
+  if ((WHAT & kForward) && peers > 1) {  // waited for before the others' memory is written
+    __syncwarp();
+    cluster_arrive();
+  }
+
+  if constexpr ((WHAT & kForward) != 0) {
+    const int words = hi > lo ? (hi - lo + 31) / 32 + 1 : 0;
+    for (int i = tid; i < words; i += kDisThreads) bits[i] = 0;
+    __syncthreads();
+    if (lists) {
+      for (int i = group.tid; i < K; i += kListThreads) {
+        const int v = ids[i];
+        if (v == -1 || lp[i] == kNegInf) continue;
+        if (v < 0 || v >= in.vocab) {
+          if (rank == 0) report(status, RANS_ERR_INDEX, r);
+          continue;
+        }
+        const int k = v + row.shift - lo;
+        if (k < 0 || k >= hi - lo) continue;
+        if (atomicOr(&bits[k >> 5], 1u << (k & 31)) >> (k & 31) & 1)
+          report(status, RANS_ERR_INDEX, r);  // listed twice
+      }
+    }
+    __syncthreads();
+    ListSums sums = {};
+    if (lists) {
+      sums = list_sums(group, row, ids, lp, K, (double)inv_t);
+    } else {
+      // R, against each lane's running maximum
+      float m = kNegInf, off = 0.0f, s = 0.0f;
+      for (int u = lo + wid * kTile; u < hi; u += kStreamWarps * kTile) {
+        uint4 q[kDisVecs];
+#pragma unroll
+        for (int k = 0; k < kDisVecs; ++k) {
+          const int u0 = u + k * kVecRow + lane * N;
+          if (row.whole(u0)) {
+            q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+          } else {
+            float z[N];
+            row.load(u0, z, kNegInf);
+            q[k] = pack16(z, T());
+          }
+        }
+        float top = m;
+#pragma unroll
+        for (int k = 0; k < kDisVecs; ++k) {
+          const int at = u + k * kVecRow + lane * N - lo;
+          const uint32_t hit = at < hi - lo ? bits[at >> 5] >> (at & 31) & ((1u << N) - 1u) : 0u;
+          if (hit) q[k] = strike(q[k], hit, T());
+          float z[N];
+          unpack16(q[k], z, T());
+#pragma unroll
+          for (int i = 0; i < N; ++i) top = fmaxf(top, z[i]);
+        }
+        if (top > m) {
+          const float to = __fmul_rn(top, c);
+          if (m != kNegInf) s *= exp2_fast(off - to);
+          off = to;
+          m = top;
+        }
+#pragma unroll
+        for (int k = 0; k < kDisVecs; ++k) {
+          float z[N];
+          unpack16(q[k], z, T());
+#pragma unroll
+          for (int i = 0; i < N; ++i) s += exp2_fast(fmaf(z[i], c, -off));
+        }
+      }
+      float w = m;
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(kFull, w, o));
+      if (m != kNegInf) s *= exp2_fast(off - __fmul_rn(w, c));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
+      if (peers > 1) cluster_wait();
+      if (lane < (int)peers) {
+        const uint32_t at = peer_address(&parts[rank * kStreamWarps + wid], lane);
+        peer_store(at, __float_as_uint(w));
+        peer_store(at + 4, __float_as_uint(s));
+      }
+    }
+    if (peers > 1) {
+      if (lists) cluster_wait();
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+    if (wid == kStreamWarps) {
+      // the first of the listing warps joins the parts, in a fixed order
+      float m_rest = kNegInf;
+      for (int i = lane; i < (int)peers * kStreamWarps; i += 32)
+        m_rest = fmaxf(m_rest, parts[i].m);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m_rest = fmaxf(m_rest, __shfl_xor_sync(kFull, m_rest, o));
+      const float offset = m_rest == kNegInf ? 0.0f : __fmul_rn(m_rest, c);
+      double R = 0.0;
+      for (int i = lane; i < (int)peers * kStreamWarps; i += 32) {
+        const Part p = parts[i];
+        // each part against its own rounded product
+        R += p.m == kNegInf ? (double)p.r : (double)p.r * (double)exp2_fast(__fmul_rn(p.m, c) - offset);
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) R += __shfl_xor_sync(kFull, R, o);
+      if (lane == 0) {
+        float loss;
+        RowStats st;
+        row_figures(sums, R, m_rest, offset, c, inv_t, tail != 0, in.vocab, loss, st);
+        figures = st;
+        if (rank == 0) {
+          losses[r] = loss;
+          if constexpr (WHAT == kForward) stats[r] = st;
+        }
+      }
+    }
+    if constexpr (WHAT == kForward) return;
+  } else {
+    if (tid == 0) figures = stats[r];
+  }
+
+  if constexpr ((WHAT & kBackward) != 0) {
+    // grad may be the logits' own memory: this block's listed ones are read
+    // before anything is written
+    if (lists)
+      for (int i = group.tid; i < K; i += kListThreads) {
+        int v;
+        float l;
+        if (entry(ids, lp, i, in.vocab, v, l) && v + row.shift >= lo && v + row.shift < hi)
+          top_z[i] = logit_float(row.at0[row.shift + v]);
+      }
+    __syncthreads();
+    // (another block's sums over the listed tokens are behind the barrier too)
+    const RowStats st = figures;
+    const float g = grads[r];
+    T *o = grad + r * grad_stride - row.shift;
+    if (!lists) {
+      const float factor = st.rest * g;
+      for (int u = lo + wid * kTile; u < hi; u += kStreamWarps * kTile) {
+        uint4 q[kDisVecs];
+#pragma unroll
+        for (int k = 0; k < kDisVecs; ++k) {
+          const int u0 = u + k * kVecRow + lane * N;
+          if (row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+        }
+#pragma unroll
+        for (int k = 0; k < kDisVecs; ++k) {
+          const int u0 = u + k * kVecRow + lane * N;
+          if (u0 - lane * N >= hi) break;  // (a whole warp's)
+          const bool whole = row.whole(u0);
+          float z[N];
+          if (whole) unpack16(q[k], z, T());
+          else row.load(u0, z, kNegInf);
+#pragma unroll
+          for (int i = 0; i < N; ++i) z[i] = exp2_fast(fmaf(z[i], c, -st.offset)) * factor;
+          store_vectors(o, u0, pack16(z, T()), whole, row.shift, row.end());
+        }
+      }
+    }
+    __syncthreads();  // the listed tokens' gradients go over what stands there
+    if (lists)
+      for (int i = group.tid; i < K; i += kListThreads) {
+        int v;
+        float l;
+        if (!entry(ids, lp, i, in.vocab, v, l) || v + row.shift < lo || v + row.shift >= hi)
+          continue;
+        const float q = expf((top_z[i] - st.m_all) * inv_t) * st.inv_z;
+        const float p = expf(l) * st.inv_p;
+        o[row.shift + v] = float_logit<T>((st.mass * q - p) * inv_t * g);
+      }
   }
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kDisThreads)
-    distill_backward_kernel(rans_logits in, const int32_t *ids, const float *lp, int K,
-                            float inv_t, const RowStats *stats, const float *grads, T *grad,
-                            int64_t grad_stride) {
-  extern __shared__ uint32_t bits[];
-  __shared__ float top_z[RANS_MAX_TOP];
-  const int64_t r = blockIdx.x;
-  const Row<T> row(in.data, r, in.row_stride, in.vocab);
-  ids += r * K;
-  lp += r * K;
-  const int words = (in.vocab + VecOf<T>::N + 31) / 32;
-  list_bits(bits, words, ids, lp, K, row.shift, in.vocab, r, nullptr);
-  backward_row(row, bits, ids, lp, K, inv_t, stats[r], grads[r], grad + r * grad_stride, top_z);
+template <typename T, int WHAT>
+int launch_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, float inv_t,
+             int tail, float *losses, float *stats, const float *grads, void *grad,
+             int64_t stride, int32_t *status, cudaStream_t st) {
+  auto kern = distill_kernel<T, WHAT>;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
+  constexpr int kTile = 32 * VecOf<T>::N * kDisVecs;
+  const int tiles = (in.vocab + VecOf<T>::N - 1 + kTile - 1) / kTile;
+  // blocks per row: one, while the rows alone fill the SMs (two blocks each);
+  // else as many as still leave every warp a tile
+  int peers = 1;
+  while (peers < kDisCluster && in.rows * peers * 2 <= 2 * num_sms(dev) &&
+         tiles >= peers * 2 * kStreamWarps)
+    peers *= 2;
+  const int slice = (tiles + peers - 1) / peers * kTile;
+  const uint32_t smem = (WHAT & kForward) ? 4u * (uint32_t)(slice / 32 + 1) : 0u;
+  if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
+  if (in.rows > 0x7fffffff / peers) return RANS_ERR_ARG;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(in.rows * peers));
+  cfg.blockDim = dim3(kDisThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)peers;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, in, ids, lp, K, inv_t, tail, losses,
+                            reinterpret_cast<RowStats *>(stats), grads, static_cast<T *>(grad),
+                            stride, status, slice) == cudaSuccess
+             ? RANS_OK
+             : RANS_ERR_CUDA;
 }
 
-// Both in one launch: the row is read again for the gradient (from L2).
-template <typename T>
-__global__ void __launch_bounds__(kDisThreads)
-    distill_both_kernel(rans_logits in, const int32_t *ids, const float *lp, int K, float inv_t,
-                        int tail, const float *grads, float *losses, T *grad,
-                        int64_t grad_stride, int32_t *status) {
-  extern __shared__ uint32_t bits[];
-  __shared__ double red[kDisWarps];
-  __shared__ float redf[kDisWarps];
-  __shared__ float top_z[RANS_MAX_TOP];
-  const int64_t r = blockIdx.x;
-  const Row<T> row(in.data, r, in.row_stride, in.vocab);
-  ids += r * K;
-  lp += r * K;
-  const int words = (in.vocab + VecOf<T>::N + 31) / 32;
-  list_bits(bits, words, ids, lp, K, row.shift, in.vocab, r, status);
-  float loss;
-  RowStats st;
-  forward_row(row, bits, ids, lp, K, inv_t, tail != 0, red, redf, loss, st);
-  if (threadIdx.x == 0) losses[r] = loss;
-  backward_row(row, bits, ids, lp, K, inv_t, st, grads[r], grad + r * grad_stride, top_z);
-}
-
-template <typename T>
-uint32_t bits_bytes(int vocab) {
-  return 4u * (uint32_t)((vocab + VecOf<T>::N + 31) / 32);
-}
-
-template <typename T>
-int forward_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, float inv_t,
-              int tail, float *losses, float *stats, int32_t *status, cudaStream_t st) {
-  auto kern = distill_forward_kernel<T>;
-  const uint32_t smem = bits_bytes<T>(in.vocab);
-  if (ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
-  kern<<<(unsigned)in.rows, kDisThreads, smem, st>>>(in, ids, lp, K, inv_t, tail, losses,
-                                                     reinterpret_cast<RowStats *>(stats), status);
-  return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
-}
-
-template <typename T>
-int backward_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, float inv_t,
-               const float *stats, const float *grads, void *grad, int64_t stride,
-               cudaStream_t st) {
-  auto kern = distill_backward_kernel<T>;
-  const uint32_t smem = bits_bytes<T>(in.vocab);
-  if (ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
-  kern<<<(unsigned)in.rows, kDisThreads, smem, st>>>(
-      in, ids, lp, K, inv_t, reinterpret_cast<const RowStats *>(stats), grads,
-      static_cast<T *>(grad), stride);
-  return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
-}
-
-template <typename T>
-int both_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, float inv_t,
-           int tail, const float *grads, float *losses, void *grad, int64_t stride,
+template <int WHAT>
+int launch(const rans_logits &in, const int32_t *ids, const float *lp, int K, float inv_t,
+           int tail, float *losses, float *stats, const float *grads, void *grad, int64_t stride,
            int32_t *status, cudaStream_t st) {
-  auto kern = distill_both_kernel<T>;
-  const uint32_t smem = bits_bytes<T>(in.vocab);
-  if (ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
-  kern<<<(unsigned)in.rows, kDisThreads, smem, st>>>(in, ids, lp, K, inv_t, tail, grads, losses,
-                                                     static_cast<T *>(grad), stride, status);
-  return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
+  switch (in.dtype) {
+    case RANS_LOGITS_F32:
+      return launch_t<float, WHAT>(in, ids, lp, K, inv_t, tail, losses, stats, grads, grad,
+                                   stride, status, st);
+    case RANS_LOGITS_F16:
+      return launch_t<__half, WHAT>(in, ids, lp, K, inv_t, tail, losses, stats, grads, grad,
+                                    stride, status, st);
+    default:
+      return launch_t<__nv_bfloat16, WHAT>(in, ids, lp, K, inv_t, tail, losses, stats, grads,
+                                           grad, stride, status, st);
+  }
 }
 
 }  // namespace
@@ -337,44 +465,22 @@ int both_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, fl
 int launch_distill_forward(const rans_logits &in, const int32_t *ids, const float *lp, int K,
                            float inv_t, int tail, float *losses, float *stats, int32_t *status,
                            cudaStream_t st) {
-  if (in.rows > 0x7fffffff) return RANS_ERR_ARG;
-  switch (in.dtype) {
-    case RANS_LOGITS_F32:
-      return forward_t<float>(in, ids, lp, K, inv_t, tail, losses, stats, status, st);
-    case RANS_LOGITS_F16:
-      return forward_t<__half>(in, ids, lp, K, inv_t, tail, losses, stats, status, st);
-    default:
-      return forward_t<__nv_bfloat16>(in, ids, lp, K, inv_t, tail, losses, stats, status, st);
-  }
+  return launch<kForward>(in, ids, lp, K, inv_t, tail, losses, stats, nullptr, nullptr, 0,
+                          status, st);
 }
 
 int launch_distill_backward(const rans_logits &in, const int32_t *ids, const float *lp, int K,
                             float inv_t, const float *stats, const float *grads, void *grad,
                             int64_t stride, cudaStream_t st) {
-  if (in.rows > 0x7fffffff) return RANS_ERR_ARG;
-  switch (in.dtype) {
-    case RANS_LOGITS_F32:
-      return backward_t<float>(in, ids, lp, K, inv_t, stats, grads, grad, stride, st);
-    case RANS_LOGITS_F16:
-      return backward_t<__half>(in, ids, lp, K, inv_t, stats, grads, grad, stride, st);
-    default:
-      return backward_t<__nv_bfloat16>(in, ids, lp, K, inv_t, stats, grads, grad, stride, st);
-  }
+  return launch<kBackward>(in, ids, lp, K, inv_t, 0, nullptr, const_cast<float *>(stats), grads,
+                           grad, stride, nullptr, st);
 }
 
 int launch_distill(const rans_logits &in, const int32_t *ids, const float *lp, int K,
                    float inv_t, int tail, const float *grads, float *losses, void *grad,
                    int64_t stride, int32_t *status, cudaStream_t st) {
-  if (in.rows > 0x7fffffff) return RANS_ERR_ARG;
-  switch (in.dtype) {
-    case RANS_LOGITS_F32:
-      return both_t<float>(in, ids, lp, K, inv_t, tail, grads, losses, grad, stride, status, st);
-    case RANS_LOGITS_F16:
-      return both_t<__half>(in, ids, lp, K, inv_t, tail, grads, losses, grad, stride, status, st);
-    default:
-      return both_t<__nv_bfloat16>(in, ids, lp, K, inv_t, tail, grads, losses, grad, stride,
-                                   status, st);
-  }
+  return launch<kForward | kBackward>(in, ids, lp, K, inv_t, tail, losses, nullptr, grads, grad,
+                                      stride, status, st);
 }
 
 }  // namespace rb

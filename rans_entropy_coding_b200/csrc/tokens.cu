@@ -9,6 +9,7 @@
 // additions can change an interval.
 #include <type_traits>
 
+#include "cluster.cuh"
 #include "logits_common.cuh"
 #include "rans_common.cuh"
 #include "rans_internal.h"
@@ -248,38 +249,6 @@ struct Coded {
   uint64_t *states_out;
   int32_t *tokens;
 };
-
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-// The address of a block's shared variable in block `rank` of the cluster.
-__device__ __forceinline__ uint32_t peer_address(const void *p, uint32_t rank) {
-  uint32_t a;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;"
-      : "=r"(a)
-      : "r"((uint32_t)__cvta_generic_to_shared(p)), "r"(rank));
-  return a;
-}
-__device__ __forceinline__ void peer_store(uint32_t a, uint32_t x) {
-  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
-}
-
-__device__ __forceinline__ void peer_store(uint32_t a, uint64_t x) {
-  asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(a), "l"(x) : "memory");
-}
 
 // The streams' side of a decoding row: a token whose interval is [s, s + f).
 __device__ __forceinline__ void take_token(const Coded &cd, int64_t r, int64_t stream, uint64_t x,

@@ -569,6 +569,36 @@ def test_distill(v, pad, dtype, tail):
         status_ok(st)
 
 
+@pytest.mark.parametrize("shift", [-20000.0, 20000.0])
+def test_distill_and_intervals_far_from_zero(shift):
+    """Only differences of logits count, wherever they lie."""
+    n, v = 3, 5000
+    x = make_logits(n, v, F32, seed=16) + shift
+    x[1, 2500:] -= 30000.0                 # a row whose ends lie far apart
+    x[2, :2500] -= 30000.0
+    ids, lp = teacher(n, v, 30, 7, True)
+    g = np.array([1.0, -0.5, 2.0], np.float32)
+    ti, tl, tg = (torch.from_numpy(a).cuda() for a in (ids, lp, g))
+    # a logit's own place is 2^-10 apart here, and c z - s is one rounding of
+    # terms of 2^15: at most 2^-9 off in the exponent, which goes into both R and
+    # the gradient; the rest is as near zero
+    losses, grad = rb.distill_loss_and_grad(x, ti, tl, tg)
+    rows = numpy_rows(x)
+    for r in range(n):
+        want, dz, parts = TO.distill(rows[r], ids[r], lp[r], 1.0, True)
+        assert math.isfinite(want)
+        assert abs(float(losses[r]) - want) <= 2.0 ** -7 + 1e-5 * abs(want)
+        off = np.abs(grad[r].double().cpu().numpy() - dz * g[r])
+        assert (off <= abs(g[r]) * parts * 2.0 ** -6 + 2.0 ** -126).all()
+    b = [TO.bounds(row, {}, 0) for row in rows]
+    tok = np.array([int(np.argmax(np.diff(q))) for q in b], np.int32)
+    st = rb.new_status()
+    s, f = rb.token_intervals(x, torch.from_numpy(tok).cuda(), status=st)
+    assert s.tolist() == [q[t] for q, t in zip(b, tok)]
+    assert f.tolist() == [q[t + 1] - q[t] for q, t in zip(b, tok)]
+    status_ok(st)
+
+
 def test_distill_in_place_and_into_a_wider_buffer():
     n, v = 5, 3001
     x = make_logits(n, v, BF16, 2, seed=8)
