@@ -39,6 +39,37 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ float2 unpair(uint64_t x) {
+  float2 f;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+  return f;
+}
+// 2^(c z - off) of two logits; c2 and off2 hold c and -off twice.
+__device__ __forceinline__ float2 exp2_pair(float a, float b, uint64_t c2, uint64_t off2) {
+  uint64_t x;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(pair(a, b)), "l"(c2), "l"(off2));
+  const float2 f = unpair(x);
+  return make_float2(exp2_fast(f.x), exp2_fast(f.y));
+}
+
+// The largest value of a packed vector (a NaN if there is one).
+__device__ __forceinline__ float vector_max(const uint4 &q, float) {
+  return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
+                 max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+}
+template <typename T>
+__device__ __forceinline__ float vector_max(const uint4 &q, T) {
+  const uint32_t m = pair_max(pair_max(q.x, q.y, T()), pair_max(q.z, q.w, T()), T());
+  float z[8];
+  unpack16(make_uint4(m, 0, 0, 0), z, T());
+  return max_nan(z[0], z[1]);
+}
+
 // Per-row figures from the forward pass to the backward one (8 floats).
 struct RowStats {
   float offset;  // s
@@ -238,8 +269,7 @@ __global__ void __launch_bounds__(kDisThreads, 2)
   }
 
   if constexpr ((WHAT & kForward) != 0) {
-    const int words = hi > lo ? (hi - lo + 31) / 32 + 1 : 0;
-    for (int i = tid; i < words; i += kDisThreads) bits[i] = 0;
+    for (int i = tid; i < slice / 32; i += kDisThreads) bits[i] = 0;
     __syncthreads();
     if (lists) {
       for (int i = group.tid; i < K; i += kListThreads) {
@@ -261,48 +291,64 @@ __global__ void __launch_bounds__(kDisThreads, 2)
       sums = list_sums(group, row, ids, lp, K, (double)inv_t);
     } else {
       // R, against each lane's running maximum
-      float m = kNegInf, off = 0.0f, s = 0.0f;
+      float m = kNegInf, off = 0.0f;
+      uint64_t s2 = 0;  // two sums
+      const uint64_t c2 = pair(c, c);
       for (int u = lo + wid * kTile; u < hi; u += kStreamWarps * kTile) {
         uint4 q[kDisVecs];
+        uint32_t word[kDisVecs];
+        const bool inside = u >= row.shift && u + kTile <= row.end();
+        if (inside) {
 #pragma unroll
-        for (int k = 0; k < kDisVecs; ++k) {
-          const int u0 = u + k * kVecRow + lane * N;
-          if (row.whole(u0)) {
-            q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
-          } else {
+          for (int k = 0; k < kDisVecs; ++k)
+            q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kDisVecs; ++k) {
             float z[N];
-            row.load(u0, z, kNegInf);
+            row.load(u + k * kVecRow + lane * N, z, kNegInf);
             q[k] = pack16(z, T());
           }
         }
-        float top = m;
+        // (a tile's bits lie inside the slice's, which is a whole number of tiles)
+#pragma unroll
+        for (int k = 0; k < kDisVecs; ++k)
+          word[k] = bits[(u - lo + k * kVecRow + lane * N) >> 5];
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
-          const int at = u + k * kVecRow + lane * N - lo;
-          const uint32_t hit = at < hi - lo ? bits[at >> 5] >> (at & 31) & ((1u << N) - 1u) : 0u;
+          const uint32_t hit = word[k] >> (lane * N & 31) & ((1u << N) - 1u);
           if (hit) q[k] = strike(q[k], hit, T());
-          float z[N];
-          unpack16(q[k], z, T());
-#pragma unroll
-          for (int i = 0; i < N; ++i) top = fmaxf(top, z[i]);
         }
-        if (top > m) {
+        float top = vector_max(q[0], T());
+#pragma unroll
+        for (int k = 1; k < kDisVecs; ++k) top = max_nan(top, vector_max(q[k], T()));
+        if (!(top <= m)) {
+          // (a NaN stays one, and makes all that follows NaN)
           const float to = __fmul_rn(top, c);
-          if (m != kNegInf) s *= exp2_fast(off - to);
+          if (m != kNegInf) {
+            const float f = exp2_fast(off - to);
+            const float2 s = unpair(s2);
+            s2 = pair(s.x * f, s.y * f);
+          }
           off = to;
           m = top;
         }
+        const uint64_t off2 = pair(m == kNegInf ? 0.0f : -off, m == kNegInf ? 0.0f : -off);
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
           float z[N];
           unpack16(q[k], z, T());
 #pragma unroll
-          for (int i = 0; i < N; ++i) s += exp2_fast(fmaf(z[i], c, -off));
+          for (int i = 0; i < N; i += 2) {
+            const float2 e = exp2_pair(z[i], z[i + 1], c2, off2);
+            asm("add.rn.f32x2 %0, %1, %2;" : "=l"(s2) : "l"(s2), "l"(pair(e.x, e.y)));
+          }
         }
       }
+      float s = unpair(s2).x + unpair(s2).y;
       float w = m;
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) w = fmaxf(w, __shfl_xor_sync(kFull, w, o));
+      for (int o = 16; o > 0; o >>= 1) w = max_nan(w, __shfl_xor_sync(kFull, w, o));
       if (m != kNegInf) s *= exp2_fast(off - __fmul_rn(w, c));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
@@ -325,9 +371,10 @@ __global__ void __launch_bounds__(kDisThreads, 2)
       // the first of the listing warps joins the parts, in a fixed order
       float m_rest = kNegInf;
       for (int i = lane; i < (int)peers * kStreamWarps; i += 32)
-        m_rest = fmaxf(m_rest, parts[i].m);
+        m_rest = max_nan(m_rest, parts[i].m);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m_rest = fmaxf(m_rest, __shfl_xor_sync(kFull, m_rest, o));
+      for (int o = 16; o > 0; o >>= 1)
+        m_rest = max_nan(m_rest, __shfl_xor_sync(kFull, m_rest, o));
       const float offset = m_rest == kNegInf ? 0.0f : __fmul_rn(m_rest, c);
       double R = 0.0;
       for (int i = lane; i < (int)peers * kStreamWarps; i += 32) {
@@ -370,24 +417,39 @@ __global__ void __launch_bounds__(kDisThreads, 2)
     T *o = grad + r * grad_stride - row.shift;
     if (!lists) {
       const float factor = st.rest * g;
-      for (int u = lo + wid * kTile; u < hi; u += kStreamWarps * kTile) {
+      const uint64_t c2 = pair(c, c), off2 = pair(-st.offset, -st.offset);
+      const uint64_t factor2 = pair(factor, factor);
+      const bool aligned = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
+      // backwards: what the first walk read last is nearest
+      const int tiles = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
+      for (int t = tiles - 1 - wid; t >= 0; t -= kStreamWarps) {
+        const int u = lo + t * kTile;
+        const bool inside = u >= row.shift && u + kTile <= row.end();
         uint4 q[kDisVecs];
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
           const int u0 = u + k * kVecRow + lane * N;
-          if (row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+          if (inside || row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
         }
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
           const int u0 = u + k * kVecRow + lane * N;
-          if (u0 - lane * N >= hi) break;  // (a whole warp's)
-          const bool whole = row.whole(u0);
+          const bool whole = inside || row.whole(u0);
           float z[N];
           if (whole) unpack16(q[k], z, T());
           else row.load(u0, z, kNegInf);
 #pragma unroll
-          for (int i = 0; i < N; ++i) z[i] = exp2_fast(fmaf(z[i], c, -st.offset)) * factor;
-          store_vectors(o, u0, pack16(z, T()), whole, row.shift, row.end());
+          for (int i = 0; i < N; i += 2) {
+            const float2 e = exp2_pair(z[i], z[i + 1], c2, off2);
+            uint64_t x;
+            asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(pair(e.x, e.y)), "l"(factor2));
+            const float2 f = unpair(x);
+            z[i] = f.x;
+            z[i + 1] = f.y;
+          }
+          const uint4 p = pack16(z, T());
+          if (inside && aligned) *reinterpret_cast<uint4 *>(o + u0) = p;
+          else if (u0 - lane * N < hi) store_vectors(o, u0, p, whole, row.shift, row.end());
         }
       }
     }
@@ -421,7 +483,7 @@ int launch_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, 
          tiles >= peers * 2 * kStreamWarps)
     peers *= 2;
   const int slice = (tiles + peers - 1) / peers * kTile;
-  const uint32_t smem = (WHAT & kForward) ? 4u * (uint32_t)(slice / 32 + 1) : 0u;
+  const uint32_t smem = (WHAT & kForward) ? (uint32_t)slice / 8u : 0u;
   if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
   if (in.rows > 0x7fffffff / peers) return RANS_ERR_ARG;
   cudaLaunchConfig_t cfg = {};

@@ -87,6 +87,35 @@ __device__ __forceinline__ uint4 pack16(const float (&z)[8], __nv_bfloat16) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// max that keeps a NaN, so that one test per row finds it.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float c;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
+  return c;
+}
+
+// The larger (NaN if either is) and the smaller of packed pairs.
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __half) {
+  uint32_t c;
+  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __half) {
+  uint32_t c;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t c;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t c;
+  asm("min.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
 // One row as the kernels walk it.
 template <typename T>
 struct Row {

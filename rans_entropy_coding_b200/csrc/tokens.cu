@@ -46,13 +46,6 @@ __device__ __forceinline__ uint32_t token_weight(float z, float scale, float yma
   return __float_as_uint(__fadd_rn(q, kUnit)) - __float_as_uint(kUnit);
 }
 
-// max that keeps a NaN, so that one test per row finds it.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float c;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(c) : "f"(a), "f"(b));
-  return c;
-}
-
 // The factor and the reference of a row's weights from its largest adjusted
 // logit.  A row whose alive tokens all overflow to -inf weighs them the same:
 // with factor 0 they get d = 0, and dead ones (-inf * 0) NaN, hence -64.
@@ -140,28 +133,6 @@ __device__ __forceinline__ float warp_max_nan(float x) {
   float y;
   asm("redux.sync.max.NaN.f32 %0, %1, 0xffffffff;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// The larger (NaN if either is) and the smaller of packed pairs.
-__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __half) {
-  uint32_t c;
-  asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-  return c;
-}
-__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __half) {
-  uint32_t c;
-  asm("min.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-  return c;
-}
-__device__ __forceinline__ uint32_t pair_max(uint32_t a, uint32_t b, __nv_bfloat16) {
-  uint32_t c;
-  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-  return c;
-}
-__device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __nv_bfloat16) {
-  uint32_t c;
-  asm("min.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
-  return c;
 }
 
 // Running extremes of raw vectors, in the type they come in.
@@ -275,7 +246,7 @@ __device__ __forceinline__ void take_token(const Coded &cd, int64_t r, int64_t s
 
 // One cluster per row.  ADJ: with penalties, biases or a mask.
 template <typename T, bool DECODE, bool ADJ>
-__global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
+__global__ void __launch_bounds__(kRowThreads, 2)
     token_rows_kernel(rans_logits in, rans_adjust adj, const int32_t *tokens, uint32_t *starts,
                       uint32_t *freqs, Coded cd, int32_t *status, int slice, uint64_t zero2) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -392,7 +363,28 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
   };
   // A tile inside the row is loaded at once, with its mask bits.
   auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
+  // Without a table the warp's next tile is on its way while one is worked on
+  // (with one, the registers are better spent on more blocks).
+  uint4 next[ADJ ? 1 : kTileVecs];
+  int next_u = -1;
+  auto fetch_next = [&](int u) {
+    if constexpr (!ADJ) {
+      if (u < hi && inside(u)) {
+#pragma unroll
+        for (int k = 0; k < kTileVecs; ++k)
+          next[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+        next_u = u;
+      }
+    }
+  };
   auto load_tile = [&](int u, uint4 (&q)[kTileVecs], uint32_t (&ok)[kTileVecs]) {
+    if constexpr (!ADJ) {
+      if (next_u != u) fetch_next(u);
+#pragma unroll
+      for (int k = 0; k < kTileVecs; ++k) q[k] = next[k];
+      fetch_next(u + warps * kTile);
+      return;
+    }
 #pragma unroll
     for (int k = 0; k < kTileVecs; ++k)
       q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
@@ -456,6 +448,7 @@ __global__ void __launch_bounds__(kRowThreads, ADJ ? 2 : 3)
     m = max_nan(m, ends.largest());
     least = ends.smallest();
   }
+  fetch_next(lo + wid * kTile);  // for the second walk
   m = warp_max_nan(m);
   if (tid == 0) own_weight = 0xffffffffu;
   if (peers > 1) {
