@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kStreamThreads = 512;  // walk the row
 constexpr int kStreamWarps = kStreamThreads / 32;
-constexpr int kListThreads = 128;    // take care of the listed tokens meanwhile
+constexpr int kListThreads = 64;     // take care of the listed tokens meanwhile
 constexpr int kListWarps = kListThreads / 32;
 constexpr int kDisThreads = kStreamThreads + kListThreads;
 constexpr int kDisVecs = 4;
@@ -133,8 +133,10 @@ struct ListSums {
   double count;
 };
 
+// (Not inlined, nor row_figures: the streaming warps' registers are not to pay
+// for the double arithmetic of these.)
 template <typename T>
-__device__ __forceinline__ ListSums list_sums(const Listed &g, const Row<T> &row,
+__device__ __noinline__ ListSums list_sums(const Listed &g, const Row<T> &row,
                                               const int32_t *ids, const float *lp, int K,
                                               double it) {
   const T *z = row.at0 + row.shift;
@@ -174,7 +176,7 @@ __device__ __forceinline__ ListSums list_sums(const Listed &g, const Row<T> &row
 
 // The row's loss and figures.  R sums 2^(c z - offset) over the unlisted
 // tokens, whose largest logit is m_rest (-inf: none has a finite one).
-__device__ __forceinline__ void row_figures(const ListSums &s, double R, float m_rest,
+__device__ __noinline__ void row_figures(const ListSums &s, double R, float m_rest,
                                             float offset, float c, float inv_t, bool tail,
                                             int vocab, float &loss, RowStats &st) {
   const double it = (double)inv_t;

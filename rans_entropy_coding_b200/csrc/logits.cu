@@ -98,8 +98,8 @@ __global__ void __launch_bounds__(TOUCH ? kAdjThreads + kTableThreads : kAdjThre
         if (tid == kAdjThreads) a = row_adjust(adj, r, in.vocab);
         among();
         if (a.touches())
-          u_lo += fill_touch(table, a, row, lo, hi, dense, tid - kAdjThreads, kTableThreads,
-                             among);
+          fill_touch(table, a, row, lo, hi, dense, nullptr, tid - kAdjThreads, kTableThreads,
+                     among);
         if (tid == kAdjThreads) table_dense = dense;
       }
       __syncthreads();
@@ -109,7 +109,7 @@ __global__ void __launch_bounds__(TOUCH ? kAdjThreads + kTableThreads : kAdjThre
       // what the first table does not cover
       u_lo = lo + table.span;
       while (u_lo < hi) {
-        u_lo += fill_touch(table, a, row, u_lo, hi, dense, tid, kAll, all);
+        u_lo += fill_touch(table, a, row, u_lo, hi, dense, nullptr, tid, kAll, all);
         write_touched();
       }
     } else {
@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(TOUCH ? kAdjThreads + kTableThreads : kAdjThre
       __syncthreads();
       while (u_lo < hi) {
         const int from = u_lo;
-        if (a.touches()) u_lo += fill_touch(table, a, row, from, hi, dense, tid, kAll, all);
+        if (a.touches()) u_lo += fill_touch(table, a, row, from, hi, dense, nullptr, tid, kAll, all);
         else u_lo = hi;
         if (tid < kAdjThreads) stream(from, u_lo);
         __syncthreads();

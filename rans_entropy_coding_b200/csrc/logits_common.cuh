@@ -266,23 +266,12 @@ __device__ __forceinline__ RowAdjust row_adjust(const rans_adjust &a, int64_t r,
   return x;
 }
 
-// Mask bits of tokens v0 .. v0 + 31 in bits 0 .. 31 (0 off the row's ends; v0
-// may be a few tokens below 0 where a row's first vector is partial).
-__device__ __forceinline__ uint32_t mask_bits(const uint32_t *mask, int words, int v0) {
-  const int w = v0 >> 5;
-  const uint32_t lo = w >= 0 && w < words ? mask[w] : 0u;
-  const int s = v0 & 31;
-  if (s <= 24) return lo >> s;  // the callers use 8 bits at most
-  const uint32_t hi = w + 1 < words ? mask[w + 1] : 0u;
-  return __funnelshift_r(lo, hi, s);
-}
-
 // Which tokens a row's history and biases touch, and their adjusted logits, in
 // shared memory.  They are few, but spread out: handled where they are met,
 // nearly every warp would stop for one in every vector (49 instructions per
 // logit, measured on rows of 50,000 tokens with 300 touched).  So they are
-// gathered and adjusted first, the kernels' main walks leave them out by a
-// bitmap, and what they add comes from the table, a token per thread.
+// gathered and adjusted first, the kernels' main walks leave them out, and what
+// they add comes from the table, a token per thread.
 // The table is a hash that covers up to kHashSpan tokens at once.  If they
 // have more than kHashTokens touched ones among them, there is a cell per token
 // instead, for kTouchSpan tokens at a time.
@@ -294,14 +283,13 @@ constexpr int kTouchSpan = 8192;
 struct __align__(16) TouchTable {
   union {
     struct {
-      uint32_t bits[kHashSpan / 32];
       int32_t key[kHashSlots];    // place in the span, or -1
       uint32_t count[kHashSlots]; // occurrences; then the adjusted logit
       uint32_t bias[kHashSlots];  // 1 + the last entry's position in the row's list
       uint16_t used[kHashTokens]; // the slots in use, in any order
     } hash;
     struct {
-      uint32_t bits[kTouchSpan / 32];
+      uint32_t bits[kTouchSpan / 32];  // touched tokens
       uint32_t count[kTouchSpan];
       uint32_t bias[kTouchSpan];
     } cells;
@@ -311,13 +299,6 @@ struct __align__(16) TouchTable {
   int shift;       // 32 - log2(slots)
   bool dense;      // a cell per token
 
-  __device__ __forceinline__ uint32_t *bitmap() { return dense ? cells.bits : hash.bits; }
-  // Bits of the touched ones of N tokens from u0 on (a multiple of N).
-  template <int N>
-  __device__ __forceinline__ uint32_t hits(int u0) {
-    const int k = u0 - u_lo;
-    return (bitmap()[k >> 5] >> (k & 31)) & ((1u << N) - 1u);
-  }
   __device__ __forceinline__ uint32_t slot(int k) const {
     return (uint32_t)k * 2654435761u >> shift;  // Fibonacci hashing
   }
@@ -344,25 +325,48 @@ __device__ __forceinline__ void each_touched(TouchTable &t, int tid, int threads
   }
 }
 
-// The adjusted logit of a touched token.
+// The adjusted logit of a token that may be touched; -inf if it is not.
 __device__ __forceinline__ float touched_logit(TouchTable &t, int u) {
   const int k = u - t.u_lo;
-  if (t.dense) return __uint_as_float(t.cells.count[k]);
-  uint32_t s = t.slot(k);
-  while (t.hash.key[s] != k) s = t.next(s);  // its bit is set: it is there
-  return __uint_as_float(t.hash.count[s]);
+  if (k < 0 || k >= t.span) return kNegInf;
+  if (t.dense)
+    return t.cells.bits[k >> 5] >> (k & 31) & 1 ? __uint_as_float(t.cells.count[k]) : kNegInf;
+  for (uint32_t s = t.slot(k); t.hash.key[s] != -1; s = t.next(s))  // (never full)
+    if (t.hash.key[s] == k) return __uint_as_float(t.hash.count[s]);
+  return kNegInf;
+}
+
+// Bits of the row's tokens u_lo .. u_lo + span - 1 that the mask leaves; 0 off
+// the row's ends.  `mask` may be NULL.  No barrier.
+template <typename T>
+__device__ __forceinline__ void fill_mask(uint32_t *ok, const uint32_t *mask, int words,
+                                          const Row<T> &row, int u_lo, int span, int tid,
+                                          int threads) {
+  for (int i = tid; i < (span + 31) / 32; i += threads) {
+    const int u = u_lo + 32 * i, v = u - row.shift;
+    uint32_t b = ~0u;
+    if (mask) {
+      const int w = v >> 5;
+      b = __funnelshift_r(mask[min(max(w, 0), words - 1)], mask[min(max(w + 1, 0), words - 1)],
+                          v & 31);
+    }
+    if (v < 0) b &= ~0u << -v;
+    if (u + 32 > row.end()) b &= ~0u >> (u + 32 - row.end());
+    ok[i] = b;
+  }
 }
 
 // Fills the table from u_lo on, up to u_hi, and returns the tokens it covers.
 // `dense` is a block's memory of having met too many touched tokens (false at
-// first).  Called by `threads` threads of the block that meet at `barrier`,
+// first).  `ok`, if given, gets the bits of the tokens covered that the mask
+// leaves and nothing touches.  Called by `threads` threads of the block that meet at `barrier`,
 // which also begins and ends it.  Counts
 // come from integer adds, maxima and ors: what a token finds does not depend on
 // the threads' order.
 template <typename T, class Barrier>
 __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, const Row<T> &row,
-                                          int u_lo, int u_hi, bool &dense, int tid, int threads,
-                                          Barrier barrier) {
+                                          int u_lo, int u_hi, bool &dense, uint32_t *ok, int tid,
+                                          int threads, Barrier barrier) {
   const int64_t n = a.history_n + a.bias_n;
   int span = min(kHashSpan, u_hi - u_lo);
   // body(place in the span or -1, entry) for the window's entries, four loads
@@ -409,8 +413,7 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
       t.shift = 32 - log2;
       t.dense = false;
     }
-    uint32_t *bits = t.hash.bits;
-    for (int i = tid; i < (span + 31) / 32; i += threads) bits[i] = 0;
+    if (ok) fill_mask(ok, a.mask, a.mask_words, row, u_lo, span, tid, threads);
     for (int i = tid; i < slots; i += threads) {
       t.hash.key[i] = -1;
       t.hash.count[i] = 0;
@@ -426,7 +429,7 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
       if (old == -1) {
         const int at = atomicAdd(&t.n_used, 1);
         if (at < kHashTokens) t.hash.used[at] = (uint16_t)s;
-        atomicOr(&bits[k >> 5], 1u << (k & 31));
+        if (ok) atomicAnd(&ok[k >> 5], ~(1u << (k & 31)));
       }
       if (old != -1 && old != k) return;
       if (i < a.history_n) atomicAdd(&t.hash.count[s], 1u);
@@ -456,6 +459,7 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
     t.cells.count[i] = 0;
     t.cells.bias[i] = 0;
   }
+  if (ok) fill_mask(ok, a.mask, a.mask_words, row, u_lo, span, tid, threads);
   barrier();
   window([&](int k, int64_t i) {
     if (i < a.history_n) atomicAdd(&t.cells.count[k], 1u);
@@ -463,11 +467,13 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
     atomicOr(&bits[k >> 5], 1u << (k & 31));
   });
   barrier();
-  for (int w = tid; w < (span + 31) / 32; w += threads)
+  for (int w = tid; w < (span + 31) / 32; w += threads) {
+    if (ok) ok[w] &= ~bits[w];
     for (uint32_t b = bits[w]; b != 0; b &= b - 1) {
       const int k = w * 32 + __ffs(b) - 1;
       t.cells.count[k] = adjusted(k, t.cells.count[k], t.cells.bias[k]);
     }
+  }
   barrier();
   return span;
 }
@@ -486,15 +492,6 @@ __device__ __forceinline__ uint32_t lane_mask(uint32_t loaded, int v0, int lane)
   const uint32_t a = __shfl_sync(0xffffffffu, loaded, from);
   const uint32_t b = __shfl_sync(0xffffffffu, loaded, from + 1);
   return __funnelshift_r(a, b, v & 31);
-}
-
-// -inf where the row's mask is 0.
-template <int N>
-__device__ __forceinline__ void mask_vector(float (&z)[N], const RowAdjust &a, int v0) {
-  const uint32_t ok = mask_bits(a.mask, a.mask_words, v0);
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (!(ok >> i & 1)) z[i] = kNegInf;
 }
 
 }  // namespace rb

@@ -158,6 +158,16 @@ struct Extremes {
       low = __float_as_uint(b);
     }
   }
+  __device__ __forceinline__ void take_low(const uint4 &q) {
+    if constexpr (sizeof(T) == 2) {
+      low = pair_min(low, pair_min(pair_min(q.x, q.y, T()), pair_min(q.z, q.w, T()), T()), T());
+    } else {
+      float z[4];
+      unpack16(q, z, T());
+#pragma unroll
+      for (int i = 0; i < 4; ++i) low = __float_as_uint(fminf(__uint_as_float(low), z[i]));
+    }
+  }
   __device__ __forceinline__ static float2 both(uint32_t x) {
     if constexpr (sizeof(T) == 2) {
       float z[8];
@@ -254,7 +264,9 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   constexpr int kVecRow = 32 * N;                // tokens of a warp's vectors
   constexpr int kTile = kVecRow * kTileVecs;
   TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
-  uint2 *tile_sums = reinterpret_cast<uint2 *>(smem + (ADJ ? sizeof(TouchTable) : 0));
+  // bits of the tokens that the mask leaves and nothing touches
+  uint32_t *ok_bits = reinterpret_cast<uint32_t *>(smem + (ADJ ? sizeof(TouchTable) : 0));
+  uint2 *tile_sums = reinterpret_cast<uint2 *>(ok_bits + (ADJ ? kHashSpan / 32 : 0));
   __shared__ float peer_max[kMaxCluster * kRowWarps];
   __shared__ WarpSums peer_sums[kMaxCluster * kRowWarps];
   __shared__ uint32_t own_weight;
@@ -311,12 +323,11 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   }
 
   __shared__ RowAdjust a;
-  bool touch = false, masked = false;
+  bool touch = false;
   if constexpr (ADJ) {
     if (tid == 0) a = row_adjust(adj, r, in.vocab);
     __syncthreads();
     touch = a.touches();
-    masked = a.mask != nullptr;
   }
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
   if (DECODE && ADJ && touch)  // added to after the first walk's barrier
@@ -324,8 +335,16 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   int table_at = -1, span = 1 << 30;  // where the table starts, its tokens
   bool dense = false;
   auto need_table = [&](int u_lo) {
-    if (!ADJ || !touch || table_at == u_lo) return;
-    span = fill_touch(table, a, row, u_lo, hi, dense, tid, threads, [] { __syncthreads(); });
+    if (!ADJ || table_at == u_lo) return;
+    if (touch) {
+      span = fill_touch(table, a, row, u_lo, hi, dense, ok_bits, tid, threads,
+                        [] { __syncthreads(); });
+    } else {
+      span = min(kHashSpan, hi - u_lo);
+      __syncthreads();
+      fill_mask(ok_bits, a.mask, a.mask_words, row, u_lo, span, tid, threads);
+      __syncthreads();
+    }
     table_at = u_lo;
   };
   // walks this block's tiles, body(tile's first u, its number), and the touched
@@ -338,117 +357,77 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       if (ADJ && touch) each_touched(table, tid, threads, touched_body);
     }
   };
-  // adjusted logits of this lane's vector at u0, wherever that is; touched ones
-  // read -inf unless asked for
-  auto fetch = [&](int u0, float (&z)[N], bool all) {
-    row.load(u0, z, kNegInf);
-    if constexpr (ADJ) {
-      if (u0 < row.end()) {
-        if (masked) mask_vector<N>(z, a, u0 - row.shift);
-        if (touch) {
-          const uint32_t hit = table.hits<N>(u0);
-          if (hit) {
-#pragma unroll
-            for (int i = 0; i < N; ++i)
-              if (hit >> i & 1) z[i] = all ? touched_logit(table, u0 + i) : kNegInf;
-          }
-        }
-      }
-      if (!row.whole(u0)) {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-          if (u0 + i < row.shift || u0 + i >= row.end()) z[i] = kNegInf;
-      }
-    }
-  };
-  // A tile inside the row is loaded at once, with its mask bits.
+  // A tile is loaded at once, with the bits of its tokens that count (`some`:
+  // not all of them do).  Places off the row's ends read 0.
   auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
-  // Without a table the warp's next tile is on its way while one is worked on
-  // (with one, the registers are better spent on more blocks).
-  uint4 next[ADJ ? 1 : kTileVecs];
-  int next_u = -1;
-  auto fetch_next = [&](int u) {
-    if constexpr (!ADJ) {
-      if (u < hi && inside(u)) {
+  auto load_tile = [&](int u, uint4 (&q)[kTileVecs], uint32_t (&ok)[kTileVecs]) -> bool {
+    const bool edge = !inside(u);
+    if (edge) {
 #pragma unroll
-        for (int k = 0; k < kTileVecs; ++k)
-          next[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
-        next_u = u;
-      }
-    }
-  };
-  auto load_tile = [&](int u, uint4 (&q)[kTileVecs], uint32_t (&ok)[kTileVecs]) {
-    if constexpr (!ADJ) {
-      if (next_u != u) fetch_next(u);
-#pragma unroll
-      for (int k = 0; k < kTileVecs; ++k) q[k] = next[k];
-      fetch_next(u + warps * kTile);
-      return;
-    }
-#pragma unroll
-    for (int k = 0; k < kTileVecs; ++k)
-      q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
-    if constexpr (ADJ) {
-      // the tokens that the mask leaves and nothing touches
-      if (masked) {
-#pragma unroll
-        for (int k = 0; k < kTileVecs; ++k)
-          ok[k] = load_mask<N>(a.mask, a.mask_words, u + k * kVecRow - row.shift, lane);
-#pragma unroll
-        for (int k = 0; k < kTileVecs; ++k)
-          ok[k] = lane_mask<N>(ok[k], u + k * kVecRow - row.shift, lane);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kTileVecs; ++k) ok[k] = ~0u;
-      }
-      if (touch) {
-#pragma unroll
-        for (int k = 0; k < kTileVecs; ++k)
-          ok[k] &= ~table.hits<N>(u + k * kVecRow + lane * N);
-      }
-    }
-  };
-
-  // First walk: the maximum, and the least logit that the mask leaves in the
-  // tiles inside the row.
-  float m = kNegInf, least = __builtin_huge_valf();
-  Extremes<T> ends;
-  walk([&](int u, int) {
-    if (inside(u)) {
-      uint4 q[kTileVecs];
-      uint32_t ok[kTileVecs];
-      load_tile(u, q, ok);
-      if constexpr (!ADJ) {
-#pragma unroll
-        for (int k = 0; k < kTileVecs; ++k) ends.take(q[k]);
-      } else {
-#pragma unroll
-        for (int k = 0; k < kTileVecs; ++k) {
+      for (int k = 0; k < kTileVecs; ++k) {
+        const int u0 = u + k * kVecRow + lane * N;
+        q[k] = make_uint4(0, 0, 0, 0);
+        if (row.whole(u0)) {
+          q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+        } else if (u0 < row.end()) {
           float z[N];
-          unpack16(q[k], z, T());
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const bool alive = ok[k] >> i & 1;
-            m = max_nan(m, alive ? z[i] : kNegInf);
-            least = fminf(least, alive ? z[i] : __builtin_huge_valf());
-          }
+          row.load(u0, z, 0.0f);
+          q[k] = pack16(z, T());
         }
+        const int from = min(max(row.shift - u0, 0), N), to = min(max(row.end() - u0, 0), N);
+        ok[k] = (1u << to) - (1u << from);
       }
     } else {
 #pragma unroll
-      for (int k = 0; k < kTileVecs; ++k) {
-        float z[N];
-        fetch(u + k * kVecRow + lane * N, z, false);
+      for (int k = 0; k < kTileVecs; ++k)
+        q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
+    }
+    if constexpr (ADJ) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) m = max_nan(m, z[i]);
+      for (int k = 0; k < kTileVecs; ++k) {
+        const int at = u + k * kVecRow + lane * N - table_at;
+        const uint32_t b = at < span ? ok_bits[at >> 5] >> (at & 31) & ((1u << N) - 1u) : 0u;
+        ok[k] = b;
+      }
+    }
+    return ADJ || edge;
+  };
+  // Adjusted logits of this lane's vector at u0; those of touched tokens read
+  // -inf unless asked for.  (For what is done once per row.)
+  auto fetch = [&](int u0, float (&z)[N], bool all) {
+    row.load(u0, z, kNegInf);
+    if constexpr (ADJ) {
+      const int at = u0 - table_at;
+      const uint32_t b = at < span ? ok_bits[at >> 5] >> (at & 31) : 0u;
+#pragma unroll
+      for (int i = 0; i < N; ++i)
+        if (!(b >> i & 1)) z[i] = all && touch ? touched_logit(table, u0 + i) : kNegInf;
+    }
+  };
+
+  // First walk: the maximum of the tokens that count, and the least logit of
+  // all in the tiles (which only has to be a bound).
+  float m = kNegInf;
+  Extremes<T> ends;
+  walk([&](int u, int) {
+    uint4 q[kTileVecs];
+    uint32_t ok[kTileVecs];
+    if (!load_tile(u, q, ok)) {
+#pragma unroll
+      for (int k = 0; k < kTileVecs; ++k) ends.take(q[k]);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kTileVecs; ++k) {
+        ends.take_low(q[k]);
+        float z[N];
+        unpack16(q[k], z, T());
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = max_nan(m, ok[k] >> i & 1 ? z[i] : kNegInf);
       }
     }
   }, [&](int, float z) { m = max_nan(m, z); });
-  if constexpr (!ADJ) {
-    m = max_nan(m, ends.largest());
-    least = ends.smallest();
-  }
-  fetch_next(lo + wid * kTile);  // for the second walk
+  const float least = ends.smallest();
+  m = max_nan(m, ends.largest());
   m = warp_max_nan(m);
   if (tid == 0) own_weight = 0xffffffffu;
   if (peers > 1) {
@@ -470,33 +449,32 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   if (rs.error != RANS_OK) return refuse(rs.error, r, true);
 
   // Second walk: the weights.  Where a warp's smallest logit needs no clamp,
-  // only the mask makes dead tokens, and the weights go two at a time; a
-  // masked token then takes a logit whose d is -40, hence weight 0 (which
-  // wants a maximum that 40 can be told from, and a factor).
+  // the only dead tokens are those that do not count, and the weights go two at
+  // a time; such a token then takes a logit whose d is -40, hence weight 0
+  // (which wants a maximum that 40 can be told from, and a factor).
   const int u_target = row.shift + target;
   const bool plain = __all_sync(
       kFull, __fsub_rn(__fmul_rn(least, rs.scale), rs.ymax) >= kLowest && least > kNegInf &&
-                 (!ADJ || (fabsf(rs.ymax) < 65536.0f && rs.scale > 0.0f)));
-  const float dead = ADJ ? (rs.ymax - 40.0f) / rs.scale : 0.0f;
+                 fabsf(rs.ymax) < 65536.0f && rs.scale > 0.0f);
+  const float dead = (rs.ymax - 40.0f) / rs.scale;
   const uint64_t scale2 = (uint64_t)__float_as_uint(rs.scale) << 32 | __float_as_uint(rs.scale);
   const uint64_t ymax2 =
       (uint64_t)__float_as_uint(-rs.ymax) << 32 | __float_as_uint(-rs.ymax);
   WarpSums s = {0, 0, 0, 0};
   walk([&](int u, int tile) {
     // a lane's weights of a tile stay below 2^26, a tile's below 2^31
-    uint32_t w = 0, n = 0;
-    if (plain && inside(u)) {
-      uint4 q[kTileVecs];
-      uint32_t ok[kTileVecs];
-      load_tile(u, q, ok);
+    uint4 q[kTileVecs];
+    uint32_t ok[kTileVecs], w = 0, n = 0;
+    const bool some = load_tile(u, q, ok);
+    if (plain) {
 #pragma unroll
       for (int k = 0; k < kTileVecs; ++k) {
         float z[N];
         unpack16(q[k], z, T());
-        if constexpr (ADJ) {
+        if (some) {
 #pragma unroll
           for (int i = 0; i < N; ++i) z[i] = ok[k] >> i & 1 ? z[i] : dead;
-          n += __popc(ok[k] & ((1u << N) - 1u));
+          n += __popc(ok[k]);
         }
 #pragma unroll
         for (int i = 0; i < N; i += 2) {
@@ -505,14 +483,15 @@ __global__ void __launch_bounds__(kRowThreads, 2)
         }
       }
       w -= (uint32_t)(N * kTileVecs) * __float_as_uint(kUnit);
-      if constexpr (!ADJ) n = N * kTileVecs;
+      if (!some) n = N * kTileVecs;
     } else {
 #pragma unroll
       for (int k = 0; k < kTileVecs; ++k) {
         float z[N];
-        fetch(u + k * kVecRow + lane * N, z, false);
+        unpack16(q[k], z, T());
 #pragma unroll
         for (int i = 0; i < N; ++i) {
+          if (some && !(ok[k] >> i & 1)) z[i] = kNegInf;
           w += token_weight(z[i], rs.scale, rs.ymax);
           n += z[i] > kNegInf ? 1u : 0u;
         }
@@ -825,7 +804,7 @@ int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *
                        (in.rows == 1 || in.row_stride % VecOf<T>::N == 0);
   const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), kTile,
                                    num_sms(dev));
-  const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) : 0u) +
+  const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) + kHashSpan / 8 : 0u) +
                         (DECODE ? (uint32_t)(shape.slice / kTile * sizeof(uint2)) : 0u);
   if (ensure_cluster((const void *)kern) != cudaSuccess) return RANS_ERR_CUDA;
   if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
