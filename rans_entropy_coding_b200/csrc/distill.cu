@@ -23,13 +23,13 @@
 namespace rb {
 namespace {
 
-constexpr int kStreamThreads = 512;  // walk the row
+constexpr int kStreamThreads = 256;  // walk the row
 constexpr int kStreamWarps = kStreamThreads / 32;
-constexpr int kListThreads = 64;     // take care of the listed tokens meanwhile
-constexpr int kListWarps = kListThreads / 32;
+constexpr int kListThreads = 32;     // one warp for the listed tokens meanwhile
 constexpr int kDisThreads = kStreamThreads + kListThreads;
 constexpr int kDisVecs = 4;
 constexpr int kDisCluster = 8;
+constexpr uint32_t kRingBytes = kStreamWarps * 2 * kDisVecs * 32 * 16;
 constexpr double kLog2eD = 1.4426950408889634;
 constexpr double kLn2D = 0.6931471805599453;
 
@@ -82,47 +82,43 @@ struct RowStats {
 };
 static_assert(sizeof(RowStats) == 32, "8 floats");
 
-__device__ __forceinline__ bool entry(const int32_t *ids, const float *lp, int i, int vocab,
-                                      int &v, float &l) {
-  v = ids[i];
-  l = lp[i];
+__device__ __forceinline__ bool present(int v, float l, int vocab) {
   return v >= 0 && v < vocab && l != kNegInf;
 }
 
-// The threads that see to the listed tokens.
-struct Listed {
-  int tid;  // 0 .. kListThreads - 1
-  double *red;
-
-  __device__ __forceinline__ void barrier() const {
-    asm volatile("bar.sync 1, %0;" ::"n"(kListThreads) : "memory");
-  }
-  // Sum over them, in a fixed order; every one gets it.
-  __device__ __forceinline__ double sum(double x) const {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
-    barrier();
-    if ((tid & 31) == 0) red[tid >> 5] = x;
-    barrier();
-    double t = red[0];
-#pragma unroll
-    for (int w = 1; w < kListWarps; ++w) t += red[w];
-    return t;
-  }
-  __device__ __forceinline__ double max(double x) const {
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) x = fmax(x, __shfl_xor_sync(kFull, x, o));
-    barrier();
-    if ((tid & 31) == 0) red[tid >> 5] = x;
-    barrier();
-    double t = red[0];
-#pragma unroll
-    for (int w = 1; w < kListWarps; ++w) t = fmax(t, red[w]);
-    return t;
-  }
+// A chunk of the list, kEntries a lane: all its loads in flight together.
+constexpr int kEntries = 4;
+constexpr int kChunk = 32 * kEntries;
+struct Entries {
+  int v[kEntries];    // token, -1 where there is no entry
+  float lp[kEntries], z[kEntries];
 };
+template <typename T>
+__device__ __forceinline__ void load_entries(Entries &e, const T *z, const int32_t *ids,
+                                             const float *lp, int from, int K, int vocab,
+                                             int lane, int64_t r, int32_t *status) {
+#pragma unroll
+  for (int j = 0; j < kEntries; ++j) {
+    const int i = from + j * 32 + lane;
+    e.v[j] = i < K ? ids[i] : -1;
+    e.lp[j] = i < K ? lp[i] : kNegInf;
+  }
+#pragma unroll
+  for (int j = 0; j < kEntries; ++j) {
+    const bool ok = present(e.v[j], e.lp[j], vocab);
+    if (status && !ok && e.v[j] != -1 && e.lp[j] != kNegInf) report(status, RANS_ERR_INDEX, r);
+    if (!ok) e.v[j] = -1;
+    e.z[j] = ok ? logit_float(z[e.v[j]]) : kNegInf;
+  }
+}
 
-// What the listed tokens give: sums over the entries present.
+__device__ __forceinline__ double lanes_sum(double x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(kFull, x, o);
+  return x;
+}
+
+// What the listed tokens give: sums over the entries present, in double.
 struct ListSums {
   double m;      // largest of their logits (0 if none is finite)
   bool some;     // one is
@@ -133,81 +129,98 @@ struct ListSums {
   double count;
 };
 
-// (Not inlined, nor row_figures: the streaming warps' registers are not to pay
-// for the double arithmetic of these.)
+// By one warp; `first` holds the list's first chunk.  (Not inlined, nor
+// row_figures: the streaming warps' registers are not to pay for the double
+// arithmetic of these.)
 template <typename T>
-__device__ __noinline__ ListSums list_sums(const Listed &g, const Row<T> &row,
-                                              const int32_t *ids, const float *lp, int K,
-                                              double it) {
-  const T *z = row.at0 + row.shift;
-  ListSums s = {-HUGE_VAL, false, 0, 0, 0, 0, 0};
-  bool nan = false;
-  for (int i = g.tid; i < K; i += kListThreads) {
-    int v;
-    float l;
-    if (!entry(ids, lp, i, row.vocab, v, l)) continue;
-    const float zi = logit_float(z[v]);
-    nan |= zi != zi;
-    s.m = fmax(s.m, (double)zi);
-    const double p = exp((double)l);
-    s.p += p;
-    s.plp += p > 0.0 || p != p ? p * (double)l : 0.0;
-    s.count += 1.0;
+__device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, const int32_t *ids,
+                                           const float *lp, int K, int vocab, double it,
+                                           int lane) {
+  Entries e = first;
+  float m = kNegInf;
+  for (int from = 0; from < K; from += kChunk) {
+    if (from > 0) load_entries(e, z, ids, lp, from, K, vocab, lane, 0, nullptr);
+#pragma unroll
+    for (int j = 0; j < kEntries; ++j) m = fmaxf(m, e.z[j]);
   }
-  s.m = g.max(s.m);
-  s.some = s.m > -HUGE_VAL;
-  if (!s.some) s.m = 0.0;
-  for (int i = g.tid; i < K; i += kListThreads) {
-    int v;
-    float l;
-    if (!entry(ids, lp, i, row.vocab, v, l)) continue;
-    const double d = ((double)logit_float(z[v]) - s.m) * it, p = exp((double)l);
-    s.z += exp(d);
-    s.pz += p > 0.0 ? p * d : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  ListSums s = {m == kNegInf ? 0.0 : (double)m, m != kNegInf, 0, 0, 0, 0, 0};
+  for (int from = 0; from < K; from += kChunk) {
+    if (K > kChunk) load_entries(e, z, ids, lp, from, K, vocab, lane, 0, nullptr);
+#pragma unroll
+    for (int j = 0; j < kEntries; ++j) {
+      if (e.v[j] < 0) continue;
+      const double l = (double)e.lp[j], d = ((double)e.z[j] - s.m) * it, p = exp(l);
+      s.z += exp(d);
+      s.p += p;
+      s.plp += p > 0.0 || p != p ? p * l : 0.0;
+      s.pz += p > 0.0 ? p * d : 0.0;
+      s.count += 1.0;
+    }
   }
-  if (nan) s.z = NAN;
-  s.z = g.sum(s.z);
-  s.p = g.sum(s.p);
-  s.plp = g.sum(s.plp);
-  s.pz = g.sum(s.pz);
-  s.count = g.sum(s.count);
+  s.z = lanes_sum(s.z);
+  s.p = lanes_sum(s.p);
+  s.plp = lanes_sum(s.plp);
+  s.pz = lanes_sum(s.pz);
+  s.count = lanes_sum(s.count);
   return s;
 }
 
-// The row's loss and figures.  R sums 2^(c z - offset) over the unlisted
-// tokens, whose largest logit is m_rest (-inf: none has a finite one).
-__device__ __noinline__ void row_figures(const ListSums &s, double R, float m_rest,
+// What the row's gradient needs, and what its loss is computed from later.
+struct RowSums {
+  double m, rest, z, mass, pt, norm;
+  bool some, ignored;
+};
+
+// R sums 2^(c z - offset) over the unlisted tokens, whose largest logit is
+// m_rest (-inf: none has a finite one).  The streaming warps wait for this:
+// two exponentials side by side and a few products; the loss's logarithms come
+// later.
+__device__ __noinline__ RowSums row_figures(const ListSums &s, double R, float m_rest,
                                             float offset, float c, float inv_t, bool tail,
-                                            int vocab, float &loss, RowStats &st) {
+                                            int vocab, RowStats &st) {
   const double it = (double)inv_t;
-  const bool some = R > 0.0 || R != R;
-  double m = fmax(s.some ? s.m : -HUGE_VAL, some ? (double)m_rest : -HUGE_VAL);
-  if (m == -HUGE_VAL) m = 0.0;
-  // R with its offset's rounding taken back, by the elements' own factor c
-  const double log_r =
-      some ? (log2(R) + ((double)offset - (double)c * (double)m_rest)) * kLn2D : -HUGE_VAL;
-  const double log_rest = log_r + ((double)(some ? m_rest : 0.0f) - m) * it;  // against m
-  const double rest = some ? exp(log_rest) : 0.0;
-  const double top = s.some || s.z != s.z ? s.z * exp((s.m - m) * it) : 0.0;
-  const double Z = rest + top, lz = log(Z);
-  const double norm = tail ? 1.0 : (s.p > 0.0 ? 1.0 / s.p : 0.0);
-  const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
-  const double mass = s.p * norm + pt;
-  const bool ignored = !tail && !(s.p > 0.0) && s.p == s.p;
-  // sum p (log p - log q), p = norm * listed p
+  RowSums f;
+  f.some = R > 0.0 || R != R;
+  f.m = fmax(s.some ? s.m : -HUGE_VAL, f.some ? (double)m_rest : -HUGE_VAL);
+  if (f.m == -HUGE_VAL) f.m = 0.0;
+  // against m, with the offset's rounding taken back by the elements' own c
+  const double back = ((double)offset - (double)c * (double)m_rest) * kLn2D;
+  f.rest = f.some ? R * exp(((double)m_rest - f.m) * it + back) : 0.0;
+  const double top = s.some || s.z != s.z ? s.z * exp((s.m - f.m) * it) : 0.0;
+  f.z = f.rest + top;
+  f.norm = tail ? 1.0 : (s.p > 0.0 ? 1.0 / s.p : 0.0);
+  f.pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
+  f.mass = s.p * f.norm + f.pt;
+  f.ignored = !tail && !(s.p > 0.0) && s.p == s.p;
+  const double inv_z = 1.0 / f.z;
+  st.offset = f.some ? offset : 0.0f;
+  st.rest = f.some && !f.ignored ? (float)(it * (f.mass * (f.rest * inv_z) - f.pt) / R) : 0.0f;
+  if (f.z != f.z) st.rest = (float)f.z;
+  st.m_all = (float)f.m;
+  st.inv_z = (float)inv_z;
+  st.mass = (float)f.mass;
+  st.inv_p = (float)f.norm;
+  st.pad[0] = st.pad[1] = 0.0f;
+  return f;
+}
+
+// sum p (log p - log q) over the list (p = norm * its entries') and the tail.
+__device__ __noinline__ float row_loss(const ListSums &s, const RowSums &f, double R,
+                                       float m_rest, float offset, float c, float inv_t) {
+  if (f.ignored) return f.z == f.z ? 0.0f : (float)f.z;
+  const double it = (double)inv_t, lz = log(f.z);
   double part = 0.0;
   if (s.p > 0.0 || s.p != s.p)
-    part = norm * (s.plp + s.p * (tail ? 0.0 : -log(s.p)) - s.pz - s.p * ((s.m - m) * it - lz));
-  if (pt > 0.0) part += pt * (log(pt) - (some ? log_rest - lz : -HUGE_VAL));
-  loss = ignored ? (Z == Z ? 0.0f : (float)Z) : (float)part;
-  st.offset = some ? offset : 0.0f;
-  st.rest = some && !ignored ? (float)(it * (mass * (rest / Z) - pt) / R) : 0.0f;
-  if (Z != Z) st.rest = (float)Z;
-  st.m_all = (float)m;
-  st.inv_z = (float)(1.0 / Z);
-  st.mass = (float)mass;
-  st.inv_p = (float)norm;
-  st.pad[0] = st.pad[1] = 0.0f;
+    part = f.norm * (s.plp + s.p * log(f.norm) - s.pz - s.p * ((s.m - f.m) * it - lz));
+  if (f.pt > 0.0) {
+    // the tail's logarithm from R's own: rest may be too small for a double
+    const double back = ((double)offset - (double)c * (double)m_rest) * kLn2D;
+    const double log_rest = f.some ? log(R) + back + ((double)m_rest - f.m) * it : -HUGE_VAL;
+    part += f.pt * (log(f.pt) - (log_rest - lz));
+  }
+  return (float)part;
 }
 
 // A warp's part of R.
@@ -244,24 +257,26 @@ enum { kForward = 1, kBackward = 2 };
 // One cluster per row.  WHAT: kForward writes losses and (without kBackward)
 // stats; kBackward the gradient, from stats where there is no forward pass.
 template <typename T, int WHAT>
-__global__ void __launch_bounds__(kDisThreads, 2)
+__global__ void __launch_bounds__(kDisThreads, 4)
     distill_kernel(rans_logits in, const int32_t *ids, const float *lp, int K, float inv_t,
                    int tail, float *losses, RowStats *stats, const float *grads, T *grad,
                    int64_t grad_stride, int32_t *status, int slice) {
-  extern __shared__ uint32_t bits[];  // listed tokens of this block's slice
+  extern __shared__ __align__(16) unsigned char smem[];
   constexpr int N = VecOf<T>::N;
   constexpr int kVecRow = 32 * N, kTile = kVecRow * kDisVecs;
-  __shared__ double red[kListWarps];
   __shared__ Part parts[kDisCluster * kStreamWarps];
   __shared__ RowStats figures;
-  __shared__ float top_z[(WHAT & kBackward) ? RANS_MAX_TOP : 1];
+  // each streaming warp's two tiles on their way; listed tokens of this
+  // block's slice; the listed tokens' logits
+  uint4 *ring = reinterpret_cast<uint4 *>(smem) + (threadIdx.x >> 5) * 2 * kDisVecs * 32;
+  uint32_t *bits = reinterpret_cast<uint32_t *>(smem + kRingBytes);
+  float *top_z = reinterpret_cast<float *>(bits + ((WHAT & kForward) ? slice / 32 : 0));
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = cluster_rank(), peers = cluster_size();
   const int64_t r = blockIdx.x / peers;
   const Row<T> row(in.data, r, in.row_stride, in.vocab);
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
   const bool lists = tid >= kStreamThreads;
-  const Listed group = {tid - kStreamThreads, red};
   const float c = (float)((double)inv_t * kLog2eD);
   ids += r * K;
   lp += r * K;
@@ -270,48 +285,90 @@ __global__ void __launch_bounds__(kDisThreads, 2)
     cluster_arrive();
   }
 
+  // Tiles reach a warp through its ring, two ahead, with no registers held
+  // meanwhile; each lane copies and reads its own vectors.  (A tile that is not
+  // inside the row is loaded when it is due.)
+  auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
+  auto send = [&](int u, int stage) {
+    if (u >= lo && u < hi && inside(u)) {
+#pragma unroll
+      for (int k = 0; k < kDisVecs; ++k)
+        cp_async16(ring + (stage * kDisVecs + k) * 32 + lane,
+                   row.at0 + u + k * kVecRow + lane * N);
+    }
+    cp_async_commit();
+  };
+  auto receive = [&](int u, int stage, uint4 (&q)[kDisVecs]) {
+    cp_async_wait<1>();
+    if (inside(u)) {
+#pragma unroll
+      for (int k = 0; k < kDisVecs; ++k) q[k] = ring[(stage * kDisVecs + k) * 32 + lane];
+    } else {
+#pragma unroll
+      for (int k = 0; k < kDisVecs; ++k) {
+        const int u0 = u + k * kVecRow + lane * N;
+        if (row.whole(u0)) {
+          q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+        } else {
+          float z[N];
+          row.load(u0, z, kNegInf);
+          q[k] = pack16(z, T());
+        }
+      }
+    }
+    // read before the stage is written again
+#pragma unroll
+    for (int k = 0; k < kDisVecs; ++k)
+      asm volatile("" : "+r"(q[k].x), "+r"(q[k].y), "+r"(q[k].z), "+r"(q[k].w));
+  };
+  constexpr int step = kStreamWarps * kTile;
+  // the second walk goes backwards: what the first read last is nearest
+  const int last = lo + ((hi > lo ? (hi - lo + kTile - 1) / kTile : 0) - 1 - wid) * kTile;
+
+  ListSums sums = {};  // (of the listing threads, as what follows)
+  RowSums row_sums = {};
+  double row_R = 0.0;
+  float row_m_rest = 0.0f, row_offset = 0.0f;
+  const int first = lo + wid * kTile;
+  Entries e;  // (the listing warp's)
+  if (lists) {
+    load_entries(e, row.at0 + row.shift, ids, lp, 0, K, in.vocab, lane, r,
+                 (WHAT & kForward) && rank == 0 ? status : nullptr);
+  } else if (WHAT & kForward) {
+    send(first, 0);
+    send(first + step, 1);
+  }
   if constexpr ((WHAT & kForward) != 0) {
     for (int i = tid; i < slice / 32; i += kDisThreads) bits[i] = 0;
     __syncthreads();
+    auto mark = [&](int v) {
+      const int k = v + row.shift - lo;
+      if (v < 0 || k < 0 || k >= hi - lo) return;
+      if (atomicOr(&bits[k >> 5], 1u << (k & 31)) >> (k & 31) & 1)
+        report(status, RANS_ERR_INDEX, r);  // listed twice
+    };
     if (lists) {
-      for (int i = group.tid; i < K; i += kListThreads) {
-        const int v = ids[i];
-        if (v == -1 || lp[i] == kNegInf) continue;
-        if (v < 0 || v >= in.vocab) {
-          if (rank == 0) report(status, RANS_ERR_INDEX, r);
-          continue;
-        }
-        const int k = v + row.shift - lo;
-        if (k < 0 || k >= hi - lo) continue;
-        if (atomicOr(&bits[k >> 5], 1u << (k & 31)) >> (k & 31) & 1)
-          report(status, RANS_ERR_INDEX, r);  // listed twice
-      }
+#pragma unroll
+      for (int j = 0; j < kEntries; ++j) mark(e.v[j]);
+    }
+    for (int i = kChunk + tid; i < K; i += kDisThreads) {
+      const int v = ids[i];
+      if (present(v, lp[i], in.vocab)) mark(v);
+      else if (rank == 0 && v != -1 && lp[i] != kNegInf) report(status, RANS_ERR_INDEX, r);
     }
     __syncthreads();
-    ListSums sums = {};
     if (lists) {
-      sums = list_sums(group, row, ids, lp, K, (double)inv_t);
+      sums = list_sums(e, row.at0 + row.shift, ids, lp, K, in.vocab, (double)inv_t, lane);
     } else {
       // R, against each lane's running maximum
       float m = kNegInf, off = 0.0f;
       uint64_t s2 = 0;  // two sums
       const uint64_t c2 = pair(c, c);
-      for (int u = lo + wid * kTile; u < hi; u += kStreamWarps * kTile) {
+      for (int u = first, stage = 0; u < hi; u += step, stage ^= 1) {
         uint4 q[kDisVecs];
         uint32_t word[kDisVecs];
-        const bool inside = u >= row.shift && u + kTile <= row.end();
-        if (inside) {
-#pragma unroll
-          for (int k = 0; k < kDisVecs; ++k)
-            q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + k * kVecRow + lane * N);
-        } else {
-#pragma unroll
-          for (int k = 0; k < kDisVecs; ++k) {
-            float z[N];
-            row.load(u + k * kVecRow + lane * N, z, kNegInf);
-            q[k] = pack16(z, T());
-          }
-        }
+        receive(u, stage, q);
+        send(u + 2 * step, stage);
         // (a tile's bits lie inside the slice's, which is a whole number of tiles)
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k)
@@ -348,6 +405,10 @@ __global__ void __launch_bounds__(kDisThreads, 2)
         }
       }
       float s = unpair(s2).x + unpair(s2).y;
+      if constexpr ((WHAT & kBackward) != 0) {  // the second walk's first tiles
+        send(last, 0);
+        send(last - step, 1);
+      }
       float w = m;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w = max_nan(w, __shfl_xor_sync(kFull, w, o));
@@ -387,17 +448,20 @@ __global__ void __launch_bounds__(kDisThreads, 2)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) R += __shfl_xor_sync(kFull, R, o);
       if (lane == 0) {
-        float loss;
         RowStats st;
-        row_figures(sums, R, m_rest, offset, c, inv_t, tail != 0, in.vocab, loss, st);
+        row_sums = row_figures(sums, R, m_rest, offset, c, inv_t, tail != 0, in.vocab, st);
+        row_R = R;
+        row_m_rest = m_rest;
+        row_offset = offset;
         figures = st;
-        if (rank == 0) {
-          losses[r] = loss;
-          if constexpr (WHAT == kForward) stats[r] = st;
-        }
+        if (WHAT == kForward && rank == 0) stats[r] = st;
       }
     }
-    if constexpr (WHAT == kForward) return;
+    if constexpr (WHAT == kForward) {
+      if (rank == 0 && tid == kStreamThreads)
+        losses[r] = row_loss(sums, row_sums, row_R, row_m_rest, row_offset, c, inv_t);
+      return;
+    }
   } else {
     if (tid == 0) figures = stats[r];
   }
@@ -405,15 +469,14 @@ __global__ void __launch_bounds__(kDisThreads, 2)
   if constexpr ((WHAT & kBackward) != 0) {
     // grad may be the logits' own memory: this block's listed ones are read
     // before anything is written
-    if (lists)
-      for (int i = group.tid; i < K; i += kListThreads) {
-        int v;
-        float l;
-        if (entry(ids, lp, i, in.vocab, v, l) && v + row.shift >= lo && v + row.shift < hi)
-          top_z[i] = logit_float(row.at0[row.shift + v]);
-      }
+    auto mine = [&](int v) { return v + row.shift >= lo && v + row.shift < hi; };
+    for (int i = kChunk + tid; i < K; i += kDisThreads)
+      if (present(ids[i], lp[i], in.vocab) && mine(ids[i]))
+        top_z[i] = logit_float(row.at0[row.shift + ids[i]]);
     __syncthreads();
     // (another block's sums over the listed tokens are behind the barrier too)
+    if ((WHAT & kForward) && rank == 0 && tid == kStreamThreads)  // while the others stream
+      losses[r] = row_loss(sums, row_sums, row_R, row_m_rest, row_offset, c, inv_t);
     const RowStats st = figures;
     const float g = grads[r];
     T *o = grad + r * grad_stride - row.shift;
@@ -422,24 +485,19 @@ __global__ void __launch_bounds__(kDisThreads, 2)
       const uint64_t c2 = pair(c, c), off2 = pair(-st.offset, -st.offset);
       const uint64_t factor2 = pair(factor, factor);
       const bool aligned = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
-      // backwards: what the first walk read last is nearest
-      const int tiles = hi > lo ? (hi - lo + kTile - 1) / kTile : 0;
-      for (int t = tiles - 1 - wid; t >= 0; t -= kStreamWarps) {
-        const int u = lo + t * kTile;
-        const bool inside = u >= row.shift && u + kTile <= row.end();
+      if constexpr (WHAT == kBackward) {
+        send(last, 0);
+        send(last - step, 1);
+      }
+      for (int u = last, stage = 0; u >= lo; u -= step, stage ^= 1) {
         uint4 q[kDisVecs];
+        receive(u, stage, q);
+        send(u - 2 * step, stage);
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
           const int u0 = u + k * kVecRow + lane * N;
-          if (inside || row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
-        }
-#pragma unroll
-        for (int k = 0; k < kDisVecs; ++k) {
-          const int u0 = u + k * kVecRow + lane * N;
-          const bool whole = inside || row.whole(u0);
           float z[N];
-          if (whole) unpack16(q[k], z, T());
-          else row.load(u0, z, kNegInf);
+          unpack16(q[k], z, T());
 #pragma unroll
           for (int i = 0; i < N; i += 2) {
             const float2 e = exp2_pair(z[i], z[i + 1], c2, off2);
@@ -450,22 +508,25 @@ __global__ void __launch_bounds__(kDisThreads, 2)
             z[i + 1] = f.y;
           }
           const uint4 p = pack16(z, T());
-          if (inside && aligned) *reinterpret_cast<uint4 *>(o + u0) = p;
-          else if (u0 - lane * N < hi) store_vectors(o, u0, p, whole, row.shift, row.end());
+          if (aligned && inside(u)) store16<true>(o + u0, p);
+          else if (u0 - lane * N < hi)
+            store_vectors<true>(o, u0, p, row.whole(u0), row.shift, row.end());
         }
       }
     }
     __syncthreads();  // the listed tokens' gradients go over what stands there
-    if (lists)
-      for (int i = group.tid; i < K; i += kListThreads) {
-        int v;
-        float l;
-        if (!entry(ids, lp, i, in.vocab, v, l) || v + row.shift < lo || v + row.shift >= hi)
-          continue;
-        const float q = expf((top_z[i] - st.m_all) * inv_t) * st.inv_z;
-        const float p = expf(l) * st.inv_p;
-        o[row.shift + v] = float_logit<T>((st.mass * q - p) * inv_t * g);
-      }
+    auto write = [&](int v, float l, float z) {
+      const float q = expf((z - st.m_all) * inv_t) * st.inv_z;
+      const float p = expf(l) * st.inv_p;
+      o[row.shift + v] = float_logit<T>((st.mass * q - p) * inv_t * g);
+    };
+    if (lists) {
+#pragma unroll
+      for (int j = 0; j < kEntries; ++j)
+        if (e.v[j] >= 0 && mine(e.v[j])) write(e.v[j], e.lp[j], e.z[j]);
+    }
+    for (int i = kChunk + tid; i < K; i += kDisThreads)
+      if (present(ids[i], lp[i], in.vocab) && mine(ids[i])) write(ids[i], lp[i], top_z[i]);
   }
 }
 
@@ -485,7 +546,8 @@ int launch_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, 
          tiles >= peers * 2 * kStreamWarps)
     peers *= 2;
   const int slice = (tiles + peers - 1) / peers * kTile;
-  const uint32_t smem = (WHAT & kForward) ? (uint32_t)slice / 8u : 0u;
+  const uint32_t smem = kRingBytes + ((WHAT & kForward) ? (uint32_t)slice / 8u : 0u) +
+                        ((WHAT & kBackward) ? 4u * (uint32_t)K : 0u);
   if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
   if (in.rows > 0x7fffffff / peers) return RANS_ERR_ARG;
   cudaLaunchConfig_t cfg = {};

@@ -152,15 +152,21 @@ struct Row {
 // anywhere), a lane joins its vector's tail to the next lane's head and stores
 // that; what is left at the two ends goes out as N single elements, a lane
 // each.  `whole`: every element of the lane's vector is to be stored; else
-// those with from <= u < to are, one by one.
-template <typename T>
+// those with from <= u < to are, one by one.  STREAM: the result is not to push
+// anything out of L2.
+template <bool STREAM>
+__device__ __forceinline__ void store16(void *at, uint4 p) {
+  if (STREAM) __stcs(static_cast<uint4 *>(at), p);
+  else *static_cast<uint4 *>(at) = p;
+}
+template <bool STREAM = false, typename T>
 __device__ __forceinline__ void store_vectors(T *o, int u0, uint4 p, bool whole, int from, int to) {
   constexpr int N = VecOf<T>::N;
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
   const int past = (int)((reinterpret_cast<uintptr_t>(o + u0) & 15) / sizeof(T));
   if (past == 0 && whole) {
-    *reinterpret_cast<uint4 *>(o + u0) = p;
+    store16<STREAM>(o + u0, p);
     return;
   }
   if (past == 0 || !__all_sync(kAll, whole)) {
@@ -204,7 +210,7 @@ __device__ __forceinline__ void store_vectors(T *o, int u0, uint4 p, bool whole,
 #pragma unroll
     for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
   }
-  if (lane < 31) *reinterpret_cast<uint4 *>(o + u0 + skip) = make_uint4(w[0], w[1], w[2], w[3]);
+  if (lane < 31) store16<STREAM>(o + u0 + skip, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // ---------------------------------------------------------- adjustments --
