@@ -37,7 +37,7 @@ def _place(dev, stream):
         if stream.device.index != dev:
             raise ValueError("stream on %s, tensors on cuda:%d" % (stream.device, dev))
         return torch.cuda.stream(stream)
-    if dev != torch.cuda.current_device():
+    if dev != torch._C._cuda_getDevice():
         return torch.cuda.device(dev)
     return _no_context
 
@@ -98,38 +98,51 @@ def _ref(adjust, rows):
 
 
 def rans_adjust_logits(logits, adjust, out, stream=None):
-    rows, o = _rows(logits), _rows(out, "out")
+    rows = _rows(logits)
+    with _place(rows[0], stream):
+        return _adjust(rows, logits, adjust, out)
+
+
+def _adjust(rows, logits, adjust, out):
+    o = _rows(out, "out")
     if o[:3] != rows[:3]:
         raise ValueError("out: a tensor of the logits' shape on their device")
-    with _place(rows[0], stream):
-        return L.lib().rans_adjust_logits(_packed(logits, rows), _ref(adjust, rows),
-                                          out.data_ptr(), o[3], o[4], _raw_stream(rows[0]))
+    return L.lib().rans_adjust_logits(_packed(logits, rows), _ref(adjust, rows),
+                                      out.data_ptr(), o[3], o[4], _raw_stream(rows[0]))
 
 
 def rans_token_intervals(logits, adjust, tokens, starts, freqs, status, stream=None):
     rows = _rows(logits)
+    with _place(rows[0], stream):
+        return _intervals(rows, logits, adjust, tokens, starts, freqs, status)
+
+
+def _intervals(rows, logits, adjust, tokens, starts, freqs, status):
     dev, n = rows[:2]
     t = _tensor(tokens, torch.int32, (n,), dev, "tokens")
     s = _tensor(starts, torch.int32, (n,), dev, "starts")
     f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
-    with _place(dev, stream):
-        return L.lib().rans_token_intervals(_packed(logits, rows), _ref(adjust, rows), t, s, f,
-                                            _status(status, dev).data_ptr(), _raw_stream(dev))
+    return L.lib().rans_token_intervals(_packed(logits, rows), _ref(adjust, rows), t, s, f,
+                                        _status(status, dev).data_ptr(), _raw_stream(dev))
 
 
 def rans_encode_intervals(starts, freqs, n, chunking, out, stream_offsets, workspace,
                           stream=None):
+    S = L.rans_num_streams(chunking, n)
+    with _place(starts.get_device(), stream):
+        return _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace)
+
+
+def _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace):
     dev = starts.get_device()
     s = _tensor(starts, torch.int32, (n,), dev, "starts")
     f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
     o = _tensor(out, torch.uint8, None, dev, "out")
     w = _tensor(workspace, torch.uint8, None, dev, "workspace")
-    S = L.rans_num_streams(chunking, n)
     offs = _tensor(stream_offsets, torch.int64, (S + 1,) if S >= 0 else None, dev,
                    "stream_offsets")
-    with _place(dev, stream):
-        return L.lib().rans_encode_intervals(s, f, n, ctypes.byref(chunking.c), o, out.numel(),
-                                             offs, w, workspace.numel(), _raw_stream(dev))
+    return L.lib().rans_encode_intervals(s, f, n, ctypes.byref(chunking.c), o, out.numel(),
+                                         offs, w, workspace.numel(), _raw_stream(dev))
 
 
 def _streams(data, stream_offsets):
@@ -154,6 +167,13 @@ def rans_token_states(data, stream_offsets, states, status, stream=None):
 def rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states_in, states_out,
                        tokens, status, stream=None):
     rows = _rows(logits)
+    with _place(rows[0], stream):
+        return _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in,
+                       states_out, tokens, status)
+
+
+def _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in, states_out,
+            tokens, status):
     dev, S, d, o = _streams(data, stream_offsets)
     if dev != rows[0]:
         raise ValueError("data on cuda:%d, logits on cuda:%d" % (dev, rows[0]))
@@ -163,10 +183,9 @@ def rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states_
     a = _tensor(states_in, torch.int64, (S, 2), dev, "states")
     b = _tensor(states_out, torch.int64, (S, 2), dev, "states_out")
     t = _tensor(tokens, torch.int32, (n,), dev, "tokens")
-    with _place(dev, stream):
-        return L.lib().rans_decode_tokens(
-            _packed(logits, rows), _ref(adjust, rows), d, data.numel(), o, S, ids, a, b, t,
-            _status(status, dev).data_ptr(), _raw_stream(dev))
+    return L.lib().rans_decode_tokens(
+        _packed(logits, rows), _ref(adjust, rows), d, data.numel(), o, S, ids, a, b, t,
+        _status(status, dev).data_ptr(), _raw_stream(dev))
 
 
 def rans_token_states_finish(stream_offsets, states, status, stream=None):
@@ -179,9 +198,9 @@ def rans_token_states_finish(stream_offsets, states, status, stream=None):
                                                 _raw_stream(dev))
 
 
-def _teacher(logits, ids, logprobs):
+def _teacher(logits, ids, logprobs, rows=None):
     """(rows of the logits, K, the teacher's two addresses)."""
-    rows = _rows(logits)
+    rows = rows or _rows(logits)
     if not isinstance(ids, torch.Tensor) or ids.dim() != 2 or not 1 <= ids.shape[1] <= MAX_TOP:
         raise ValueError("ids: a tensor [rows, K], K from 1 to %d" % MAX_TOP)
     K = ids.shape[1]
@@ -223,15 +242,21 @@ def rans_distill_backward(logits, ids, logprobs, inv_temperature, stats, grad_lo
 
 def rans_distill(logits, ids, logprobs, inv_temperature, tail, grad_losses, losses, grad, status,
                  stream=None):
-    rows, K, i, lp = _teacher(logits, ids, logprobs)
+    rows = _rows(logits)
+    with _place(rows[0], stream):
+        return _both(rows, logits, ids, logprobs, inv_temperature, tail, grad_losses, losses,
+                     grad, status)
+
+
+def _both(rows, logits, ids, logprobs, inv_temperature, tail, grad_losses, losses, grad, status):
+    _, K, i, lp = _teacher(logits, ids, logprobs, rows)
     dev, n = rows[:2]
     w = _tensor(grad_losses, torch.float32, (n,), dev, "weights")
     o = _tensor(losses, torch.float32, (n,), dev, "losses")
     g, step = _grad_of(rows, grad)
-    with _place(dev, stream):
-        return L.lib().rans_distill(_packed(logits, rows), i, lp, K, inv_temperature, int(tail),
-                                    w, o, g, step, _status(status, dev).data_ptr(),
-                                    _raw_stream(dev))
+    return L.lib().rans_distill(_packed(logits, rows), i, lp, K, inv_temperature, int(tail),
+                                w, o, g, step, _status(status, dev).data_ptr(),
+                                _raw_stream(dev))
 
 
 # ----------------------------------------------------------------- helpers --
@@ -359,11 +384,11 @@ class LogitAdjust:
 def adjust_logits(logits, adjust, out=None, dtype=None, stream=None):
     """Adjusted logits (penalties, biases, temperature, mask) for a sampler, in
     the logits' type or `dtype`; out may be the logits themselves."""
-    if out is None:
-        dev = _rows(logits)[0]
-        with _place(dev, stream):
-            out = torch.empty(logits.shape, dtype=dtype or logits.dtype, device=logits.device)
-    L.check(rans_adjust_logits(logits, adjust, out, stream), "adjust_logits")
+    rows = _rows(logits)
+    with _place(rows[0], stream):
+        if out is None:
+            out = logits.new_empty(rows[1:3], dtype=dtype)
+        L.check(_adjust(rows, logits, adjust, out), "adjust_logits")
     return out
 
 
@@ -371,15 +396,14 @@ def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status
                     stream=None):
     """(starts, freqs), int32 [rows]: each row's interval of its token at
     TOKEN_PRECISION bits.  Rows with token -1 are skipped."""
-    dev, n = _rows(logits)[:2]
-    with _place(dev, stream):
+    rows = _rows(logits)
+    with _place(rows[0], stream):
         if starts is None:
-            starts = torch.empty(n, dtype=torch.int32, device=logits.device)
+            starts = logits.new_empty(rows[1], dtype=torch.int32)
         if freqs is None:
-            freqs = torch.empty(n, dtype=torch.int32, device=logits.device)
-        status = _status(status, dev)
-    L.check(rans_token_intervals(logits, adjust, tokens, starts, freqs, status, stream),
-            "token_intervals")
+            freqs = logits.new_empty(rows[1], dtype=torch.int32)
+        L.check(_intervals(rows, logits, adjust, tokens, starts, freqs, status),
+                "token_intervals")
     return starts, freqs
 
 
@@ -387,21 +411,18 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
     """(buffer, stream_offsets[S + 1], workspace): like encode_with_indexes;
     the coded bytes are buffer[:stream_offsets[-1]], device errors
     rans_get_status(workspace).  ws: a workspace to reuse."""
-    n, dev = starts.numel(), starts.device
+    n = starts.numel()
     S = L.rans_num_streams(chunking, n)
     if S < 0:
         L.check(int(S), "num_streams")
     with _place(starts.get_device(), stream):
         if ws is None:
             # torch's blocks are aligned to 512 bytes, as the workspace has to be to 256
-            ws = torch.empty(L.rans_encode_workspace_bytes(chunking, n), dtype=torch.uint8,
-                             device=dev)
+            ws = starts.new_empty(L.rans_encode_workspace_bytes(chunking, n), dtype=torch.uint8)
         if out is None:
-            out = torch.empty(L.rans_max_compressed_bytes(chunking, n), dtype=torch.uint8,
-                              device=dev)
-        offsets = torch.empty(S + 1, dtype=torch.int64, device=dev)
-    L.check(rans_encode_intervals(starts, freqs, n, chunking, out, offsets, ws, stream),
-            "encode_intervals")
+            out = starts.new_empty(L.rans_max_compressed_bytes(chunking, n), dtype=torch.uint8)
+        offsets = starts.new_empty(S + 1, dtype=torch.int64)
+        L.check(_encode(starts, freqs, n, S, chunking, out, offsets, ws), "encode_intervals")
     return out, offsets, ws
 
 
@@ -420,40 +441,48 @@ def decode_tokens(logits, data, stream_offsets, states, adjust=None, stream_ids=
     """One decoding step: (tokens int32 [rows], new states).  Row r is the next
     position of stream stream_ids[r] (default r); out_states may be `states`.
     Rows with stream id -1 are skipped; without `tokens` they read -1."""
-    dev, n = _rows(logits)[:2]
-    with _place(dev, stream):
+    rows = _rows(logits)
+    n = rows[1]
+    with _place(rows[0], stream):
         if out_states is None:
             every = stream_ids is None and n == stream_offsets.numel() - 1
             out_states = torch.empty_like(states) if every else states.clone()
         if tokens is None:
-            tokens = torch.empty(n, dtype=torch.int32, device=logits.device) \
-                if stream_ids is None else \
-                torch.full((n,), -1, dtype=torch.int32, device=logits.device)
-        status = _status(status, dev)
-    L.check(rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states,
-                               out_states, tokens, status, stream), "decode_tokens")
+            tokens = logits.new_empty(n, dtype=torch.int32) if stream_ids is None else \
+                logits.new_full((n,), -1, dtype=torch.int32)
+        L.check(_decode(rows, logits, adjust, data, stream_offsets, stream_ids, states,
+                        out_states, tokens, status), "decode_tokens")
     return tokens, out_states
 
 
 class _Distill(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, ids, logprobs, inv_temperature, tail, status):
-        n, dev = logits.shape[0], logits.device
-        losses = torch.empty(n, dtype=torch.float32, device=dev)
-        stats = torch.empty(n, 8, dtype=torch.float32, device=dev)
-        L.check(rans_distill_forward(logits, ids, logprobs, inv_temperature, tail, losses, stats,
-                                     status), "distill_forward")
+        rows, K, i, lp = _teacher(logits, ids, logprobs)
+        dev, n = rows[:2]
+        losses = logits.new_empty(n, dtype=torch.float32)
+        stats = logits.new_empty((n, 8), dtype=torch.float32)
+        L.check(L.lib().rans_distill_forward(
+            _packed(logits, rows), i, lp, K, inv_temperature, int(tail), losses.data_ptr(),
+            stats.data_ptr(), _status(status, dev).data_ptr(), _raw_stream(dev)),
+            "distill_forward")
         ctx.save_for_backward(logits, ids, logprobs, stats)
-        ctx.inv_temperature = inv_temperature
+        ctx.inv_temperature, ctx.rows = inv_temperature, rows
         return losses
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_losses):
         logits, ids, logprobs, stats = ctx.saved_tensors
-        grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        L.check(rans_distill_backward(logits, ids, logprobs, ctx.inv_temperature, stats,
-                                      grad_losses.contiguous(), grad), "distill_backward")
+        rows = ctx.rows
+        dev, n, v = rows[:3]
+        grad = logits.new_empty((n, v))
+        g = grad_losses.contiguous()
+        with _place(dev, None):
+            L.check(L.lib().rans_distill_backward(
+                _packed(logits, rows), ids.data_ptr(), logprobs.data_ptr(), ids.shape[1],
+                ctx.inv_temperature, stats.data_ptr(), g.data_ptr(), grad.data_ptr(), v,
+                _raw_stream(dev)), "distill_backward")
         return grad, None, None, None, None, None
 
 
@@ -464,10 +493,10 @@ def distill_loss(logits, ids, logprobs, temperature=1.0, tail=True, status=None)
     remaining mass is one more bucket; else its list is renormalised.  The
     teacher's probabilities take no gradient."""
     inv = _positive(1.0 / _positive(temperature, "temperature"), "1 / temperature")
-    dev = _rows(logits)[0]
-    with _place(dev, None):
-        return _Distill.apply(logits, ids, logprobs.detach(), inv, bool(tail),
-                              _status(status, dev))
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise ValueError("logits: a CUDA tensor [rows, vocab]")
+    with _place(logits.get_device(), None):
+        return _Distill.apply(logits, ids, logprobs.detach(), inv, tail, status)
 
 
 def distill_loss_and_grad(logits, ids, logprobs, weights, temperature=1.0, tail=True, grad=None,
@@ -476,12 +505,11 @@ def distill_loss_and_grad(logits, ids, logprobs, weights, temperature=1.0, tail=
     training loops that know the rows' weights; no autograd graph is built.
     grad may be the logits themselves."""
     inv = _positive(1.0 / _positive(temperature, "temperature"), "1 / temperature")
-    dev, n = _rows(logits)[:2]
-    with _place(dev, stream):
-        losses = torch.empty(n, dtype=torch.float32, device=logits.device)
+    rows = _rows(logits)
+    with _place(rows[0], stream):
+        losses = logits.new_empty(rows[1], dtype=torch.float32)
         if grad is None:
-            grad = torch.empty(logits.shape, dtype=logits.dtype, device=logits.device)
-        status = _status(status, dev)
-    L.check(rans_distill(logits, ids, logprobs, inv, tail, weights, losses, grad, status, stream),
-            "distill")
+            grad = logits.new_empty(rows[1:3])
+        L.check(_both(rows, logits, ids, logprobs, inv, tail, weights, losses, grad, status),
+                "distill")
     return losses, grad
