@@ -648,18 +648,9 @@ RANS_API int rans_encode_intervals(const uint32_t *starts, const uint32_t *freqs
   if (g.kind != RANS_CHUNK_CONTIG && g.kind != RANS_CHUNK_EXPLICIT) return RANS_ERR_ARG;
   if (g.W != 1 || g.ib_shift != 0 || g.fmt != RANS_FMT_RANS64 || g.alias) return RANS_ERR_ARG;
   if (workspace_bytes < enc_ws_bytes(g)) return RANS_ERR_CAPACITY;
-  cudaStream_t s = as_stream(stream);
-  char *ws = reinterpret_cast<char *>(workspace);
-  int32_t *status = reinterpret_cast<int32_t *>(ws);
-  uint64_t *lens = reinterpret_cast<uint64_t *>(ws + kWsHeader);
-  char *scratch = ws + kWsHeader + lens_bytes(g);
-  if (cudaMemsetAsync(ws, 0, kWsHeader + 8ull * (uint64_t)g.S, s) != cudaSuccess)
-    return RANS_ERR_CUDA;
-  if (g.S > 0) {
-    st = rb::launch_encode_intervals(starts, freqs, g, scratch, lens, status, s);
-    if (st) return st;
-  }
-  return rb::launch_compact(g, scratch, lens, out, out_capacity, stream_offsets, status, s);
+  return rb::launch_encode_intervals(starts, freqs, g, reinterpret_cast<char *>(workspace),
+                                     kWsHeader, lens_bytes(g), out, out_capacity, stream_offsets,
+                                     as_stream(stream));
 }
 
 RANS_API int rans_token_states(const uint8_t *in, uint64_t in_bytes,

@@ -542,7 +542,7 @@ int launch_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, 
   // blocks per row: one, while the rows alone fill the SMs (two blocks each);
   // else as many as still leave every warp a tile
   int peers = 1;
-  while (peers < kDisCluster && in.rows * peers * 2 <= 2 * num_sms(dev) &&
+  while (peers < kDisCluster && in.rows * peers * 2 <= 4 * num_sms(dev) &&
          tiles >= peers * 2 * kStreamWarps)
     peers *= 2;
   const int slice = (tiles + peers - 1) / peers * kTile;

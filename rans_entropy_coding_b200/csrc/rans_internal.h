@@ -67,8 +67,8 @@ int launch_debug_divide(const uint64_t *x, const uint32_t *f, int64_t n, uint64_
 // Adjusted logits into out (dtype RANS_LOGITS_*).
 int launch_adjust(const rans_logits &in, const rans_adjust &adj, void *out, int out_dtype,
                   int64_t out_stride, cudaStream_t st);
-// One token's interval per row; rows of one decoding step; streams of
-// intervals into scratch slots (lengths in lens, as launch_encode); decoder
+// One token's interval per row; rows of one decoding step; packed streams of
+// intervals (ws: header with the status word, lengths, scratch slots); decoder
 // states of S streams and their check at the end.
 int launch_token_intervals(const rans_logits &in, const rans_adjust &adj, const int32_t *tokens,
                            uint32_t *starts, uint32_t *freqs, int32_t *status, cudaStream_t st);
@@ -78,7 +78,8 @@ int launch_decode_tokens(const rans_logits &in, const rans_adjust &adj, const ui
                          uint64_t *states_out, int32_t *tokens, int32_t *status,
                          cudaStream_t st);
 int launch_encode_intervals(const uint32_t *starts, const uint32_t *freqs, const Geom &g,
-                            char *scratch, uint64_t *lens, int32_t *status, cudaStream_t st);
+                            char *ws, uint64_t header_bytes, uint64_t lens_bytes, uint8_t *out,
+                            uint64_t capacity, uint64_t *offsets, cudaStream_t st);
 int launch_token_states(const uint8_t *in, uint64_t in_bytes, const uint64_t *offsets, int64_t S,
                         uint64_t *states, int32_t *status, cudaStream_t st);
 int launch_token_finish(const uint64_t *offsets, int64_t S, const uint64_t *states,

@@ -674,73 +674,176 @@ __global__ void __launch_bounds__(kRowThreads, 2)
 // --------------------------------------------------------------- streams --
 // One warp per stream.  The states of a stream follow from one another, so the
 // warp's lanes carry the same state; what does not depend on it is done 32
-// tokens at a time, one per lane: loading the interval and turning the
-// division by its freq into a product.  q = floor(x / f) for x < 2^63 is the
-// high part of x times the ceiling of 2^(63 + l) / f, l = ceil(log2 f), shifted
-// right by l (Granlund and Montgomery, "Division by invariant integers using
-// multiplication", 1994: exact since the factor exceeds 2^(63 + l) / f by less
-// than 2^l / f).
+// tokens at a time, one per lane, a group ahead: loading the interval and
+// turning the division by its freq into a product.  q = floor(x / f) for
+// x < 2^63 is the high part of x times the ceiling of 2^(63 + l) / f,
+// l = ceil(log2 f), shifted right by l (Granlund and Montgomery, "Division by
+// invariant integers using multiplication", 1994: exact since the factor
+// exceeds 2^(63 + l) / f by less than 2^l / f).  What bounds the kernel is the
+// chain of a step: compare, select, 64-bit product, shift, product, add.
 constexpr int kIntervalWarps = 4;
+constexpr int kFusedStreams = 16;  // most streams of the one-block form
 
-__global__ void __launch_bounds__(kIntervalWarps * 32)
-    encode_intervals_kernel(const uint32_t *__restrict__ starts,
-                            const uint32_t *__restrict__ freqs, Geom g, char *scratch,
-                            uint64_t *lens, int32_t *status) {
-  const int lane = threadIdx.x & 31;
-  const int64_t s = (int64_t)blockIdx.x * kIntervalWarps + (threadIdx.x >> 5);
-  if (s >= g.S) return;
-  const StreamDesc d = stream_desc(g, s);
-  // scratch slots are laid out from the first stream's start on
-  if (!d.ok || (g.kind == RANS_CHUNK_EXPLICIT && (g.starts[0] < 0 || d.base < g.starts[0]))) {
-    if (lane == 0) report(status, RANS_ERR_ARG, s);
-    return;
+// What a step needs of its token.
+struct Step {
+  uint64_t inv;    // ceil(2^(63 + l) / freq)
+  uint32_t freq;
+  uint32_t start;  // | l << 24
+};
+static_assert(sizeof(Step) == 16, "one shared-memory load");
+
+// floor(a 2^k / f) for f <= 2^24 and a quotient of at most 2^32, by a double
+// quotient whose error is far below 1, and the remainder.
+__device__ __forceinline__ uint64_t quotient(double a, uint64_t n, uint32_t f, double r,
+                                             uint64_t &rem) {
+  uint64_t q = (uint64_t)(a * r);
+  int64_t left = (int64_t)(n - q * f);
+  if (left < 0) {
+    --q;
+    left += f;
+  } else if (left >= (int64_t)f) {
+    ++q;
+    left -= f;
   }
-  uint32_t *end = reinterpret_cast<uint32_t *>(scratch + slot_end(g, d, s));
+  rem = (uint64_t)left;
+  return q;
+}
+
+__device__ __forceinline__ Step make_step(uint32_t start, uint32_t f) {
+  const int l = f > 1 ? 32 - __clz(f - 1) : 0;
+  const double r = 1.0 / (double)f;
+  // 2^(63 + l) / f in two digits of 2^32
+  const uint64_t top = 1ull << (31 + l);
+  uint64_t r1, r2;
+  const uint64_t q1 = quotient((double)top, top, f, r, r1);
+  const uint64_t low = r1 << 32;
+  const uint64_t q2 = quotient((double)low, low, f, r, r2);
+  return {(q1 << 32) + q2 + (r2 ? 1u : 0u), f, start | (uint32_t)l << 24};
+}
+
+// Codes stream s into its scratch slot; returns its words (0: a bad extent).
+__device__ __forceinline__ int64_t encode_stream(const uint32_t *__restrict__ starts,
+                                                 const uint32_t *__restrict__ freqs,
+                                                 const Geom &g, const StreamDesc &d, int64_t s,
+                                                 uint32_t *end, Step *steps, int lane,
+                                                 int32_t *status) {
   uint64_t x = kL;
   int64_t used = 0;
-  for (int64_t hi = d.n; hi > 0; hi -= 32) {
-    const int count = hi < 32 ? (int)hi : 32;
-    uint32_t st = 0, f = 1;
-    if (lane < count) {
+  auto load = [&](int64_t hi, uint32_t &st, uint32_t &f) {
+    st = 0;
+    f = 1;
+    if (lane < hi) {
       st = starts[d.base + hi - 1 - lane];
       f = freqs[d.base + hi - 1 - lane];
-      if (f == 0 || f > kTokTotal || st > kTokTotal - f) {
-        report(status, f == 0 ? RANS_ERR_ZERO_FREQ : RANS_ERR_RANGE, s);
-        st = 0;
-        f = 1;
-      }
     }
-    const int l = f > 1 ? 32 - __clz(f - 1) : 0;
-    const uint64_t top = 1ull << (31 + l);
-    const uint64_t q1 = top / f, r1 = top - q1 * f;
-    const uint64_t low = r1 << 32;
-    const uint64_t q2 = low / f;
-    const uint64_t inv = (q1 << 32) + q2 + (low != q2 * f ? 1 : 0);
+  };
+  auto prepare = [&](uint32_t st, uint32_t f) {
+    if (f == 0 || f > kTokTotal || st > kTokTotal - f) {
+      report(status, f == 0 ? RANS_ERR_ZERO_FREQ : RANS_ERR_RANGE, s);
+      st = 0;
+      f = 1;
+    }
+    return make_step(st, f);
+  };
+  uint32_t st, f;
+  load(d.n, st, f);
+  Step mine = prepare(st, f);
+  load(d.n - 32, st, f);
+  for (int64_t hi = d.n; hi > 0; hi -= 32) {
+    const int count = hi < 32 ? (int)hi : 32;
+    __syncwarp();
+    steps[lane] = mine;
+    __syncwarp();
     uint32_t word = 0;
     int emitted = 0;
-    for (int i = 0; i < count; ++i) {
-      const uint32_t fi = __shfl_sync(kFull, f, i);
-      const uint32_t si = __shfl_sync(kFull, st, i);
-      const int li = __shfl_sync(kFull, l, i);
-      const uint64_t mi = __shfl_sync(kFull, inv, i);
+    auto take = [&](const Step &p) {
       // x >= 2^39 f, in the high words
-      const bool emit = (uint32_t)(x >> 32) >= fi << 7;
+      const bool emit = (uint32_t)(x >> 32) >= p.freq << 7;
       if (emit) {
         if (lane == emitted) word = (uint32_t)x;
         x >>= 32;
         ++emitted;
       }
-      const uint64_t q = __umul64hi(x + x, mi) >> li;
-      x += (uint64_t)si + q * (uint64_t)(kTokTotal - fi);
+      const uint64_t q = __umul64hi(x + x, p.inv) >> (p.start >> 24);
+      x += (uint64_t)(p.start & (kTokTotal - 1)) + q * (uint64_t)(kTokTotal - p.freq);
+    };
+    if (count == 32) {
+#pragma unroll 8
+      for (int i = 0; i < 32; ++i) take(steps[i]);
+    } else {
+      for (int i = 0; i < count; ++i) take(steps[i]);
     }
     if (lane < emitted) end[-1 - used - lane] = word;
     used += emitted;
+    mine = prepare(st, f);
+    load(hi - 64, st, f);
   }
   if (lane == 0) {
     end[-1 - used] = (uint32_t)(x >> 32);
     end[-2 - used] = (uint32_t)x;
-    lens[s] = 4ull * (uint64_t)(used + 2);
   }
+  return used + 2;
+}
+
+// Whether a stream's extent lies within the scratch (slots are laid out from
+// the first stream's start on).
+__device__ __forceinline__ bool extent_ok(const Geom &g, const StreamDesc &d, int64_t s,
+                                          int lane, int32_t *status) {
+  const bool ok =
+      d.ok && (g.kind != RANS_CHUNK_EXPLICIT || (g.starts[0] >= 0 && d.base >= g.starts[0]));
+  if (!ok && lane == 0) report(status, RANS_ERR_ARG, s);
+  return ok;
+}
+
+__global__ void __launch_bounds__(kIntervalWarps * 32)
+    encode_intervals_kernel(const uint32_t *__restrict__ starts,
+                            const uint32_t *__restrict__ freqs, Geom g, char *scratch,
+                            uint64_t *lens, int32_t *status) {
+  __shared__ Step steps[kIntervalWarps][32];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  const int64_t s = (int64_t)blockIdx.x * kIntervalWarps + wid;
+  if (s >= g.S) return;
+  const StreamDesc d = stream_desc(g, s);
+  if (!extent_ok(g, d, s, lane, status)) return;
+  uint32_t *end = reinterpret_cast<uint32_t *>(scratch + slot_end(g, d, s));
+  const int64_t words =
+      encode_stream(starts, freqs, g, d, s, end, steps[wid], lane, status);
+  if (lane == 0) lens[s] = 4ull * (uint64_t)words;
+}
+
+// Few streams in one block: status, streams, offsets and compaction in one
+// launch (three otherwise, and a memset).
+__global__ void __launch_bounds__(kFusedStreams * 32)
+    encode_fused_kernel(const uint32_t *__restrict__ starts, const uint32_t *__restrict__ freqs,
+                        Geom g, char *scratch, uint8_t *out, uint64_t capacity,
+                        uint64_t *offsets, int32_t *status) {
+  __shared__ Step steps[kFusedStreams][32];
+  __shared__ uint64_t lens[kFusedStreams];
+  const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5;
+  if (threadIdx.x < (int)(sizeof(StatusWord) / 4)) status[threadIdx.x] = 0;
+  __threadfence_block();
+  __syncthreads();
+  const StreamDesc d = stream_desc(g, wid);
+  uint32_t *end = nullptr;
+  int64_t words = 0;
+  if (extent_ok(g, d, wid, lane, status)) {
+    end = reinterpret_cast<uint32_t *>(scratch + slot_end(g, d, wid));
+    words = encode_stream(starts, freqs, g, d, wid, end, steps[wid], lane, status);
+  }
+  if (lane == 0) lens[wid] = 4ull * (uint64_t)words;
+  __syncthreads();
+  uint64_t off = 0;
+  for (int w = 0; w < wid; ++w) off += lens[w];
+  const uint64_t to = off + 4ull * (uint64_t)words;
+  if (lane == 0) {
+    offsets[wid + 1] = to;
+    if (wid == 0) offsets[0] = 0;
+    if (wid == (int)g.S - 1 && to > capacity) report(status, RANS_ERR_CAPACITY, -1);
+  }
+  if (to > capacity) return;
+  __syncwarp();  // the stream's words, written by the warp's lanes
+  uint32_t *dst = reinterpret_cast<uint32_t *>(out + off);
+  for (int64_t i = lane; i < words; i += 32) dst[i] = end[i - words];
 }
 
 __global__ void token_states_kernel(const uint8_t *in, uint64_t in_bytes,
@@ -858,12 +961,26 @@ int launch_decode_tokens(const rans_logits &in, const rans_adjust &adj, const ui
 }
 
 int launch_encode_intervals(const uint32_t *starts, const uint32_t *freqs, const Geom &g,
-                            char *scratch, uint64_t *lens, int32_t *status, cudaStream_t st) {
-  const int64_t blocks = (g.S + kIntervalWarps - 1) / kIntervalWarps;
-  if (blocks > 0x7fffffff) return RANS_ERR_ARG;
-  encode_intervals_kernel<<<(unsigned)blocks, kIntervalWarps * 32, 0, st>>>(
-      starts, freqs, g, scratch, lens, status);
-  return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
+                            char *ws, uint64_t header_bytes, uint64_t lens_bytes, uint8_t *out,
+                            uint64_t capacity, uint64_t *offsets, cudaStream_t st) {
+  int32_t *status = reinterpret_cast<int32_t *>(ws);
+  uint64_t *lens = reinterpret_cast<uint64_t *>(ws + header_bytes);
+  char *scratch = ws + header_bytes + lens_bytes;
+  if (g.S > 0 && g.S <= kFusedStreams) {
+    encode_fused_kernel<<<1, (unsigned)g.S * 32, 0, st>>>(starts, freqs, g, scratch, out,
+                                                          capacity, offsets, status);
+    return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
+  }
+  if (cudaMemsetAsync(ws, 0, header_bytes + 8ull * (uint64_t)g.S, st) != cudaSuccess)
+    return RANS_ERR_CUDA;
+  if (g.S > 0) {
+    const int64_t blocks = (g.S + kIntervalWarps - 1) / kIntervalWarps;
+    if (blocks > 0x7fffffff) return RANS_ERR_ARG;
+    encode_intervals_kernel<<<(unsigned)blocks, kIntervalWarps * 32, 0, st>>>(
+        starts, freqs, g, scratch, lens, status);
+    if (cudaGetLastError() != cudaSuccess) return RANS_ERR_CUDA;
+  }
+  return launch_compact(g, scratch, lens, out, capacity, offsets, status, st);
 }
 
 int launch_token_states(const uint8_t *in, uint64_t in_bytes, const uint64_t *offsets, int64_t S,

@@ -337,6 +337,25 @@ def test_streams_of_intervals(cuts):
     assert got == [TO.encode(s[a:b], f[a:b]) for a, b in zip(cuts, cuts[1:])]
 
 
+@pytest.mark.parametrize("S", [1, 16, 17, 40])
+def test_long_streams(S):
+    """Thousands of divisors, on both sides of the one-block form's 16 streams;
+    reusing a workspace that holds an old error."""
+    n = 6000
+    s, f = random_intervals(n, np.random.default_rng(S))
+    f[::7] = np.random.default_rng(1).integers(1, 1 << 24, f[::7].size)
+    s = np.minimum(s, (1 << 24) - f)
+    ch = rb.Chunking.contig(S)
+    bad = f.copy()
+    bad[5] = 0
+    _, _, ws = rb.encode_intervals(cuda32(s), cuda32(bad), ch)
+    out, offs, ws = rb.encode_intervals(cuda32(s), cuda32(f), ch, ws=ws)
+    status_ok(ws)
+    per = -(-n // S)
+    assert rb.to_byte_strings(out, offs) == [
+        TO.encode(s[k * per:(k + 1) * per], f[k * per:(k + 1) * per]) for k in range(S)]
+
+
 def test_streams_extremes_and_contiguous_chunks():
     for f0 in (1, 2, 3, (1 << 24) - 1, 1 << 24):
         s, f = np.zeros(100, np.int64), np.full(100, f0)
