@@ -484,7 +484,6 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       const float factor = st.rest * g;
       const uint64_t c2 = pair(c, c), off2 = pair(-st.offset, -st.offset);
       const uint64_t factor2 = pair(factor, factor);
-      const bool aligned = (reinterpret_cast<uintptr_t>(o) & 15) == 0;
       if constexpr (WHAT == kBackward) {
         send(last, 0);
         send(last - step, 1);
@@ -495,7 +494,6 @@ __global__ void __launch_bounds__(kDisThreads, 4)
         send(u - 2 * step, stage);
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
-          const int u0 = u + k * kVecRow + lane * N;
           float z[N];
           unpack16(q[k], z, T());
 #pragma unroll
@@ -507,11 +505,9 @@ __global__ void __launch_bounds__(kDisThreads, 4)
             z[i] = f.x;
             z[i + 1] = f.y;
           }
-          const uint4 p = pack16(z, T());
-          if (aligned && inside(u)) store16<true>(o + u0, p);
-          else if (u0 - lane * N < hi)
-            store_vectors<true>(o, u0, p, row.whole(u0), row.shift, row.end());
+          q[k] = pack16(z, T());
         }
+        store_tile<true>(o, u, q, inside(u), row.shift, hi);
       }
     }
     __syncthreads();  // the listed tokens' gradients go over what stands there

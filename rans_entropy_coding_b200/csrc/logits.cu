@@ -36,44 +36,45 @@ __global__ void __launch_bounds__(TOUCH ? kAdjThreads + kTableThreads : kAdjThre
   O *o = out + r * out_stride - row.shift;  // element u goes to o[u]
 
   auto stream = [&](int from, int to) {
-    for (int u = from; u < to; u += kTile) {
+    constexpr int kWarpTile = 32 * kAdjVecs * N;
+    for (int u = from + (tid >> 5) * kWarpTile; u < to; u += kTile) {
+      const bool inside = u >= row.shift && u + kWarpTile <= row.end();
       uint4 q[kAdjVecs];
       uint32_t ok[kAdjVecs];
 #pragma unroll
       for (int k = 0; k < kAdjVecs; ++k) {
-        const int u0 = u + (k * kAdjThreads + tid) * N;
-        if (row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
+        const int u0 = u + (32 * k + lane) * N;
+        if (inside || row.whole(u0)) q[k] = *reinterpret_cast<const uint4 *>(row.at0 + u0);
       }
       if constexpr (MASK) {
 #pragma unroll
         for (int k = 0; k < kAdjVecs; ++k)
-          ok[k] = load_mask<N>(mask, words, u + (k * kAdjThreads + tid - lane) * N - row.shift,
-                               lane);
+          ok[k] = load_mask<N>(mask, words, u + 32 * k * N - row.shift, lane);
       }
 #pragma unroll
       for (int k = 0; k < kAdjVecs; ++k) {
-        const int u0 = u + (k * kAdjThreads + tid) * N;
-        if (u0 - lane * N >= to) break;  // (a whole warp's)
-        const bool whole = row.whole(u0);
+        const int u0 = u + (32 * k + lane) * N;
         float z[N];
-        if (whole) unpack16(q[k], z, T());
+        if (inside || row.whole(u0)) unpack16(q[k], z, T());
         else row.load(u0, z, 0.0f);
 #pragma unroll
         for (int i = 0; i < N; ++i) z[i] = __fmul_rn(z[i], inv_temperature);
         if constexpr (MASK) {
-          const uint32_t bits = lane_mask<N>(ok[k], u0 - lane * N - row.shift, lane);
+          const uint32_t bits = lane_mask<N>(ok[k], u + 32 * k * N - row.shift, lane);
 #pragma unroll
           for (int i = 0; i < N; ++i)
             if (!(bits >> i & 1)) z[i] = kNegInf;
         }
         if constexpr (sizeof(O) == sizeof(T)) {
-          store_vectors(o, u0, pack16(z, O()), whole, row.shift, row.end());
+          q[k] = pack16(z, O());
         } else {
 #pragma unroll
           for (int i = 0; i < N; ++i)
-            if (u0 + i >= row.shift && u0 + i < row.end()) o[u0 + i] = float_logit<O>(z[i]);
+            if (u0 + i >= row.shift && u0 + i < to) o[u0 + i] = float_logit<O>(z[i]);
         }
       }
+      if constexpr (sizeof(O) == sizeof(T))
+        store_tile<false>(o, u, q, inside, row.shift, to);
     }
   };
   if constexpr (!TOUCH) {

@@ -146,71 +146,83 @@ struct Row {
   }
 };
 
-// Stores a warp's 32 vectors of packed elements (lane l's at u0 = the warp's
-// first + l * N) to o[u0 ...], any alignment.  Where o's 16-byte boundaries fall
-// inside the vectors (odd vocabularies: the rows of a contiguous result start
-// anywhere), a lane joins its vector's tail to the next lane's head and stores
-// that; what is left at the two ends goes out as N single elements, a lane
-// each.  `whole`: every element of the lane's vector is to be stored; else
-// those with from <= u < to are, one by one.  STREAM: the result is not to push
-// anything out of L2.
+// STREAM: the result is not to push anything out of L2.
 template <bool STREAM>
 __device__ __forceinline__ void store16(void *at, uint4 p) {
   if (STREAM) __stcs(static_cast<uint4 *>(at), p);
   else *static_cast<uint4 *>(at) = p;
 }
-template <bool STREAM = false, typename T>
-__device__ __forceinline__ void store_vectors(T *o, int u0, uint4 p, bool whole, int from, int to) {
+
+// Stores a warp's tile: K vector rows of packed elements, p[k] of lane l at
+// u + (32 k + l) N, to o[u ...], at any alignment.  Where o's 16-byte boundaries
+// fall inside the vectors (odd vocabularies: the rows of a contiguous result
+// start anywhere), a lane joins its vector's tail to the head of the next one,
+// lane 31 to lane 0's of the next vector row, and stores that; what is left at
+// the tile's two ends goes out as N single elements, a lane each.  (Joining each
+// vector row by itself cost 15 instructions an element, half of a kernel's.)
+// `inside`: the whole tile is to be stored; else elements from <= u < to are.
+template <bool STREAM, int K, typename T>
+__device__ __forceinline__ void store_tile(T *o, int u, const uint4 (&p)[K], bool inside, int from,
+                                           int to) {
   constexpr int N = VecOf<T>::N;
   constexpr unsigned kAll = 0xffffffffu;
   const int lane = threadIdx.x & 31;
-  const int past = (int)((reinterpret_cast<uintptr_t>(o + u0) & 15) / sizeof(T));
-  if (past == 0 && whole) {
-    store16<STREAM>(o + u0, p);
-    return;
-  }
-  if (past == 0 || !__all_sync(kAll, whole)) {
-    const T *e = reinterpret_cast<const T *>(&p);
+  const int past = (int)((reinterpret_cast<uintptr_t>(o + u) & 15) / sizeof(T));
+  if (past == 0 || !inside) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (u0 + i >= from && u0 + i < to) o[u0 + i] = e[i];
+    for (int k = 0; k < K; ++k) {
+      const int u0 = u + (32 * k + lane) * N;
+      if (past == 0 && (inside || (u0 >= from && u0 + N <= to))) {
+        store16<STREAM>(o + u0, p[k]);
+      } else {
+        const T *e = reinterpret_cast<const T *>(&p[k]);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+          if (u0 + i >= from && u0 + i < to) o[u0 + i] = e[i];
+      }
+    }
     return;
   }
   const int skip = N - past;  // elements up to the boundary; the same for the row
-  uint32_t w[8] = {p.x, p.y, p.z, p.w};
+  {
+    // lane 0's first `skip` elements and lane 31's last others
+    const uint32_t a[4] = {p[0].x, p[0].y, p[0].z, p[0].w};
+    const uint32_t b[4] = {p[K - 1].x, p[K - 1].y, p[K - 1].z, p[K - 1].w};
+    const int i = lane * (int)sizeof(T) / 4;  // its word
+    uint32_t x = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w[4 + i] = __shfl_down_sync(kAll, w[i], 1);
-  // lane 0's first `skip` elements and lane 31's others, one per lane
-  uint32_t ends[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t a = __shfl_sync(kAll, w[i], 0), b = __shfl_sync(kAll, w[i], 31);
-    // an element of lane 0 sits below `skip`, one of lane 31 from it on
-    const int first = i * (int)(4 / sizeof(T));
-    if constexpr (sizeof(T) == 4) ends[i] = first < skip ? a : b;
-    else ends[i] = ((first < skip ? a : b) & 0xffffu) | ((first + 1 < skip ? a : b) & 0xffff0000u);
-  }
-  if (lane < N) {
-    const int i = lane * (int)sizeof(T) / 4;
-    const uint32_t x = i == 0 ? ends[0] : i == 1 ? ends[1] : i == 2 ? ends[2] : ends[3];
-    T *at = o + u0 - lane * N + (lane < skip ? lane : 31 * N + lane);
-    if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t *>(at) = x;
-    else *reinterpret_cast<uint16_t *>(at) = (uint16_t)(lane & 1 ? x >> 16 : x);
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t f = __shfl_sync(kAll, a[j], 0), l = __shfl_sync(kAll, b[j], 31);
+      if (j == i) x = lane < skip ? f : l;
+    }
+    if (lane < N) {
+      T *at = o + u + (lane < skip ? lane : (32 * K - 1) * N + lane);
+      if constexpr (sizeof(T) == 4) *reinterpret_cast<uint32_t *>(at) = x;
+      else *reinterpret_cast<uint16_t *>(at) = (uint16_t)(lane & 1 ? x >> 16 : x);
+    }
   }
   const int words = skip * (int)sizeof(T) / 4;
-  if (words & 1) {
 #pragma unroll
-    for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
-  }
-  if (words & 2) {
+  for (int k = 0; k < K; ++k) {
+    const uint4 n = k + 1 < K && lane == 0 ? p[k + 1 < K ? k + 1 : k] : p[k];
+    uint32_t w[8] = {p[k].x, p[k].y, p[k].z, p[k].w, n.x, n.y, n.z, n.w};
 #pragma unroll
-    for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
-  }
-  if (sizeof(T) == 2 && (skip & 1)) {
+    for (int i = 4; i < 8; ++i) w[i] = __shfl_sync(kAll, w[i], lane + 1);  // (31: lane 0's)
+    if (words & 1) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+      for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
+    }
+    if (words & 2) {
+#pragma unroll
+      for (int i = 0; i < 5; ++i) w[i] = w[i + 2];
+    }
+    if (sizeof(T) == 2 && (skip & 1)) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+    }
+    if (k + 1 < K || lane < 31)
+      store16<STREAM>(o + u + (32 * k + lane) * N + skip, make_uint4(w[0], w[1], w[2], w[3]));
   }
-  if (lane < 31) store16<STREAM>(o + u0 + skip, make_uint4(w[0], w[1], w[2], w[3]));
 }
 
 // ---------------------------------------------------------- adjustments --
