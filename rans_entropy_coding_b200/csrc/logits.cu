@@ -15,7 +15,7 @@ namespace {
 // all threads wait for that.
 constexpr int kAdjThreads = 512;
 constexpr int kAdjVecs = 4;
-constexpr int kTableThreads = 128;
+constexpr int kTableThreads = 256;
 
 template <typename T, typename O, bool TOUCH, bool MASK>
 __global__ void __launch_bounds__(TOUCH ? kAdjThreads + kTableThreads : kAdjThreads, TOUCH ? 2 : 3)

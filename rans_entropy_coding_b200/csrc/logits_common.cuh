@@ -387,35 +387,42 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
                                           int threads, Barrier barrier) {
   const int64_t n = a.history_n + a.bias_n;
   int span = min(kHashSpan, u_hi - u_lo);
-  // body(place in the span or -1, entry) for the window's entries, four loads
-  // in flight per thread
+  // body(place in the span, entry) for the window's entries, kFlight loads in
+  // flight per thread
+  constexpr int kFlight = 8;
   auto window = [&](auto body) {
-    for (int64_t i0 = tid; i0 < n; i0 += 4 * threads) {
-      int v[4];
+    for (int64_t i0 = tid; i0 < n; i0 += kFlight * threads) {
+      int v[kFlight];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kFlight; ++j) {
         const int64_t i = i0 + j * threads;
         v[j] = i >= n ? -1 : i < a.history_n ? a.history[i] : a.bias_ids[i - a.history_n];
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kFlight; ++j) {
         const int k = v[j] + row.shift - u_lo;
         if (v[j] >= 0 && v[j] < row.vocab && k >= 0 && k < span) body(k, i0 + j * threads);
       }
     }
   };
-  // the adjusted logit of the token at place k
-  auto adjusted = [&](int k, uint32_t count, uint32_t entry) {
+  // what the token at place k needs from memory, and its adjusted logit
+  struct Raw {
+    float z, bias;
+    uint32_t mask;
+  };
+  auto raw_of = [&](int k, uint32_t entry) {
     const int u = u_lo + k, v = u - row.shift;
-    float z = logit_float(row.at0[u]);
-    const uint32_t ok = a.mask ? a.mask[v >> 5] >> (v & 31) & 1u : 1u;
-    const float bias = entry > 0 ? a.bias_values[entry - 1] : 0.0f;
+    return Raw{logit_float(row.at0[u]), entry > 0 ? a.bias_values[entry - 1] : 0.0f,
+               a.mask ? a.mask[v >> 5] >> (v & 31) : 1u};
+  };
+  auto adjusted = [&](const Raw &w, uint32_t count, uint32_t entry) {
+    float z = w.z;
     if (count > 0) {
       z = z > 0.0f ? __fdiv_rn(z, a.repetition) : __fmul_rn(z, a.repetition);
       z = __fsub_rn(z, __fadd_rn(__fmul_rn(__uint2float_rn(count), a.frequency), a.presence));
     }
-    if (entry > 0) z = __fadd_rn(z, bias);
-    return __float_as_uint(ok ? z : kNegInf);
+    if (entry > 0) z = __fadd_rn(z, w.bias);
+    return __float_as_uint(w.mask & 1 ? z : kNegInf);
   };
 
   if (!dense) {
@@ -456,9 +463,21 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
     barrier();
     dense = t.n_used > kHashTokens;
     if (!dense) {
-      for (int i = tid; i < t.n_used; i += threads) {
-        const int s = t.hash.used[i];
-        t.hash.count[s] = adjusted(t.hash.key[s], t.hash.count[s], t.hash.bias[s]);
+      // (four tokens' logits in flight per thread)
+      for (int i0 = tid; i0 < t.n_used; i0 += 4 * threads) {
+        Raw raw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i0 + j * threads < t.n_used) {
+            const int s = t.hash.used[i0 + j * threads];
+            raw[j] = raw_of(t.hash.key[s], t.hash.bias[s]);
+          }
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (i0 + j * threads < t.n_used) {
+            const int s = t.hash.used[i0 + j * threads];
+            t.hash.count[s] = adjusted(raw[j], t.hash.count[s], t.hash.bias[s]);
+          }
       }
       barrier();
       return span;
@@ -489,7 +508,8 @@ __device__ __forceinline__ int fill_touch(TouchTable &t, const RowAdjust &a, con
     if (ok) ok[w] &= ~bits[w];
     for (uint32_t b = bits[w]; b != 0; b &= b - 1) {
       const int k = w * 32 + __ffs(b) - 1;
-      t.cells.count[k] = adjusted(k, t.cells.count[k], t.cells.bias[k]);
+      t.cells.count[k] =
+          adjusted(raw_of(k, t.cells.bias[k]), t.cells.count[k], t.cells.bias[k]);
     }
   }
   barrier();

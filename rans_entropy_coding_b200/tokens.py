@@ -24,9 +24,11 @@ TOKEN_PRECISION = 24
 
 # These calls are made once per decoded token, where the host's time counts: a
 # tensor's facts are asked once each, devices are compared by index, and
-# rans_logits is packed rather than built field by field.
+# the structs are packed rather than built field by field.
 _pack_logits = struct.Struct("@Piiqq").pack
+_pack_adjust = struct.Struct("@ffffPPPPqPPPPqPq").pack
 assert struct.calcsize("@Piiqq") == ctypes.sizeof(L.rans_logits)
+assert struct.calcsize("@ffffPPPPqPPPPqPq") == ctypes.sizeof(L.rans_adjust)
 _no_context = contextlib.nullcontext()
 
 
@@ -303,82 +305,95 @@ class LogitAdjust:
 
     def __init__(self, temperature=1.0, repetition=1.0, frequency=0.0, presence=0.0,
                  history=None, bias=None, mask=None):
-        c = L.rans_adjust()
-        self.c, self._n, self._words, self._dev = c, None, 0, None
-        self._keep = keep = [history, bias, mask]
-        parts = (repetition, frequency, presence, temperature)
-        if any(isinstance(x, torch.Tensor) for x in parts):
-            one = [x for x in parts if isinstance(x, torch.Tensor)][0]
-            dev, n = self._on(one, one.numel()), one.numel()
-            cols = [x if isinstance(x, torch.Tensor) else
-                    torch.full((n,), float(x), device=one.device) for x in parts]
-            for x in cols:
-                _tensor(x, torch.float32, (n,), dev, "per-row parameters")
-            cols[3] = 1.0 / cols[3]
-            keep.append(torch.stack(cols, 1))
-            c.params = keep[-1].data_ptr()
+        self._n, self._words, self._dev = None, 0, None
+        self._keep = (history, bias, mask)
+        params = 0
+        scalars = (1.0, 0.0, 0.0, 1.0)
+        tensor = torch.Tensor
+        if isinstance(temperature, tensor) or isinstance(repetition, tensor) or \
+                isinstance(frequency, tensor) or isinstance(presence, tensor):
+            params = self._per_row((repetition, frequency, presence, temperature))
         else:
-            c.repetition = _positive(repetition, "repetition")
-            c.frequency = _finite(frequency, "frequency")
-            c.presence = _finite(presence, "presence")
-            c.inv_temperature = _positive(1.0 / _positive(temperature, "temperature"),
-                                          "1 / temperature")
+            scalars = (_positive(repetition, "repetition"), _finite(frequency, "frequency"),
+                       _finite(presence, "presence"),
+                       _positive(1.0 / _positive(temperature, "temperature"),
+                                 "1 / temperature"))
+        hist = (0, 0, 0, 0)
         if history is not None:
             tokens, begin, end = history
-            k, n = tokens.numel(), begin.numel()
-            dev = self._on(begin, n)
-            t = _tensor(tokens, torch.int32, (k,), dev, "history tokens")
-            b = _tensor(begin, torch.int64, (n,), dev, "history begin")
-            e = _tensor(end, torch.int64, (n,), dev, "history end")
-            if k > 0:
-                c.history, c.history_begin, c.history_end, c.history_len = t, b, e, k
+            n = begin.shape
+            dev = self._on(begin, n[0])
+            hist = (_tensor(tokens, torch.int32, tokens.shape, dev, "history tokens"),
+                    _tensor(begin, torch.int64, n, dev, "history begin"),
+                    _tensor(end, torch.int64, n, dev, "history end"), tokens.numel())
+            if hist[3] == 0:
+                hist = (0, 0, 0, 0)
+        extra = (0, 0, 0, 0, 0)
         if bias is not None:
             ids, values, begin, end = bias
-            k, n = ids.numel(), begin.numel()
-            dev = self._on(begin, n)
-            i = _tensor(ids, torch.int32, (k,), dev, "bias ids")
-            w = _tensor(values, torch.float32, (k,), dev, "bias values")
-            b = _tensor(begin, torch.int64, (n,), dev, "bias begin")
-            e = _tensor(end, torch.int64, (n,), dev, "bias end")
-            if k > 0:
-                c.bias_ids, c.bias_values, c.bias_len = i, w, k
-                c.bias_begin, c.bias_end = b, e
+            k, n = ids.shape, begin.shape
+            dev = self._on(begin, n[0])
+            extra = (_tensor(ids, torch.int32, k, dev, "bias ids"),
+                     _tensor(values, torch.float32, k, dev, "bias values"),
+                     _tensor(begin, torch.int64, n, dev, "bias begin"),
+                     _tensor(end, torch.int64, n, dev, "bias end"), ids.numel())
+            if extra[4] == 0:
+                extra = (0, 0, 0, 0, 0)
+        allowed = (0, 0)
         if mask is not None:
             if mask.dtype is not torch.int32 or mask.dim() not in (1, 2) or \
                     (mask.shape[-1] > 1 and mask.stride(-1) != 1):
                 raise ValueError("mask: int32 words [rows, words] or [words], from pack_mask")
             self._words = mask.shape[-1]
+            if self._words < 1:
+                raise ValueError("mask: no words")
             if mask.dim() == 2:
                 n, step = mask.shape[0], mask.stride(0)
                 if n > 1 and step < self._words:
                     raise ValueError("mask: rows must not overlap")
                 self._on(mask, n)
-                c.mask_stride = max(step, self._words)
+                allowed = (mask.data_ptr(), max(step, self._words))
             else:
                 self._on(mask, self._n)
-            c.mask = mask.data_ptr()
+                allowed = (mask.data_ptr(), 0)
+        self._c = _pack_adjust(*scalars, params, *hist, *extra, *allowed)
+
+    def _per_row(self, parts):
+        """Address of the parameters [rows, 4], numbers widened to all rows."""
+        one = [x for x in parts if isinstance(x, torch.Tensor)][0]
+        dev, n = self._on(one, one.numel()), one.numel()
+        cols = [x if isinstance(x, torch.Tensor) else
+                torch.full((n,), float(x), device=one.device) for x in parts]
+        for x in cols:
+            _tensor(x, torch.float32, (n,), dev, "per-row parameters")
+        cols[3] = 1.0 / cols[3]
+        rows = torch.stack(cols, 1)
+        self._keep += (rows,)
+        return rows.data_ptr()
 
     def _on(self, x, n):
         """The device of a part for n rows, which all parts share."""
         dev = x.get_device()
-        if dev < 0 or self._dev not in (None, dev):
+        if dev < 0 or (self._dev is not None and self._dev != dev):
             raise ValueError("LogitAdjust takes CUDA tensors on one device")
-        if n is not None and self._n not in (None, n):
+        if self._n is not None and n is not None and self._n != n:
             raise ValueError("parts for %d and for %d rows" % (self._n, n))
-        self._dev, self._n = dev, n
+        self._dev = dev
+        if n is not None:
+            self._n = n
         return dev
 
     def bind(self, rows):
-        """The C struct, checked against the rows it is to be used on (as
-        _rows has them)."""
+        """The C struct's bytes, checked against the rows it is to be used on
+        (as _rows has them)."""
         dev, n, v = rows[:3]
-        if self._dev not in (None, dev):
+        if self._dev is not None and self._dev != dev:
             raise ValueError("LogitAdjust on cuda:%d, logits on cuda:%d" % (self._dev, dev))
-        if self._n not in (None, n):
+        if self._n is not None and self._n != n:
             raise ValueError("LogitAdjust for %d rows, logits of %d" % (self._n, n))
-        if self.c.mask and self._words < (v + 31) // 32:
+        if self._words and self._words < (v + 31) // 32:
             raise ValueError("mask: %d words for %d tokens" % (self._words, v))
-        return ctypes.byref(self.c)
+        return self._c
 
 
 def adjust_logits(logits, adjust, out=None, dtype=None, stream=None):
