@@ -484,7 +484,9 @@ int rans_decode_to_values(const uint8_t *in, uint64_t in_bytes, const uint64_t *
  * decoder, which sees one row per step, reproduces what the encoder saw in a
  * whole text.  If every alive y is -inf (finite logits that overflow), all
  * alive tokens weigh the same.  A NaN or +inf logit of an alive token (or one
- * whose y overflows) is RANS_ERR_RANGE; one under a 0 mask bit is not read.
+ * whose y overflows), or a row whose own inv_temperature is not positive and
+ * finite, is RANS_ERR_RANGE; what a logit under a 0 mask bit holds does not
+ * matter.
  *
  * Streams: RANS64 states and words (lower bound 2^31, 32-bit words, one state
  * per stream) at RANS_TOKEN_PRECISION bits: a token renormalises when
@@ -557,7 +559,8 @@ int rans_adjust_logits(const rans_logits *logits, const rans_adjust *adjust, voi
  *           it.  A token outside the vocabulary is RANS_ERR_INDEX, one that is
  *           not alive RANS_ERR_ZERO_FREQ, a row with a bad logit
  *           RANS_ERR_RANGE; such a row's start and freq are 0.
- *   tokens: device int32[rows]; starts, freqs: device uint32[rows] out.
+ *   tokens: device int32[rows]; starts, freqs: device uint32[rows] out; none
+ *           of the three may overlap another.
  * Asynchronous.
  */
 int rans_token_intervals(const rans_logits *logits, const rans_adjust *adjust,
@@ -596,6 +599,7 @@ int rans_token_states(const uint8_t *in, uint64_t in_bytes, const uint64_t *stre
  * RANS_ERR_CORRUPT; no token alive: RANS_ERR_ZERO_FREQ; a bad logit:
  * RANS_ERR_RANGE) the row's token is -1 and its stream's state goes out as it
  * came in (for an id that is out of range or named twice, it is not written).
+ *   tokens and states_out overlap no input (but for states_out = states_in).
  *   Other arguments as above.  Asynchronous.
  */
 int rans_decode_tokens(const rans_logits *logits, const rans_adjust *adjust, const uint8_t *in,

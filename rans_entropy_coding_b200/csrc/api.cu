@@ -84,7 +84,12 @@ cudaError_t ensure_cluster(const void *fn) {
   for (const auto &x : g_cluster_set)
     if (x.first == fn && x.second == dev) return cudaSuccess;
   e = cudaFuncSetAttribute(fn, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-  if (e == cudaSuccess) g_cluster_set.push_back({fn, dev});
+  if (e == cudaSuccess) {
+    try {
+      g_cluster_set.push_back({fn, dev});
+    } catch (...) {  // no memory to remember it: set again next time
+    }
+  }
   return e;
 }
 
@@ -583,6 +588,12 @@ int check_distill(const rans_logits *in, const int32_t *ids, const float *lp, in
   return RANS_OK;
 }
 
+// Whether two arrays share memory (an absent one shares none).
+bool overlap(const void *a, uint64_t na, const void *b, uint64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + nb && y < x + na;
+}
+
 // A result of the logits' shape: its rows, and what it may share with them.
 int check_result(const rans_logits *in, const void *out, int32_t dtype, int64_t stride) {
   const int e = logits_bytes(dtype);
@@ -630,6 +641,11 @@ RANS_API int rans_token_intervals(const rans_logits *logits, const rans_adjust *
   if (st) return st;
   if (logits->rows == 0) return RANS_OK;
   if (!tokens || !starts || !freqs) return RANS_ERR_ARG;
+  // a row's blocks read its token while others may be done with theirs
+  const uint64_t bytes = 4ull * (uint64_t)logits->rows;
+  if (overlap(tokens, bytes, starts, bytes) || overlap(tokens, bytes, freqs, bytes) ||
+      overlap(starts, bytes, freqs, bytes) || overlap(status, 256, tokens, bytes))
+    return RANS_ERR_ARG;
   return rb::launch_token_intervals(*logits, a, tokens, starts, freqs,
                                     static_cast<int32_t *>(status), as_stream(stream));
 }
@@ -682,6 +698,14 @@ RANS_API int rans_decode_tokens(const rans_logits *logits, const rans_adjust *ad
   if (!stream_ids && logits->rows > S) return RANS_ERR_ARG;
   if (logits->rows == 0) return RANS_OK;
   if (!states_in || !states_out || !tokens || !stream_offsets) return RANS_ERR_ARG;
+  const uint64_t row_bytes = 4ull * (uint64_t)logits->rows, state_bytes = 16ull * (uint64_t)S;
+  if ((states_in != states_out && overlap(states_in, state_bytes, states_out, state_bytes)) ||
+      overlap(tokens, row_bytes, stream_ids, row_bytes) ||
+      overlap(tokens, row_bytes, states_in, state_bytes) ||
+      overlap(tokens, row_bytes, states_out, state_bytes) ||
+      overlap(states_out, state_bytes, stream_ids, row_bytes) ||
+      overlap(status, 256, stream_ids, row_bytes) || overlap(status, 256, states_in, state_bytes))
+    return RANS_ERR_ARG;
   return rb::launch_decode_tokens(*logits, a, in, in_bytes, stream_offsets, S, stream_ids,
                                   states_in, states_out, tokens, static_cast<int32_t *>(status),
                                   as_stream(stream));

@@ -58,7 +58,9 @@ __device__ __forceinline__ RowScale row_scale(float zmax, float inv_temperature)
   s.scale = __fmul_rn(kLog2e, inv_temperature);
   s.ymax = __fmul_rn(zmax, s.scale);
   s.error = RANS_OK;
-  if (zmax == kNegInf) {
+  if (!(s.scale > 0.0f && s.scale < __builtin_huge_valf())) {
+    s.error = RANS_ERR_RANGE;  // (per-row parameters are not known to the host)
+  } else if (zmax == kNegInf) {
     s.error = RANS_ERR_ZERO_FREQ;
   } else if (!(s.ymax < __builtin_huge_valf())) {  // NaN or +inf
     s.error = RANS_ERR_RANGE;
@@ -278,42 +280,64 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   const int64_t r = blockIdx.x / peers;
   const Row<T> row(in.data, r, in.row_stride, in.vocab);
 
-  int target = -1;
-  int64_t stream = r;
-  uint64_t x = 0, taken = 0;
-  // every block of a row finds the same, and all leave before their first
-  // barrier or none
-  auto refuse = [&](int code, int64_t detail, bool state) {
-    if (rank != 0 || tid != 0) return;
-    report(status, code, detail);
+  // One thread reads what decides whether the row is worked on: should another
+  // call be writing it meanwhile, a block's threads still agree.
+  __shared__ int64_t head_stream;
+  __shared__ uint64_t head_state, head_taken;
+  __shared__ int head_target;
+  if (tid == 0) {
     if constexpr (DECODE) {
-      cd.tokens[r] = -1;
-      if (state) {
-        cd.states_out[2 * stream] = x;
-        cd.states_out[2 * stream + 1] = taken;
-      }
+      head_stream = cd.stream_ids ? (int64_t)cd.stream_ids[r] : r;
+      const bool known = head_stream >= 0 && head_stream < cd.S;
+      head_state = known ? cd.states_in[2 * head_stream] : 0;
+      head_taken = known ? cd.states_in[2 * head_stream + 1] : 0;
     } else {
-      starts[r] = 0;
-      freqs[r] = 0;
+      head_target = tokens[r];
+    }
+  }
+  __syncthreads();
+  const int64_t stream = DECODE ? head_stream : r;
+  const uint64_t x = DECODE ? head_state : 0, taken = DECODE ? head_taken : 0;
+  const int target = DECODE ? -1 : head_target;
+  // A block of a cluster may only leave when the others write to it no more, so
+  // one that has nothing to do still meets their `phases` barriers.
+  auto leave = [&](int phases) {
+    if (peers == 1) return;
+    for (int i = 0; i < phases; ++i) {
+      __syncwarp();
+      cluster_arrive();
+      cluster_wait();
     }
   };
+  auto refuse = [&](int phases, int code, int64_t detail, bool state) {
+    if (rank == 0 && tid == 0) {
+      report(status, code, detail);
+      if constexpr (DECODE) {
+        cd.tokens[r] = -1;
+        if (state) {
+          cd.states_out[2 * stream] = x;
+          cd.states_out[2 * stream + 1] = taken;
+        }
+      } else {
+        starts[r] = 0;
+        freqs[r] = 0;
+      }
+    }
+    leave(phases);
+  };
   if constexpr (DECODE) {
-    if (cd.stream_ids) stream = cd.stream_ids[r];
-    if (stream == -1) return;
+    if (stream == -1) return leave(3);
     int bad = stream < 0 || stream >= cd.S;
     if (!bad && cd.stream_ids) {
       for (int64_t i = tid; i < in.rows; i += threads)
         bad |= i != r && cd.stream_ids[i] == (int32_t)stream;
       bad = __syncthreads_or(bad);
     }
-    if (bad) return refuse(RANS_ERR_INDEX, r, false);
-    x = cd.states_in[2 * stream];
-    taken = cd.states_in[2 * stream + 1];
-    if (x < kL || x >> 63) return refuse(RANS_ERR_CORRUPT, stream, true);
+    if (bad) return refuse(3, RANS_ERR_INDEX, r, false);
+    if (x < kL || x >> 63) return refuse(3, RANS_ERR_CORRUPT, stream, true);
   } else {
-    target = tokens[r];
-    if (target == -1) return;
-    if (target < 0 || target >= in.vocab) return refuse(RANS_ERR_INDEX, r, false);
+    if (target == -1) return leave(3);
+    if (target < 0 || target >= in.vocab) return refuse(3, RANS_ERR_INDEX, r, false);
   }
   // a block's shared memory may be written by others once it runs: waited for
   // below, after the first walk
@@ -446,17 +470,17 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   m = warp_max_nan(m);
   const RowScale rs =
       row_scale(m, adj.params ? adj.params[4 * r + 3] : adj.inv_temperature);
-  if (rs.error != RANS_OK) return refuse(rs.error, r, true);
+  if (rs.error != RANS_OK) return refuse(1, rs.error, r, true);
 
   // Second walk: the weights.  Where a warp's smallest logit needs no clamp,
   // the only dead tokens are those that do not count, and the weights go two at
   // a time; such a token then takes a logit whose d is -40, hence weight 0
   // (which wants a maximum that 40 can be told from, and a factor).
   const int u_target = row.shift + target;
+  const float dead = (rs.ymax - 40.0f) / rs.scale;
   const bool plain = __all_sync(
       kFull, __fsub_rn(__fmul_rn(least, rs.scale), rs.ymax) >= kLowest && least > kNegInf &&
-                 fabsf(rs.ymax) < 65536.0f && rs.scale > 0.0f);
-  const float dead = (rs.ymax - 40.0f) / rs.scale;
+                 fabsf(rs.ymax) < 65536.0f && fabsf(dead) < 1e30f);
   const uint64_t scale2 = (uint64_t)__float_as_uint(rs.scale) << 32 | __float_as_uint(rs.scale);
   const uint64_t ymax2 =
       (uint64_t)__float_as_uint(-rs.ymax) << 32 | __float_as_uint(-rs.ymax);
@@ -586,7 +610,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     before = warp_total(before);
     if constexpr (!DECODE) {
       if (lane != 0) return;
-      if (own_weight == 0xffffffffu) return refuse(RANS_ERR_ZERO_FREQ, r, false);
+      if (own_weight == 0xffffffffu) return refuse(0, RANS_ERR_ZERO_FREQ, r, false);
       const uint32_t b = interval_start(before.w, before.n, all.w, all.n);
       starts[r] = b;
       freqs[r] = interval_start(before.w + own_weight, before.n + 1, all.w, all.n) - b;

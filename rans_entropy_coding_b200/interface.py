@@ -127,9 +127,12 @@ class TokenCoder:
         self._in = None
 
     def add(self, logits, tokens, adjust=None):
-        """Intervals of the next tokens.len() positions."""
+        """The next positions: rows of logits and the token that each is to code."""
         tokens = torch.as_tensor(tokens, dtype=torch.int32, device=self.device).reshape(-1)
-        self._parts.append(T.token_intervals(logits, tokens, adjust, status=self.status))
+        # a skipped row (token -1) stays at 0, which the streams refuse
+        blank = torch.zeros(2, tokens.numel(), dtype=torch.int32, device=self.device)
+        self._parts.append(T.token_intervals(logits, tokens, adjust, blank[0], blank[1],
+                                             self.status))
         return self
 
     def streams(self, lengths):

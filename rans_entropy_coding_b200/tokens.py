@@ -410,7 +410,8 @@ def adjust_logits(logits, adjust, out=None, dtype=None, stream=None):
 def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status=None,
                     stream=None):
     """(starts, freqs), int32 [rows]: each row's interval of its token at
-    TOKEN_PRECISION bits.  Rows with token -1 are skipped."""
+    TOKEN_PRECISION bits.  Rows with token -1 are skipped: what stands in
+    starts and freqs stays (nothing useful, where they are not given)."""
     rows = _rows(logits)
     with _place(rows[0], stream):
         if starts is None:

@@ -124,6 +124,11 @@ def test_adjust_in_place_and_neutral(dtype):
     assert rb.adjust_logits(y, a, out=y) is y and torch.equal(y, want)
     assert torch.equal(rb.adjust_logits(x, None), x)
     assert torch.equal(rb.adjust_logits(x, rb.LogitAdjust()), x)
+    a, _ = make_adjust(n, v, seed=6, long=30000)     # too many touched tokens for a hash
+    want = rb.adjust_logits(x, a)
+    y = x.clone()
+    rb.adjust_logits(y, a, out=y)
+    assert torch.equal(y, want)
     # penalties that are neutral change no bit
     (h, b, e) = torch.arange(50, dtype=torch.int32, device="cuda"), *torch.tensor(
         [[0] * n, [50] * n], device="cuda")
@@ -242,6 +247,10 @@ def test_intervals_errors_and_skipped_rows():
     row[5] = torch.finfo(F32).min
     b = TO.bounds(row.numpy(), {}, 0)
     assert one(row, 5) == (b[5], 1, rb.OK)
+    # per-row parameters that are no temperature
+    for bad in (0.0, -1.0, math.nan, math.inf):
+        p = rb.LogitAdjust(temperature=torch.full((1,), bad, device="cuda"))
+        assert one(base, 5, p) == (0, 0, rb.ERR_RANGE)
     # and where a row has nothing else, its tokens weigh the same
     low = torch.full((v,), torch.finfo(F32).min)
     low[0] = -math.inf
@@ -741,6 +750,54 @@ def test_distill_through_autograd():
     rb.distill_loss(z * 0.5, ti, tl).sum().backward()
     _, half = rb.distill_loss_and_grad(x * 0.5, ti, tl, torch.ones(n, device="cuda"))
     assert torch.equal(z.grad, half * 0.5)
+
+
+def test_offsets_past_32_bits():
+    """Rows that lie 2^30 elements apart."""
+    v, step = 1003, (1 << 30) + 3
+    flat = torch.zeros(2 * step + v, device="cuda", dtype=F16)
+    far = flat.as_strided((3, v), (step, 1))
+    x = make_logits(3, v, F16, seed=17)
+    far.copy_(x)
+    a, _ = make_adjust(3, v, seed=17)
+    tok = torch.full((3,), 7, dtype=torch.int32, device="cuda")
+    ids, lp = (torch.from_numpy(t).cuda() for t in teacher(3, v, 9, 8, True))
+    w = torch.ones(3, device="cuda")
+    assert torch.equal(rb.adjust_logits(far, a), rb.adjust_logits(x, a))
+    for p, q in zip(rb.token_intervals(far, tok), rb.token_intervals(x, tok)):
+        assert torch.equal(p, q)
+    want = rb.distill_loss_and_grad(x, ids, lp, w)
+    for p, q in zip(rb.distill_loss_and_grad(far, ids, lp, w), want):
+        assert torch.equal(p, q)
+    rb.distill_loss_and_grad(far, ids, lp, w, grad=far)
+    assert torch.equal(far, want[1])
+
+
+@pytest.mark.parametrize("K", [128, 129, 1000, 4096])
+def test_distill_long_lists_and_the_same_bits_twice(K):
+    n, v = 3, 6000
+    x = make_logits(n, v, BF16, 5, seed=18)
+    ids, lp = teacher(n, v, K, K, True)
+    g = np.array([1.0, 2.0, -1.0], np.float32)
+    args = (x, *(torch.from_numpy(t).cuda() for t in (ids, lp, g)))
+    st = rb.new_status()
+    one, two = (rb.distill_loss_and_grad(*args, status=st) for _ in range(2))
+    check_distill(x, ids, lp, 1.0, True, g, *one)
+    assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+    y = x.detach().requires_grad_()
+    loss = rb.distill_loss(y, *args[1:3], status=st)
+    (grad,) = torch.autograd.grad(loss, y, args[3])
+    assert torch.equal(loss, one[0])
+    check_distill(x, ids, lp, 1.0, True, g, loss.detach(), grad)
+    status_ok(st)
+
+
+def test_a_token_that_was_not_given_is_not_coded():
+    x = make_logits(3, 50, F32)
+    c = rb.TokenCoder()
+    c.add(x, torch.tensor([1, -1, 2]))
+    with pytest.raises(rb.RansError):
+        c.streams([3])
 
 
 # -------------------------------------------------- streams, graphs, runs --

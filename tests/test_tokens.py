@@ -13,6 +13,11 @@ from rans_entropy_coding_b200 import build as rbuild
 P = 1 << 20  # an address that nothing reads: every call here is refused on the host
 
 
+def A(k):
+    """Addresses far from P and from one another."""
+    return P + (k << 24)
+
+
 @pytest.fixture(scope="module")
 def lib():
     rbuild.build()
@@ -50,13 +55,13 @@ def calls(lib, lg, ad=None):
     """Every entry point that takes logits, with good other arguments."""
     a = None if ad is None else ctypes.byref(ad)
     x = ctypes.byref(lg)
-    yield lib.rans_adjust_logits(x, a, P + (8 << 20), 0, 100, None)
-    yield lib.rans_token_intervals(x, a, P, P, P, P, None)
-    yield lib.rans_decode_tokens(x, a, P, 64, P, 8, None, P, P, P, P, None)
+    yield lib.rans_adjust_logits(x, a, A(1), 0, 100, None)
+    yield lib.rans_token_intervals(x, a, A(1), A(2), A(3), A(4), None)
+    yield lib.rans_decode_tokens(x, a, A(1), 64, A(2), 8, None, A(3), A(4), A(5), A(6), None)
     if ad is None:
-        yield lib.rans_distill_forward(x, P, P, 5, 1.0, 1, P, P, P, None)
-        yield lib.rans_distill_backward(x, P, P, 5, 1.0, P, P, P + (8 << 20), 100, None)
-        yield lib.rans_distill(x, P, P, 5, 1.0, 1, P, P, P + (8 << 20), 100, P, None)
+        yield lib.rans_distill_forward(x, A(1), A(2), 5, 1.0, 1, A(3), A(4), A(5), None)
+        yield lib.rans_distill_backward(x, A(1), A(2), 5, 1.0, A(3), A(4), A(5), 100, None)
+        yield lib.rans_distill(x, A(1), A(2), 5, 1.0, 1, A(3), A(4), A(5), 100, A(6), None)
 
 
 @pytest.mark.parametrize("bad", BAD_LOGITS, ids=str)
@@ -104,18 +109,24 @@ def test_results_that_overlap_are_refused(lib):
 def test_bad_pointers_and_counts_are_refused(lib):
     x = ctypes.byref(logits())
     S = rb.ERR_ARG
-    for k in (3, 4, 5):  # tokens, starts, freqs
-        args = [x, None, P, P, P, P, None]
-        args[k - 1] = None
-        assert lib.rans_token_intervals(*args) == S
-    assert lib.rans_token_intervals(x, None, P, P, P, P + 8, None) == S   # status alignment
-    assert lib.rans_token_intervals(x, None, P, P, P, None, None) == S
-    good = [x, None, P, 64, P, 8, None, P, P, P, P, None]
-    for k, v in ((2, None), (2, P + 2), (4, None), (5, -1), (5, 3), (7, None), (8, None),
-                 (9, None), (10, None), (10, P + 4)):
+    good = [x, None, A(1), A(2), A(3), A(4), None]
+    for k, v in ((2, None), (3, None), (4, None), (5, None), (5, A(4) + 8),
+                 (3, A(1)), (4, A(1) + 12), (4, A(2) - 12), (5, A(1) & ~255)):
+        args = list(good)
+        args[k] = v
+        assert lib.rans_token_intervals(*args) == S, (k, v)
+    good = [x, None, A(1), 64, A(2), 8, A(3), A(4), A(5), A(6), A(7), None]
+    for k, v in ((2, None), (2, A(1) + 2), (4, None), (5, -1), (7, None), (8, None), (9, None),
+                 (10, None), (10, A(7) + 4),
+                 (8, A(4) + 16),            # states that overlap but are not the same
+                 (9, A(3) + 4),             # tokens over stream ids
+                 (9, A(4)), (9, A(5) + 124), (6, A(5)), (10, A(3)), (10, A(4))):
         args = list(good)
         args[k] = v
         assert lib.rans_decode_tokens(*args) == S, (k, v)
+    args = list(good)
+    args[5], args[6] = 3, None              # fewer streams than rows
+    assert lib.rans_decode_tokens(*args) == S
     assert lib.rans_token_states(P, 64, None, 2, P, P, None) == S
     assert lib.rans_token_states(P, 64, P, 2, None, P, None) == S
     assert lib.rans_token_states(P + 1, 64, P, 2, P, P, None) == S
