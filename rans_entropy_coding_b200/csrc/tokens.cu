@@ -236,14 +236,13 @@ struct Coded {
 // The streams' side of a decoding row: a token whose interval is [s, s + f).
 __device__ __forceinline__ void take_token(const Coded &cd, int64_t r, int64_t stream, uint64_t x,
                                            uint64_t taken, int token, uint32_t s, uint32_t f,
+                                           bool refill_ok, uint32_t refill_word,
                                            int32_t *status) {
   uint64_t y = (uint64_t)f * (x >> kTokPrec) + (x & (kTokTotal - 1)) - s;
   uint64_t used = taken;
   if (y < kL) {
-    const uint64_t off = cd.offsets[stream], lim = cd.offsets[stream + 1];
-    const bool ok = !(off & 3) && off <= lim && lim <= cd.in_bytes && taken < (lim - off) / 4;
-    if (ok) {
-      y = y << 32 | reinterpret_cast<const uint32_t *>(cd.in)[off / 4 + taken];
+    if (refill_ok) {
+      y = y << 32 | refill_word;
       used = taken + 1;
     } else {
       report(status, RANS_ERR_CORRUPT, stream);
@@ -285,6 +284,16 @@ __global__ void __launch_bounds__(kRowThreads, 2)
   __shared__ int64_t head_stream;
   __shared__ uint64_t head_state, head_taken;
   __shared__ int head_target;
+  __shared__ RowAdjust a;
+  if (ADJ && tid == (warps > 1 ? 32 : 0)) a = row_adjust(adj, r, in.vocab);
+  // each warp's first tile comes nearer while the row's particulars are read
+  const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
+#pragma unroll
+  for (int k = 0; k < kTileVecs; ++k) {
+    const int u0 = lo + wid * kTile + k * kVecRow + lane * N;
+    if (u0 >= row.shift && u0 < hi)
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(row.at0 + u0));
+  }
   if (tid == 0) {
     if constexpr (DECODE) {
       head_stream = cd.stream_ids ? (int64_t)cd.stream_ids[r] : r;
@@ -339,6 +348,14 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     if (target == -1) return leave(3);
     if (target < 0 || target >= in.vocab) return refuse(3, RANS_ERR_INDEX, r, false);
   }
+  // the word that the stream would go on with, read long before it is needed
+  __shared__ uint32_t refill_word;
+  __shared__ bool refill_ok;
+  if (DECODE && tid == threads - 1) {
+    const uint64_t off = cd.offsets[stream], lim = cd.offsets[stream + 1];
+    refill_ok = !(off & 3) && off <= lim && lim <= cd.in_bytes && taken < (lim - off) / 4;
+    if (refill_ok) refill_word = reinterpret_cast<const uint32_t *>(cd.in)[off / 4 + taken];
+  }
   // a block's shared memory may be written by others once it runs: waited for
   // below, after the first walk
   if (peers > 1) {
@@ -346,14 +363,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
     cluster_arrive();
   }
 
-  __shared__ RowAdjust a;
-  bool touch = false;
-  if constexpr (ADJ) {
-    if (tid == 0) a = row_adjust(adj, r, in.vocab);
-    __syncthreads();
-    touch = a.touches();
-  }
-  const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
+  const bool touch = ADJ && a.touches();
   if (DECODE && ADJ && touch)  // added to after the first walk's barrier
     for (int i = tid; i < slice / kTile; i += threads) tile_sums[i] = make_uint2(0, 0);
   int table_at = -1, span = 1 << 30;  // where the table starts, its tokens
@@ -684,7 +694,8 @@ __global__ void __launch_bounds__(kRowThreads, 2)
           if (holds(at, after)) {
             const uint32_t b = interval_start(at.w, at.n, all.w, all.n);
             take_token(cd, r, stream, x, taken, u0 + i - row.shift, b,
-                       interval_start(after.w, after.n, all.w, all.n) - b, status);
+                       interval_start(after.w, after.n, all.w, all.n) - b, refill_ok,
+                       refill_word, status);
           }
           at = after;
         }
