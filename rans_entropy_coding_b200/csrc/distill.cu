@@ -93,10 +93,9 @@ struct Entries {
   int v[kEntries];    // token, -1 where there is no entry
   float lp[kEntries], z[kEntries];
 };
-template <typename T>
-__device__ __forceinline__ void load_entries(Entries &e, const T *z, const int32_t *ids,
-                                             const float *lp, int from, int K, int vocab,
-                                             int lane, int64_t r, int32_t *status) {
+__device__ __forceinline__ void load_entries(Entries &e, const int32_t *ids, const float *lp,
+                                             int from, int K, int vocab, int lane, int64_t r,
+                                             int32_t *status) {
 #pragma unroll
   for (int j = 0; j < kEntries; ++j) {
     const int i = from + j * 32 + lane;
@@ -108,8 +107,12 @@ __device__ __forceinline__ void load_entries(Entries &e, const T *z, const int32
     const bool ok = present(e.v[j], e.lp[j], vocab);
     if (status && !ok && e.v[j] != -1 && e.lp[j] != kNegInf) report(status, RANS_ERR_INDEX, r);
     if (!ok) e.v[j] = -1;
-    e.z[j] = ok ? logit_float(z[e.v[j]]) : kNegInf;
   }
+}
+template <typename T>
+__device__ __forceinline__ void load_logits(Entries &e, const T *z) {
+#pragma unroll
+  for (int j = 0; j < kEntries; ++j) e.z[j] = e.v[j] >= 0 ? logit_float(z[e.v[j]]) : kNegInf;
 }
 
 __device__ __forceinline__ double lanes_sum(double x) {
@@ -130,7 +133,7 @@ struct ListSums {
 };
 
 // By one warp; `first` holds the list's first chunk.  (Not inlined, nor
-// row_figures: the streaming warps' registers are not to pay for the double
+// row_loss: the streaming warps' registers are not to pay for the double
 // arithmetic of these.)
 template <typename T>
 __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, const int32_t *ids,
@@ -139,7 +142,10 @@ __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, con
   Entries e = first;
   float m = kNegInf;
   for (int from = 0; from < K; from += kChunk) {
-    if (from > 0) load_entries(e, z, ids, lp, from, K, vocab, lane, 0, nullptr);
+    if (from > 0) {
+      load_entries(e, ids, lp, from, K, vocab, lane, 0, nullptr);
+      load_logits(e, z);
+    }
 #pragma unroll
     for (int j = 0; j < kEntries; ++j) m = fmaxf(m, e.z[j]);
   }
@@ -147,7 +153,10 @@ __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, con
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
   ListSums s = {m == kNegInf ? 0.0 : (double)m, m != kNegInf, 0, 0, 0, 0, 0};
   for (int from = 0; from < K; from += kChunk) {
-    if (K > kChunk) load_entries(e, z, ids, lp, from, K, vocab, lane, 0, nullptr);
+    if (K > kChunk) {
+      load_entries(e, ids, lp, from, K, vocab, lane, 0, nullptr);
+      load_logits(e, z);
+    }
 #pragma unroll
     for (int j = 0; j < kEntries; ++j) {
       if (e.v[j] < 0) continue;
@@ -167,58 +176,72 @@ __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, con
   return s;
 }
 
-// What the row's gradient needs, and what its loss is computed from later.
-struct RowSums {
-  double m, rest, z, mass, pt, norm;
-  bool some, ignored;
+// What the list has for the gradient.
+struct ListFigures {
+  float m;     // largest of its logits (-inf: none is finite)
+  float z;     // e^(inv_t (z - m)), summed
+  float mass, pt, norm;
+  bool ignored;  // no entry left, and no tail
 };
-
-// R sums 2^(c z - offset) over the unlisted tokens, whose largest logit is
-// m_rest (-inf: none has a finite one).  The streaming warps wait for this:
-// two exponentials side by side and a few products; the loss's logarithms come
-// later.
-__device__ __noinline__ RowSums row_figures(const ListSums &s, double R, float m_rest,
-                                            float offset, float c, float inv_t, bool tail,
-                                            int vocab, RowStats &st) {
-  const double it = (double)inv_t;
-  RowSums f;
-  f.some = R > 0.0 || R != R;
-  f.m = fmax(s.some ? s.m : -HUGE_VAL, f.some ? (double)m_rest : -HUGE_VAL);
-  if (f.m == -HUGE_VAL) f.m = 0.0;
-  // against m, with the offset's rounding taken back by the elements' own c
-  const double back = ((double)offset - (double)c * (double)m_rest) * kLn2D;
-  f.rest = f.some ? R * exp(((double)m_rest - f.m) * it + back) : 0.0;
-  const double top = s.some || s.z != s.z ? s.z * exp((s.m - f.m) * it) : 0.0;
-  f.z = f.rest + top;
-  f.norm = tail ? 1.0 : (s.p > 0.0 ? 1.0 / s.p : 0.0);
-  f.pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
-  f.mass = s.p * f.norm + f.pt;
-  f.ignored = !tail && !(s.p > 0.0) && s.p == s.p;
-  const double inv_z = 1.0 / f.z;
-  st.offset = f.some ? offset : 0.0f;
-  st.rest = f.some && !f.ignored ? (float)(it * (f.mass * (f.rest * inv_z) - f.pt) / R) : 0.0f;
-  if (f.z != f.z) st.rest = (float)f.z;
-  st.m_all = (float)f.m;
-  st.inv_z = (float)inv_z;
-  st.mass = (float)f.mass;
-  st.inv_p = (float)f.norm;
-  st.pad[0] = st.pad[1] = 0.0f;
-  return f;
+__device__ __forceinline__ ListFigures list_figures(const ListSums &s, bool tail, int vocab) {
+  const double norm = tail ? 1.0 : (s.p > 0.0 ? 1.0 / s.p : 0.0);
+  const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
+  return {s.some ? (float)s.m : kNegInf, (float)s.z, (float)(s.p * norm + pt), (float)pt,
+          (float)norm, !tail && !(s.p > 0.0) && s.p == s.p};
 }
 
-// sum p (log p - log q) over the list (p = norm * its entries') and the tail.
-__device__ __noinline__ float row_loss(const ListSums &s, const RowSums &f, double R,
-                                       float m_rest, float offset, float c, float inv_t) {
-  if (f.ignored) return f.z == f.z ? 0.0f : (float)f.z;
-  const double it = (double)inv_t, lz = log(f.z);
+// The row's figures from the list's and R, the sum of 2^(c z - offset) over the
+// unlisted tokens, whose largest logit is m_rest (-inf: none has a finite one).
+// Every thread computes them for itself: in double, by one thread for all to
+// wait for, this stood between the two walks for 10,000 cycles of a row's
+// 100,000.  The difference P q_t - p_t is of numbers that float holds to 1e-7,
+// as exact as the gradient's own terms.
+__device__ __forceinline__ RowStats row_figures(const ListFigures &s, float R, float m_rest,
+                                                float offset, float c, float inv_t) {
+  const bool some = R > 0.0f || R != R;
+  float m = fmaxf(s.m, some ? m_rest : kNegInf);
+  if (m == kNegInf) m = 0.0f;
+  // against m, with the offset's rounding taken back
+  const float back = fmaf(-c, m_rest, offset);
+  const float rest = some ? R * exp2_fast((m_rest - m) * c + back) : 0.0f;
+  const float top = s.m > kNegInf || s.z != s.z
+                        ? s.z * exp2_fast(((s.m > kNegInf ? s.m : 0.0f) - m) * c)
+                        : 0.0f;
+  const float z = rest + top;
+  RowStats st;
+  st.offset = some ? offset : 0.0f;
+  st.rest = some && !s.ignored ? inv_t * (s.mass * (rest / z) - s.pt) / R : 0.0f;
+  if (z != z) st.rest = z;
+  st.m_all = m;
+  st.inv_z = 1.0f / z;
+  st.mass = s.mass;
+  st.inv_p = s.norm;
+  st.pad[0] = st.pad[1] = 0.0f;
+  return st;
+}
+
+// sum p (log p - log q) over the list and the tail, in double, by the listing
+// warp's first thread while the others go on.
+__device__ __noinline__ float row_loss(const ListSums &s, double R, float m_rest, float offset,
+                                       float c, float inv_t, bool tail, int vocab) {
+  const double it = (double)inv_t;
+  const bool some = R > 0.0 || R != R;
+  double m = fmax(s.some ? s.m : -HUGE_VAL, some ? (double)m_rest : -HUGE_VAL);
+  if (m == -HUGE_VAL) m = 0.0;
+  const double back = ((double)offset - (double)c * (double)m_rest) * kLn2D;
+  const double rest = some ? R * exp(((double)m_rest - m) * it + back) : 0.0;
+  const double top = s.some || s.z != s.z ? s.z * exp((s.m - m) * it) : 0.0;
+  const double z = rest + top, lz = log(z);
+  if (!tail && !(s.p > 0.0) && s.p == s.p) return z == z ? 0.0f : (float)z;
+  const double norm = tail ? 1.0 : 1.0 / s.p;
+  const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
   double part = 0.0;
   if (s.p > 0.0 || s.p != s.p)
-    part = f.norm * (s.plp + s.p * log(f.norm) - s.pz - s.p * ((s.m - f.m) * it - lz));
-  if (f.pt > 0.0) {
+    part = norm * (s.plp + s.p * log(norm) - s.pz - s.p * ((s.m - m) * it - lz));
+  if (pt > 0.0) {
     // the tail's logarithm from R's own: rest may be too small for a double
-    const double back = ((double)offset - (double)c * (double)m_rest) * kLn2D;
-    const double log_rest = f.some ? log(R) + back + ((double)m_rest - f.m) * it : -HUGE_VAL;
-    part += f.pt * (log(f.pt) - (log_rest - lz));
+    const double log_rest = some ? log(R) + back + ((double)m_rest - m) * it : -HUGE_VAL;
+    part += pt * (log(pt) - (log_rest - lz));
   }
   return (float)part;
 }
@@ -252,6 +275,14 @@ __device__ __forceinline__ uint4 strike(uint4 q, uint32_t hit, __nv_bfloat16) {
   return strike16(q, hit, 0xff80ff80u);
 }
 
+// 16 bytes to shared memory under an L2 policy.
+__device__ __forceinline__ void copy16(void *dst, const void *src, uint64_t policy) {
+  asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2;" ::"r"(
+                   (uint32_t)__cvta_generic_to_shared(dst)),
+               "l"(src), "l"(policy)
+               : "memory");
+}
+
 enum { kForward = 1, kBackward = 2 };
 
 // One cluster per row.  WHAT: kForward writes losses and (without kBackward)
@@ -265,7 +296,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   constexpr int N = VecOf<T>::N;
   constexpr int kVecRow = 32 * N, kTile = kVecRow * kDisVecs;
   __shared__ Part parts[kDisCluster * kStreamWarps];
-  __shared__ RowStats figures;
+  __shared__ ListFigures list;
   // each streaming warp's two tiles on their way; listed tokens of this
   // block's slice; the listed tokens' logits
   uint4 *ring = reinterpret_cast<uint4 *>(smem) + (threadIdx.x >> 5) * 2 * kDisVecs * 32;
@@ -289,12 +320,17 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   // meanwhile; each lane copies and reads its own vectors.  (A tile that is not
   // inside the row is loaded when it is due.)
   auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
-  auto send = [&](int u, int stage) {
+  // Four rows an SM are more than L2 holds, but half of them is behind its
+  // second walk: what that has read goes first, what it will read last.
+  uint64_t keep, drop;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
+  auto send = [&](int u, int stage, uint64_t policy) {
     if (u >= lo && u < hi && inside(u)) {
 #pragma unroll
       for (int k = 0; k < kDisVecs; ++k)
-        cp_async16(ring + (stage * kDisVecs + k) * 32 + lane,
-                   row.at0 + u + k * kVecRow + lane * N);
+        copy16(ring + (stage * kDisVecs + k) * 32 + lane,
+               row.at0 + u + k * kVecRow + lane * N, policy);
     }
     cp_async_commit();
   };
@@ -325,19 +361,27 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   // the second walk goes backwards: what the first read last is nearest
   const int last = lo + ((hi > lo ? (hi - lo + kTile - 1) / kTile : 0) - 1 - wid) * kTile;
 
-  ListSums sums = {};  // (of the listing threads, as what follows)
-  RowSums row_sums = {};
-  double row_R = 0.0;
-  float row_m_rest = 0.0f, row_offset = 0.0f;
+  RowStats st;
+  ListSums sums = {};  // (the listing warp's)
   const int first = lo + wid * kTile;
   Entries e;  // (the listing warp's)
   if (lists) {
-    load_entries(e, row.at0 + row.shift, ids, lp, 0, K, in.vocab, lane, r,
+    load_entries(e, ids, lp, 0, K, in.vocab, lane, r,
                  (WHAT & kForward) && rank == 0 ? status : nullptr);
   } else if (WHAT & kForward) {
-    send(first, 0);
-    send(first + step, 1);
+    send(first, 0, keep);
+    send(first + step, 1, keep);
   }
+  auto mine = [&](int v) { return v + row.shift >= lo && v + row.shift < hi; };
+  // grad may be the logits' own memory: the listed ones are read before the
+  // first is written
+  auto read_listed = [&] {
+    if (lists) load_logits(e, row.at0 + row.shift);
+    if constexpr ((WHAT & kBackward) != 0)
+      for (int i = kChunk + tid; i < K; i += kDisThreads)
+        if (present(ids[i], lp[i], in.vocab) && mine(ids[i]))
+          top_z[i] = logit_float(row.at0[row.shift + ids[i]]);
+  };
   if constexpr ((WHAT & kForward) != 0) {
     for (int i = tid; i < slice / 32; i += kDisThreads) bits[i] = 0;
     __syncthreads();
@@ -357,8 +401,10 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       else if (rank == 0 && v != -1 && lp[i] != kNegInf) report(status, RANS_ERR_INDEX, r);
     }
     __syncthreads();
+    read_listed();
     if (lists) {
       sums = list_sums(e, row.at0 + row.shift, ids, lp, K, in.vocab, (double)inv_t, lane);
+      if (lane == 0) list = list_figures(sums, tail != 0, in.vocab);
     } else {
       // R, against each lane's running maximum
       float m = kNegInf, off = 0.0f;
@@ -368,7 +414,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
         uint4 q[kDisVecs];
         uint32_t word[kDisVecs];
         receive(u, stage, q);
-        send(u + 2 * step, stage);
+        send(u + 2 * step, stage, keep);
         // (a tile's bits lie inside the slice's, which is a whole number of tiles)
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k)
@@ -406,8 +452,8 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       }
       float s = unpair(s2).x + unpair(s2).y;
       if constexpr ((WHAT & kBackward) != 0) {  // the second walk's first tiles
-        send(last, 0);
-        send(last - step, 1);
+        send(last, 0, drop);
+        send(last - step, 1, drop);
       }
       float w = m;
 #pragma unroll
@@ -430,54 +476,34 @@ __global__ void __launch_bounds__(kDisThreads, 4)
     } else {
       __syncthreads();
     }
-    if (wid == kStreamWarps) {
-      // the first of the listing warps joins the parts, in a fixed order
-      float m_rest = kNegInf;
-      for (int i = lane; i < (int)peers * kStreamWarps; i += 32)
-        m_rest = max_nan(m_rest, parts[i].m);
+    // the parts joined, by every warp alike
+    float m_rest = kNegInf;
+    for (int i = lane; i < (int)peers * kStreamWarps; i += 32)
+      m_rest = max_nan(m_rest, parts[i].m);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        m_rest = max_nan(m_rest, __shfl_xor_sync(kFull, m_rest, o));
-      const float offset = m_rest == kNegInf ? 0.0f : __fmul_rn(m_rest, c);
-      double R = 0.0;
-      for (int i = lane; i < (int)peers * kStreamWarps; i += 32) {
-        const Part p = parts[i];
-        // each part against its own rounded product
-        R += p.m == kNegInf ? (double)p.r : (double)p.r * (double)exp2_fast(__fmul_rn(p.m, c) - offset);
-      }
+    for (int o = 16; o > 0; o >>= 1) m_rest = max_nan(m_rest, __shfl_xor_sync(kFull, m_rest, o));
+    const float offset = m_rest == kNegInf ? 0.0f : __fmul_rn(m_rest, c);
+    float R = 0.0f;
+    for (int i = lane; i < (int)peers * kStreamWarps; i += 32) {
+      const Part p = parts[i];
+      // each part against its own rounded product
+      R += p.m == kNegInf ? p.r : p.r * exp2_fast(__fmul_rn(p.m, c) - offset);
+    }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) R += __shfl_xor_sync(kFull, R, o);
-      if (lane == 0) {
-        RowStats st;
-        row_sums = row_figures(sums, R, m_rest, offset, c, inv_t, tail != 0, in.vocab, st);
-        row_R = R;
-        row_m_rest = m_rest;
-        row_offset = offset;
-        figures = st;
-        if (WHAT == kForward && rank == 0) stats[r] = st;
-      }
+    for (int o = 16; o > 0; o >>= 1) R += __shfl_xor_sync(kFull, R, o);
+    st = row_figures(list, R, m_rest, offset, c, inv_t);
+    if (rank == 0 && tid == kStreamThreads) {
+      if constexpr (WHAT == kForward) stats[r] = st;
+      losses[r] = row_loss(sums, (double)R, m_rest, offset, c, inv_t, tail != 0, in.vocab);
     }
-    if constexpr (WHAT == kForward) {
-      if (rank == 0 && tid == kStreamThreads)
-        losses[r] = row_loss(sums, row_sums, row_R, row_m_rest, row_offset, c, inv_t);
-      return;
-    }
+    if constexpr (WHAT == kForward) return;
   } else {
-    if (tid == 0) figures = stats[r];
+    st = stats[r];
+    read_listed();
+    __syncthreads();
   }
 
   if constexpr ((WHAT & kBackward) != 0) {
-    // grad may be the logits' own memory: this block's listed ones are read
-    // before anything is written
-    auto mine = [&](int v) { return v + row.shift >= lo && v + row.shift < hi; };
-    for (int i = kChunk + tid; i < K; i += kDisThreads)
-      if (present(ids[i], lp[i], in.vocab) && mine(ids[i]))
-        top_z[i] = logit_float(row.at0[row.shift + ids[i]]);
-    __syncthreads();
-    // (another block's sums over the listed tokens are behind the barrier too)
-    if ((WHAT & kForward) && rank == 0 && tid == kStreamThreads)  // while the others stream
-      losses[r] = row_loss(sums, row_sums, row_R, row_m_rest, row_offset, c, inv_t);
-    const RowStats st = figures;
     const float g = grads[r];
     T *o = grad + r * grad_stride - row.shift;
     if (!lists) {
@@ -485,13 +511,13 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       const uint64_t c2 = pair(c, c), off2 = pair(-st.offset, -st.offset);
       const uint64_t factor2 = pair(factor, factor);
       if constexpr (WHAT == kBackward) {
-        send(last, 0);
-        send(last - step, 1);
+        send(last, 0, drop);
+        send(last - step, 1, drop);
       }
       for (int u = last, stage = 0; u >= lo; u -= step, stage ^= 1) {
         uint4 q[kDisVecs];
         receive(u, stage, q);
-        send(u - 2 * step, stage);
+        send(u - 2 * step, stage, drop);
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
           float z[N];
