@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
   const bool lists = tid >= kStreamThreads;
   const float c = (float)((double)inv_t * kLog2eD);
+  const float g = (WHAT & kBackward) ? grads[r] : 0.0f;
   ids += r * K;
   lp += r * K;
   if ((WHAT & kForward) && peers > 1) {  // waited for before the others' memory is written
@@ -504,7 +505,6 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   }
 
   if constexpr ((WHAT & kBackward) != 0) {
-    const float g = grads[r];
     T *o = grad + r * grad_stride - row.shift;
     if (!lists) {
       const float factor = st.rest * g;
