@@ -2,6 +2,9 @@
  * rans_b200.h -- C ABI of librans_b200: indexed 64-bit rANS entropy coding on
  * one NVIDIA B200 (sm_100a).
  *
+ * It codes symbols under prepared tables, and tokens under a language model's
+ * logits (last section).
+ *
  * What is coded (sources are page title + section):
  *   - rANS with a 64-bit state, 32-bit renormalisation words and 16-bit CDF
  *     precision ("torch_ans 0.3.0", Usage, variants table, rans64 row;
@@ -65,9 +68,9 @@ extern "C" {
 typedef enum rans_status {
     RANS_OK = 0,
     RANS_ERR_ARG = -1,        /* invalid argument (host-side or a bad chunking) */
-    RANS_ERR_INDEX = -2,      /* an index outside [0, K) */
+    RANS_ERR_INDEX = -2,      /* an index outside [0, K); a bad or repeated token or stream id */
     RANS_ERR_ZERO_FREQ = -3,  /* a symbol maps to a bucket of width 0 */
-    RANS_ERR_RANGE = -4,      /* an escape raw value of 2^60 or more */
+    RANS_ERR_RANGE = -4,      /* an escape raw value of 2^60 or more; a bad interval or logit */
     RANS_ERR_CAPACITY = -5,   /* an output or table buffer is too small */
     RANS_ERR_CORRUPT = -6,    /* a stream is truncated, too long or inconsistent */
     RANS_ERR_CUDA = -7,       /* a CUDA runtime call failed */

@@ -261,9 +261,9 @@ RANS_API const char *rans_status_string(int status) {
   switch (status) {
     case RANS_OK: return "ok";
     case RANS_ERR_ARG: return "invalid argument";
-    case RANS_ERR_INDEX: return "index outside [0, K)";
-    case RANS_ERR_ZERO_FREQ: return "symbol maps to a bucket of width 0";
-    case RANS_ERR_RANGE: return "escape raw value of 2^60 or more";
+    case RANS_ERR_INDEX: return "index, token or stream id out of range, or named twice";
+    case RANS_ERR_ZERO_FREQ: return "symbol or token maps to a bucket of width 0";
+    case RANS_ERR_RANGE: return "value out of range (escape raw value, interval, logit)";
     case RANS_ERR_CAPACITY: return "buffer too small";
     case RANS_ERR_CORRUPT: return "stream truncated, too long or inconsistent";
     case RANS_ERR_CUDA: return "CUDA runtime call failed";
@@ -273,7 +273,7 @@ RANS_API const char *rans_status_string(int status) {
   }
 }
 
-RANS_API int rans_version(void) { return 100; }
+RANS_API int rans_version(void) { return 200; }
 
 RANS_API int rans_gaussian_lengths(const float *scales, int32_t K, double tail_mass,
                                    int32_t *cdf_lengths, int32_t *offsets, void *stream) {

@@ -11,8 +11,14 @@
 // with no difference of close numbers per element.
 //
 // A row is walked twice, once for R and once for the gradient; the second walk
-// finds it in L2.  With many rows a block takes a row; with few, a cluster of
-// blocks shares it and exchanges its maxima and sums.
+// finds most of it in L2.  With many rows a block takes a row; with few, a
+// cluster of blocks shares it and exchanges its maxima and sums.
+// Measured, loss and gradient: 4096 x 131072 bf16 with 128 listed tokens 480 us
+// (4.5 TB/s of one read and one write; 328 us at the copy's rate), 1001 x 50021
+// fp16 into rows at any alignment 62 us (31 us).  16 instructions a logit keep
+// the schedulers two thirds busy; four blocks an SM, each with a row of its own,
+// fill one another's waits (two blocks of 512 threads: 640 us; rows over
+// clusters of 4: 760 us).
 #include <cmath>
 
 #include "cluster.cuh"
@@ -561,7 +567,7 @@ int launch_t(const rans_logits &in, const int32_t *ids, const float *lp, int K, 
   if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
   constexpr int kTile = 32 * VecOf<T>::N * kDisVecs;
   const int tiles = (in.vocab + VecOf<T>::N - 1 + kTile - 1) / kTile;
-  // blocks per row: one, while the rows alone fill the SMs (two blocks each);
+  // blocks per row: one, while the rows alone fill the SMs (four blocks each);
   // else as many as still leave every warp a tile
   int peers = 1;
   while (peers < kDisCluster && in.rows * peers * 2 <= 4 * num_sms(dev) &&

@@ -13,6 +13,10 @@ namespace {
 // logits is a chain of memory latencies; before the stream, it cost as much as
 // the stream itself.)  In place, the touched logits have to be read first, and
 // all threads wait for that.
+// Measured, 256 x 131072 bf16: 22 us with a temperature alone (6.1 TB/s; copying
+// the rows takes 25 us), 31 us with a mask, 41 us with histories of 1024 to 2048
+// tokens, 51 us with everything (2.75 TB/s): the tables, whose window every
+// block of a row reads, are what is left.
 constexpr int kAdjThreads = 512;
 constexpr int kAdjVecs = 4;
 constexpr int kTableThreads = 256;
@@ -141,7 +145,8 @@ int launch_adjust_t(const rans_logits &in, const rans_adjust &adj, void *out, in
   if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
   constexpr int kTile = kAdjThreads * kAdjVecs * VecOf<T>::N;
   const int tiles = (in.vocab + VecOf<T>::N - 1 + kTile - 1) / kTile;
-  // tiles per block: one, until there are kAdjBlocks blocks for every SM
+  // tiles per block: one, until there are kAdjBlocks blocks for every SM (256
+  // rows of 131072 with everything in use: 6 blocks an SM 51 us, 4 52 us, 2 81 us)
   constexpr int kAdjBlocks = 6;
   int64_t per = in.rows * tiles / ((int64_t)kAdjBlocks * num_sms(dev));
   per = per < 1 ? 1 : per > tiles ? tiles : per;
