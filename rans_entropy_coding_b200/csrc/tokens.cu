@@ -926,11 +926,11 @@ struct RowShape {
 };
 constexpr int kFewWarps = 8;
 
-RowShape row_shape(int64_t rows, int tokens, int tile, int sms) {
+RowShape row_shape(int64_t rows, int tokens, int tile, int most, int sms) {
   const int tiles = (tokens + tile - 1) / tile;
   auto per = [&](int peers) { return (tiles + peers - 1) / peers; };
   int peers = 1;
-  while (peers < kMaxCluster && rows * peers * 2 <= 2 * sms && per(peers * 2) >= kFewWarps)
+  while (peers < most && rows * peers * 2 <= 2 * sms && per(peers * 2) >= kFewWarps)
     peers *= 2;
   const int warps = per(peers) < kRowWarps ? per(peers) : kRowWarps;
   return {peers, warps * 32, per(peers) * tile};
@@ -950,29 +950,34 @@ int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *
   // rows that all start on 16 bytes have no empty places before them
   const bool aligned = reinterpret_cast<uintptr_t>(in.data) % 16 == 0 &&
                        (in.rows == 1 || in.row_stride % VecOf<T>::N == 0);
-  const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), kTile,
-                                   num_sms(dev));
-  const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) + kHashSpan / 8 : 0u) +
-                        (DECODE ? (uint32_t)(shape.slice / kTile * sizeof(uint2)) : 0u);
   if (ensure_cluster((const void *)kern) != cudaSuccess) return RANS_ERR_CUDA;
-  if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
-  if (in.rows > 0x7fffffff / shape.peers) return RANS_ERR_ARG;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(in.rows * shape.peers));
-  cfg.blockDim = dim3((unsigned)shape.threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)shape.peers;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, in, adj, tokens, starts, freqs, cd, status,
-                            shape.slice, (uint64_t)0x8000000080000000ull) == cudaSuccess
-             ? RANS_OK
-             : RANS_ERR_CUDA;
+  // clusters of 16 need a processor group with 16 multiprocessors free of
+  // defects; where a launch finds none, 8 are always to be had
+  for (int most = kMaxCluster;; most = 8) {
+    const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), kTile,
+                                     most, num_sms(dev));
+    const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) + kHashSpan / 8 : 0u) +
+                          (DECODE ? (uint32_t)(shape.slice / kTile * sizeof(uint2)) : 0u);
+    if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
+    if (in.rows > 0x7fffffff / shape.peers) return RANS_ERR_ARG;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(in.rows * shape.peers));
+    cfg.blockDim = dim3((unsigned)shape.threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)shape.peers;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaLaunchKernelEx(&cfg, kern, in, adj, tokens, starts, freqs, cd, status, shape.slice,
+                           (uint64_t)0x8000000080000000ull) == cudaSuccess)
+      return RANS_OK;
+    (void)cudaGetLastError();
+    if (shape.peers <= 8) return RANS_ERR_CUDA;
+  }
 }
 
 template <bool DECODE>

@@ -483,21 +483,22 @@ class _Distill(torch.autograd.Function):
             stats.data_ptr(), _status(status, dev).data_ptr(), _raw_stream(dev)),
             "distill_forward")
         ctx.save_for_backward(logits, ids, logprobs, stats)
-        ctx.inv_temperature, ctx.rows = inv_temperature, rows
+        ctx.inv_temperature = inv_temperature
         return losses
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, grad_losses):
+        # (hooks on saved tensors may give back others than were saved)
         logits, ids, logprobs, stats = ctx.saved_tensors
-        rows = ctx.rows
+        rows, K, i, lp = _teacher(logits, ids, logprobs)
         dev, n, v = rows[:3]
-        grad = logits.new_empty((n, v))
-        g = grad_losses.contiguous()
+        s = _tensor(stats, torch.float32, (n, 8), dev, "stats")
         with _place(dev, None):
+            grad = logits.new_empty((n, v))
+            g = _tensor(grad_losses.contiguous(), torch.float32, (n,), dev, "grad_losses")
             L.check(L.lib().rans_distill_backward(
-                _packed(logits, rows), ids.data_ptr(), logprobs.data_ptr(), ids.shape[1],
-                ctx.inv_temperature, stats.data_ptr(), g.data_ptr(), grad.data_ptr(), v,
+                _packed(logits, rows), i, lp, K, ctx.inv_temperature, s, g, grad.data_ptr(), v,
                 _raw_stream(dev)), "distill_backward")
         return grad, None, None, None, None, None
 

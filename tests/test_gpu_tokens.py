@@ -746,6 +746,15 @@ def test_distill_through_autograd():
     assert torch.equal(y.grad, want)
     loss.backward()
     assert torch.equal(y.grad, want * 2)
+    # what is saved may come back elsewhere and with other strides
+    wide = torch.zeros(n, v + 3, device="cuda")
+    wide[:, :v] = x
+    y = wide[:, :v].detach().requires_grad_()
+    (here,) = torch.autograd.grad(rb.distill_loss(y, ti, tl).mean(), y)
+    with torch.autograd.graph.save_on_cpu():
+        loss = rb.distill_loss(y, ti, tl).mean()
+    (g,) = torch.autograd.grad(loss, y)
+    assert torch.equal(g, here)
     z = x.clone().requires_grad_()
     rb.distill_loss(z * 0.5, ti, tl).sum().backward()
     _, half = rb.distill_loss_and_grad(x * 0.5, ti, tl, torch.ones(n, device="cuda"))
