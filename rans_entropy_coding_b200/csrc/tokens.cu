@@ -100,10 +100,14 @@ __device__ __forceinline__ bool starts_by(uint64_t c, uint32_t r, uint64_t total
 // exchanges of 1 us.  Four blocks of 256 threads an SM instead of two of 512
 // took 398 us and 43 us; a first form that held a row in registers over
 // clusters of 8, 900 us and 108 us.
-// A warp takes "tiles" of 32 lanes x kTileVecs vectors of 16 bytes, lane after
+// A warp takes "tiles" of 32 lanes x row_vecs vectors of 16 bytes, lane after
 // lane and vector row after vector row, so that a tile is a run of consecutive
 // tokens whose sums a decoding row keeps.
-constexpr int kTileVecs = 4;
+// (Four vectors a lane; two where a row has tables or a mask, whose blocks have
+// few tiles each: 48 x 50021 f32 21 us against 23, 777 x 50021 fp16 the same;
+// without, 4096 x 131072 bf16 takes 425 us with two, 366 with four, 412 with
+// eight.)
+__host__ __device__ constexpr int row_vecs(bool adjusted) { return adjusted ? 2 : 4; }
 constexpr int kRowThreads = 512;  // most threads of a block
 constexpr int kRowWarps = kRowThreads / 32;
 constexpr int kMaxCluster = 16;
@@ -268,6 +272,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
                       uint32_t *freqs, Coded cd, int32_t *status, int slice, uint64_t zero2) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int N = VecOf<T>::N;
+  constexpr int kTileVecs = row_vecs(ADJ);
   constexpr int kVecRow = 32 * N;                // tokens of a warp's vectors
   constexpr int kTile = kVecRow * kTileVecs;
   TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
@@ -946,7 +951,7 @@ int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *
   const bool adjusted = touch || adj.mask;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
-  constexpr int kTile = 32 * VecOf<T>::N * kTileVecs;
+  const int tile = 32 * VecOf<T>::N * row_vecs(adjusted);
   // rows that all start on 16 bytes have no empty places before them
   const bool aligned = reinterpret_cast<uintptr_t>(in.data) % 16 == 0 &&
                        (in.rows == 1 || in.row_stride % VecOf<T>::N == 0);
@@ -954,10 +959,10 @@ int launch_rows_t(const rans_logits &in, const rans_adjust &adj, const int32_t *
   // clusters of 16 need a processor group with 16 multiprocessors free of
   // defects; where a launch finds none, 8 are always to be had
   for (int most = kMaxCluster;; most = 8) {
-    const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), kTile,
+    const RowShape shape = row_shape(in.rows, in.vocab + (aligned ? 0 : VecOf<T>::N - 1), tile,
                                      most, num_sms(dev));
     const uint32_t smem = (adjusted ? (uint32_t)sizeof(TouchTable) + kHashSpan / 8 : 0u) +
-                          (DECODE ? (uint32_t)(shape.slice / kTile * sizeof(uint2)) : 0u);
+                          (DECODE ? (uint32_t)(shape.slice / tile * sizeof(uint2)) : 0u);
     if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
     if (in.rows > 0x7fffffff / shape.peers) return RANS_ERR_ARG;
     cudaLaunchConfig_t cfg = {};
