@@ -299,8 +299,9 @@ class LogitAdjust:
     mask: int32 [rows, words] or [words] (for all rows) with 1 bits where
         tokens are allowed; see pack_mask.
 
-    The tensors are read by each call, so a program may keep one LogitAdjust
-    and update them in place between steps.
+    The tensors of history, bias and mask are read by each call, so a program
+    may keep one LogitAdjust and update them in place between steps (per-row
+    numbers are copied when it is made).
     """
 
     def __init__(self, temperature=1.0, repetition=1.0, frequency=0.0, presence=0.0,
