@@ -69,6 +69,14 @@ def _packed(x, rows):
     return _pack_logits(x.data_ptr(), rows[3], rows[2], rows[1], rows[4])
 
 
+def _device(x, what):
+    """The index of a CUDA tensor's device.  (Host tensors share -1: without this
+    they would all be "on one device".)"""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise ValueError("%s: a CUDA tensor" % what)
+    return x.get_device()
+
+
 def _tensor(x, dtype, shape, dev, what):
     """The address of a contiguous CUDA tensor of this type and shape on device
     `dev` (an index)."""
@@ -130,13 +138,17 @@ def _intervals(rows, logits, adjust, tokens, starts, freqs, status):
 
 def rans_encode_intervals(starts, freqs, n, chunking, out, stream_offsets, workspace,
                           stream=None):
+    dev = _device(starts, "starts")
     S = L.rans_num_streams(chunking, n)
-    with _place(starts.get_device(), stream):
+    with _place(dev, stream):
         return _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace)
 
 
 def _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace):
-    dev = starts.get_device()
+    dev = _device(starts, "starts")
+    # (the chunking's own tensor: explicit stream starts)
+    if chunking._keep is not None and _device(chunking._keep, "stream starts") != dev:
+        raise ValueError("chunking on %s, starts on cuda:%d" % (chunking._keep.device, dev))
     s = _tensor(starts, torch.int32, (n,), dev, "starts")
     f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
     o = _tensor(out, torch.uint8, None, dev, "out")
@@ -149,7 +161,7 @@ def _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace):
 
 def _streams(data, stream_offsets):
     """(device index, S, the two addresses)."""
-    dev = data.get_device()
+    dev = _device(data, "data")
     d = _tensor(data, torch.uint8, None, dev, "data")
     o = _tensor(stream_offsets, torch.int64, None, dev, "stream_offsets")
     S = stream_offsets.numel() - 1
@@ -191,7 +203,7 @@ def _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in, s
 
 
 def rans_token_states_finish(stream_offsets, states, status, stream=None):
-    dev = states.get_device()
+    dev = _device(states, "states")
     o = _tensor(stream_offsets, torch.int64, None, dev, "stream_offsets")
     S = stream_offsets.numel() - 1
     s = _tensor(states, torch.int64, (S, 2), dev, "states")
@@ -428,11 +440,12 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
     """(buffer, stream_offsets[S + 1], workspace): like encode_with_indexes;
     the coded bytes are buffer[:stream_offsets[-1]], device errors
     rans_get_status(workspace).  ws: a workspace to reuse."""
+    dev = _device(starts, "starts")
     n = starts.numel()
     S = L.rans_num_streams(chunking, n)
     if S < 0:
         L.check(int(S), "num_streams")
-    with _place(starts.get_device(), stream):
+    with _place(dev, stream):
         if ws is None:
             # torch's blocks are aligned to 512 bytes, as the workspace has to be to 256
             ws = starts.new_empty(L.rans_encode_workspace_bytes(chunking, n), dtype=torch.uint8)

@@ -213,3 +213,46 @@ def test_oracle_coder_round_trip():
     d = TO.Decoder(data)
     assert [d.step(b) for _ in tokens] == list(tokens)
     assert d.x == TO.LOW and d.at == len(d.words)
+
+
+# ------------------------------------------------------ the Python layer --
+class Untouchable:
+    """A library whose every call is a failure of the checks before it."""
+
+    def __getattr__(self, name):
+        raise AssertionError("%s was called" % name)
+
+
+def test_host_tensors_never_reach_the_library(monkeypatch):
+    """Every tensor on the host: no entry point may take its addresses for
+    device ones (and the calls that need no logits have only these checks)."""
+    i32 = torch.zeros(8, dtype=torch.int32)
+    data = torch.zeros(64, dtype=torch.uint8)
+    offs = torch.tensor([0, 32, 64])
+    states = torch.zeros(2, 2, dtype=torch.int64)
+    status = torch.zeros(32, dtype=torch.int64)
+    x = torch.zeros(2, 8)
+    two, chunks = i32[:2].clone(), rb.Chunking.contig(2)
+    buf = torch.zeros(4096, dtype=torch.uint8)
+    ids, lp = torch.zeros(2, 1, dtype=torch.int32), torch.zeros(2, 1)
+    w, stats = torch.zeros(2), torch.zeros(2, 8)
+    monkeypatch.setattr(rb.tokens.L, "lib", lambda: Untouchable())
+    monkeypatch.setattr(rb.tokens.L, "rans_num_streams", lambda chunking, n: 2)
+    for call in (
+            lambda: rb.encode_intervals(i32, i32, chunks),
+            lambda: rb.rans_encode_intervals(i32, i32, 8, chunks, buf, offs, buf),
+            lambda: rb.token_states(data, offs),
+            lambda: rb.token_states(data, offs, status),
+            lambda: rb.rans_token_states(data, offs, states, status),
+            lambda: rb.rans_token_states_finish(offs, states, status),
+            lambda: rb.decode_tokens(x, data, offs, states),
+            lambda: rb.rans_decode_tokens(x, None, data, offs, None, states, states, two, status),
+            lambda: rb.token_intervals(x, two),
+            lambda: rb.rans_token_intervals(x, None, two, two, two, status),
+            lambda: rb.rans_adjust_logits(x, None, x),
+            lambda: rb.rans_distill(x, ids, lp, 1.0, True, w, w, x, status),
+            lambda: rb.rans_distill_forward(x, ids, lp, 1.0, True, w, stats, status),
+            lambda: rb.rans_distill_backward(x, ids, lp, 1.0, stats, w, x),
+            lambda: rb.encode_intervals([1, 2], [1, 2], chunks)):
+        with pytest.raises(ValueError):
+            call()
