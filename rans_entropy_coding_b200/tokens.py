@@ -94,6 +94,10 @@ def new_status(device="cuda"):
 
 
 def _status(status, dev):
+    """The call's status word.  Like every tensor whose address goes to the
+    library, it has to be held by a name until the call returns: the calls
+    release the interpreter's lock, and memory that another thread was given
+    meanwhile would be written to."""
     if status is None:
         return new_status(dev)
     if not isinstance(status, torch.Tensor) or status.get_device() != dev or \
@@ -132,8 +136,9 @@ def _intervals(rows, logits, adjust, tokens, starts, freqs, status):
     t = _tensor(tokens, torch.int32, (n,), dev, "tokens")
     s = _tensor(starts, torch.int32, (n,), dev, "starts")
     f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
+    status = _status(status, dev)
     return L.lib().rans_token_intervals(_packed(logits, rows), _ref(adjust, rows), t, s, f,
-                                        _status(status, dev).data_ptr(), _raw_stream(dev))
+                                        status.data_ptr(), _raw_stream(dev))
 
 
 def rans_encode_intervals(starts, freqs, n, chunking, out, stream_offsets, workspace,
@@ -174,8 +179,9 @@ def rans_token_states(data, stream_offsets, states, status, stream=None):
     dev, S, d, o = _streams(data, stream_offsets)
     s = _tensor(states, torch.int64, (S, 2), dev, "states")
     with _place(dev, stream):
-        return L.lib().rans_token_states(d, data.numel(), o, S, s,
-                                         _status(status, dev).data_ptr(), _raw_stream(dev))
+        status = _status(status, dev)
+        return L.lib().rans_token_states(d, data.numel(), o, S, s, status.data_ptr(),
+                                         _raw_stream(dev))
 
 
 def rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states_in, states_out,
@@ -197,9 +203,10 @@ def _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in, s
     a = _tensor(states_in, torch.int64, (S, 2), dev, "states")
     b = _tensor(states_out, torch.int64, (S, 2), dev, "states_out")
     t = _tensor(tokens, torch.int32, (n,), dev, "tokens")
+    status = _status(status, dev)
     return L.lib().rans_decode_tokens(
         _packed(logits, rows), _ref(adjust, rows), d, data.numel(), o, S, ids, a, b, t,
-        _status(status, dev).data_ptr(), _raw_stream(dev))
+        status.data_ptr(), _raw_stream(dev))
 
 
 def rans_token_states_finish(stream_offsets, states, status, stream=None):
@@ -208,8 +215,8 @@ def rans_token_states_finish(stream_offsets, states, status, stream=None):
     S = stream_offsets.numel() - 1
     s = _tensor(states, torch.int64, (S, 2), dev, "states")
     with _place(dev, stream):
-        return L.lib().rans_token_states_finish(o, S, s, _status(status, dev).data_ptr(),
-                                                _raw_stream(dev))
+        status = _status(status, dev)
+        return L.lib().rans_token_states_finish(o, S, s, status.data_ptr(), _raw_stream(dev))
 
 
 def _teacher(logits, ids, logprobs, rows=None):
@@ -229,9 +236,10 @@ def rans_distill_forward(logits, ids, logprobs, inv_temperature, tail, losses, s
     o = _tensor(losses, torch.float32, (n,), dev, "losses")
     s = _tensor(stats, torch.float32, (n, 8), dev, "stats")
     with _place(dev, stream):
+        status = _status(status, dev)
         return L.lib().rans_distill_forward(
             _packed(logits, rows), i, lp, K, inv_temperature, int(tail), o, s,
-            _status(status, dev).data_ptr(), _raw_stream(dev))
+            status.data_ptr(), _raw_stream(dev))
 
 
 def _grad_of(rows, grad):
@@ -268,9 +276,9 @@ def _both(rows, logits, ids, logprobs, inv_temperature, tail, grad_losses, losse
     w = _tensor(grad_losses, torch.float32, (n,), dev, "weights")
     o = _tensor(losses, torch.float32, (n,), dev, "losses")
     g, step = _grad_of(rows, grad)
+    status = _status(status, dev)
     return L.lib().rans_distill(_packed(logits, rows), i, lp, K, inv_temperature, int(tail),
-                                w, o, g, step, _status(status, dev).data_ptr(),
-                                _raw_stream(dev))
+                                w, o, g, step, status.data_ptr(), _raw_stream(dev))
 
 
 # ----------------------------------------------------------------- helpers --
@@ -492,10 +500,10 @@ class _Distill(torch.autograd.Function):
         dev, n = rows[:2]
         losses = logits.new_empty(n, dtype=torch.float32)
         stats = logits.new_empty((n, 8), dtype=torch.float32)
+        status = _status(status, dev)
         L.check(L.lib().rans_distill_forward(
             _packed(logits, rows), i, lp, K, inv_temperature, int(tail), losses.data_ptr(),
-            stats.data_ptr(), _status(status, dev).data_ptr(), _raw_stream(dev)),
-            "distill_forward")
+            stats.data_ptr(), status.data_ptr(), _raw_stream(dev)), "distill_forward")
         ctx.save_for_backward(logits, ids, logprobs, stats)
         ctx.inv_temperature = inv_temperature
         return losses
@@ -510,7 +518,8 @@ class _Distill(torch.autograd.Function):
         s = _tensor(stats, torch.float32, (n, 8), dev, "stats")
         with _place(dev, None):
             grad = logits.new_empty((n, v))
-            g = _tensor(grad_losses.contiguous(), torch.float32, (n,), dev, "grad_losses")
+            grad_losses = grad_losses.contiguous()
+            g = _tensor(grad_losses, torch.float32, (n,), dev, "grad_losses")
             L.check(L.lib().rans_distill_backward(
                 _packed(logits, rows), i, lp, K, ctx.inv_temperature, s, g, grad.data_ptr(), v,
                 _raw_stream(dev)), "distill_backward")

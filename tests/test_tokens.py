@@ -1,6 +1,8 @@
 """Tokens under a model's logits, without a GPU: refusals at the C entry
 points and in the Python layer, the mask packing, and the oracle's own coder."""
+import contextlib
 import ctypes
+import weakref
 
 import numpy as np
 import pytest
@@ -256,3 +258,72 @@ def test_host_tensors_never_reach_the_library(monkeypatch):
             lambda: rb.encode_intervals([1, 2], [1, 2], chunks)):
         with pytest.raises(ValueError):
             call()
+
+
+class Watching:
+    """A library that asks, in every call, whether the tensors whose addresses
+    it was given are still there."""
+
+    def __init__(self):
+        self.refs, self.calls = [], []
+
+    def __getattr__(self, name):
+        def call(*args):
+            mine = [r for a, r in self.refs if a in args]
+            self.calls.append((name, len(mine), [r() is not None for r in mine]))
+            self.refs.clear()
+            return rb.OK
+        return call
+
+
+@pytest.fixture
+def watched(monkeypatch):
+    """The Python layer on host tensors, with a Watching in the library's place."""
+    T, lib = rb.tokens, Watching()
+
+    def note(x):
+        lib.refs.append((x.data_ptr(), weakref.ref(x)))
+        return x
+
+    def rows_of(x, what="logits"):
+        return 0, x.shape[0], x.shape[1], 0, x.shape[1]
+
+    monkeypatch.setattr(T, "_rows", rows_of)
+    monkeypatch.setattr(T, "_tensor", lambda x, *args: note(x).data_ptr())
+    monkeypatch.setattr(T, "_device", lambda x, what: 0)
+    monkeypatch.setattr(T, "_place", lambda dev, stream: contextlib.nullcontext())
+    monkeypatch.setattr(T, "_raw_stream", lambda dev: 0)
+    # (an allocation that nothing else holds; its address is its own)
+    monkeypatch.setattr(T, "new_status",
+                        lambda dev="cuda": note(torch.zeros(1 << 16, dtype=torch.int64)))
+    monkeypatch.setattr(T, "_status", lambda status, dev: T.new_status() if status is None
+                        else note(status))
+    monkeypatch.setattr(T.L, "lib", lambda: lib)
+    return lib
+
+
+def test_what_a_call_reads_outlives_it(watched):
+    x, ids, lp = torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    i32 = torch.zeros(3, dtype=torch.int32)
+    data, offs = torch.zeros(64, dtype=torch.uint8), torch.tensor([0, 16, 32, 48])
+    states, w = torch.zeros(3, 2, dtype=torch.int64), torch.zeros(3)
+    stats = torch.zeros(3, 8)
+    rb.token_intervals(x, i32)
+    rb.rans_token_intervals(x, None, i32, i32, i32, None)
+    rb.token_states(data, offs)
+    rb.rans_token_states(data, offs, states, None)
+    rb.decode_tokens(x, data, offs, states)
+    rb.rans_decode_tokens(x, None, data, offs, None, states, states, i32, None)
+    rb.rans_token_states_finish(offs, states, None)
+    rb.rans_distill_forward(x, ids, lp, 1.0, True, w, stats, None)
+    rb.rans_distill(x, ids, lp, 1.0, True, w, w, x, None)
+    rb.distill_loss_and_grad(x, ids, lp, w)
+    assert len(watched.calls) == 10
+    y = x.clone().requires_grad_()
+    # (distill_loss itself asks for CUDA logits)
+    for reduce in (torch.sum, torch.mean, lambda t: (t * w).sum()):
+        reduce(rb.tokens._Distill.apply(y, ids, lp, 1.0, True, None)).backward()
+    names = [c[0] for c in watched.calls]
+    assert names[10:] == ["rans_distill_forward", "rans_distill_backward"] * 3
+    for name, seen, alive in watched.calls:
+        assert seen >= 2 and all(alive), (name, alive)
