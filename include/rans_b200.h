@@ -521,7 +521,9 @@ typedef struct rans_logits {
  */
 typedef struct rans_adjust {
     /* for all rows, when `params` is NULL: repetition and inv_temperature
-     * positive and finite, frequency and presence finite */
+     * positive and finite, frequency and presence finite.  (inv_temperature is
+     * taken as it is; the Python layer makes it from a temperature T, a number
+     * or a row's, as the float32 nearest to 1 / float32(T).) */
     float repetition, frequency, presence, inv_temperature;
     const float *params;           /* device: the same four per row, or NULL */
     const int32_t *history;        /* device int32[history_len], or NULL */

@@ -296,6 +296,20 @@ def _finite(x, what):
     return x
 
 
+def _in_float32(x, check, what):
+    """A number as float32 has it, checked there (where 1e-50 is not positive
+    and 1e39 not finite)."""
+    return check(ctypes.c_float(float(x)).value, what)
+
+
+def _inverse(temperature):
+    """1 / T of a number, as the per-row form has it: T rounded to float32 and
+    its reciprocal rounded once more.  (A double reciprocal of the number itself
+    is another float32 for 0.85 or 1.1, and other intervals.)"""
+    t = _in_float32(temperature, _positive, "temperature")
+    return _in_float32(1.0 / t, _positive, "1 / temperature")
+
+
 def pack_mask(allowed):
     """Words of a bool tensor [rows, vocab] (or [vocab]) of allowed tokens, as
     LogitAdjust takes them: bit v & 31 of word v >> 5."""
@@ -311,7 +325,9 @@ class LogitAdjust:
     """What is done to rows of logits before they are used.
 
     temperature, repetition, frequency, presence: numbers for all rows, or
-        float32 CUDA tensors [rows] (any of them).
+        float32 CUDA tensors [rows] (any of them).  A number is rounded to
+        float32, and the logits are multiplied by the temperature's reciprocal,
+        rounded to float32: a number and rows that hold it code alike.
     history: (tokens int32, begin int64 [rows], end int64 [rows]): row r's
         history is tokens[begin[r]:end[r]].
     bias: (ids int32, values float32, begin int64 [rows], end int64 [rows]);
@@ -335,10 +351,9 @@ class LogitAdjust:
                 isinstance(frequency, tensor) or isinstance(presence, tensor):
             params = self._per_row((repetition, frequency, presence, temperature))
         else:
-            scalars = (_positive(repetition, "repetition"), _finite(frequency, "frequency"),
-                       _finite(presence, "presence"),
-                       _positive(1.0 / _positive(temperature, "temperature"),
-                                 "1 / temperature"))
+            scalars = (_in_float32(repetition, _positive, "repetition"),
+                       _in_float32(frequency, _finite, "frequency"),
+                       _in_float32(presence, _finite, "presence"), _inverse(temperature))
         hist = (0, 0, 0, 0)
         if history is not None:
             tokens, begin, end = history
@@ -387,7 +402,8 @@ class LogitAdjust:
                 torch.full((n,), float(x), device=one.device) for x in parts]
         for x in cols:
             _tensor(x, torch.float32, (n,), dev, "per-row parameters")
-        cols[3] = 1.0 / cols[3]
+        # (a float32's reciprocal in double, rounded to float32, is correctly rounded)
+        cols[3] = cols[3].double().reciprocal().float()
         rows = torch.stack(cols, 1)
         self._keep += (rows,)
         return rows.data_ptr()

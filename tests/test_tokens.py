@@ -3,6 +3,7 @@ points and in the Python layer, the mask packing, and the oracle's own coder."""
 import contextlib
 import ctypes
 import weakref
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -327,3 +328,22 @@ def test_what_a_call_reads_outlives_it(watched):
     assert names[10:] == ["rans_distill_forward", "rans_distill_backward"] * 3
     for name, seen, alive in watched.calls:
         assert seen >= 2 and all(alive), (name, alive)
+
+
+def test_a_number_and_a_row_that_holds_it_have_the_same_reciprocal():
+    """The float32 nearest to 1 / float32(T), here from exact fractions."""
+    for i in range(1, 800):
+        t = i / 200
+        f = np.float32(t)
+        exact = 1 / Fraction(float(f))
+        near = np.float32(float(exact))
+        best = min((np.nextafter(near, np.float32(0)), near, np.nextafter(near, np.float32(9))),
+                   key=lambda c: abs(Fraction(float(c)) - exact))
+        assert np.float32(rb.tokens._inverse(t)) == best, t
+        assert torch.tensor([f]).double().reciprocal().float().item() == best, t
+        assert rb.LogitAdjust(temperature=t)._c[12:16] == best.tobytes(), t
+    for kw in (dict(repetition=1e-50), dict(repetition=1e39), dict(frequency=1e39),
+               dict(presence=-1e39), dict(temperature=1e-50), dict(temperature=1e-39),
+               dict(temperature=1e39)):
+        with pytest.raises(ValueError):
+            rb.LogitAdjust(**kw)
