@@ -395,13 +395,21 @@ class LogitAdjust:
         self._c = _pack_adjust(*scalars, params, *hist, *extra, *allowed)
 
     def _per_row(self, parts):
-        """Address of the parameters [rows, 4], numbers widened to all rows."""
+        """Address of the parameters [rows, 4], numbers checked and widened to
+        all rows."""
         one = [x for x in parts if isinstance(x, torch.Tensor)][0]
         dev, n = self._on(one, one.numel()), one.numel()
-        cols = [x if isinstance(x, torch.Tensor) else
-                torch.full((n,), float(x), device=one.device) for x in parts]
-        for x in cols:
-            _tensor(x, torch.float32, (n,), dev, "per-row parameters")
+        cols = []
+        for x, check, what in zip(parts, (_positive, _finite, _finite, _positive),
+                                  ("repetition", "frequency", "presence", "temperature")):
+            if isinstance(x, torch.Tensor):
+                _tensor(x, torch.float32, (n,), dev, "per-row " + what)
+            else:
+                if what == "temperature":
+                    _inverse(x)  # (it has to have one)
+                x = torch.full((n,), _in_float32(x, check, what), dtype=torch.float32,
+                               device=one.device)
+            cols.append(x)
         # (a float32's reciprocal in double, rounded to float32, is correctly rounded)
         cols[3] = cols[3].double().reciprocal().float()
         rows = torch.stack(cols, 1)

@@ -347,3 +347,25 @@ def test_a_number_and_a_row_that_holds_it_have_the_same_reciprocal():
                dict(temperature=1e39)):
         with pytest.raises(ValueError):
             rb.LogitAdjust(**kw)
+
+
+def test_numbers_beside_per_row_tensors_are_checked_too(monkeypatch):
+    """... and are float32 whatever the default type is."""
+    monkeypatch.setattr(rb.LogitAdjust, "_on", lambda self, x, n: -1)
+    rows = torch.full((3,), 0.7)
+    for kw in (dict(repetition=-1.0), dict(repetition=0.0), dict(repetition=1e39),
+               dict(frequency=float("nan")), dict(presence=float("inf"))):
+        with pytest.raises(ValueError):
+            rb.LogitAdjust(temperature=rows, **kw)
+    for t in (0.0, -1.0, float("inf"), float("nan"), 1e39, 1e-39):
+        with pytest.raises(ValueError):
+            rb.LogitAdjust(repetition=rows, temperature=t)
+    torch.set_default_dtype(torch.float64)
+    try:
+        a = rb.LogitAdjust(temperature=rows, repetition=1.1, frequency=0.25)
+    finally:
+        torch.set_default_dtype(torch.float32)
+    params = a._keep[-1]
+    assert params.dtype == torch.float32 and params.shape == (3, 4)
+    want = np.array([1.1, 0.25, 0.0, 1 / np.float32(0.7)], np.float32)
+    assert np.array_equal(params.numpy(), np.tile(want, (3, 1)))
