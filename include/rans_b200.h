@@ -628,7 +628,8 @@ int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S, const ui
  * student's mass outside the list:
  *   tail != 0: p_t = max(0, 1 - sum p);
  *     loss = sum p_i (log p_i - log q_i) + p_t (log p_t - log q_t)
- *   tail == 0: p_i /= sum p, p_t = 0.
+ *   tail == 0: p_i /= sum p, p_t = 0 (the list may be normalised or not: only
+ *     differences of its log probabilities count).
  * With K = 1 and log probability 0 the loss is the token's own code length.
  *   d loss / d logit v = inv_temperature * (P q_v - p_v) for listed v,
  *                        inv_temperature * (P - p_t / q_t) q_v for others,

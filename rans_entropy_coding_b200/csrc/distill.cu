@@ -83,8 +83,9 @@ struct RowStats {
   float m_all;   // m
   float inv_z;   // 1 / Z
   float mass;    // P
-  float inv_p;   // 1 / sum p without a tail (0: no entry left), else 1
-  float pad[2];
+  float inv_p;   // 1 / sum e^(log p - base) without a tail (0: no entry left), else 1
+  float base;    // the list's largest log probability without a tail, else 0
+  float pad;
 };
 static_assert(sizeof(RowStats) == 32, "8 floats");
 
@@ -132,32 +133,43 @@ struct ListSums {
   double m;      // largest of their logits (0 if none is finite)
   bool some;     // one is
   double z;      // e^(inv_t (z - m))
+  float base;    // what is taken off their log probabilities; p = e^(log p - base)
   double p;      // p
   double plp;    // p log p
   double pz;     // p inv_t (z - m), where p > 0
   double count;
 };
 
-// By one warp; `first` holds the list's first chunk.  (Not inlined, nor
+// By one warp; `first` holds the list's first chunk.  Without a tail only ratios
+// of the list's probabilities count, so they are taken against the largest one:
+// a list far from normalised (log probabilities of +-100, say) stays in float's
+// range.  (Not inlined, nor
 // row_loss: the streaming warps' registers are not to pay for the double
 // arithmetic of these.)
 template <typename T>
 __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, const int32_t *ids,
                                            const float *lp, int K, int vocab, double it,
-                                           int lane) {
+                                           bool tail, int lane) {
   Entries e = first;
-  float m = kNegInf;
+  float m = kNegInf, base = kNegInf;
   for (int from = 0; from < K; from += kChunk) {
     if (from > 0) {
       load_entries(e, ids, lp, from, K, vocab, lane, 0, nullptr);
       load_logits(e, z);
     }
 #pragma unroll
-    for (int j = 0; j < kEntries; ++j) m = fmaxf(m, e.z[j]);
+    for (int j = 0; j < kEntries; ++j) {
+      m = fmaxf(m, e.z[j]);
+      if (e.v[j] >= 0) base = fmaxf(base, e.lp[j]);
+    }
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-  ListSums s = {m == kNegInf ? 0.0 : (double)m, m != kNegInf, 0, 0, 0, 0, 0};
+  for (int o = 16; o > 0; o >>= 1) {
+    m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    base = fmaxf(base, __shfl_xor_sync(kFull, base, o));
+  }
+  if (tail || base == kNegInf) base = 0.0f;
+  ListSums s = {m == kNegInf ? 0.0 : (double)m, m != kNegInf, 0, base, 0, 0, 0, 0};
   for (int from = 0; from < K; from += kChunk) {
     if (K > kChunk) {
       load_entries(e, ids, lp, from, K, vocab, lane, 0, nullptr);
@@ -166,7 +178,7 @@ __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, con
 #pragma unroll
     for (int j = 0; j < kEntries; ++j) {
       if (e.v[j] < 0) continue;
-      const double l = (double)e.lp[j], d = ((double)e.z[j] - s.m) * it, p = exp(l);
+      const double l = (double)e.lp[j] - (double)base, d = ((double)e.z[j] - s.m) * it, p = exp(l);
       s.z += exp(d);
       s.p += p;
       s.plp += p > 0.0 || p != p ? p * l : 0.0;
@@ -186,14 +198,16 @@ __device__ __noinline__ ListSums list_sums(const Entries &first, const T *z, con
 struct ListFigures {
   float m;     // largest of its logits (-inf: none is finite)
   float z;     // e^(inv_t (z - m)), summed
-  float mass, pt, norm;
-  bool ignored;  // no entry left, and no tail
+  float mass, pt, norm, base;
+  bool ignored;  // no entry left
 };
 __device__ __forceinline__ ListFigures list_figures(const ListSums &s, bool tail, int vocab) {
-  const double norm = tail ? 1.0 : (s.p > 0.0 ? 1.0 / s.p : 0.0);
+  const bool ignored = s.count == 0.0;
+  // (a sum of p without a tail is at least 1)
+  const double norm = tail ? 1.0 : (ignored ? 0.0 : 1.0 / s.p);
   const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
   return {s.some ? (float)s.m : kNegInf, (float)s.z, (float)(s.p * norm + pt), (float)pt,
-          (float)norm, !tail && !(s.p > 0.0) && s.p == s.p};
+          (float)norm, s.base, ignored};
 }
 
 // The row's figures from the list's and R, the sum of 2^(c z - offset) over the
@@ -222,7 +236,8 @@ __device__ __forceinline__ RowStats row_figures(const ListFigures &s, float R, f
   st.inv_z = 1.0f / z;
   st.mass = s.mass;
   st.inv_p = s.norm;
-  st.pad[0] = st.pad[1] = 0.0f;
+  st.base = s.base;
+  st.pad = 0.0f;
   return st;
 }
 
@@ -238,7 +253,7 @@ __device__ __noinline__ float row_loss(const ListSums &s, double R, float m_rest
   const double rest = some ? R * exp(((double)m_rest - m) * it + back) : 0.0;
   const double top = s.some || s.z != s.z ? s.z * exp((s.m - m) * it) : 0.0;
   const double z = rest + top, lz = log(z);
-  if (!tail && !(s.p > 0.0) && s.p == s.p) return z == z ? 0.0f : (float)z;
+  if (s.count == 0.0) return z == z ? 0.0f : (float)z;
   const double norm = tail ? 1.0 : 1.0 / s.p;
   const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
   double part = 0.0;
@@ -410,7 +425,8 @@ __global__ void __launch_bounds__(kDisThreads, 4)
     __syncthreads();
     read_listed();
     if (lists) {
-      sums = list_sums(e, row.at0 + row.shift, ids, lp, K, in.vocab, (double)inv_t, lane);
+      sums = list_sums(e, row.at0 + row.shift, ids, lp, K, in.vocab, (double)inv_t,
+                       tail != 0, lane);
       if (lane == 0) list = list_figures(sums, tail != 0, in.vocab);
     } else {
       // R, against each lane's running maximum
@@ -545,7 +561,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
     __syncthreads();  // the listed tokens' gradients go over what stands there
     auto write = [&](int v, float l, float z) {
       const float q = expf((z - st.m_all) * inv_t) * st.inv_z;
-      const float p = expf(l) * st.inv_p;
+      const float p = expf(l - st.base) * st.inv_p;
       o[row.shift + v] = float_logit<T>((st.mass * q - p) * inv_t * g);
     };
     if (lists) {

@@ -47,3 +47,63 @@ def test_texts_coded_under_a_number_decode_under_rows_of_it(T):
         got = c.step(x[t:t + 1].expand(n, v).contiguous(), many)
         assert got.tolist() == tok[:, t].tolist()
     c.finish()
+
+
+# ----------------------------------------------------------- distillation --
+def both_ways(x, ids, lp, w, T=1.0, tail=True, st=None):
+    """(losses, gradient) in one call, and by autograd."""
+    ti, tl, tw = (torch.from_numpy(np.ascontiguousarray(a)).cuda() if isinstance(a, np.ndarray)
+                  else a for a in (ids, lp, w))
+    yield rb.distill_loss_and_grad(x, ti, tl, tw, T, tail, status=st)
+    y = x.detach().requires_grad_()
+    losses = rb.distill_loss(y, ti, tl, T, tail, status=st)
+    (grad,) = torch.autograd.grad(losses, y, tw)
+    yield losses.detach(), grad
+
+
+@pytest.mark.parametrize("shift", [0.0, 64.0, -64.0, 128.0, -128.0, -1024.0, 1e30, -1e30])
+@pytest.mark.parametrize("K", [3, 128, 300])
+def test_lists_without_a_tail_count_by_their_differences(K, shift):
+    """Log probabilities moved as a whole, as unnormalised scores are.  The
+    multiples of 2^-10 here stay exact under the shift (to 1024 + 16: 21 bits),
+    so moved and unmoved lists are the same teacher; at 1e30 all entries
+    are equal."""
+    n, v = 4, 3001
+    x = make_logits(n, v, F32, 3, seed=32)
+    ids, lp = teacher(n, v, K, K, False)
+    if K == 3:
+        ids[0], lp[0] = -1, -np.inf     # a row without entries
+    lp = (np.round(lp * 1024) / 1024).astype(np.float32)
+    moved = (lp + np.float32(shift)).astype(np.float32)
+    if abs(shift) <= 1024:
+        assert np.array_equal(moved - np.float32(shift), lp)
+    else:
+        lp = np.where(np.isinf(lp), lp, np.float32(0))
+    g = np.array([1.0, -0.5, 2.0, 1.0], np.float32)
+    st = rb.new_status()
+    same = list(both_ways(x, ids, lp, g, tail=False, st=st))
+    for a, b in zip(both_ways(x, ids, moved, g, tail=False, st=st), same):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+        check_distill(x, ids, lp, 1.0, False, g, *a)
+    status_ok(st)
+
+
+def test_rows_without_entries_add_nothing_at_all():
+    """Padding of a batch, whatever its logits are (but for NaN and +inf)."""
+    n, v = 4, 900
+    x = make_logits(n, v, BF16, 1, seed=33)
+    x[2] = -math.inf
+    x[3, 5:] = -math.inf
+    w = torch.ones(n, device="cuda")
+    none = np.full((n, 2), -1, np.int32), np.full((n, 2), -0.5, np.float32)
+    gone = np.full((n, 2), 3, np.int32), np.full((n, 2), -np.inf, np.float32)
+    for tail in (True, False):
+        for ids, lp in (none, gone):
+            for losses, grad in both_ways(x, ids, lp, w, tail=tail):
+                assert losses.tolist() == [0.0] * n and not bool(grad.any())
+                assert not bool(grad.isnan().any())
+    # entries that are there, however unlikely, are not absent
+    far = np.array([[7, 9]] * n, np.int32), np.full((n, 2), -2000.0, np.float32)
+    for losses, grad in both_ways(x[:2], far[0][:2], far[1][:2], w[:2], tail=False):
+        check_distill(x[:2], far[0][:2], far[1][:2] + 2000, 1.0, False, np.ones(2), losses, grad)
+        assert float(losses.min()) > 0
