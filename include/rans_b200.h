@@ -637,7 +637,9 @@ int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S, const ui
  * Entries with id -1 or log probability -inf are absent; a row with none left
  * gives loss 0 and gradient 0.  If the entries list the whole vocabulary there
  * is no tail and p_t = 0.  A student with no mass where the teacher has some
- * has loss +inf.  Rows with a NaN or +inf logit give NaN.  An id outside the
+ * has loss +inf.  Rows with a NaN or +inf logit give NaN, and so do rows with
+ * entries and no logit above -inf.  Finite logits may be as large as the type
+ * holds (a mask's lowest value among them).  An id outside the
  * vocabulary, or listed twice in a row, is RANS_ERR_INDEX in `status` (as for
  * rans_token_intervals); the row's results are then undefined.
  *   ids: device int32[rows][K]; logprobs: device float[rows][K];

@@ -3,12 +3,15 @@
 //
 // Write c = inv_temperature * log2(e).  The listed tokens are few: their terms
 // are summed in double.  All others only enter through their own sum
-//   R = sum over others of 2^(c z - s),   s = c * (their largest logit), rounded,
+//   R = sum over others of 2^(c (z - s)),   s = their largest logit,
 // so that a student's small tail mass keeps its precision (1 - sum q would lose
 // it).  With m the row's largest logit and Z = sum of e^(inv_t (z - m)) over all,
-// the gradient of an unlisted token is 2^(c z - s) times one factor per row,
-// inv_t (P q_t - p_t) / R: one multiply-add, one exponential and one product,
-// with no difference of close numbers per element.
+// the gradient of an unlisted token is 2^(c (z - s)) times one factor per row,
+// inv_t (P q_t - p_t) / R: one difference, two products and one exponential, with
+// no difference of close numbers but z - s, which is exact where it is small.
+// (As one multiply-add, c z - c s, the rounding of c s stays in every exponent:
+// past logits of 10^10, as masks have them, that is more than the exponential's
+// range.)
 //
 // A row is walked twice, once for R and once for the gradient; the second walk
 // finds most of it in L2.  With many rows a block takes a row; with few, a
@@ -37,7 +40,6 @@ constexpr int kDisVecs = 4;
 constexpr int kDisCluster = 8;
 constexpr uint32_t kRingBytes = kStreamWarps * 2 * kDisVecs * 32 * 16;
 constexpr double kLog2eD = 1.4426950408889634;
-constexpr double kLn2D = 0.6931471805599453;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -55,10 +57,11 @@ __device__ __forceinline__ float2 unpair(uint64_t x) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
   return f;
 }
-// 2^(c z - off) of two logits; c2 and off2 hold c and -off twice.
-__device__ __forceinline__ float2 exp2_pair(float a, float b, uint64_t c2, uint64_t off2) {
+// 2^(c (z - s)) of two logits; c2 and s2 hold c and -s twice.
+__device__ __forceinline__ float2 exp2_pair(float a, float b, uint64_t c2, uint64_t s2) {
   uint64_t x;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(x) : "l"(pair(a, b)), "l"(c2), "l"(off2));
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(pair(a, b)), "l"(s2));
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(x), "l"(c2));
   const float2 f = unpair(x);
   return make_float2(exp2_fast(f.x), exp2_fast(f.y));
 }
@@ -78,7 +81,7 @@ __device__ __forceinline__ float vector_max(const uint4 &q, T) {
 
 // Per-row figures from the forward pass to the backward one (8 floats).
 struct RowStats {
-  float offset;  // s
+  float others;  // s, the unlisted tokens' largest logit
   float rest;    // inv_t (P q_t - p_t) / R, the unlisted tokens' factor
   float m_all;   // m
   float inv_z;   // 1 / Z
@@ -210,28 +213,28 @@ __device__ __forceinline__ ListFigures list_figures(const ListSums &s, bool tail
           (float)norm, s.base, ignored};
 }
 
-// The row's figures from the list's and R, the sum of 2^(c z - offset) over the
-// unlisted tokens, whose largest logit is m_rest (-inf: none has a finite one).
+// The row's figures from the list's and R, the sum of 2^(c (z - m_rest)) over the
+// unlisted tokens, whose largest logit is m_rest (-inf: none has a finite one;
+// else R is 1 at least).
 // Every thread computes them for itself: in double, by one thread for all to
 // wait for, this stood between the two walks for 10,000 cycles of a row's
 // 100,000.  The difference P q_t - p_t is of numbers that float holds to 1e-7,
 // as exact as the gradient's own terms.
 __device__ __forceinline__ RowStats row_figures(const ListFigures &s, float R, float m_rest,
-                                                float offset, float c, float inv_t) {
+                                                float c, float inv_t) {
   const bool some = R > 0.0f || R != R;
   float m = fmaxf(s.m, some ? m_rest : kNegInf);
   if (m == kNegInf) m = 0.0f;
-  // against m, with the offset's rounding taken back
-  const float back = fmaf(-c, m_rest, offset);
-  const float rest = some ? R * exp2_fast((m_rest - m) * c + back) : 0.0f;
+  const float rest = some ? R * exp2_fast((m_rest - m) * c) : 0.0f;
   const float top = s.m > kNegInf || s.z != s.z
                         ? s.z * exp2_fast(((s.m > kNegInf ? s.m : 0.0f) - m) * c)
                         : 0.0f;
   const float z = rest + top;
   RowStats st;
-  st.offset = some ? offset : 0.0f;
+  st.others = some ? m_rest : 0.0f;
   st.rest = some && !s.ignored ? inv_t * (s.mass * (rest / z) - s.pt) / R : 0.0f;
-  if (z != z) st.rest = z;
+  if (!(z > 0.0f) && !(s.ignored && z == 0.0f))  // a bad logit, or none above -inf
+    st.rest = __int_as_float(0x7fffffff);
   st.m_all = m;
   st.inv_z = 1.0f / z;
   st.mass = s.mass;
@@ -243,17 +246,17 @@ __device__ __forceinline__ RowStats row_figures(const ListFigures &s, float R, f
 
 // sum p (log p - log q) over the list and the tail, in double, by the listing
 // warp's first thread while the others go on.
-__device__ __noinline__ float row_loss(const ListSums &s, double R, float m_rest, float offset,
-                                       float c, float inv_t, bool tail, int vocab) {
+__device__ __noinline__ float row_loss(const ListSums &s, double R, float m_rest, float inv_t,
+                                       bool tail, int vocab) {
   const double it = (double)inv_t;
   const bool some = R > 0.0 || R != R;
   double m = fmax(s.some ? s.m : -HUGE_VAL, some ? (double)m_rest : -HUGE_VAL);
   if (m == -HUGE_VAL) m = 0.0;
-  const double back = ((double)offset - (double)c * (double)m_rest) * kLn2D;
-  const double rest = some ? R * exp(((double)m_rest - m) * it + back) : 0.0;
+  const double rest = some ? R * exp(((double)m_rest - m) * it) : 0.0;
   const double top = s.some || s.z != s.z ? s.z * exp((s.m - m) * it) : 0.0;
   const double z = rest + top, lz = log(z);
   if (s.count == 0.0) return z == z ? 0.0f : (float)z;
+  if (!(z > 0.0)) return __int_as_float(0x7fffffff);  // a bad logit, or none above -inf
   const double norm = tail ? 1.0 : 1.0 / s.p;
   const double pt = !tail || s.count >= (double)vocab ? 0.0 : fmax(0.0, 1.0 - s.p);
   double part = 0.0;
@@ -261,7 +264,7 @@ __device__ __noinline__ float row_loss(const ListSums &s, double R, float m_rest
     part = norm * (s.plp + s.p * log(norm) - s.pz - s.p * ((s.m - m) * it - lz));
   if (pt > 0.0) {
     // the tail's logarithm from R's own: rest may be too small for a double
-    const double log_rest = some ? log(R) + back + ((double)m_rest - m) * it : -HUGE_VAL;
+    const double log_rest = some ? log(R) + ((double)m_rest - m) * it : -HUGE_VAL;
     part += pt * (log(pt) - (log_rest - lz));
   }
   return (float)part;
@@ -269,7 +272,7 @@ __device__ __noinline__ float row_loss(const ListSums &s, double R, float m_rest
 
 // A warp's part of R.
 struct Part {
-  float m, r;  // largest unlisted logit; sum of 2^(c z - c m)
+  float m, r;  // largest unlisted logit; sum of 2^(c (z - m))
 };
 
 // -inf in the places of a packed vector that `hit` names.
@@ -329,7 +332,8 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   const Row<T> row(in.data, r, in.row_stride, in.vocab);
   const int lo = (int)rank * slice, hi = min(lo + slice, row.end());
   const bool lists = tid >= kStreamThreads;
-  const float c = (float)((double)inv_t * kLog2eD);
+  // (finite, so that 0 times it is 0)
+  const float c = fminf((float)((double)inv_t * kLog2eD), 3.4028234663852886e38f);
   const float g = (WHAT & kBackward) ? grads[r] : 0.0f;
   ids += r * K;
   lp += r * K;
@@ -430,7 +434,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       if (lane == 0) list = list_figures(sums, tail != 0, in.vocab);
     } else {
       // R, against each lane's running maximum
-      float m = kNegInf, off = 0.0f;
+      float m = kNegInf;
       uint64_t s2 = 0;  // two sums
       const uint64_t c2 = pair(c, c);
       for (int u = first, stage = 0; u < hi; u += step, stage ^= 1) {
@@ -452,23 +456,22 @@ __global__ void __launch_bounds__(kDisThreads, 4)
         for (int k = 1; k < kDisVecs; ++k) top = max_nan(top, vector_max(q[k], T()));
         if (!(top <= m)) {
           // (a NaN stays one, and makes all that follows NaN)
-          const float to = __fmul_rn(top, c);
           if (m != kNegInf) {
-            const float f = exp2_fast(off - to);
+            const float f = exp2_fast((m - top) * c);
             const float2 s = unpair(s2);
             s2 = pair(s.x * f, s.y * f);
           }
-          off = to;
           m = top;
         }
-        const uint64_t off2 = pair(m == kNegInf ? 0.0f : -off, m == kNegInf ? 0.0f : -off);
+        const float at = m == kNegInf ? 0.0f : -m;
+        const uint64_t at2 = pair(at, at);
 #pragma unroll
         for (int k = 0; k < kDisVecs; ++k) {
           float z[N];
           unpack16(q[k], z, T());
 #pragma unroll
           for (int i = 0; i < N; i += 2) {
-            const float2 e = exp2_pair(z[i], z[i + 1], c2, off2);
+            const float2 e = exp2_pair(z[i], z[i + 1], c2, at2);
             asm("add.rn.f32x2 %0, %1, %2;" : "=l"(s2) : "l"(s2), "l"(pair(e.x, e.y)));
           }
         }
@@ -481,7 +484,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       float w = m;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w = max_nan(w, __shfl_xor_sync(kFull, w, o));
-      if (m != kNegInf) s *= exp2_fast(off - __fmul_rn(w, c));
+      if (m != kNegInf) s *= exp2_fast((m - w) * c);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(kFull, s, o);
       if (peers > 1) cluster_wait();
@@ -505,19 +508,17 @@ __global__ void __launch_bounds__(kDisThreads, 4)
       m_rest = max_nan(m_rest, parts[i].m);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m_rest = max_nan(m_rest, __shfl_xor_sync(kFull, m_rest, o));
-    const float offset = m_rest == kNegInf ? 0.0f : __fmul_rn(m_rest, c);
     float R = 0.0f;
     for (int i = lane; i < (int)peers * kStreamWarps; i += 32) {
       const Part p = parts[i];
-      // each part against its own rounded product
-      R += p.m == kNegInf ? p.r : p.r * exp2_fast(__fmul_rn(p.m, c) - offset);
+      R += p.m == kNegInf ? p.r : p.r * exp2_fast((p.m - m_rest) * c);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) R += __shfl_xor_sync(kFull, R, o);
-    st = row_figures(list, R, m_rest, offset, c, inv_t);
+    st = row_figures(list, R, m_rest, c, inv_t);
     if (rank == 0 && tid == kStreamThreads) {
       if constexpr (WHAT == kForward) stats[r] = st;
-      losses[r] = row_loss(sums, (double)R, m_rest, offset, c, inv_t, tail != 0, in.vocab);
+      losses[r] = row_loss(sums, (double)R, m_rest, inv_t, tail != 0, in.vocab);
     }
     if constexpr (WHAT == kForward) return;
   } else {
@@ -530,7 +531,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
     T *o = grad + r * grad_stride - row.shift;
     if (!lists) {
       const float factor = st.rest * g;
-      const uint64_t c2 = pair(c, c), off2 = pair(-st.offset, -st.offset);
+      const uint64_t c2 = pair(c, c), at2 = pair(-st.others, -st.others);
       const uint64_t factor2 = pair(factor, factor);
       if constexpr (WHAT == kBackward) {
         send(last, 0, drop);
@@ -546,7 +547,7 @@ __global__ void __launch_bounds__(kDisThreads, 4)
           unpack16(q[k], z, T());
 #pragma unroll
           for (int i = 0; i < N; i += 2) {
-            const float2 e = exp2_pair(z[i], z[i + 1], c2, off2);
+            const float2 e = exp2_pair(z[i], z[i + 1], c2, at2);
             uint64_t x;
             asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(x) : "l"(pair(e.x, e.y)), "l"(factor2));
             const float2 f = unpair(x);

@@ -107,3 +107,103 @@ def test_rows_without_entries_add_nothing_at_all():
     for losses, grad in both_ways(x[:2], far[0][:2], far[1][:2], w[:2], tail=False):
         check_distill(x[:2], far[0][:2], far[1][:2] + 2000, 1.0, False, np.ones(2), losses, grad)
         assert float(losses.min()) > 0
+
+
+@pytest.mark.parametrize("tail", [True, False])
+@pytest.mark.parametrize("absent", [True, False])
+@pytest.mark.parametrize("dtype,low", [(F32, -1e4), (F32, -1e9), (F32, -1e10), (F32, -1e30),
+                                       (F32, torch.finfo(F32).min), (F16, -65504.0),
+                                       (BF16, -1e10), (BF16, torch.finfo(BF16).min)], ids=str)
+def test_masked_students_whose_list_holds_all_that_is_left(dtype, low, absent, tail):
+    """A mask written as a low value, on every token outside the list (`absent`:
+    but for the ids of entries that are absent): the mass there is 0 in
+    any type, and its logarithm finite."""
+    n, v, K, T = 3, 3001, 40, 2.0
+    x = make_logits(n, v, dtype, 3, seed=34)
+    ids, lp = teacher(n, v, K, 9, tail)
+    out = torch.ones(n, v, dtype=torch.bool, device="cuda")
+    for r in range(n):
+        some = (ids[r] >= 0) & (absent | (lp[r] > -np.inf))
+        out[r, torch.from_numpy(ids[r][some].astype(np.int64)).cuda()] = False
+    x[out] = low
+    x[0] = low                          # (row 0 has no entries: all equal)
+    x[0, 5] = 1.0
+    g = np.array([1.0, -0.5, 2.0], np.float32)
+
+    def lse(z):
+        return z.max() + math.log(np.exp(z - z.max()).sum())
+
+    for losses, grad in both_ways(x, ids, lp, g, T, tail):
+        if not tail:
+            check_distill(x, ids, lp, T, tail, g, losses, grad)
+            continue
+        rows, eps = numpy_rows(x).astype(np.float64), torch.finfo(grad.dtype).eps
+        G = grad.double().cpu().numpy()
+        assert float(losses[0]) == 0.0 and not G[0].any()
+        for r in range(1, n):
+            # in logarithms: the tail's mass may have no double
+            keep = (ids[r] >= 0) & (lp[r] > -np.inf)
+            p, z = np.exp(lp[r][keep].astype(np.float64)), rows[r] / T
+            others = np.ones(v, bool)
+            others[ids[r][keep]] = False
+            lz, lr, pt = lse(z), lse(z[others]), 1 - p.sum()
+            want = (p * (np.log(p) - z[ids[r][keep]] + lz)).sum() + pt * (math.log(pt) + lz - lr)
+            # float32's log probabilities, the loss's own rounding
+            assert abs(float(losses[r]) - want) <= 1e-5 + 2 * U * abs(want)
+            dz = np.exp(z - lz)
+            dz[ids[r][keep]] -= p
+            share = np.exp(z[others] - z[others].max())  # (lr has no room for log v at 1e30)
+            dz[others] -= pt * share / share.sum()
+            dz *= g[r] / T
+            tol = 1e-5 * abs(g[r]) + np.abs(dz) * eps
+            assert (np.abs(G[r] - dz) <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=str)
+def test_students_at_the_ends_of_their_type(dtype):
+    """Logits of both signs up to the largest, -inf rows, small temperatures:
+    against 64 bits, where every sum of these is held."""
+    v = 2000
+    x = make_logits(7, v, dtype, 1, seed=35)
+    top = torch.finfo(dtype).max
+    x[0, 100:] = -top
+    x[1, ::2], x[1, 7] = top, -math.inf
+    x[2] = top
+    x[3] = -top
+    x[4, :900], x[4, 900:] = -top, -top / 2
+    x[5] = -math.inf
+    ids = np.tile(np.array([[7, 9, 1500]], np.int32), (7, 1))
+    lp = np.log(np.tile(np.array([[0.25, 0.125, 0.5]], np.float32), (7, 1)))
+    g = np.ones(7, np.float32)
+    for T in (1.0, 0.01, 4.0):              # (with reciprocals that float32 holds)
+        for tail in (True, False):
+            for losses, grad in both_ways(x, ids, lp, g, T, tail):
+                assert bool(losses[5].isnan()) and bool(grad[5].isnan().all())
+                assert losses[1] == math.inf        # token 7 has no mass at all
+                assert bool(grad[:5].isfinite().all())
+                for r in (0, 2, 3, 4, 6):
+                    one = slice(r, r + 1)
+                    if TO.distill(numpy_rows(x)[r], ids[r], lp[r], 1.0 / T, tail)[0] > 3.4e38:
+                        assert losses[r] == math.inf
+                    else:
+                        check_distill(x[one], ids[one], lp[one], T, tail, g[one], losses[one],
+                                      grad[one])
+    # the whole list far below the rest: the listed have no mass, the others all
+    y = make_logits(1, v, dtype, 1, seed=36)
+    y[0, torch.tensor([7, 9, 1500], device="cuda")] = -1e4
+    for losses, grad in both_ways(y, ids[:1], lp[:1], g[:1]):
+        check_distill(y, ids[:1], lp[:1], 1.0, True, g[:1], losses, grad)
+
+
+@pytest.mark.parametrize("shift", [-20000.0, 20000.0, 1e7])
+def test_distillation_counts_differences_to_their_last_bit(shift):
+    """Logits far from zero: their differences are exact, so the error is
+    that of rows near zero."""
+    n, v = 3, 5000
+    x = make_logits(n, v, F32, seed=16) + shift
+    x[1, 2500:] -= 30000.0                 # a row whose ends lie far apart
+    x[2, :2500] -= 30000.0
+    ids, lp = teacher(n, v, 30, 7, True)
+    g = np.array([1.0, -0.5, 2.0], np.float32)
+    for losses, grad in both_ways(x, ids, lp, g):
+        check_distill(x, ids, lp, 1.0, True, g, losses, grad)
