@@ -49,6 +49,30 @@ def _raw_stream(dev):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+class _MadeOn:
+    """A tensor of the library's own that was computed on the stream current at
+    the time, for calls on other streams: they wait for it, and its memory
+    for them.  Not where either is captured: a capture may not wait for work
+    outside of it, nor the reverse.  There the program orders its streams, and
+    its replays, as it does for its own tensors."""
+
+    def __init__(self, x, dev):
+        self.x, self.dev = x, dev
+        self.stream = torch.cuda.current_stream(dev)
+        self.captured = torch.cuda.is_current_stream_capturing()
+        self.done = torch.cuda.Event()
+        self.done.record(self.stream)
+
+    def use(self):
+        if _raw_stream(self.dev) == self.stream.cuda_stream:
+            return
+        if self.captured or torch.cuda.is_current_stream_capturing():
+            return
+        here = torch.cuda.current_stream(self.dev)
+        here.wait_event(self.done)
+        self.x.record_stream(here)
+
+
 def _rows(x, what="logits"):
     """(device index, rows, vocab, dtype code, row stride) of rows of logits."""
     if not isinstance(x, torch.Tensor) or not x.is_cuda or x.dim() != 2:
@@ -337,13 +361,16 @@ class LogitAdjust:
 
     The tensors of history, bias and mask are read by each call, so a program
     may keep one LogitAdjust and update them in place between steps (per-row
-    numbers are copied when it is made).
+    numbers are copied when it is made, on the stream current then; calls on
+    other streams wait for the copy, captured calls not.  A captured call reads
+    that copy at every replay: keep the LogitAdjust as long as the graph).
     """
 
     def __init__(self, temperature=1.0, repetition=1.0, frequency=0.0, presence=0.0,
                  history=None, bias=None, mask=None):
         self._n, self._words, self._dev = None, 0, None
         self._keep = (history, bias, mask)
+        self._made = None
         params = 0
         scalars = (1.0, 0.0, 0.0, 1.0)
         tensor = torch.Tensor
@@ -414,6 +441,8 @@ class LogitAdjust:
         cols[3] = cols[3].double().reciprocal().float()
         rows = torch.stack(cols, 1)
         self._keep += (rows,)
+        with _place(dev, None):
+            self._made = _MadeOn(rows, dev)
         return rows.data_ptr()
 
     def _on(self, x, n):
@@ -430,7 +459,7 @@ class LogitAdjust:
 
     def bind(self, rows):
         """The C struct's bytes, checked against the rows it is to be used on
-        (as _rows has them)."""
+        (as _rows has them), for a call on the device's current stream."""
         dev, n, v = rows[:3]
         if self._dev is not None and self._dev != dev:
             raise ValueError("LogitAdjust on cuda:%d, logits on cuda:%d" % (self._dev, dev))
@@ -438,6 +467,8 @@ class LogitAdjust:
             raise ValueError("LogitAdjust for %d rows, logits of %d" % (self._n, n))
         if self._words and self._words < (v + 31) // 32:
             raise ValueError("mask: %d words for %d tokens" % (self._words, v))
+        if self._made is not None:
+            self._made.use()
         return self._c
 
 

@@ -49,6 +49,56 @@ def test_texts_coded_under_a_number_decode_under_rows_of_it(T):
     c.finish()
 
 
+SLEEP = 50_000_000  # cycles: some 25 ms, far longer than a call takes to arrive
+
+
+def test_per_row_numbers_on_a_stream_of_their_own():
+    """The copy of per-row numbers is waited for by calls on other streams, and
+    outlives them, with no synchronisation by the caller."""
+    n, v = 6, 3000
+    x = make_logits(n, v, F32, seed=37)
+    a, _ = make_adjust(n, v, seed=37, per_row=True)
+    tok = torch.full((n,), 3, dtype=torch.int32, device="cuda")
+    per_row = make_adjust(n, v, seed=37, per_row=True)[1]
+    fixed = {k: tuple(torch.from_numpy(t).cuda() for t in per_row[k]) for k in ("history", "bias")}
+    fixed["mask"] = torch.from_numpy(per_row["mask"]).cuda()
+    numbers = {k: torch.from_numpy(per_row[k]).cuda()
+               for k in ("temperature", "repetition", "frequency", "presence")}
+    want = [rb.adjust_logits(x, a), *rb.token_intervals(x, tok, a)]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    # the copy is late
+    torch.cuda._sleep(SLEEP)
+    b = rb.LogitAdjust(**fixed, **numbers)
+    got = [rb.adjust_logits(x, b, stream=s), *rb.token_intervals(x, tok, b, stream=s)]
+    s.synchronize()
+    for p, q in zip(got, want):
+        assert torch.equal(p, q)
+    # the call is late, and what it was given gone
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(SLEEP)
+    b = rb.LogitAdjust(**fixed, **numbers)
+    got = rb.adjust_logits(x, b, stream=s)
+    del b
+    junk = [torch.full((n, 4), 1e6, device="cuda") for _ in range(64)]
+    s.synchronize()
+    assert torch.equal(got, want[0]) and len(junk) == 64
+
+
+def test_per_row_numbers_in_a_captured_call():
+    """Made before a capture and used in it, on torch's capture stream."""
+    n, v = 4, 500
+    x = make_logits(n, v, F32, seed=38)
+    a, _ = make_adjust(n, v, seed=38, per_row=True)
+    out, want = torch.empty_like(x), rb.adjust_logits(x, a)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        rb.adjust_logits(x, a, out=out)
+    g.replay()
+    assert torch.equal(out, want)
+
+
 # ----------------------------------------------------------- distillation --
 def both_ways(x, ids, lp, w, T=1.0, tail=True, st=None):
     """(losses, gradient) in one call, and by autograd."""

@@ -352,6 +352,8 @@ def test_a_number_and_a_row_that_holds_it_have_the_same_reciprocal():
 def test_numbers_beside_per_row_tensors_are_checked_too(monkeypatch):
     """... and are float32 whatever the default type is."""
     monkeypatch.setattr(rb.LogitAdjust, "_on", lambda self, x, n: -1)
+    monkeypatch.setattr(rb.tokens, "_place", lambda dev, stream: contextlib.nullcontext())
+    monkeypatch.setattr(rb.tokens, "_MadeOn", lambda x, dev: None)
     rows = torch.full((3,), 0.7)
     for kw in (dict(repetition=-1.0), dict(repetition=0.0), dict(repetition=1e39),
                dict(frequency=float("nan")), dict(presence=float("inf"))):
