@@ -27,6 +27,8 @@ TOKEN_PRECISION = 24
 # the structs are packed rather than built field by field.
 _pack_logits = struct.Struct("@Piiqq").pack
 _pack_adjust = struct.Struct("@ffffPPPPqPPPPqPq").pack
+_float4 = struct.Struct("@ffff")
+_INF = float("inf")
 assert struct.calcsize("@Piiqq") == ctypes.sizeof(L.rans_logits)
 assert struct.calcsize("@ffffPPPPqPPPPqPq") == ctypes.sizeof(L.rans_adjust)
 _no_context = contextlib.nullcontext()
@@ -96,9 +98,10 @@ def _packed(x, rows):
 def _device(x, what):
     """The index of a CUDA tensor's device.  (Host tensors share -1: without this
     they would all be "on one device".)"""
-    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+    dev = x.get_device() if isinstance(x, torch.Tensor) else -1
+    if dev < 0:
         raise ValueError("%s: a CUDA tensor" % what)
-    return x.get_device()
+    return dev
 
 
 def _tensor(x, dtype, shape, dev, what):
@@ -109,6 +112,13 @@ def _tensor(x, dtype, shape, dev, what):
         raise ValueError("%s: a contiguous %s tensor%s on cuda:%d" % (
             what, dtype, "" if shape is None else " of shape %s" % (tuple(shape),), dev))
     return x.data_ptr()
+
+
+def _written(*tensors):
+    """Tells autograd that a call wrote to the caller's tensors, as torch's own
+    in-place operations do: a backward pass that had saved one of them then
+    raises, where it would use what stands there now."""
+    torch.autograd.graph.increment_version(tensors)
 
 
 def new_status(device="cuda"):
@@ -138,7 +148,9 @@ def _ref(adjust, rows):
 def rans_adjust_logits(logits, adjust, out, stream=None):
     rows = _rows(logits)
     with _place(rows[0], stream):
-        return _adjust(rows, logits, adjust, out)
+        result = _adjust(rows, logits, adjust, out)
+    _written(out)
+    return result
 
 
 def _adjust(rows, logits, adjust, out):
@@ -152,7 +164,9 @@ def _adjust(rows, logits, adjust, out):
 def rans_token_intervals(logits, adjust, tokens, starts, freqs, status, stream=None):
     rows = _rows(logits)
     with _place(rows[0], stream):
-        return _intervals(rows, logits, adjust, tokens, starts, freqs, status)
+        result = _intervals(rows, logits, adjust, tokens, starts, freqs, status)
+    _written(starts, freqs)
+    return result
 
 
 def _intervals(rows, logits, adjust, tokens, starts, freqs, status):
@@ -170,11 +184,12 @@ def rans_encode_intervals(starts, freqs, n, chunking, out, stream_offsets, works
     dev = _device(starts, "starts")
     S = L.rans_num_streams(chunking, n)
     with _place(dev, stream):
-        return _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace)
+        result = _encode(dev, starts, freqs, n, S, chunking, out, stream_offsets, workspace)
+    _written(out, stream_offsets, workspace)
+    return result
 
 
-def _encode(starts, freqs, n, S, chunking, out, stream_offsets, workspace):
-    dev = _device(starts, "starts")
+def _encode(dev, starts, freqs, n, S, chunking, out, stream_offsets, workspace):
     # (the chunking's own tensor: explicit stream starts)
     if chunking._keep is not None and _device(chunking._keep, "stream starts") != dev:
         raise ValueError("chunking on %s, starts on cuda:%d" % (chunking._keep.device, dev))
@@ -204,16 +219,20 @@ def rans_token_states(data, stream_offsets, states, status, stream=None):
     s = _tensor(states, torch.int64, (S, 2), dev, "states")
     with _place(dev, stream):
         status = _status(status, dev)
-        return L.lib().rans_token_states(d, data.numel(), o, S, s, status.data_ptr(),
-                                         _raw_stream(dev))
+        result = L.lib().rans_token_states(d, data.numel(), o, S, s, status.data_ptr(),
+                                           _raw_stream(dev))
+    _written(states)
+    return result
 
 
 def rans_decode_tokens(logits, adjust, data, stream_offsets, stream_ids, states_in, states_out,
                        tokens, status, stream=None):
     rows = _rows(logits)
     with _place(rows[0], stream):
-        return _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in,
-                       states_out, tokens, status)
+        result = _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in,
+                         states_out, tokens, status)
+    _written(states_out, tokens)
+    return result
 
 
 def _decode(rows, logits, adjust, data, stream_offsets, stream_ids, states_in, states_out,
@@ -261,9 +280,11 @@ def rans_distill_forward(logits, ids, logprobs, inv_temperature, tail, losses, s
     s = _tensor(stats, torch.float32, (n, 8), dev, "stats")
     with _place(dev, stream):
         status = _status(status, dev)
-        return L.lib().rans_distill_forward(
+        result = L.lib().rans_distill_forward(
             _packed(logits, rows), i, lp, K, inv_temperature, int(tail), o, s,
             status.data_ptr(), _raw_stream(dev))
+    _written(losses, stats)
+    return result
 
 
 def _grad_of(rows, grad):
@@ -282,16 +303,20 @@ def rans_distill_backward(logits, ids, logprobs, inv_temperature, stats, grad_lo
     w = _tensor(grad_losses, torch.float32, (n,), dev, "grad_losses")
     g, step = _grad_of(rows, grad)
     with _place(dev, stream):
-        return L.lib().rans_distill_backward(_packed(logits, rows), i, lp, K, inv_temperature, s,
-                                             w, g, step, _raw_stream(dev))
+        result = L.lib().rans_distill_backward(_packed(logits, rows), i, lp, K, inv_temperature,
+                                               s, w, g, step, _raw_stream(dev))
+    _written(grad)
+    return result
 
 
 def rans_distill(logits, ids, logprobs, inv_temperature, tail, grad_losses, losses, grad, status,
                  stream=None):
     rows = _rows(logits)
     with _place(rows[0], stream):
-        return _both(rows, logits, ids, logprobs, inv_temperature, tail, grad_losses, losses,
-                     grad, status)
+        result = _both(rows, logits, ids, logprobs, inv_temperature, tail, grad_losses, losses,
+                       grad, status)
+    _written(losses, grad)
+    return result
 
 
 def _both(rows, logits, ids, logprobs, inv_temperature, tail, grad_losses, losses, grad, status):
@@ -378,9 +403,14 @@ class LogitAdjust:
                 isinstance(frequency, tensor) or isinstance(presence, tensor):
             params = self._per_row((repetition, frequency, presence, temperature))
         else:
-            scalars = (_in_float32(repetition, _positive, "repetition"),
-                       _in_float32(frequency, _finite, "frequency"),
-                       _in_float32(presence, _finite, "presence"), _inverse(temperature))
+            # rounded to float32 at once; one by one, to say which, if one is bad
+            r, f, p, t = _float4.unpack(_float4.pack(repetition, frequency, presence, temperature))
+            if 0.0 < r < _INF and f - f == 0.0 and p - p == 0.0 and 1e-38 < t < _INF:
+                scalars = (r, f, p, 1.0 / t)
+            else:
+                scalars = (_in_float32(repetition, _positive, "repetition"),
+                           _in_float32(frequency, _finite, "frequency"),
+                           _in_float32(presence, _finite, "presence"), _inverse(temperature))
         hist = (0, 0, 0, 0)
         if history is not None:
             tokens, begin, end = history
@@ -474,12 +504,16 @@ class LogitAdjust:
 
 def adjust_logits(logits, adjust, out=None, dtype=None, stream=None):
     """Adjusted logits (penalties, biases, temperature, mask) for a sampler, in
-    the logits' type or `dtype`; out may be the logits themselves."""
+    the logits' type or `dtype`; out may be the logits themselves.  No gradient
+    flows through the result, whether the logits require one or not."""
     rows = _rows(logits)
+    given = out is not None
     with _place(rows[0], stream):
-        if out is None:
+        if not given:
             out = logits.new_empty(rows[1:3], dtype=dtype)
         L.check(_adjust(rows, logits, adjust, out), "adjust_logits")
+    if given:
+        _written(out)
     return out
 
 
@@ -489,6 +523,7 @@ def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status
     TOKEN_PRECISION bits.  Rows with token -1 are skipped: what stands in
     starts and freqs stays (nothing useful, where they are not given)."""
     rows = _rows(logits)
+    given = [x for x in (starts, freqs) if x is not None]
     with _place(rows[0], stream):
         if starts is None:
             starts = logits.new_empty(rows[1], dtype=torch.int32)
@@ -496,6 +531,8 @@ def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status
             freqs = logits.new_empty(rows[1], dtype=torch.int32)
         L.check(_intervals(rows, logits, adjust, tokens, starts, freqs, status),
                 "token_intervals")
+    if given:
+        _written(*given)
     return starts, freqs
 
 
@@ -508,6 +545,7 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
     S = L.rans_num_streams(chunking, n)
     if S < 0:
         L.check(int(S), "num_streams")
+    given = [x for x in (out, ws) if x is not None]
     with _place(dev, stream):
         if ws is None:
             # torch's blocks are aligned to 512 bytes, as the workspace has to be to 256
@@ -515,7 +553,9 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
         if out is None:
             out = starts.new_empty(L.rans_max_compressed_bytes(chunking, n), dtype=torch.uint8)
         offsets = starts.new_empty(S + 1, dtype=torch.int64)
-        L.check(_encode(starts, freqs, n, S, chunking, out, offsets, ws), "encode_intervals")
+        L.check(_encode(dev, starts, freqs, n, S, chunking, out, offsets, ws), "encode_intervals")
+    if given:
+        _written(*given)
     return out, offsets, ws
 
 
@@ -536,6 +576,7 @@ def decode_tokens(logits, data, stream_offsets, states, adjust=None, stream_ids=
     Rows with stream id -1 are skipped; without `tokens` they read -1."""
     rows = _rows(logits)
     n = rows[1]
+    given = [x for x in (out_states, tokens) if x is not None]
     with _place(rows[0], stream):
         if out_states is None:
             every = stream_ids is None and n == stream_offsets.numel() - 1
@@ -545,6 +586,8 @@ def decode_tokens(logits, data, stream_offsets, states, adjust=None, stream_ids=
                 logits.new_full((n,), -1, dtype=torch.int32)
         L.check(_decode(rows, logits, adjust, data, stream_offsets, stream_ids, states,
                         out_states, tokens, status), "decode_tokens")
+    if given:
+        _written(*given)
     return tokens, out_states
 
 
@@ -601,10 +644,13 @@ def distill_loss_and_grad(logits, ids, logprobs, weights, temperature=1.0, tail=
     grad may be the logits themselves."""
     inv = _positive(1.0 / _positive(temperature, "temperature"), "1 / temperature")
     rows = _rows(logits)
+    given = grad is not None
     with _place(rows[0], stream):
         losses = logits.new_empty(rows[1], dtype=torch.float32)
-        if grad is None:
+        if not given:
             grad = logits.new_empty(rows[1:3])
         L.check(_both(rows, logits, ids, logprobs, inv, tail, weights, losses, grad, status),
                 "distill")
+    if given:
+        _written(grad)
     return losses, grad

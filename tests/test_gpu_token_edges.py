@@ -257,3 +257,27 @@ def test_distillation_counts_differences_to_their_last_bit(shift):
     g = np.array([1.0, -0.5, 2.0], np.float32)
     for losses, grad in both_ways(x, ids, lp, g):
         check_distill(x, ids, lp, 1.0, True, g, losses, grad)
+
+
+def test_a_backward_pass_whose_logits_were_written_over_raises():
+    n, v = 3, 200
+    x = make_logits(n, v, F32, seed=39).contiguous()
+    ids, lp = (torch.from_numpy(t).cuda() for t in teacher(n, v, 5, 1, True))
+    w = torch.ones(n, device="cuda")
+    for write in (lambda z: rb.adjust_logits(z, rb.LogitAdjust(temperature=0.5), out=z),
+                  lambda z: rb.distill_loss_and_grad(z, ids, lp, w, grad=z)):
+        y = x.clone().requires_grad_()
+        z = y * 1.0
+        loss = rb.distill_loss(z, ids, lp).sum()
+        write(z.detach())
+        with pytest.raises(RuntimeError, match="inplace operation"):
+            loss.backward()
+    # what is not saved may be written to
+    loss = rb.distill_loss(y, ids, lp).sum()
+    rb.adjust_logits(y.detach(), None, out=torch.empty_like(x))
+    loss.backward()
+    with torch.inference_mode():
+        z = x.clone()
+        rb.adjust_logits(z, None, out=z)
+    rb.adjust_logits(z, None, out=z)
+    assert torch.equal(z, x)

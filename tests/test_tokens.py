@@ -371,3 +371,46 @@ def test_numbers_beside_per_row_tensors_are_checked_too(monkeypatch):
     assert params.dtype == torch.float32 and params.shape == (3, 4)
     want = np.array([1.1, 0.25, 0.0, 1 / np.float32(0.7)], np.float32)
     assert np.array_equal(params.numpy(), np.tile(want, (3, 1)))
+
+
+def test_autograd_learns_of_what_a_call_writes(watched, monkeypatch):
+    monkeypatch.setattr(rb.tokens.L, "rans_num_streams", lambda chunking, n: 2)
+    x, ids, lp = torch.zeros(3, 8), torch.zeros(3, 2, dtype=torch.int32), torch.zeros(3, 2)
+    i32, w, stats = torch.zeros(3, dtype=torch.int32), torch.zeros(3), torch.zeros(3, 8)
+    data, offs = torch.zeros(64, dtype=torch.uint8), torch.tensor([0, 16, 32, 48])
+    states, chunks = torch.zeros(3, 2, dtype=torch.int64), rb.Chunking.contig(2)
+
+    def new(like):
+        return torch.zeros_like(like)
+
+    # (a call given its outputs, the outputs)
+    for call, outs in (
+            (lambda o: rb.adjust_logits(x, None, out=o), (x,)),
+            (lambda o: rb.rans_adjust_logits(x, None, o), (x,)),
+            (lambda a, b: rb.token_intervals(x, i32, starts=a, freqs=b), (i32, i32)),
+            (lambda a: rb.token_intervals(x, i32, freqs=a), (i32,)),
+            (lambda a, b: rb.rans_token_intervals(x, None, i32, a, b, None), (i32, i32)),
+            (lambda a, b: rb.encode_intervals(i32, i32, chunks, out=a, ws=b), (data, data)),
+            (lambda a, b, c: rb.rans_encode_intervals(i32, i32, 3, chunks, a, b, c),
+             (data, offs, data)),
+            (lambda a: rb.rans_token_states(data, offs, a, None), (states,)),
+            (lambda a, b: rb.decode_tokens(x, data, offs, states, out_states=a, tokens=b),
+             (states, i32)),
+            (lambda a, b: rb.rans_decode_tokens(x, None, data, offs, None, states, a, b, None),
+             (states, i32)),
+            (lambda a, b: rb.rans_distill_forward(x, ids, lp, 1.0, True, a, b, None), (w, stats)),
+            (lambda a: rb.rans_distill_backward(x, ids, lp, 1.0, stats, w, a), (x,)),
+            (lambda a, b: rb.rans_distill(x, ids, lp, 1.0, True, w, a, b, None), (w, x)),
+            (lambda a: rb.distill_loss_and_grad(x, ids, lp, w, grad=a), (x,))):
+        mine = [new(o) for o in outs]
+        call(*mine)
+        assert [o._version for o in mine] == [1] * len(mine)
+    for read in (x, ids, lp, i32, w, data, offs, states, stats):
+        assert read._version == 0
+    # a backward pass whose logits were written over says so
+    y = torch.zeros(3, 8, requires_grad=True)
+    z = y * 1.0
+    loss = rb.tokens._Distill.apply(z, ids, lp, 1.0, True, None).sum()
+    rb.adjust_logits(z, None, out=z)
+    with pytest.raises(RuntimeError, match="inplace operation"):
+        loss.backward()
