@@ -122,7 +122,8 @@ class TokenCoder:
 
     def __init__(self, device="cuda"):
         self.device = torch.device(device)
-        self.status = T.new_status(self.device)
+        # errors of the texts added; of the streams being decoded
+        self.status, self.decoding = T.new_status(self.device), None
         self._parts = []
         self._in = None
 
@@ -137,7 +138,8 @@ class TokenCoder:
 
     def streams(self, lengths):
         """(data, stream_offsets) of the texts added so far, of these lengths
-        (summing to the positions added); device errors raise."""
+        (summing to the positions added); device errors raise, and what was
+        added is dropped with them."""
         starts = torch.cat([p[0] for p in self._parts]) if self._parts else \
             torch.empty(0, dtype=torch.int32, device=self.device)
         freqs = torch.cat([p[1] for p in self._parts]) if self._parts else starts.clone()
@@ -146,18 +148,20 @@ class TokenCoder:
             cuts.append(cuts[-1] + int(n))
         if cuts[-1] != starts.numel() or min(lengths, default=0) < 0:
             raise ValueError("lengths sum to %d, %d positions added" % (cuts[-1], starts.numel()))
+        self._parts = []
         L.check(L.rans_get_status(self.status), "token_intervals")
         cuts = torch.tensor(cuts, dtype=torch.int64, device=self.device)
         out, offs, ws = T.encode_intervals(starts, freqs, L.Chunking.explicit(cuts))
         L.check(L.rans_get_status(ws), "encode_intervals")
-        self._parts = []
         return out[:int(offs[-1].item())].clone(), offs
 
     def begin(self, data, stream_offsets):
         data = torch.as_tensor(data, dtype=torch.uint8).to(self.device).contiguous()
         offs = torch.as_tensor(stream_offsets, dtype=torch.int64).to(self.device).contiguous()
         self._in = (data, offs)
-        self.states = T.token_states(data, offs, self.status)
+        # (its own word: streams given up halfway may have left an error)
+        self.decoding = T.new_status(self.device)
+        self.states = T.token_states(data, offs, self.decoding)
         return self
 
     def step(self, logits, adjust=None, stream_ids=None):
@@ -166,14 +170,16 @@ class TokenCoder:
         if self._in is None:
             raise RuntimeError("begin with the streams first")
         tokens, _ = T.decode_tokens(logits, *self._in, self.states, adjust, stream_ids,
-                                    out_states=self.states, status=self.status)
+                                    out_states=self.states, status=self.decoding)
         return tokens
 
     def finish(self):
         """Raises unless every stream was decoded without an error and to its
         end."""
-        L.check(T.rans_token_states_finish(self._in[1], self.states, self.status), "finish")
-        L.check(L.rans_get_status(self.status), "decode_tokens")
+        if self._in is None:
+            raise RuntimeError("begin with the streams first")
+        L.check(T.rans_token_states_finish(self._in[1], self.states, self.decoding), "finish")
+        L.check(L.rans_get_status(self.decoding), "decode_tokens")
 
 
 def to_byte_strings(data, stream_offsets):

@@ -281,3 +281,33 @@ def test_a_backward_pass_whose_logits_were_written_over_raises():
         rb.adjust_logits(z, None, out=z)
     rb.adjust_logits(z, None, out=z)
     assert torch.equal(z, x)
+
+
+# ------------------------------------------------------- the coder object --
+def test_a_coder_starts_afresh_after_an_error():
+    x, tok, (data, offs) = coded(1, 60, 4, seed=40)
+    c = rb.TokenCoder()
+    with pytest.raises(RuntimeError):
+        c.step(x[:1])
+    with pytest.raises(RuntimeError):
+        c.finish()
+    c.begin(data[:4], offs)             # streams that are not there, given up
+    c.begin(data, offs)
+    for t in range(4):
+        assert int(c.step(x[t:t + 1])) == int(tok[0, t])
+    c.finish()
+    c.begin(data[:4], offs)             # nor do they spoil texts that are coded
+    again, _ = c.add(x, tok[0]).streams([4])
+    assert torch.equal(again, data)
+    with pytest.raises(rb.RansError):   # and an error is told once
+        c.finish()
+    c.add(x, torch.tensor([1, 2, 60, 3]))
+    with pytest.raises(rb.RansError):
+        c.streams([4])
+    again, _ = c.add(x, tok[0]).streams([4])
+    assert torch.equal(again, data)
+    c.add(x[:1], tok[0, :1])
+    with pytest.raises(ValueError):     # (the call's own mistake drops nothing)
+        c.streams([4])
+    again, _ = c.add(x[1:], tok[0, 1:]).streams([4])
+    assert torch.equal(again, data)
