@@ -129,7 +129,7 @@ class TokenCoder:
 
     def add(self, logits, tokens, adjust=None):
         """The next positions: rows of logits and the token that each is to code."""
-        tokens = torch.as_tensor(tokens, dtype=torch.int32, device=self.device).reshape(-1)
+        tokens = _token_ids(tokens, self.device)
         # a skipped row (token -1) stays at 0, which the streams refuse
         blank = torch.zeros(2, tokens.numel(), dtype=torch.int32, device=self.device)
         self._parts.append(T.token_intervals(logits, tokens, adjust, blank[0], blank[1],
@@ -180,6 +180,15 @@ class TokenCoder:
             raise RuntimeError("begin with the streams first")
         L.check(T.rans_token_states_finish(self._in[1], self.states, self.decoding), "finish")
         L.check(L.rans_get_status(self.decoding), "decode_tokens")
+
+
+def _token_ids(tokens, device):
+    """int32 ids on the device.  Those that int32 does not hold become ids that no
+    vocabulary has (a plain conversion would wrap them into it)."""
+    tokens = torch.as_tensor(tokens, device=device).reshape(-1)
+    if tokens.dtype is torch.int64:
+        tokens = tokens.clamp(-2, 2**31 - 1)
+    return tokens.to(torch.int32)
 
 
 def to_byte_strings(data, stream_offsets):

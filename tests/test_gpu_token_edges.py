@@ -311,3 +311,13 @@ def test_a_coder_starts_afresh_after_an_error():
         c.streams([4])
     again, _ = c.add(x[1:], tok[0, 1:]).streams([4])
     assert torch.equal(again, data)
+
+
+def test_wide_token_ids_are_refused():
+    x = make_logits(3, 50, F32, seed=41)
+    for bad in (2**32 + 5, 2**31, -2**32 + 7):
+        c = rb.TokenCoder()
+        c.add(x, torch.tensor([1, bad, 2], device="cuda"))
+        with pytest.raises(rb.RansError) as e:
+            c.streams([3])
+        assert e.value.status == rb.ERR_INDEX

@@ -414,3 +414,16 @@ def test_autograd_learns_of_what_a_call_writes(watched, monkeypatch):
     rb.adjust_logits(z, None, out=z)
     with pytest.raises(RuntimeError, match="inplace operation"):
         loss.backward()
+
+
+def test_wide_token_ids_do_not_wrap_into_the_vocabulary():
+    from rans_entropy_coding_b200.interface import _token_ids
+    wide = torch.tensor([[5, -1, -2], [2**32 + 5, 2**31, -2**32 - 1], [-2**33, 2**31 - 1, 0]])
+    ids = _token_ids(wide, "cpu")
+    assert ids.dtype == torch.int32
+    assert ids.tolist() == [5, -1, -2, 2**31 - 1, 2**31 - 1, -2, -2, 2**31 - 1, 0]
+    assert all(v in (-1, -2, 2**31 - 1) or 0 <= v < 6 for v in ids.tolist())
+    for same in ([3, 1], np.array([3, 1]), torch.tensor([3, 1], dtype=torch.int16),
+                 torch.tensor([[3], [1]], dtype=torch.int32)):
+        assert _token_ids(same, "cpu").tolist() == [3, 1]
+    assert _token_ids([], "cpu").tolist() == []
