@@ -306,7 +306,10 @@ def rans_decode_to_values(data, stream_offsets, scales, means, n, scale_table, s
 
 
 def rans_get_status(workspace, stream=None):
-    return lib().rans_get_status(_ptr(workspace), _stream(stream))
+    """The first device error in a workspace or status word, read on `stream`
+    or the current stream of the device that it lies on."""
+    with torch.cuda.device(workspace.device):  # (a default stream is its device's)
+        return lib().rans_get_status(_ptr(workspace), _stream(stream))
 
 
 def rans_debug_wait_timeout(workspace, limit, stream=None):

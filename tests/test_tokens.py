@@ -427,3 +427,33 @@ def test_wide_token_ids_do_not_wrap_into_the_vocabulary():
                  torch.tensor([[3], [1]], dtype=torch.int32)):
         assert _token_ids(same, "cpu").tolist() == [3, 1]
     assert _token_ids([], "cpu").tolist() == []
+
+
+def test_a_status_is_read_on_its_own_device(monkeypatch):
+    """With another device current, its stream is not ordered behind the calls
+    that wrote the word (and a default stream's address names the current one)."""
+    now, got = ["cuda:0"], []
+
+    class Word:
+        device = torch.device("cuda:1")
+
+        def data_ptr(self):
+            return 99
+
+    class Lib:
+        def rans_get_status(self, word, stream):
+            got.append((word.value, stream.value, now[0]))
+            return rb.OK
+
+    @contextlib.contextmanager
+    def device(d):
+        was, now[0] = now[0], str(d)
+        yield
+        now[0] = was
+
+    stream = type("Stream", (), dict(cuda_stream=7))
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: stream)
+    monkeypatch.setattr(rb._lib, "lib", lambda: Lib())
+    assert rb.rans_get_status(Word()) == rb.OK and now == ["cuda:0"]
+    assert got == [(99, 7, "cuda:1")]
