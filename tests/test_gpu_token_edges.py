@@ -321,3 +321,145 @@ def test_wide_token_ids_are_refused():
         with pytest.raises(rb.RansError) as e:
             c.streams([3])
         assert e.value.status == rb.ERR_INDEX
+
+
+# ------------------------------------------------- decoders that are lied to --
+def test_a_refill_is_read_inside_its_stream_or_not_at_all():
+    """Every row needs a word, and whether its offsets allow one is decided on
+    the host: the oracle's step where they do; else no token, the state as it
+    was, and an error."""
+    x, _, (data, offs) = coded(4, 50, 3)
+    st = rb.new_status()
+    rows = x[:4].contiguous() if x.shape[0] >= 4 else x[:1].expand(4, 50).contiguous()
+    bounds = [TO.bounds(r, {}, 0) for r in numpy_rows(rows)]
+    words = np.frombuffer(data.cpu().numpy().tobytes(), np.uint32)
+    total, seen = data.numel(), set()
+    for lie in (offs.tolist(), [0, 10, 20, 30, 40], [64, 48, 32, 16, 0], [0] * 4 + [1 << 40],
+                [0] * 5, [-8, 16, 32, 48, 64], [0, total, total, total, total + 4],
+                [0, total, 0, total, 0], [total - 12, total, total + 4, 8, total]):
+        for taken in (2, 0, 1 << 40, (1 << 62) - 1):
+            states = torch.tensor([[(1 << 31) + 3 * r, taken] for r in range(4)], device="cuda")
+            tok, new = rb.decode_tokens(rows, data, torch.tensor(lie, device="cuda"), states,
+                                        status=st)
+            ok = []
+            for r in range(4):
+                off, lim = lie[r] % (1 << 64), lie[r + 1] % (1 << 64)
+                ok.append(off % 4 == 0 and off <= lim <= total and taken < (lim - off) // 4)
+                if not ok[r]:
+                    assert int(tok[r]) == -1 and torch.equal(new[r], states[r])
+                    continue
+                b, slot = bounds[r], 3 * r
+                t = int(np.searchsorted(np.array(b), slot, side="right")) - 1
+                y = (b[t + 1] - b[t]) * ((1 << 31) >> 24) + slot - b[t]
+                assert y < 1 << 31 and int(tok[r]) == t
+                assert new[r].tolist() == [y << 32 | int(words[off // 4 + taken]), taken + 1]
+            seen.update(ok)
+            assert rb.rans_get_status(st) == (rb.OK if all(ok) else rb.ERR_CORRUPT)
+    assert seen == {True, False}
+
+
+# ------------------------------------------ rows of several tables and tiles --
+def check_token_rows(x, a, o, sample, seed):
+    """Adjusted logits, intervals and decoding steps of some of the rows."""
+    n, rng, st = x.shape[0], np.random.default_rng(seed), rb.new_status()
+    rows = {r: numpy_rows(x[r:r + 1])[0] for r in sample}
+    b = {r: TO.bounds(rows[r], o, r) for r in sample}
+    tok = np.full(n, -1, np.int32)
+    slots = rng.integers(0, 1 << 24, n)
+    for r in sample:
+        alive = np.flatnonzero(np.diff(b[r]))
+        tok[r] = alive[-1 - len(alive) // 7] if r % 2 else rng.choice(alive)
+    s, f = rb.token_intervals(x, torch.from_numpy(tok).cuda(), a, status=st)
+    states = torch.stack([torch.from_numpy(slots).cuda() + (1 << 62),
+                          torch.full((n,), 2, device="cuda")], 1)
+    got, _ = rb.decode_tokens(x, torch.zeros(8 * n, dtype=torch.uint8, device="cuda"),
+                              torch.arange(n + 1, device="cuda") * 8, states, a, status=st)
+    out = rb.adjust_logits(x, a, dtype=F32)
+    for r in sample:
+        assert int(s[r]) == b[r][tok[r]] and int(f[r]) == b[r][tok[r] + 1] - b[r][tok[r]]
+        assert int(got[r]) == int(np.searchsorted(np.array(b[r]), slots[r], side="right")) - 1
+        want, err = TO.adjust(rows[r], o, r)
+        z, dead = out[r].double().cpu().numpy(), np.isinf(want)
+        assert np.array_equal(z[dead], want[dead])
+        assert (np.abs(z[~dead] - want[~dead]) <=
+                err[~dead] + U * (np.abs(want[~dead]) + err[~dead]) + 2.0 ** -149).all()
+    status_ok(st)
+    y = x.clone()
+    assert torch.equal(rb.adjust_logits(y, a, out=y), rb.adjust_logits(x, a))
+
+
+@pytest.mark.parametrize("dtype,v,pad", [(BF16, 131072, 0), (F16, 131071, 2), (F32, 150001, 1)],
+                         ids=str)
+def test_rows_of_many_tables_in_one_block(dtype, v, pad):
+    """Enough rows that a block has one to itself, histories of more distinct
+    tokens than a hash takes: a table for every 8,192 tokens, walked twice, and
+    once more for the decoded token."""
+    n = 150
+    x = make_logits(n, v, dtype, pad, seed=42, offset=pad)
+    a, o = make_adjust(n, v, seed=42, long=120000)
+    assert np.unique(o["history"][0]).size > 50000
+    check_token_rows(x, a, o, [0, 1, 2, 71, 149], 42)
+
+
+@pytest.mark.parametrize("parts", [dict(history=False, bias=False), dict(bias=False), dict()],
+                         ids=str)
+@pytest.mark.parametrize("dtype,v,n", [(BF16, 150001, 900), (F32, 140000, 150),
+                                       (F16, rb.MAX_VOCAB, 150)], ids=str)
+def test_masks_past_a_tables_span(dtype, v, n, parts):
+    """More tokens than a table's bitmap and hash cover, in one block: the mask
+    alone, and with few touched tokens.  (At 900 rows adjust_logits has one
+    block a row too.)"""
+    x = make_logits(n, v, dtype, v % 2, seed=43)
+    a, o = make_adjust(n, v, seed=43, **parts)
+    check_token_rows(x, a, o, [1, n - 2], 43)
+
+
+def check_rows(x, ids, lp, T, tail, g, losses, grad, sample, rescales):
+    """As check_distill, with the 2^-22 of each exponential that a sum is
+    rescaled by when its maximum rises (`rescales` times at most)."""
+    L, G, inv, fi = (losses.double().cpu().numpy(), grad.cpu(), 1.0 / T, torch.finfo(grad.dtype))
+    v = x.shape[1]
+    for r in sample:
+        row = numpy_rows(x[r:r + 1])[0]
+        want, dz, parts = TO.distill(row, ids[r], lp[r], inv, tail)
+        arg = np.abs(row.astype(np.float64) - row.max()) * inv
+        eps = 2.0 ** -22 * (1 + rescales) + U * (3 * 0.7 * (math.log2(v) + 1) + v / 512 + 20)
+        assert abs(L[r] - want) <= 2 * eps + U * abs(want), (r, L[r], want)
+        tol = abs(g[r]) * parts * (2 * eps + U * (8 + 4 * arg)) + \
+            np.abs(dz * g[r]) * (fi.eps / 2 + 2 * U) + fi.smallest_normal * fi.eps / 2 + 2.0 ** -126
+        assert (np.abs(G[r].double().numpy() - dz * g[r]) <= tol).all(), r
+
+
+@pytest.mark.parametrize("n", [3, 300])
+@pytest.mark.parametrize("dtype,v,pad", [(BF16, 131072, 0), (F16, 150001, 3), (F32, 150001, 0),
+                                         (F32, 131072, 5)], ids=str)
+def test_distillation_of_rows_longer_than_their_ring(dtype, v, pad, n):
+    """Many tiles a warp: stages that are filled again while others are read, in
+    both walks, with one block a row (300) and several (3); in place, where
+    later tiles are on their way while earlier ones are written.  Row 2's logits
+    rise, so that every tile raises the maximum."""
+    T, tail, K = 1.5, n > 3, 60 if n > 3 else 300
+    x = make_logits(n, v, dtype, pad, seed=44, offset=pad)
+    x[2] = x[2].float().sort().values.to(dtype)
+    ids, lp = teacher(n, v, K, 44, tail)
+    g = np.random.default_rng(44).uniform(0.5, 2.0, n).astype(np.float32)
+    if dtype == F16:
+        g *= 1024                       # (gradients above the type's smallest)
+    sample = sorted({0, 1, 2, n // 2, n - 1})
+    st = rb.new_status()
+    # a warp's tiles are kStep tokens apart
+    rescales = -(-v // (8 * 32 * 4 * (16 // x.element_size())))
+    both = list(both_ways(x, ids, lp, g, T, tail, st))
+    for losses, grad in both:
+        check_rows(x, ids, lp, T, tail, g, losses, grad, sample, rescales)
+    ti, tl, tg = (torch.from_numpy(t).cuda() for t in (ids, lp, g))
+    wide = torch.empty(n * (v + 16), device="cuda", dtype=dtype).view(n, v + 16)[:, 8:v + 8]
+    y = wide.copy_(x) if pad == 0 else x.clone()
+    losses, _ = rb.distill_loss_and_grad(y, ti, tl, tg, T, tail, grad=y, status=st)
+    # (a clone of padded rows is packed: other vectors, the same to rounding)
+    check_rows(x, ids, lp, T, tail, g, losses, y, sample, rescales)
+    y = make_logits(n, v, dtype, pad, seed=44, offset=pad)
+    y[2] = x[2]
+    losses, _ = rb.distill_loss_and_grad(y, ti, tl, tg, T, tail, grad=y, status=st)
+    assert torch.equal(losses, both[0][0]) and torch.equal(y, both[0][1])
+    status_ok(st)
