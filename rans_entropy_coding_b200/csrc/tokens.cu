@@ -507,7 +507,7 @@ __global__ void __launch_bounds__(kRowThreads, 2)
       (uint64_t)__float_as_uint(-rs.ymax) << 32 | __float_as_uint(-rs.ymax);
   WarpSums s = {0, 0, 0, 0};
   walk([&](int u, int tile) {
-    // a lane's weights of a tile stay below 2^26, a tile's below 2^31
+    // a lane's weights of a tile sum to at most 2^26, a tile's to 2^31
     uint4 q[kTileVecs];
     uint32_t ok[kTileVecs], w = 0, n = 0;
     const bool some = load_tile(u, q, ok);
