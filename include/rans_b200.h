@@ -494,6 +494,9 @@ int rans_decode_to_values(const uint8_t *in, uint64_t in_bytes, const uint64_t *
  * Streams: RANS64 states and words (lower bound 2^31, 32-bit words, one state
  * per stream) at RANS_TOKEN_PRECISION bits: a token renormalises when
  * x >= 2^39 * freq, then x -> (x / freq) 2^24 + x mod freq + start.
+ *
+ * Every array of this section is aligned to its element type (where no more is
+ * asked for); a pointer that is not is RANS_ERR_ARG.
  */
 #define RANS_MAX_VOCAB ((1 << 19) - 8)
 #define RANS_TOKEN_PRECISION 24

@@ -536,6 +536,13 @@ bool aligned_to(const void *p, uint64_t bytes) {
   return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0;
 }
 
+// Whether all of these lie as their type has to (an absent one does): a kernel's
+// access to one that does not would end the caller's context.
+template <typename... T>
+bool natural(const T *...p) {
+  return (aligned_to(p, sizeof(T)) && ...);
+}
+
 int check_logits(const rans_logits *in) {
   if (!in || in->rows < 0 || in->vocab < 1 || in->vocab > RANS_MAX_VOCAB) return RANS_ERR_ARG;
   const int e = logits_bytes(in->dtype);
@@ -565,6 +572,9 @@ int check_adjust(const rans_adjust *a, int32_t vocab, rans_adjust &out) {
   if (a->bias_ids && (!a->bias_values || !a->bias_begin || !a->bias_end || a->bias_len < 0))
     return RANS_ERR_ARG;
   if (a->mask && a->mask_stride != 0 && a->mask_stride < (vocab + 31) / 32) return RANS_ERR_ARG;
+  if (!natural(a->params, a->history, a->history_begin, a->history_end, a->bias_ids,
+               a->bias_values, a->bias_begin, a->bias_end, a->mask))
+    return RANS_ERR_ARG;
   return RANS_OK;
 }
 
@@ -573,7 +583,7 @@ int check_status_word(const void *status) {
 }
 
 int check_streams(const uint8_t *in, uint64_t in_bytes, const uint64_t *offsets, int64_t S) {
-  if (S < 0 || (S > 0 && !offsets)) return RANS_ERR_ARG;
+  if (S < 0 || (S > 0 && !offsets) || !natural(offsets)) return RANS_ERR_ARG;
   if ((in_bytes > 0 && !in) || !aligned_to(in, 4)) return RANS_ERR_ARG;
   return RANS_OK;
 }
@@ -585,6 +595,7 @@ int check_distill(const rans_logits *in, const int32_t *ids, const float *lp, in
   if (K < 1 || K > RANS_MAX_TOP) return RANS_ERR_ARG;
   if (!(inv_temperature > 0.0f) || !finite(inv_temperature)) return RANS_ERR_ARG;
   if (in->rows > 0 && (!ids || !lp)) return RANS_ERR_ARG;
+  if (!natural(ids, lp)) return RANS_ERR_ARG;
   return RANS_OK;
 }
 
@@ -640,7 +651,7 @@ RANS_API int rans_token_intervals(const rans_logits *logits, const rans_adjust *
   if (!st) st = check_status_word(status);
   if (st) return st;
   if (logits->rows == 0) return RANS_OK;
-  if (!tokens || !starts || !freqs) return RANS_ERR_ARG;
+  if (!tokens || !starts || !freqs || !natural(tokens, starts, freqs)) return RANS_ERR_ARG;
   // a row's blocks read its token while others may be done with theirs
   const uint64_t bytes = 4ull * (uint64_t)logits->rows;
   if (overlap(tokens, bytes, starts, bytes) || overlap(tokens, bytes, freqs, bytes) ||
@@ -658,10 +669,12 @@ RANS_API int rans_encode_intervals(const uint32_t *starts, const uint32_t *freqs
   if (n > 0 && (!starts || !freqs)) return RANS_ERR_ARG;
   if (!stream_offsets || !workspace || (out_capacity > 0 && !out)) return RANS_ERR_ARG;
   if (!aligned_to(workspace, 256) || !aligned_to(out, 4)) return RANS_ERR_ARG;
+  if (!natural(starts, freqs, stream_offsets)) return RANS_ERR_ARG;
   Geom g;
   int st = make_geom(chunking, n, g);
   if (st) return st;
   if (g.kind != RANS_CHUNK_CONTIG && g.kind != RANS_CHUNK_EXPLICIT) return RANS_ERR_ARG;
+  if (g.kind == RANS_CHUNK_EXPLICIT && !natural(g.starts)) return RANS_ERR_ARG;
   if (g.W != 1 || g.ib_shift != 0 || g.fmt != RANS_FMT_RANS64 || g.alias) return RANS_ERR_ARG;
   if (workspace_bytes < enc_ws_bytes(g)) return RANS_ERR_CAPACITY;
   return rb::launch_encode_intervals(starts, freqs, g, reinterpret_cast<char *>(workspace),
@@ -677,7 +690,7 @@ RANS_API int rans_token_states(const uint8_t *in, uint64_t in_bytes,
   if (!st) st = check_status_word(status);
   if (st) return st;
   if (S == 0) return RANS_OK;
-  if (!states) return RANS_ERR_ARG;
+  if (!states || !natural(states)) return RANS_ERR_ARG;
   return rb::launch_token_states(in, in_bytes, stream_offsets, S, states,
                                  static_cast<int32_t *>(status), as_stream(stream));
 }
@@ -698,6 +711,7 @@ RANS_API int rans_decode_tokens(const rans_logits *logits, const rans_adjust *ad
   if (!stream_ids && logits->rows > S) return RANS_ERR_ARG;
   if (logits->rows == 0) return RANS_OK;
   if (!states_in || !states_out || !tokens || !stream_offsets) return RANS_ERR_ARG;
+  if (!natural(stream_ids, states_in, states_out, tokens)) return RANS_ERR_ARG;
   const uint64_t row_bytes = 4ull * (uint64_t)logits->rows, state_bytes = 16ull * (uint64_t)S;
   if ((states_in != states_out && overlap(states_in, state_bytes, states_out, state_bytes)) ||
       overlap(tokens, row_bytes, stream_ids, row_bytes) ||
@@ -715,6 +729,7 @@ RANS_API int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S,
                                       const uint64_t *states, void *status, void *stream) {
   NvtxRange nvtx_("rans_token_states_finish");
   if (S < 0 || (S > 0 && (!stream_offsets || !states))) return RANS_ERR_ARG;
+  if (!natural(stream_offsets, states)) return RANS_ERR_ARG;
   const int st = check_status_word(status);
   if (st || S == 0) return st;
   return rb::launch_token_finish(stream_offsets, S, states, static_cast<int32_t *>(status),
@@ -729,7 +744,7 @@ RANS_API int rans_distill_forward(const rans_logits *logits, const int32_t *ids,
   int st = check_distill(logits, ids, logprobs, K, inv_temperature);
   if (!st) st = check_status_word(status);
   if (st || logits->rows == 0) return st;
-  if (!losses || !stats || !aligned_to(stats, 16)) return RANS_ERR_ARG;
+  if (!losses || !stats || !aligned_to(stats, 16) || !natural(losses)) return RANS_ERR_ARG;
   return rb::launch_distill_forward(*logits, ids, logprobs, K, inv_temperature, tail, losses,
                                     stats, static_cast<int32_t *>(status), as_stream(stream));
 }
@@ -742,7 +757,8 @@ RANS_API int rans_distill_backward(const rans_logits *logits, const int32_t *ids
   int st = check_distill(logits, ids, logprobs, K, inv_temperature);
   if (!st) st = check_result(logits, grad, logits->dtype, grad_stride);
   if (st || logits->rows == 0) return st;
-  if (!stats || !aligned_to(stats, 16) || !grad_losses) return RANS_ERR_ARG;
+  if (!stats || !aligned_to(stats, 16) || !grad_losses || !natural(grad_losses))
+    return RANS_ERR_ARG;
   return rb::launch_distill_backward(*logits, ids, logprobs, K, inv_temperature, stats,
                                      grad_losses, grad, grad_stride, as_stream(stream));
 }
@@ -756,7 +772,7 @@ RANS_API int rans_distill(const rans_logits *logits, const int32_t *ids, const f
   if (!st) st = check_result(logits, grad, logits->dtype, grad_stride);
   if (!st) st = check_status_word(status);
   if (st || logits->rows == 0) return st;
-  if (!losses || !grad_losses) return RANS_ERR_ARG;
+  if (!losses || !grad_losses || !natural(losses, grad_losses)) return RANS_ERR_ARG;
   return rb::launch_distill(*logits, ids, logprobs, K, inv_temperature, tail, grad_losses, losses,
                             grad, grad_stride, static_cast<int32_t *>(status),
                             as_stream(stream));

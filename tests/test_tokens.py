@@ -457,3 +457,41 @@ def test_a_status_is_read_on_its_own_device(monkeypatch):
     monkeypatch.setattr(rb._lib, "lib", lambda: Lib())
     assert rb.rans_get_status(Word()) == rb.OK and now == ["cuda:0"]
     assert got == [(99, 7, "cuda:1")]
+
+
+def test_pointers_off_their_types_boundaries_are_refused(lib):
+    """Half an element (or, for arrays of rows, a byte) beside where one lies."""
+    lg, one = logits(), rb.Chunking.contig(2)
+    x = ctypes.byref(lg)
+
+    def off(call, good, at, by):
+        for k in at:
+            args = list(good)
+            args[k] += by
+            assert call(*args) == rb.ERR_ARG, (call.__name__, k)
+
+    off(lib.rans_token_intervals, [x, None, A(1), A(2), A(3), A(4), None], (2, 3, 4), 2)
+    good = [x, None, A(1), 64, A(2), 8, A(3), A(4), A(5), A(6), A(7), None]
+    off(lib.rans_decode_tokens, good, (4, 7, 8), 4)
+    off(lib.rans_decode_tokens, good, (6, 9), 2)
+    off(lib.rans_token_states, [A(1), 64, A(2), 2, A(3), A(4), None], (2, 4), 4)
+    off(lib.rans_token_states_finish, [A(1), 2, A(2), A(3), None], (0, 2), 4)
+    off(lib.rans_distill_forward, [x, A(1), A(2), 5, 1.0, 1, A(3), A(4), A(5), None], (1, 2, 6), 2)
+    off(lib.rans_distill_backward, [x, A(1), A(2), 5, 1.0, A(3), A(4), A(5), 100, None],
+        (1, 2, 6, 7), 2)
+    off(lib.rans_distill, [x, A(1), A(2), 5, 1.0, 1, A(3), A(4), A(5), 100, A(6), None],
+        (1, 2, 6, 7, 8), 2)
+    off(lib.rans_encode_intervals, [A(1), A(2), 10, ctypes.byref(one.c), A(3), 4096, A(4), A(5),
+                                    1 << 20, None], (0, 1, 6), 2)
+    c = rb.rans_chunking()
+    c.kind, c.interleave, c.n_streams, c.index_block = rb._lib.CHUNK_EXPLICIT, 1, 2, 1
+    c.stream_starts = A(6) + 4
+    assert lib.rans_encode_intervals(A(1), A(2), 10, ctypes.byref(c), A(3), 4096, A(4), A(5),
+                                     1 << 20, None) == rb.ERR_ARG
+    whole = dict(history=A(8), history_begin=A(9), history_end=A(10), history_len=5,
+                 bias_ids=A(11), bias_values=A(12), bias_begin=A(13), bias_end=A(14), bias_len=5,
+                 mask=A(15), mask_stride=4, params=A(16))
+    for k, v in whole.items():
+        if k not in ("history_len", "bias_len", "mask_stride"):
+            by = 4 if k.endswith(("begin", "end")) else 2
+            assert list(calls(lib, lg, adjust(**{**whole, k: v + by}))) == [rb.ERR_ARG] * 3, k
