@@ -651,6 +651,8 @@ int rans_token_states_finish(const uint64_t *stream_offsets, int64_t S, const ui
  *   grad: device, the logits' dtype, row r at grad + r * grad_stride elements
  *         (>= vocab when rows > 1); may be logits->data itself when the
  *         strides agree, and overlaps it in no other way.
+ * losses may be grad_losses; else no result overlaps an argument or another
+ * result (RANS_ERR_ARG).
  * rans_distill_backward takes the same logits, ids, logprobs and
  * inv_temperature as the forward call that wrote `stats`.  rans_distill is both in one call,
  * for loops that know the rows' weights beforehand.  All are asynchronous.  A

@@ -628,6 +628,48 @@ int check_result(const rans_logits *in, const void *out, int32_t dtype, int64_t 
   return RANS_OK;
 }
 
+// Whether an array lies on any of a result's rows (between them it may).
+bool on_rows(const void *p, uint64_t bytes, const rans_logits *in, const void *out,
+             int64_t stride) {
+  const uint64_t e = (uint64_t)logits_bytes(in->dtype), len = (uint64_t)in->vocab * e;
+  const uint64_t step = (uint64_t)stride * e;
+  if (!overlap(p, bytes, out, (in->rows > 1 ? (uint64_t)(in->rows - 1) * step : 0) + len))
+    return false;
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(out);
+  if (in->rows == 1 || a < b) return true;
+  const uint64_t off = (a - b) % step;
+  return off < len || off + bytes > step;
+}
+
+// A distillation reads its lists more than once, and from several blocks: no
+// result may lie on them, nor on what else is read, nor on another result.
+// (losses may be the weights: every block has read its row's before.)
+int check_distill_memory(const rans_logits *in, const int32_t *ids, const float *lp, int32_t K,
+                         const float *weights, const float *losses, const float *stats,
+                         bool stats_written, const void *grad, int64_t stride) {
+  const uint64_t row = 4ull * (uint64_t)in->rows, list = row * (uint64_t)K, st = 8 * row;
+  auto on_grad = [&](const void *p, uint64_t bytes) {
+    return p && grad && on_rows(p, bytes, in, grad, stride);
+  };
+  auto on_stats = [&](const void *p, uint64_t bytes) {
+    return stats_written && overlap(p, bytes, stats, st);
+  };
+  auto on_losses = [&](const void *p, uint64_t bytes) { return overlap(p, bytes, losses, row); };
+  auto on_logits = [&](const void *p, uint64_t bytes) {
+    return p && on_rows(p, bytes, in, in->data, in->row_stride);
+  };
+  if (on_grad(ids, list) || on_stats(ids, list) || on_losses(ids, list) || on_grad(lp, list) ||
+      on_stats(lp, list) || on_losses(lp, list))
+    return RANS_ERR_ARG;
+  if (on_grad(weights, row) || on_stats(weights, row) ||
+      (weights != losses && on_losses(weights, row)))
+    return RANS_ERR_ARG;
+  if (on_grad(losses, row) || on_stats(losses, row) || on_logits(losses, row) ||
+      on_grad(stats, st) || (stats_written && on_logits(stats, st)))
+    return RANS_ERR_ARG;
+  return RANS_OK;
+}
+
 }  // namespace
 
 RANS_API int rans_adjust_logits(const rans_logits *logits, const rans_adjust *adjust, void *out,
@@ -745,6 +787,8 @@ RANS_API int rans_distill_forward(const rans_logits *logits, const int32_t *ids,
   if (!st) st = check_status_word(status);
   if (st || logits->rows == 0) return st;
   if (!losses || !stats || !aligned_to(stats, 16) || !natural(losses)) return RANS_ERR_ARG;
+  if (check_distill_memory(logits, ids, logprobs, K, nullptr, losses, stats, true, nullptr, 0))
+    return RANS_ERR_ARG;
   return rb::launch_distill_forward(*logits, ids, logprobs, K, inv_temperature, tail, losses,
                                     stats, static_cast<int32_t *>(status), as_stream(stream));
 }
@@ -758,6 +802,9 @@ RANS_API int rans_distill_backward(const rans_logits *logits, const int32_t *ids
   if (!st) st = check_result(logits, grad, logits->dtype, grad_stride);
   if (st || logits->rows == 0) return st;
   if (!stats || !aligned_to(stats, 16) || !grad_losses || !natural(grad_losses))
+    return RANS_ERR_ARG;
+  if (check_distill_memory(logits, ids, logprobs, K, grad_losses, nullptr, stats, false, grad,
+                           grad_stride))
     return RANS_ERR_ARG;
   return rb::launch_distill_backward(*logits, ids, logprobs, K, inv_temperature, stats,
                                      grad_losses, grad, grad_stride, as_stream(stream));
@@ -773,6 +820,9 @@ RANS_API int rans_distill(const rans_logits *logits, const int32_t *ids, const f
   if (!st) st = check_status_word(status);
   if (st || logits->rows == 0) return st;
   if (!losses || !grad_losses || !natural(losses, grad_losses)) return RANS_ERR_ARG;
+  if (check_distill_memory(logits, ids, logprobs, K, grad_losses, losses, nullptr, false, grad,
+                           grad_stride))
+    return RANS_ERR_ARG;
   return rb::launch_distill(*logits, ids, logprobs, K, inv_temperature, tail, grad_losses, losses,
                             grad, grad_stride, static_cast<int32_t *>(status),
                             as_stream(stream));

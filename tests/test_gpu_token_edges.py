@@ -463,3 +463,27 @@ def test_distillation_of_rows_longer_than_their_ring(dtype, v, pad, n):
     losses, _ = rb.distill_loss_and_grad(y, ti, tl, tg, T, tail, grad=y, status=st)
     assert torch.equal(losses, both[0][0]) and torch.equal(y, both[0][1])
     status_ok(st)
+
+
+@pytest.mark.parametrize("n", [2, 300])
+def test_distillation_memory_that_may_be_shared(n):
+    """Losses over the weights that they were asked for with; lists that lie
+    between a result's rows."""
+    v, K = 20011, 8
+    x = make_logits(n, v, F32, seed=45)
+    ids, lp = teacher(n, v, K, 45, True)
+    ti, tl = torch.from_numpy(ids).cuda(), torch.from_numpy(lp).cuda()
+    w = torch.linspace(0.5, 2.0, n, device="cuda")
+    st = rb.new_status()
+    want, grad = rb.distill_loss_and_grad(x, ti, tl, w, status=st)
+    out, again = w.clone(), torch.empty_like(grad)
+    rb.check(rb.rans_distill(x, ti, tl, 1.0, True, out, out, again, st))
+    assert torch.equal(out, want) and torch.equal(again, grad)
+    wide = torch.zeros(n, v + 2 * n * K + 1, device="cuda")
+    wide[0, v:v + n * K].view(torch.int32).copy_(ti.view(-1))
+    wide[1, v + n * K:v + 2 * n * K].copy_(tl.view(-1))
+    got, g = rb.distill_loss_and_grad(x, wide[0, v:v + n * K].view(torch.int32).view(n, K),
+                                      wide[1, v + n * K:v + 2 * n * K].view(n, K), w,
+                                      grad=wide[:, :v], status=st)
+    assert torch.equal(got, want) and torch.equal(g, grad)
+    status_ok(st)

@@ -495,3 +495,32 @@ def test_pointers_off_their_types_boundaries_are_refused(lib):
         if k not in ("history_len", "bias_len", "mask_stride"):
             by = 4 if k.endswith(("begin", "end")) else 2
             assert list(calls(lib, lg, adjust(**{**whole, k: v + by}))) == [rb.ERR_ARG] * 3, k
+
+
+def test_distillations_whose_results_overlap_are_refused(lib):
+    lg = logits(rows=4, vocab=100, stride=160)   # 640 bytes a row, 400 of them logits
+    x, S = ctypes.byref(lg), rb.ERR_ARG
+
+    def refused(call, good, changes):
+        for k, v in changes:
+            args = list(good)
+            args[k] = v
+            assert call(*args) == S, (call.__name__, k, v)
+
+    # ids, logprobs (4 x 5 each), weights, losses, grad (stride 160)
+    good = [x, A(1), A(2), 5, 1.0, 1, A(3), A(4), A(5), 160, A(6), None]
+    refused(lib.rans_distill, good, [
+        (7, A(1)), (7, A(1) + 76), (7, A(2) - 12), (7, A(3) + 4), (7, P), (7, P + 3 * 640 + 396),
+        (7, A(5)), (7, A(5) + 640 + 396), (7, A(5) + 632), (8, A(1)), (8, A(2) + 76),
+        (8, A(3) - 396), (8, A(4) + 12), (1, A(5) + 640), (2, A(5) + 3 * 640 + 100),
+        (6, A(5) + 396)])
+    # ids, logprobs, losses, stats (4 x 8)
+    good = [x, A(1), A(2), 5, 1.0, 1, A(3), A(4), A(5), None]
+    refused(lib.rans_distill_forward, good, [
+        (6, A(1) + 76), (6, A(2)), (6, A(4) + 124), (6, P + 640), (7, A(1) + 64), (7, A(2) - 112),
+        (7, A(3)), (7, P + 2 * 640)])
+    # ids, logprobs, stats, weights, grad
+    good = [x, A(1), A(2), 5, 1.0, A(3), A(4), A(5), 160, None]
+    refused(lib.rans_distill_backward, good, [
+        (7, A(1)), (7, A(2) + 76), (7, A(3) + 124), (7, A(4) + 12), (1, A(5) + 396),
+        (5, A(5) + 384)])
