@@ -2,8 +2,9 @@
 a model's logits"): logit adjustment, intervals of tokens, streams of
 intervals, decoding steps and the distillation loss.
 
-Argument checks and marshalling only, as in ``_lib``; every step runs in the
-library's kernels.  Logits are CUDA tensors [rows, vocab] of float32, float16
+Argument checks and marshalling only, as in ``_lib``; every step of a call runs
+in the library's kernels (LogitAdjust's copy of per-row numbers and pack_mask,
+which prepare a call's arguments, are torch operations).  Logits are CUDA tensors [rows, vocab] of float32, float16
 or bfloat16 whose rows are contiguous (a column slice of a wider buffer is
 fine).  Calls run on the tensors' device, on ``stream`` or that device's
 current stream.  ``status`` is a CUDA tensor from ``new_status()``; pass one to
@@ -361,7 +362,9 @@ def _inverse(temperature):
 
 def pack_mask(allowed):
     """Words of a bool tensor [rows, vocab] (or [vocab]) of allowed tokens, as
-    LogitAdjust takes them: bit v & 31 of word v >> 5."""
+    LogitAdjust takes them: bit v & 31 of word v >> 5.  For rules that are packed
+    once: in torch operations, with 16 bytes a token of temporary memory.  A
+    grammar that changes with every token should keep its words itself."""
     flat = allowed if allowed.dim() == 2 else allowed[None]
     n, v = flat.shape
     bits = torch.nn.functional.pad(flat, (0, -v % 32)).view(n, -1, 32).to(torch.int64)
