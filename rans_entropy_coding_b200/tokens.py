@@ -526,7 +526,7 @@ def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status
     TOKEN_PRECISION bits.  Rows with token -1 are skipped: what stands in
     starts and freqs stays (nothing useful, where they are not given)."""
     rows = _rows(logits)
-    given = [x for x in (starts, freqs) if x is not None]
+    given = starts is not None or freqs is not None
     with _place(rows[0], stream):
         if starts is None:
             starts = logits.new_empty(rows[1], dtype=torch.int32)
@@ -535,7 +535,7 @@ def token_intervals(logits, tokens, adjust=None, starts=None, freqs=None, status
         L.check(_intervals(rows, logits, adjust, tokens, starts, freqs, status),
                 "token_intervals")
     if given:
-        _written(*given)
+        _written(starts, freqs)
     return starts, freqs
 
 
@@ -548,7 +548,7 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
     S = L.rans_num_streams(chunking, n)
     if S < 0:
         L.check(int(S), "num_streams")
-    given = [x for x in (out, ws) if x is not None]
+    given = out is not None or ws is not None
     with _place(dev, stream):
         if ws is None:
             # torch's blocks are aligned to 512 bytes, as the workspace has to be to 256
@@ -558,7 +558,7 @@ def encode_intervals(starts, freqs, chunking, out=None, ws=None, stream=None):
         offsets = starts.new_empty(S + 1, dtype=torch.int64)
         L.check(_encode(dev, starts, freqs, n, S, chunking, out, offsets, ws), "encode_intervals")
     if given:
-        _written(*given)
+        _written(out, ws)
     return out, offsets, ws
 
 
@@ -579,7 +579,7 @@ def decode_tokens(logits, data, stream_offsets, states, adjust=None, stream_ids=
     Rows with stream id -1 are skipped; without `tokens` they read -1."""
     rows = _rows(logits)
     n = rows[1]
-    given = [x for x in (out_states, tokens) if x is not None]
+    given = out_states is not None or tokens is not None
     with _place(rows[0], stream):
         if out_states is None:
             every = stream_ids is None and n == stream_offsets.numel() - 1
@@ -590,7 +590,7 @@ def decode_tokens(logits, data, stream_offsets, states, adjust=None, stream_ids=
         L.check(_decode(rows, logits, adjust, data, stream_offsets, stream_ids, states,
                         out_states, tokens, status), "decode_tokens")
     if given:
-        _written(*given)
+        _written(out_states, tokens)
     return tokens, out_states
 
 
