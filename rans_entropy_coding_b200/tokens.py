@@ -192,7 +192,7 @@ def rans_encode_intervals(starts, freqs, n, chunking, out, stream_offsets, works
 
 def _encode(dev, starts, freqs, n, S, chunking, out, stream_offsets, workspace):
     # (the chunking's own tensor: explicit stream starts)
-    if chunking._keep is not None and _device(chunking._keep, "stream starts") != dev:
+    if chunking._keep is not None and chunking._keep.get_device() != dev:
         raise ValueError("chunking on %s, starts on cuda:%d" % (chunking._keep.device, dev))
     s = _tensor(starts, torch.int32, (n,), dev, "starts")
     f = _tensor(freqs, torch.int32, (n,), dev, "freqs")
