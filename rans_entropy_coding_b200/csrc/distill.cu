@@ -13,15 +13,20 @@
 // past logits of 10^10, as masks have them, that is more than the exponential's
 // range.)
 //
-// A row is walked twice, once for R and once for the gradient; the second walk
-// finds most of it in L2.  With many rows a block takes a row; with few, a
-// cluster of blocks shares it and exchanges its maxima and sums.
-// Measured, loss and gradient: 4096 x 131072 bf16 with 128 listed tokens 480 us
-// (4.5 TB/s of one read and one write; 328 us at the copy's rate), 1001 x 50021
-// fp16 into rows at any alignment 62 us (31 us).  16 instructions a logit keep
-// the schedulers two thirds busy; four blocks an SM, each with a row of its own,
-// fill one another's waits (two blocks of 512 threads: 640 us; rows over
-// clusters of 4: 760 us).
+// A row is walked twice, once for R and once for the gradient.  With many rows a
+// block takes a row; with few, a cluster of blocks shares it and exchanges its
+// maxima and sums.
+// Measured, loss and gradient: 4096 x 131072 bf16 with 128 listed tokens 485 to
+// 498 us (4.4 TB/s of one read and one write; 328 us at the copy's rate),
+// 1001 x 50021 fp16 into rows at any alignment 63 us (31 us).  What bounds the
+// long rows is DRAM: four rows of 256 KB an SM are more than L2 holds, and 55%
+// of the second walk's reads leave it (480 MB read for 310 MB of rows, at
+// 1184 rows), at 84% of the copy's rate with the writes.  18 instructions a
+// logit keep the schedulers 63% and the special function units 50% busy; four
+// blocks an SM, each with a row of its own, fill one another's waits (two
+// blocks of 512 threads: 640 us; rows over clusters of 4: 760 us).  The exponent
+// as a difference and a product, where one multiply-add had 492 and 62 us,
+// costs 1 to 2%.
 #include <cmath>
 
 #include "cluster.cuh"
@@ -347,7 +352,8 @@ __global__ void __launch_bounds__(kDisThreads, 4)
   // inside the row is loaded when it is due.)
   auto inside = [&](int u) { return u >= row.shift && u + kTile <= row.end(); };
   // Four rows an SM are more than L2 holds, but half of them is behind its
-  // second walk: what that has read goes first, what it will read last.
+  // second walk: what that has read goes first, what it will read last.  (Nearly
+  // half of the second walk's reads are found there.)
   uint64_t keep, drop;
   asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(keep));
   asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(drop));
