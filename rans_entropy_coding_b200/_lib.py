@@ -308,6 +308,8 @@ def rans_decode_to_values(data, stream_offsets, scales, means, n, scale_table, s
 def rans_get_status(workspace, stream=None):
     """The first device error in a workspace or status word, read on `stream`
     or the current stream of the device that it lies on."""
+    if workspace is None:
+        return lib().rans_get_status(None, None)
     with torch.cuda.device(workspace.device):  # (a default stream is its device's)
         return lib().rans_get_status(_ptr(workspace), _stream(stream))
 

@@ -63,8 +63,9 @@ class _MadeOn:
         self.x, self.dev = x, dev
         self.stream = torch.cuda.current_stream(dev)
         self.captured = torch.cuda.is_current_stream_capturing()
-        self.done = torch.cuda.Event()
-        self.done.record(self.stream)
+        if not self.captured:
+            self.done = torch.cuda.Event()
+            self.done.record(self.stream)
 
     def use(self):
         if _raw_stream(self.dev) == self.stream.cuda_stream:

@@ -97,6 +97,21 @@ def test_per_row_numbers_in_a_captured_call():
         rb.adjust_logits(x, a, out=out)
     g.replay()
     assert torch.equal(out, want)
+    # made in the capture: its numbers are read at every replay, on a stream
+    # that joins as any other
+    t, side = torch.full((n,), 0.5, device="cuda"), torch.cuda.Stream()
+    g, other = torch.cuda.CUDAGraph(), torch.empty_like(x)
+    with torch.cuda.graph(g):
+        b = rb.LogitAdjust(temperature=t)
+        rb.adjust_logits(x, b, out=out)
+        side.wait_stream(torch.cuda.current_stream())
+        rb.adjust_logits(x, b, out=other, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+    for temperature in (2.0, 0.25):
+        t.fill_(temperature)
+        g.replay()
+        want = rb.adjust_logits(x, rb.LogitAdjust(temperature=temperature))
+        assert torch.equal(out, want) and torch.equal(other, want)
 
 
 # ----------------------------------------------------------- distillation --
