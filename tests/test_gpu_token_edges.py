@@ -502,3 +502,20 @@ def test_distillation_memory_that_may_be_shared(n):
                                       grad=wide[:, :v], status=st)
     assert torch.equal(got, want) and torch.equal(g, grad)
     status_ok(st)
+
+
+@pytest.mark.parametrize("dtype,n", [(BF16, 3), (BF16, 300), (F32, 2)], ids=str)
+def test_distillation_at_its_largest_sizes(dtype, n):
+    """The largest vocabulary and the longest list, in one block a row and in
+    several: the most shared memory that a launch asks for."""
+    v, K, T = rb.MAX_VOCAB, rb.MAX_TOP, 0.8
+    x = make_logits(n, v, dtype, 0, seed=46)
+    few = min(n, 4)
+    ids, lp = teacher(few, v, K, 46, True)
+    ids, lp = (np.concatenate([a] * (-(-n // few)))[:n] for a in (ids, lp))
+    g = np.linspace(0.5, 2.0, n).astype(np.float32)
+    st = rb.new_status()
+    rescales = -(-v // (8 * 32 * 4 * (16 // x.element_size())))
+    for losses, grad in both_ways(x, ids, lp, g, T, True, st):
+        check_rows(x, ids, lp, T, True, g, losses, grad, sorted({1, n // 2, n - 1}), rescales)
+    status_ok(st)
