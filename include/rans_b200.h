@@ -675,6 +675,82 @@ int rans_distill(const rans_logits *logits, const int32_t *ids, const float *log
                  int32_t K, float inv_temperature, int32_t tail, const float *grad_losses,
                  float *losses, void *grad, int64_t grad_stride, void *status, void *stream);
 
+/* --------------------------------------- microscaled 4-bit numbers ---- */
+
+/*
+ * A model's last product, hidden rows by the head's rows, on microscaled 4-bit
+ * numbers, for programs whose logits go to the coder above: it asks for the same
+ * logits, bit for bit, whether a text's rows come together or one by one.  Here a
+ * logit is one sum over the columns in one order, whatever the number of rows,
+ * their order or place, and the rows' quantisation is each row's own.
+ *
+ * The numbers (OCP Microscaling Formats (MX) Specification v1.0, MXFP4): a row
+ * is cut into blocks of 32 columns; a block has a scale 2^(byte - 127), and its
+ * elements are 0, 0.5, 1, 1.5, 2, 3, 4 or 6 with a sign, times the scale.
+ *   codes:  a row's elements two to a byte, the lower column in the low half,
+ *           16 bytes a block; a code is the magnitude's place in the list above,
+ *           plus 8 for negative ones.  Rows follow one another; a last block
+ *           that the columns do not fill is filled up with 0.
+ *   scales: tiles of 128 rows by 4 blocks, a row of tiles after another; in a
+ *           tile of 512 bytes row r's four bytes lie at 16 (r mod 32) +
+ *           4 (r div 32 mod 4).  Bytes of blocks past the columns must not be 255 (the
+ *           quantisation writes 0); rows past the last are not used.
+ * A byte of 255 makes its block's elements no numbers.
+ */
+typedef struct rans_mxfp4 {
+    uint8_t *codes;         /* device, 16-byte aligned */
+    uint8_t *scales;        /* device, 16-byte aligned */
+    int64_t rows;           /* up to 2^31 - 1 */
+    int64_t cols;           /* 1 .. RANS_MAX_VOCAB */
+} rans_mxfp4;
+
+/* Bytes of the two arrays; 0 for sizes out of range. */
+uint64_t rans_mxfp4_codes_bytes(int64_t rows, int64_t cols);
+uint64_t rans_mxfp4_scales_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Quantisation of rows (`vocab` columns of the logits' types, of any meaning).
+ * A block's scale is 2^(floor(log2 a) - 2), a its largest magnitude, at least
+ * 2^-127 (which blocks of zeros get); elements go to the nearest multiple, ties
+ * to the even code, and saturate at 6 (as the specification has it).  A block with an infinity or a NaN gets
+ * byte 255.
+ *   out: rows and cols as x has them; the arrays overlap neither x nor each
+ *        other.
+ * Asynchronous.
+ */
+int rans_mxfp4_quantize(const rans_logits *x, const rans_mxfp4 *out, void *stream);
+
+/* The numbers that the codes stand for, rounded once to out_dtype
+ * (RANS_LOGITS_*), row r at out + r * out_stride elements (out_stride >= cols
+ * when rows > 1), not over the codes or scales.  Asynchronous. */
+int rans_mxfp4_values(const rans_mxfp4 *q, void *out, int32_t out_dtype, int64_t out_stride,
+                      void *stream);
+
+/*
+ * out[n, v] = sum over k of a[n, k] * head[v, k], products exact, summed in
+ * float32 by the tensor cores in steps of 64 columns, one after another, and rounded once to
+ * out_dtype.  A NaN in a row of a, or of the head, makes its logits NaN.
+ *   a->cols == head->cols; head->rows is 1 .. RANS_MAX_VOCAB; row n of the
+ *   result at out + n * out_stride elements (out_stride >= head->rows when
+ *   a->rows > 1), over none of the arguments.
+ *   status: as for rans_token_intervals, or NULL; RANS_ERR_TIMEOUT if a bounded
+ *           wait gave up (the result is then undefined).
+ * Asynchronous.
+ */
+int rans_mxfp4_product(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out, int32_t out_dtype,
+                       int64_t out_stride, void *status, void *stream);
+
+/*
+ * Both for rows of floats: hidden (`vocab` = head->cols columns) is quantised
+ * into the workspace and multiplied.  workspace: device, 256-byte aligned,
+ * >= rans_mxfp4_logits_workspace_bytes(rows, cols); calls that may run at the
+ * same time need one each.  Other arguments as above.  Asynchronous.
+ */
+uint64_t rans_mxfp4_logits_workspace_bytes(int64_t rows, int64_t cols);
+int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head, void *out,
+                      int32_t out_dtype, int64_t out_stride, void *workspace,
+                      uint64_t workspace_bytes, void *status, void *stream);
+
 /* Synchronises `stream` and returns the first error recorded in `workspace`
  * (RANS_OK if none), then clears it. */
 int rans_get_status(void *workspace, void *stream);

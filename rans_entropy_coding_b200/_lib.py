@@ -78,13 +78,18 @@ class rans_adjust(ctypes.Structure):
                 ("mask", ctypes.c_void_p), ("mask_stride", ctypes.c_int64)]
 
 
+class rans_mxfp4(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
 # (name, restype, argtypes) for every exported symbol of include/rans_b200.h
 _P, _I32, _I64, _U64, _F64, _F32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint64, ctypes.c_double, ctypes.c_float)
 _CHP = ctypes.POINTER(rans_chunking)
 _TBP = ctypes.POINTER(rans_tables)
-# rans_logits and rans_adjust pointers: a byref() or a struct's packed bytes
-_LGP = _ADP = ctypes.c_void_p
+# rans_logits, rans_adjust and rans_mxfp4 pointers: a byref() or a struct's packed bytes
+_LGP = _ADP = _MXP = ctypes.c_void_p
 SIGNATURES = [
     ("rans_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("rans_version", ctypes.c_int, []),
@@ -124,6 +129,13 @@ SIGNATURES = [
     ("rans_distill_forward", ctypes.c_int, [_LGP, _P, _P, _I32, _F32, _I32, _P, _P, _P, _P]),
     ("rans_distill_backward", ctypes.c_int, [_LGP, _P, _P, _I32, _F32, _P, _P, _P, _I64, _P]),
     ("rans_distill", ctypes.c_int, [_LGP, _P, _P, _I32, _F32, _I32, _P, _P, _P, _I64, _P, _P]),
+    ("rans_mxfp4_codes_bytes", _U64, [_I64, _I64]),
+    ("rans_mxfp4_scales_bytes", _U64, [_I64, _I64]),
+    ("rans_mxfp4_quantize", ctypes.c_int, [_LGP, _MXP, _P]),
+    ("rans_mxfp4_values", ctypes.c_int, [_MXP, _P, _I32, _I64, _P]),
+    ("rans_mxfp4_product", ctypes.c_int, [_MXP, _MXP, _P, _I32, _I64, _P, _P]),
+    ("rans_mxfp4_logits_workspace_bytes", _U64, [_I64, _I64]),
+    ("rans_mxfp4_logits", ctypes.c_int, [_LGP, _MXP, _P, _I32, _I64, _P, _U64, _P, _P]),
     ("rans_get_status", ctypes.c_int, [_P, _P]),
     ("rans_debug_divide", ctypes.c_int, [_P, _P, _I64, _P, _P, _P]),
     ("rans_debug_wait_timeout", ctypes.c_int, [_P, ctypes.c_uint32, _P]),

@@ -10,6 +10,7 @@
 #include <nvtx3/nvToolsExt.h>
 
 #include "rans_common.cuh"
+#include "mxfp4.cuh"
 #include "rans_internal.h"
 
 #define RANS_API extern "C" __attribute__((visibility("default")))
@@ -670,6 +671,49 @@ int check_distill_memory(const rans_logits *in, const int32_t *ids, const float 
   return RANS_OK;
 }
 
+// ------------------------------------------ microscaled 4-bit numbers --
+bool mx_sizes_ok(int64_t rows, int64_t cols) {
+  return rows >= 0 && rows <= 0x7fffffff && cols >= 1 && cols <= RANS_MAX_VOCAB;
+}
+uint64_t mx_codes(const rans_mxfp4 *q) { return rans_mxfp4_codes_bytes(q->rows, q->cols); }
+uint64_t mx_scales(const rans_mxfp4 *q) { return rans_mxfp4_scales_bytes(q->rows, q->cols); }
+
+int check_mxfp4(const rans_mxfp4 *q) {
+  if (!q || !mx_sizes_ok(q->rows, q->cols)) return RANS_ERR_ARG;
+  if (q->rows > 0 && (!q->codes || !q->scales)) return RANS_ERR_ARG;
+  return aligned_to(q->codes, 16) && aligned_to(q->scales, 16) ? RANS_OK : RANS_ERR_ARG;
+}
+
+// Whether a result of `rows` rows of `cols` elements is well formed.
+int check_rows_out(const void *out, int64_t rows, int64_t cols, int32_t dtype, int64_t stride) {
+  const int e = logits_bytes(dtype);
+  if (e == 0) return RANS_ERR_ARG;
+  if (rows == 0) return RANS_OK;
+  if (!out || !aligned_to(out, (uint64_t)e) || (rows > 1 && stride < cols)) return RANS_ERR_ARG;
+  return RANS_OK;
+}
+uint64_t rows_bytes(int64_t rows, int64_t cols, int64_t stride, int32_t dtype) {
+  return rows == 0 ? 0
+                   : ((uint64_t)(rows - 1) * (uint64_t)stride + (uint64_t)cols) *
+                         (uint64_t)logits_bytes(dtype);
+}
+bool on_mxfp4(const void *p, uint64_t bytes, const rans_mxfp4 *q) {
+  return overlap(p, bytes, q->codes, mx_codes(q)) || overlap(p, bytes, q->scales, mx_scales(q));
+}
+
+int check_head(const rans_mxfp4 *head, int64_t rows, int64_t cols, const void *out,
+               int32_t out_dtype, int64_t out_stride, const void *status) {
+  int st = check_mxfp4(head);
+  if (st) return st;
+  if (head->rows < 1 || head->rows > RANS_MAX_VOCAB || head->cols != cols) return RANS_ERR_ARG;
+  st = check_rows_out(out, rows, head->rows, out_dtype, out_stride);
+  if (!st && status) st = check_status_word(status);
+  if (st) return st;
+  const uint64_t bytes = rows_bytes(rows, head->rows, out_stride, out_dtype);
+  return on_mxfp4(out, bytes, head) || overlap(out, bytes, status, 256) ? RANS_ERR_ARG : RANS_OK;
+}
+uint64_t up256(uint64_t x) { return (x + 255) & ~255ull; }
+
 }  // namespace
 
 RANS_API int rans_adjust_logits(const rans_logits *logits, const rans_adjust *adjust, void *out,
@@ -826,6 +870,82 @@ RANS_API int rans_distill(const rans_logits *logits, const int32_t *ids, const f
   return rb::launch_distill(*logits, ids, logprobs, K, inv_temperature, tail, grad_losses, losses,
                             grad, grad_stride, static_cast<int32_t *>(status),
                             as_stream(stream));
+}
+
+RANS_API uint64_t rans_mxfp4_codes_bytes(int64_t rows, int64_t cols) {
+  if (!mx_sizes_ok(rows, cols)) return 0;
+  return (uint64_t)rows * (uint64_t)rb::mx_row_bytes(cols);
+}
+
+RANS_API uint64_t rans_mxfp4_scales_bytes(int64_t rows, int64_t cols) {
+  if (!mx_sizes_ok(rows, cols)) return 0;
+  return (uint64_t)cdiv(rows, rb::kMxTileRows) * (uint64_t)rb::mx_groups(cols) * rb::kMxTileBytes;
+}
+
+RANS_API int rans_mxfp4_quantize(const rans_logits *x, const rans_mxfp4 *out, void *stream) {
+  NvtxRange nvtx_("rans_mxfp4_quantize");
+  int st = check_logits(x);
+  if (!st) st = check_mxfp4(out);
+  if (st) return st;
+  if (x->rows != out->rows || x->vocab != out->cols) return RANS_ERR_ARG;
+  if (x->rows == 0) return RANS_OK;
+  const uint64_t in = rows_bytes(x->rows, x->vocab, x->row_stride, x->dtype);
+  if (on_mxfp4(x->data, in, out) || overlap(out->codes, mx_codes(out), out->scales, mx_scales(out)))
+    return RANS_ERR_ARG;
+  return rb::launch_mxfp4_quantize(*x, *out, as_stream(stream));
+}
+
+RANS_API int rans_mxfp4_values(const rans_mxfp4 *q, void *out, int32_t out_dtype,
+                               int64_t out_stride, void *stream) {
+  NvtxRange nvtx_("rans_mxfp4_values");
+  int st = check_mxfp4(q);
+  if (!st) st = check_rows_out(out, q->rows, q->cols, out_dtype, out_stride);
+  if (st || q->rows == 0) return st;
+  if (on_mxfp4(out, rows_bytes(q->rows, q->cols, out_stride, out_dtype), q)) return RANS_ERR_ARG;
+  return rb::launch_mxfp4_values(*q, out, out_dtype, out_stride, as_stream(stream));
+}
+
+RANS_API int rans_mxfp4_product(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
+                                int32_t out_dtype, int64_t out_stride, void *status,
+                                void *stream) {
+  NvtxRange nvtx_("rans_mxfp4_product");
+  int st = check_mxfp4(a);
+  if (!st) st = check_head(head, a->rows, a->cols, out, out_dtype, out_stride, status);
+  if (st || a->rows == 0) return st;
+  if (on_mxfp4(out, rows_bytes(a->rows, head->rows, out_stride, out_dtype), a)) return RANS_ERR_ARG;
+  return rb::launch_mxfp4_product(*a, *head, out, out_dtype, out_stride,
+                                  static_cast<int32_t *>(status), false, as_stream(stream));
+}
+
+RANS_API uint64_t rans_mxfp4_logits_workspace_bytes(int64_t rows, int64_t cols) {
+  return up256(rans_mxfp4_codes_bytes(rows, cols)) + rans_mxfp4_scales_bytes(rows, cols);
+}
+
+RANS_API int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head, void *out,
+                               int32_t out_dtype, int64_t out_stride, void *workspace,
+                               uint64_t workspace_bytes, void *status, void *stream) {
+  NvtxRange nvtx_("rans_mxfp4_logits");
+  int st = check_logits(hidden);
+  if (!st) st = check_head(head, hidden->rows, hidden->vocab, out, out_dtype, out_stride, status);
+  if (st) return st;
+  if (hidden->rows == 0) return RANS_OK;
+  if (hidden->rows > 0x7fffffff) return RANS_ERR_ARG;
+  const uint64_t need = rans_mxfp4_logits_workspace_bytes(hidden->rows, hidden->vocab);
+  if (!workspace || !aligned_to(workspace, 256)) return RANS_ERR_ARG;
+  if (workspace_bytes < need) return RANS_ERR_CAPACITY;
+  const uint64_t res = rows_bytes(hidden->rows, head->rows, out_stride, out_dtype);
+  const uint64_t in = rows_bytes(hidden->rows, hidden->vocab, hidden->row_stride, hidden->dtype);
+  if (overlap(workspace, need, out, res) || overlap(workspace, need, hidden->data, in) ||
+      overlap(out, res, hidden->data, in) || on_mxfp4(workspace, need, head) ||
+      overlap(workspace, need, status, 256))
+    return RANS_ERR_ARG;
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  const rans_mxfp4 a = {ws, ws + up256(rans_mxfp4_codes_bytes(hidden->rows, hidden->vocab)),
+                        hidden->rows, hidden->vocab};
+  st = rb::launch_mxfp4_quantize(*hidden, a, as_stream(stream));
+  if (st) return st;
+  return rb::launch_mxfp4_product(a, *head, out, out_dtype, out_stride,
+                                  static_cast<int32_t *>(status), true, as_stream(stream));
 }
 
 RANS_API int rans_get_status(void *workspace, void *stream) {

@@ -1,0 +1,375 @@
+// mxfp4_product.cu -- products of rows of microscaled 4-bit numbers: a model's
+// output head, out[n, v] = sum over k of a[n, k] w[v, k].
+//
+// The fifth-generation tensor cores multiply such numbers with their scales
+// (kind::mxf4, 64 columns an instruction) into float32 accumulators in tensor
+// memory.  The head's rows are the instruction's 128 rows and the tokens its
+// columns (16 to 256): one token then costs no more than the weights' bytes,
+// and an accumulator's lanes are consecutive logits.  An output is the sum of
+// the same instructions' results over k in the same order whatever the number
+// of tokens, their place in the batch or the tile's width, and no tile is split
+// along k: a row's logits do not depend on the batch it came in.
+//
+// A block per SM walks tiles of 128 head rows by up to 256 tokens (tokens
+// fastest, so that neighbours share the head's rows in L2).  One thread copies
+// stages of 256 columns (TMA, 128-byte swizzle; scales by bulk copies) through a
+// ring in shared memory, one copies the scales on to tensor memory and issues
+// the products, and eight warps take the accumulators: each keeps half of a
+// row's columns in registers, so that the next tile's products start as soon as
+// tensor memory is read, while the logits are still being rounded and stored.
+#include <cuda.h>
+
+#include "mxfp4.cuh"
+#include "logits_common.cuh"
+#include "rans_common.cuh"
+#include "rans_internal.h"
+
+namespace rb {
+namespace {
+
+constexpr int kHeadRows = 128;                  // of a tile
+constexpr int kMostTokens = 256;
+constexpr int kStageCols = 256;                 // 128 bytes of codes a row
+constexpr int kStageBytes = kStageCols / 2;
+constexpr int kStepCols = 64;                   // of one instruction
+constexpr int kMaxStages = 12;
+constexpr int kEpilogueWarps = 8;
+constexpr int kProductThreads = 128 + 32 * kEpilogueWarps;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kScaleCol = 256;             // scales behind the accumulators
+constexpr uint32_t kScaleCols = 24;             // of one stage: 8 of the head, 16 of the tokens
+constexpr uint32_t kTries = 1u << 21;           // of a bounded wait, about 1 us each
+
+struct ProductShape {
+  int32_t tokens, head_rows;  // n, V
+  int32_t box;                // tokens of a stage's tile (a multiple of 16)
+  int32_t token_tiles, tiles;
+  int32_t steps;              // of 64 columns
+  int32_t groups;             // of 128 columns
+  int32_t stages;             // of the ring
+  int32_t wait;               // the tokens come from the kernel before
+};
+
+__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr) {
+  // 8 rows of 128 bytes are 1024 bytes; version 1; 128-byte swizzle
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
+         (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+__device__ __forceinline__ uint64_t plain_desc(uint32_t addr) {
+  // 8 rows of 16 bytes are 128 bytes; no swizzle
+  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
+}
+// 4-bit floats with scales of an exponent's byte, rows along k on both sides.
+__device__ __forceinline__ uint32_t instruction(int tokens, int scale_byte) {
+  return (uint32_t)scale_byte << 4 | 1u << 7 | 1u << 10 | (uint32_t)(tokens >> 3) << 17 |
+         1u << 23 | (uint32_t)(kHeadRows >> 4) << 24 | (uint32_t)scale_byte << 29;
+}
+__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t sfa, uint32_t sfb, bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
+      "[%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+      : "memory");
+}
+__device__ __forceinline__ void copy_scales(uint32_t to, uint64_t desc) {
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                   bar)
+               : "memory");
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void load_2d(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void load_bulk(uint32_t dst, const void *src, uint32_t bytes,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// Eight columns of a warp's 32 accumulator lanes.
+__device__ __forceinline__ void load_columns(float *v, uint32_t at) {
+  uint32_t *u = reinterpret_cast<uint32_t *>(v);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]),
+                 "=r"(u[6]), "=r"(u[7])
+               : "r"(at));
+}
+
+// HALF: most columns that an epilogue warp keeps.
+template <typename O, int HALF>
+__global__ void __launch_bounds__(kProductThreads, 1)
+    product_kernel(const __grid_constant__ CUtensorMap head_map,
+                   const __grid_constant__ CUtensorMap token_map, const uint8_t *head_scales,
+                   const uint8_t *token_scales, O *out, int64_t out_stride, ProductShape sh,
+                   int32_t *status) {
+  extern __shared__ unsigned char smem_raw[];
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, free_bar;
+  __shared__ uint32_t tmem_base;
+  __shared__ volatile int dead;  // a wait gave up
+  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  const uint32_t token_bytes = (uint32_t)sh.box * kStageBytes;
+  const int row_tiles = (sh.box + kMxTileRows - 1) / kMxTileRows;
+  const uint32_t at_tokens = kHeadRows * kStageBytes, at_head_scales = at_tokens + token_bytes;
+  const uint32_t at_token_scales = at_head_scales + 2 * kMxTileBytes;
+  const uint32_t stage_bytes = at_token_scales + (uint32_t)row_tiles * 2 * kMxTileBytes;
+  const int per_tile = (sh.steps + 3) / 4;  // stages of a tile
+
+  if (wid == 0) {
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&head_map)) : "memory");
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&token_map)) : "memory");
+    }
+  } else if (wid == 1) {
+    if (lane == 0) {
+      for (int i = 0; i < sh.stages; ++i) {
+        tma::mbar_init(smem_addr(&full_bar[i]), 1);
+        tma::mbar_init(smem_addr(&empty_bar[i]), 1);
+      }
+      tma::mbar_init(smem_addr(&done_bar), 1);
+      tma::mbar_init(smem_addr(&free_bar), kEpilogueWarps);
+      dead = 0;
+      tma::fence_mbar_init();
+      tma::fence_proxy_async();
+    }
+  } else if (wid == 2) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&tmem_base)),
+                 "n"(kTmemCols)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  }
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+  const uint32_t tmem = tmem_base;
+  // (what a thread may wait: until another gave up, or for its own share)
+  auto wait = [&](uint64_t *bar, uint32_t parity) {
+    const uint32_t b = smem_addr(bar);
+    for (uint32_t i = 0; i < kTries && !dead; ++i)
+      if (mbar_try_wait(b, parity)) return true;
+    if (!dead) {
+      dead = 1;
+      if (status) report(status, RANS_ERR_TIMEOUT, -1);
+    }
+    return false;
+  };
+
+  if (wid == 0 && lane == 0) {
+    // ------------------------------------------------------- the copies --
+    const int total = ((sh.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x) * per_tile;
+    auto place = [&](int it, int &stage, int &mt, int &nt, int &kb, uint32_t &groups) {
+      stage = it % sh.stages;
+      const int tile = (int)blockIdx.x + it / per_tile * (int)gridDim.x;
+      kb = it % per_tile;
+      mt = tile / sh.token_tiles;
+      nt = tile % sh.token_tiles;
+      groups = (uint32_t)min(2, sh.groups - 2 * kb);
+    };
+    auto load_head = [&](int it) {
+      int stage, mt, nt, kb;
+      uint32_t groups;
+      place(it, stage, mt, nt, kb, groups);
+      const uint32_t bar = smem_addr(&full_bar[stage]), s = smem + stage * stage_bytes;
+      const int tiles = min(row_tiles, (sh.tokens - nt * kMostTokens + kMxTileRows - 1) / kMxTileRows);
+      tma::arrive_expect(bar, at_head_scales + groups * kMxTileBytes * (uint32_t)(1 + tiles));
+      load_2d(s, &head_map, kb * kStageBytes, mt * kHeadRows, bar);
+      load_bulk(s + at_head_scales, head_scales + ((int64_t)mt * sh.groups + 2 * kb) * kMxTileBytes,
+                groups * kMxTileBytes, bar);
+    };
+    auto load_tokens = [&](int it) {
+      int stage, mt, nt, kb;
+      uint32_t groups;
+      place(it, stage, mt, nt, kb, groups);
+      const uint32_t bar = smem_addr(&full_bar[stage]), s = smem + stage * stage_bytes;
+      load_2d(s + at_tokens, &token_map, kb * kStageBytes, nt * kMostTokens, bar);
+      for (int h = 0; h < row_tiles; ++h) {
+        const int64_t tile = nt * (kMostTokens / kMxTileRows) + h;
+        if (tile * kMxTileRows < sh.tokens)
+          load_bulk(s + at_token_scales + h * 2 * kMxTileBytes,
+                    token_scales + (tile * sh.groups + 2 * kb) * kMxTileBytes,
+                    groups * kMxTileBytes, bar);
+      }
+    };
+    // the head's first stages do not wait for the tokens' quantisation
+    const int ahead = min(total, sh.stages);
+    for (int it = 0; it < ahead; ++it) load_head(it);
+    if (sh.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int it = 0; it < ahead; ++it) load_tokens(it);
+    int it = ahead;
+    for (; it < total; ++it) {
+      if (!wait(&empty_bar[it % sh.stages], (uint32_t)(it / sh.stages - 1) & 1)) break;
+      load_head(it);
+      load_tokens(it);
+    }
+    if (dead) {
+      // copies in flight write to this block's memory: they end first
+      for (int i = max(0, it - sh.stages); i < it; ++i)
+        tma::wait_bounded(smem_addr(&full_bar[i % sh.stages]), (uint32_t)(i / sh.stages) & 1, kTries);
+    }
+  } else if (wid == 1 && lane == 0) {
+    // ----------------------------------------------------- the products --
+    int it = 0, n_tile = 0;
+    for (int tile = (int)blockIdx.x; tile < sh.tiles && !dead; tile += (int)gridDim.x, ++n_tile) {
+      const int left = sh.tokens - tile % sh.token_tiles * kMostTokens;
+      const int width = min(sh.box, (left + 15) & ~15);
+      const uint32_t idesc0 = instruction(width, 0), idesc2 = instruction(width, 2);
+      if (n_tile > 0 && !wait(&free_bar, (uint32_t)(n_tile - 1) & 1)) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      bool ok = true;
+      for (int kb = 0; kb < per_tile; ++kb, ++it) {
+        const int stage = it % sh.stages;
+        ok = wait(&full_bar[stage], (uint32_t)(it / sh.stages) & 1);
+        if (!ok) break;
+        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+        const uint32_t s = smem + stage * stage_bytes;
+        const uint32_t sf = tmem + kScaleCol + (it & 1) * kScaleCols;
+        const int groups = min(2, sh.groups - 2 * kb), steps = min(4, sh.steps - 4 * kb);
+        for (int g = 0; g < groups; ++g) {
+          copy_scales(sf + 4 * g, plain_desc(s + at_head_scales + g * kMxTileBytes));
+          for (int h = 0; h * kMxTileRows < width; ++h)
+            copy_scales(sf + 8 + 8 * g + 4 * h,
+                        plain_desc(s + at_token_scales + h * 2 * kMxTileBytes + g * kMxTileBytes));
+        }
+        const uint64_t a = swizzled_desc(s), b = swizzled_desc(s + at_tokens);
+        for (int j = 0; j < steps; ++j)
+          // 64 columns are 32 bytes, 2 in units of the descriptor
+          multiply(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0, sf + 4 * (j >> 1),
+                   sf + 8 + 8 * (j >> 1), kb > 0 || j > 0);
+        commit(smem_addr(&empty_bar[stage]));
+      }
+      if (!ok) break;
+      commit(smem_addr(&done_bar));
+    }
+    if (dead) {
+      // products in flight: a last commit follows them
+      commit(smem_addr(&done_bar));
+      tma::wait_bounded(smem_addr(&done_bar), (uint32_t)n_tile & 1, kTries);
+    }
+  } else if (wid >= 4) {
+    // --------------------------------------------------- the accumulators --
+    const int quarter = wid & 3, half = (wid - 4) >> 2;
+    int n_tile = 0;
+    for (int tile = (int)blockIdx.x; tile < sh.tiles; tile += (int)gridDim.x, ++n_tile) {
+      const int mt = tile / sh.token_tiles, n0 = tile % sh.token_tiles * kMostTokens;
+      const int left = sh.tokens - n0, width = min(sh.box, (left + 15) & ~15);
+      const int c0 = half * (width / 2);
+      const int count = min(width / 2, left - c0);  // columns of this warp that are tokens
+      if (!__all_sync(kFull, wait(&done_bar, (uint32_t)n_tile & 1))) break;
+      asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+      float v[HALF];
+#pragma unroll
+      for (int i = 0; i < HALF; i += 8)
+        if (i < count) load_columns(v + i, tmem + ((uint32_t)quarter << 21) + c0 + i);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+      // (nothing is computed from the registers before that)
+#pragma unroll
+      for (int i = 0; i < HALF; ++i) asm volatile("" : "+f"(v[i]));
+      asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+      __syncwarp();
+      if (lane == 0) arrive(smem_addr(&free_bar));
+      const int row = mt * kHeadRows + quarter * 32 + lane;
+      if (row < sh.head_rows) {
+        O *o = out + (int64_t)(n0 + c0) * out_stride + row;
+#pragma unroll
+        for (int i = 0; i < HALF; ++i)
+          if (i < count) o[i * out_stride] = float_logit<O>(v[i]);
+      }
+    }
+  }
+  __syncwarp();
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+  __syncthreads();
+  if (wid == 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "n"(kTmemCols));
+  }
+}
+
+template <typename O, int HALF>
+int launch_t(const CUtensorMap &hm, const CUtensorMap &tm, const rans_mxfp4 &a,
+             const rans_mxfp4 &w, void *out, int64_t stride, const ProductShape &sh,
+             uint32_t smem, int32_t *status, int sms, cudaStream_t st) {
+  auto kern = product_kernel<O, HALF>;
+  if (ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(sh.tiles < sms ? sh.tiles : sms));
+  cfg.blockDim = dim3(kProductThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = sh.wait ? 1 : 0;
+  const cudaError_t e =
+      cudaLaunchKernelEx(&cfg, kern, hm, tm, (const uint8_t *)w.scales, (const uint8_t *)a.scales,
+                         static_cast<O *>(out), stride, sh, status);
+  return e == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
+}
+
+template <typename O>
+int launch_o(const CUtensorMap &hm, const CUtensorMap &tm, const rans_mxfp4 &a,
+             const rans_mxfp4 &w, void *out, int64_t stride, const ProductShape &sh,
+             uint32_t smem, int32_t *status, int sms, cudaStream_t st) {
+  if (sh.box <= 32) return launch_t<O, 16>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+  if (sh.box <= 128) return launch_t<O, 64>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+  return launch_t<O, 128>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+}
+
+}  // namespace
+
+int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, int dtype,
+                         int64_t stride, int32_t *status, bool follows, cudaStream_t st) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
+  ProductShape sh;
+  sh.tokens = (int32_t)a.rows;
+  sh.head_rows = (int32_t)w.rows;
+  sh.box = a.rows >= kMostTokens ? kMostTokens : (int32_t)((a.rows + 15) & ~15);
+  sh.token_tiles = (sh.tokens + kMostTokens - 1) / kMostTokens;
+  const int64_t tiles = (int64_t)sh.token_tiles * ((w.rows + kHeadRows - 1) / kHeadRows);
+  sh.steps = (int32_t)((w.cols + kStepCols - 1) / kStepCols);
+  sh.groups = mx_groups(w.cols);
+  // a block's stages are counted in 31 bits
+  if (tiles * ((sh.steps + 3) / 4) > 0x3fffffff) return RANS_ERR_ARG;
+  sh.tiles = (int32_t)tiles;
+  sh.wait = follows ? 1 : 0;
+  const uint32_t stage = kHeadRows * kStageBytes + (uint32_t)sh.box * kStageBytes +
+                         2 * kMxTileBytes * (1 + (uint32_t)(sh.box + kMxTileRows - 1) / kMxTileRows);
+  const uint32_t room = (uint32_t)smem_optin(dev) - 2048;  // its static part, alignment
+  sh.stages = (int32_t)(room / stage < (uint32_t)kMaxStages ? room / stage : kMaxStages);
+  if (sh.stages < 2) return RANS_ERR_CUDA;
+  CUtensorMap hm, tm;
+  const uint64_t row = (uint64_t)mx_row_bytes(w.cols);
+  int e = encode_rows_map(&hm, w.codes, row, (uint64_t)w.rows, kStageBytes, kHeadRows);
+  if (!e) e = encode_rows_map(&tm, a.codes, row, (uint64_t)a.rows, kStageBytes, (uint32_t)sh.box);
+  if (e) return e;
+  const uint32_t smem = stage * (uint32_t)sh.stages + 1024;
+  const int sms = num_sms(dev);
+  switch (dtype) {
+    case RANS_LOGITS_F32:
+      return launch_o<float>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+    case RANS_LOGITS_F16:
+      return launch_o<__half>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+    default:
+      return launch_o<__nv_bfloat16>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+  }
+}
+
+}  // namespace rb

@@ -95,11 +95,25 @@ int launch_distill(const rans_logits &in, const int32_t *ids, const float *lp, i
                    float inv_t, int tail, const float *grads, float *losses, void *grad,
                    int64_t stride, int32_t *status, cudaStream_t st);
 
+// Rows to microscaled 4-bit numbers and back; products of such rows.  follows:
+// a's codes and scales come from the launch before, which the product's first
+// steps overlap.
+int launch_mxfp4_quantize(const rans_logits &x, const rans_mxfp4 &q, cudaStream_t st);
+int launch_mxfp4_values(const rans_mxfp4 &q, void *out, int dtype, int64_t stride,
+                        cudaStream_t st);
+int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, int dtype,
+                         int64_t stride, int32_t *status, bool follows, cudaStream_t st);
+
 // A tensor map (CUtensorMap, 128 bytes, 64-byte aligned) for a 3-D int32
 // tensor of width x height x depth elements (row-major, width fastest) and a
 // box of box_w x box_h x 1; base 16-byte aligned, width * 4 a multiple of 16.
 int encode_tile_map(void *map, const void *base, uint64_t width, uint64_t height,
                     uint64_t depth, uint32_t box_w, uint32_t box_h);
+
+// The same for rows of bytes (16-byte aligned, a multiple of 16 each), in boxes
+// of 128 bytes by box_rows, with the 128-byte swizzle; bytes off the ends read 0.
+int encode_rows_map(void *map, const void *base, uint64_t row_bytes, uint64_t rows,
+                    uint32_t box_bytes, uint32_t box_rows);
 
 // Whether float latents (staged tensors a and b) can take the tile kernels.
 bool flt_tile_shape_ok(const Geom &g, const void *a, const void *b);

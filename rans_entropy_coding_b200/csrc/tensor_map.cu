@@ -59,6 +59,24 @@ int encode_tile_map(void *map, const void *base, uint64_t width, uint64_t height
   return r == CUDA_SUCCESS ? RANS_OK : RANS_ERR_CUDA;
 }
 
+int encode_rows_map(void *map, const void *base, uint64_t row_bytes, uint64_t rows,
+                    uint32_t box_bytes, uint32_t box_rows) {
+  EncodeTiledFn f = encode_fn();
+  if (f == nullptr) return RANS_ERR_CUDA;
+  if ((reinterpret_cast<uintptr_t>(base) & 15) != 0 || row_bytes % 16 != 0 || box_bytes != 128 ||
+      box_rows == 0 || box_rows > 256)
+    return RANS_ERR_ARG;
+  const cuuint64_t dims[2] = {row_bytes, rows};
+  const cuuint64_t strides[1] = {row_bytes};
+  const cuuint32_t box[2] = {box_bytes, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  const CUresult r = f(reinterpret_cast<CUtensorMap *>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
+                       const_cast<void *>(base), dims, strides, box, estr,
+                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                       CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? RANS_OK : RANS_ERR_CUDA;
+}
+
 // Float latents on the tile kernels: tiled W = 32 streams (64-bit format,
 // no alias, one scale per element) whose tiles are all 64 or 56 wide and a
 // multiple of 4 rows high, the two staged tensors 16-byte aligned.
