@@ -751,6 +751,114 @@ int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head, void *o
                       int32_t out_dtype, int64_t out_stride, void *workspace,
                       uint64_t workspace_bytes, void *status, void *stream);
 
+/* ---------------------------------------------------- beam search ---- */
+
+/*
+ * The best continuations of every text.  Rows of logits are the beams of the
+ * texts, `beams` rows a text, in order; scores[r] is the log probability of beam
+ * r so far (-inf: the beam is dead, and its row is not read).  With x = the
+ * adjusted logits (as rans_adjust_logits has them, in float32 before the output's
+ * rounding) a continuation of beam r by token v has
+ *     total = scores[r] + x_v - log(sum over w of e^(x_w)),
+ * summed beyond float32's precision and compared in 64 bits; of equal totals the
+ * lower beam, then the lower token is the better one.  Per text the `count` best go
+ * out, best first: scores_out (the total rounded to float32), tokens and
+ * parents (the beam within its text), [texts][count] each.  Tokens whose x is
+ * -inf are no continuations; where there are fewer than `count`, the rest is
+ * -inf, -1 and -1.
+ *   A NaN or +inf logit of a token that the mask allows, a score that is NaN or
+ *   +inf, and a row's own inv_temperature that is not positive and finite are
+ *   RANS_ERR_RANGE in `status`; such a beam has no continuations.
+ *   beams: 1 .. RANS_MAX_BEAMS, dividing the rows; count: 1 ..
+ *   RANS_MAX_CONTINUATIONS; adjust may be NULL; status: as for
+ *   rans_token_intervals, or NULL.
+ *   workspace: device, 256-byte aligned, >= rans_beam_workspace_bytes; calls
+ *   that may run at the same time need one each.  No result overlaps an
+ *   argument or another result.
+ * The same call twice gives the same bits.  Asynchronous.
+ */
+#define RANS_MAX_BEAMS 64
+#define RANS_MAX_CONTINUATIONS 128
+
+uint64_t rans_beam_workspace_bytes(int32_t dtype, int64_t rows, int32_t vocab, int32_t count);
+int rans_beam_select(const rans_logits *logits, const rans_adjust *adjust, const float *scores,
+                     int32_t beams, int32_t count, float *scores_out, int32_t *tokens,
+                     int32_t *parents, void *workspace, uint64_t workspace_bytes, void *status,
+                     void *stream);
+
+/*
+ * A search's bookkeeping.  Per text the candidates (as rans_beam_select writes
+ * them) are taken best first.  One that ends (its token is one of `ends`)
+ * becomes a result if it is among the first `beams` candidates: its score
+ * is divided by length^length_penalty (length with the ending token), and the
+ * `beams` best results are kept, earlier ones before equal later ones.  The others
+ * go on until `beams` do.  The first child of a beam takes its slot and other
+ * children the free slots, in order, so that few states have to move and a
+ * moving beam's source stays; scores are not sorted.  Slots without a child are dead: score
+ * -inf, token `pad`, parent themselves.
+ *   A text is over, and its beams' scores -inf, when no beam goes on; when its
+ *   results are full and no beam can come to more than the worst of them
+ *   (at the present length, or at the capacity for a positive penalty); or, with
+ *   `early`, as soon as they are full.  A text whose length has reached the
+ *   capacity is left as it is (its parents are the beams themselves).
+ * All device arrays, caller-owned, none over another; T texts, K beams, C the
+ * capacity.  Start: lengths, done_counts and over 0, scores 0 for each text's first
+ * beam and -inf for the others.
+ * Asynchronous.
+ */
+typedef struct rans_beams {
+    int64_t texts;
+    int32_t beams;             /* 1 .. RANS_MAX_BEAMS */
+    int32_t capacity;          /* tokens of a history, >= 1 */
+    const int32_t *ends;       /* [n_ends] */
+    int32_t n_ends;            /* 0 .. 64 */
+    int32_t pad;
+    float length_penalty;      /* finite */
+    int32_t early;
+    float *scores;             /* [T][K] of the beams, for the next selection */
+    int32_t *tokens;           /* [T][K] their last tokens */
+    int32_t *parents;          /* [T][K] the slots they come from */
+    int32_t *history;          /* [T][K][C] their tokens */
+    int64_t *window_end;       /* [T][K] where these end in `history` (rans_adjust) */
+    int32_t *lengths;          /* [T] tokens so far */
+    int32_t *over;             /* [T] 1: over */
+    float *done_scores;        /* [T][K] results: penalised score, */
+    int32_t *done_lengths;     /* [T][K] tokens, */
+    int32_t *done_tokens;      /* [T][K][C] the tokens */
+    int32_t *done_counts;      /* [T] and how many there are */
+} rans_beams;
+
+int rans_beam_advance(const float *scores, const int32_t *tokens, const int32_t *parents,
+                      int32_t count, const rans_beams *search, void *stream);
+
+/*
+ * States that follow their beams, in place: row b of text t becomes what row
+ * parents[t][b] was (any map, cycles too; -1 and b itself leave the row as it is,
+ * anything else outside 0 .. beams - 1 is RANS_ERR_INDEX in `status` and leaves
+ * it too).  A state has `texts` * `beams` rows; row r is `segments` pieces of
+ * positions * position_bytes bytes, at data + r * row_stride + s *
+ * segment_stride (in bytes).  lengths [texts] (or NULL: all): only the first
+ * lengths[t] positions of a piece are moved, what lies behind is left.
+ *   States neither overlap each other nor parents, lengths or status
+ *   (RANS_ERR_ARG), nor do a state's own rows and pieces: row_stride holds a
+ *   row's pieces, and segment_stride one piece.
+ *   n_states: 0 .. RANS_MAX_STATES; status: as above, or NULL.  Asynchronous.
+ */
+#define RANS_MAX_STATES 4096
+
+typedef struct rans_state {
+    void *data;
+    int64_t row_stride;
+    int64_t segment_stride;
+    int64_t positions;
+    int32_t segments;
+    int32_t position_bytes;
+} rans_state;
+
+int rans_reorder_states(const rans_state *states, int32_t n_states, int64_t texts, int32_t beams,
+                        const int32_t *parents, const int32_t *lengths, void *status,
+                        void *stream);
+
 /* Synchronises `stream` and returns the first error recorded in `workspace`
  * (RANS_OK if none), then clears it. */
 int rans_get_status(void *workspace, void *stream);

@@ -18,7 +18,7 @@ from ._lib import (  # noqa: F401
     rans_gaussian_lengths, rans_get_status, rans_max_compressed_bytes, rans_num_streams,
     rans_tables, rans_tables_bytes, rans_tables_prepare, rans_tables_refresh,
     rans_tables_refresh_from_scales)
-from ._lib import rans_adjust, rans_logits, rans_mxfp4  # noqa: F401,E402
+from ._lib import rans_adjust, rans_beams, rans_logits, rans_mxfp4, rans_state  # noqa: F401,E402
 from .tokens import (  # noqa: F401,E402
     MAX_TOP, MAX_VOCAB, TOKEN_PRECISION, LogitAdjust, adjust_logits, decode_tokens,
     distill_loss, distill_loss_and_grad, encode_intervals, new_status, pack_mask,
@@ -29,5 +29,8 @@ from .mxfp4 import (  # noqa: F401,E402
     Mxfp4, mxfp4_logits, quantize_mxfp4, rans_mxfp4_codes_bytes, rans_mxfp4_logits,
     rans_mxfp4_logits_workspace_bytes, rans_mxfp4_product, rans_mxfp4_quantize,
     rans_mxfp4_scales_bytes, rans_mxfp4_values)
+from .beams import (  # noqa: F401,E402
+    MAX_BEAMS, MAX_CONTINUATIONS, MAX_STATES, BeamSearch, beam_select, rans_beam_advance,
+    rans_beam_select, rans_beam_workspace_bytes, rans_reorder_states, reorder_states)
 from .interface import (  # noqa: F401,E402
     RansCoder, TokenCoder, from_byte_strings, to_byte_strings)

@@ -83,13 +83,33 @@ class rans_mxfp4(ctypes.Structure):
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
 
 
+class rans_beams(ctypes.Structure):
+    _fields_ = [("texts", ctypes.c_int64), ("beams", ctypes.c_int32),
+                ("capacity", ctypes.c_int32), ("ends", ctypes.c_void_p),
+                ("n_ends", ctypes.c_int32), ("pad", ctypes.c_int32),
+                ("length_penalty", ctypes.c_float), ("early", ctypes.c_int32),
+                ("scores", ctypes.c_void_p), ("tokens", ctypes.c_void_p),
+                ("parents", ctypes.c_void_p), ("history", ctypes.c_void_p),
+                ("window_end", ctypes.c_void_p), ("lengths", ctypes.c_void_p),
+                ("over", ctypes.c_void_p), ("done_scores", ctypes.c_void_p),
+                ("done_lengths", ctypes.c_void_p), ("done_tokens", ctypes.c_void_p),
+                ("done_counts", ctypes.c_void_p)]
+
+
+class rans_state(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64),
+                ("segment_stride", ctypes.c_int64), ("positions", ctypes.c_int64),
+                ("segments", ctypes.c_int32), ("position_bytes", ctypes.c_int32)]
+
+
 # (name, restype, argtypes) for every exported symbol of include/rans_b200.h
 _P, _I32, _I64, _U64, _F64, _F32 = (ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64,
                                    ctypes.c_uint64, ctypes.c_double, ctypes.c_float)
 _CHP = ctypes.POINTER(rans_chunking)
 _TBP = ctypes.POINTER(rans_tables)
-# rans_logits, rans_adjust and rans_mxfp4 pointers: a byref() or a struct's packed bytes
-_LGP = _ADP = _MXP = ctypes.c_void_p
+# pointers to rans_logits, rans_adjust, rans_mxfp4, rans_beams and rans_state: a byref()
+# or a struct's packed bytes
+_LGP = _ADP = _MXP = _BMP = _STP = ctypes.c_void_p
 SIGNATURES = [
     ("rans_status_string", ctypes.c_char_p, [ctypes.c_int]),
     ("rans_version", ctypes.c_int, []),
@@ -136,6 +156,11 @@ SIGNATURES = [
     ("rans_mxfp4_product", ctypes.c_int, [_MXP, _MXP, _P, _I32, _I64, _P, _P]),
     ("rans_mxfp4_logits_workspace_bytes", _U64, [_I64, _I64]),
     ("rans_mxfp4_logits", ctypes.c_int, [_LGP, _MXP, _P, _I32, _I64, _P, _U64, _P, _P]),
+    ("rans_beam_workspace_bytes", _U64, [_I32, _I64, _I32, _I32]),
+    ("rans_beam_select", ctypes.c_int,
+     [_LGP, _ADP, _P, _I32, _I32, _P, _P, _P, _P, _U64, _P, _P]),
+    ("rans_beam_advance", ctypes.c_int, [_P, _P, _P, _I32, _BMP, _P]),
+    ("rans_reorder_states", ctypes.c_int, [_STP, _I32, _I64, _I32, _P, _P, _P, _P]),
     ("rans_get_status", ctypes.c_int, [_P, _P]),
     ("rans_debug_divide", ctypes.c_int, [_P, _P, _I64, _P, _P, _P]),
     ("rans_debug_wait_timeout", ctypes.c_int, [_P, ctypes.c_uint32, _P]),

@@ -2,6 +2,7 @@
 // chunking geometry, workspace layout and launch order.  Every coding step
 // runs in the kernels of tables.cu, encode.cu and decode.cu; logits.cu,
 // tokens.cu and distill.cu hold those of tokens under a model's logits.
+#include <algorithm>
 #include <cstring>
 #include <mutex>
 #include <utility>
@@ -714,6 +715,59 @@ int check_head(const rans_mxfp4 *head, int64_t rows, int64_t cols, const void *o
 }
 uint64_t up256(uint64_t x) { return (x + 255) & ~255ull; }
 
+// ----------------------------------------------------------- beam search --
+// Arrays of a call; every one that is written may share memory with no other.
+struct Range {
+  const void *p;
+  uint64_t bytes;
+  bool written;
+};
+template <size_t N>
+bool clash(const Range (&r)[N]) {
+  for (size_t i = 0; i < N; ++i)
+    for (size_t j = 0; j < N; ++j)
+      if (i != j && r[i].written && overlap(r[i].p, r[i].bytes, r[j].p, r[j].bytes)) return true;
+  return false;
+}
+
+uint64_t state_row_bytes(const rans_state &s) {
+  return (uint64_t)(s.segments - 1) * (uint64_t)(s.segments > 1 ? s.segment_stride : 0) +
+         (uint64_t)s.positions * (uint64_t)s.position_bytes;
+}
+uint64_t state_bytes(const rans_state &s, int64_t rows) {
+  return (uint64_t)(rows - 1) * (uint64_t)(rows > 1 ? s.row_stride : 0) + state_row_bytes(s);
+}
+bool state_empty(const rans_state &s) {
+  return s.segments == 0 || s.positions == 0 || s.position_bytes == 0;
+}
+
+int check_state(const rans_state &s, int64_t rows) {
+  constexpr int64_t kMost = int64_t(1) << 46;
+  if (s.segments < 0 || s.positions < 0 || s.position_bytes < 0) return RANS_ERR_ARG;
+  if (state_empty(s)) return RANS_OK;
+  if (!s.data || s.positions > kMost / s.position_bytes) return RANS_ERR_ARG;
+  const int64_t piece = s.positions * s.position_bytes;
+  if (s.segments > 1 &&
+      (s.segment_stride < piece || s.segment_stride > kMost / s.segments))
+    return RANS_ERR_ARG;
+  if (rows > 1 && (s.row_stride < (int64_t)state_row_bytes(s) || s.row_stride > kMost / rows))
+    return RANS_ERR_ARG;
+  return RANS_OK;
+}
+
+// Whether two states share bytes: never where their rows interleave with the
+// same stride.
+bool states_clash(const rans_state &a, const rans_state &b, int64_t rows) {
+  if (!overlap(a.data, state_bytes(a, rows), b.data, state_bytes(b, rows))) return false;
+  if (rows == 1 || a.row_stride != b.row_stride) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a.data), y = reinterpret_cast<uintptr_t>(b.data);
+  const uint64_t step = (uint64_t)a.row_stride;
+  const uint64_t off = x < y ? (y - x) % step : (x - y) % step;
+  const uint64_t lower = x < y ? state_row_bytes(a) : state_row_bytes(b);
+  const uint64_t upper = x < y ? state_row_bytes(b) : state_row_bytes(a);
+  return off < lower || off + upper > step;
+}
+
 }  // namespace
 
 RANS_API int rans_adjust_logits(const rans_logits *logits, const rans_adjust *adjust, void *out,
@@ -946,6 +1000,138 @@ RANS_API int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head
   if (st) return st;
   return rb::launch_mxfp4_product(a, *head, out, out_dtype, out_stride,
                                   static_cast<int32_t *>(status), true, as_stream(stream));
+}
+
+RANS_API uint64_t rans_beam_workspace_bytes(int32_t dtype, int64_t rows, int32_t vocab,
+                                             int32_t count) {
+  if (logits_bytes(dtype) == 0 || rows < 0 || vocab < 1 || vocab > RANS_MAX_VOCAB || count < 1 ||
+      count > RANS_MAX_CONTINUATIONS)
+    return 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  return rb::beam_workspace_bytes(dtype, rows, vocab, count, rb::num_sms(dev));
+}
+
+RANS_API int rans_beam_select(const rans_logits *logits, const rans_adjust *adjust,
+                              const float *scores, int32_t beams, int32_t count,
+                              float *scores_out, int32_t *tokens, int32_t *parents,
+                              void *workspace, uint64_t workspace_bytes, void *status,
+                              void *stream) {
+  NvtxRange nvtx_("rans_beam_select");
+  rans_adjust a;
+  int st = check_logits(logits);
+  if (!st) st = check_adjust(adjust, logits->vocab, a);
+  if (!st && status) st = check_status_word(status);
+  if (st) return st;
+  if (beams < 1 || beams > RANS_MAX_BEAMS || logits->rows % beams != 0 || count < 1 ||
+      count > RANS_MAX_CONTINUATIONS)
+    return RANS_ERR_ARG;
+  if (logits->rows == 0) return RANS_OK;
+  if (logits->rows > 0x7fffffff) return RANS_ERR_ARG;
+  if (!scores || !scores_out || !tokens || !parents || !natural(scores, (const float *)scores_out) ||
+      !natural(tokens, parents))
+    return RANS_ERR_ARG;
+  if (!workspace || !aligned_to(workspace, 256)) return RANS_ERR_ARG;
+  const uint64_t out = 4ull * (uint64_t)count * (uint64_t)(logits->rows / beams);
+  const uint64_t need = rans_beam_workspace_bytes(logits->dtype, logits->rows, logits->vocab, count);
+  const Range r[] = {{scores, 4ull * (uint64_t)logits->rows, false},
+                     {scores_out, out, true},
+                     {tokens, out, true},
+                     {parents, out, true},
+                     {workspace, need, true},
+                     {logits->data,
+                      rows_bytes(logits->rows, logits->vocab, logits->row_stride, logits->dtype),
+                      false},
+                     {status, 256, true},
+                     {a.history, 4ull * (uint64_t)a.history_len, false},
+                     {a.bias_ids, 4ull * (uint64_t)a.bias_len, false},
+                     {a.bias_values, 4ull * (uint64_t)a.bias_len, false}};
+  if (clash(r)) return RANS_ERR_ARG;
+  if (need == 0) return RANS_ERR_CUDA;
+  if (workspace_bytes < need) return RANS_ERR_CAPACITY;
+  return rb::launch_beam_select(*logits, a, scores, beams, count, scores_out, tokens, parents,
+                                workspace, static_cast<int32_t *>(status), as_stream(stream));
+}
+
+RANS_API int rans_beam_advance(const float *scores, const int32_t *tokens, const int32_t *parents,
+                               int32_t count, const rans_beams *s, void *stream) {
+  NvtxRange nvtx_("rans_beam_advance");
+  if (!s || s->texts < 0 || s->beams < 1 || s->beams > RANS_MAX_BEAMS || s->capacity < 1 ||
+      count < 1 || count > RANS_MAX_CONTINUATIONS || s->n_ends < 0 || s->n_ends > 64 ||
+      (s->n_ends > 0 && !s->ends) || !finite(s->length_penalty))
+    return RANS_ERR_ARG;
+  if (s->texts == 0) return RANS_OK;
+  if (!scores || !tokens || !parents || !s->scores || !s->tokens || !s->parents || !s->history ||
+      !s->window_end || !s->lengths || !s->over || !s->done_scores || !s->done_lengths ||
+      !s->done_tokens || !s->done_counts)
+    return RANS_ERR_ARG;
+  if (!natural(scores, (const float *)s->scores, (const float *)s->done_scores) ||
+      !natural(s->window_end) ||
+      !natural(tokens, parents, s->ends, (const int32_t *)s->tokens, (const int32_t *)s->parents,
+               (const int32_t *)s->history, (const int32_t *)s->lengths, (const int32_t *)s->over,
+               (const int32_t *)s->done_lengths, (const int32_t *)s->done_tokens,
+               (const int32_t *)s->done_counts))
+    return RANS_ERR_ARG;
+  const uint64_t T = 4ull * (uint64_t)s->texts, K = T * (uint64_t)s->beams;
+  const uint64_t C = K * (uint64_t)s->capacity, in = T * (uint64_t)count;
+  const Range r[] = {{scores, in, false},
+                     {tokens, in, false},
+                     {parents, in, false},
+                     {s->ends, 4ull * (uint64_t)s->n_ends, false},
+                     {s->scores, K, true},
+                     {s->tokens, K, true},
+                     {s->parents, K, true},
+                     {s->history, C, true},
+                     {s->window_end, 2 * K, true},
+                     {s->lengths, T, true},
+                     {s->over, T, true},
+                     {s->done_scores, K, true},
+                     {s->done_lengths, K, true},
+                     {s->done_tokens, C, true},
+                     {s->done_counts, T, true}};
+  if (clash(r)) return RANS_ERR_ARG;
+  return rb::launch_beam_advance(scores, tokens, parents, count, *s, as_stream(stream));
+}
+
+RANS_API int rans_reorder_states(const rans_state *states, int32_t n_states, int64_t texts,
+                                 int32_t beams, const int32_t *parents, const int32_t *lengths,
+                                 void *status, void *stream) {
+  NvtxRange nvtx_("rans_reorder_states");
+  if (n_states < 0 || n_states > RANS_MAX_STATES || (n_states > 0 && !states) || texts < 0 ||
+      texts > 0x7fffffff || beams < 1 || beams > RANS_MAX_BEAMS)
+    return RANS_ERR_ARG;
+  if (status && check_status_word(status)) return RANS_ERR_ARG;
+  if (n_states == 0 || texts == 0) return RANS_OK;
+  if (!parents || !natural(parents, lengths)) return RANS_ERR_ARG;
+  const int64_t rows = texts * beams;
+  int32_t order[RANS_MAX_STATES];
+  int32_t n = 0;
+  for (int32_t i = 0; i < n_states; ++i) {
+    const rans_state &s = states[i];
+    if (check_state(s, rows)) return RANS_ERR_ARG;
+    if (state_empty(s)) continue;
+    const uint64_t bytes = state_bytes(s, rows);
+    if (overlap(s.data, bytes, parents, 4ull * (uint64_t)rows) ||
+        overlap(s.data, bytes, lengths, 4ull * (uint64_t)texts) ||
+        overlap(s.data, bytes, status, 256))
+      return RANS_ERR_ARG;
+    order[n++] = i;
+  }
+  // by address, a state can only meet those that begin before its end
+  std::sort(order, order + n, [&](int32_t i, int32_t j) {
+    return reinterpret_cast<uintptr_t>(states[i].data) < reinterpret_cast<uintptr_t>(states[j].data);
+  });
+  for (int32_t i = 0; i < n; ++i) {
+    const rans_state &a = states[order[i]];
+    const uintptr_t end = reinterpret_cast<uintptr_t>(a.data) + state_bytes(a, rows);
+    for (int32_t j = i + 1; j < n; ++j) {
+      const rans_state &b = states[order[j]];
+      if (reinterpret_cast<uintptr_t>(b.data) >= end) break;
+      if (states_clash(a, b, rows)) return RANS_ERR_ARG;
+    }
+  }
+  return rb::launch_reorder_states(states, n_states, texts, beams, parents, lengths,
+                                   static_cast<int32_t *>(status), as_stream(stream));
 }
 
 RANS_API int rans_get_status(void *workspace, void *stream) {

@@ -1,0 +1,601 @@
+// beam.cu -- rans_beam_select: the best continuations of every text, over its
+// beams and the vocabulary.
+//
+// A continuation's total is score + x - logsumexp(x) with x the row's adjusted
+// logits; the order is that of totals in 64 bits.  Within a row it is the order
+// of x, which is exact, so rows and parts of rows can be thinned out to their
+// best few before any sum is known; only between beams do the sums decide.
+//
+// Two launches.  The first reads the rows once.  A block takes part of a row and
+// keeps, per thread, the running maximum and sum of exponentials, and in
+// shared memory the tokens that may be among its best `count`: at least `count`
+// threads have met a logit as large as the count-th largest of the threads'
+// maxima, so nothing below that need be kept.  The second merges a text's parts.
+//
+// The sums: e^t for t <= 0 by reduction to |r| <= ln 2 / 2 in two parts (Cody and
+// Waite, "Software Manual for the Elementary Functions", 1980) and the power
+// series to r^7 (remainder 6e-9), each at most an ulp off; a thread adds them in
+// float32 with the lost part carried along (Kahan), threads and blocks add up in 64 bits.  The sum's error is
+// then that of its largest terms, 2^-24 or less of their share, where plain
+// float32 sums would lose 1e-6 and swap neighbours.  Equal rows of a call get
+// equal sums: a thread's tokens go by their ids, not by where a row starts in
+// memory, and tokens that penalties and biases touch, which come in a table's
+// order, are added as integers.
+#include "logits_common.cuh"
+#include "rans_common.cuh"
+#include "rans_internal.h"
+
+namespace rb {
+namespace {
+
+constexpr int kBeamThreads = 256;
+constexpr int kBeamWarps = kBeamThreads / 32;
+constexpr int kBeamVecs = 4;      // vectors of 16 bytes a lane has in a tile
+constexpr int kBeamList = 1024;   // tokens kept by a block
+constexpr int kMergeThreads = 256;
+constexpr int kMergeList = 512;
+static_assert(RANS_MAX_CONTINUATIONS <= kBeamThreads, "a threshold needs that many maxima");
+
+// What a block says of its part of a row.
+struct Part {
+  double sum;   // of e^(x - top)
+  float top;
+  int32_t n;    // candidates, -1: a bad logit or parameter
+};
+struct Candidate {
+  float x;
+  int32_t token;
+};
+
+// Floats in the order of their values, as integers; -inf is kNoKey.
+__device__ __forceinline__ uint32_t key_of(float x) {
+  const uint32_t b = __float_as_uint(x);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+constexpr uint32_t kNoKey = 0x007fffffu;
+__device__ __forceinline__ uint64_t key_of(double x) {
+  const uint64_t b = (uint64_t)__double_as_longlong(x);
+  return b >> 63 ? ~b : b | 1ull << 63;
+}
+constexpr uint64_t kNoKey64 = 0x000fffffffffffffull;
+
+__device__ __forceinline__ int block_sum(int x, int *words) {
+  x = __reduce_add_sync(0xffffffffu, x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) words[threadIdx.x >> 5] = x;
+  __syncthreads();
+  int s = 0;
+  for (int i = 0; i < (int)(blockDim.x >> 5); ++i) s += words[i];
+  return s;
+}
+
+// A key that at least `count` of the threads' keys reach, near the largest such;
+// `none` + 1 if fewer than that are above `none`.  `most`: at least the largest.
+template <typename K>
+__device__ __forceinline__ K threshold(K mine, int count, K none, K most) {
+  K lo = none + 1, hi = most;  // count(lo) >= count or lo = none + 1; the answer is in [lo, hi]
+  if (__syncthreads_count(mine >= lo) < count) return lo;
+  while (lo < hi) {
+    const K mid = lo + (hi - lo + 1) / 2;
+    const int n = __syncthreads_count(mine >= mid);
+    if (n >= count) {
+      lo = mid;
+      if (n <= count + count / 2) break;
+    } else {
+      hi = mid - 1;
+    }
+  }
+  return lo;
+}
+
+// The exact cut: value key and last place such that exactly min(count, all) of
+// the items (key > cut, or key == cut at a place <= last) are the best, ties by
+// place.  n_of(k, p): how many items are above key k, or at k up to place p.
+template <typename K, class Count>
+__device__ __forceinline__ void exact_cut(int count, K none, K most, int places, K &cut, int &last,
+                                          Count n_of) {
+  K lo = none, hi = most;  // the largest k with n(key >= k) >= count, if there is one
+  while (lo < hi) {
+    const K mid = lo + (hi - lo + 1) / 2;
+    if (n_of(mid, places) >= count) lo = mid;
+    else hi = mid - 1;
+  }
+  cut = lo;
+  last = places;
+  if (lo == none) {  // fewer than count items: all of them
+    cut = none + 1;
+    return;
+  }
+  int a = 0, b = places;
+  while (a < b) {
+    const int mid = (int)(((int64_t)a + b) >> 1);
+    if (n_of(lo, mid) >= count) b = mid;
+    else a = mid + 1;
+  }
+  last = a;
+}
+
+// e^t for t <= 0.
+__device__ __forceinline__ float exp_of(float t) {
+  t = fmaxf(t, -104.0f);
+  const float k = __fsub_rn(__fmaf_rn(t, 0x1.715476p+0f, 12582912.0f), 12582912.0f);
+  // ln 2 = 0x1.62e4p-1 + 0x1.7f7d1cp-20: the first part's products with k are exact
+  float r = __fmaf_rn(k, -0x1.62e4p-1f, t);
+  r = __fmaf_rn(k, -0x1.7f7d1cp-20f, r);
+  float p = __fmaf_rn(r, 1.0f / 5040.0f, 1.0f / 720.0f);
+  p = __fmaf_rn(p, r, 1.0f / 120.0f);
+  p = __fmaf_rn(p, r, 1.0f / 24.0f);
+  p = __fmaf_rn(p, r, 1.0f / 6.0f);
+  p = __fmaf_rn(p, r, 0.5f);
+  p = __fmaf_rn(p, r, 1.0f);
+  p = __fmaf_rn(p, r, 1.0f);
+  // (below 2^-126 in two steps)
+  const int e = (int)k, half = e >> 1;
+  return __fmul_rn(__fmul_rn(p, __uint_as_float((uint32_t)(127 + half) << 23)),
+                   __uint_as_float((uint32_t)(127 + e - half) << 23));
+}
+
+template <typename T, bool ADJ>
+__global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
+    beam_rows_kernel(rans_logits in, rans_adjust adj, const float *scores, int count, int parts,
+                     int slice, Part *part_out, Candidate *cand_out) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int N = VecOf<T>::N;
+  constexpr int kWarpTile = 32 * N * kBeamVecs;
+  TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
+  uint32_t *ok_bits = reinterpret_cast<uint32_t *>(smem + (ADJ ? sizeof(TouchTable) : 0));
+  __shared__ Candidate list[kBeamList];
+  __shared__ int listed, emitted, words[kBeamWarps];
+  __shared__ double sums[kBeamWarps];
+  __shared__ unsigned long long whole_sums[kBeamWarps];
+  __shared__ RowAdjust a;
+  __shared__ float head_score;
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int64_t r = blockIdx.x / parts;
+  const Row<T> row(in.data, r, in.row_stride, in.vocab);
+  const int lo = row.shift + (int)(blockIdx.x % parts) * slice, hi = min(lo + slice, row.end());
+  Part *part = part_out + blockIdx.x;
+  Candidate *out = cand_out + (int64_t)blockIdx.x * 2 * count;
+  // (the merge may prepare itself meanwhile)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    // one thread reads what decides whether the row is worked on
+    head_score = scores[r];
+    listed = emitted = 0;
+    if (ADJ) a = row_adjust(adj, r, in.vocab);
+  }
+  __syncthreads();
+  const float inv = adj.params ? adj.params[4 * r + 3] : adj.inv_temperature;
+  const bool good = inv > 0.0f && inv < __builtin_huge_valf();
+  if (lo >= hi || head_score == kNegInf || !good) {
+    if (tid == 0) *part = Part{0.0, kNegInf, good ? 0 : -1};
+    return;
+  }
+
+  const bool touch = ADJ && a.touches();
+  int table_at = -1, span = 1 << 30;
+  bool dense = false;
+  auto need_table = [&](int u_lo) {
+    if (!ADJ || table_at == u_lo) return;
+    if (touch) {
+      span = fill_touch(table, a, row, u_lo, hi, dense, ok_bits, tid, kBeamThreads,
+                        [] { __syncthreads(); });
+    } else {
+      span = min(kHashSpan, hi - u_lo);
+      __syncthreads();
+      fill_mask(ok_bits, a.mask, a.mask_words, row, u_lo, span, tid, kBeamThreads);
+      __syncthreads();
+    }
+    table_at = u_lo;
+  };
+  // The vector of the tokens at u0, a whole number of vectors after token 0; where
+  // the row starts off 16 bytes it is joined from the two that hold it.
+  auto raw_at = [&](int u0, int u_hi) {
+    uint4 q = make_uint4(0, 0, 0, 0);
+    if (u0 < u_hi) q = load_joined(row.at0 + row.shift, row.at0 + u0, row.at0 + row.end());
+    return q;
+  };
+  auto ok_at = [&](int u0, int u_hi) -> uint32_t {
+    if (u0 >= u_hi) return 0u;
+    if constexpr (ADJ) return ok_bits[(u0 - table_at) >> 5] >> ((u0 - table_at) & 31);
+    else return (1u << min(row.end() - u0, N)) - 1u;
+  };
+  auto logits_of = [&](const uint4 &q, uint32_t ok, float (&x)[N]) {
+    unpack16(q, x, T());
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = ok >> i & 1 ? __fmul_rn(x[i], inv) : kNegInf;
+  };
+  // walks the part, a table's tokens at a time: body(u_lo, u_hi), then touched_body()
+  // where there are touched ones
+  auto walk = [&](auto body, auto touched_body) {
+    for (int u_lo = lo, u_hi; u_lo < hi; u_lo = u_hi) {
+      need_table(u_lo);
+      u_hi = span < hi - u_lo ? u_lo + span : hi;
+      body(u_lo, u_hi);
+      if (ADJ && touch) touched_body();
+    }
+  };
+  auto touched = [&](auto body) {  // body(u, x)
+    each_touched(table, tid, kBeamThreads, [&](int u, float z) { body(u, __fmul_rn(z, inv)); });
+  };
+
+  float top = kNegInf, s = 0.0f, lost = 0.0f, cut = kNegInf;
+  float touched_top = kNegInf;
+  double touched_sum = 0.0;
+  auto raise = [&](float to) {  // a larger maximum: the sum is relative to it
+    if (to > top) {
+      const float f = exp_of(__fsub_rn(top, to));  // (0 for the first: e^-inf, s is 0)
+      s = __fmul_rn(s, f);
+      lost = __fmul_rn(lost, f);
+      top = to;
+    } else if (to != to) {
+      top = to;
+    }
+  };
+  auto add = [&](float x) {
+    const float e = x > kNegInf ? exp_of(__fsub_rn(x, top)) : 0.0f;
+    const float y = __fsub_rn(e, lost), t = __fadd_rn(s, y);
+    lost = __fsub_rn(__fsub_rn(t, s), y);
+    s = t;
+  };
+  auto keep = [&](int u, float x) {
+    const int at = atomicAdd(&listed, 1);
+    if (at < kBeamList) list[at] = Candidate{x, u - row.shift};
+  };
+  auto most_key = [&](float x) {  // of all threads
+    const uint32_t k = __reduce_max_sync(0xffffffffu, key_of(x));
+    __syncthreads();
+    if (lane == 0) words[wid] = (int)k;
+    __syncthreads();
+    uint32_t m = 0;
+    for (int i = 0; i < kBeamWarps; ++i) m = max(m, (uint32_t)words[i]);
+    return m;
+  };
+  auto value_of = [](uint32_t k) {
+    return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
+  };
+
+  int round = 0;
+  walk([&](int u_lo, int u_hi) {
+    constexpr int kTile = kWarpTile * kBeamWarps;
+    uint4 q[kBeamVecs], next[kBeamVecs];
+    const int u_first = u_lo + wid * kWarpTile + lane * N;
+#pragma unroll
+    for (int k = 0; k < kBeamVecs; ++k) next[k] = raw_at(u_first + 32 * N * k, u_hi);
+    for (int u = u_first, base = u_lo; base < u_hi; u += kTile, base += kTile, ++round) {
+#pragma unroll
+      for (int k = 0; k < kBeamVecs; ++k) q[k] = next[k];
+      if (base + kTile < u_hi) {
+#pragma unroll
+        for (int k = 0; k < kBeamVecs; ++k) next[k] = raw_at(u + kTile + 32 * N * k, u_hi);
+      }
+      uint32_t ok[kBeamVecs];
+      float m = kNegInf;
+#pragma unroll
+      for (int k = 0; k < kBeamVecs; ++k) {
+        ok[k] = ok_at(u + 32 * N * k, u_hi);
+        float x[N];
+        logits_of(q[k], ok[k], x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) m = max_nan(m, x[i]);
+      }
+      raise(m);
+      if (m > kNegInf) {
+#pragma unroll
+        for (int k = 0; k < kBeamVecs; ++k) {
+          float x[N];
+          logits_of(q[k], ok[k], x);
+#pragma unroll
+          for (int i = 0; i < N; ++i) add(x[i]);
+        }
+      }
+      // the first tile says what to look for, and tiles 2, 4, 8, ... raise it
+      if ((round & (round - 1)) == 0)
+        cut = fmaxf(cut, value_of(threshold(key_of(top), count, kNoKey, most_key(top))));
+      if (m >= cut) {
+#pragma unroll
+        for (int k = 0; k < kBeamVecs; ++k) {
+          float x[N];
+          logits_of(q[k], ok[k], x);
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            if (x[i] >= cut && x[i] > kNegInf) keep(u + 32 * N * k + i, x[i]);
+        }
+      }
+    }
+  }, [&] {
+    // their own maximum, and their sum in units of 2^-40 of it
+    float m = kNegInf;
+    touched([&](int u, float x) {
+      m = max_nan(m, x);
+      if (x >= cut && x > kNegInf) keep(u, x);
+    });
+    m = value_of(most_key(m));
+    if (m > kNegInf) {
+      unsigned long long q = 0;
+      touched([&](int, float x) {
+        if (x > kNegInf) q += __float2ull_rn(__fmul_rn(exp_of(__fsub_rn(x, m)), 0x1p+40f));
+      });
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+      if (lane == 0) whole_sums[wid] = q;
+      __syncthreads();
+      q = 0;
+      for (int i = 0; i < kBeamWarps; ++i) q += whole_sums[i];
+      const float both = max_nan(touched_top, m);
+      touched_sum = touched_sum * exp((double)touched_top - (double)both) +
+                    (double)q * 0x1p-40 * exp((double)m - (double)both);
+      touched_top = both;
+    } else if (m != m) {
+      touched_top = m;
+    }
+  });
+
+  // the part's maximum and sum
+  const bool bad = __syncthreads_or(!(top < __builtin_huge_valf()) ||
+                                    !(touched_top < __builtin_huge_valf()));
+  if (bad) {
+    if (tid == 0) *part = Part{0.0, kNegInf, -1};
+    return;
+  }
+  const float all_top = fmaxf(value_of(most_key(top)), touched_top);
+  const uint32_t most = key_of(all_top);
+  cut = fmaxf(cut, value_of(threshold(key_of(top), count, kNoKey, most)));
+  double sum = top > kNegInf ? ((double)s - (double)lost) * exp((double)top - (double)all_top) : 0.0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane == 0) sums[wid] = sum;
+  int n = listed;  // (after the barriers above)
+  const bool whole = n <= kBeamList;
+  int mine = 0;
+  if (whole)
+    for (int i = tid; i < n; i += kBeamThreads) mine += list[i].x >= cut;
+  n = block_sum(mine, words);
+  uint32_t key = key_of(cut);
+  int last = in.vocab;
+  if (!whole || n > 2 * count) {
+    // more than the merge has room for (ties, mostly): exactly the best `count`
+    exact_cut<uint32_t>(count, kNoKey, most, in.vocab, key, last, [&](uint32_t k, int place) {
+      int c = 0;
+      if (whole) {
+        for (int i = tid; i < listed; i += kBeamThreads) {
+          const uint32_t v = key_of(list[i].x);
+          c += v > k || (v == k && list[i].token <= place);
+        }
+      } else {
+        walk([&](int u_lo, int u_hi) {
+          for (int u = u_lo + tid * N; u < u_hi; u += kBeamThreads * N) {
+            float x[N];
+            logits_of(raw_at(u, u_hi), ok_at(u, u_hi), x);
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const uint32_t v = key_of(x[i]);
+              c += v > k || (v == k && u + i - row.shift <= place);
+            }
+          }
+        }, [&] {
+          touched([&](int u, float x) {
+            const uint32_t v = key_of(x);
+            c += v > k || (v == k && u - row.shift <= place);
+          });
+        });
+      }
+      return block_sum(c, words);
+    });
+  }
+  auto emit = [&](float x, int token) {
+    const uint32_t v = key_of(x);
+    if (x > kNegInf && (v > key || (v == key && token <= last)))
+      out[atomicAdd(&emitted, 1)] = Candidate{x, token};
+  };
+  if (whole) {
+    for (int i = tid; i < listed; i += kBeamThreads) emit(list[i].x, list[i].token);
+  } else {
+    walk([&](int u_lo, int u_hi) {
+      for (int u = u_lo + tid * N; u < u_hi; u += kBeamThreads * N) {
+        float x[N];
+        logits_of(raw_at(u, u_hi), ok_at(u, u_hi), x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) emit(x[i], u + i - row.shift);
+      }
+    }, [&] { touched([&](int u, float x) { emit(x, u - row.shift); }); });
+  }
+  __syncthreads();
+  if (tid == 0) {
+    double all = touched_sum > 0.0 ? touched_sum * exp((double)touched_top - (double)all_top) : 0.0;
+    for (int i = 0; i < kBeamWarps; ++i) all += sums[i];
+    *part = Part{all, all_top, emitted};
+  }
+}
+
+// One block per text.
+__global__ void __launch_bounds__(kMergeThreads)
+    beam_merge_kernel(const float *scores, int beams, int count, int vocab, int parts,
+                      const Part *part_in, const Candidate *cand_in, float *out_scores,
+                      int32_t *out_tokens, int32_t *out_parents, int32_t *status) {
+  __shared__ double base[RANS_MAX_BEAMS];  // score - logsumexp
+  __shared__ double total[kMergeList];
+  __shared__ int place[kMergeList];        // beam * vocab + token
+  __shared__ int listed, words[kMergeThreads / 32];
+  __shared__ uint64_t tops[kMergeThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
+  const int64_t t = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (tid == 0) listed = 0;
+  // a warp per beam
+  for (int b = wid; b < beams; b += kMergeThreads / 32) {
+    const int64_t r = t * beams + b;
+    const float score = scores[r];
+    float top = kNegInf;
+    bool bad = !(score < __builtin_huge_valf());
+    for (int p = lane; p < parts; p += 32) {
+      const Part &x = part_in[r * parts + p];
+      bad |= x.n < 0;
+      top = fmaxf(top, x.top);
+    }
+    bad = __any_sync(0xffffffffu, bad) && score != kNegInf;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    double sum = 0.0;
+    for (int p = lane; p < parts; p += 32) {
+      const Part &x = part_in[r * parts + p];
+      if (x.n >= 0 && x.top > kNegInf) sum += x.sum * exp((double)x.top - (double)top);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      const bool some = !bad && top > kNegInf && score > kNegInf;
+      base[b] = some ? (double)score - ((double)top + log(sum)) : -__builtin_huge_val();
+      if (bad && status) report(status, RANS_ERR_RANGE, r);
+    }
+  }
+  __syncthreads();
+  // body(total, place) for all candidates of the text
+  const int slots = 2 * count, items = beams * parts * slots;
+  auto each = [&](auto body) {
+    for (int i = tid; i < items; i += kMergeThreads) {
+      const int p = i / slots, b = p / parts;
+      if (i - p * slots >= part_in[t * beams * parts + p].n) continue;
+      const double c = base[b];
+      if (c == -__builtin_huge_val()) continue;
+      const Candidate x = cand_in[t * beams * parts * slots + i];
+      body((double)x.x + c, b * vocab + x.token);
+    }
+  };
+  uint64_t best = kNoKey64;
+  each([&](double v, int) { best = max(best, key_of(v)); });
+  uint64_t most = best;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  if (lane == 0) tops[wid] = most;
+  __syncthreads();
+  for (int i = 0; i < kMergeThreads / 32; ++i) most = max(most, tops[i]);
+  uint64_t key = threshold(best, count, kNoKey64, most);
+  each([&](double v, int p) {
+    if (key_of(v) < key) return;
+    const int at = atomicAdd(&listed, 1);
+    if (at < kMergeList) {
+      total[at] = v;
+      place[at] = p;
+    }
+  });
+  __syncthreads();
+  if (listed > kMergeList) {
+    int last;
+    exact_cut<uint64_t>(count, kNoKey64, most, 0x7fffffff, key, last, [&](uint64_t k, int q) {
+      int c = 0;
+      each([&](double v, int p) {
+        const uint64_t x = key_of(v);
+        c += x > k || (x == k && p <= q);
+      });
+      return block_sum(c, words);
+    });
+    __syncthreads();
+    if (tid == 0) listed = 0;
+    __syncthreads();
+    each([&](double v, int p) {
+      const uint64_t x = key_of(v);
+      if (x > key || (x == key && p <= last)) {
+        const int at = atomicAdd(&listed, 1);
+        total[at] = v;
+        place[at] = p;
+      }
+    });
+    __syncthreads();
+  }
+  // each one's rank is its place in the result
+  const int n = listed;
+  for (int i = tid; i < n; i += kMergeThreads) {
+    const double v = total[i];
+    const int p = place[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += total[j] > v || (total[j] == v && place[j] < p);
+    if (rank < count) {
+      out_scores[t * count + rank] = (float)v;
+      out_tokens[t * count + rank] = p % vocab;
+      out_parents[t * count + rank] = p / vocab;
+    }
+  }
+  for (int i = n + tid; i < count; i += kMergeThreads) {
+    out_scores[t * count + i] = kNegInf;
+    out_tokens[t * count + i] = -1;
+    out_parents[t * count + i] = -1;
+  }
+}
+
+// Parts of a row: twice as many as long as there are blocks to spare and each
+// keeps a tile.
+struct BeamShape {
+  int parts, slice;
+};
+template <typename T>
+BeamShape beam_shape(int64_t rows, int vocab, int sms) {
+  constexpr int kTile = kBeamThreads * kBeamVecs * VecOf<T>::N;
+  const int tiles = (vocab + kTile - 1) / kTile;
+  int parts = 1;
+  while (rows * parts * 2 <= 4 * sms && parts * 2 <= tiles) parts *= 2;
+  const int per = (tiles + parts - 1) / parts;
+  return {(tiles + per - 1) / per, per * kTile};
+}
+BeamShape beam_shape(int dtype, int64_t rows, int vocab, int sms) {
+  return dtype == RANS_LOGITS_F32 ? beam_shape<float>(rows, vocab, sms)
+                                  : beam_shape<__half>(rows, vocab, sms);
+}
+uint64_t part_bytes(int64_t rows, int parts) {
+  return ((uint64_t)rows * (uint64_t)parts * sizeof(Part) + 255) & ~255ull;
+}
+
+template <typename T>
+int launch_rows(const rans_logits &in, const rans_adjust &adj, const float *scores, int count,
+                const BeamShape &sh, Part *parts, Candidate *cands, cudaStream_t st) {
+  const bool adjusted = adj.history != nullptr || adj.bias_ids != nullptr || adj.mask;
+  auto kern = adjusted ? beam_rows_kernel<T, true> : beam_rows_kernel<T, false>;
+  const uint32_t smem = adjusted ? (uint32_t)sizeof(TouchTable) + kHashSpan / 8 : 0u;
+  if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
+  kern<<<(unsigned)(in.rows * sh.parts), kBeamThreads, smem, st>>>(in, adj, scores, count, sh.parts,
+                                                                   sh.slice, parts, cands);
+  return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
+}
+
+}  // namespace
+
+uint64_t beam_workspace_bytes(int dtype, int64_t rows, int vocab, int count, int sms) {
+  const BeamShape sh = beam_shape(dtype, rows, vocab, sms);
+  return part_bytes(rows, sh.parts) +
+         (uint64_t)rows * (uint64_t)sh.parts * 2 * (uint64_t)count * sizeof(Candidate);
+}
+
+int launch_beam_select(const rans_logits &in, const rans_adjust &adj, const float *scores,
+                       int beams, int count, float *out_scores, int32_t *tokens,
+                       int32_t *parents, void *ws, int32_t *status, cudaStream_t st) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
+  const BeamShape sh = beam_shape(in.dtype, in.rows, in.vocab, num_sms(dev));
+  if (in.rows > 0x7fffffff / sh.parts) return RANS_ERR_ARG;
+  Part *parts = static_cast<Part *>(ws);
+  Candidate *cands =
+      reinterpret_cast<Candidate *>(static_cast<char *>(ws) + part_bytes(in.rows, sh.parts));
+  int e;
+  switch (in.dtype) {
+    case RANS_LOGITS_F32: e = launch_rows<float>(in, adj, scores, count, sh, parts, cands, st); break;
+    case RANS_LOGITS_F16: e = launch_rows<__half>(in, adj, scores, count, sh, parts, cands, st); break;
+    default: e = launch_rows<__nv_bfloat16>(in, adj, scores, count, sh, parts, cands, st);
+  }
+  if (e) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(in.rows / beams));
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, beam_merge_kernel, scores, beams, count, (int)in.vocab, sh.parts,
+                            (const Part *)parts, (const Candidate *)cands, out_scores, tokens,
+                            parents, status) == cudaSuccess
+             ? RANS_OK
+             : RANS_ERR_CUDA;
+}
+
+}  // namespace rb

@@ -48,39 +48,6 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) {
   return __uint_as_float((byte > 252 ? 1u : 254u - byte) << 23);
 }
 
-// N elements from p on, any alignment of their type; those at or past `end`
-// read 0.  Vectors off the 16-byte boundaries are joined from the two aligned
-// ones that hold them.
-template <typename T>
-__device__ __forceinline__ uint4 load_joined(const T *first, const T *p, const T *end) {
-  constexpr int N = VecOf<T>::N;
-  const int past = (int)((reinterpret_cast<uintptr_t>(p) & 15) / sizeof(T));
-  const T *a = p - past;
-  if (past == 0 && p + N <= end) return *reinterpret_cast<const uint4 *>(p);
-  if (past != 0 && a >= first && a + 2 * N <= end) {
-    const uint4 lo = reinterpret_cast<const uint4 *>(a)[0], hi = reinterpret_cast<const uint4 *>(a)[1];
-    uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-    const int bytes = past * (int)sizeof(T), words = bytes >> 2;
-    if (words & 1) {
-#pragma unroll
-      for (int i = 0; i < 7; ++i) w[i] = w[i + 1];
-    }
-    if (words & 2) {
-#pragma unroll
-      for (int i = 0; i < 6; ++i) w[i] = w[i + 2 < 8 ? i + 2 : 7];
-    }
-    if (bytes & 2) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-    }
-    return make_uint4(w[0], w[1], w[2], w[3]);
-  }
-  float z[N];
-#pragma unroll
-  for (int i = 0; i < N; ++i) z[i] = p + i < end ? logit_float(p[i]) : 0.0f;
-  return pack16(z, T());
-}
-
 // A warp takes kQuantVecs runs of 32 vectors, one after another along a row.
 template <typename T>
 __global__ void __launch_bounds__(32 * kQuantWarps)

@@ -104,6 +104,17 @@ int launch_mxfp4_values(const rans_mxfp4 &q, void *out, int dtype, int64_t strid
 int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, int dtype,
                          int64_t stride, int32_t *status, bool follows, cudaStream_t st);
 
+// The best continuations of texts; a search's bookkeeping; states in place.
+uint64_t beam_workspace_bytes(int dtype, int64_t rows, int vocab, int count, int sms);
+int launch_beam_select(const rans_logits &in, const rans_adjust &adj, const float *scores,
+                       int beams, int count, float *out_scores, int32_t *tokens,
+                       int32_t *parents, void *ws, int32_t *status, cudaStream_t st);
+int launch_beam_advance(const float *scores, const int32_t *tokens, const int32_t *parents,
+                        int count, const rans_beams &s, cudaStream_t st);
+int launch_reorder_states(const rans_state *states, int32_t n, int64_t texts, int beams,
+                          const int32_t *parents, const int32_t *lengths, int32_t *status,
+                          cudaStream_t st);
+
 // A tensor map (CUtensorMap, 128 bytes, 64-byte aligned) for a 3-D int32
 // tensor of width x height x depth elements (row-major, width fastest) and a
 // box of box_w x box_h x 1; base 16-byte aligned, width * 4 a multiple of 16.

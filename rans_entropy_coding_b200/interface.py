@@ -10,6 +10,7 @@ Argument marshalling only: every coding step runs in librans_b200's kernels.
 import torch
 
 from . import _lib as L
+from . import mxfp4 as M
 from . import tokens as T
 
 _SYM = {torch.int32, torch.int16, torch.uint8}
@@ -118,17 +119,30 @@ class TokenCoder:
     that follow from the tokens so far, then ``finish``.  Both sides must see
     the same logits, bit for bit, and the same adjustments; a row's interval
     does not depend on the batch it comes in.
+
+    head: a model's output head (Mxfp4 [vocab, cols]).  With one, ``add`` and
+    ``step`` take hidden rows [rows, cols] (or Mxfp4) in place of logits and compute
+    these, in `logits_dtype`, so that they too are the same in every batch: both
+    sides then need the same hidden rows, and the same logits_dtype.
     """
 
-    def __init__(self, device="cuda"):
+    def __init__(self, device="cuda", head=None, logits_dtype=torch.float32):
         self.device = torch.device(device)
+        self.head, self.logits_dtype = head, logits_dtype
         # errors of the texts added; of the streams being decoded
         self.status, self.decoding = T.new_status(self.device), None
         self._parts = []
         self._in = None
 
+    def _logits(self, rows, status):
+        if self.head is None:
+            return rows
+        return M.mxfp4_logits(rows, self.head, dtype=self.logits_dtype, status=status)
+
     def add(self, logits, tokens, adjust=None):
-        """The next positions: rows of logits and the token that each is to code."""
+        """The next positions: rows of logits (hidden rows, with a head) and the
+        token that each is to code."""
+        logits = self._logits(logits, self.status)
         tokens = _token_ids(tokens, self.device)
         # a skipped row (token -1) stays at 0, which the streams refuse
         blank = torch.zeros(2, tokens.numel(), dtype=torch.int32, device=self.device)
@@ -165,10 +179,12 @@ class TokenCoder:
         return self
 
     def step(self, logits, adjust=None, stream_ids=None):
-        """Next tokens (int32 [rows]); row r belongs to stream stream_ids[r]
+        """Next tokens (int32 [rows]) under rows of logits (hidden rows, with a head);
+        row r belongs to stream stream_ids[r]
         (default r; -1 skips the row)."""
         if self._in is None:
             raise RuntimeError("begin with the streams first")
+        logits = self._logits(logits, self.decoding)
         tokens, _ = T.decode_tokens(logits, *self._in, self.states, adjust, stream_ids,
                                     out_states=self.states, status=self.decoding)
         return tokens

@@ -193,3 +193,26 @@ def test_numbers_that_are_none_stay_in_their_rows():
     bad[7] = bad[9] = True
     bad[:, 200] = True
     assert torch.equal(out.isnan(), bad)
+
+
+def test_texts_coded_under_a_head():
+    """Whole texts in, one row per stream and step out, hidden rows alone
+    shared; and the intervals are those of the head's logits."""
+    v, k, lengths = 5003, 416, [37, 0, 5, 64]
+    w, n = head_of(v, k), sum([37, 0, 5, 64])
+    hidden = rows(n, k, BF16, seed=5)
+    tokens = torch.randint(0, v, (n,), device="cuda")
+    for dtype in (F32, BF16):
+        coder = rb.TokenCoder(head=w, logits_dtype=dtype)
+        coder.add(hidden[:50], tokens[:50]).add(rb.quantize_mxfp4(hidden[50:]), tokens[50:])
+        data, offsets = coder.streams(lengths)
+        plain = rb.TokenCoder().add(rb.mxfp4_logits(hidden, w, dtype=dtype), tokens)
+        assert torch.equal(plain.streams(lengths)[0], data)
+        coder.begin(data, offsets)
+        first = [0, 37, 37, 42]
+        for t in range(max(lengths)):
+            ids = [i for i, m in enumerate(lengths) if t < m]
+            got = coder.step(torch.stack([hidden[first[i] + t] for i in ids]),
+                             stream_ids=torch.tensor(ids, dtype=torch.int32, device="cuda"))
+            assert got.tolist() == [int(tokens[first[i] + t]) for i in ids]
+        coder.finish()
