@@ -100,6 +100,16 @@ __device__ __forceinline__ void load_bulk(uint32_t dst, const void *src, uint32_
       "l"(src), "r"(bytes), "r"(bar)
       : "memory");
 }
+// One lane of a converged warp.  What only one thread issues stands behind this, in
+// code that the whole warp runs: behind `lane == 0`, where the compiler cannot tell
+// that its operands are the warp's, every copy and product cost over 100 cycles.
+__device__ __forceinline__ bool elected() {
+  uint32_t yes;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(yes));
+  return yes != 0;
+}
 // Eight columns of a warp's 32 accumulator lanes.
 __device__ __forceinline__ void load_columns(float *v, uint32_t at) {
   uint32_t *u = reinterpret_cast<uint32_t *>(v);
@@ -120,7 +130,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, free_bar;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;  // a wait gave up
-  const int tid = threadIdx.x, wid = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(kFull, tid >> 5, 0);
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t token_bytes = (uint32_t)sh.box * kStageBytes;
   const int row_tiles = (sh.box + kMxTileRows - 1) / kMxTileRows;
@@ -157,108 +167,140 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
-  // (what a thread may wait: until another gave up, or for its own share)
+  // A warp's wait: until another gave up, or for its own share.
   auto wait = [&](uint64_t *bar, uint32_t parity) {
     const uint32_t b = smem_addr(bar);
-    for (uint32_t i = 0; i < kTries && !dead; ++i)
-      if (mbar_try_wait(b, parity)) return true;
-    if (!dead) {
+    for (uint32_t i = 0; i < kTries; ++i) {
+      if (__all_sync(kFull, mbar_try_wait(b, parity))) return true;
+      if (__any_sync(kFull, dead)) return false;
+    }
+    if (lane == 0) {
       dead = 1;
       if (status) report(status, RANS_ERR_TIMEOUT, -1);
     }
+    __syncwarp();
     return false;
   };
 
-  if (wid == 0 && lane == 0) {
+  if (wid == 0) {
     // ------------------------------------------------------- the copies --
-    const int total = ((sh.tiles - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x) * per_tile;
-    auto place = [&](int it, int &stage, int &mt, int &nt, int &kb, uint32_t &groups) {
-      stage = it % sh.stages;
-      const int tile = (int)blockIdx.x + it / per_tile * (int)gridDim.x;
-      kb = it % per_tile;
-      mt = tile / sh.token_tiles;
-      nt = tile % sh.token_tiles;
-      groups = (uint32_t)min(2, sh.groups - 2 * kb);
+    // (a stage's place is counted up: a division took longer than the stage's
+    // products)
+    struct Place {
+      int tile, kb, stage, mt, nt;
+      uint32_t lap;
     };
-    auto load_head = [&](int it) {
-      int stage, mt, nt, kb;
-      uint32_t groups;
-      place(it, stage, mt, nt, kb, groups);
-      const uint32_t bar = smem_addr(&full_bar[stage]), s = smem + stage * stage_bytes;
-      const int tiles = min(row_tiles, (sh.tokens - nt * kMostTokens + kMxTileRows - 1) / kMxTileRows);
+    auto start = [&] {
+      const int tile = (int)blockIdx.x;
+      return Place{tile, 0, 0, tile / sh.token_tiles, tile % sh.token_tiles, 0};
+    };
+    auto step = [&](Place &p) {
+      if (++p.stage == sh.stages) {
+        p.stage = 0;
+        ++p.lap;
+      }
+      if (++p.kb == per_tile) {
+        p.kb = 0;
+        p.tile += (int)gridDim.x;
+        p.mt = p.tile / sh.token_tiles;
+        p.nt = p.tile - p.mt * sh.token_tiles;
+      }
+    };
+    auto load_head = [&](const Place &p) {
+      const uint32_t bar = smem_addr(&full_bar[p.stage]), s = smem + p.stage * stage_bytes;
+      const uint32_t groups = (uint32_t)min(2, sh.groups - 2 * p.kb);
+      const int tiles =
+          min(row_tiles, (sh.tokens - p.nt * kMostTokens + kMxTileRows - 1) / kMxTileRows);
+      if (!elected()) return;
       tma::arrive_expect(bar, at_head_scales + groups * kMxTileBytes * (uint32_t)(1 + tiles));
-      load_2d(s, &head_map, kb * kStageBytes, mt * kHeadRows, bar);
-      load_bulk(s + at_head_scales, head_scales + ((int64_t)mt * sh.groups + 2 * kb) * kMxTileBytes,
+      load_2d(s, &head_map, p.kb * kStageBytes, p.mt * kHeadRows, bar);
+      load_bulk(s + at_head_scales,
+                head_scales + ((int64_t)p.mt * sh.groups + 2 * p.kb) * kMxTileBytes,
                 groups * kMxTileBytes, bar);
     };
-    auto load_tokens = [&](int it) {
-      int stage, mt, nt, kb;
-      uint32_t groups;
-      place(it, stage, mt, nt, kb, groups);
-      const uint32_t bar = smem_addr(&full_bar[stage]), s = smem + stage * stage_bytes;
-      load_2d(s + at_tokens, &token_map, kb * kStageBytes, nt * kMostTokens, bar);
+    auto load_tokens = [&](const Place &p) {
+      const uint32_t bar = smem_addr(&full_bar[p.stage]), s = smem + p.stage * stage_bytes;
+      const uint32_t groups = (uint32_t)min(2, sh.groups - 2 * p.kb);
+      if (!elected()) return;
+      load_2d(s + at_tokens, &token_map, p.kb * kStageBytes, p.nt * kMostTokens, bar);
       for (int h = 0; h < row_tiles; ++h) {
-        const int64_t tile = nt * (kMostTokens / kMxTileRows) + h;
+        const int64_t tile = p.nt * (kMostTokens / kMxTileRows) + h;
         if (tile * kMxTileRows < sh.tokens)
           load_bulk(s + at_token_scales + h * 2 * kMxTileBytes,
-                    token_scales + (tile * sh.groups + 2 * kb) * kMxTileBytes,
+                    token_scales + (tile * sh.groups + 2 * p.kb) * kMxTileBytes,
                     groups * kMxTileBytes, bar);
       }
     };
     // the head's first stages do not wait for the tokens' quantisation
-    const int ahead = min(total, sh.stages);
-    for (int it = 0; it < ahead; ++it) load_head(it);
+    Place p = start(), q = p;
+    int issued = 0;
+    for (; issued < sh.stages && p.tile < sh.tiles; ++issued, step(p)) {
+      load_head(p);
+      __syncwarp();
+    }
     if (sh.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int it = 0; it < ahead; ++it) load_tokens(it);
-    int it = ahead;
-    for (; it < total; ++it) {
-      if (!wait(&empty_bar[it % sh.stages], (uint32_t)(it / sh.stages - 1) & 1)) break;
-      load_head(it);
-      load_tokens(it);
+    for (int i = 0; i < issued; ++i, step(q)) {
+      load_tokens(q);
+      __syncwarp();
+    }
+    for (; p.tile < sh.tiles; step(p)) {
+      if (!wait(&empty_bar[p.stage], (p.lap - 1) & 1)) break;
+      load_head(p);
+      load_tokens(p);
+      __syncwarp();
     }
     if (dead) {
       // copies in flight write to this block's memory: they end first
-      for (int i = max(0, it - sh.stages); i < it; ++i)
-        tma::wait_bounded(smem_addr(&full_bar[i % sh.stages]), (uint32_t)(i / sh.stages) & 1, kTries);
+      for (int i = 0; i < issued; ++i)
+        tma::wait_bounded(smem_addr(&full_bar[i]), (i < p.stage ? p.lap : p.lap - 1) & 1, 1u << 21);
     }
-  } else if (wid == 1 && lane == 0) {
+  } else if (wid == 1) {
     // ----------------------------------------------------- the products --
-    int it = 0, n_tile = 0;
-    for (int tile = (int)blockIdx.x; tile < sh.tiles && !dead; tile += (int)gridDim.x, ++n_tile) {
+    int stage = 0, n_tile = 0;
+    uint32_t lap = 0, odd = 0;
+    bool ok = true;
+    for (int tile = (int)blockIdx.x; tile < sh.tiles; tile += (int)gridDim.x, ++n_tile) {
       const int left = sh.tokens - tile % sh.token_tiles * kMostTokens;
       const int width = min(sh.box, (left + 15) & ~15);
       const uint32_t idesc0 = instruction(width, 0), idesc2 = instruction(width, 2);
-      if (n_tile > 0 && !wait(&free_bar, (uint32_t)(n_tile - 1) & 1)) break;
+      ok = n_tile == 0 || wait(&free_bar, (uint32_t)(n_tile - 1) & 1);
+      if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-      bool ok = true;
-      for (int kb = 0; kb < per_tile; ++kb, ++it) {
-        const int stage = it % sh.stages;
-        ok = wait(&full_bar[stage], (uint32_t)(it / sh.stages) & 1);
+      for (int kb = 0; kb < per_tile; ++kb) {
+        ok = wait(&full_bar[stage], lap & 1);
         if (!ok) break;
         asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
         const uint32_t s = smem + stage * stage_bytes;
-        const uint32_t sf = tmem + kScaleCol + (it & 1) * kScaleCols;
+        const uint32_t sf = tmem + kScaleCol + odd * kScaleCols;
         const int groups = min(2, sh.groups - 2 * kb), steps = min(4, sh.steps - 4 * kb);
-        for (int g = 0; g < groups; ++g) {
-          copy_scales(sf + 4 * g, plain_desc(s + at_head_scales + g * kMxTileBytes));
-          for (int h = 0; h * kMxTileRows < width; ++h)
-            copy_scales(sf + 8 + 8 * g + 4 * h,
-                        plain_desc(s + at_token_scales + h * 2 * kMxTileBytes + g * kMxTileBytes));
+        if (elected()) {
+          for (int g = 0; g < groups; ++g) {
+            copy_scales(sf + 4 * g, plain_desc(s + at_head_scales + g * kMxTileBytes));
+            for (int h = 0; h * kMxTileRows < width; ++h)
+              copy_scales(sf + 8 + 8 * g + 4 * h,
+                          plain_desc(s + at_token_scales + h * 2 * kMxTileBytes + g * kMxTileBytes));
+          }
+          const uint64_t a = swizzled_desc(s), b = swizzled_desc(s + at_tokens);
+          for (int j = 0; j < steps; ++j)
+            // 64 columns are 32 bytes, 2 in units of the descriptor
+            multiply(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0, sf + 4 * (j >> 1),
+                     sf + 8 + 8 * (j >> 1), kb > 0 || j > 0);
+          commit(smem_addr(&empty_bar[stage]));
+          if (kb == per_tile - 1) commit(smem_addr(&done_bar));
         }
-        const uint64_t a = swizzled_desc(s), b = swizzled_desc(s + at_tokens);
-        for (int j = 0; j < steps; ++j)
-          // 64 columns are 32 bytes, 2 in units of the descriptor
-          multiply(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0, sf + 4 * (j >> 1),
-                   sf + 8 + 8 * (j >> 1), kb > 0 || j > 0);
-        commit(smem_addr(&empty_bar[stage]));
+        __syncwarp();
+        odd ^= 1;
+        if (++stage == sh.stages) {
+          stage = 0;
+          ++lap;
+        }
       }
       if (!ok) break;
-      commit(smem_addr(&done_bar));
     }
-    if (dead) {
+    if (!ok) {
       // products in flight: a last commit follows them
-      commit(smem_addr(&done_bar));
-      tma::wait_bounded(smem_addr(&done_bar), (uint32_t)n_tile & 1, kTries);
+      if (elected()) commit(smem_addr(&done_bar));
+      tma::wait_bounded(smem_addr(&done_bar), (uint32_t)n_tile & 1, 1u << 21);
     }
   } else if (wid >= 4) {
     // --------------------------------------------------- the accumulators --
@@ -269,7 +311,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       const int left = sh.tokens - n0, width = min(sh.box, (left + 15) & ~15);
       const int c0 = half * (width / 2);
       const int count = min(width / 2, left - c0);  // columns of this warp that are tokens
-      if (!__all_sync(kFull, wait(&done_bar, (uint32_t)n_tile & 1))) break;
+      if (!wait(&done_bar, (uint32_t)n_tile & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float v[HALF];
 #pragma unroll
