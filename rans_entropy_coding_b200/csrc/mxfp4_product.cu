@@ -50,31 +50,32 @@ struct ProductShape {
   int32_t wait;               // the tokens come from the kernel before
 };
 
-__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr) {
-  // 8 rows of 128 bytes are 1024 bytes; version 1; 128-byte swizzle
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024 >> 4) << 32 |
-         (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-__device__ __forceinline__ uint64_t plain_desc(uint32_t addr) {
-  // 8 rows of 16 bytes are 128 bytes; no swizzle
-  return (uint64_t)((addr & 0x3ffff) >> 4) | (uint64_t)(128 >> 4) << 32 | (uint64_t)1 << 46;
-}
+// Descriptors of shared memory: the upper half is the layout's, the lower one the
+// address in units of 16 bytes.
+constexpr uint32_t kSwizzledDesc = 1024 >> 4 | 1u << 14 | 2u << 29;  // 8 rows of 128 bytes, swizzled
+constexpr uint32_t kPlainDesc = 128 >> 4 | 1u << 14;                 // 8 rows of 16 bytes
+__device__ __forceinline__ uint32_t desc_of(uint32_t addr) { return (addr & 0x3ffff) >> 4; }
 // 4-bit floats with scales of an exponent's byte, rows along k on both sides.
 __device__ __forceinline__ uint32_t instruction(int tokens, int scale_byte) {
   return (uint32_t)scale_byte << 4 | 1u << 7 | 1u << 10 | (uint32_t)(tokens >> 3) << 17 |
          1u << 23 | (uint32_t)(kHeadRows >> 4) << 24 | (uint32_t)scale_byte << 29;
 }
-__device__ __forceinline__ void multiply(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+__device__ __forceinline__ void multiply(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                          uint32_t sfa, uint32_t sfb, bool add) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], "
-      "[%5], p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add)
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+      "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], "
+      "p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add), "n"(kSwizzledDesc)
       : "memory");
 }
-__device__ __forceinline__ void copy_scales(uint32_t to, uint64_t desc) {
-  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(to), "l"(desc) : "memory");
+__device__ __forceinline__ void copy_scales(uint32_t to, uint32_t from) {
+  asm volatile(
+      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
+      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(to),
+      "r"(from), "n"(kPlainDesc)
+      : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   } else if (wid == 1) {
     if (lane == 0) {
       for (int i = 0; i < sh.stages; ++i) {
-        tma::mbar_init(smem_addr(&full_bar[i]), 1);
+        tma::mbar_init(smem_addr(&full_bar[i]), 2);  // the head's side, the tokens'
         tma::mbar_init(smem_addr(&empty_bar[i]), 1);
       }
       tma::mbar_init(smem_addr(&done_bar), 1);
@@ -156,7 +157,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       tma::fence_mbar_init();
       tma::fence_proxy_async();
     }
-  } else if (wid == 2) {
+  } else if (wid == 3) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
                      smem_addr(&tmem_base)),
                  "n"(kTmemCols)
@@ -182,77 +183,57 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     return false;
   };
 
-  if (wid == 0) {
+  if (wid == 0 || wid == 2) {
     // ------------------------------------------------------- the copies --
-    // (a stage's place is counted up: a division took longer than the stage's
-    // products)
-    struct Place {
-      int tile, kb, stage, mt, nt;
-      uint32_t lap;
-    };
-    auto start = [&] {
-      const int tile = (int)blockIdx.x;
-      return Place{tile, 0, 0, tile / sh.token_tiles, tile % sh.token_tiles, 0};
-    };
-    auto step = [&](Place &p) {
-      if (++p.stage == sh.stages) {
-        p.stage = 0;
-        ++p.lap;
+    // one warp for the head's, one for the tokens'.  (A stage's place is counted up: a
+    // division took longer than the stage's products.)
+    if (wid == 2 && sh.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
+    int tile = (int)blockIdx.x, kb = 0, stage = 0;
+    uint32_t lap = 0;
+    bool ok = true;
+    int mt = tile / sh.token_tiles, nt = tile - mt * sh.token_tiles;
+    while (tile < sh.tiles) {
+      if (lap > 0) {
+        ok = wait(&empty_bar[stage], (lap - 1) & 1);
+        if (!ok) break;
       }
-      if (++p.kb == per_tile) {
-        p.kb = 0;
-        p.tile += (int)gridDim.x;
-        p.mt = p.tile / sh.token_tiles;
-        p.nt = p.tile - p.mt * sh.token_tiles;
+      const uint32_t bar = smem_addr(&full_bar[stage]), s = smem + stage * stage_bytes;
+      const uint32_t bytes = (uint32_t)min(2, sh.groups - 2 * kb) * kMxTileBytes;
+      if (elected()) {
+        if (wid == 0) {
+          tma::arrive_expect(bar, at_tokens + bytes);
+          load_2d(s, &head_map, kb * kStageBytes, mt * kHeadRows, bar);
+          load_bulk(s + at_head_scales,
+                    head_scales + ((int64_t)mt * sh.groups + 2 * kb) * kMxTileBytes, bytes, bar);
+        } else {
+          const int first = nt * (kMostTokens / kMxTileRows);
+          const bool two = row_tiles > 1 && (first + 1) * kMxTileRows < sh.tokens;
+          tma::arrive_expect(bar, token_bytes + (two ? 2 * bytes : bytes));
+          load_2d(s + at_tokens, &token_map, kb * kStageBytes, nt * kMostTokens, bar);
+          const uint8_t *scales = token_scales + ((int64_t)first * sh.groups + 2 * kb) * kMxTileBytes;
+          load_bulk(s + at_token_scales, scales, bytes, bar);
+          if (two)
+            load_bulk(s + at_token_scales + 2 * kMxTileBytes,
+                      scales + (int64_t)sh.groups * kMxTileBytes, bytes, bar);
+        }
       }
-    };
-    auto load_head = [&](const Place &p) {
-      const uint32_t bar = smem_addr(&full_bar[p.stage]), s = smem + p.stage * stage_bytes;
-      const uint32_t groups = (uint32_t)min(2, sh.groups - 2 * p.kb);
-      const int tiles =
-          min(row_tiles, (sh.tokens - p.nt * kMostTokens + kMxTileRows - 1) / kMxTileRows);
-      if (!elected()) return;
-      tma::arrive_expect(bar, at_head_scales + groups * kMxTileBytes * (uint32_t)(1 + tiles));
-      load_2d(s, &head_map, p.kb * kStageBytes, p.mt * kHeadRows, bar);
-      load_bulk(s + at_head_scales,
-                head_scales + ((int64_t)p.mt * sh.groups + 2 * p.kb) * kMxTileBytes,
-                groups * kMxTileBytes, bar);
-    };
-    auto load_tokens = [&](const Place &p) {
-      const uint32_t bar = smem_addr(&full_bar[p.stage]), s = smem + p.stage * stage_bytes;
-      const uint32_t groups = (uint32_t)min(2, sh.groups - 2 * p.kb);
-      if (!elected()) return;
-      load_2d(s + at_tokens, &token_map, p.kb * kStageBytes, p.nt * kMostTokens, bar);
-      for (int h = 0; h < row_tiles; ++h) {
-        const int64_t tile = p.nt * (kMostTokens / kMxTileRows) + h;
-        if (tile * kMxTileRows < sh.tokens)
-          load_bulk(s + at_token_scales + h * 2 * kMxTileBytes,
-                    token_scales + (tile * sh.groups + 2 * p.kb) * kMxTileBytes,
-                    groups * kMxTileBytes, bar);
+      __syncwarp();
+      if (++stage == sh.stages) {
+        stage = 0;
+        ++lap;
       }
-    };
-    // the head's first stages do not wait for the tokens' quantisation
-    Place p = start(), q = p;
-    int issued = 0;
-    for (; issued < sh.stages && p.tile < sh.tiles; ++issued, step(p)) {
-      load_head(p);
-      __syncwarp();
+      if (++kb == per_tile) {
+        kb = 0;
+        tile += (int)gridDim.x;
+        mt = tile / sh.token_tiles;
+        nt = tile - mt * sh.token_tiles;
+      }
     }
-    if (sh.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
-    for (int i = 0; i < issued; ++i, step(q)) {
-      load_tokens(q);
-      __syncwarp();
-    }
-    for (; p.tile < sh.tiles; step(p)) {
-      if (!wait(&empty_bar[p.stage], (p.lap - 1) & 1)) break;
-      load_head(p);
-      load_tokens(p);
-      __syncwarp();
-    }
-    if (dead) {
-      // copies in flight write to this block's memory: they end first
-      for (int i = 0; i < issued; ++i)
-        tma::wait_bounded(smem_addr(&full_bar[i]), (i < p.stage ? p.lap : p.lap - 1) & 1, 1u << 21);
+    if (!ok) {
+      // copies in flight write to this block's memory: they end first (as far as both
+      // warps have issued theirs)
+      for (int i = 0; i < sh.stages; ++i)
+        tma::wait_bounded(smem_addr(&full_bar[i]), (i < stage ? lap : lap - 1) & 1, 1u << 18);
     }
   } else if (wid == 1) {
     // ----------------------------------------------------- the products --
@@ -274,17 +255,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         const uint32_t sf = tmem + kScaleCol + odd * kScaleCols;
         const int groups = min(2, sh.groups - 2 * kb), steps = min(4, sh.steps - 4 * kb);
         if (elected()) {
-          for (int g = 0; g < groups; ++g) {
-            copy_scales(sf + 4 * g, plain_desc(s + at_head_scales + g * kMxTileBytes));
-            for (int h = 0; h * kMxTileRows < width; ++h)
-              copy_scales(sf + 8 + 8 * g + 4 * h,
-                          plain_desc(s + at_token_scales + h * 2 * kMxTileBytes + g * kMxTileBytes));
-          }
-          const uint64_t a = swizzled_desc(s), b = swizzled_desc(s + at_tokens);
-          for (int j = 0; j < steps; ++j)
-            // 64 columns are 32 bytes, 2 in units of the descriptor
-            multiply(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0, sf + 4 * (j >> 1),
-                     sf + 8 + 8 * (j >> 1), kb > 0 || j > 0);
+          const uint32_t a = desc_of(s), b = desc_of(s + at_tokens);
+          const uint32_t fa = desc_of(s + at_head_scales), fb = desc_of(s + at_token_scales);
+          // a whole stage as constants, the last one of a row by its sizes; 64 columns
+          // are 32 bytes, 2 in units of a descriptor, a tile of scales 32
+          auto work = [&](int groups, int steps) {
+#pragma unroll
+            for (int g = 0; g < 2; ++g)
+              if (g < groups) {
+                copy_scales(sf + 4 * g, fa + 32 * g);
+                copy_scales(sf + 8 + 8 * g, fb + 32 * g);
+                if (width > kMxTileRows) copy_scales(sf + 12 + 8 * g, fb + 64 + 32 * g);
+              }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (j < steps)
+                multiply(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0, sf + 4 * (j >> 1),
+                         sf + 8 + 8 * (j >> 1), j > 0 || kb > 0);
+          };
+          if (steps == 4) work(2, 4);
+          else work(groups, steps);
           commit(smem_addr(&empty_bar[stage]));
           if (kb == per_tile - 1) commit(smem_addr(&done_bar));
         }
@@ -336,7 +326,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
-  if (wid == 2) {
+  if (wid == 3) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "n"(kTmemCols));
