@@ -21,6 +21,8 @@
 // equal sums: a thread's tokens go by their ids, not by where a row starts in
 // memory, and tokens that penalties and biases touch, which come in a table's
 // order, are added as integers.
+#include <type_traits>
+
 #include "logits_common.cuh"
 #include "rans_common.cuh"
 #include "rans_internal.h"
@@ -32,6 +34,7 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamVecs = 4;      // vectors of 16 bytes a lane has in a tile
 constexpr int kBeamList = 1024;   // tokens kept by a block
+constexpr int kNearLanes = 4;     // most lanes of a warp whose vectors near the top are added singly
 constexpr int kMergeThreads = 256;
 constexpr int kMergeList = 512;
 static_assert(RANS_MAX_CONTINUATIONS <= kBeamThreads, "a threshold needs that many maxima");
@@ -47,17 +50,17 @@ struct Candidate {
   int32_t token;
 };
 
-// Floats in the order of their values, as integers; -inf is kNoKey.
+// Floats in the order of their values, as integers.
 __device__ __forceinline__ uint32_t key_of(float x) {
   const uint32_t b = __float_as_uint(x);
   return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
-constexpr uint32_t kNoKey = 0x007fffffu;
+constexpr float kLowest = -3.402823466e38f;
 __device__ __forceinline__ uint64_t key_of(double x) {
   const uint64_t b = (uint64_t)__double_as_longlong(x);
   return b >> 63 ? ~b : b | 1ull << 63;
 }
-constexpr uint64_t kNoKey64 = 0x000fffffffffffffull;
+constexpr double kLowest64 = -1.7976931348623157e308;
 
 __device__ __forceinline__ int block_sum(int x, int *words) {
   x = __reduce_add_sync(0xffffffffu, x);
@@ -69,56 +72,64 @@ __device__ __forceinline__ int block_sum(int x, int *words) {
   return s;
 }
 
-// A key that at least `count` of the threads' keys reach, near the largest such;
-// `none` + 1 if fewer than that are above `none`.  `most`: at least the largest.
-template <typename K>
-__device__ __forceinline__ K threshold(K mine, int count, K none, K most) {
-  K lo = none + 1, hi = most;  // count(lo) >= count or lo = none + 1; the answer is in [lo, hi]
-  if (__syncthreads_count(mine >= lo) < count) return lo;
-  while (lo < hi) {
-    const K mid = lo + (hi - lo + 1) / 2;
-    const int n = __syncthreads_count(mine >= mid);
-    if (n >= count) {
+// A value that at least `count` of the threads' values reach, near the largest
+// such, down from the largest, `most`, in steps twice as long each; the type's
+// lowest if fewer are above -inf.
+template <typename F>
+__device__ __forceinline__ F threshold(F mine, int count, F most, F lowest) {
+  F lo = most, hi = most, d = 1;
+  int n = __syncthreads_count(mine >= most);
+  if (n >= count) return most > lowest ? most : lowest;
+  for (;;) {
+    lo = most - d;
+    if (!(lo > lowest)) return lowest;
+    n = __syncthreads_count(mine >= lo);
+    if (n >= count) break;
+    hi = lo;
+    d *= 2;
+  }
+  for (int i = 0; i < 6 && n > count + count / 2; ++i) {
+    const F mid = (lo + hi) / 2;
+    const int m = __syncthreads_count(mine >= mid);
+    if (m >= count) {
       lo = mid;
-      if (n <= count + count / 2) break;
+      n = m;
     } else {
-      hi = mid - 1;
+      hi = mid;
     }
   }
   return lo;
 }
 
-// The exact cut: value key and last place such that exactly min(count, all) of
-// the items (key > cut, or key == cut at a place <= last) are the best, ties by
-// place.  n_of(k, p): how many items are above key k, or at k up to place p.
-template <typename K, class Count>
-__device__ __forceinline__ void exact_cut(int count, K none, K most, int places, K &cut, int &last,
-                                          Count n_of) {
-  K lo = none, hi = most;  // the largest k with n(key >= k) >= count, if there is one
+// The exact cut: a key and a place such that the items above the key, and those
+// at it up to the place, are the best min(count, all), ties by place.  From `lo`
+// on, which at least `count` items reach (or nothing more is below than above it).
+// reach(k): how many items' keys are >= k; equal(k, p): how many are k, up to place p.
+template <typename K, class Reach, class Equal>
+__device__ __forceinline__ void exact_cut(int count, K lo, K most, int places, K &cut, int &last,
+                                          Reach reach, Equal equal) {
+  K hi = most;
   while (lo < hi) {
     const K mid = lo + (hi - lo + 1) / 2;
-    if (n_of(mid, places) >= count) lo = mid;
+    if (reach(mid) >= count) lo = mid;
     else hi = mid - 1;
   }
-  cut = lo;
-  last = places;
-  if (lo == none) {  // fewer than count items: all of them
-    cut = none + 1;
-    return;
-  }
+  const int need = count - reach(lo + 1);
   int a = 0, b = places;
   while (a < b) {
     const int mid = (int)(((int64_t)a + b) >> 1);
-    if (n_of(lo, mid) >= count) b = mid;
+    if (equal(lo, mid) >= need) b = mid;
     else a = mid + 1;
   }
+  cut = lo;
   last = a;
 }
 
-// e^t for t <= 0.
+// e^t for t <= 0 (below -80 as at -80, which no sum notices).
 __device__ __forceinline__ float exp_of(float t) {
-  t = fmaxf(t, -104.0f);
-  const float k = __fsub_rn(__fmaf_rn(t, 0x1.715476p+0f, 12582912.0f), 12582912.0f);
+  t = fmaxf(t, -80.0f);
+  const float j = __fmaf_rn(t, 0x1.715476p+0f, 12582912.0f);  // k in its low bits
+  const float k = __fsub_rn(j, 12582912.0f);
   // ln 2 = 0x1.62e4p-1 + 0x1.7f7d1cp-20: the first part's products with k are exact
   float r = __fmaf_rn(k, -0x1.62e4p-1f, t);
   r = __fmaf_rn(k, -0x1.7f7d1cp-20f, r);
@@ -129,10 +140,46 @@ __device__ __forceinline__ float exp_of(float t) {
   p = __fmaf_rn(p, r, 0.5f);
   p = __fmaf_rn(p, r, 1.0f);
   p = __fmaf_rn(p, r, 1.0f);
-  // (below 2^-126 in two steps)
-  const int e = (int)k, half = e >> 1;
-  return __fmul_rn(__fmul_rn(p, __uint_as_float((uint32_t)(127 + half) << 23)),
-                   __uint_as_float((uint32_t)(127 + e - half) << 23));
+  return __uint_as_float(__float_as_uint(p) + (__float_as_uint(j) << 23));
+}
+// Two at a time.
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+  uint64_t x;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a), "f"(b));
+  return x;
+}
+__device__ __forceinline__ uint64_t both(float a) { return pair_of(a, a); }
+__device__ __forceinline__ float2 halves(uint64_t x) {
+  return make_float2(__uint_as_float((uint32_t)x), __uint_as_float((uint32_t)(x >> 32)));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// 2^x by the special function unit, to 2^-22: for the terms that are small one by one.
+__device__ __forceinline__ float small_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// The largest element of a vector, NaN if one is.
+template <typename T>
+__device__ __forceinline__ float vector_max(const uint4 &q) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t m = pair_max(pair_max(q.x, q.y, T()), pair_max(q.z, q.w, T()), T());
+    float z[8];
+    unpack16(make_uint4(m, 0, 0, 0), z, T());
+    return max_nan(z[0], z[1]);
+  } else {
+    return max_nan(max_nan(__uint_as_float(q.x), __uint_as_float(q.y)),
+                   max_nan(__uint_as_float(q.z), __uint_as_float(q.w)));
+  }
 }
 
 template <typename T, bool ADJ>
@@ -219,21 +266,21 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
     each_touched(table, tid, kBeamThreads, [&](int u, float z) { body(u, __fmul_rn(z, inv)); });
   };
 
-  float top = kNegInf, s = 0.0f, lost = 0.0f, cut = kNegInf;
+  // mine: this thread's largest logit; top: what its sum is relative to, at least
+  // that (and the block's largest so far, as far as it was asked for)
+  float mine = kNegInf, top = kNegInf, cut = kNegInf;
+  float s = 0.0f, lost = 0.0f;  // the sum, and what its additions lost
   float touched_top = kNegInf;
   double touched_sum = 0.0;
-  auto raise = [&](float to) {  // a larger maximum: the sum is relative to it
+  auto raise = [&](float to) {
     if (to > top) {
-      const float f = exp_of(__fsub_rn(top, to));  // (0 for the first: e^-inf, s is 0)
+      const float f = top > kNegInf ? exp_of(__fsub_rn(top, to)) : 0.0f;
       s = __fmul_rn(s, f);
       lost = __fmul_rn(lost, f);
       top = to;
-    } else if (to != to) {
-      top = to;
     }
   };
-  auto add = [&](float x) {
-    const float e = x > kNegInf ? exp_of(__fsub_rn(x, top)) : 0.0f;
+  auto add = [&](float e) {
     const float y = __fsub_rn(e, lost), t = __fadd_rn(s, y);
     lost = __fsub_rn(__fsub_rn(t, s), y);
     s = t;
@@ -255,53 +302,114 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
   };
 
+  // A warp's tile.  ALL: every element counts.  SCALED: inv is not 1.
   int round = 0;
+  auto tile = [&](auto every, auto scaled, const uint4 (&q)[kBeamVecs], int u, int u_hi) {
+    constexpr bool ALL = decltype(every)::value, SCALED = decltype(scaled)::value;
+    uint32_t ok[kBeamVecs];
+    float m = kNegInf, top_of[kBeamVecs];
+#pragma unroll
+    for (int k = 0; k < kBeamVecs; ++k) {
+      if constexpr (ALL) {
+        // compared as it lies in memory: x is monotonous in z
+        top_of[k] = __fmul_rn(vector_max<T>(q[k]), inv);
+      } else {
+        ok[k] = ok_at(u + 32 * N * k, u_hi);
+        float x[N];
+        logits_of(q[k], ok[k], x);
+        top_of[k] = x[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) top_of[k] = max_nan(top_of[k], x[i]);
+      }
+      m = max_nan(m, top_of[k]);
+    }
+    mine = max_nan(mine, m);
+    // the first tile says what to look for; tiles 2, 8, 32, ... raise it
+    const bool fresh = round == 0 || ((round & 0x2aaaaaaa) == round && (round & (round - 1)) == 0);
+    if (fresh) {
+      const float most = value_of(most_key(mine));
+      raise(most);
+      cut = fmaxf(cut, threshold(mine, count, most, kLowest));
+    }
+    raise(m);
+    // Terms add up vector by vector in a tree of float32, from the special function
+    // unit (2^-22 of each); where few lanes have vectors with terms above e^-1.5 of
+    // the top, those are left out here and added one by one.
+    const float near = __fsub_rn(top, 1.5f);
+    uint32_t sums = 0;
+#pragma unroll
+    for (int k = 0; k < kBeamVecs; ++k)
+      if (!(top_of[k] < near)) sums |= 1u << k;
+    if (!(top > kNegInf) || __popc(__ballot_sync(0xffffffffu, sums != 0)) > kNearLanes) sums = 0;
+#pragma unroll
+    for (int k = 0; k < kBeamVecs; ++k) {
+      float x[N];
+      if constexpr (ALL) {
+        unpack16(q[k], x, T());
+        if constexpr (SCALED) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) x[i] = __fmul_rn(x[i], inv);
+        }
+      } else {
+        logits_of(q[k], ok[k], x);
+      }
+      uint64_t e[N / 2];
+#pragma unroll
+      for (int i = 0; i < N; i += 2) {
+        // (log2 e to a float32: a term e^t comes out too large by 1.4e-8 |t| of itself)
+        const float2 y =
+            halves(mul2(add2(pair_of(x[i], x[i + 1]), both(-top)), both(0x1.715476p+0f)));
+        e[i / 2] = pair_of(small_exp2(y.x), small_exp2(y.y));
+      }
+#pragma unroll
+      for (int o = N / 4; o > 0; o >>= 1) {
+#pragma unroll
+        for (int i = 0; i < o; ++i) e[i] = add2(e[i], e[i + o]);
+      }
+      const float2 pair = halves(e[0]);
+      add(!(sums >> k & 1) && top > kNegInf ? __fadd_rn(pair.x, pair.y) : 0.0f);
+    }
+    // A warp goes through what few lanes have: near the top, or perhaps among the best
+    // (ties with the cut of an earlier tile are not: their tokens are higher).
+    const bool keeps = fresh ? m >= cut : m > cut;
+    for (uint32_t lanes = __ballot_sync(0xffffffffu, keeps || sums != 0); lanes != 0;
+         lanes &= lanes - 1) {
+      const int l = __ffs(lanes) - 1;
+      const uint32_t add_it = __shfl_sync(0xffffffffu, sums, l);
+      const int k = lane / N, at = u + (l - lane) * N + 32 * N * k + lane % N;
+      if (k < kBeamVecs &&
+          (ALL || (at < u_hi && (!ADJ || ok_bits[(at - table_at) >> 5] >> ((at - table_at) & 31) & 1)))) {
+        const float x = __fmul_rn(logit_float(row.at0[at]), inv);
+        if (add_it >> k & 1) {
+          raise(x);
+          add(exp_of(__fsub_rn(x, top)));
+        }
+        if ((fresh ? x >= cut : x > cut) && x > kNegInf) keep(at, x);
+      }
+    }
+  };
   walk([&](int u_lo, int u_hi) {
     constexpr int kTile = kWarpTile * kBeamWarps;
     uint4 q[kBeamVecs], next[kBeamVecs];
     const int u_first = u_lo + wid * kWarpTile + lane * N;
+    auto fetch = [&](int u, int end) {  // a tile that ends at `end`
+      if (row.shift == 0 && end <= u_hi) {
 #pragma unroll
-    for (int k = 0; k < kBeamVecs; ++k) next[k] = raw_at(u_first + 32 * N * k, u_hi);
+        for (int k = 0; k < kBeamVecs; ++k)
+          next[k] = *reinterpret_cast<const uint4 *>(row.at0 + u + 32 * N * k);
+      } else {
+#pragma unroll
+        for (int k = 0; k < kBeamVecs; ++k) next[k] = raw_at(u + 32 * N * k, u_hi);
+      }
+    };
+    fetch(u_first, u_lo + kTile);
     for (int u = u_first, base = u_lo; base < u_hi; u += kTile, base += kTile, ++round) {
 #pragma unroll
       for (int k = 0; k < kBeamVecs; ++k) q[k] = next[k];
-      if (base + kTile < u_hi) {
-#pragma unroll
-        for (int k = 0; k < kBeamVecs; ++k) next[k] = raw_at(u + kTile + 32 * N * k, u_hi);
-      }
-      uint32_t ok[kBeamVecs];
-      float m = kNegInf;
-#pragma unroll
-      for (int k = 0; k < kBeamVecs; ++k) {
-        ok[k] = ok_at(u + 32 * N * k, u_hi);
-        float x[N];
-        logits_of(q[k], ok[k], x);
-#pragma unroll
-        for (int i = 0; i < N; ++i) m = max_nan(m, x[i]);
-      }
-      raise(m);
-      if (m > kNegInf) {
-#pragma unroll
-        for (int k = 0; k < kBeamVecs; ++k) {
-          float x[N];
-          logits_of(q[k], ok[k], x);
-#pragma unroll
-          for (int i = 0; i < N; ++i) add(x[i]);
-        }
-      }
-      // the first tile says what to look for, and tiles 2, 4, 8, ... raise it
-      if ((round & (round - 1)) == 0)
-        cut = fmaxf(cut, value_of(threshold(key_of(top), count, kNoKey, most_key(top))));
-      if (m >= cut) {
-#pragma unroll
-        for (int k = 0; k < kBeamVecs; ++k) {
-          float x[N];
-          logits_of(q[k], ok[k], x);
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            if (x[i] >= cut && x[i] > kNegInf) keep(u + 32 * N * k + i, x[i]);
-        }
-      }
+      if (base + kTile < u_hi) fetch(u + kTile, base + 2 * kTile);
+      if (ADJ || base + kTile > u_hi) tile(std::false_type(), std::true_type(), q, u, u_hi);
+      else if (inv != 1.0f) tile(std::true_type(), std::true_type(), q, u, u_hi);
+      else tile(std::true_type(), std::false_type(), q, u, u_hi);
     }
   }, [&] {
     // their own maximum, and their sum in units of 2^-40 of it
@@ -332,54 +440,53 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
   });
 
   // the part's maximum and sum
-  const bool bad = __syncthreads_or(!(top < __builtin_huge_valf()) ||
+  const bool bad = __syncthreads_or(!(mine < __builtin_huge_valf()) ||
                                     !(touched_top < __builtin_huge_valf()));
   if (bad) {
     if (tid == 0) *part = Part{0.0, kNegInf, -1};
     return;
   }
-  const float all_top = fmaxf(value_of(most_key(top)), touched_top);
-  const uint32_t most = key_of(all_top);
-  cut = fmaxf(cut, value_of(threshold(key_of(top), count, kNoKey, most)));
-  double sum = top > kNegInf ? ((double)s - (double)lost) * exp((double)top - (double)all_top) : 0.0;
+  const float all_top = fmaxf(value_of(most_key(mine)), touched_top);
+  cut = fmaxf(cut, threshold(mine, count, all_top, kLowest));
+  double sum = 0.0;
+  if (top > kNegInf) sum = ((double)s - (double)lost) * exp((double)top - (double)all_top);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sums[wid] = sum;
   int n = listed;  // (after the barriers above)
   const bool whole = n <= kBeamList;
-  int mine = 0;
+  int above = 0;
   if (whole)
-    for (int i = tid; i < n; i += kBeamThreads) mine += list[i].x >= cut;
-  n = block_sum(mine, words);
+    for (int i = tid; i < n; i += kBeamThreads) above += list[i].x >= cut;
+  n = block_sum(above, words);
   uint32_t key = key_of(cut);
   int last = in.vocab;
   if (!whole || n > 2 * count) {
     // more than the merge has room for (ties, mostly): exactly the best `count`
-    exact_cut<uint32_t>(count, kNoKey, most, in.vocab, key, last, [&](uint32_t k, int place) {
-      int c = 0;
+    // body(key, token) for the list, or for the part's tokens up to `place`
+    auto each = [&](int place, auto body) {
       if (whole) {
-        for (int i = tid; i < listed; i += kBeamThreads) {
-          const uint32_t v = key_of(list[i].x);
-          c += v > k || (v == k && list[i].token <= place);
-        }
+        for (int i = tid; i < listed; i += kBeamThreads) body(key_of(list[i].x), list[i].token);
       } else {
         walk([&](int u_lo, int u_hi) {
-          for (int u = u_lo + tid * N; u < u_hi; u += kBeamThreads * N) {
+          const int to = min(u_hi, place < in.vocab ? place + 1 + row.shift : u_hi);
+          for (int u = u_lo + tid * N; u < to; u += kBeamThreads * N) {
             float x[N];
             logits_of(raw_at(u, u_hi), ok_at(u, u_hi), x);
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-              const uint32_t v = key_of(x[i]);
-              c += v > k || (v == k && u + i - row.shift <= place);
-            }
+            for (int i = 0; i < N; ++i) body(key_of(x[i]), u + i - row.shift);
           }
-        }, [&] {
-          touched([&](int u, float x) {
-            const uint32_t v = key_of(x);
-            c += v > k || (v == k && u - row.shift <= place);
-          });
-        });
+        }, [&] { touched([&](int u, float x) { body(key_of(x), u - row.shift); }); });
       }
+    };
+    // (the cut that was looked for is reached by `count`, or is the lowest value)
+    exact_cut<uint32_t>(count, key_of(cut), key_of(all_top), in.vocab, key, last, [&](uint32_t k) {
+      int c = 0;
+      each(in.vocab, [&](uint32_t v, int) { c += v >= k; });
+      return block_sum(c, words);
+    }, [&](uint32_t k, int place) {
+      int c = 0;
+      each(place, [&](uint32_t v, int p) { c += v == k && p <= place; });
       return block_sum(c, words);
     });
   }
@@ -417,7 +524,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   __shared__ double total[kMergeList];
   __shared__ int place[kMergeList];        // beam * vocab + token
   __shared__ int listed, words[kMergeThreads / 32];
-  __shared__ uint64_t tops[kMergeThreads / 32];
+  __shared__ double tops[kMergeThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const int64_t t = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -462,17 +569,17 @@ __global__ void __launch_bounds__(kMergeThreads)
       body((double)x.x + c, b * vocab + x.token);
     }
   };
-  uint64_t best = kNoKey64;
-  each([&](double v, int) { best = max(best, key_of(v)); });
-  uint64_t most = best;
+  double best = -__builtin_huge_val();
+  each([&](double v, int) { best = fmax(best, v); });
+  double most = best;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  for (int o = 16; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
   if (lane == 0) tops[wid] = most;
   __syncthreads();
-  for (int i = 0; i < kMergeThreads / 32; ++i) most = max(most, tops[i]);
-  uint64_t key = threshold(best, count, kNoKey64, most);
+  for (int i = 0; i < kMergeThreads / 32; ++i) most = fmax(most, tops[i]);
+  const double cut = threshold(best, count, most, kLowest64);
   each([&](double v, int p) {
-    if (key_of(v) < key) return;
+    if (v < cut) return;
     const int at = atomicAdd(&listed, 1);
     if (at < kMergeList) {
       total[at] = v;
@@ -481,13 +588,15 @@ __global__ void __launch_bounds__(kMergeThreads)
   });
   __syncthreads();
   if (listed > kMergeList) {
+    uint64_t key;
     int last;
-    exact_cut<uint64_t>(count, kNoKey64, most, 0x7fffffff, key, last, [&](uint64_t k, int q) {
+    exact_cut<uint64_t>(count, key_of(cut), key_of(most), 0x7fffffff, key, last, [&](uint64_t k) {
       int c = 0;
-      each([&](double v, int p) {
-        const uint64_t x = key_of(v);
-        c += x > k || (x == k && p <= q);
-      });
+      each([&](double v, int) { c += key_of(v) >= k; });
+      return block_sum(c, words);
+    }, [&](uint64_t k, int q) {
+      int c = 0;
+      each([&](double v, int p) { c += key_of(v) == k && p <= q; });
       return block_sum(c, words);
     });
     __syncthreads();
