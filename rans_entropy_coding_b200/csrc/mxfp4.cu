@@ -48,87 +48,127 @@ __device__ __forceinline__ float inverse_scale(uint32_t byte) {
   return __uint_as_float((byte > 252 ? 1u : 254u - byte) << 23);
 }
 
+// The bits of a float32 at least as large as the magnitudes of a vector's elements and
+// with the largest one's exponent; an infinity or NaN where there is one.
+template <typename T>
+__device__ __forceinline__ uint32_t top_bits(const uint4 &q) {
+  if constexpr (sizeof(T) == 2) {
+    constexpr uint32_t kMagnitude = 0x7fff7fffu;
+    const uint32_t m = pair_max(pair_max(q.x & kMagnitude, q.y & kMagnitude, T()),
+                                pair_max(q.z & kMagnitude, q.w & kMagnitude, T()), T());
+    float z[8];
+    unpack16(make_uint4(m, 0, 0, 0), z, T());
+    return max(__float_as_uint(z[0]), __float_as_uint(z[1]));
+  } else {
+    constexpr uint32_t kMagnitude = 0x7fffffffu;
+    return max(max(q.x & kMagnitude, q.y & kMagnitude), max(q.z & kMagnitude, q.w & kMagnitude));
+  }
+}
+
 // A warp takes kQuantVecs runs of 32 vectors, one after another along a row.
+// Bound by the ALUs (unpacking, maxima and conversions, some 10 instructions an
+// element) more than by memory.
 template <typename T>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-    quantize_kernel(const T *x, int64_t rows, int64_t cols, int64_t stride, uint8_t *codes,
-                    uint8_t *scales, int64_t units, int per_row) {
+    quantize_kernel(const T *x, int64_t cols, int64_t stride, uint8_t *codes, uint8_t *scales,
+                    int64_t units, int per_row) {
   constexpr int N = VecOf<T>::N;
   constexpr int kLanes = kMxBlock / N;  // lanes of a block
   constexpr int kRun = 32 * N;
+  constexpr int kRunGroups = kRun / kMxGroup;
   // (a product behind this launch may prepare itself meanwhile)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
   if (unit >= units) return;
   const int64_t r = unit / per_row;
-  const int64_t c0 = (unit - r * per_row) * (kRun * kQuantVecs);
-  const T *row = x + r * stride, *end = row + cols;
-  const int64_t row_bytes = mx_row_bytes(cols), padded = row_bytes * 2;
+  const int c0 = (int)(unit - r * per_row) * (kRun * kQuantVecs), c = c0 + lane * N;
+  const T *row = x + r * stride;
+  const int64_t row_bytes = mx_row_bytes(cols);
   const int groups = mx_groups(cols);
+  uint8_t *code_at = codes + r * row_bytes + c / 2;
+  uint8_t *scale_at = scales + mx_scale_at(r, c / kMxGroup, groups) + c % kMxGroup / kMxBlock;
+  const bool whole = c0 + kRun * kQuantVecs <= cols;
   uint4 q[kQuantVecs];
+  if (whole && reinterpret_cast<uintptr_t>(row) % 16 == 0) {
 #pragma unroll
-  for (int k = 0; k < kQuantVecs; ++k) {
-    const int64_t c = c0 + k * kRun + lane * N;
-    q[k] = c < cols ? load_joined(row, row + c, end) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kQuantVecs; ++k)
+      q[k] = __ldcs(reinterpret_cast<const uint4 *>(row + c + k * kRun));
+  } else {
+#pragma unroll
+    for (int k = 0; k < kQuantVecs; ++k)
+      q[k] = c + k * kRun < cols ? load_joined(row, row + c + k * kRun, row + cols)
+                                 : make_uint4(0, 0, 0, 0);
   }
 #pragma unroll
   for (int k = 0; k < kQuantVecs; ++k) {
-    const int64_t c = c0 + k * kRun + lane * N;
-    float z[N];
-    unpack16(q[k], z, T());
-    uint32_t top = 0;
-#pragma unroll
-    for (int i = 0; i < N; ++i) top = max(top, __float_as_uint(z[i]) & 0x7fffffffu);
+    uint32_t top = top_bits<T>(q[k]);
 #pragma unroll
     for (int o = 1; o < kLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
     const uint32_t byte = scale_byte(top);
     const float inv = inverse_scale(byte);
+    float z[N];
+    unpack16(q[k], z, T());
 #pragma unroll
     for (int i = 0; i < N; ++i) z[i] = __fmul_rn(z[i], inv);
     const uint32_t w = codes8(z);
-    if (c < padded) {
-      uint8_t *at = codes + r * row_bytes + c / 2;
-      if constexpr (N == 8) *reinterpret_cast<uint32_t *>(at) = w;
-      else *reinterpret_cast<uint16_t *>(at) = (uint16_t)w;
+    if (whole || c + k * kRun < 2 * row_bytes) {
+      if constexpr (N == 8) *reinterpret_cast<uint32_t *>(code_at + k * kRun / 2) = w;
+      else *reinterpret_cast<uint16_t *>(code_at + k * kRun / 2) = (uint16_t)w;
     }
     // (bytes of a group's blocks past the row's end are 0)
-    const int g = (int)(c / kMxGroup);
-    if (lane % kLanes == 0 && g < groups)
-      scales[mx_scale_at(r, g, groups) + c % kMxGroup / kMxBlock] = (uint8_t)byte;
+    if (lane % kLanes == 0 && (whole || (c + k * kRun) / kMxGroup < groups))
+      scale_at[k * kRunGroups * kMxTileBytes] = (uint8_t)byte;
   }
 }
 
-// Eight codes (or four, in the low half) as their magnitudes' floats: a code's
-// exponent and mantissa bits become a float's, whose scale 2^126 undoes that the
-// smallest magnitude is a subnormal.
-__device__ __forceinline__ float code_value(uint32_t c) {
-  const float a = __fmul_rn(__uint_as_float((c & 7u) << 22), 0x1p+126f);
-  return __uint_as_float(__float_as_uint(a) | (c & 8u) << 28);
+// The numbers of N codes.
+__device__ __forceinline__ void code_values(uint32_t w, float (&z)[8]) {
+  uint32_t h[4];
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+      : "r"(w));
+  unpack16(make_uint4(h[0], h[1], h[2], h[3]), z, __half());
+}
+__device__ __forceinline__ void code_values(uint32_t w, float (&z)[4]) {
+  uint32_t h[2];
+  asm("{\n\t.reg .b8 a, b;\n\tmov.b16 {a, b}, %2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t}"
+      : "=r"(h[0]), "=r"(h[1])
+      : "h"((uint16_t)w));
+  float y[8];
+  unpack16(make_uint4(h[0], h[1], 0, 0), y, __half());
+#pragma unroll
+  for (int i = 0; i < 4; ++i) z[i] = y[i];
 }
 
 template <typename O>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-    values_kernel(const uint8_t *codes, const uint8_t *scales, int64_t rows, int64_t cols, O *out,
+    values_kernel(const uint8_t *codes, const uint8_t *scales, int64_t cols, O *out,
                   int64_t stride, int64_t units, int per_row) {
   constexpr int N = VecOf<O>::N;
   constexpr int kRun = 32 * N;
+  constexpr int kRunGroups = kRun / kMxGroup;
   const int lane = threadIdx.x & 31;
   const int64_t unit = (int64_t)blockIdx.x * kQuantWarps + (threadIdx.x >> 5);
   if (unit >= units) return;
   const int64_t r = unit / per_row;
-  const int64_t c0 = (unit - r * per_row) * (kRun * kQuantVecs);
-  const int64_t row_bytes = mx_row_bytes(cols), padded = row_bytes * 2;
+  const int c0 = (int)(unit - r * per_row) * (kRun * kQuantVecs), c = c0 + lane * N;
+  const int64_t row_bytes = mx_row_bytes(cols);
   const int groups = mx_groups(cols);
+  const uint8_t *code_at = codes + r * row_bytes + c / 2;
+  const uint8_t *scale_at = scales + mx_scale_at(r, c / kMxGroup, groups) + c % kMxGroup / kMxBlock;
+  const bool whole = c0 + kRun * kQuantVecs <= cols;
   uint32_t w[kQuantVecs], byte[kQuantVecs];
 #pragma unroll
   for (int k = 0; k < kQuantVecs; ++k) {
-    const int64_t c = c0 + k * kRun + lane * N;
     w[k] = byte[k] = 0;
-    if (c < padded) {
-      const uint8_t *at = codes + r * row_bytes + c / 2;
-      w[k] = N == 8 ? *reinterpret_cast<const uint32_t *>(at) : *reinterpret_cast<const uint16_t *>(at);
-      byte[k] = scales[mx_scale_at(r, (int)(c / kMxGroup), groups) + c % kMxGroup / kMxBlock];
+    if (whole || c + k * kRun < 2 * row_bytes) {
+      if constexpr (N == 8) w[k] = *reinterpret_cast<const uint32_t *>(code_at + k * kRun / 2);
+      else w[k] = *reinterpret_cast<const uint16_t *>(code_at + k * kRun / 2);
+      byte[k] = scale_at[k * kRunGroups * kMxTileBytes];
     }
   }
   uint4 p[kQuantVecs];
@@ -138,13 +178,13 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
                         : byte[k] > 0  ? __uint_as_float(byte[k] << 23)
                                        : 0x1p-127f;
     float z[N];
+    code_values(w[k], z);
 #pragma unroll
-    for (int i = 0; i < N; ++i) z[i] = __fmul_rn(code_value(w[k] >> (4 * i)), scale);
+    for (int i = 0; i < N; ++i) z[i] = __fmul_rn(z[i], scale);
     p[k] = pack16(z, O());
   }
-  const bool inside = c0 + kRun * kQuantVecs <= cols;
   // (columns fit an int: RANS_MAX_VOCAB of them at most)
-  store_tile<false>(out + r * stride, (int)c0, p, inside, 0, (int)cols);
+  store_tile<false>(out + r * stride, c0, p, whole, 0, (int)cols);
 }
 
 struct Units {
@@ -164,8 +204,7 @@ int quantize_t(const rans_logits &x, const rans_mxfp4 &q, cudaStream_t st) {
   const Units u = units_of(x.rows, x.vocab, 32 * VecOf<T>::N);
   if (!u.ok) return RANS_ERR_ARG;
   quantize_kernel<T><<<u.blocks, 32 * kQuantWarps, 0, st>>>(
-      static_cast<const T *>(x.data), x.rows, x.vocab, x.row_stride, q.codes, q.scales, u.units,
-      u.per_row);
+      static_cast<const T *>(x.data), x.vocab, x.row_stride, q.codes, q.scales, u.units, u.per_row);
   return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
 }
 
@@ -174,7 +213,7 @@ int values_t(const rans_mxfp4 &q, void *out, int64_t stride, cudaStream_t st) {
   const Units u = units_of(q.rows, q.cols, 32 * VecOf<O>::N);
   if (!u.ok) return RANS_ERR_ARG;
   values_kernel<O><<<u.blocks, 32 * kQuantWarps, 0, st>>>(
-      q.codes, q.scales, q.rows, q.cols, static_cast<O *>(out), stride, u.units, u.per_row);
+      q.codes, q.scales, q.cols, static_cast<O *>(out), stride, u.units, u.per_row);
   return cudaGetLastError() == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
 }
 
