@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(32 * kQuantWarps)
   }
 }
 
-// The numbers of N codes.
+// The numbers of N codes.  (Each width unpacks a register of its own size: four bytes
+// unpacked from a zero-extended half gave zeros.)
 __device__ __forceinline__ void code_values(uint32_t w, float (&z)[8]) {
   uint32_t h[4];
   asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"

@@ -11,7 +11,10 @@
 // along k: a row's logits do not depend on the batch it came in.
 //
 // A block per SM walks tiles of 128 head rows by up to 256 tokens (tokens
-// fastest, so that neighbours share the head's rows in L2).  One thread copies
+// fastest, so that neighbours share the head's rows in L2).  With more than 128
+// tokens two blocks work as a pair (cta_group::2): on 256 head rows, each with its own
+// 128 and half of the tokens in shared memory, so that a token's codes cross from
+// L2 once for 256 rows.  One thread copies
 // stages of 256 columns (TMA, 128-byte swizzle; scales by bulk copies) through a
 // ring in shared memory, one copies the scales on to tensor memory and issues
 // the products, and eight warps take the accumulators: each keeps half of a
@@ -19,6 +22,7 @@
 // tensor memory is read, while the logits are still being rounded and stored.
 #include <cuda.h>
 
+#include "cluster.cuh"
 #include "mxfp4.cuh"
 #include "logits_common.cuh"
 #include "rans_common.cuh"
@@ -35,6 +39,7 @@ constexpr int kStepCols = 64;                   // of one instruction
 constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kProductThreads = 128 + 32 * kEpilogueWarps;
+constexpr int kStoreTokens = 16;                // that change places at a time
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 256;             // scales behind the accumulators
 constexpr uint32_t kScaleCols = 24;             // of one stage: 8 of the head, 16 of the tokens
@@ -56,31 +61,73 @@ constexpr uint32_t kSwizzledDesc = 1024 >> 4 | 1u << 14 | 2u << 29;  // 8 rows o
 constexpr uint32_t kPlainDesc = 128 >> 4 | 1u << 14;                 // 8 rows of 16 bytes
 __device__ __forceinline__ uint32_t desc_of(uint32_t addr) { return (addr & 0x3ffff) >> 4; }
 // 4-bit floats with scales of an exponent's byte, rows along k on both sides.
-__device__ __forceinline__ uint32_t instruction(int tokens, int scale_byte) {
+__device__ __forceinline__ uint32_t instruction(int head_rows, int tokens, int scale_byte) {
   return (uint32_t)scale_byte << 4 | 1u << 7 | 1u << 10 | (uint32_t)(tokens >> 3) << 17 |
-         1u << 23 | (uint32_t)(kHeadRows >> 4) << 24 | (uint32_t)scale_byte << 29;
+         1u << 23 | (uint32_t)(head_rows >> 4) << 24 | (uint32_t)scale_byte << 29;
 }
+template <bool PAIR>
 __device__ __forceinline__ void multiply(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                          uint32_t sfa, uint32_t sfb, bool add) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-      "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"
-      "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], "
-      "p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add), "n"(kSwizzledDesc)
-      : "memory");
+#define RB_MULTIPLY(GROUP)                                                                     \
+  asm volatile(                                                                                \
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\t"                     \
+      "mov.b64 a, {%1, %7};\n\tmov.b64 b, {%2, %7};\n\t"                                       \
+      "tcgen05.mma.cta_group::" GROUP                                                          \
+      ".kind::mxf4.block_scale.scale_vec::2X [%0], a, b, %3, [%4], [%5], p;\n\t}" ::"r"(d),    \
+      "r"(a), "r"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"((uint32_t)add), "n"(kSwizzledDesc)   \
+      : "memory")
+  if constexpr (PAIR) RB_MULTIPLY("2");
+  else RB_MULTIPLY("1");
+#undef RB_MULTIPLY
 }
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t to, uint32_t from) {
-  asm volatile(
-      "{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"
-      "tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], d;\n\t}" ::"r"(to),
-      "r"(from), "n"(kPlainDesc)
-      : "memory");
+#define RB_COPY(GROUP)                                                             \
+  asm volatile("{\n\t.reg .b64 d;\n\tmov.b64 d, {%1, %2};\n\t"                     \
+               "tcgen05.cp.cta_group::" GROUP ".32x128b.warpx4 [%0], d;\n\t}" ::"r"(to), \
+               "r"(from), "n"(kPlainDesc)                                          \
+               : "memory")
+  if constexpr (PAIR) RB_COPY("2");
+  else RB_COPY("1");
+#undef RB_COPY
 }
+// Arrives when the products issued so far are done; of a pair, at both blocks'.
+template <bool PAIR>
 __device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                   bar)
-               : "memory");
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+  else
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+}
+// A barrier in this block or in another one of the cluster.
+__device__ __forceinline__ void arrive_at(uint32_t bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok != 0;
+}
+// A tile into this block's memory, announced at a barrier of either of the pair.
+__device__ __forceinline__ void load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y,
+                                             uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
 }
 __device__ __forceinline__ void arrive(uint32_t bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -120,11 +167,45 @@ __device__ __forceinline__ void load_columns(float *v, uint32_t at) {
                : "r"(at));
 }
 
-// HALF: most columns that an epilogue warp keeps.
-template <typename O, int HALF>
+// A warp's copy of up to 128 logits of one token from shared memory, four a lane, at
+// any alignment of the result.
+template <typename O>
+__device__ __forceinline__ void store_logits(O *to, const O *from, int valid, int lane) {
+  struct __align__(4 * sizeof(O)) Four {
+    O x[4];
+  };
+  const int past = (int)((reinterpret_cast<uintptr_t>(to) / sizeof(O)) & 3);
+  const int e = 4 * lane - past;
+  if (past == 0 && valid == kHeadRows) {
+    *reinterpret_cast<Four *>(to + e) = *reinterpret_cast<const Four *>(from + e);
+    return;
+  }
+  if (e >= 0 && e + 4 <= valid) {
+    Four f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f.x[i] = from[e + i];
+    *reinterpret_cast<Four *>(to + e) = f;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (e + i >= 0 && e + i < valid) to[e + i] = from[e + i];
+  }
+  // the last lane's end lies before the row's
+  if (lane < past && kHeadRows - past + lane < valid)
+    to[kHeadRows - past + lane] = from[kHeadRows - past + lane];
+}
+
+// The tensor maps of a product.
+struct ProductMaps {
+  CUtensorMap head, tokens;               // codes
+  CUtensorMap head_scales, token_scales;  // of a pair
+};
+
+// HALF: most columns that an epilogue warp keeps.  PAIR: two blocks on 256 head rows;
+// the first of them issues the products, and all copies are announced at its barriers.
+template <typename O, int HALF, bool PAIR>
 __global__ void __launch_bounds__(kProductThreads, 1)
-    product_kernel(const __grid_constant__ CUtensorMap head_map,
-                   const __grid_constant__ CUtensorMap token_map, const uint8_t *head_scales,
+    product_kernel(const __grid_constant__ ProductMaps maps, const uint8_t *head_scales,
                    const uint8_t *token_scales, O *out, int64_t out_stride, ProductShape sh,
                    int32_t *status) {
   extern __shared__ unsigned char smem_raw[];
@@ -132,47 +213,69 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;  // a wait gave up
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(kFull, tid >> 5, 0);
+  const int rank = PAIR ? (int)cluster_rank() : 0;
+  const int first_tile = PAIR ? (int)blockIdx.x >> 1 : (int)blockIdx.x;
+  const int tile_step = PAIR ? (int)gridDim.x >> 1 : (int)gridDim.x;
+  constexpr int kRows = PAIR ? 2 * kHeadRows : kHeadRows;
   const uint32_t smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t token_bytes = (uint32_t)sh.box * kStageBytes;
+  const uint32_t token_bytes = (uint32_t)(PAIR ? kMostTokens / 2 : sh.box) * kStageBytes;
   const int row_tiles = (sh.box + kMxTileRows - 1) / kMxTileRows;
   const uint32_t at_tokens = kHeadRows * kStageBytes, at_head_scales = at_tokens + token_bytes;
   const uint32_t at_token_scales = at_head_scales + 2 * kMxTileBytes;
   const uint32_t stage_bytes = at_token_scales + (uint32_t)row_tiles * 2 * kMxTileBytes;
   const int per_tile = (sh.steps + 3) / 4;  // stages of a tile
+  // tokens of a tile as the products take them: a pair's halves are a multiple of 16
+  auto width_of = [&](int left) {
+    return PAIR ? min(kMostTokens, (left + 31) & ~31) : min(sh.box, (left + 15) & ~15);
+  };
 
-  if (wid == 0) {
-    if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&head_map)) : "memory");
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&token_map)) : "memory");
-    }
-  } else if (wid == 1) {
+  if (wid == 1) {
     if (lane == 0) {
       for (int i = 0; i < sh.stages; ++i) {
         tma::mbar_init(smem_addr(&full_bar[i]), 2);  // the head's side, the tokens'
         tma::mbar_init(smem_addr(&empty_bar[i]), 1);
       }
       tma::mbar_init(smem_addr(&done_bar), 1);
-      tma::mbar_init(smem_addr(&free_bar), kEpilogueWarps);
+      tma::mbar_init(smem_addr(&free_bar), PAIR ? 2 * kEpilogueWarps : kEpilogueWarps);
       dead = 0;
       tma::fence_mbar_init();
       tma::fence_proxy_async();
     }
   } else if (wid == 3) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&tmem_base)),
-                 "n"(kTmemCols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if constexpr (PAIR) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmem_base)),
+                   "n"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&tmem_base)),
+                   "n"(kTmemCols)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   }
   __syncthreads();
+  if constexpr (PAIR) {  // the other block's barriers are there
+    cluster_arrive();
+    cluster_wait();
+  }
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
   const uint32_t tmem = tmem_base;
+  // A barrier's address in the block that issues the products.
+  auto leader = [&](const uint64_t *bar) {
+    return PAIR ? peer_address(bar, 0) : smem_addr(bar);
+  };
   // A warp's wait: until another gave up, or for its own share.
-  auto wait = [&](uint64_t *bar, uint32_t parity) {
+  // (Only what the other block's threads arrive at is waited for at the cluster's scope,
+  // whose fences cost more than a stage.)
+  auto wait = [&](uint64_t *bar, uint32_t parity, bool cluster = false) {
     const uint32_t b = smem_addr(bar);
     for (uint32_t i = 0; i < kTries; ++i) {
-      if (__all_sync(kFull, mbar_try_wait(b, parity))) return true;
+      if (__all_sync(kFull, cluster ? try_wait_cluster(b, parity) : mbar_try_wait(b, parity)))
+        return true;
       if (__any_sync(kFull, dead)) return false;
     }
     if (lane == 0) {
@@ -188,7 +291,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     // one warp for the head's, one for the tokens'.  (A stage's place is counted up: a
     // division took longer than the stage's products.)
     if (wid == 2 && sh.wait) asm volatile("griddepcontrol.wait;" ::: "memory");
-    int tile = (int)blockIdx.x, kb = 0, stage = 0;
+    int tile = first_tile, kb = 0, stage = 0;
     uint32_t lap = 0;
     bool ok = true;
     int mt = tile / sh.token_tiles, nt = tile - mt * sh.token_tiles;
@@ -197,24 +300,50 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         ok = wait(&empty_bar[stage], (lap - 1) & 1);
         if (!ok) break;
       }
-      const uint32_t bar = smem_addr(&full_bar[stage]), s = smem + stage * stage_bytes;
-      const uint32_t bytes = (uint32_t)min(2, sh.groups - 2 * kb) * kMxTileBytes;
-      if (elected()) {
-        if (wid == 0) {
-          tma::arrive_expect(bar, at_tokens + bytes);
-          load_2d(s, &head_map, kb * kStageBytes, mt * kHeadRows, bar);
-          load_bulk(s + at_head_scales,
-                    head_scales + ((int64_t)mt * sh.groups + 2 * kb) * kMxTileBytes, bytes, bar);
-        } else {
-          const int first = nt * (kMostTokens / kMxTileRows);
-          const bool two = row_tiles > 1 && (first + 1) * kMxTileRows < sh.tokens;
-          tma::arrive_expect(bar, token_bytes + (two ? 2 * bytes : bytes));
-          load_2d(s + at_tokens, &token_map, kb * kStageBytes, nt * kMostTokens, bar);
-          const uint8_t *scales = token_scales + ((int64_t)first * sh.groups + 2 * kb) * kMxTileBytes;
-          load_bulk(s + at_token_scales, scales, bytes, bar);
-          if (two)
-            load_bulk(s + at_token_scales + 2 * kMxTileBytes,
-                      scales + (int64_t)sh.groups * kMxTileBytes, bytes, bar);
+      const uint32_t bar = leader(&full_bar[stage]), s = smem + stage * stage_bytes;
+      const int row = mt * kRows + rank * kHeadRows;
+      if constexpr (PAIR) {
+        // Scales as tiles of 1024 bytes, zeros past the last.  The first block expects
+        // what both copy: the other's may be there before that, but not before the
+        // stage's last use, which its own wait has seen.
+        if (elected()) {
+          if (wid == 0) {
+            if (rank == 0) tma::arrive_expect(smem_addr(&full_bar[stage]), 2 * (at_tokens + 2 * kMxTileBytes));
+            load_2d_pair(s, &maps.head, kb * kStageBytes, row, bar);
+            load_2d_pair(s + at_head_scales, &maps.head_scales, kb * (2 * kMxTileBytes / 4),
+                         row / kMxTileRows, bar);
+          } else {
+            const int n0 = nt * kMostTokens;
+            const int half = width_of(sh.tokens - n0) / 2;
+            if (rank == 0)
+              tma::arrive_expect(smem_addr(&full_bar[stage]),
+                                 2 * (token_bytes + (uint32_t)row_tiles * 2 * kMxTileBytes));
+            load_2d_pair(s + at_tokens, &maps.tokens, kb * kStageBytes, n0 + rank * half, bar);
+            for (int h = 0; h < row_tiles; ++h)
+              load_2d_pair(s + at_token_scales + h * 2 * kMxTileBytes, &maps.token_scales,
+                           kb * (2 * kMxTileBytes / 4), n0 / kMxTileRows + h, bar);
+          }
+        }
+      } else {
+        const uint32_t bytes = (uint32_t)min(2, sh.groups - 2 * kb) * kMxTileBytes;
+        if (elected()) {
+          if (wid == 0) {
+            tma::arrive_expect(bar, at_tokens + bytes);
+            load_2d(s, &maps.head, kb * kStageBytes, row, bar);
+            load_bulk(s + at_head_scales,
+                      head_scales + ((int64_t)mt * sh.groups + 2 * kb) * kMxTileBytes, bytes, bar);
+          } else {
+            const int first = nt * (kMostTokens / kMxTileRows);
+            const bool two = row_tiles > 1 && (first + 1) * kMxTileRows < sh.tokens;
+            tma::arrive_expect(bar, token_bytes + (two ? 2 * bytes : bytes));
+            load_2d(s + at_tokens, &maps.tokens, kb * kStageBytes, nt * kMostTokens, bar);
+            const uint8_t *scales =
+                token_scales + ((int64_t)first * sh.groups + 2 * kb) * kMxTileBytes;
+            load_bulk(s + at_token_scales, scales, bytes, bar);
+            if (two)
+              load_bulk(s + at_token_scales + 2 * kMxTileBytes,
+                        scales + (int64_t)sh.groups * kMxTileBytes, bytes, bar);
+          }
         }
       }
       __syncwarp();
@@ -224,27 +353,26 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       }
       if (++kb == per_tile) {
         kb = 0;
-        tile += (int)gridDim.x;
+        tile += tile_step;
         mt = tile / sh.token_tiles;
         nt = tile - mt * sh.token_tiles;
       }
     }
-    if (!ok) {
-      // copies in flight write to this block's memory: they end first (as far as both
+    if (!ok && rank == 0) {
+      // copies in flight write to this block's memory: they end first (as far as all
       // warps have issued theirs)
       for (int i = 0; i < sh.stages; ++i)
         tma::wait_bounded(smem_addr(&full_bar[i]), (i < stage ? lap : lap - 1) & 1, 1u << 18);
     }
-  } else if (wid == 1) {
+  } else if (wid == 1 && rank == 0) {
     // ----------------------------------------------------- the products --
     int stage = 0, n_tile = 0;
     uint32_t lap = 0, odd = 0;
     bool ok = true;
-    for (int tile = (int)blockIdx.x; tile < sh.tiles; tile += (int)gridDim.x, ++n_tile) {
-      const int left = sh.tokens - tile % sh.token_tiles * kMostTokens;
-      const int width = min(sh.box, (left + 15) & ~15);
-      const uint32_t idesc0 = instruction(width, 0), idesc2 = instruction(width, 2);
-      ok = n_tile == 0 || wait(&free_bar, (uint32_t)(n_tile - 1) & 1);
+    for (int tile = first_tile; tile < sh.tiles; tile += tile_step, ++n_tile) {
+      const int width = width_of(sh.tokens - tile % sh.token_tiles * kMostTokens);
+      const uint32_t idesc0 = instruction(kRows, width, 0), idesc2 = instruction(kRows, width, 2);
+      ok = n_tile == 0 || wait(&free_bar, (uint32_t)(n_tile - 1) & 1, PAIR);
       if (!ok) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       for (int kb = 0; kb < per_tile; ++kb) {
@@ -263,20 +391,20 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
             for (int g = 0; g < 2; ++g)
               if (g < groups) {
-                copy_scales(sf + 4 * g, fa + 32 * g);
-                copy_scales(sf + 8 + 8 * g, fb + 32 * g);
-                if (width > kMxTileRows) copy_scales(sf + 12 + 8 * g, fb + 64 + 32 * g);
+                copy_scales<PAIR>(sf + 4 * g, fa + 32 * g);
+                copy_scales<PAIR>(sf + 8 + 8 * g, fb + 32 * g);
+                if (width > kMxTileRows) copy_scales<PAIR>(sf + 12 + 8 * g, fb + 64 + 32 * g);
               }
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               if (j < steps)
-                multiply(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0, sf + 4 * (j >> 1),
-                         sf + 8 + 8 * (j >> 1), j > 0 || kb > 0);
+                multiply<PAIR>(tmem, a + 2 * j, b + 2 * j, j & 1 ? idesc2 : idesc0,
+                               sf + 4 * (j >> 1), sf + 8 + 8 * (j >> 1), j > 0 || kb > 0);
           };
           if (steps == 4) work(2, 4);
           else work(groups, steps);
-          commit(smem_addr(&empty_bar[stage]));
-          if (kb == per_tile - 1) commit(smem_addr(&done_bar));
+          commit<PAIR>(smem_addr(&empty_bar[stage]));
+          if (kb == per_tile - 1) commit<PAIR>(smem_addr(&done_bar));
         }
         __syncwarp();
         odd ^= 1;
@@ -289,16 +417,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     }
     if (!ok) {
       // products in flight: a last commit follows them
-      if (elected()) commit(smem_addr(&done_bar));
+      if (elected()) commit<PAIR>(smem_addr(&done_bar));
       tma::wait_bounded(smem_addr(&done_bar), (uint32_t)n_tile & 1, 1u << 21);
     }
   } else if (wid >= 4) {
     // --------------------------------------------------- the accumulators --
     const int quarter = wid & 3, half = (wid - 4) >> 2;
-    int n_tile = 0;
-    for (int tile = (int)blockIdx.x; tile < sh.tiles; tile += (int)gridDim.x, ++n_tile) {
+    const uint32_t freed = leader(&free_bar);
+    unsigned char *exchange = smem_raw + (smem - smem_addr(smem_raw)) + sh.stages * stage_bytes;
+    int n_tile = 0, turn = 0;
+    for (int tile = first_tile; tile < sh.tiles; tile += tile_step, ++n_tile) {
       const int mt = tile / sh.token_tiles, n0 = tile % sh.token_tiles * kMostTokens;
-      const int left = sh.tokens - n0, width = min(sh.box, (left + 15) & ~15);
+      const int left = sh.tokens - n0, width = width_of(left);
       const int c0 = half * (width / 2);
       const int count = min(width / 2, left - c0);  // columns of this warp that are tokens
       if (!wait(&done_bar, (uint32_t)n_tile & 1)) break;
@@ -313,55 +443,99 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       for (int i = 0; i < HALF; ++i) asm volatile("" : "+f"(v[i]));
       asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
       __syncwarp();
-      if (lane == 0) arrive(smem_addr(&free_bar));
-      const int row = mt * kHeadRows + quarter * 32 + lane;
-      if (row < sh.head_rows) {
-        O *o = out + (int64_t)(n0 + c0) * out_stride + row;
+      if (lane == 0) {
+        if constexpr (PAIR) arrive_at(freed);
+        else arrive(freed);
+      }
+      const int row0 = mt * kRows + rank * kHeadRows, row = quarter * 32 + lane;
+      O *o = out + (int64_t)(n0 + c0) * out_stride + row0;
+      if constexpr (HALF < kStoreTokens * 2) {
+        if (row0 + row < sh.head_rows) {
 #pragma unroll
-        for (int i = 0; i < HALF; ++i)
-          if (i < count) o[i * out_stride] = float_logit<O>(v[i]);
+          for (int i = 0; i < HALF; ++i)
+            if (i < count) o[i * out_stride + row] = float_logit<O>(v[i]);
+        }
+      } else {
+        // A lane has one logit of many tokens; 16 tokens at a time change places in shared
+        // memory, so that a store takes a token's 128 logits.  (Stored as they come, two
+        // bytes a lane, they took longer than the products.)
+        const int valid = min(kHeadRows, sh.head_rows - row0);
+#pragma unroll
+        for (int p = 0; p < HALF; p += kStoreTokens) {
+          if (p < count) {
+            O *buf = reinterpret_cast<O *>(exchange) + (half * 2 + turn) * kStoreTokens * kHeadRows;
+#pragma unroll
+            for (int i = 0; i < kStoreTokens; ++i)
+              buf[i * kHeadRows + row] = float_logit<O>(v[p + i]);
+            asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+            for (int i = quarter; i < min(kStoreTokens, count - p); i += 4)
+              store_logits(o + (p + i) * out_stride, buf + i * kHeadRows, valid, lane);
+            turn ^= 1;
+          }
+        }
       }
     }
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
   __syncthreads();
+  if constexpr (PAIR) {  // nothing reaches into a block that has left
+    cluster_arrive();
+    cluster_wait();
+  }
   if (wid == 3) {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "n"(kTmemCols));
+    if constexpr (PAIR)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "n"(kTmemCols));
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                   "n"(kTmemCols));
   }
 }
 
-template <typename O, int HALF>
-int launch_t(const CUtensorMap &hm, const CUtensorMap &tm, const rans_mxfp4 &a,
-             const rans_mxfp4 &w, void *out, int64_t stride, const ProductShape &sh,
-             uint32_t smem, int32_t *status, int sms, cudaStream_t st) {
-  auto kern = product_kernel<O, HALF>;
+template <typename O, int HALF, bool PAIR>
+int launch_t(const ProductMaps &maps, const rans_mxfp4 &a, const rans_mxfp4 &w, void *out,
+             int64_t stride, const ProductShape &sh, uint32_t smem, int32_t *status, int blocks,
+             cudaStream_t st) {
+  auto kern = product_kernel<O, HALF, PAIR>;
   if (ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(sh.tiles < sms ? sh.tiles : sms));
+  cfg.gridDim = dim3((unsigned)blocks);
   cfg.blockDim = dim3(kProductThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchAttribute attr[2];
+  unsigned n = 0;
+  if (PAIR) {
+    attr[n].id = cudaLaunchAttributeClusterDimension;
+    attr[n].val.clusterDim.x = 2;
+    attr[n].val.clusterDim.y = attr[n].val.clusterDim.z = 1;
+    ++n;
+  }
+  if (sh.wait) {
+    attr[n].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[n].val.programmaticStreamSerializationAllowed = 1;
+    ++n;
+  }
   cfg.attrs = attr;
-  cfg.numAttrs = sh.wait ? 1 : 0;
+  cfg.numAttrs = n;
   const cudaError_t e =
-      cudaLaunchKernelEx(&cfg, kern, hm, tm, (const uint8_t *)w.scales, (const uint8_t *)a.scales,
+      cudaLaunchKernelEx(&cfg, kern, maps, (const uint8_t *)w.scales, (const uint8_t *)a.scales,
                          static_cast<O *>(out), stride, sh, status);
   return e == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
 }
 
 template <typename O>
-int launch_o(const CUtensorMap &hm, const CUtensorMap &tm, const rans_mxfp4 &a,
-             const rans_mxfp4 &w, void *out, int64_t stride, const ProductShape &sh,
-             uint32_t smem, int32_t *status, int sms, cudaStream_t st) {
-  if (sh.box <= 32) return launch_t<O, 16>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
-  if (sh.box <= 128) return launch_t<O, 64>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
-  return launch_t<O, 128>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+int launch_o(const ProductMaps &maps, const rans_mxfp4 &a, const rans_mxfp4 &w, void *out,
+             int64_t stride, const ProductShape &sh, bool pair, uint32_t smem, int32_t *status,
+             int blocks, cudaStream_t st) {
+  if (pair) return launch_t<O, 128, true>(maps, a, w, out, stride, sh, smem, status, blocks, st);
+  if (sh.box <= 32)
+    return launch_t<O, 16, false>(maps, a, w, out, stride, sh, smem, status, blocks, st);
+  if (sh.box <= 128)
+    return launch_t<O, 64, false>(maps, a, w, out, stride, sh, smem, status, blocks, st);
+  return launch_t<O, 128, false>(maps, a, w, out, stride, sh, smem, status, blocks, st);
 }
 
 }  // namespace
@@ -370,37 +544,55 @@ int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, in
                          int64_t stride, int32_t *status, bool follows, cudaStream_t st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
+  const int sms = num_sms(dev);
+  // pairs where there are tokens to share and head rows for all of them
+  const bool pair = a.rows > kMostTokens / 2 && w.rows >= (int64_t)kHeadRows * sms;
+  const int rows = pair ? 2 * kHeadRows : kHeadRows;
   ProductShape sh;
   sh.tokens = (int32_t)a.rows;
   sh.head_rows = (int32_t)w.rows;
-  sh.box = a.rows >= kMostTokens ? kMostTokens : (int32_t)((a.rows + 15) & ~15);
+  sh.box = pair || a.rows >= kMostTokens ? kMostTokens : (int32_t)((a.rows + 15) & ~15);
   sh.token_tiles = (sh.tokens + kMostTokens - 1) / kMostTokens;
-  const int64_t tiles = (int64_t)sh.token_tiles * ((w.rows + kHeadRows - 1) / kHeadRows);
+  const int64_t tiles = (int64_t)sh.token_tiles * ((w.rows + rows - 1) / rows);
   sh.steps = (int32_t)((w.cols + kStepCols - 1) / kStepCols);
   sh.groups = mx_groups(w.cols);
   // a block's stages are counted in 31 bits
   if (tiles * ((sh.steps + 3) / 4) > 0x3fffffff) return RANS_ERR_ARG;
   sh.tiles = (int32_t)tiles;
   sh.wait = follows ? 1 : 0;
-  const uint32_t stage = kHeadRows * kStageBytes + (uint32_t)sh.box * kStageBytes +
+  const int box = pair ? kMostTokens / 2 : sh.box;  // tokens in a block's memory
+  const uint32_t stage = kHeadRows * kStageBytes + (uint32_t)box * kStageBytes +
                          2 * kMxTileBytes * (1 + (uint32_t)(sh.box + kMxTileRows - 1) / kMxTileRows);
-  const uint32_t room = (uint32_t)smem_optin(dev) - 2048;  // its static part, alignment
+  // both halves' logits changing places, two buffers each
+  const uint32_t exchange =
+      sh.box <= 32 ? 0 : 4u * kStoreTokens * kHeadRows * (dtype == RANS_LOGITS_F32 ? 4u : 2u);
+  const uint32_t room = (uint32_t)smem_optin(dev) - 2048 - exchange;  // its static part, alignment
   sh.stages = (int32_t)(room / stage < (uint32_t)kMaxStages ? room / stage : kMaxStages);
   if (sh.stages < 2) return RANS_ERR_CUDA;
-  CUtensorMap hm, tm;
+  ProductMaps maps;
   const uint64_t row = (uint64_t)mx_row_bytes(w.cols);
-  int e = encode_rows_map(&hm, w.codes, row, (uint64_t)w.rows, kStageBytes, kHeadRows);
-  if (!e) e = encode_rows_map(&tm, a.codes, row, (uint64_t)a.rows, kStageBytes, (uint32_t)sh.box);
+  int e = encode_rows_map(&maps.head, w.codes, row, (uint64_t)w.rows, kHeadRows);
+  if (!e) e = encode_rows_map(&maps.tokens, a.codes, row, (uint64_t)a.rows, (uint32_t)box);
+  if (!e && pair) {
+    const uint64_t width = (uint64_t)sh.groups * (kMxTileBytes / 4);
+    auto scale_tiles = [](int64_t n) { return (uint64_t)((n + kMxTileRows - 1) / kMxTileRows); };
+    e = encode_words_map(&maps.head_scales, w.scales, width, scale_tiles(w.rows),
+                         2 * kMxTileBytes / 4);
+    if (!e)
+      e = encode_words_map(&maps.token_scales, a.scales, width, scale_tiles(a.rows),
+                           2 * kMxTileBytes / 4);
+  }
   if (e) return e;
-  const uint32_t smem = stage * (uint32_t)sh.stages + 1024;
-  const int sms = num_sms(dev);
+  const uint32_t smem = stage * (uint32_t)sh.stages + 1024 + exchange;
+  const int most = pair ? sms / 2 : sms;
+  const int blocks = (sh.tiles < most ? sh.tiles : most) * (pair ? 2 : 1);
   switch (dtype) {
     case RANS_LOGITS_F32:
-      return launch_o<float>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+      return launch_o<float>(maps, a, w, out, stride, sh, pair, smem, status, blocks, st);
     case RANS_LOGITS_F16:
-      return launch_o<__half>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+      return launch_o<__half>(maps, a, w, out, stride, sh, pair, smem, status, blocks, st);
     default:
-      return launch_o<__nv_bfloat16>(hm, tm, a, w, out, stride, sh, smem, status, sms, st);
+      return launch_o<__nv_bfloat16>(maps, a, w, out, stride, sh, pair, smem, status, blocks, st);
   }
 }
 

@@ -121,10 +121,13 @@ int launch_reorder_states(const rans_state *states, int32_t n, int64_t texts, in
 int encode_tile_map(void *map, const void *base, uint64_t width, uint64_t height,
                     uint64_t depth, uint32_t box_w, uint32_t box_h);
 
-// The same for rows of bytes (16-byte aligned, a multiple of 16 each), in boxes
-// of 128 bytes by box_rows, with the 128-byte swizzle; bytes off the ends read 0.
+// 2-D maps: of rows of bytes (16-byte aligned, a multiple of 16 each) in boxes of 128
+// bytes by box_rows, with the 128-byte swizzle; of rows of 4-byte words in boxes of
+// box_words by one row.  What lies off the ends reads 0.
 int encode_rows_map(void *map, const void *base, uint64_t row_bytes, uint64_t rows,
-                    uint32_t box_bytes, uint32_t box_rows);
+                    uint32_t box_rows);
+int encode_words_map(void *map, const void *base, uint64_t words, uint64_t rows,
+                     uint32_t box_words);
 
 // Whether float latents (staged tensors a and b) can take the tile kernels.
 bool flt_tile_shape_ok(const Geom &g, const void *a, const void *b);

@@ -59,22 +59,38 @@ int encode_tile_map(void *map, const void *base, uint64_t width, uint64_t height
   return r == CUDA_SUCCESS ? RANS_OK : RANS_ERR_CUDA;
 }
 
-int encode_rows_map(void *map, const void *base, uint64_t row_bytes, uint64_t rows,
-                    uint32_t box_bytes, uint32_t box_rows) {
+namespace {
+
+// A 2-D map: rows of `width` elements one after another.
+int encode_2d(void *map, CUtensorMapDataType type, uint64_t element, CUtensorMapSwizzle swizzle,
+              const void *base, uint64_t width, uint64_t height, uint32_t box_w, uint32_t box_h) {
   EncodeTiledFn f = encode_fn();
   if (f == nullptr) return RANS_ERR_CUDA;
-  if ((reinterpret_cast<uintptr_t>(base) & 15) != 0 || row_bytes % 16 != 0 || box_bytes != 128 ||
-      box_rows == 0 || box_rows > 256)
+  if ((reinterpret_cast<uintptr_t>(base) & 15) != 0 || (width * element) % 16 != 0 ||
+      (box_w * element) % 16 != 0 || box_w == 0 || box_w > 256 || box_h == 0 || box_h > 256)
     return RANS_ERR_ARG;
-  const cuuint64_t dims[2] = {row_bytes, rows};
-  const cuuint64_t strides[1] = {row_bytes};
-  const cuuint32_t box[2] = {box_bytes, box_rows};
+  const cuuint64_t dims[2] = {width, height};
+  const cuuint64_t strides[1] = {width * element};
+  const cuuint32_t box[2] = {box_w, box_h};
   const cuuint32_t estr[2] = {1, 1};
-  const CUresult r = f(reinterpret_cast<CUtensorMap *>(map), CU_TENSOR_MAP_DATA_TYPE_UINT8, 2,
-                       const_cast<void *>(base), dims, strides, box, estr,
-                       CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = f(reinterpret_cast<CUtensorMap *>(map), type, 2, const_cast<void *>(base),
+                       dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? RANS_OK : RANS_ERR_CUDA;
+}
+
+}  // namespace
+
+int encode_rows_map(void *map, const void *base, uint64_t row_bytes, uint64_t rows,
+                    uint32_t box_rows) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, CU_TENSOR_MAP_SWIZZLE_128B, base,
+                   row_bytes, rows, 128, box_rows);
+}
+
+int encode_words_map(void *map, const void *base, uint64_t words, uint64_t rows,
+                     uint32_t box_words) {
+  return encode_2d(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 4, CU_TENSOR_MAP_SWIZZLE_NONE, base, words,
+                   rows, box_words, 1);
 }
 
 // Float latents on the tile kernels: tiled W = 32 streams (64-bit format,

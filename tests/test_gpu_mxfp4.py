@@ -169,6 +169,24 @@ def test_product(n, v, k, dtype):
     assert torch.equal(rb.mxfp4_logits(x, w, dtype=dtype), out)
 
 
+@pytest.mark.parametrize("n,k", [(129, 64), (160, 96), (200, 320), (256, 512), (257, 1056),
+                                 (300, 288), (385, 640), (520, 128)])
+def test_product_of_many_head_rows(n, k):
+    """Blocks in pairs (more than 128 tokens, head rows for every SM)."""
+    v = 148 * 128 + 301
+    w, x = head_of(v, k), rows(n, k, F32, seed=6)
+    a = rb.quantize_mxfp4(x)
+    out = wide(n, v, F32, pad=3, offset=1, fill=77.0)
+    status = rb.new_status()
+    rb.mxfp4_logits(a, w, out=out, status=status)
+    rb.check(rb.rans_get_status(status))
+    check_product(out, dense(a), dense(w))
+    assert bool((out.as_strided((n, 3), (v + 3, 1), 1 + v)[:-1] == 77).all())
+    for m in (1, 100, 128):  # the same rows in batches that blocks take alone
+        assert torch.equal(rb.mxfp4_logits(x[:m], w, dtype=F32), out[:m])
+    assert torch.equal(rb.mxfp4_logits(x, w, dtype=BF16), out.bfloat16())
+
+
 def test_rows_do_not_depend_on_their_batch():
     v, k = 1201, 1056
     w = head_of(v, k)
