@@ -105,9 +105,10 @@ __device__ __forceinline__ void commit(uint32_t bar) {
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
 }
-// A barrier in this block or in another one of the cluster.
+// A barrier in this block or in another one of the cluster.  Relaxed: nothing in memory
+// goes with it (a release would wait for the logits' stores).
 __device__ __forceinline__ void arrive_at(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
   uint32_t ok;
@@ -158,7 +159,17 @@ __device__ __forceinline__ bool elected() {
       : "=r"(yes));
   return yes != 0;
 }
-// Eight columns of a warp's 32 accumulator lanes.
+// Columns of a warp's 32 accumulator lanes, 16 or 8.
+__device__ __forceinline__ void load_columns16(float *v, uint32_t at) {
+  uint32_t *u = reinterpret_cast<uint32_t *>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]),
+        "=r"(u[7]), "=r"(u[8]), "=r"(u[9]), "=r"(u[10]), "=r"(u[11]), "=r"(u[12]), "=r"(u[13]),
+        "=r"(u[14]), "=r"(u[15])
+      : "r"(at));
+}
 __device__ __forceinline__ void load_columns(float *v, uint32_t at) {
   uint32_t *u = reinterpret_cast<uint32_t *>(v);
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
@@ -167,24 +178,21 @@ __device__ __forceinline__ void load_columns(float *v, uint32_t at) {
                : "r"(at));
 }
 
+template <typename O>
+struct __align__(4 * sizeof(O)) Four {
+  O x[4];
+};
 // A warp's copy of up to 128 logits of one token from shared memory, four a lane, at
 // any alignment of the result.
 template <typename O>
 __device__ __forceinline__ void store_logits(O *to, const O *from, int valid, int lane) {
-  struct __align__(4 * sizeof(O)) Four {
-    O x[4];
-  };
   const int past = (int)((reinterpret_cast<uintptr_t>(to) / sizeof(O)) & 3);
   const int e = 4 * lane - past;
-  if (past == 0 && valid == kHeadRows) {
-    *reinterpret_cast<Four *>(to + e) = *reinterpret_cast<const Four *>(from + e);
-    return;
-  }
   if (e >= 0 && e + 4 <= valid) {
-    Four f;
+    Four<O> f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) f.x[i] = from[e + i];
-    *reinterpret_cast<Four *>(to + e) = f;
+    *reinterpret_cast<Four<O> *>(to + e) = f;
   } else {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -434,9 +442,12 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (!wait(&done_bar, (uint32_t)n_tile & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float v[HALF];
+      const uint32_t from = tmem + ((uint32_t)quarter << 21) + c0;
 #pragma unroll
-      for (int i = 0; i < HALF; i += 8)
-        if (i < count) load_columns(v + i, tmem + ((uint32_t)quarter << 21) + c0 + i);
+      for (int i = 0; i < HALF; i += 16) {
+        if (i + 8 < count) load_columns16(v + i, from + i);
+        else if (i < count) load_columns(v + i, from + i);
+      }
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
       // (nothing is computed from the registers before that)
 #pragma unroll
@@ -460,6 +471,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         // memory, so that a store takes a token's 128 logits.  (Stored as they come, two
         // bytes a lane, they took longer than the products.)
         const int valid = min(kHeadRows, sh.head_rows - row0);
+        const bool fast = valid == kHeadRows && out_stride % 4 == 0 &&
+                          reinterpret_cast<uintptr_t>(o) % sizeof(Four<O>) == 0;
 #pragma unroll
         for (int p = 0; p < HALF; p += kStoreTokens) {
           if (p < count) {
@@ -468,8 +481,18 @@ __global__ void __launch_bounds__(kProductThreads, 1)
             for (int i = 0; i < kStoreTokens; ++i)
               buf[i * kHeadRows + row] = float_logit<O>(v[p + i]);
             asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-            for (int i = quarter; i < min(kStoreTokens, count - p); i += 4)
-              store_logits(o + (p + i) * out_stride, buf + i * kHeadRows, valid, lane);
+            if (fast && p + kStoreTokens <= count) {
+              Four<O> f[kStoreTokens / 4];
+#pragma unroll
+              for (int i = 0; i < kStoreTokens / 4; ++i)
+                f[i] = *reinterpret_cast<const Four<O> *>(buf + (quarter + 4 * i) * kHeadRows + 4 * lane);
+#pragma unroll
+              for (int i = 0; i < kStoreTokens / 4; ++i)
+                *reinterpret_cast<Four<O> *>(o + (p + quarter + 4 * i) * out_stride + 4 * lane) = f[i];
+            } else {
+              for (int i = quarter; i < min(kStoreTokens, count - p); i += 4)
+                store_logits(o + (p + i) * out_stride, buf + i * kHeadRows, valid, lane);
+            }
             turn ^= 1;
           }
         }
