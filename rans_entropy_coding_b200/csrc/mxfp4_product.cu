@@ -180,27 +180,44 @@ __device__ __forceinline__ void load_columns(float *v, uint32_t at) {
 
 template <typename O>
 struct __align__(4 * sizeof(O)) Four {
-  O x[4];
+  uint32_t x[sizeof(O)];
 };
 // A warp's copy of up to 128 logits of one token from shared memory, four a lane, at
-// any alignment of the result.
+// any alignment of the result: a lane joins the end of the four before its own to
+// the head of its own, and what is left at the two ends goes out singly.
 template <typename O>
 __device__ __forceinline__ void store_logits(O *to, const O *from, int valid, int lane) {
-  const int past = (int)((reinterpret_cast<uintptr_t>(to) / sizeof(O)) & 3);
-  const int e = 4 * lane - past;
-  if (e >= 0 && e + 4 <= valid) {
-    Four<O> f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) f.x[i] = from[e + i];
-    *reinterpret_cast<Four<O> *>(to + e) = f;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (e + i >= 0 && e + i < valid) to[e + i] = from[e + i];
+  if (valid < kHeadRows) {
+    for (int e = lane; e < valid; e += 32) to[e] = from[e];
+    return;
   }
-  // the last lane's end lies before the row's
-  if (lane < past && kHeadRows - past + lane < valid)
-    to[kHeadRows - past + lane] = from[kHeadRows - past + lane];
+  const int past = (int)((reinterpret_cast<uintptr_t>(to) / sizeof(O)) & 3);
+  constexpr int W = (int)sizeof(O);  // words of four
+  uint32_t w[2 * W + 1];
+  *reinterpret_cast<Four<O> *>(w + W) = *reinterpret_cast<const Four<O> *>(from + 4 * lane);
+  if (past == 0) {
+    *reinterpret_cast<Four<O> *>(to + 4 * lane) = *reinterpret_cast<Four<O> *>(w + W);
+    return;
+  }
+  const O end = from[lane < 4 - past ? lane : (kHeadRows - 4 + lane) & (kHeadRows - 1)];
+#pragma unroll
+  for (int i = 0; i < W; ++i) w[i] = __shfl_up_sync(kFull, w[W + i], 1);
+  w[2 * W] = 0;
+  const int bytes = (4 - past) * (int)sizeof(O);
+  if (bytes & 4) {
+#pragma unroll
+    for (int i = 0; i < 2 * W; ++i) w[i] = w[i + 1];
+  }
+  if (bytes & 8) {
+#pragma unroll
+    for (int i = 0; i < W + 1; ++i) w[i] = w[i + 2 < 2 * W + 1 ? i + 2 : 2 * W];
+  }
+  if (bytes & 2) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  }
+  if (lane > 0) *reinterpret_cast<Four<O> *>(to + 4 * lane - past) = *reinterpret_cast<Four<O> *>(w);
+  if (lane < 4) to[lane < 4 - past ? lane : kHeadRows - 4 + lane] = end;
 }
 
 // The tensor maps of a product.
@@ -490,8 +507,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
               for (int i = 0; i < kStoreTokens / 4; ++i)
                 *reinterpret_cast<Four<O> *>(o + (p + quarter + 4 * i) * out_stride + 4 * lane) = f[i];
             } else {
-              for (int i = quarter; i < min(kStoreTokens, count - p); i += 4)
-                store_logits(o + (p + i) * out_stride, buf + i * kHeadRows, valid, lane);
+#pragma unroll
+              for (int i = 0; i < kStoreTokens / 4; ++i)
+                if (p + quarter + 4 * i < count)
+                  store_logits(o + (p + quarter + 4 * i) * out_stride,
+                               buf + (quarter + 4 * i) * kHeadRows, valid, lane);
             }
             turn ^= 1;
           }
