@@ -20,6 +20,8 @@
 // the products, and eight warps take the accumulators: each keeps half of a
 // row's columns in registers, so that the next tile's products start as soon as
 // tensor memory is read, while the logits are still being rounded and stored.
+#include <type_traits>
+
 #include <cuda.h>
 
 #include "cluster.cuh"
@@ -40,6 +42,7 @@ constexpr int kMaxStages = 12;
 constexpr int kEpilogueWarps = 8;
 constexpr int kProductThreads = 128 + 32 * kEpilogueWarps;
 constexpr int kStoreTokens = 16;                // that change places at a time
+constexpr int kPitch = kHeadRows + 4;           // of their rows there
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 256;             // scales behind the accumulators
 constexpr uint32_t kScaleCols = 24;             // of one stage: 8 of the head, 16 of the tokens
@@ -182,44 +185,6 @@ template <typename O>
 struct __align__(4 * sizeof(O)) Four {
   uint32_t x[sizeof(O)];
 };
-// A warp's copy of up to 128 logits of one token from shared memory, four a lane, at
-// any alignment of the result: a lane joins the end of the four before its own to
-// the head of its own, and what is left at the two ends goes out singly.
-template <typename O>
-__device__ __forceinline__ void store_logits(O *to, const O *from, int valid, int lane) {
-  if (valid < kHeadRows) {
-    for (int e = lane; e < valid; e += 32) to[e] = from[e];
-    return;
-  }
-  const int past = (int)((reinterpret_cast<uintptr_t>(to) / sizeof(O)) & 3);
-  constexpr int W = (int)sizeof(O);  // words of four
-  uint32_t w[2 * W + 1];
-  *reinterpret_cast<Four<O> *>(w + W) = *reinterpret_cast<const Four<O> *>(from + 4 * lane);
-  if (past == 0) {
-    *reinterpret_cast<Four<O> *>(to + 4 * lane) = *reinterpret_cast<Four<O> *>(w + W);
-    return;
-  }
-  const O end = from[lane < 4 - past ? lane : (kHeadRows - 4 + lane) & (kHeadRows - 1)];
-#pragma unroll
-  for (int i = 0; i < W; ++i) w[i] = __shfl_up_sync(kFull, w[W + i], 1);
-  w[2 * W] = 0;
-  const int bytes = (4 - past) * (int)sizeof(O);
-  if (bytes & 4) {
-#pragma unroll
-    for (int i = 0; i < 2 * W; ++i) w[i] = w[i + 1];
-  }
-  if (bytes & 8) {
-#pragma unroll
-    for (int i = 0; i < W + 1; ++i) w[i] = w[i + 2 < 2 * W + 1 ? i + 2 : 2 * W];
-  }
-  if (bytes & 2) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
-  }
-  if (lane > 0) *reinterpret_cast<Four<O> *>(to + 4 * lane - past) = *reinterpret_cast<Four<O> *>(w);
-  if (lane < 4) to[lane < 4 - past ? lane : kHeadRows - 4 + lane] = end;
-}
-
 // The tensor maps of a product.
 struct ProductMaps {
   CUtensorMap head, tokens;               // codes
@@ -485,37 +450,76 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         }
       } else {
         // A lane has one logit of many tokens; 16 tokens at a time change places in shared
-        // memory, so that a store takes a token's 128 logits.  (Stored as they come, two
-        // bytes a lane, they took longer than the products.)
+        // memory, so that a store takes a token's 128 logits, four a lane.  (Stored as they
+        // come, two bytes a lane, they took longer than the products.)  Rows of the
+        // result that do not start on a multiple of four lie shifted by as much there, so
+        // that whole fours go to aligned places; the four logits left at the two ends go
+        // singly.
         const int valid = min(kHeadRows, sh.head_rows - row0);
-        const bool fast = valid == kHeadRows && out_stride % 4 == 0 &&
-                          reinterpret_cast<uintptr_t>(o) % sizeof(Four<O>) == 0;
+        const int past0 = (int)((reinterpret_cast<uintptr_t>(o) / sizeof(O)) & 3);
+        const int skew = (int)(out_stride & 3);  // from one token to the next
+        int at[4];
 #pragma unroll
-        for (int p = 0; p < HALF; p += kStoreTokens) {
-          if (p < count) {
-            O *buf = reinterpret_cast<O *>(exchange) + (half * 2 + turn) * kStoreTokens * kHeadRows;
+        for (int i = 0; i < 4; ++i) at[i] = row + ((past0 + i * skew) & 3);
+        // (a warp's tokens are four apart: their rows are shifted alike)
+        const int past = (past0 + quarter * skew) & 3;
+        const int edge = lane < 4 - past ? lane : kHeadRows - 4 + lane;
+        const O *from = reinterpret_cast<const O *>(exchange) + quarter * kPitch;
+        O *to = o + quarter * out_stride;
+        const int64_t four = 4 * out_stride;
+        // A form for what a result allows, so that little code is run: whole fours; fours
+        // between edges; any part of a row.
+        auto pieces = [&](auto form) {
+          constexpr int FORM = decltype(form)::value;
+#pragma unroll
+          for (int p = 0; p < HALF; p += kStoreTokens) {
+            if (p >= count) break;
+            const int shift = (half * 2 + turn) * kStoreTokens * kPitch;
+            O *buf = reinterpret_cast<O *>(exchange) + shift;
 #pragma unroll
             for (int i = 0; i < kStoreTokens; ++i)
-              buf[i * kHeadRows + row] = float_logit<O>(v[p + i]);
+              buf[i * kPitch + at[i & 3]] = float_logit<O>(v[p + i]);
             asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-            if (fast && p + kStoreTokens <= count) {
-              Four<O> f[kStoreTokens / 4];
+            const O *f = from + shift;
+            if constexpr (FORM == 0) {
+              Four<O> x[kStoreTokens / 4];
 #pragma unroll
               for (int i = 0; i < kStoreTokens / 4; ++i)
-                f[i] = *reinterpret_cast<const Four<O> *>(buf + (quarter + 4 * i) * kHeadRows + 4 * lane);
+                x[i] = *reinterpret_cast<const Four<O> *>(f + 4 * i * kPitch + 4 * lane);
 #pragma unroll
-              for (int i = 0; i < kStoreTokens / 4; ++i)
-                *reinterpret_cast<Four<O> *>(o + (p + quarter + 4 * i) * out_stride + 4 * lane) = f[i];
+              for (int i = 0; i < kStoreTokens / 4; ++i, to += four)
+                *reinterpret_cast<Four<O> *>(to + 4 * lane) = x[i];
             } else {
+              const int rows = min(kStoreTokens / 4, (count - p - quarter + 3) >> 2);
+              if constexpr (FORM == 1) {
+                Four<O> x[kStoreTokens / 4];
+                O one[kStoreTokens / 4];
 #pragma unroll
-              for (int i = 0; i < kStoreTokens / 4; ++i)
-                if (p + quarter + 4 * i < count)
-                  store_logits(o + (p + quarter + 4 * i) * out_stride,
-                               buf + (quarter + 4 * i) * kHeadRows, valid, lane);
+                for (int i = 0; i < kStoreTokens / 4; ++i) {
+                  x[i] = *reinterpret_cast<const Four<O> *>(f + 4 * i * kPitch + 4 * lane);
+                  one[i] = f[4 * i * kPitch + past + (edge & (kHeadRows - 1))];
+                }
+#pragma unroll
+                for (int i = 0; i < kStoreTokens / 4; ++i, to += four)
+                  if (i < rows) {
+                    if (past == 0 || lane > 0)
+                      *reinterpret_cast<Four<O> *>(to + 4 * lane - past) = x[i];
+                    if (past && lane < 4) to[edge] = one[i];
+                  }
+              } else {
+#pragma unroll 1
+                for (int i = 0; i < kStoreTokens / 4; ++i, to += four)
+                  for (int e = lane; e < valid && i < rows; e += 32)
+                    to[e] = f[4 * i * kPitch + past + e];
+              }
             }
             turn ^= 1;
           }
-        }
+        };
+        if (valid < kHeadRows) pieces(std::integral_constant<int, 2>());
+        else if (past0 != 0 || skew != 0 || count % kStoreTokens != 0)
+          pieces(std::integral_constant<int, 1>());
+        else pieces(std::integral_constant<int, 0>());
       }
     }
   }
@@ -608,7 +612,7 @@ int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, in
                          2 * kMxTileBytes * (1 + (uint32_t)(sh.box + kMxTileRows - 1) / kMxTileRows);
   // both halves' logits changing places, two buffers each
   const uint32_t exchange =
-      sh.box <= 32 ? 0 : 4u * kStoreTokens * kHeadRows * (dtype == RANS_LOGITS_F32 ? 4u : 2u);
+      sh.box <= 32 ? 0 : 4u * kStoreTokens * kPitch * (dtype == RANS_LOGITS_F32 ? 4u : 2u);
   const uint32_t room = (uint32_t)smem_optin(dev) - 2048 - exchange;  // its static part, alignment
   sh.stages = (int32_t)(room / stage < (uint32_t)kMaxStages ? room / stage : kMaxStages);
   if (sh.stages < 2) return RANS_ERR_CUDA;
