@@ -8,6 +8,7 @@ torch operations).  Calls run on the tensors' device, on ``stream`` or that
 device's current stream; nothing here takes part in autograd.
 """
 import ctypes
+import functools
 import math
 import struct
 
@@ -20,9 +21,11 @@ from .mxfp4 import _word
 MAX_BEAMS = 64
 MAX_CONTINUATIONS = 128
 MAX_STATES = 4096
-_pack_state = struct.Struct("@Pqqqii").pack
+_pack_address = struct.Struct("@P").pack
+_pack_layout = struct.Struct("@qqqii").pack
 _pack_beams = struct.Struct("@qiiPiifiPPPPPPPPPPP").pack
 assert struct.calcsize("@Pqqqii") == ctypes.sizeof(L.rans_state)
+assert struct.calcsize("@P") + struct.calcsize("@qqqii") == struct.calcsize("@Pqqqii")
 assert struct.calcsize("@qiiPiifiPPPPPPPPPPP") == ctypes.sizeof(L.rans_beams)
 
 
@@ -91,35 +94,36 @@ def rans_reorder_states(states, parents, lengths, axis, status, stream=None):
     return result
 
 
-def _state(x, rows, axis, dev):
-    """A rans_state's bytes."""
-    if not isinstance(x, torch.Tensor) or x.get_device() != dev or x.dim() < 1 or \
-            x.shape[0] != rows:
-        raise ValueError("states: tensors of %d rows on cuda:%d" % (rows, dev))
-    shape, step, e = x.shape, x.stride(0), x.element_size()
-    if not x.is_contiguous():
-        if rows > 0 and not x[0].is_contiguous():
-            raise ValueError("states: each row must be contiguous")
-    row = 1
-    for d in shape[1:]:
-        row *= d
+def _state(x, rows, axis, dev, known):
+    """A rans_state's bytes.  known: of this call's shapes so far, all but the address."""
+    if not isinstance(x, torch.Tensor) or x.get_device() != dev:
+        raise ValueError("states: CUDA tensors on cuda:%d" % dev)
+    key = (x.shape, x.stride(), x.element_size(), axis)
+    rest = known.get(key)
+    if rest is None:
+        rest = known[key] = _layout(x, rows, axis)
+    return _pack_address(x.data_ptr()) + rest
+
+
+def _layout(x, rows, axis):
+    shape, e = x.shape, x.element_size()
+    if x.dim() < 1 or shape[0] != rows:
+        raise ValueError("states: tensors of %d rows" % rows)
+    if not x.is_contiguous() and rows > 0 and not x[0].is_contiguous():
+        raise ValueError("states: each row must be contiguous")
+    step, row = x.stride(0), math.prod(shape[1:])
     if rows > 1 and step < row:
         raise ValueError("states: rows must not overlap")
-    if axis is None:
-        return _pack_state(x.data_ptr(), step * e, row * e, 1, 1, row * e) if row * e < 1 << 31 \
-            else _pack_state(x.data_ptr(), step * e, row * e, row, 1, e)
+    if axis is None:  # one piece, in positions of a size that the library counts
+        return _pack_layout(step * e, row * e, 1, 1, row * e) if row * e < 1 << 31 else \
+            _pack_layout(step * e, row * e, row, 1, e)
     if not 1 <= axis < len(shape):
         raise ValueError("axis: 1 to %d for a state of shape %s" % (len(shape) - 1, tuple(shape)))
-    outer = inner = 1
-    for d in shape[1:axis]:
-        outer *= d
-    for d in shape[axis + 1:]:
-        inner *= d
+    outer, inner = math.prod(shape[1:axis]), math.prod(shape[axis + 1:])
     if outer >= 1 << 31 or inner * e >= 1 << 31:
         raise ValueError("states: a shape of %s is too large around axis %d" % (
             tuple(shape), axis))
-    return _pack_state(x.data_ptr(), step * e, shape[axis] * inner * e, shape[axis], outer,
-                       inner * e)
+    return _pack_layout(step * e, shape[axis] * inner * e, shape[axis], outer, inner * e)
 
 
 def _reorder(dev, states, parents, lengths, axis, status):
@@ -135,7 +139,8 @@ def _reorder(dev, states, parents, lengths, axis, status):
     one = axis is None or isinstance(axis, int)
     if not one and len(axis) != len(states):
         raise ValueError("axis: %d for %d states" % (len(axis), len(states)))
-    packed = b"".join([_state(x, t * k, axis if one else axis[i], dev)
+    known = {}
+    packed = b"".join([_state(x, t * k, axis if one else axis[i], dev, known)
                        for i, x in enumerate(states)])
     return L.lib().rans_reorder_states(packed, len(states), t, k, p, n, _word(status, dev),
                                        T._raw_stream(dev))
@@ -156,14 +161,28 @@ def beam_select(logits, scores, beams, count=None, adjust=None, status=None, str
     if count is None:
         count = 2 * beams
     t = _shape(rows, beams, count)
-    with T._place(rows[0], stream):
-        out = logits.new_empty((3, t, count), dtype=torch.int32)
-        best, tokens, parents = out[0].view(torch.float32), out[1], out[2]
-        ws = logits.new_empty(L.lib().rans_beam_workspace_bytes(rows[3], rows[1], rows[2], count),
-                              dtype=torch.uint8)
-        L.check(_select(rows, logits, adjust, scores, beams, count, best, tokens, parents, ws,
-                        status), "beam_select")
+    dev, n = rows[:2]
+    if not isinstance(scores, torch.Tensor) or scores.numel() != n:
+        raise ValueError("scores: a float32 tensor of %d elements" % n)
+    c = T._tensor(scores, torch.float32, None, dev, "scores")
+    with T._place(dev, stream):
+        best = scores.new_empty((t, count))
+        tokens = scores.new_empty((t, count), dtype=torch.int32)
+        parents = scores.new_empty((t, count), dtype=torch.int32)
+        size = _workspace(rows[3], n, rows[2], count, dev)
+        ws = scores.new_empty(size, dtype=torch.uint8)
+        word = None if status is None else T._status(status, dev).data_ptr()
+        L.check(L.lib().rans_beam_select(
+            T._packed(logits, rows), T._ref(adjust, rows), c, beams, count, best.data_ptr(),
+            tokens.data_ptr(), parents.data_ptr(), ws.data_ptr(), size, word,
+            T._raw_stream(dev)), "beam_select")
     return best, tokens, parents
+
+
+@functools.lru_cache(maxsize=256)
+def _workspace(code, rows, vocab, count, dev):
+    """Bytes for sizes on a device (the current one)."""
+    return L.lib().rans_beam_workspace_bytes(code, rows, vocab, count)
 
 
 def reorder_states(states, parents, lengths=None, axis=None, status=None, stream=None):

@@ -632,8 +632,8 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
 }
 
-// Parts of a row: twice as many as long as there are blocks to spare and each
-// keeps a tile.
+// Parts of a row: as many as there are blocks at once for (four an SM), of a tile at
+// least.
 struct BeamShape {
   int parts, slice;
 };
@@ -641,8 +641,8 @@ template <typename T>
 BeamShape beam_shape(int64_t rows, int vocab, int sms) {
   constexpr int kTile = kBeamThreads * kBeamVecs * VecOf<T>::N;
   const int tiles = (vocab + kTile - 1) / kTile;
-  int parts = 1;
-  while (rows * parts * 2 <= 4 * sms && parts * 2 <= tiles) parts *= 2;
+  const int64_t most = rows > 0 ? 4 * (int64_t)sms / rows : 1;
+  const int parts = most < 1 ? 1 : most < tiles ? (int)most : tiles;
   const int per = (tiles + parts - 1) / parts;
   return {(tiles + per - 1) / per, per * kTile};
 }

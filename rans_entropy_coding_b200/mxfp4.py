@@ -58,18 +58,29 @@ class Mxfp4:
         if scales.numel() != need:
             raise ValueError("scales: %d bytes for %d rows of %d columns, not %d" % (
                 need, rows, cols, scales.numel()))
-        c, s = codes.data_ptr(), scales.data_ptr()
-        if (c | s) & 15:
+        if (codes.data_ptr() | scales.data_ptr()) & 15:
             raise ValueError("codes and scales: aligned to 16 bytes")
+        self._set(codes, scales, rows, cols, dev)
+
+    def _set(self, codes, scales, rows, cols, dev):
         self.codes, self.scales, self.rows, self.cols, self.dev = codes, scales, rows, cols, dev
-        self._c = _pack(c, s, rows, cols)
+        self._c = _pack(codes.data_ptr(), scales.data_ptr(), rows, cols)
+        return self
 
     @classmethod
     def empty(cls, rows, cols, device="cuda"):
         """Room for rows that a quantisation writes."""
+        if not 1 <= cols <= T.MAX_VOCAB or not 0 <= rows <= _MAX_ROWS:
+            raise ValueError("1 to %d columns, up to %d rows" % (T.MAX_VOCAB, _MAX_ROWS))
+        return cls._room(rows, cols, torch.empty(0, device=device))
+
+    @classmethod
+    def _room(cls, rows, cols, like):
+        """Room on a tensor's device, of sizes that are known to be good."""
         row, scales = _sizes(rows, cols)
-        return cls(torch.empty((rows, row), dtype=torch.uint8, device=device),
-                   torch.empty(scales, dtype=torch.uint8, device=device), cols)
+        return cls.__new__(cls)._set(like.new_empty((rows, row), dtype=torch.uint8),
+                                     like.new_empty(scales, dtype=torch.uint8), rows, cols,
+                                     T._device(like, "device"))
 
     @classmethod
     def from_rows(cls, codes, scales, cols=None):
@@ -92,16 +103,23 @@ class Mxfp4:
 
     def values(self, dtype=torch.float32, out=None, stream=None):
         """What the codes stand for, [rows, cols], rounded once to `dtype`."""
-        given = out is not None
         with T._place(self.dev, stream):
-            if not given:
-                if dtype not in T._LOGITS_CODE:
-                    raise ValueError("dtype: float32, float16 or bfloat16, not %s" % dtype)
-                out = torch.empty((self.rows, self.cols), dtype=dtype, device=self.codes.device)
+            if out is None:
+                code = _code(dtype)
+                out = self.codes.new_empty((self.rows, self.cols), dtype=dtype)
+                L.check(L.lib().rans_mxfp4_values(self._c, out.data_ptr(), code, self.cols,
+                                                  T._raw_stream(self.dev)), "mxfp4_values")
+                return out
             L.check(_values(self, out), "mxfp4_values")
-        if given:
-            T._written(out)
+        T._written(out)
         return out
+
+
+def _code(dtype):
+    code = T._LOGITS_CODE.get(dtype)
+    if code is None:
+        raise ValueError("dtype: float32, float16 or bfloat16, not %s" % dtype)
+    return code
 
 
 # ---------------------------------------------------------- C entry points --
@@ -213,7 +231,7 @@ def quantize_mxfp4(x, out=None, stream=None):
     given = out is not None
     with T._place(rows[0], stream):
         if not given:
-            out = Mxfp4.empty(rows[1], rows[2], x.device)
+            out = Mxfp4._room(rows[1], rows[2], x)
         L.check(_quantize(rows, x, out), "quantize_mxfp4")
     if given:
         T._written(out.codes, out.scales)
@@ -228,25 +246,29 @@ def mxfp4_logits(hidden, head, out=None, dtype=None, status=None, stream=None):
     the same, bit for bit, in every batch, which is what TokenCoder asks for.
     """
     given = out is not None
-    if isinstance(hidden, Mxfp4):
-        dev, n = hidden.dev, hidden.rows
-        _same(dev, hidden.cols, head)
-        with T._place(dev, stream):
-            if not given:
-                out = torch.empty((n, head.rows), dtype=dtype or torch.float32,
-                                  device=hidden.codes.device)
-            L.check(_product(hidden, head, out, status), "mxfp4_logits")
-    else:
-        rows = T._rows(hidden, "hidden")
-        dev, n, k = rows[:3]
-        _same(dev, k, head)
-        with T._place(dev, stream):
-            if not given:
-                out = hidden.new_empty((n, head.rows), dtype=dtype)
+    quantised = isinstance(hidden, Mxfp4)
+    rows = (hidden.dev, hidden.rows, hidden.cols) if quantised else T._rows(hidden, "hidden")
+    dev, n, k = rows[:3]
+    _same(dev, k, head)
+    with T._place(dev, stream):
+        if given:
+            code, step = _result(dev, n, head, out)
+        else:
+            dtype = dtype or (torch.float32 if quantised else hidden.dtype)
+            code, step = _code(dtype), head.rows
+            out = head.codes.new_empty((n, step), dtype=dtype)
+        word = None if status is None else T._status(status, dev).data_ptr()
+        if quantised:
+            done = L.lib().rans_mxfp4_product(hidden._c, head._c, out.data_ptr(), code, step, word,
+                                              T._raw_stream(dev))
+        else:
             row, scales = _sizes(n, k)
+            size = ((n * row + 255) & ~255) + scales
             # (torch's blocks are aligned to 512 bytes)
-            ws = hidden.new_empty(((n * row + 255) & ~255) + scales, dtype=torch.uint8)
-            L.check(_logits(rows, hidden, head, out, ws, status), "mxfp4_logits")
+            ws = head.codes.new_empty(size)
+            done = L.lib().rans_mxfp4_logits(T._packed(hidden, rows), head._c, out.data_ptr(), code,
+                                             step, ws.data_ptr(), size, word, T._raw_stream(dev))
+        L.check(done, "mxfp4_logits")
     if given:
         T._written(out)
     return out
