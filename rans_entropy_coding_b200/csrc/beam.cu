@@ -34,9 +34,11 @@ constexpr int kBeamThreads = 256;
 constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamVecs = 4;      // vectors of 16 bytes a lane has in a tile
 constexpr int kBeamList = 1024;   // tokens kept by a block
+constexpr int kRanked = 256;      // of them, that are thinned out by their ranks
 constexpr int kNearLanes = 4;     // most lanes of a warp whose vectors near the top are added singly
 constexpr int kMergeThreads = 256;
 constexpr int kMergeList = 512;
+constexpr int kMergeItems = 4;   // candidates of a thread in registers
 static_assert(RANS_MAX_CONTINUATIONS <= kBeamThreads, "a threshold needs that many maxima");
 
 // What a block says of its part of a row.
@@ -78,8 +80,9 @@ __device__ __forceinline__ int block_sum(int x, int *words) {
 template <typename F>
 __device__ __forceinline__ F threshold(F mine, int count, F most, F lowest) {
   F lo = most, hi = most, d = 1;
+  if (__syncthreads_count(mine >= lowest) < count) return lowest;
   int n = __syncthreads_count(mine >= most);
-  if (n >= count) return most > lowest ? most : lowest;
+  if (n >= count) return most;
   for (;;) {
     lo = most - d;
     if (!(lo > lowest)) return lowest;
@@ -461,8 +464,19 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
   n = block_sum(above, words);
   uint32_t key = key_of(cut);
   int last = in.vocab;
-  if (!whole || n > 2 * count) {
-    // more than the merge has room for (ties, mostly): exactly the best `count`
+  const bool ranked = whole && n > 2 * count && listed <= kRanked;
+  if (ranked) {
+    // a few more than the merge has room for: their ranks
+    for (int i = tid; i < listed; i += kBeamThreads) {
+      const Candidate c = list[i];
+      int rank = 0;
+      for (int j = 0; j < listed; ++j)
+        rank += list[j].x > c.x || (list[j].x == c.x && list[j].token < c.token);
+      if (rank < count) out[rank] = c;
+    }
+    if (tid == 0) emitted = min(count, listed);
+  } else if (!whole || n > 2 * count) {
+    // many more (ties, mostly): exactly the best `count`
     // body(key, token) for the list, or for the part's tokens up to `place`
     auto each = [&](int place, auto body) {
       if (whole) {
@@ -495,7 +509,8 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
     if (x > kNegInf && (v > key || (v == key && token <= last)))
       out[atomicAdd(&emitted, 1)] = Candidate{x, token};
   };
-  if (whole) {
+  if (ranked) {
+  } else if (whole) {
     for (int i = tid; i < listed; i += kBeamThreads) emit(list[i].x, list[i].token);
   } else {
     walk([&](int u_lo, int u_hi) {
@@ -529,6 +544,20 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int64_t t = blockIdx.x;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (tid == 0) listed = 0;
+  // Candidates that fit the block's registers are asked for at once, with all else.
+  const int slots = 2 * count, items = beams * parts * slots;
+  const int64_t first = t * beams * parts;
+  const bool few = items <= kMergeItems * kMergeThreads;
+  Candidate kept[kMergeItems];
+  int parts_n[kMergeItems];
+#pragma unroll
+  for (int k = 0; k < kMergeItems; ++k) {
+    const int i = tid + k * kMergeThreads;
+    if (few && i < items) {
+      kept[k] = cand_in[first * slots + i];
+      parts_n[k] = part_in[first + i / slots].n;
+    }
+  }
   // a warp per beam
   for (int b = wid; b < beams; b += kMergeThreads / 32) {
     const int64_t r = t * beams + b;
@@ -558,15 +587,19 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
   __syncthreads();
   // body(total, place) for all candidates of the text
-  const int slots = 2 * count, items = beams * parts * slots;
   auto each = [&](auto body) {
-    for (int i = tid; i < items; i += kMergeThreads) {
+    auto one = [&](int i, int n, const Candidate &x) {
       const int p = i / slots, b = p / parts;
-      if (i - p * slots >= part_in[t * beams * parts + p].n) continue;
       const double c = base[b];
-      if (c == -__builtin_huge_val()) continue;
-      const Candidate x = cand_in[t * beams * parts * slots + i];
-      body((double)x.x + c, b * vocab + x.token);
+      if (i - p * slots < n && c > -__builtin_huge_val()) body((double)x.x + c, b * vocab + x.token);
+    };
+    if (few) {
+#pragma unroll
+      for (int k = 0; k < kMergeItems; ++k)
+        if (tid + k * kMergeThreads < items) one(tid + k * kMergeThreads, parts_n[k], kept[k]);
+    } else {
+      for (int i = tid; i < items; i += kMergeThreads)
+        one(i, part_in[first + i / slots].n, cand_in[first * slots + i]);
     }
   };
   double best = -__builtin_huge_val();
