@@ -275,7 +275,7 @@ RANS_API const char *rans_status_string(int status) {
   }
 }
 
-RANS_API int rans_version(void) { return 200; }
+RANS_API int rans_version(void) { return 300; }
 
 RANS_API int rans_gaussian_lengths(const float *scales, int32_t K, double tail_mass,
                                    int32_t *cdf_lengths, int32_t *offsets, void *stream) {

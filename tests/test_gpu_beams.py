@@ -38,6 +38,10 @@ def exact_rows(x, o):
     return out
 
 
+def host_rows(x):
+    return numpy_rows(x).astype(np.float64)
+
+
 def totals(x, scores):
     with np.errstate(all="ignore"):
         m = x.max(1, keepdims=True)
@@ -163,6 +167,39 @@ def test_ties(v, dtype):
     none = rb.beam_select(x, s, beams, count,
                           rb.LogitAdjust(mask=rb.pack_mask(torch.zeros_like(allowed))))
     assert bool((none[0] == -math.inf).all()) and bool((none[2] == -1).all())
+
+
+def test_ties_of_zeros_and_under_penalties():
+    """Zeros of both signs are equal; more equal logits than a block keeps, some of
+    them touched; a mask that leaves single tokens in whole tiles of nothing."""
+    v, beams, count = 30000, 2, 10
+    x = torch.zeros(beams, v, device="cuda")
+    x[:, ::2] = -0.0
+    s = torch.tensor([-1.0, -1.0], device="cuda")
+    best, tokens, parents = rb.beam_select(x, s, beams, count)
+    assert tokens[0].tolist() == list(range(count)) and parents[0].tolist() == [0] * count
+    n = torch.zeros(beams, dtype=torch.int64, device="cuda")
+    history = torch.tensor([0, 3, 5, 29999], dtype=torch.int32, device="cuda")
+    for bias, want in ((1.0, [4, 29998, 0, 1]), (-1.0, [0, 1, 2, 3])):
+        ids = torch.tensor([4, 29998], dtype=torch.int32, device="cuda")
+        values = torch.full((2,), bias, device="cuda")
+        rules = rb.LogitAdjust(history=(history[:0], n, n), bias=(ids, values, n, n + 2))
+        tokens = rb.beam_select(x[:1], s[:1], 1, 4, rb.LogitAdjust(
+            bias=(ids, values, n[:1], n[:1] + 2)))[1]
+        assert tokens[0].tolist() == want
+        assert rb.beam_select(x, s, beams, 2, rules)[1][0].tolist() == (
+            [4, 29998] if bias > 0 else [0, 1])
+    tokens = rb.beam_select(x[:1], s[:1], 1, 4, rb.LogitAdjust(
+        presence=1.0, history=(history, n[:1], n[:1] + 4)))[1]
+    assert tokens[0].tolist() == [1, 2, 4, 6]
+    allowed = torch.zeros(beams, v, dtype=torch.bool, device="cuda")
+    for at in (9000, 9777, 17000, 29000):
+        allowed[0, at] = True
+    x[0, 17000] = 2.0
+    got = rb.beam_select(x, s, beams, 6, rb.LogitAdjust(mask=rb.pack_mask(allowed)))
+    assert got[1][0].tolist() == [17000, 9000, 9777, 29000, -1, -1]
+    check_selection(got, totals(np.where(allowed.cpu().numpy(), host_rows(x), -np.inf),
+                                np.array([-1.0, -np.inf])), beams, 6)
 
 
 def test_low_values_and_infinities():
