@@ -193,6 +193,23 @@ __device__ __forceinline__ float vector_max(const uint4 &q) {
   }
 }
 
+// A vector with -inf in the places whose bit is 0.
+template <typename T>
+__device__ __forceinline__ uint4 keep_bits(const uint4 &q, uint32_t ok) {
+  uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 2) {
+      constexpr uint32_t kDead = std::is_same<T, __half>::value ? 0xfc00fc00u : 0xff80ff80u;
+      const uint32_t b = ok >> (2 * i) & 3u, m = ((b | b << 15) & 0x00010001u) * 0xffffu;
+      w[i] = (w[i] & m) | (kDead & ~m);
+    } else {
+      w[i] = ok >> i & 1 ? w[i] : 0xff800000u;
+    }
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 template <typename T, bool ADJ>
 __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
     beam_rows_kernel(rans_logits in, rans_adjust adj, const float *scores, int count, int parts,
@@ -313,25 +330,15 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
     return __uint_as_float(k & 0x80000000u ? k & 0x7fffffffu : ~k);
   };
 
-  // A warp's tile.  ALL: every element counts.  SCALED: inv is not 1.
+  // A warp's tile, -inf where nothing counts.  SCALED: inv is not 1.
   int round = 0;
-  auto tile = [&](auto every, auto scaled, const uint4 (&q)[kBeamVecs], int u, int u_hi) {
-    constexpr bool ALL = decltype(every)::value, SCALED = decltype(scaled)::value;
-    uint32_t ok[kBeamVecs];
+  auto tile = [&](auto scaled, const uint4 (&q)[kBeamVecs], int u, int u_hi) {
+    constexpr bool SCALED = decltype(scaled)::value;
     float m = kNegInf, top_of[kBeamVecs];
 #pragma unroll
     for (int k = 0; k < kBeamVecs; ++k) {
-      if constexpr (ALL) {
-        // compared as it lies in memory: x is monotonous in z
-        top_of[k] = __fmul_rn(vector_max<T>(q[k]), inv);
-      } else {
-        ok[k] = ok_at(u + 32 * N * k, u_hi);
-        float x[N];
-        logits_of(q[k], ok[k], x);
-        top_of[k] = x[0];
-#pragma unroll
-        for (int i = 1; i < N; ++i) top_of[k] = max_nan(top_of[k], x[i]);
-      }
+      // compared as it lies in memory: x is monotonous in z
+      top_of[k] = __fmul_rn(vector_max<T>(q[k]), inv);
       m = max_nan(m, top_of[k]);
     }
     mine = max_nan(mine, m);
@@ -356,14 +363,10 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
 #pragma unroll
     for (int k = 0; k < kBeamVecs; ++k) {
       float x[N];
-      if constexpr (ALL) {
-        unpack16(q[k], x, T());
-        if constexpr (SCALED) {
+      unpack16(q[k], x, T());
+      if constexpr (SCALED) {
 #pragma unroll
-          for (int i = 0; i < N; ++i) x[i] = __fmul_rn(x[i], inv);
-        }
-      } else {
-        logits_of(q[k], ok[k], x);
+        for (int i = 0; i < N; ++i) x[i] = __fmul_rn(x[i], inv);
       }
       uint64_t e[N / 2];
 #pragma unroll
@@ -389,8 +392,8 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
       const int l = __ffs(lanes) - 1;
       const uint32_t add_it = __shfl_sync(0xffffffffu, sums, l);
       const int k = lane / N, at = u + (l - lane) * N + 32 * N * k + lane % N;
-      if (k < kBeamVecs &&
-          (ALL || (at < u_hi && (!ADJ || ok_bits[(at - table_at) >> 5] >> ((at - table_at) & 31) & 1)))) {
+      if (k < kBeamVecs && at < u_hi &&
+          (!ADJ || ok_bits[(at - table_at) >> 5] >> ((at - table_at) & 31) & 1)) {
         const float x = __fmul_rn(logit_float(row.at0[at]), inv);
         if (add_it >> k & 1) {
           raise(x);
@@ -419,9 +422,13 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
 #pragma unroll
       for (int k = 0; k < kBeamVecs; ++k) q[k] = next[k];
       if (base + kTile < u_hi) fetch(u + kTile, base + 2 * kTile);
-      if (ADJ || base + kTile > u_hi) tile(std::false_type(), std::true_type(), q, u, u_hi);
-      else if (inv != 1.0f) tile(std::true_type(), std::true_type(), q, u, u_hi);
-      else tile(std::true_type(), std::false_type(), q, u, u_hi);
+      if (ADJ || base + kTile > u_hi) {
+#pragma unroll
+        for (int k = 0; k < kBeamVecs; ++k)
+          q[k] = keep_bits<T>(q[k], ok_at(u + 32 * N * k, u_hi));
+      }
+      if (inv != 1.0f) tile(std::true_type(), q, u, u_hi);
+      else tile(std::false_type(), q, u, u_hi);
     }
   }, [&] {
     // their own maximum, and their sum in units of 2^-40 of it
