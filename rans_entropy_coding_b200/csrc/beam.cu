@@ -44,6 +44,7 @@ constexpr int kBeamVecs = 4;      // vectors of 16 bytes a lane has in a tile
 constexpr int kBeamList = 1024;   // tokens kept by a block
 constexpr int kRanked = 256;      // of them, that are thinned out by their ranks
 constexpr int kNearLanes = 4;     // most lanes of a warp whose vectors near the top are added singly
+constexpr int kPlainBlocks = 4, kTableBlocks = 3;  // of an SM at once
 constexpr int kMergeThreads = 256;
 constexpr int kMergeList = 512;
 constexpr int kMergeItems = 4;   // candidates of a thread in registers
@@ -210,15 +211,20 @@ __device__ __forceinline__ uint4 keep_bits(const uint4 &q, uint32_t ok) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-template <typename T, bool ADJ>
-__global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
+// ADJ: kMask with a mask alone, kTables with penalties or biases, whose tables leave shared
+// memory for three blocks an SM, with more registers each (256 x 131072 f16 at odd
+// addresses: 70 us with tables, 56 with a mask alone, 45 with neither; three blocks
+// for a mask took 71, four for tables 80).
+enum { kPlain, kMask, kTables };
+template <typename T, int ADJ>
+__global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : kPlainBlocks)
     beam_rows_kernel(rans_logits in, rans_adjust adj, const float *scores, int count, int parts,
                      int slice, Part *part_out, Candidate *cand_out) {
   extern __shared__ __align__(16) unsigned char smem[];
   constexpr int N = VecOf<T>::N;
   constexpr int kWarpTile = 32 * N * kBeamVecs;
   TouchTable &table = *reinterpret_cast<TouchTable *>(smem);
-  uint32_t *ok_bits = reinterpret_cast<uint32_t *>(smem + (ADJ ? sizeof(TouchTable) : 0));
+  uint32_t *ok_bits = reinterpret_cast<uint32_t *>(smem + (ADJ == kTables ? sizeof(TouchTable) : 0));
   __shared__ Candidate list[kBeamList];
   __shared__ int listed, emitted, words[kBeamWarps];
   __shared__ double sums[kBeamWarps];
@@ -247,7 +253,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ ? 3 : 4)
     return;
   }
 
-  const bool touch = ADJ && a.touches();
+  const bool touch = ADJ == kTables && a.touches();
   int table_at = -1, span = 1 << 30;
   bool dense = false;
   auto need_table = [&](int u_lo) {
@@ -681,34 +687,51 @@ __global__ void __launch_bounds__(kMergeThreads)
   }
 }
 
-// Parts of a row: as many as there are blocks at once for (four an SM), of a tile at
-// least.
+// Parts of a row, of so many tiles each that the blocks, as many at once as an SM
+// takes, are done soonest; a block has `extra` tiles' worth of work besides (its first
+// threshold, a table of touched tokens).
 struct BeamShape {
   int parts, slice;
 };
+constexpr int kMostParts = 64;
 template <typename T>
-BeamShape beam_shape(int64_t rows, int vocab, int sms) {
+BeamShape beam_shape(int64_t rows, int vocab, int sms, bool tables) {
   constexpr int kTile = kBeamThreads * kBeamVecs * VecOf<T>::N;
-  const int tiles = (vocab + kTile - 1) / kTile;
-  const int64_t most = rows > 0 ? 4 * (int64_t)sms / rows : 1;
-  const int parts = most < 1 ? 1 : most < tiles ? (int)most : tiles;
-  const int per = (tiles + parts - 1) / parts;
-  return {(tiles + per - 1) / per, per * kTile};
+  const int tiles = (vocab + kTile - 1) / kTile, extra = tables ? 8 : 1;
+  const int64_t slots = (int64_t)sms * (tables ? kTableBlocks : kPlainBlocks);
+  int best = tiles;
+  int64_t least = -1;
+  for (int p = 1; p <= kMostParts && p <= tiles; ++p) {
+    const int per = (tiles + p - 1) / p;
+    const int64_t time = (rows * ((tiles + per - 1) / per) + slots - 1) / slots * (per + extra);
+    if (least < 0 || time < least) {
+      least = time;
+      best = per;
+    }
+  }
+  return {(tiles + best - 1) / best, best * kTile};
 }
-BeamShape beam_shape(int dtype, int64_t rows, int vocab, int sms) {
-  return dtype == RANS_LOGITS_F32 ? beam_shape<float>(rows, vocab, sms)
-                                  : beam_shape<__half>(rows, vocab, sms);
+BeamShape beam_shape(int dtype, int64_t rows, int vocab, int sms, bool tables) {
+  return dtype == RANS_LOGITS_F32 ? beam_shape<float>(rows, vocab, sms, tables)
+                                  : beam_shape<__half>(rows, vocab, sms, tables);
 }
 uint64_t part_bytes(int64_t rows, int parts) {
   return ((uint64_t)rows * (uint64_t)parts * sizeof(Part) + 255) & ~255ull;
 }
 
+bool has_tables(const rans_adjust &adj) {
+  return adj.history != nullptr || adj.bias_ids != nullptr;
+}
+
 template <typename T>
 int launch_rows(const rans_logits &in, const rans_adjust &adj, const float *scores, int count,
                 const BeamShape &sh, Part *parts, Candidate *cands, cudaStream_t st) {
-  const bool adjusted = adj.history != nullptr || adj.bias_ids != nullptr || adj.mask;
-  auto kern = adjusted ? beam_rows_kernel<T, true> : beam_rows_kernel<T, false>;
-  const uint32_t smem = adjusted ? (uint32_t)sizeof(TouchTable) + kHashSpan / 8 : 0u;
+  const bool tables = has_tables(adj), adjusted = tables || adj.mask;
+  auto kern = tables     ? beam_rows_kernel<T, kTables>
+              : adjusted ? beam_rows_kernel<T, kMask>
+                         : beam_rows_kernel<T, kPlain>;
+  const uint32_t smem =
+      (tables ? (uint32_t)sizeof(TouchTable) : 0u) + (adjusted ? kHashSpan / 8 : 0u);
   if (smem && ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
   kern<<<(unsigned)(in.rows * sh.parts), kBeamThreads, smem, st>>>(in, adj, scores, count, sh.parts,
                                                                    sh.slice, parts, cands);
@@ -718,9 +741,11 @@ int launch_rows(const rans_logits &in, const rans_adjust &adj, const float *scor
 }  // namespace
 
 uint64_t beam_workspace_bytes(int dtype, int64_t rows, int vocab, int count, int sms) {
-  const BeamShape sh = beam_shape(dtype, rows, vocab, sms);
-  return part_bytes(rows, sh.parts) +
-         (uint64_t)rows * (uint64_t)sh.parts * 2 * (uint64_t)count * sizeof(Candidate);
+  // (whether tables come with a call is not known here)
+  const int a = beam_shape(dtype, rows, vocab, sms, false).parts;
+  const int b = beam_shape(dtype, rows, vocab, sms, true).parts, parts = a > b ? a : b;
+  return part_bytes(rows, parts) +
+         (uint64_t)rows * (uint64_t)parts * 2 * (uint64_t)count * sizeof(Candidate);
 }
 
 int launch_beam_select(const rans_logits &in, const rans_adjust &adj, const float *scores,
@@ -728,7 +753,7 @@ int launch_beam_select(const rans_logits &in, const rans_adjust &adj, const floa
                        int32_t *parents, void *ws, int32_t *status, cudaStream_t st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
-  const BeamShape sh = beam_shape(in.dtype, in.rows, in.vocab, num_sms(dev));
+  const BeamShape sh = beam_shape(in.dtype, in.rows, in.vocab, num_sms(dev), has_tables(adj));
   if (in.rows > 0x7fffffff / sh.parts) return RANS_ERR_ARG;
   Part *parts = static_cast<Part *>(ws);
   Candidate *cands =
