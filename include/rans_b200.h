@@ -780,6 +780,7 @@ int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head, void *o
 #define RANS_MAX_BEAMS 64
 #define RANS_MAX_CONTINUATIONS 128
 
+/* For the current device; 0 for sizes out of range or without a device. */
 uint64_t rans_beam_workspace_bytes(int32_t dtype, int64_t rows, int32_t vocab, int32_t count);
 int rans_beam_select(const rans_logits *logits, const rans_adjust *adjust, const float *scores,
                      int32_t beams, int32_t count, float *scores_out, int32_t *tokens,

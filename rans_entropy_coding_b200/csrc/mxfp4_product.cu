@@ -20,6 +20,11 @@
 // the products, and eight warps take the accumulators: each keeps half of a
 // row's columns in registers, so that the next tile's products start as soon as
 // tensor memory is read, while the logits are still being rounded and stored.
+// Measured, 131072 head rows of 4096 columns: one token 53 us (5.4 TB/s of codes and
+// scales; memory's copy rate would take 43), 256 tokens 70 us (54), 4096 tokens 776 us
+// by itself (5.7 PFLOP/s; the tensor pipe is busy 78% of the time) and 916 us again and
+// again, under the power limit.  Single blocks took 922 us, pairs without the
+// exchange of logits 916.
 #include <type_traits>
 
 #include <cuda.h>
