@@ -221,7 +221,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   const int per_tile = (sh.steps + 3) / 4;  // stages of a tile
   // tokens of a tile as the products take them: a pair's halves are a multiple of 16
   auto width_of = [&](int left) {
-    return PAIR ? min(kMostTokens, (left + 31) & ~31) : min(sh.box, (left + 15) & ~15);
+    const int n = min(left, kMostTokens);
+    return PAIR ? (n + 31) & ~31 : min(sh.box, (n + 15) & ~15);
   };
 
   if (wid == 1) {
@@ -604,7 +605,7 @@ int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, in
   sh.tokens = (int32_t)a.rows;
   sh.head_rows = (int32_t)w.rows;
   sh.box = pair || a.rows >= kMostTokens ? kMostTokens : (int32_t)((a.rows + 15) & ~15);
-  sh.token_tiles = (sh.tokens + kMostTokens - 1) / kMostTokens;
+  sh.token_tiles = (int32_t)((a.rows + kMostTokens - 1) / kMostTokens);
   const int64_t tiles = (int64_t)sh.token_tiles * ((w.rows + rows - 1) / rows);
   sh.steps = (int32_t)((w.cols + kStepCols - 1) / kStepCols);
   sh.groups = mx_groups(w.cols);

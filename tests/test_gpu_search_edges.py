@@ -141,6 +141,13 @@ def test_offsets_past_31_and_32_bits():
     for r in (0, 2048, 4095, 4096, 4199):
         assert torch.equal(out[r:r + 1], rb.mxfp4_logits(x[r:r + 1], w))
     del out
+    # many tiles of tokens on few head rows
+    w, x = head_of(130, 96), rows(200001, 96, F16)
+    out = rb.mxfp4_logits(x, w)
+    for at in (0, 255, 256, 131071, 199936, 200000):
+        assert torch.equal(out[at:at + 1], rb.mxfp4_logits(x[at:at + 1], w))
+    assert torch.equal(out[1000:1100], rb.mxfp4_logits(x[1000:1100], w))
+    del out
     # quantisation: 2.3e9 elements
     big = torch.empty(70000, 32800, device="cuda", dtype=BF16).normal_()
     q = rb.quantize_mxfp4(big)
