@@ -1,6 +1,6 @@
 // logits_common.cuh -- reading rows of logits with their adjustments
-// (penalties, biases, masks), shared by the kernels of logits.cu, tokens.cu
-// and distill.cu.
+// (penalties, biases, masks), shared by the kernels of logits.cu, tokens.cu,
+// distill.cu and beam.cu (and, for rows of any numbers, mxfp4.cu).
 //
 // Rows may start anywhere an element may (odd vocabularies, strided views).
 // A kernel walks a row in vectors of 16 bytes at 16-byte aligned addresses:

@@ -123,7 +123,8 @@ class TokenCoder:
     head: a model's output head (Mxfp4 [vocab, cols]).  With one, ``add`` and
     ``step`` take hidden rows [rows, cols] (or Mxfp4) in place of logits and compute
     these, in `logits_dtype`, so that they too are the same in every batch: both
-    sides then need the same hidden rows, and the same logits_dtype.
+    sides then need the same hidden rows, and the same logits_dtype.  An ``add``
+    holds the logits of its rows meanwhile.
     """
 
     def __init__(self, device="cuda", head=None, logits_dtype=torch.float32):
@@ -180,8 +181,7 @@ class TokenCoder:
 
     def step(self, logits, adjust=None, stream_ids=None):
         """Next tokens (int32 [rows]) under rows of logits (hidden rows, with a head);
-        row r belongs to stream stream_ids[r]
-        (default r; -1 skips the row)."""
+        row r belongs to stream stream_ids[r] (default r; -1 skips the row)."""
         if self._in is None:
             raise RuntimeError("begin with the streams first")
         logits = self._logits(logits, self.decoding)

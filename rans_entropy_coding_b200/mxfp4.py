@@ -34,7 +34,8 @@ class Mxfp4:
         column in the low half; a last block that the columns do not fill is
         filled up with 0.
     scales: uint8, the blocks' scale bytes in tiles of 128 rows by 4 blocks
-        (see from_rows for bytes in plain rows).
+        (see from_rows for bytes in plain rows); those of blocks past the columns
+        must not be 255.
     cols: columns of the matrix; all that the codes hold, if not given.
 
     The tensors are kept, not copied.
