@@ -84,12 +84,12 @@ __device__ __forceinline__ int block_sum(int x, int *words) {
 }
 
 // A value that at least `count` of the threads' values reach, near the largest
-// such, down from the largest, `most`, in steps twice as long each; the type's
-// lowest if fewer are above -inf.
+// such, down from the largest, `most`, in steps twice as long each; -inf if fewer
+// are above it.  (Not the type's lowest then: a logit may be that, too.)
 template <typename F>
 __device__ __forceinline__ F threshold(F mine, int count, F most, F lowest) {
   F lo = most, hi = most, d = 1;
-  if (__syncthreads_count(mine >= lowest) < count) return lowest;
+  if (__syncthreads_count(mine >= lowest) < count) return -(F)__builtin_huge_val();
   int n = __syncthreads_count(mine >= most);
   if (n >= count) return most;
   for (;;) {
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
     }
     // A warp goes through what few lanes have: near the top, or perhaps among the best
     // (ties with the cut of an earlier tile are not: their tokens are higher).
-    const bool keeps = fresh ? m >= cut : m > cut;
+    const bool keeps = fresh ? m >= cut && m > kNegInf : m > cut;
     for (uint32_t lanes = __ballot_sync(0xffffffffu, keeps || sums != 0); lanes != 0;
          lanes &= lanes - 1) {
       const int l = __ffs(lanes) - 1;
@@ -515,7 +515,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
         }, [&] { touched([&](int u, float x) { body(key_of(x), u - row.shift); }); });
       }
     };
-    // (the cut that was looked for is reached by `count`, or is the lowest value)
+    // (the cut that was looked for is reached by `count`, or is -inf)
     exact_cut<uint32_t>(count, key_of(cut), key_of(all_top), in.vocab, key, last, [&](uint32_t k) {
       int c = 0;
       each(in.vocab, [&](uint32_t v, int) { c += v >= k; });
