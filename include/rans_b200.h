@@ -761,7 +761,8 @@ int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head, void *o
  * rounding) a continuation of beam r by token v has
  *     total = scores[r] + x_v - log(sum over w of e^(x_w)),
  * summed beyond float32's precision and compared in 64 bits; of equal totals the
- * lower beam, then the lower token is the better one.  Per text the `count` best go
+ * lower beam is the better one, within a beam the larger x (whose total may be
+ * the same in 64 bits), then the lower token.  Per text the `count` best go
  * out, best first: scores_out (the total rounded to float32), tokens and
  * parents (the beam within its text), [texts][count] each.  Tokens whose x is
  * -inf are no continuations; where there are fewer than `count`, the rest is

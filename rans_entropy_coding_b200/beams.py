@@ -154,8 +154,9 @@ def beam_select(logits, scores, beams, count=None, adjust=None, status=None, str
     logits: a row per beam, `beams` rows a text; scores: float32, each beam's log
     probability so far (-inf: a dead beam).  A continuation's total is its beam's
     score and the log probability of its token under the adjusted logits.
-    Totals are compared in 64 bits, ties go to the lower beam and token; where
-    there are too few, the rest is -inf, -1, -1.
+    Totals are compared in 64 bits, ties go to the lower beam, within a beam to the
+    larger logit, then to the lower token; where there are too few, the rest is -inf,
+    -1, -1.
     """
     rows = T._rows(logits)
     if count is None:

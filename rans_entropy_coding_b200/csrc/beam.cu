@@ -2,9 +2,10 @@
 // beams and the vocabulary.
 //
 // A continuation's total is score + x - logsumexp(x) with x the row's adjusted
-// logits; the order is that of totals in 64 bits.  Within a row it is the order
-// of x, which is exact, so rows and parts of rows can be thinned out to their
-// best few before any sum is known; only between beams do the sums decide.
+// logits; the order is that of totals in 64 bits, of equal ones by beam.  Within a row
+// it is the order of x, which is exact (totals cannot say otherwise, only be equal), so
+// rows and parts of rows can be thinned out to their best few before any sum is known;
+// only between beams do the sums decide.
 //
 // Two launches.  The first reads the rows once.  A block takes part of a row and
 // keeps, per thread, the running maximum and sum of exponentials, and in
@@ -73,6 +74,14 @@ __device__ __forceinline__ uint64_t key_of(double x) {
 }
 constexpr double kLowest64 = -1.7976931348623157e308;
 
+// The order of continuations of equal totals: the lower beam, then the larger logit,
+// then the lower token.
+constexpr int kTokenBits = 19, kPlaceBits = kTokenBits + 32;
+static_assert(RANS_MAX_VOCAB <= 1 << kTokenBits && RANS_MAX_BEAMS < 1 << (63 - kPlaceBits), "places");
+__device__ __forceinline__ uint64_t place_of(int beam, float x, int token) {
+  return (uint64_t)beam << kPlaceBits | (uint64_t)~key_of(x) << kTokenBits | (uint64_t)token;
+}
+
 __device__ __forceinline__ int block_sum(int x, int *words) {
   x = __reduce_add_sync(0xffffffffu, x);
   __syncthreads();
@@ -117,8 +126,8 @@ __device__ __forceinline__ F threshold(F mine, int count, F most, F lowest) {
 // at it up to the place, are the best min(count, all), ties by place.  From `lo`
 // on, which at least `count` items reach (or nothing more is below than above it).
 // reach(k): how many items' keys are >= k; equal(k, p): how many are k, up to place p.
-template <typename K, class Reach, class Equal>
-__device__ __forceinline__ void exact_cut(int count, K lo, K most, int places, K &cut, int &last,
+template <typename K, typename P, class Reach, class Equal>
+__device__ __forceinline__ void exact_cut(int count, K lo, K most, P places, K &cut, P &last,
                                           Reach reach, Equal equal) {
   K hi = most;
   while (lo < hi) {
@@ -127,9 +136,9 @@ __device__ __forceinline__ void exact_cut(int count, K lo, K most, int places, K
     else hi = mid - 1;
   }
   const int need = count - reach(lo + 1);
-  int a = 0, b = places;
+  P a = 0, b = places;
   while (a < b) {
-    const int mid = (int)(((int64_t)a + b) >> 1);
+    const P mid = a + (b - a) / 2;
     if (equal(lo, mid) >= need) b = mid;
     else a = mid + 1;
   }
@@ -516,7 +525,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
       }
     };
     // (the cut that was looked for is reached by `count`, or is -inf)
-    exact_cut<uint32_t>(count, key_of(cut), key_of(all_top), in.vocab, key, last, [&](uint32_t k) {
+    exact_cut(count, key_of(cut), key_of(all_top), in.vocab, key, last, [&](uint32_t k) {
       int c = 0;
       each(in.vocab, [&](uint32_t v, int) { c += v >= k; });
       return block_sum(c, words);
@@ -554,12 +563,12 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
 
 // One block per text.
 __global__ void __launch_bounds__(kMergeThreads)
-    beam_merge_kernel(const float *scores, int beams, int count, int vocab, int parts,
+    beam_merge_kernel(const float *scores, int beams, int count, int parts,
                       const Part *part_in, const Candidate *cand_in, float *out_scores,
                       int32_t *out_tokens, int32_t *out_parents, int32_t *status) {
   __shared__ double base[RANS_MAX_BEAMS];  // score - logsumexp
   __shared__ double total[kMergeList];
-  __shared__ int place[kMergeList];        // beam * vocab + token
+  __shared__ uint64_t place[kMergeList];
   __shared__ int listed, words[kMergeThreads / 32];
   __shared__ double tops[kMergeThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
@@ -608,12 +617,13 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
   }
   __syncthreads();
-  // body(total, place) for all candidates of the text
+  // body(total, place_of) for all candidates of the text
   auto each = [&](auto body) {
     auto one = [&](int i, int n, const Candidate &x) {
       const int p = i / slots, b = p / parts;
       const double c = base[b];
-      if (i - p * slots < n && c > -__builtin_huge_val()) body((double)x.x + c, b * vocab + x.token);
+      if (i - p * slots < n && c > -__builtin_huge_val())
+        body((double)x.x + c, place_of(b, x.x, x.token));
     };
     if (few) {
 #pragma unroll
@@ -625,7 +635,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
   };
   double best = -__builtin_huge_val();
-  each([&](double v, int) { best = fmax(best, v); });
+  each([&](double v, uint64_t) { best = fmax(best, v); });
   double most = best;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) most = fmax(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -633,7 +643,7 @@ __global__ void __launch_bounds__(kMergeThreads)
   __syncthreads();
   for (int i = 0; i < kMergeThreads / 32; ++i) most = fmax(most, tops[i]);
   const double cut = threshold(best, count, most, kLowest64);
-  each([&](double v, int p) {
+  each([&](double v, uint64_t p) {
     if (v < cut) return;
     const int at = atomicAdd(&listed, 1);
     if (at < kMergeList) {
@@ -644,20 +654,20 @@ __global__ void __launch_bounds__(kMergeThreads)
   __syncthreads();
   if (listed > kMergeList) {
     uint64_t key;
-    int last;
-    exact_cut<uint64_t>(count, key_of(cut), key_of(most), 0x7fffffff, key, last, [&](uint64_t k) {
+    uint64_t last = 0;
+    exact_cut(count, key_of(cut), key_of(most), ~(uint64_t)0 >> 1, key, last, [&](uint64_t k) {
       int c = 0;
-      each([&](double v, int) { c += key_of(v) >= k; });
+      each([&](double v, uint64_t) { c += key_of(v) >= k; });
       return block_sum(c, words);
-    }, [&](uint64_t k, int q) {
+    }, [&](uint64_t k, uint64_t q) {
       int c = 0;
-      each([&](double v, int p) { c += key_of(v) == k && p <= q; });
+      each([&](double v, uint64_t p) { c += key_of(v) == k && p <= q; });
       return block_sum(c, words);
     });
     __syncthreads();
     if (tid == 0) listed = 0;
     __syncthreads();
-    each([&](double v, int p) {
+    each([&](double v, uint64_t p) {
       const uint64_t x = key_of(v);
       if (x > key || (x == key && p <= last)) {
         const int at = atomicAdd(&listed, 1);
@@ -671,13 +681,13 @@ __global__ void __launch_bounds__(kMergeThreads)
   const int n = listed;
   for (int i = tid; i < n; i += kMergeThreads) {
     const double v = total[i];
-    const int p = place[i];
+    const uint64_t p = place[i];
     int rank = 0;
     for (int j = 0; j < n; ++j) rank += total[j] > v || (total[j] == v && place[j] < p);
     if (rank < count) {
       out_scores[t * count + rank] = (float)v;
-      out_tokens[t * count + rank] = p % vocab;
-      out_parents[t * count + rank] = p / vocab;
+      out_tokens[t * count + rank] = (int)(p & ((1u << kTokenBits) - 1));
+      out_parents[t * count + rank] = (int)(p >> kPlaceBits);
     }
   }
   for (int i = n + tid; i < count; i += kMergeThreads) {
@@ -774,7 +784,7 @@ int launch_beam_select(const rans_logits &in, const rans_adjust &adj, const floa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, beam_merge_kernel, scores, beams, count, (int)in.vocab, sh.parts,
+  return cudaLaunchKernelEx(&cfg, beam_merge_kernel, scores, beams, count, sh.parts,
                             (const Part *)parts, (const Candidate *)cands, out_scores, tokens,
                             parents, status) == cudaSuccess
              ? RANS_OK

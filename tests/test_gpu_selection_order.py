@@ -42,3 +42,38 @@ def test_lowest_values_behind_tiles_of_nothing(by, dtype):
     exact = np.array([-1.0 + t - lse for t in (3.0, 2.0, 1.0, low, low, low, low, low)])
     got = best.cpu().numpy().astype(np.float64)
     assert (np.abs(got - exact) <= 2.0 ** -20 + 2.0 ** -24 * np.abs(exact)).all()
+
+
+@pytest.mark.parametrize("v", [40, 5000, 70000])
+@pytest.mark.parametrize("count", [1, 3, 6, 64])
+def test_equal_totals_of_different_logits(v, count):
+    """Logits too close for their totals to differ: the lower beam first, within a
+    beam the larger logit, and of equal ones the lower token, whatever is thinned out
+    on the way."""
+    x = torch.zeros(2, v, device="cuda")
+    x[0, [v - 1, 30, 7]] = torch.tensor([1e-20, 2e-20, -1e-20], device="cuda")
+    x[1, [0, v - 3]] = torch.tensor([-3e-20, 3e-20], device="cuda")
+    s = torch.full((2,), -2.0, device="cuda")
+    rest = [t for t in range(v) if t not in (v - 1, 30, 7)]
+    first = [30, v - 1] + rest + [7]
+    rest = [t for t in range(v) if t not in (0, v - 3)]
+    second = [v - 3] + rest + [0]
+    want = ([(0, t) for t in first] + [(1, t) for t in second])[:count]
+    best, tokens, parents = rb.beam_select(x, s, 2, count)
+    n = len(want)
+    assert list(zip(parents[0, :n].tolist(), tokens[0, :n].tolist())) == want
+    for b in (0, 1):
+        one = rb.beam_select(x[b:b + 1], s[:1], 1, count)[1][0].tolist()
+        want = (first, second)[b][:count]
+        assert one[:len(want)] == want
+
+
+def test_equal_totals_of_far_scores():
+    """Scores so large that a row's logits do not show in its totals."""
+    v = 20000
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn(3, v, device="cuda", generator=g)
+    s = torch.full((3,), -1e30, device="cuda")
+    _, tokens, parents = rb.beam_select(x, s, 3, 5)
+    order = torch.sort(x[0], descending=True, stable=True).indices[:5]
+    assert tokens[0].tolist() == order.tolist() and parents[0].tolist() == [0] * 5
