@@ -760,7 +760,8 @@ int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head, void *o
  * adjusted logits (as rans_adjust_logits has them, in float32 before the output's
  * rounding) a continuation of beam r by token v has
  *     total = scores[r] + x_v - log(sum over w of e^(x_w)),
- * summed beyond float32's precision and compared in 64 bits; of equal totals the
+ * the sum right to 2^-21 of itself (2^-23 and better where errors average out), totals
+ * compared in 64 bits; of equal totals the
  * lower beam is the better one, within a beam the larger x (whose total may be
  * the same in 64 bits), then the lower token.  Per text the `count` best go
  * out, best first: scores_out (the total rounded to float32), tokens and

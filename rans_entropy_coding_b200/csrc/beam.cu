@@ -13,23 +13,23 @@
 // threads have met a logit as large as the count-th largest of the threads'
 // maxima, so nothing below that need be kept.  The second merges a text's parts.
 //
-// The sums: where few lanes of a warp have terms above e^-1.5 of the top, those are
-// taken one by one, by reduction to |r| <= ln 2 / 2 in two parts (Cody and Waite,
-// "Software Manual for the Elementary Functions", 1980) and the power series to r^7
-// (remainder 6e-9; 1.3 units of 2^-24 in all); the others come from the special
-// function unit (2^-22 of each term), a vector's in a tree of float32.  A thread adds
-// with the lost part carried along (Kahan), threads and blocks add up in 64 bits.
-// Measured against 64 bits, totals are off by 2e-8 of themselves, which is their last
-// rounding; plain float32 sums lose 1e-6 and swap neighbours.  Equal rows of a call get
-// equal sums: a thread's tokens go by their ids, not by where a row starts in
-// memory, and tokens that penalties and biases touch, which come in a table's
-// order, are added as integers.
+// The sums: a term e^x is 2^k 2^f with k = round(x log2 e), f = x log2 e - k, log2 e in two
+// parts (so f is off by no more than its two last roundings, 0.35 units of 2^-24 in the
+// term; a difference x - top and its product were off by up to 11 units, all together
+// where a row's body is one logit) and 2^f from the special function unit (2.45 units
+// at most: measured over every float32 from -0.5 to 0.5).  k is counted from a whole
+// number near the row's top.  A vector's terms add up in a tree of float32 (three
+// additions of a unit each, without error where the terms are equal), all else in 64
+// bits.  So a row's log sum is off by 2.8 units (1.7e-7) for a body of one logit, 5.8
+// (3.5e-7) for any row; measured 1.5 at most on bodies of one to four logits, far
+// less where logits differ and errors average out.
+// Equal rows of a call get equal sums: a thread's tokens go by their ids, not by where a
+// row starts in memory, and tokens that penalties and biases touch, which come in a
+// table's order, are added as integers.
 //
-// Measured, 256 x 131072 bf16 in 32 texts: 25 us for the rows (2.7 TB/s; memory alone 10),
-// 31 with the merge.  What bounds the rows is issue: some 14 instructions a logit
-// (unpacking, difference, product, exponential, tree, maxima), a barrier now and
-// then, and what may be among the best.  All terms by the series took 65 us, all logits
-// kept by their own threads 52.
+// Measured, 256 x 131072 bf16 in 32 texts: 34 us with the merge's 6 (memory alone 10; 31
+// with the terms of rounded differences, 43 with power series of 1.1 units a term in
+// place of the special function unit: the FP32 pipes then take 12 instructions a logit).
 #include <type_traits>
 
 #include "logits_common.cuh"
@@ -44,7 +44,6 @@ constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamVecs = 4;      // vectors of 16 bytes a lane has in a tile
 constexpr int kBeamList = 1024;   // tokens kept by a block
 constexpr int kRanked = 256;      // of them, that are thinned out by their ranks
-constexpr int kNearLanes = 4;     // most lanes of a warp whose vectors near the top are added singly
 constexpr int kPlainBlocks = 4, kTableBlocks = 3;  // of an SM at once
 constexpr int kMergeThreads = 256;
 constexpr int kMergeList = 512;
@@ -146,23 +145,6 @@ __device__ __forceinline__ void exact_cut(int count, K lo, K most, P places, K &
   last = a;
 }
 
-// e^t for t <= 0 (below -80 as at -80, which no sum notices).
-__device__ __forceinline__ float exp_of(float t) {
-  t = fmaxf(t, -80.0f);
-  const float j = __fmaf_rn(t, 0x1.715476p+0f, 12582912.0f);  // k in its low bits
-  const float k = __fsub_rn(j, 12582912.0f);
-  // ln 2 = 0x1.62e4p-1 + 0x1.7f7d1cp-20: the first part's products with k are exact
-  float r = __fmaf_rn(k, -0x1.62e4p-1f, t);
-  r = __fmaf_rn(k, -0x1.7f7d1cp-20f, r);
-  float p = __fmaf_rn(r, 1.0f / 5040.0f, 1.0f / 720.0f);
-  p = __fmaf_rn(p, r, 1.0f / 120.0f);
-  p = __fmaf_rn(p, r, 1.0f / 24.0f);
-  p = __fmaf_rn(p, r, 1.0f / 6.0f);
-  p = __fmaf_rn(p, r, 0.5f);
-  p = __fmaf_rn(p, r, 1.0f);
-  p = __fmaf_rn(p, r, 1.0f);
-  return __uint_as_float(__float_as_uint(p) + (__float_as_uint(j) << 23));
-}
 // Two at a time.
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
   uint64_t x;
@@ -183,11 +165,100 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// 2^x by the special function unit, to 2^-22: for the terms that are small one by one.
-__device__ __forceinline__ float small_exp2(float x) {
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
+// The larger of a vector's elements and `low`, one of its type (twice, for 16 bits).
+template <typename T>
+__device__ __forceinline__ uint4 at_least(const uint4 &q, uint32_t low) {
+  if constexpr (sizeof(T) == 2) {
+    return make_uint4(pair_most(q.x, low, T()), pair_most(q.y, low, T()),
+                      pair_most(q.z, low, T()), pair_most(q.w, low, T()));
+  } else {
+    const float f = __uint_as_float(low);
+    return make_uint4(__float_as_uint(fmaxf(__uint_as_float(q.x), f)),
+                      __float_as_uint(fmaxf(__uint_as_float(q.y), f)),
+                      __float_as_uint(fmaxf(__uint_as_float(q.z), f)),
+                      __float_as_uint(fmaxf(__uint_as_float(q.w), f)));
+  }
+}
+
+// What a thread's sum is relative to: 2^whole, or, where logits are so large (kFar) that
+// x - base is exact for whatever counts, e^base.
+template <typename T>
+struct Reference {
+  static constexpr float kFar = 4096.0f;
+  static constexpr float kSlack = 32.0f;  // logits above the reference by less stay with it
+  static constexpr float kDepth = 64.0f;  // those further below count as such, which no sum notices
+  static constexpr double kLn2 = 0.693147180559945309417;
+  float at = kNegInf, base = 0.0f, whole = 0.0f;
+  uint32_t low;  // kDepth below, as logits lie in memory (to 8 bits; far: their lowest)
+
+  __device__ __forceinline__ bool some() const { return at > kNegInf; }
+  // Moves to a logit that lies too far above; what a sum is multiplied by then.
+  __device__ __forceinline__ void raise(float to, float inv, double &sum) {
+    if (!(to > at + kSlack)) return;
+    const bool far = !(fabsf(to) < kFar);
+    const float b = far ? to : 0.0f, w = far ? 0.0f : rintf(__fmul_rn(to, 0x1.715476p+0f));
+    if (sum != 0.0)
+      sum *= exp((double)base - (double)b + ((double)whole - (double)w) * kLn2);
+    at = to;
+    base = b;
+    whole = w;
+    const float lowest = std::is_same<T, __half>::value ? -65504.0f
+                         : sizeof(T) == 2               ? -0x1.fep+127f
+                                                        : kLowest;
+    const float z = far ? lowest : fmaxf(__fdiv_rn(__fsub_rn(to, kDepth), inv), lowest);
+    if constexpr (sizeof(T) == 2) {
+      const T t = float_logit<T>(z);
+      low = (uint32_t)*reinterpret_cast<const uint16_t *>(&t) * 0x10001u;
+    } else {
+      low = __float_as_uint(z);
+    }
+  }
+  // e^(the reference - to)
+  __device__ __forceinline__ double over(float to) const {
+    return exp((double)base - (double)to + (double)whole * kLn2);
+  }
+};
+
+// 2^x by the special function unit.
+__device__ __forceinline__ float exp2_of(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// The sum of N terms e^x relative to 2^whole.
+template <int N>
+__device__ __forceinline__ float vector_sum(const uint64_t (&x)[N / 2], float whole) {
+  const float magic = __fsub_rn(12582912.0f, whole);  // k - whole in its low bits
+  uint64_t e[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    // log2 e = 0x1.715476p+0 + 0x1.4ae0cp-26
+    const uint64_t j = fma2(x[i], both(0x1.715476p+0f), both(magic));
+    uint64_t f = fma2(x[i], both(0x1.715476p+0f), sub2(both(magic), j));
+    f = fma2(x[i], both(0x1.4ae0cp-26f), f);
+    const float2 y = halves(f);
+    e[i] = pair_of(__uint_as_float(__float_as_uint(exp2_of(y.x)) + ((uint32_t)j << 23)),
+                   __uint_as_float(__float_as_uint(exp2_of(y.y)) + ((uint32_t)(j >> 32) << 23)));
+  }
+#pragma unroll
+  for (int o = N / 4; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < o; ++i) e[i] = add2(e[i], e[i + o]);
+  }
+  const float2 p = halves(e[0]);
+  return __fadd_rn(p.x, p.y);
 }
 // The largest element of a vector, NaN if one is.
 template <typename T>
@@ -309,25 +380,13 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
     each_touched(table, tid, kBeamThreads, [&](int u, float z) { body(u, __fmul_rn(z, inv)); });
   };
 
-  // mine: this thread's largest logit; top: what its sum is relative to, at least
-  // that (and the block's largest so far, as far as it was asked for)
-  float mine = kNegInf, top = kNegInf, cut = kNegInf;
-  float s = 0.0f, lost = 0.0f;  // the sum, and what its additions lost
+  // mine: this thread's largest logit; ref: what its sum is relative to (the block's
+  // largest so far, as far as it was asked for)
+  float mine = kNegInf, cut = kNegInf;
+  Reference<T> ref;
+  double s = 0.0;
   float touched_top = kNegInf;
   double touched_sum = 0.0;
-  auto raise = [&](float to) {
-    if (to > top) {
-      const float f = top > kNegInf ? exp_of(__fsub_rn(top, to)) : 0.0f;
-      s = __fmul_rn(s, f);
-      lost = __fmul_rn(lost, f);
-      top = to;
-    }
-  };
-  auto add = [&](float e) {
-    const float y = __fsub_rn(e, lost), t = __fadd_rn(s, y);
-    lost = __fsub_rn(__fsub_rn(t, s), y);
-    s = t;
-  };
   auto keep = [&](int u, float x) {
     const int at = atomicAdd(&listed, 1);
     if (at < kBeamList) list[at] = Candidate{x, u - row.shift};
@@ -349,71 +408,51 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
   int round = 0;
   auto tile = [&](auto scaled, const uint4 (&q)[kBeamVecs], int u, int u_hi) {
     constexpr bool SCALED = decltype(scaled)::value;
-    float m = kNegInf, top_of[kBeamVecs];
+    float m = kNegInf;
 #pragma unroll
     for (int k = 0; k < kBeamVecs; ++k) {
       // compared as it lies in memory: x is monotonous in z
-      top_of[k] = __fmul_rn(vector_max<T>(q[k]), inv);
-      m = max_nan(m, top_of[k]);
+      m = max_nan(m, __fmul_rn(vector_max<T>(q[k]), inv));
     }
     mine = max_nan(mine, m);
     // the first tile says what to look for; tiles 2, 8, 32, ... raise it
     const bool fresh = round == 0 || ((round & 0x2aaaaaaa) == round && (round & (round - 1)) == 0);
     if (fresh) {
       const float most = value_of(most_key(mine));
-      raise(most);
+      ref.raise(most, inv, s);
       cut = fmaxf(cut, threshold(mine, count, most, kLowest));
     }
-    raise(m);
-    // Terms add up vector by vector in a tree of float32, from the special function
-    // unit (2^-22 of each); where few lanes have vectors with terms above e^-1.5 of
-    // the top, those are left out here and added one by one.
-    const float near = __fsub_rn(top, 1.5f);
-    uint32_t sums = 0;
+    ref.raise(m, inv, s);
+    if (ref.some()) {
 #pragma unroll
-    for (int k = 0; k < kBeamVecs; ++k)
-      if (!(top_of[k] < near)) sums |= 1u << k;
-    const int near_lanes = __popc(__ballot_sync(0xffffffffu, sums != 0));
-    if (!(top > kNegInf) || near_lanes > kNearLanes) sums = 0;
+      for (int k = 0; k < kBeamVecs; ++k) {
+        float x[N];
+        unpack16(at_least<T>(q[k], ref.low), x, T());
+        uint64_t pairs[N / 2];
 #pragma unroll
-    for (int k = 0; k < kBeamVecs; ++k) {
-      float x[N];
-      unpack16(q[k], x, T());
-      if constexpr (SCALED) {
+        for (int i = 0; i < N; i += 2) {
+          pairs[i / 2] = pair_of(x[i], x[i + 1]);
+          if constexpr (SCALED) pairs[i / 2] = mul2(pairs[i / 2], both(inv));
+        }
+        if (ref.base != 0.0f) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) x[i] = __fmul_rn(x[i], inv);
+          for (int i = 0; i < N / 2; ++i) {
+            const float2 d = halves(add2(pairs[i], both(-ref.base)));
+            pairs[i] = pair_of(fmaxf(d.x, -ref.kDepth), fmaxf(d.y, -ref.kDepth));
+          }
+        }
+        s += (double)vector_sum<N>(pairs, ref.whole);
       }
-      uint64_t e[N / 2];
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        // (log2 e to a float32: a term e^t comes out too large by 1.4e-8 |t| of itself)
-        const float2 y =
-            halves(mul2(add2(pair_of(x[i], x[i + 1]), both(-top)), both(0x1.715476p+0f)));
-        e[i / 2] = pair_of(small_exp2(y.x), small_exp2(y.y));
-      }
-#pragma unroll
-      for (int o = N / 4; o > 0; o >>= 1) {
-#pragma unroll
-        for (int i = 0; i < o; ++i) e[i] = add2(e[i], e[i + o]);
-      }
-      const float2 pair = halves(e[0]);
-      add(!(sums >> k & 1) && top > kNegInf ? __fadd_rn(pair.x, pair.y) : 0.0f);
     }
-    // A warp goes through what few lanes have: near the top, or perhaps among the best
-    // (ties with the cut of an earlier tile are not: their tokens are higher).
+    // A warp goes through what few lanes have: perhaps among the best (ties with the cut
+    // of an earlier tile are not: their tokens are higher).
     const bool keeps = fresh ? m >= cut && m > kNegInf : m > cut;
-    for (uint32_t lanes = __ballot_sync(0xffffffffu, keeps || sums != 0); lanes != 0;
-         lanes &= lanes - 1) {
+    for (uint32_t lanes = __ballot_sync(0xffffffffu, keeps); lanes != 0; lanes &= lanes - 1) {
       const int l = __ffs(lanes) - 1;
-      const uint32_t add_it = __shfl_sync(0xffffffffu, sums, l);
       const int k = lane / N, at = u + (l - lane) * N + 32 * N * k + lane % N;
       if (k < kBeamVecs && at < u_hi &&
           (!ADJ || ok_bits[(at - table_at) >> 5] >> ((at - table_at) & 31) & 1)) {
         const float x = __fmul_rn(logit_float(row.at0[at]), inv);
-        if (add_it >> k & 1) {
-          raise(x);
-          add(exp_of(__fsub_rn(x, top)));
-        }
         if ((fresh ? x >= cut : x > cut) && x > kNegInf) keep(at, x);
       }
     }
@@ -446,7 +485,8 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
       else tile(std::false_type(), q, u, u_hi);
     }
   }, [&] {
-    // their own maximum, and their sum in units of 2^-40 of it
+    // their own maximum, and their sum in units of 2^-50 of it (below 2^13 of them at a
+    // time)
     float m = kNegInf;
     touched([&](int u, float x) {
       m = max_nan(m, x);
@@ -456,7 +496,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
     if (m > kNegInf) {
       unsigned long long q = 0;
       touched([&](int, float x) {
-        if (x > kNegInf) q += __float2ull_rn(__fmul_rn(exp_of(__fsub_rn(x, m)), 0x1p+40f));
+        if (x > kNegInf) q += __double2ull_rn(exp((double)x - (double)m) * 0x1p+50);
       });
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
@@ -466,7 +506,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
       for (int i = 0; i < kBeamWarps; ++i) q += whole_sums[i];
       const float both = max_nan(touched_top, m);
       touched_sum = touched_sum * exp((double)touched_top - (double)both) +
-                    (double)q * 0x1p-40 * exp((double)m - (double)both);
+                    (double)q * 0x1p-50 * exp((double)m - (double)both);
       touched_top = both;
     } else if (m != m) {
       touched_top = m;
@@ -483,7 +523,7 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
   const float all_top = fmaxf(value_of(most_key(mine)), touched_top);
   cut = fmaxf(cut, threshold(mine, count, all_top, kLowest));
   double sum = 0.0;
-  if (top > kNegInf) sum = ((double)s - (double)lost) * exp((double)top - (double)all_top);
+  if (ref.some()) sum = s * ref.over(all_top);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   if (lane == 0) sums[wid] = sum;

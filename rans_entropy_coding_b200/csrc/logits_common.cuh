@@ -116,6 +116,18 @@ __device__ __forceinline__ uint32_t pair_min(uint32_t a, uint32_t b, __nv_bfloat
   return c;
 }
 
+// The larger of packed pairs; a NaN gives way.
+__device__ __forceinline__ uint32_t pair_most(uint32_t a, uint32_t b, __half) {
+  uint32_t c;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+__device__ __forceinline__ uint32_t pair_most(uint32_t a, uint32_t b, __nv_bfloat16) {
+  uint32_t c;
+  asm("max.bf16x2 %0, %1, %2;" : "=r"(c) : "r"(a), "r"(b));
+  return c;
+}
+
 // One row as the kernels walk it.
 template <typename T>
 struct Row {
