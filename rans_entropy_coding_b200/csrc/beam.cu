@@ -606,7 +606,10 @@ __global__ void __launch_bounds__(kMergeThreads)
     beam_merge_kernel(const float *scores, int beams, int count, int parts,
                       const Part *part_in, const Candidate *cand_in, float *out_scores,
                       int32_t *out_tokens, int32_t *out_parents, int32_t *status) {
-  __shared__ double base[RANS_MAX_BEAMS];  // score - logsumexp
+  // score - log of the sum of e^(x - top), and top: a total is base + (x - top).  (With one
+  // number for both, rows at the type's lowest value would lose the score and the sum.)
+  __shared__ double base[RANS_MAX_BEAMS];
+  __shared__ float tops_of[RANS_MAX_BEAMS];
   __shared__ double total[kMergeList];
   __shared__ uint64_t place[kMergeList];
   __shared__ int listed, words[kMergeThreads / 32];
@@ -652,7 +655,8 @@ __global__ void __launch_bounds__(kMergeThreads)
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
       const bool some = !bad && top > kNegInf && score > kNegInf;
-      base[b] = some ? (double)score - ((double)top + log(sum)) : -__builtin_huge_val();
+      base[b] = some ? (double)score - log(sum) : -__builtin_huge_val();
+      tops_of[b] = top;
       if (bad && status) report(status, RANS_ERR_RANGE, r);
     }
   }
@@ -663,7 +667,7 @@ __global__ void __launch_bounds__(kMergeThreads)
       const int p = i / slots, b = p / parts;
       const double c = base[b];
       if (i - p * slots < n && c > -__builtin_huge_val())
-        body((double)x.x + c, place_of(b, x.x, x.token));
+        body(c + ((double)x.x - (double)tops_of[b]), place_of(b, x.x, x.token));
     };
     if (few) {
 #pragma unroll
