@@ -200,7 +200,9 @@ struct Reference {
   static constexpr float kDepth = 64.0f;  // those further below count as such, which no sum notices
   static constexpr double kLn2 = 0.693147180559945309417;
   float at = kNegInf, base = 0.0f, whole = 0.0f;
-  uint32_t low;  // kDepth below, as logits lie in memory (to 8 bits; far: their lowest)
+  // kDepth below, as logits lie in memory (about), or -inf: then below x - base instead
+  uint32_t low;
+  bool outside;
 
   __device__ __forceinline__ bool some() const { return at > kNegInf; }
   // Moves to a logit that lies too far above; what a sum is multiplied by then.
@@ -213,16 +215,22 @@ struct Reference {
     at = to;
     base = b;
     whole = w;
-    const float lowest = std::is_same<T, __half>::value ? -65504.0f
-                         : sizeof(T) == 2               ? -0x1.fep+127f
-                                                        : kLowest;
-    const float z = far ? lowest : fmaxf(__fdiv_rn(__fsub_rn(to, kDepth), inv), lowest);
-    if constexpr (sizeof(T) == 2) {
-      const T t = float_logit<T>(z);
+    // (not where the type rounds that to something else: beyond its range, by its steps
+    // near 0)
+    T t = float_logit<T>(__fdiv_rn(__fsub_rn(to, kDepth), inv));
+    const float back = __fmul_rn(logit_float(t), inv);
+    outside = far || !(back < to - 40.0f && back > to - 85.0f);
+    if (outside) t = float_logit<T>(kNegInf);
+    if constexpr (sizeof(T) == 2)
       low = (uint32_t)*reinterpret_cast<const uint16_t *>(&t) * 0x10001u;
-    } else {
-      low = __float_as_uint(z);
-    }
+    else
+      low = *reinterpret_cast<const uint32_t *>(&t);
+  }
+  // x - base, not further below than kDepth.
+  __device__ __forceinline__ uint64_t inside(uint64_t x) const {
+    const float floor = __fsub_rn(__fsub_rn(at, base), kDepth);
+    const float2 d = halves(add2(x, both(-base)));
+    return pair_of(fmaxf(d.x, floor), fmaxf(d.y, floor));
   }
   // e^(the reference - to)
   __device__ __forceinline__ double over(float to) const {
@@ -434,12 +442,9 @@ __global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : 
           pairs[i / 2] = pair_of(x[i], x[i + 1]);
           if constexpr (SCALED) pairs[i / 2] = mul2(pairs[i / 2], both(inv));
         }
-        if (ref.base != 0.0f) {
+        if (ref.outside) {
 #pragma unroll
-          for (int i = 0; i < N / 2; ++i) {
-            const float2 d = halves(add2(pairs[i], both(-ref.base)));
-            pairs[i] = pair_of(fmaxf(d.x, -ref.kDepth), fmaxf(d.y, -ref.kDepth));
-          }
+          for (int i = 0; i < N / 2; ++i) pairs[i] = ref.inside(pairs[i]);
         }
         s += (double)vector_sum<N>(pairs, ref.whole);
       }

@@ -82,3 +82,54 @@ def test_temperatures_at_the_ends(dtype, temperature):
         assert tokens[:, 0].tolist() == [int(t) for t in z.argmax(1)]
         want = s.cpu().numpy().astype(np.float64) + exact
         assert np.abs(best[:, 0].cpu().numpy() - want).max() <= SUM + U * np.abs(want).max()
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+def test_a_row_of_lowest_values_is_even(dtype):
+    """Such a beam's score and the logits do not cancel one another: its continuations
+    have a V-th of it, and better beams come first."""
+    v = 5000
+    x = torch.full((3, v), torch.finfo(dtype).min, device="cuda", dtype=dtype)
+    x[1] = 0.0
+    x[1, 7] = 20.0
+    s = torch.tensor([-1.0, -2.0, -9.0], device="cuda")
+    best, tokens, parents = rb.beam_select(x, s, 3, 4)
+    share = 20.0 - math.log(math.exp(20.0) + v - 1)
+    want = [-2.0 + share] + [-1.0 - math.log(v)] * 3
+    assert parents[0].tolist() == [1, 0, 0, 0] and tokens[0].tolist() == [7, 0, 1, 2]
+    assert best[0].tolist() == pytest.approx(want, rel=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("temperature", [1.0, 1000.0])
+def test_what_is_masked_or_off_the_end_counts_for_nothing(dtype, temperature):
+    """In rows at the lowest value too, where nothing lies below."""
+    n, v = 2, 9001
+    x = torch.full((n, v + 7), 0.0, device="cuda", dtype=dtype)[:, :v]
+    x.fill_(torch.finfo(dtype).min)
+    x[1] = -60000.0
+    allowed = torch.ones(n, v, dtype=torch.bool, device="cuda")
+    allowed[:, 100:] = torch.rand(v - 100, device="cuda") < 0.5
+    left = int(allowed[0].sum())
+    s = torch.full((n,), -1.0, device="cuda")
+    for mask, size in ((rb.pack_mask(allowed), left), (None, v)):
+        rules = rb.LogitAdjust(temperature=temperature, mask=mask)
+        best, tokens, _ = rb.beam_select(x, s, 1, 3, rules)
+        assert tokens.tolist() == [[0, 1, 2]] * n
+        assert best.flatten().tolist() == pytest.approx([-1.0 - math.log(size)] * 6, rel=1e-6)
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=str)
+@pytest.mark.parametrize("below", [1.0, 2.0, 3.0])
+def test_steps_near_zero_under_small_temperatures(dtype, below):
+    """A type's smallest step is thousands after the temperature: all but the zeros
+    count for nothing."""
+    v, step = 9001, {F32: 2.0 ** -100, F16: 2.0 ** -24, BF16: 2.0 ** -100}[dtype]
+    for over in (20.0, 70.0, 100.0, 130.0, 260.0, 1e4):  # what a step comes to
+        x = torch.full((1, v), -below * step, device="cuda", dtype=dtype)
+        x[0, 5:105] = 0.0
+        s = torch.tensor([-1.0], device="cuda")
+        best, tokens, _ = rb.beam_select(x, s, 1, 2, rb.LogitAdjust(temperature=step / over))
+        share = math.log(100 + (v - 100) * math.exp(-below * over))
+        assert tokens.tolist() == [[5, 6]]
+        assert best[0].tolist() == pytest.approx([-1.0 - share] * 2, rel=1e-6)
