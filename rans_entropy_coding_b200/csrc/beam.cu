@@ -44,11 +44,22 @@ constexpr int kBeamWarps = kBeamThreads / 32;
 constexpr int kBeamVecs = 4;      // vectors of 16 bytes a lane has in a tile
 constexpr int kBeamList = 1024;   // tokens kept by a block
 constexpr int kRanked = 256;      // of them, that are thinned out by their ranks
-constexpr int kPlainBlocks = 4, kTableBlocks = 3;  // of an SM at once
 constexpr int kMergeThreads = 256;
 constexpr int kMergeList = 512;
 constexpr int kMergeItems = 4;   // candidates of a thread in registers
 static_assert(RANS_MAX_CONTINUATIONS <= kBeamThreads, "a threshold needs that many maxima");
+
+// What adjusts a call's logits: nothing, a mask alone, penalties or biases (and a mask).
+enum { kPlain, kMask, kTables };
+// Blocks of the first launch that an SM takes at once.  With tables two fit into its 228
+// KB (66592 bytes of table, 16384 of mask bits, 8.5 KB besides); a rule that counted
+// three planned half as many blocks again and ran them in a second turn (80 x 128256 f16
+// under penalties: 43 us for 31; 100 x 50021: 35 for 28).  Of the others registers take
+// four, of float32 three (128 x 131072: 29.4 us for 30.3 with four, which spill).
+template <typename T>
+constexpr int blocks_of(int adj) {
+  return adj == kTables ? 2 : sizeof(T) == 4 ? 3 : 4;
+}
 
 // What a block says of its part of a row.
 struct Part {
@@ -299,13 +310,8 @@ __device__ __forceinline__ uint4 keep_bits(const uint4 &q, uint32_t ok) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// ADJ: kMask with a mask alone, kTables with penalties or biases, whose tables leave shared
-// memory for three blocks an SM, with more registers each (256 x 131072 f16 at odd
-// addresses: 70 us with tables, 56 with a mask alone, 45 with neither; three blocks
-// for a mask took 71, four for tables 80).
-enum { kPlain, kMask, kTables };
 template <typename T, int ADJ>
-__global__ void __launch_bounds__(kBeamThreads, ADJ == kTables ? kTableBlocks : kPlainBlocks)
+__global__ void __launch_bounds__(kBeamThreads, blocks_of<T>(ADJ))
     beam_rows_kernel(rans_logits in, rans_adjust adj, const float *scores, int count, int parts,
                      int slice, Part *part_out, Candidate *cand_out) {
   extern __shared__ __align__(16) unsigned char smem[];
@@ -749,6 +755,11 @@ __global__ void __launch_bounds__(kMergeThreads)
 // Parts of a row, of so many tiles each that the blocks, as many at once as an SM
 // takes, are done soonest; a block has `extra` tiles' worth of work besides (its first
 // threshold, a table of touched tokens).
+constexpr int kTableBytes = (int)sizeof(TouchTable) + kHashSpan / 8;  // of a block with tables
+constexpr int kBlockBytes = kTableBytes + kBeamList * (int)sizeof(Candidate) + 240 + 1024;
+static_assert(blocks_of<float>(kTables) * kBlockBytes <= 228 * 1024 &&
+                  (blocks_of<float>(kTables) + 1) * kBlockBytes > 228 * 1024,
+              "the blocks with tables that an SM takes");
 struct BeamShape {
   int parts, slice;
 };
@@ -757,7 +768,7 @@ template <typename T>
 BeamShape beam_shape(int64_t rows, int vocab, int sms, bool tables) {
   constexpr int kTile = kBeamThreads * kBeamVecs * VecOf<T>::N;
   const int tiles = (vocab + kTile - 1) / kTile, extra = tables ? 8 : 1;
-  const int64_t slots = (int64_t)sms * (tables ? kTableBlocks : kPlainBlocks);
+  const int64_t slots = (int64_t)sms * blocks_of<T>(tables ? kTables : kPlain);
   int best = tiles;
   int64_t least = -1;
   for (int p = 1; p <= kMostParts && p <= tiles; ++p) {
