@@ -9,6 +9,8 @@
 
 #include <stdint.h>
 
+#include "rans_b200.h"
+
 #ifdef __cplusplus
 extern "C" {
 #endif
@@ -22,6 +24,17 @@ extern "C" {
  * leaving the context usable.  limit must be in [1, 2^21].  Asynchronous.
  */
 int rans_debug_wait_timeout(void *workspace, uint32_t limit, void *stream);
+
+/*
+ * rans_mxfp4_product whose blocks copy no more than `stages` stages (256 columns
+ * each) of the tokens' numbers and wait `limit` tries in place of 2^21: blocks that
+ * need more of them give up, record RANS_ERR_TIMEOUT in `status` (required) and return
+ * after the copies and products in flight; the context stays usable.  The result is
+ * undefined then.  limit must be in [1000, 2^21].  Asynchronous.
+ */
+int rans_debug_product_timeout(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
+                               int32_t out_dtype, int64_t out_stride, void *status,
+                               uint32_t stages, uint32_t limit, void *stream);
 
 #ifdef __cplusplus
 }

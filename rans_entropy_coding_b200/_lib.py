@@ -164,6 +164,8 @@ SIGNATURES = [
     ("rans_get_status", ctypes.c_int, [_P, _P]),
     ("rans_debug_divide", ctypes.c_int, [_P, _P, _I64, _P, _P, _P]),
     ("rans_debug_wait_timeout", ctypes.c_int, [_P, ctypes.c_uint32, _P]),
+    ("rans_debug_product_timeout", ctypes.c_int,
+     [_MXP, _MXP, _P, _I32, _I64, _P, ctypes.c_uint32, ctypes.c_uint32, _P]),
 ]
 
 _lib = None

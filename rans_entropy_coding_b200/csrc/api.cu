@@ -12,6 +12,7 @@
 
 #include "rans_common.cuh"
 #include "mxfp4.cuh"
+#include "rans_b200_debug.h"
 #include "rans_internal.h"
 
 #define RANS_API extern "C" __attribute__((visibility("default")))
@@ -959,16 +960,31 @@ RANS_API int rans_mxfp4_values(const rans_mxfp4 *q, void *out, int32_t out_dtype
   return rb::launch_mxfp4_values(*q, out, out_dtype, out_stride, as_stream(stream));
 }
 
-RANS_API int rans_mxfp4_product(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
-                                int32_t out_dtype, int64_t out_stride, void *status,
-                                void *stream) {
-  NvtxRange nvtx_("rans_mxfp4_product");
+static int product(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out, int32_t out_dtype,
+                   int64_t out_stride, void *status, const rb::ProductLimits &limits,
+                   void *stream) {
   int st = check_mxfp4(a);
   if (!st) st = check_head(head, a->rows, a->cols, out, out_dtype, out_stride, status);
   if (st || a->rows == 0) return st;
   if (on_mxfp4(out, rows_bytes(a->rows, head->rows, out_stride, out_dtype), a)) return RANS_ERR_ARG;
   return rb::launch_mxfp4_product(*a, *head, out, out_dtype, out_stride,
-                                  static_cast<int32_t *>(status), false, as_stream(stream));
+                                  static_cast<int32_t *>(status), false, limits,
+                                  as_stream(stream));
+}
+
+RANS_API int rans_mxfp4_product(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
+                                int32_t out_dtype, int64_t out_stride, void *status,
+                                void *stream) {
+  NvtxRange nvtx_("rans_mxfp4_product");
+  return product(a, head, out, out_dtype, out_stride, status, rb::ProductLimits(), stream);
+}
+
+RANS_API int rans_debug_product_timeout(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
+                                        int32_t out_dtype, int64_t out_stride, void *status,
+                                        uint32_t stages, uint32_t limit, void *stream) {
+  if (!status || limit < 1000 || limit > rb::ProductLimits().tries) return RANS_ERR_ARG;
+  return product(a, head, out, out_dtype, out_stride, status, rb::ProductLimits{limit, stages},
+                 stream);
 }
 
 RANS_API uint64_t rans_mxfp4_logits_workspace_bytes(int64_t rows, int64_t cols) {
@@ -999,7 +1015,8 @@ RANS_API int rans_mxfp4_logits(const rans_logits *hidden, const rans_mxfp4 *head
   st = rb::launch_mxfp4_quantize(*hidden, a, as_stream(stream));
   if (st) return st;
   return rb::launch_mxfp4_product(a, *head, out, out_dtype, out_stride,
-                                  static_cast<int32_t *>(status), true, as_stream(stream));
+                                  static_cast<int32_t *>(status), true, rb::ProductLimits(),
+                                  as_stream(stream));
 }
 
 RANS_API uint64_t rans_beam_workspace_bytes(int32_t dtype, int64_t rows, int32_t vocab,

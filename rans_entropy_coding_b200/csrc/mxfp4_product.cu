@@ -51,7 +51,6 @@ constexpr int kPitch = kHeadRows + 4;           // of their rows there
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kScaleCol = 256;             // scales behind the accumulators
 constexpr uint32_t kScaleCols = 24;             // of one stage: 8 of the head, 16 of the tokens
-constexpr uint32_t kTries = 1u << 21;           // of a bounded wait, about 1 us each
 
 struct ProductShape {
   int32_t tokens, head_rows;  // n, V
@@ -61,6 +60,7 @@ struct ProductShape {
   int32_t groups;             // of 128 columns
   int32_t stages;             // of the ring
   int32_t wait;               // the tokens come from the kernel before
+  ProductLimits limits;
 };
 
 // Descriptors of shared memory: the upper half is the layout's, the lower one the
@@ -112,6 +112,20 @@ __device__ __forceinline__ void commit(uint32_t bar) {
     asm volatile(
         "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
         : "memory");
+}
+// Arrives at one in this block alone.
+template <bool PAIR>
+__device__ __forceinline__ void commit_here(uint32_t bar) {
+  if constexpr (PAIR)
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+        : "memory");
+  else
+    commit<false>(bar);
+}
+// The four warps of a half of the accumulators.
+__device__ __forceinline__ void meet(int half) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
 }
 // A barrier in this block or in another one of the cluster.  Relaxed: nothing in memory
 // goes with it (a release would wait for the logits' stores).
@@ -204,7 +218,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
                    const uint8_t *token_scales, O *out, int64_t out_stride, ProductShape sh,
                    int32_t *status) {
   extern __shared__ unsigned char smem_raw[];
-  __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, free_bar;
+  __shared__ __align__(8) uint64_t full_bar[kMaxStages], empty_bar[kMaxStages], done_bar, free_bar,
+      last_bar;
   __shared__ uint32_t tmem_base;
   __shared__ volatile int dead;  // a wait gave up
   const int tid = threadIdx.x, lane = tid & 31, wid = __shfl_sync(kFull, tid >> 5, 0);
@@ -232,6 +247,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         tma::mbar_init(smem_addr(&empty_bar[i]), 1);
       }
       tma::mbar_init(smem_addr(&done_bar), 1);
+      tma::mbar_init(smem_addr(&last_bar), 1);
       tma::mbar_init(smem_addr(&free_bar), PAIR ? 2 * kEpilogueWarps : kEpilogueWarps);
       dead = 0;
       tma::fence_mbar_init();
@@ -269,7 +285,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   // whose fences cost more than a stage.)
   auto wait = [&](uint64_t *bar, uint32_t parity, bool cluster = false) {
     const uint32_t b = smem_addr(bar);
-    for (uint32_t i = 0; i < kTries; ++i) {
+    for (uint32_t i = 0; i < sh.limits.tries; ++i) {
       if (__all_sync(kFull, cluster ? try_wait_cluster(b, parity) : mbar_try_wait(b, parity)))
         return true;
       if (__any_sync(kFull, dead)) return false;
@@ -291,7 +307,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t lap = 0;
     bool ok = true;
     int mt = tile / sh.token_tiles, nt = tile - mt * sh.token_tiles;
-    while (tile < sh.tiles) {
+    uint32_t left = wid == 2 ? sh.limits.token_stages : ~0u;
+    while (tile < sh.tiles && left-- != 0) {
       if (lap > 0) {
         ok = wait(&empty_bar[stage], (lap - 1) & 1);
         if (!ok) break;
@@ -358,7 +375,8 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // copies in flight write to this block's memory: they end first (as far as all
       // warps have issued theirs)
       for (int i = 0; i < sh.stages; ++i)
-        tma::wait_bounded(smem_addr(&full_bar[i]), (i < stage ? lap : lap - 1) & 1, 1u << 18);
+        tma::wait_bounded(smem_addr(&full_bar[i]), (i < stage ? lap : lap - 1) & 1,
+                          min(sh.limits.tries, 1u << 18));
     }
   } else if (wid == 1 && rank == 0) {
     // ----------------------------------------------------- the products --
@@ -412,9 +430,10 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       if (!ok) break;
     }
     if (!ok) {
-      // products in flight: a last commit follows them
-      if (elected()) commit<PAIR>(smem_addr(&done_bar));
-      tma::wait_bounded(smem_addr(&done_bar), (uint32_t)n_tile & 1, 1u << 21);
+      // products in flight: a last commit follows them (at a barrier of its own: nobody
+      // is to take it for a tile's)
+      if (elected()) commit_here<PAIR>(smem_addr(&last_bar));
+      tma::wait_bounded(smem_addr(&last_bar), 0, sh.limits.tries);
     }
   } else if (wid >= 4) {
     // --------------------------------------------------- the accumulators --
@@ -422,12 +441,22 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t freed = leader(&free_bar);
     unsigned char *exchange = smem_raw + (smem - smem_addr(smem_raw)) + sh.stages * stage_bytes;
     int n_tile = 0, turn = 0;
+    auto count_of = [&](int tile) {  // columns of this warp that are tokens
+      const int left = sh.tokens - tile % sh.token_tiles * kMostTokens, width = width_of(left);
+      return min(width / 2, left - half * (width / 2));
+    };
     for (int tile = first_tile; tile < sh.tiles; tile += tile_step, ++n_tile) {
       const int mt = tile / sh.token_tiles, n0 = tile % sh.token_tiles * kMostTokens;
-      const int left = sh.tokens - n0, width = width_of(left);
-      const int c0 = half * (width / 2);
-      const int count = min(width / 2, left - c0);  // columns of this warp that are tokens
-      if (!wait(&done_bar, (uint32_t)n_tile & 1)) break;
+      const int c0 = half * (width_of(sh.tokens - n0) / 2), count = count_of(tile);
+      if (!wait(&done_bar, (uint32_t)n_tile & 1)) {
+        // A half's four warps meet for every piece of a tile (below), and those that saw
+        // the tile done would wait for ever for one that had left: it meets them in all
+        // that is left.
+        if constexpr (HALF >= kStoreTokens * 2)
+          for (int n = count_of(tile); tile < sh.tiles; n = count_of(tile += tile_step))
+            for (int p = 0; p < n; p += kStoreTokens) meet(half);
+        break;
+      }
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float v[HALF];
       const uint32_t from = tmem + ((uint32_t)quarter << 21) + c0;
@@ -485,7 +514,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
 #pragma unroll
             for (int i = 0; i < kStoreTokens; ++i)
               buf[i * kPitch + at[i & 3]] = float_logit<O>(v[p + i]);
-            asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+            meet(half);
             const O *f = from + shift;
             if constexpr (FORM == 0) {
               Four<O> x[kStoreTokens / 4];
@@ -594,7 +623,8 @@ int launch_o(const ProductMaps &maps, const rans_mxfp4 &a, const rans_mxfp4 &w, 
 }  // namespace
 
 int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, int dtype,
-                         int64_t stride, int32_t *status, bool follows, cudaStream_t st) {
+                         int64_t stride, int32_t *status, bool follows,
+                         const ProductLimits &limits, cudaStream_t st) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return RANS_ERR_CUDA;
   const int sms = num_sms(dev);
@@ -613,6 +643,7 @@ int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, in
   if (tiles * ((sh.steps + 3) / 4) > 0x3fffffff) return RANS_ERR_ARG;
   sh.tiles = (int32_t)tiles;
   sh.wait = follows ? 1 : 0;
+  sh.limits = limits;
   const int box = pair ? kMostTokens / 2 : sh.box;  // tokens in a block's memory
   const uint32_t stage = kHeadRows * kStageBytes + (uint32_t)box * kStageBytes +
                          2 * kMxTileBytes * (1 + (uint32_t)(sh.box + kMxTileRows - 1) / kMxTileRows);

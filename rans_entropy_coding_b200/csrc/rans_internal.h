@@ -101,8 +101,13 @@ int launch_distill(const rans_logits &in, const int32_t *ids, const float *lp, i
 int launch_mxfp4_quantize(const rans_logits &x, const rans_mxfp4 &q, cudaStream_t st);
 int launch_mxfp4_values(const rans_mxfp4 &q, void *out, int dtype, int64_t stride,
                         cudaStream_t st);
+struct ProductLimits {
+  uint32_t tries = 1u << 21;    // of a bounded wait, about 1 us each
+  uint32_t token_stages = ~0u;  // that a block copies (fewer, to see waits give up)
+};
 int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, int dtype,
-                         int64_t stride, int32_t *status, bool follows, cudaStream_t st);
+                         int64_t stride, int32_t *status, bool follows,
+                         const ProductLimits &limits, cudaStream_t st);
 
 // The best continuations of texts; a search's bookkeeping; states in place.
 uint64_t beam_workspace_bytes(int dtype, int64_t rows, int vocab, int count, int sms);
