@@ -290,27 +290,51 @@ __global__ void __launch_bounds__(kAdvanceThreads)
 
 }  // namespace
 
+namespace {
+
+// The next states' moves as one launch has them, of a text; how many there are, or an
+// error.
+int plan_moves(const rans_state *states, int32_t n, int64_t texts, Moves &mv) {
+  mv.n = n < kStatesPerLaunch ? n : kStatesPerLaunch;
+  mv.first[0] = 0;
+  for (int32_t i = 0; i < mv.n; ++i) {
+    const rans_state &s = states[i];
+    mv.state[i] = s;
+    mv.bytes[i] = access_bytes(s);
+    const int64_t chunk = (int64_t)kMoveThreads * kMoveSteps * mv.bytes[i];
+    const int64_t chunks = (s.positions * s.position_bytes + chunk - 1) / chunk;
+    if (chunks > 0x7fffffff) return RANS_ERR_ARG;
+    mv.chunks[i] = (int32_t)chunks;
+    mv.first[i + 1] = mv.first[i] + chunks * s.segments;
+    if (mv.first[i + 1] > 0x7fffffff) return RANS_ERR_ARG;
+  }
+  if (mv.first[mv.n] > 0 && texts > 0x7fffffff / mv.first[mv.n]) return RANS_ERR_ARG;
+  return mv.n;
+}
+
+}  // namespace
+
+int check_reorder_states(const rans_state *states, int32_t n, int64_t texts) {
+  Moves mv;
+  for (int32_t i = 0; i < n; i += mv.n) {
+    const int e = plan_moves(states + i, n - i, texts, mv);
+    if (e < 0) return e;
+  }
+  return RANS_OK;
+}
+
 int launch_reorder_states(const rans_state *states, int32_t n, int64_t texts, int beams,
                           const int32_t *parents, const int32_t *lengths, int32_t *status,
                           cudaStream_t st) {
-  for (int32_t i0 = 0; i0 < n; i0 += kStatesPerLaunch) {
-    Moves mv;
-    mv.n = n - i0 < kStatesPerLaunch ? n - i0 : kStatesPerLaunch;
-    mv.first[0] = 0;
-    for (int32_t i = 0; i < mv.n; ++i) {
-      const rans_state &s = states[i0 + i];
-      mv.state[i] = s;
-      mv.bytes[i] = access_bytes(s);
-      const int64_t chunk = (int64_t)kMoveThreads * kMoveSteps * mv.bytes[i];
-      const int64_t chunks = (s.positions * s.position_bytes + chunk - 1) / chunk;
-      if (chunks > 0x7fffffff) return RANS_ERR_ARG;
-      mv.chunks[i] = (int32_t)chunks;
-      mv.first[i + 1] = mv.first[i] + chunks * s.segments;
-      if (mv.first[i + 1] > 0x7fffffff) return RANS_ERR_ARG;
-    }
+  // (what the second launch would refuse, the first must not have moved)
+  const int bad = n > kStatesPerLaunch ? check_reorder_states(states, n, texts) : RANS_OK;
+  if (bad) return bad;
+  Moves mv;
+  for (int32_t i = 0; i < n; i += mv.n) {
+    const int e = plan_moves(states + i, n - i, texts, mv);
+    if (e < 0) return e;
     const int64_t per_text = mv.first[mv.n];
     if (per_text == 0) continue;
-    if (texts > 0x7fffffff / per_text) return RANS_ERR_ARG;
     reorder_kernel<<<(unsigned)(texts * per_text), kMoveThreads, 0, st>>>(mv, beams, parents,
                                                                           lengths, status);
     if (cudaGetLastError() != cudaSuccess) return RANS_ERR_CUDA;

@@ -116,6 +116,7 @@ int launch_beam_select(const rans_logits &in, const rans_adjust &adj, const floa
                        int32_t *parents, void *ws, int32_t *status, cudaStream_t st);
 int launch_beam_advance(const float *scores, const int32_t *tokens, const int32_t *parents,
                         int count, const rans_beams &s, cudaStream_t st);
+int check_reorder_states(const rans_state *states, int32_t n, int64_t texts);
 int launch_reorder_states(const rans_state *states, int32_t n, int64_t texts, int beams,
                           const int32_t *parents, const int32_t *lengths, int32_t *status,
                           cudaStream_t st);

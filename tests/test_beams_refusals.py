@@ -1,0 +1,32 @@
+"""Refusals of selections and state moves that must come before anything has run, at the C
+entry points without a GPU: what is not refused there would fail with RANS_ERR_CUDA."""
+import ctypes
+
+import pytest
+
+import rans_entropy_coding_b200 as rb
+from rans_entropy_coding_b200 import build as rbuild
+from test_beams import A
+
+
+@pytest.fixture(scope="module")
+def lib():
+    rbuild.build()
+    return rb.lib()
+
+
+def states(n, large):
+    """n small states; the one at `large` with more blocks than a launch takes."""
+    s = (rb.rans_state * n)()
+    for i in range(n):
+        s[i].data, s[i].row_stride, s[i].segment_stride = A(4 + i), 64, 64
+        s[i].positions, s[i].segments, s[i].position_bytes = 4, 1, 16
+    s[large].data = 1 << 60
+    s[large].row_stride, s[large].positions, s[large].position_bytes = 1 << 42, 1 << 38, 16
+    return s
+
+
+@pytest.mark.parametrize("n,large", [(1, 0), (56, 55), (57, 56), (200, 57), (200, 199)])
+def test_states_too_large_for_a_later_launch_are_refused_before_the_first(lib, n, large):
+    s = states(n, large)
+    assert lib.rans_reorder_states(s, n, 8, 2, A(1), A(2), None, None) == rb.ERR_ARG
