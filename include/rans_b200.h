@@ -862,6 +862,12 @@ int rans_reorder_states(const rans_state *states, int32_t n_states, int64_t text
                         const int32_t *parents, const int32_t *lengths, void *status,
                         void *stream);
 
+/* What rans_reorder_states would refuse, for programs that have to know before they
+ * compute the parents.  Reads no device memory and launches nothing. */
+int rans_reorder_states_check(const rans_state *states, int32_t n_states, int64_t texts,
+                              int32_t beams, const int32_t *parents, const int32_t *lengths,
+                              void *status);
+
 /* Synchronises `stream` and returns the first error recorded in `workspace`
  * (RANS_OK if none), then clears it. */
 int rans_get_status(void *workspace, void *stream);

@@ -31,6 +31,7 @@ from .mxfp4 import (  # noqa: F401,E402
     rans_mxfp4_scales_bytes, rans_mxfp4_values)
 from .beams import (  # noqa: F401,E402
     MAX_BEAMS, MAX_CONTINUATIONS, MAX_STATES, BeamSearch, beam_select, rans_beam_advance,
-    rans_beam_select, rans_beam_workspace_bytes, rans_reorder_states, reorder_states)
+    rans_beam_select, rans_beam_workspace_bytes, rans_reorder_states,
+    rans_reorder_states_check, reorder_states)
 from .interface import (  # noqa: F401,E402
     RansCoder, TokenCoder, from_byte_strings, to_byte_strings)

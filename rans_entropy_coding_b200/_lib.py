@@ -161,6 +161,7 @@ SIGNATURES = [
      [_LGP, _ADP, _P, _I32, _I32, _P, _P, _P, _P, _U64, _P, _P]),
     ("rans_beam_advance", ctypes.c_int, [_P, _P, _P, _I32, _BMP, _P]),
     ("rans_reorder_states", ctypes.c_int, [_STP, _I32, _I64, _I32, _P, _P, _P, _P]),
+    ("rans_reorder_states_check", ctypes.c_int, [_STP, _I32, _I64, _I32, _P, _P, _P]),
     ("rans_get_status", ctypes.c_int, [_P, _P]),
     ("rans_debug_divide", ctypes.c_int, [_P, _P, _I64, _P, _P, _P]),
     ("rans_debug_wait_timeout", ctypes.c_int, [_P, ctypes.c_uint32, _P]),

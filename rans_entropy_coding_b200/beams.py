@@ -127,6 +127,12 @@ def _layout(x, rows, axis):
 
 
 def _reorder(dev, states, parents, lengths, axis, status):
+    return L.lib().rans_reorder_states(*_moves(dev, states, parents, lengths, axis, status),
+                                       T._raw_stream(dev))
+
+
+def _moves(dev, states, parents, lengths, axis, status):
+    """The arguments of a move of states, up to the stream."""
     if parents.dim() != 2 or not 1 <= parents.shape[1] <= MAX_BEAMS:
         raise ValueError("parents: int32 [texts, beams], 1 to %d beams" % MAX_BEAMS)
     t, k = parents.shape
@@ -142,8 +148,7 @@ def _reorder(dev, states, parents, lengths, axis, status):
     known = {}
     packed = b"".join([_state(x, t * k, axis if one else axis[i], dev, known)
                        for i, x in enumerate(states)])
-    return L.lib().rans_reorder_states(packed, len(states), t, k, p, n, _word(status, dev),
-                                       T._raw_stream(dev))
+    return packed, len(states), t, k, p, n, _word(status, dev)
 
 
 # ----------------------------------------------------------------- helpers --
@@ -184,6 +189,11 @@ def beam_select(logits, scores, beams, count=None, adjust=None, status=None, str
 def _workspace(code, rows, vocab, count, dev):
     """Bytes for sizes on a device (the current one)."""
     return L.lib().rans_beam_workspace_bytes(code, rows, vocab, count)
+
+
+def rans_reorder_states_check(states, parents, lengths, axis, status):
+    return L.lib().rans_reorder_states_check(
+        *_moves(T._device(parents, "parents"), states, parents, lengths, axis, status))
 
 
 def reorder_states(states, parents, lengths=None, axis=None, status=None, stream=None):
@@ -278,12 +288,20 @@ class BeamSearch:
         # enough that `beams` go on even if every beam ends in every way (as far as
         # a selection goes: beyond it beams may die out)
         count = min(self.beams * max(2, 1 + self._ends.numel()), MAX_CONTINUATIONS)
+        moves = None
+        if len(states) > 0:
+            # (before anything has run: a search is not to be a step ahead of its states)
+            every = [states] if isinstance(states, torch.Tensor) else states
+            moves = _moves(self.dev, every, self.parents, lengths, axis, status)
+            L.check(L.lib().rans_reorder_states_check(*moves), "reorder_states")
         with T._place(self.dev, stream):
             best = beam_select(logits, self.scores, self.beams, count, adjust, status)
             L.check(_advance(*best, self), "beam_advance")
             T._written(*self._parts)
-            if len(states) > 0:
-                reorder_states(states, self.parents, lengths, axis, status)
+            if moves is not None:
+                L.check(L.lib().rans_reorder_states(*moves, T._raw_stream(self.dev)),
+                        "reorder_states")
+                T._written(*every)
         return self.tokens
 
     def results(self, n=1):

@@ -1110,10 +1110,8 @@ RANS_API int rans_beam_advance(const float *scores, const int32_t *tokens, const
   return rb::launch_beam_advance(scores, tokens, parents, count, *s, as_stream(stream));
 }
 
-RANS_API int rans_reorder_states(const rans_state *states, int32_t n_states, int64_t texts,
-                                 int32_t beams, const int32_t *parents, const int32_t *lengths,
-                                 void *status, void *stream) {
-  NvtxRange nvtx_("rans_reorder_states");
+static int check_reorder(const rans_state *states, int32_t n_states, int64_t texts, int32_t beams,
+                         const int32_t *parents, const int32_t *lengths, const void *status) {
   if (n_states < 0 || n_states > RANS_MAX_STATES || (n_states > 0 && !states) || texts < 0 ||
       texts > 0x7fffffff || beams < 1 || beams > RANS_MAX_BEAMS)
     return RANS_ERR_ARG;
@@ -1147,6 +1145,23 @@ RANS_API int rans_reorder_states(const rans_state *states, int32_t n_states, int
       if (states_clash(a, b, rows)) return RANS_ERR_ARG;
     }
   }
+  return RANS_OK;
+}
+
+RANS_API int rans_reorder_states_check(const rans_state *states, int32_t n_states, int64_t texts,
+                                       int32_t beams, const int32_t *parents,
+                                       const int32_t *lengths, void *status) {
+  const int st = check_reorder(states, n_states, texts, beams, parents, lengths, status);
+  return st || n_states == 0 || texts == 0 ? st
+                                           : rb::check_reorder_states(states, n_states, texts);
+}
+
+RANS_API int rans_reorder_states(const rans_state *states, int32_t n_states, int64_t texts,
+                                 int32_t beams, const int32_t *parents, const int32_t *lengths,
+                                 void *status, void *stream) {
+  NvtxRange nvtx_("rans_reorder_states");
+  const int st = check_reorder(states, n_states, texts, beams, parents, lengths, status);
+  if (st || n_states == 0 || texts == 0) return st;
   return rb::launch_reorder_states(states, n_states, texts, beams, parents, lengths,
                                    static_cast<int32_t *>(status), as_stream(stream));
 }
