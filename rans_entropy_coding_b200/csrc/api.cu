@@ -1050,6 +1050,7 @@ RANS_API int rans_beam_select(const rans_logits *logits, const rans_adjust *adju
     return RANS_ERR_ARG;
   if (!workspace || !aligned_to(workspace, 256)) return RANS_ERR_ARG;
   const uint64_t out = 4ull * (uint64_t)count * (uint64_t)(logits->rows / beams);
+  const uint64_t rows = (uint64_t)logits->rows, words = (uint64_t)(logits->vocab + 31) / 32;
   const uint64_t need = rans_beam_workspace_bytes(logits->dtype, logits->rows, logits->vocab, count);
   const Range r[] = {{scores, 4ull * (uint64_t)logits->rows, false},
                      {scores_out, out, true},
@@ -1060,9 +1061,15 @@ RANS_API int rans_beam_select(const rans_logits *logits, const rans_adjust *adju
                       rows_bytes(logits->rows, logits->vocab, logits->row_stride, logits->dtype),
                       false},
                      {status, 256, true},
+                     {a.params, 16 * rows, false},
                      {a.history, 4ull * (uint64_t)a.history_len, false},
+                     {a.history_begin, 8 * rows, false},
+                     {a.history_end, 8 * rows, false},
                      {a.bias_ids, 4ull * (uint64_t)a.bias_len, false},
-                     {a.bias_values, 4ull * (uint64_t)a.bias_len, false}};
+                     {a.bias_values, 4ull * (uint64_t)a.bias_len, false},
+                     {a.bias_begin, 8 * rows, false},
+                     {a.bias_end, 8 * rows, false},
+                     {a.mask, 4 * ((rows - 1) * (uint64_t)a.mask_stride + words), false}};
   if (clash(r)) return RANS_ERR_ARG;
   if (need == 0) return RANS_ERR_CUDA;
   if (workspace_bytes < need) return RANS_ERR_CAPACITY;

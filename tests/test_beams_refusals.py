@@ -6,7 +6,7 @@ import pytest
 
 import rans_entropy_coding_b200 as rb
 from rans_entropy_coding_b200 import build as rbuild
-from test_beams import A
+from test_beams import A, adjust, select
 
 
 @pytest.fixture(scope="module")
@@ -41,3 +41,18 @@ def test_the_check_of_states_alone(lib):
                        ((s, 2, 0, 2, None, None, None), rb.OK),
                        ((s, 2, 8, 2, A(1), A(2), A(3) + 8), rb.ERR_ARG)):
         assert lib.rans_reorder_states_check(*args) == want
+
+
+@pytest.mark.parametrize("at", [A(2), A(3), A(4), A(5), A(6)], ids=["scores", "tokens", "parents",
+                                                                  "workspace", "status"])
+@pytest.mark.parametrize("what", [
+    dict(mask=-4, mask_stride=4), dict(mask=-124, mask_stride=4), dict(mask=-12),
+    dict(params=-8), dict(params=-124),
+    dict(history=-40, history_begin=-8, history_end=1 << 40),
+    dict(history=-40, history_begin=1 << 40, history_end=-56),
+    dict(bias_ids=-40, bias_values=-40, bias_begin=-8, bias_end=1 << 40),
+    dict(bias_ids=-40, bias_values=-40, bias_begin=1 << 40, bias_end=-56)], ids=str)
+def test_selections_that_would_write_to_rules_are_refused(lib, what, at):
+    """8 rows of 100 tokens; offsets from a result's place (strides and lengths as they are)."""
+    rules = adjust(**{k: x if k == "mask_stride" else at + x for k, x in what.items()})
+    assert select(lib, adj=rules, status=A(6)) == rb.ERR_ARG
