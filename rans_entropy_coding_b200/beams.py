@@ -229,7 +229,9 @@ class BeamSearch:
     scores (float32 [texts * beams]), tokens (int32, the same), parents (int32
     [texts, beams]), lengths and over (int32 [texts]) are the search's state
     on the device, updated in place; `window` is the beams' tokens as
-    LogitAdjust takes a history.  Steps may be captured into a graph.
+    LogitAdjust takes a history.  Steps may be captured into a graph.  They may run on
+    another stream than the one on which the search was made (they wait for that; captured
+    steps do not); steps on several streams, and results, are for the program to order.
     """
 
     def __init__(self, texts, beams, capacity, ends=(), length_penalty=0.0, early=False, pad=0,
@@ -268,6 +270,7 @@ class BeamSearch:
         self._parts = (self.scores, self.tokens, self.parents, self._history, self._end,
                        self.lengths, self.over, self._done_scores, self._done_lengths,
                        self._done_tokens, self._done_counts)
+        self._made = T._MadeOn(self._begin, self.dev, self._ends, *self._parts)
         self._c = _pack_beams(texts, beams, capacity, self._ends.data_ptr(), len(ends), pad,
                               self.length_penalty, int(bool(early)),
                               *[x.data_ptr() for x in self._parts])
@@ -295,6 +298,7 @@ class BeamSearch:
             moves = _moves(self.dev, every, self.parents, lengths, axis, status)
             L.check(L.lib().rans_reorder_states_check(*moves), "reorder_states")
         with T._place(self.dev, stream):
+            self._made.use()
             best = beam_select(logits, self.scores, self.beams, count, adjust, status)
             L.check(_advance(*best, self), "beam_advance")
             T._written(*self._parts)

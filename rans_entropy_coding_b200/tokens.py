@@ -53,14 +53,14 @@ def _raw_stream(dev):
 
 
 class _MadeOn:
-    """A tensor of the library's own that was computed on the stream current at
-    the time, for calls on other streams: they wait for it, and its memory
+    """A tensor (or more) of the library's own that was computed on the stream
+    current at the time, for calls on other streams: they wait for it, and its memory
     for them.  Not where either is captured: a capture may not wait for work
     outside of it, nor the reverse.  There the program orders its streams, and
     its replays, as it does for its own tensors."""
 
-    def __init__(self, x, dev):
-        self.x, self.dev = x, dev
+    def __init__(self, x, dev, *more):
+        self.tensors, self.dev = (x, *more), dev
         self.stream = torch.cuda.current_stream(dev)
         self.captured = torch.cuda.is_current_stream_capturing()
         if not self.captured:
@@ -74,7 +74,8 @@ class _MadeOn:
             return
         here = torch.cuda.current_stream(self.dev)
         here.wait_event(self.done)
-        self.x.record_stream(here)
+        for x in self.tensors:
+            x.record_stream(here)
 
 
 def _rows(x, what="logits"):
