@@ -30,7 +30,8 @@ int rans_debug_wait_timeout(void *workspace, uint32_t limit, void *stream);
  * each) of the tokens' numbers and wait `limit` tries in place of 2^21: blocks that
  * need more of them give up, record RANS_ERR_TIMEOUT in `status` (required) and return
  * after the copies and products in flight; the context stays usable.  The result is
- * undefined then.  limit must be in [1000, 2^21].  Asynchronous.
+ * undefined then.  limit must be in [1000, 2^21], out_dtype float32 or bfloat16.
+ * Asynchronous.
  */
 int rans_debug_product_timeout(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
                                int32_t out_dtype, int64_t out_stride, void *status,

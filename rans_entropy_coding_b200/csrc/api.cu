@@ -982,7 +982,9 @@ RANS_API int rans_mxfp4_product(const rans_mxfp4 *a, const rans_mxfp4 *head, voi
 RANS_API int rans_debug_product_timeout(const rans_mxfp4 *a, const rans_mxfp4 *head, void *out,
                                         int32_t out_dtype, int64_t out_stride, void *status,
                                         uint32_t stages, uint32_t limit, void *stream) {
-  if (!status || limit < 1000 || limit > rb::ProductLimits().tries) return RANS_ERR_ARG;
+  if (!status || limit < 1000 || limit > rb::ProductLimits::kTries ||
+      out_dtype == RANS_LOGITS_F16)
+    return RANS_ERR_ARG;
   return product(a, head, out, out_dtype, out_stride, status, rb::ProductLimits{limit, stages},
                  stream);
 }

@@ -210,9 +210,12 @@ struct ProductMaps {
   CUtensorMap head_scales, token_scales;  // of a pair
 };
 
+// SHORT: waits and copies are limited by the call (always, for float32; to the others a
+// limit that is not a constant costs registers: 907 us for 868 for the corpus, where
+// float32 with a constant takes 287 us for 250 for 4096 x 50021 x 1024).
 // HALF: most columns that an epilogue warp keeps.  PAIR: two blocks on 256 head rows;
 // the first of them issues the products, and all copies are announced at its barriers.
-template <typename O, int HALF, bool PAIR>
+template <typename O, int HALF, bool PAIR, bool SHORT>
 __global__ void __launch_bounds__(kProductThreads, 1)
     product_kernel(const __grid_constant__ ProductMaps maps, const uint8_t *head_scales,
                    const uint8_t *token_scales, O *out, int64_t out_stride, ProductShape sh,
@@ -283,9 +286,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   // A warp's wait: until another gave up, or for its own share.
   // (Only what the other block's threads arrive at is waited for at the cluster's scope,
   // whose fences cost more than a stage.)
+  constexpr bool kLimited = SHORT || sizeof(O) == 4;
+  const uint32_t tries = kLimited ? sh.limits.tries : ProductLimits::kTries;
   auto wait = [&](uint64_t *bar, uint32_t parity, bool cluster = false) {
     const uint32_t b = smem_addr(bar);
-    for (uint32_t i = 0; i < sh.limits.tries; ++i) {
+    for (uint32_t i = 0; i < tries; ++i) {
       if (__all_sync(kFull, cluster ? try_wait_cluster(b, parity) : mbar_try_wait(b, parity)))
         return true;
       if (__any_sync(kFull, dead)) return false;
@@ -307,7 +312,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     uint32_t lap = 0;
     bool ok = true;
     int mt = tile / sh.token_tiles, nt = tile - mt * sh.token_tiles;
-    uint32_t left = wid == 2 ? sh.limits.token_stages : ~0u;
+    uint32_t left = wid == 2 && kLimited ? sh.limits.token_stages : ~0u;
     while (tile < sh.tiles && left-- != 0) {
       if (lap > 0) {
         ok = wait(&empty_bar[stage], (lap - 1) & 1);
@@ -376,7 +381,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // warps have issued theirs)
       for (int i = 0; i < sh.stages; ++i)
         tma::wait_bounded(smem_addr(&full_bar[i]), (i < stage ? lap : lap - 1) & 1,
-                          min(sh.limits.tries, 1u << 18));
+                          min(tries, 1u << 18));
     }
   } else if (wid == 1 && rank == 0) {
     // ----------------------------------------------------- the products --
@@ -433,7 +438,7 @@ __global__ void __launch_bounds__(kProductThreads, 1)
       // products in flight: a last commit follows them (at a barrier of its own: nobody
       // is to take it for a tile's)
       if (elected()) commit_here<PAIR>(smem_addr(&last_bar));
-      tma::wait_bounded(smem_addr(&last_bar), 0, sh.limits.tries);
+      tma::wait_bounded(smem_addr(&last_bar), 0, tries);
     }
   } else if (wid >= 4) {
     // --------------------------------------------------- the accumulators --
@@ -441,22 +446,13 @@ __global__ void __launch_bounds__(kProductThreads, 1)
     const uint32_t freed = leader(&free_bar);
     unsigned char *exchange = smem_raw + (smem - smem_addr(smem_raw)) + sh.stages * stage_bytes;
     int n_tile = 0, turn = 0;
-    auto count_of = [&](int tile) {  // columns of this warp that are tokens
-      const int left = sh.tokens - tile % sh.token_tiles * kMostTokens, width = width_of(left);
-      return min(width / 2, left - half * (width / 2));
-    };
-    for (int tile = first_tile; tile < sh.tiles; tile += tile_step, ++n_tile) {
+    int tile = first_tile;
+    for (; tile < sh.tiles; tile += tile_step, ++n_tile) {
       const int mt = tile / sh.token_tiles, n0 = tile % sh.token_tiles * kMostTokens;
-      const int c0 = half * (width_of(sh.tokens - n0) / 2), count = count_of(tile);
-      if (!wait(&done_bar, (uint32_t)n_tile & 1)) {
-        // A half's four warps meet for every piece of a tile (below), and those that saw
-        // the tile done would wait for ever for one that had left: it meets them in all
-        // that is left.
-        if constexpr (HALF >= kStoreTokens * 2)
-          for (int n = count_of(tile); tile < sh.tiles; n = count_of(tile += tile_step))
-            for (int p = 0; p < n; p += kStoreTokens) meet(half);
-        break;
-      }
+      const int left = sh.tokens - n0, width = width_of(left);
+      const int c0 = half * (width / 2);
+      const int count = min(width / 2, left - c0);  // columns of this warp that are tokens
+      if (!wait(&done_bar, (uint32_t)n_tile & 1)) break;
       asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
       float v[HALF];
       const uint32_t from = tmem + ((uint32_t)quarter << 21) + c0;
@@ -557,6 +553,15 @@ __global__ void __launch_bounds__(kProductThreads, 1)
         else pieces(std::integral_constant<int, 0>());
       }
     }
+    // Where a wait gave up: a half's four warps meet for every piece of a tile, and those
+    // that saw the tile done would wait for ever for one that had left.  It meets them
+    // in all that is left.
+    if constexpr (HALF >= kStoreTokens * 2)
+      for (; tile < sh.tiles; tile += tile_step) {
+        const int left = sh.tokens - tile % sh.token_tiles * kMostTokens, width = width_of(left);
+        const int count = min(width / 2, left - half * (width / 2));
+        for (int p = 0; p < count; p += kStoreTokens) meet(half);
+      }
   }
   __syncwarp();
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
@@ -576,11 +581,11 @@ __global__ void __launch_bounds__(kProductThreads, 1)
   }
 }
 
-template <typename O, int HALF, bool PAIR>
+template <typename O, int HALF, bool PAIR, bool SHORT>
 int launch_t(const ProductMaps &maps, const rans_mxfp4 &a, const rans_mxfp4 &w, void *out,
              int64_t stride, const ProductShape &sh, uint32_t smem, int32_t *status, int blocks,
              cudaStream_t st) {
-  auto kern = product_kernel<O, HALF, PAIR>;
+  auto kern = product_kernel<O, HALF, PAIR, SHORT>;
   if (ensure_dyn_smem((const void *)kern, smem) != cudaSuccess) return RANS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)blocks);
@@ -608,16 +613,18 @@ int launch_t(const ProductMaps &maps, const rans_mxfp4 &a, const rans_mxfp4 &w, 
   return e == cudaSuccess ? RANS_OK : RANS_ERR_CUDA;
 }
 
-template <typename O>
+template <typename O, bool SHORT = false>
 int launch_o(const ProductMaps &maps, const rans_mxfp4 &a, const rans_mxfp4 &w, void *out,
              int64_t stride, const ProductShape &sh, bool pair, uint32_t smem, int32_t *status,
              int blocks, cudaStream_t st) {
-  if (pair) return launch_t<O, 128, true>(maps, a, w, out, stride, sh, smem, status, blocks, st);
-  if (sh.box <= 32)
-    return launch_t<O, 16, false>(maps, a, w, out, stride, sh, smem, status, blocks, st);
-  if (sh.box <= 128)
-    return launch_t<O, 64, false>(maps, a, w, out, stride, sh, smem, status, blocks, st);
-  return launch_t<O, 128, false>(maps, a, w, out, stride, sh, smem, status, blocks, st);
+  auto go = [&](auto half, auto two) {
+    return launch_t<O, decltype(half)::value, decltype(two)::value, SHORT>(
+        maps, a, w, out, stride, sh, smem, status, blocks, st);
+  };
+  if (pair) return go(std::integral_constant<int, 128>(), std::true_type());
+  if (sh.box <= 32) return go(std::integral_constant<int, 16>(), std::false_type());
+  if (sh.box <= 128) return go(std::integral_constant<int, 64>(), std::false_type());
+  return go(std::integral_constant<int, 128>(), std::false_type());
 }
 
 }  // namespace
@@ -676,6 +683,9 @@ int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, in
     case RANS_LOGITS_F16:
       return launch_o<__half>(maps, a, w, out, stride, sh, pair, smem, status, blocks, st);
     default:
+      if (!limits.none())
+        return launch_o<__nv_bfloat16, true>(maps, a, w, out, stride, sh, pair, smem, status,
+                                             blocks, st);
       return launch_o<__nv_bfloat16>(maps, a, w, out, stride, sh, pair, smem, status, blocks, st);
   }
 }

@@ -101,9 +101,12 @@ int launch_distill(const rans_logits &in, const int32_t *ids, const float *lp, i
 int launch_mxfp4_quantize(const rans_logits &x, const rans_mxfp4 &q, cudaStream_t st);
 int launch_mxfp4_values(const rans_mxfp4 &q, void *out, int dtype, int64_t stride,
                         cudaStream_t st);
+// Limits of a product, which the forms of float32 and bfloat16 take.
 struct ProductLimits {
-  uint32_t tries = 1u << 21;    // of a bounded wait, about 1 us each
+  static constexpr uint32_t kTries = 1u << 21;
+  uint32_t tries = kTries;      // of a bounded wait, about 1 us each
   uint32_t token_stages = ~0u;  // that a block copies (fewer, to see waits give up)
+  bool none() const { return tries == kTries && token_stages == ~0u; }
 };
 int launch_mxfp4_product(const rans_mxfp4 &a, const rans_mxfp4 &w, void *out, int dtype,
                          int64_t stride, int32_t *status, bool follows,

@@ -35,9 +35,11 @@ def test_states_too_large_for_a_later_launch_are_refused_before_the_first(lib, n
 
 def test_the_check_of_states_alone(lib):
     s = states(3, 2)
-    for args, want in (((s, 2, 8, 2, A(1), A(2), None), rb.OK), ((s, 2, 8, 2, None, None, None), rb.ERR_ARG),
+    for args, want in (((s, 2, 8, 2, A(1), A(2), None), rb.OK),
+                       ((s, 2, 8, 2, None, None, None), rb.ERR_ARG),
                        ((s, 2, 8, 65, A(1), None, None), rb.ERR_ARG),
-                       ((s, 2, 8, 2, A(4), None, None), rb.ERR_ARG), ((None, 0, 8, 2, None, None, None), rb.OK),
+                       ((s, 2, 8, 2, A(4), None, None), rb.ERR_ARG),
+                       ((None, 0, 8, 2, None, None, None), rb.OK),
                        ((s, 2, 0, 2, None, None, None), rb.OK),
                        ((s, 2, 8, 2, A(1), A(2), A(3) + 8), rb.ERR_ARG)):
         assert lib.rans_reorder_states_check(*args) == want

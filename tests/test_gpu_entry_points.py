@@ -36,7 +36,8 @@ def test_numbers_and_products(own_stream):
     assert torch.equal(q.codes, want.codes) and torch.equal(q.scale_rows(), want.scale_rows())
     assert torch.equal(values, want.values())
     assert torch.equal(out, logits) and torch.equal(again, logits)
-    for call in (lambda: rb.rans_mxfp4_quantize(x, want.codes), lambda: rb.rans_mxfp4_values(x, values),
+    for call in (lambda: rb.rans_mxfp4_quantize(x, want.codes),
+                 lambda: rb.rans_mxfp4_values(x, values),
                  lambda: rb.rans_mxfp4_product(q, x, out, None),
                  lambda: rb.rans_mxfp4_logits(x, head, out[:1], ws, None),
                  lambda: rb.rans_mxfp4_logits(x, head, out, ws.cpu(), None)):

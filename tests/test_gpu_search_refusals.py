@@ -16,9 +16,11 @@ def test_a_refused_step_changes_nothing():
     good = torch.zeros(texts * beams, 4, 3, device="cuda")
     odd = torch.zeros(texts * beams, 8, device="cuda")
     lengths = torch.zeros(texts, dtype=torch.int32, device="cuda")
-    for kw in (dict(states=[good[:-1]]), dict(states=[good.cpu()]), dict(states=[good.transpose(1, 2)]),
+    for kw in (dict(states=[good[:-1]]), dict(states=[good.cpu()]),
+               dict(states=[good.transpose(1, 2)]),
                dict(states=[good], axis=3), dict(states=[good], lengths=lengths),
-               dict(states=[good], lengths=lengths.long(), axis=1), dict(states=[good], axis=[1, 1]),
+               dict(states=[good], lengths=lengths.long(), axis=1),
+               dict(states=[good], axis=[1, 1]),
                dict(states=good, status=torch.zeros(2, device="cuda")),
                dict(states=[good, good]), dict(states=[odd[:, :5], odd[:, 4:]]),
                dict(states=[search.parents.view(-1, 1)]),
