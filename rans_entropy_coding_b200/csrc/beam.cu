@@ -30,6 +30,10 @@
 // Measured, 256 x 131072 bf16 in 32 texts: 34 us with the merge's 6 (memory alone 10; 31
 // with the terms of rounded differences, 43 with power series of 1.1 units a term in
 // place of the special function unit: the FP32 pipes then take 12 instructions a logit).
+// Nothing is full: 16 instructions a logit keep issue 63% busy, the special function unit
+// 42%, the ALUs 38%; warps wait at barriers (thresholds over the block in tiles 0 and 2 and at
+// the end), for one another's results, and SMs for those with four blocks instead of
+// three.
 #include <type_traits>
 
 #include "logits_common.cuh"

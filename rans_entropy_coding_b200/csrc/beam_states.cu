@@ -4,9 +4,13 @@
 // States are moved in place: a thread takes the same bytes of all beams of a
 // text, so what it moves is its own, and only moving beams' live positions are read
 // and written.  Where no source moves itself, as in a search's own maps, beams
-// are moved four at a time.  In any other map (chains, cycles) a thread loads
-// all that moves before it stores any, in accesses that fit its registers.  Bound by
-// memory.
+// are moved a few at a time; bound by memory.  In any other map (chains, cycles) a thread
+// loads all that moves before it stores any: up to 16 beams as words of 8 bytes in
+// registers, more, or rows off 8 bytes, as 64 words under the same limit of registers,
+// most of which then lie in local memory (696 bytes stored and 1512 loaded a thread, as
+// compiled).  Measured, 1.07 GB moved where half of 32 x 8 beams' states move: 322 us; all
+// of them in cycles (2.1 GB): 1.07 ms; cycles of 32 beams 4.4 ms; rows off 4 bytes, byte by
+// byte, 9 to 20 ms.
 #include "logits_common.cuh"
 #include "rans_common.cuh"
 #include "rans_internal.h"
@@ -167,7 +171,10 @@ __device__ __forceinline__ float penalised(float score, int length, float penalt
 }
 
 // One block per text.  One thread goes through the candidates, best first; the
-// block then copies token histories.
+// block then copies token histories.  Measured in a graph, behind a fill of the lengths,
+// 512 tokens a beam: 1 text of 4 beams 6 us, 32 of 8 10 us (7 ends: 11), 256 of 8 11 us, 32
+// of 64 56 us.  Bound by that thread's chain of reads, with many beams by the histories,
+// row after row.
 __global__ void __launch_bounds__(kAdvanceThreads)
     beam_advance_kernel(const float *scores, const int32_t *tokens, const int32_t *parents,
                         int count, rans_beams s) {

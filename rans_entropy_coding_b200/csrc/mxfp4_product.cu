@@ -24,7 +24,8 @@
 // scales; memory's copy rate would take 43), 256 tokens 70 us (54), 4096 tokens 776 us
 // by itself (5.7 PFLOP/s; the tensor pipe is busy 78% of the time) and 916 us again and
 // again, under the power limit.  Single blocks took 922 us, pairs without the
-// exchange of logits 916.
+// exchange of logits 916.  (At 168 registers the wide forms keep a few values in local memory:
+// 92 bytes in 16 bits, 56 in float32.)
 #include <type_traits>
 
 #include <cuda.h>

@@ -244,7 +244,11 @@ def mxfp4_logits(hidden, head, out=None, dtype=None, status=None, stream=None):
 
     hidden: rows of floats, which are quantised first, or Mxfp4.  The result is
     of `dtype` (by default the hidden rows' own, float32 for Mxfp4).  A row's logits are
-    the same, bit for bit, in every batch, which is what TokenCoder asks for.
+    the same, bit for bit, in every batch, which is what TokenCoder asks for: of the same
+    hidden row.  One whose numbers differ in a last place (computed in another batch, by
+    libraries that split sums by it) may quantise to other codes, and then has other
+    logits.  Against the float product, quantisation moves logits by some 16% of their
+    spread for rows of even numbers, 20% with a few large channels.
     """
     given = out is not None
     quantised = isinstance(hidden, Mxfp4)
