@@ -91,7 +91,8 @@ constexpr double kLowest64 = -1.7976931348623157e308;
 // The order of continuations of equal totals: the lower beam, then the larger logit,
 // then the lower token.
 constexpr int kTokenBits = 19, kPlaceBits = kTokenBits + 32;
-static_assert(RANS_MAX_VOCAB <= 1 << kTokenBits && RANS_MAX_BEAMS < 1 << (63 - kPlaceBits), "places");
+static_assert(RANS_MAX_VOCAB <= 1 << kTokenBits && RANS_MAX_BEAMS < 1 << (63 - kPlaceBits),
+              "places");
 __device__ __forceinline__ uint64_t place_of(int beam, float x, int token) {
   return (uint64_t)beam << kPlaceBits | (uint64_t)~key_of(x) << kTokenBits | (uint64_t)token;
 }
@@ -676,7 +677,7 @@ __global__ void __launch_bounds__(kMergeThreads)
     }
   }
   __syncthreads();
-  // body(total, place_of) for all candidates of the text
+  // body(total, place) for all candidates of the text
   auto each = [&](auto body) {
     auto one = [&](int i, int n, const Candidate &x) {
       const int p = i / slots, b = p / parts;

@@ -18,7 +18,8 @@ def test_a_search_made_behind_other_work_on_another_stream():
     a, out = torch.randn(4096, 4096, device="cuda"), torch.empty(4096, 4096, device="cuda")
     other = torch.cuda.Stream()
     torch.cuda.synchronize()
-    junk = [torch.full((texts, beams, steps), 7, dtype=torch.int32, device="cuda") for _ in range(8)]
+    junk = [torch.full((texts, beams, steps), 7, dtype=torch.int32, device="cuda")
+            for _ in range(8)]
     del junk  # (what the search's memory holds before it is written)
     torch.cuda.synchronize()
     for _ in range(20):  # some 30 ms on the stream on which the search is made
